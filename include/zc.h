@@ -135,7 +135,8 @@ typedef enum zc_status {
   ZC_ERR_SIZE_MISMATCH = 10,  /* header n differs from the n passed in */
   ZC_ERR_TIMEOUT = 11,        /* an inter-block wait gave up (about one second); output invalid */
   ZC_ERR_DUP_CODEBOOK = 12,   /* a device codebook holds a repeated exponent; nothing was encoded */
-  ZC_ERR_OUT_OF_ROOM = 13     /* the output buffer is smaller than the stream (QLC) */
+  ZC_ERR_OUT_OF_ROOM = 13,    /* the output buffer is smaller than the stream (QLC) */
+  ZC_ERR_BAD_INDEX = 14       /* a slot's row lies outside the rows given (combine); the slot is skipped */
 } zc_status;
 
 /* Human-readable name of a status value (static string, never NULL). */
@@ -481,6 +482,170 @@ zc_status zq_compress(const void* d_in, uint64_t n, const zq_table* h_table, voi
  * ZC_ERR_CORRUPT_STREAM.  No workspace. */
 zc_status zq_decompress(const void* d_in, uint64_t in_bytes, uint64_t n, void* d_out, int32_t* d_status,
                         void* stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * Operators around an expert-parallel exchange
+ * ------------------------------------------------------------------------
+ * The MoE all-to-all of [ZipCCL §2.D] moves rows that were sorted by expert
+ * and brings the experts' outputs back.  These entry points are what stands
+ * on both sides of it: choosing experts, sorting, the weighted way back, and
+ * the norms around the block with its gate and residual scale; each with its
+ * gradient.
+ *   - Matrices are row-major; a *_stride is the distance of two rows of an
+ *     input in values (0: every row is the same one); columns are contiguous.
+ *     Outputs are contiguous.  Any alignment of the type is accepted; where every address,
+ *     stride and width is a multiple of 16 bytes, values move in 16-byte
+ *     pieces.
+ *   - dtype (zc_dtype) is the type of the activations; computation is in fp32
+ *     and each result is rounded once, to nearest even.
+ *   - Sums have a fixed order: the same inputs give the same bits.
+ *   - Workspaces need no initialisation.  Conventions as above otherwise.
+ * Limits: 1 <= k <= ZC_MOE_MAX_K, k <= experts <= ZC_MOE_MAX_EXPERTS,
+ * tokens * k < 2^31, 1 <= hidden <= ZC_NORM_MAX_HIDDEN for the norms and
+ * < 2^31 elsewhere (ZC_ERR_TOO_LARGE beyond).  tokens may be 0.
+ */
+#define ZC_MOE_MAX_K 32
+#define ZC_MOE_MAX_EXPERTS 1024
+#define ZC_NORM_MAX_HIDDEN 16384
+
+typedef enum zc_dtype { ZC_BF16 = 0, ZC_F16 = 1, ZC_F32 = 2 } zc_dtype;
+typedef enum zc_score { ZC_SOFTMAX = 0, ZC_SIGMOID = 1 } zc_score;
+
+/*
+ * Top-k routing.  d_logits: tokens x experts.  For each token the k experts
+ * with the largest choice are taken, largest first, the lowest expert on
+ * ties; a logit of minus infinity (or, with a bias, a choice of minus
+ * infinity) is never taken, and where fewer than k experts remain the slot
+ * gets expert -1 and weight 0.  NaN counts as the largest choice.
+ *   ZC_SOFTMAX  p = softmax of the row; choice = the logit (d_bias must be NULL)
+ *   ZC_SIGMOID  p = 1 / (1 + exp(-logit)); choice = p + d_bias[expert]
+ *               (fp32, NULL = 0; the bias balances the load and is not in p)
+ * weight = scale * p, or scale * p / (sum of the chosen p + 1e-20) with
+ * renormalize.  d_weights: tokens x k fp32; d_experts: tokens x k int32.
+ */
+zc_status zc_moe_route(const void* d_logits, int dtype, uint64_t logits_stride, uint64_t tokens, uint32_t experts,
+                       uint32_t k, int score, const float* d_bias, int renormalize, float scale, float* d_weights,
+                       int32_t* d_experts, void* stream);
+
+/* Gradient of the logits (tokens x experts, their type) from d_dweights
+ * (tokens x k fp32), for the experts that zc_moe_route chose (others, -1
+ * among them, pass nothing on).  The choice itself has no gradient. */
+zc_status zc_moe_route_backward(const float* d_dweights, const void* d_logits, int dtype, uint64_t logits_stride,
+                                uint64_t tokens, uint32_t experts, uint32_t k, const int32_t* d_experts, int score,
+                                int renormalize, float scale, void* d_dlogits, void* stream);
+
+/* Workspace of a dispatch (bytes; 4-byte aligned). */
+zc_status zc_moe_workspace_size(uint64_t tokens, uint32_t k, uint32_t experts, uint64_t* bytes);
+
+/*
+ * Tokens sorted by expert.  Slot s = token * k + j asks for expert
+ * d_experts[s] (int32, or int64 with experts_are_int64; any value outside [0, experts) = not
+ * routed).  The slots are sorted by expert, stably, unrouted ones last:
+ *   d_rows       (tokens * k) x hidden: row r is the token of the slot sorted to r;
+ *                rows of unrouted slots, all at the end, are zero
+ *   d_positions  int32[tokens * k]: the row r of slot s, or -1 - r if it is not routed
+ *   d_slots      int32[tokens * k]: the slot sorted to row r (the inverse)
+ *   d_offsets    int32[experts + 1]: expert e has rows [d_offsets[e], d_offsets[e + 1])
+ */
+zc_status zc_moe_dispatch(const void* d_x, int dtype, uint64_t x_stride, uint64_t tokens, uint32_t hidden,
+                          const void* d_experts, int experts_are_int64, uint32_t k, uint32_t experts, void* d_rows,
+                          int32_t* d_positions, int32_t* d_slots, int32_t* d_offsets, void* d_ws, uint64_t ws_bytes,
+                          void* stream);
+
+/*
+ * The way back: d_out[t] = sum over j of d_weights[t][j] * row d_positions[t][j]
+ * of d_rows (n_rows x hidden), added in order of j; unrouted slots (negative
+ * positions) add nothing, whatever their weight.  d_weights NULL = all ones:
+ * the gradient of zc_moe_dispatch.  A position >= n_rows sets
+ * ZC_ERR_BAD_INDEX and adds nothing.
+ */
+zc_status zc_moe_combine(const void* d_rows, int dtype, uint64_t rows_stride, uint64_t n_rows, const float* d_weights,
+                         const int32_t* d_positions, uint64_t tokens, uint32_t k, uint32_t hidden, void* d_out,
+                         int32_t* d_status, void* stream);
+
+/*
+ * Gradient of zc_moe_combine: d_drows (n_rows x hidden) gets weight * dout in
+ * the row of every routed slot and zero in row -1 - position of every unrouted
+ * one (rows that no slot names are not written); d_dweights[t][j] (fp32) the product of
+ * dout[t] and the slot's row, 0 for unrouted slots.
+ */
+zc_status zc_moe_combine_backward(const void* d_dout, int dtype, uint64_t dout_stride, const void* d_rows,
+                                  uint64_t rows_stride, uint64_t n_rows, const float* d_weights,
+                                  const int32_t* d_positions, uint64_t tokens, uint32_t k, uint32_t hidden,
+                                  void* d_drows, float* d_dweights, int32_t* d_status, void* stream);
+
+/*
+ * The norms around a block.  With r(z) = 1 / sqrt(mean(z^2) + eps) over a row:
+ *   x_new = residual_scale * x + gate * (y * r(y) * weight)
+ *   h     = x_new * r(x_new) * next_weight
+ * y is the block's output, x the residual stream, h the next block's input
+ * (taken from x_new before x_new is rounded).
+ *   - next_weight NULL: no h.  y NULL (then x_new, weight and gate are NULL too): h of x
+ *     itself, the norm before the first block.
+ *   - gate NULL: 1.  Otherwise gate_rows rows (a divisor of tokens) of hidden
+ *     values (gate_wide) or of one: token t uses row t / (tokens / gate_rows).
+ *   - weight, next_weight and the gate have the activations' type, or fp32 with params_f32.
+ */
+typedef struct zc_norm_args {
+  const void* y;
+  const void* x;
+  uint64_t y_stride;
+  uint64_t x_stride;
+  uint64_t tokens;
+  const void* weight;
+  const void* gate;
+  const void* next_weight;
+  uint64_t gate_rows;
+  uint32_t hidden;
+  int32_t dtype;
+  int32_t gate_wide;
+  int32_t params_f32;
+  float residual_scale;
+  float eps;
+  void* x_new;
+  void* h;
+} zc_norm_args;
+zc_status zc_norm(const zc_norm_args* h_args, void* stream);
+
+/* Workspace of zc_norm_backward (bytes; 4-byte aligned). */
+zc_status zc_norm_workspace_size(uint64_t tokens, uint32_t hidden, uint64_t* bytes);
+
+/*
+ * Gradient of zc_norm: from dx_new (the gradient of x_new that does not come through h; NULL =
+ * zero) and dh (with next_weight), the saved y and x_new (x where y is NULL):
+ * dy, dx, and in the parameters' type dweight, dgate, dnext_weight (summed
+ * over the tokens in fp32).  Outputs without their input are NULL.
+ */
+typedef struct zc_norm_backward_args {
+  const void* dx_new;
+  const void* dh;
+  const void* y;
+  const void* x_new;
+  uint64_t dx_new_stride;
+  uint64_t dh_stride;
+  uint64_t y_stride;
+  uint64_t x_new_stride;
+  uint64_t tokens;
+  const void* weight;
+  const void* gate;
+  const void* next_weight;
+  uint64_t gate_rows;
+  uint32_t hidden;
+  int32_t dtype;
+  int32_t gate_wide;
+  int32_t params_f32;
+  float residual_scale;
+  float eps;
+  void* dy;
+  void* dx;
+  void* dweight;
+  void* dgate;
+  void* dnext_weight;
+  void* ws;
+  uint64_t ws_bytes;
+} zc_norm_backward_args;
+zc_status zc_norm_backward(const zc_norm_backward_args* h_args, void* stream);
 
 #ifdef __cplusplus
 }

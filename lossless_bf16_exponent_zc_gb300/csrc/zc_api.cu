@@ -91,6 +91,45 @@ double binade_mass(int e, double sigma) {
   return (std::isinf(hi) ? 1.0 : std::erf(hi * scale)) - std::erf(a);
 }
 
+// ---- argument checks of the operators around an expert-parallel exchange ----
+uint32_t dtype_bytes(int dtype) { return dtype == ZC_BF16 || dtype == ZC_F16 ? 2 : dtype == ZC_F32 ? 4 : 0; }
+
+// Whether rows of `width` values at p, `stride` apart, move in 16-byte pieces.
+bool in_pieces(const void* p, uint64_t stride, uint64_t width, uint32_t size) {
+  return aligned(p, 16) && stride * size % 16 == 0 && width * size % 16 == 0;
+}
+
+// An input matrix: present (unless it has no rows) and aligned to its type.
+zc_status check_rows(const void* p, uint64_t rows, uint64_t stride, uint32_t size) {
+  if (!p && rows) return ZC_ERR_INVALID_ARG;
+  if (stride > (1ull << 40)) return ZC_ERR_TOO_LARGE;
+  return aligned(p, size) ? ZC_OK : ZC_ERR_ALIGNMENT;
+}
+
+zc_status check_slots(uint64_t tokens, uint32_t k) {
+  if (k < 1) return ZC_ERR_INVALID_ARG;
+  if (k > ZC_MOE_MAX_K || tokens > 0x7FFFFFFFull / k) return ZC_ERR_TOO_LARGE;
+  return ZC_OK;
+}
+
+zc_status check_experts(uint32_t experts, uint32_t k) {
+  if (experts < 1) return ZC_ERR_INVALID_ARG;
+  if (experts > ZC_MOE_MAX_EXPERTS) return ZC_ERR_TOO_LARGE;
+  return k > experts ? ZC_ERR_INVALID_ARG : ZC_OK;
+}
+
+// What the norms' forward and backward arguments have in common.
+template <typename A>
+zc_status check_norm(const A& a, uint32_t size) {
+  if (!size || a.hidden < 1 || !(a.eps >= 0.f)) return ZC_ERR_INVALID_ARG;
+  if (a.hidden > ZC_NORM_MAX_HIDDEN || a.tokens > 0x7FFFFFFFull) return ZC_ERR_TOO_LARGE;
+  if (!a.y != !a.weight || (!a.y && (a.gate || !a.next_weight))) return ZC_ERR_INVALID_ARG;
+  if (a.gate && (a.gate_rows < 1 || a.tokens % a.gate_rows)) return ZC_ERR_INVALID_ARG;
+  const uint32_t psize = a.params_f32 ? 4 : size;
+  if (!aligned(a.weight, psize) || !aligned(a.gate, psize) || !aligned(a.next_weight, psize)) return ZC_ERR_ALIGNMENT;
+  return ZC_OK;
+}
+
 }  // namespace
 
 namespace zc {
@@ -165,6 +204,7 @@ const char* zc_status_string(int status) {
     case ZC_ERR_TIMEOUT: return "ZC_ERR_TIMEOUT";
     case ZC_ERR_DUP_CODEBOOK: return "ZC_ERR_DUP_CODEBOOK";
     case ZC_ERR_OUT_OF_ROOM: return "ZC_ERR_OUT_OF_ROOM";
+    case ZC_ERR_BAD_INDEX: return "ZC_ERR_BAD_INDEX";
     default: return "ZC_ERR_UNKNOWN";
   }
 }
@@ -546,6 +586,229 @@ zc_status zc_decompress_batched(int count, const zc_tensor* h_tensors, int32_t* 
     if (e != cudaSuccess) return ZC_ERR_CUDA;
   }
   return ZC_OK;
+}
+
+// ---- operators around an expert-parallel exchange --------------------------
+zc_status zc_moe_route(const void* d_logits, int dtype, uint64_t logits_stride, uint64_t tokens, uint32_t experts,
+                       uint32_t k, int score, const float* d_bias, int renormalize, float scale, float* d_weights,
+                       int32_t* d_experts, void* stream) {
+  const ApiRange range_("zc_moe_route");
+  const uint32_t size = dtype_bytes(dtype);
+  if (!size || (score != ZC_SOFTMAX && score != ZC_SIGMOID) || (d_bias && score == ZC_SOFTMAX))
+    return ZC_ERR_INVALID_ARG;
+  if (zc_status s = check_slots(tokens, k)) return s;
+  if (zc_status s = check_experts(experts, k)) return s;
+  if (zc_status s = check_rows(d_logits, tokens, logits_stride, size)) return s;
+  if (tokens && (!d_weights || !d_experts)) return ZC_ERR_INVALID_ARG;
+  if (!aligned(d_bias, 4) || !aligned(d_weights, 4) || !aligned(d_experts, 4)) return ZC_ERR_ALIGNMENT;
+  RouteParams p = {d_logits, logits_stride, tokens, d_bias, d_weights, d_experts, experts, k,
+                   score == ZC_SIGMOID, renormalize != 0, scale};
+  return cuda_status(launch_route(p, dtype, as_stream(stream)));
+}
+
+zc_status zc_moe_route_backward(const float* d_dweights, const void* d_logits, int dtype, uint64_t logits_stride,
+                                uint64_t tokens, uint32_t experts, uint32_t k, const int32_t* d_experts, int score,
+                                int renormalize, float scale, void* d_dlogits, void* stream) {
+  const ApiRange range_("zc_moe_route_backward");
+  const uint32_t size = dtype_bytes(dtype);
+  if (!size || (score != ZC_SOFTMAX && score != ZC_SIGMOID)) return ZC_ERR_INVALID_ARG;
+  if (zc_status s = check_slots(tokens, k)) return s;
+  if (zc_status s = check_experts(experts, k)) return s;
+  if (zc_status s = check_rows(d_logits, tokens, logits_stride, size)) return s;
+  if (tokens && (!d_dweights || !d_experts || !d_dlogits)) return ZC_ERR_INVALID_ARG;
+  if (!aligned(d_dweights, 4) || !aligned(d_experts, 4) || !aligned(d_dlogits, size)) return ZC_ERR_ALIGNMENT;
+  RouteBwdParams p = {d_dweights, d_logits, logits_stride, tokens, d_experts, d_dlogits, experts, k,
+                      score == ZC_SIGMOID, renormalize != 0, scale};
+  return cuda_status(launch_route_bwd(p, dtype, as_stream(stream)));
+}
+
+zc_status zc_moe_workspace_size(uint64_t tokens, uint32_t k, uint32_t experts, uint64_t* bytes) {
+  if (!bytes) return ZC_ERR_INVALID_ARG;
+  if (zc_status s = check_slots(tokens, k)) return s;
+  if (experts < 1) return ZC_ERR_INVALID_ARG;
+  if (experts > ZC_MOE_MAX_EXPERTS) return ZC_ERR_TOO_LARGE;
+  *bytes = moe_workspace_bytes(tokens, k, experts);
+  return ZC_OK;
+}
+
+zc_status zc_moe_dispatch(const void* d_x, int dtype, uint64_t x_stride, uint64_t tokens, uint32_t hidden,
+                          const void* d_experts, int experts_are_int64, uint32_t k, uint32_t experts, void* d_rows,
+                          int32_t* d_positions, int32_t* d_slots, int32_t* d_offsets, void* d_ws, uint64_t ws_bytes,
+                          void* stream) {
+  const ApiRange range_("zc_moe_dispatch");
+  const uint32_t size = dtype_bytes(dtype);
+  if (!size || hidden < 1 || experts < 1 || !d_offsets) return ZC_ERR_INVALID_ARG;
+  if (hidden > 0x7FFFFFFFu || experts > ZC_MOE_MAX_EXPERTS) return ZC_ERR_TOO_LARGE;
+  if (zc_status s = check_slots(tokens, k)) return s;
+  if (zc_status s = check_rows(d_x, tokens, x_stride, size)) return s;
+  if (tokens && (!d_experts || !d_rows || !d_positions || !d_slots)) return ZC_ERR_INVALID_ARG;
+  if (!d_ws) return ZC_ERR_INVALID_ARG;
+  if (!aligned(d_experts, experts_are_int64 ? 8 : 4) || !aligned(d_rows, size) || !aligned(d_positions, 4) ||
+      !aligned(d_slots, 4) || !aligned(d_offsets, 4) || !aligned(d_ws, 4))
+    return ZC_ERR_ALIGNMENT;
+  if (ws_bytes < moe_workspace_bytes(tokens, k, experts)) return ZC_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;
+  DispatchParams p = {};
+  p.x = d_x;
+  p.stride = x_stride;
+  p.tokens = tokens;
+  p.hidden = hidden;
+  p.experts = experts;
+  p.k = k;
+  p.ids64 = experts_are_int64 != 0;
+  p.ids = d_experts;
+  p.rows = d_rows;
+  p.positions = d_positions;
+  p.slots = d_slots;
+  p.offsets = d_offsets;
+  p.counts = static_cast<uint32_t*>(d_ws);
+  const bool vec = in_pieces(d_x, x_stride, hidden, size) && aligned(d_rows, 16);
+  return cuda_status(launch_dispatch(p, dtype, vec, as_stream(stream), dev));
+}
+
+zc_status zc_moe_combine(const void* d_rows, int dtype, uint64_t rows_stride, uint64_t n_rows, const float* d_weights,
+                         const int32_t* d_positions, uint64_t tokens, uint32_t k, uint32_t hidden, void* d_out,
+                         int32_t* d_status, void* stream) {
+  const ApiRange range_("zc_moe_combine");
+  const uint32_t size = dtype_bytes(dtype);
+  if (!size || hidden < 1 || !d_status) return ZC_ERR_INVALID_ARG;
+  if (hidden > 0x7FFFFFFFu) return ZC_ERR_TOO_LARGE;
+  if (zc_status s = check_slots(tokens, k)) return s;
+  if (zc_status s = check_rows(d_rows, n_rows, rows_stride, size)) return s;
+  if (tokens && (!d_positions || !d_out)) return ZC_ERR_INVALID_ARG;
+  if (!aligned(d_weights, 4) || !aligned(d_positions, 4) || !aligned(d_out, size) || !aligned(d_status, 4))
+    return ZC_ERR_ALIGNMENT;
+  CombineParams p = {d_rows, rows_stride, n_rows, tokens, d_weights, d_positions, d_out, d_status, hidden, k};
+  const bool vec = in_pieces(d_rows, rows_stride, hidden, size) && aligned(d_out, 16);
+  return cuda_status(launch_combine(p, dtype, vec, as_stream(stream)));
+}
+
+zc_status zc_moe_combine_backward(const void* d_dout, int dtype, uint64_t dout_stride, const void* d_rows,
+                                  uint64_t rows_stride, uint64_t n_rows, const float* d_weights,
+                                  const int32_t* d_positions, uint64_t tokens, uint32_t k, uint32_t hidden,
+                                  void* d_drows, float* d_dweights, int32_t* d_status, void* stream) {
+  const ApiRange range_("zc_moe_combine_backward");
+  const uint32_t size = dtype_bytes(dtype);
+  if (!size || hidden < 1 || !d_status) return ZC_ERR_INVALID_ARG;
+  if (hidden > 0x7FFFFFFFu) return ZC_ERR_TOO_LARGE;
+  if (zc_status s = check_slots(tokens, k)) return s;
+  if (zc_status s = check_rows(d_rows, n_rows, rows_stride, size)) return s;
+  if (zc_status s = check_rows(d_dout, tokens, dout_stride, size)) return s;
+  if (tokens && (!d_weights || !d_positions || !d_dweights || (!d_drows && n_rows))) return ZC_ERR_INVALID_ARG;
+  if (!aligned(d_weights, 4) || !aligned(d_positions, 4) || !aligned(d_dweights, 4) || !aligned(d_drows, size) ||
+      !aligned(d_status, 4))
+    return ZC_ERR_ALIGNMENT;
+  CombineBwdParams p = {d_dout,    d_rows,      dout_stride, rows_stride, n_rows,   tokens,
+                        d_weights, d_positions, d_drows,     d_dweights,  d_status, hidden, k};
+  const bool vec = in_pieces(d_rows, rows_stride, hidden, size) && in_pieces(d_dout, dout_stride, hidden, size) &&
+                   aligned(d_drows, 16);
+  return cuda_status(launch_combine_bwd(p, dtype, vec, as_stream(stream)));
+}
+
+zc_status zc_norm(const zc_norm_args* h_args, void* stream) {
+  const ApiRange range_("zc_norm");
+  if (!h_args) return ZC_ERR_INVALID_ARG;
+  const zc_norm_args& a = *h_args;
+  const uint32_t size = dtype_bytes(a.dtype);
+  // without tokens the tensors may be NULL, so which of them the call is about does not matter
+  if (size && a.tokens == 0) return a.hidden < 1 ? ZC_ERR_INVALID_ARG : ZC_OK;
+  if (zc_status s = check_norm(a, size)) return s;
+  if (zc_status s = check_rows(a.x, a.tokens, a.x_stride, size)) return s;
+  if (a.y)
+    if (zc_status s = check_rows(a.y, a.tokens, a.y_stride, size)) return s;
+  if (!a.x_new != !a.y || !a.h != !a.next_weight) return ZC_ERR_INVALID_ARG;
+  if (!aligned(a.x_new, size) || !aligned(a.h, size)) return ZC_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;
+  NormParams p = {};
+  p.y = a.y;
+  p.x = a.x;
+  p.y_stride = a.y_stride;
+  p.x_stride = a.x_stride;
+  p.tokens = a.tokens;
+  p.weight = a.weight;
+  p.gate = a.gate;
+  p.next_weight = a.next_weight;
+  p.gate_tokens = a.gate ? a.tokens / a.gate_rows : 1;
+  p.gate_wide = a.gate_wide != 0;
+  p.params_f32 = a.params_f32 != 0;
+  p.residual_scale = a.residual_scale;
+  p.eps = a.eps;
+  p.x_new = a.x_new;
+  p.h = a.h;
+  p.hidden = a.hidden;
+  const bool vec = in_pieces(a.x, a.x_stride, a.hidden, size) && (!a.y || in_pieces(a.y, a.y_stride, a.hidden, size)) &&
+                   aligned(a.x_new, 16) && aligned(a.h, 16) && aligned(a.weight, 16) && aligned(a.next_weight, 16) &&
+                   aligned(a.gate, 16);
+  return cuda_status(launch_norm(p, a.dtype, vec, as_stream(stream), dev));
+}
+
+zc_status zc_norm_workspace_size(uint64_t tokens, uint32_t hidden, uint64_t* bytes) {
+  if (!bytes || hidden < 1) return ZC_ERR_INVALID_ARG;
+  if (hidden > ZC_NORM_MAX_HIDDEN || tokens > 0x7FFFFFFFull) return ZC_ERR_TOO_LARGE;
+  *bytes = norm_workspace_bytes(tokens, hidden);
+  return ZC_OK;
+}
+
+zc_status zc_norm_backward(const zc_norm_backward_args* h_args, void* stream) {
+  const ApiRange range_("zc_norm_backward");
+  if (!h_args) return ZC_ERR_INVALID_ARG;
+  const zc_norm_backward_args& a = *h_args;
+  const uint32_t size = dtype_bytes(a.dtype);
+  if (zc_status s = check_norm(a, size)) return s;
+  if (!a.dh != !a.next_weight || (!a.dh && !a.dx_new)) return ZC_ERR_INVALID_ARG;
+  if (a.next_weight)
+    if (zc_status s = check_rows(a.x_new, a.tokens, a.x_new_stride, size)) return s;
+  if (a.dh)
+    if (zc_status s = check_rows(a.dh, a.tokens, a.dh_stride, size)) return s;
+  if (a.dx_new)
+    if (zc_status s = check_rows(a.dx_new, a.tokens, a.dx_new_stride, size)) return s;
+  if (a.y)
+    if (zc_status s = check_rows(a.y, a.tokens, a.y_stride, size)) return s;
+  if (!a.dx || !a.dy != !a.y || !a.dweight != !a.weight || !a.dgate != !a.gate || !a.dnext_weight != !a.next_weight)
+    return ZC_ERR_INVALID_ARG;
+  const uint32_t psize = a.params_f32 ? 4 : size;
+  if (!aligned(a.dx, size) || !aligned(a.dy, size) || !aligned(a.dweight, psize) || !aligned(a.dgate, psize) ||
+      !aligned(a.dnext_weight, psize) || !aligned(a.ws, 4))
+    return ZC_ERR_ALIGNMENT;
+  const uint64_t need = norm_workspace_bytes(a.tokens, a.hidden);
+  if (!a.ws && need) return ZC_ERR_INVALID_ARG;
+  if (a.ws_bytes < need) return ZC_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;
+  NormBwdParams p = {};
+  p.dx_new = a.dx_new;
+  p.dh = a.dh;
+  p.y = a.y;
+  p.x_new = a.x_new;
+  p.dx_new_stride = a.dx_new_stride;
+  p.dh_stride = a.dh_stride;
+  p.y_stride = a.y_stride;
+  p.x_new_stride = a.x_new_stride;
+  p.tokens = a.tokens;
+  p.weight = a.weight;
+  p.gate = a.gate;
+  p.next_weight = a.next_weight;
+  p.gate_rows = a.gate ? a.gate_rows : 1;
+  p.gate_tokens = a.tokens / p.gate_rows;
+  p.gate_wide = a.gate_wide != 0;
+  p.params_f32 = a.params_f32 != 0;
+  p.residual_scale = a.residual_scale;
+  p.eps = a.eps;
+  p.dy = a.dy;
+  p.dx = a.dx;
+  p.dweight = a.dweight;
+  p.dgate = a.dgate;
+  p.dnext_weight = a.dnext_weight;
+  p.parts = static_cast<float*>(a.ws);
+  p.hidden = a.hidden;
+  const bool vec = (!a.next_weight || in_pieces(a.x_new, a.x_new_stride, a.hidden, size)) &&
+                   (!a.dh || in_pieces(a.dh, a.dh_stride, a.hidden, size)) &&
+                   (!a.dx_new || in_pieces(a.dx_new, a.dx_new_stride, a.hidden, size)) &&
+                   (!a.y || in_pieces(a.y, a.y_stride, a.hidden, size)) && aligned(a.dx, 16) && aligned(a.dy, 16) &&
+                   aligned(a.weight, 16) && aligned(a.gate, 16) && aligned(a.next_weight, 16);
+  return cuda_status(launch_norm_bwd(p, a.dtype, vec, as_stream(stream), dev));
 }
 
 }  // extern "C"

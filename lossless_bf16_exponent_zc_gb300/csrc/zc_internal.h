@@ -104,6 +104,103 @@ cudaError_t launch_zq_encode(const uint8_t* in, uint64_t n, const uint8_t width[
 cudaError_t launch_zq_decode(const uint8_t* in, uint64_t in_bytes, uint64_t n, uint8_t* out, int32_t* status,
                              cudaStream_t stream, const DeviceInfo& dev);
 
+// ---- the operators around an expert-parallel layer (zc_moe.cu, zc_norm.cu);
+// arguments validated by the caller.  `dtype` is a zc_dtype; `vec`: every
+// address, stride and width is a multiple of 16 bytes.
+constexpr uint32_t kMoeMaxExperts = ZC_MOE_MAX_EXPERTS;
+constexpr uint32_t kMoeMaxK = ZC_MOE_MAX_K;
+constexpr uint32_t kMoePlaceTokens = 8;    // most tokens one CTA of the dispatch places
+constexpr uint32_t kMoeChunkSlots = 2048;  // most slots of a counting chunk (whole groups of 8 tokens)
+constexpr uint64_t kMoeSingleSlots = 2048; // up to here every CTA counts all slots itself: one launch
+
+struct RouteParams {
+  const void* logits;
+  uint64_t stride, tokens;
+  const float* bias;
+  float* weights;
+  int32_t* ids;
+  uint32_t experts, k;
+  int sigmoid, renormalize;
+  float scale;
+};
+struct RouteBwdParams {
+  const float* dweights;
+  const void* logits;
+  uint64_t stride, tokens;
+  const int32_t* ids;
+  void* dlogits;
+  uint32_t experts, k;
+  int sigmoid, renormalize;
+  float scale;
+};
+cudaError_t launch_route(const RouteParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_route_bwd(const RouteBwdParams& p, int dtype, cudaStream_t stream);
+
+struct DispatchParams {
+  const void* x;
+  uint64_t stride, tokens;
+  uint32_t hidden, experts, k;
+  int ids64;
+  const void* ids;
+  void* rows;
+  int32_t *positions, *slots, *offsets;
+  uint32_t* counts;  // workspace: [experts + 1][chunks], then [experts + 1] totals
+  uint32_t chunks, chunk_tokens, cta_tokens;  // set by the launch
+  int single;
+};
+uint64_t moe_workspace_bytes(uint64_t tokens, uint32_t k, uint32_t experts);
+cudaError_t launch_dispatch(const DispatchParams& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev);
+
+struct CombineParams {
+  const void* rows;
+  uint64_t row_stride, n_rows, tokens;
+  const float* weights;  // NULL: all ones
+  const int32_t* positions;
+  void* out;
+  int32_t* status;
+  uint32_t hidden, k;
+};
+struct CombineBwdParams {
+  const void *dout, *rows;
+  uint64_t dout_stride, row_stride, n_rows, tokens;
+  const float* weights;
+  const int32_t* positions;
+  void* drows;
+  float* dweights;
+  int32_t* status;
+  uint32_t hidden, k;
+};
+cudaError_t launch_combine(const CombineParams& p, int dtype, bool vec, cudaStream_t stream);
+cudaError_t launch_combine_bwd(const CombineBwdParams& p, int dtype, bool vec, cudaStream_t stream);
+
+// Gate of a token: row token / gate_tokens of a table with `hidden` columns, or
+// with one (gate_wide = 0); gate NULL: 1.
+struct NormParams {
+  const void *y, *x;                     // y NULL: no branch (the norm of x alone)
+  uint64_t y_stride, x_stride, tokens;
+  const void *weight, *gate, *next_weight;  // next_weight NULL: no norm of the new x
+  uint64_t gate_tokens;
+  int gate_wide, params_f32;
+  float residual_scale, eps;
+  void *x_new, *h;
+  uint32_t hidden;
+};
+struct NormBwdParams {
+  const void *dx_new, *dh, *y, *x_new;  // dx_new NULL: zero
+  uint64_t dx_new_stride, dh_stride, y_stride, x_new_stride, tokens;
+  const void *weight, *gate, *next_weight;
+  uint64_t gate_tokens, gate_rows;
+  int gate_wide, params_f32;
+  float residual_scale, eps;
+  void *dy, *dx, *dweight, *dgate, *dnext_weight;
+  float* parts;  // workspace
+  uint32_t hidden;
+  uint32_t splits, units, ctas;  // set by the launch: row ranges per gate row, ranges in all, CTAs
+};
+uint64_t norm_workspace_bytes(uint64_t tokens, uint32_t hidden);
+cudaError_t launch_norm(const NormParams& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev);
+cudaError_t launch_norm_bwd(const NormBwdParams& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev);
+
 cudaError_t launch_histogram(const uint16_t* in, uint64_t n, uint8_t* cb_out, uint32_t* hist_out, WsHeader* ws,
                              int32_t* status, cudaStream_t stream, const DeviceInfo& dev);
 

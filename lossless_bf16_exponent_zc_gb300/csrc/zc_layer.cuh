@@ -1,0 +1,134 @@
+// zc_layer.cuh -- device building blocks of the operators around an
+// expert-parallel layer (zc_moe.cu, zc_norm.cu): values of three types moved
+// in 16-byte pieces or one at a time, computed in fp32, and sums over a warp
+// or a CTA whose order is fixed (the same inputs give the same bits).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "zc_device.cuh"
+
+namespace zc {
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// fp32 -> T, round to nearest even: the one rounding of a result.
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// V values of T as they lie in memory: one 16-byte piece (V = 16 / sizeof(T))
+// or a single value (V = 1, for widths, strides and addresses that 16 bytes
+// do not divide).
+template <typename T, int V>
+struct Piece;
+
+template <typename T>
+struct Piece<T, 1> {
+  T v;
+  __device__ __forceinline__ static Piece load(const T* p) { return Piece{*p}; }
+  __device__ __forceinline__ void store(T* p) const { *p = v; }
+  __device__ __forceinline__ static Piece zero() { return Piece{from_f32<T>(0.f)}; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32<T>(v); }
+  __device__ __forceinline__ void set(const float (&f)[1]) { v = from_f32<T>(f[0]); }
+};
+
+template <>
+struct Piece<float, 4> {
+  uint4 v;
+  __device__ __forceinline__ static Piece load(const float* p) { return Piece{*reinterpret_cast<const uint4*>(p)}; }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ static Piece zero() { return Piece{make_uint4(0u, 0u, 0u, 0u)}; }
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+  }
+  __device__ __forceinline__ void set(const float (&f)[4]) {
+    v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, __nv_bfloat16) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, __half) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  a = f.x;
+  b = f.y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T>
+struct Piece<T, 8> {
+  uint4 v;
+  __device__ __forceinline__ static Piece load(const T* p) { return Piece{*reinterpret_cast<const uint4*>(p)}; }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ static Piece zero() { return Piece{make_uint4(0u, 0u, 0u, 0u)}; }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    unpack2(v.x, f[0], f[1], T());
+    unpack2(v.y, f[2], f[3], T());
+    unpack2(v.z, f[4], f[5], T());
+    unpack2(v.w, f[6], f[7], T());
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    v = make_uint4(pack2(f[0], f[1], T()), pack2(f[2], f[3], T()), pack2(f[4], f[5], T()), pack2(f[6], f[7], T()));
+  }
+};
+
+// Values of T in a 16-byte piece.
+template <typename T>
+constexpr int kPieceOf = 16 / static_cast<int>(sizeof(T));
+
+__device__ __forceinline__ float warp_sum_f32(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  return v;
+}
+
+__device__ __forceinline__ float warp_max_f32(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
+  return v;
+}
+
+// Sums of N values over a CTA of whole warps, every thread getting all of
+// them.  `red` holds N x 32 floats; a caller that sums again before a
+// __syncthreads of its own passes another buffer.
+template <int N>
+__device__ __forceinline__ void block_sum_f32(float (&v)[N], float* red) {
+  const uint32_t warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = lane_id();
+#pragma unroll
+  for (int i = 0; i < N; i++) v[i] = warp_sum_f32(v[i]);
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i++) red[i * 32 + warp] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; i++) v[i] = warp_sum_f32(lane < warps ? red[i * 32 + lane] : 0.f);
+}
+
+}  // namespace zc

@@ -1,0 +1,151 @@
+// zc_norm.cu -- the norms before and after a block, with the block's gate and
+// residual scale, forward (the gradient is in zc_norm_bwd.cu).
+//
+//   x' = a x + g * (y r(y) w),   h = x' r(x') w2,   r(z) = 1 / sqrt(mean(z^2) + eps)
+//
+// One pass: a row of y and x is read once into registers, both sums of
+// squares are taken there, and x' and the next block's input h are written.
+// h is the norm of x' before its rounding to the stored type, so each output
+// is rounded once.  Bound by memory: 4 values moved per 11 operations.
+#include "zc_norm.cuh"
+
+namespace zc {
+
+namespace {
+
+template <typename T, int V, int NV, bool WARP, bool BRANCH, bool NEXT, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_kernel(NormParams p) {
+  __shared__ float red[2][32];
+  pdl_begin();
+  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
+  const uint32_t me = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
+  const uint32_t pieces = p.hidden / V;
+  const float inv_d = 1.f / static_cast<float>(p.hidden);
+  const uint64_t rows_a_turn = WARP ? static_cast<uint64_t>(gridDim.x) * kNormWarps : gridDim.x;
+  int turn = 0;
+  auto row_sum = [&](float v) {
+    if (WARP) return warp_sum_f32(v);
+    float s[1] = {v};
+    block_sum_f32<1>(s, red[turn]);
+    turn ^= 1;
+    return s[0];
+  };
+  for (uint64_t t = WARP ? static_cast<uint64_t>(blockIdx.x) * kNormWarps + warp : blockIdx.x; t < p.tokens;
+       t += rows_a_turn) {
+    Piece<T, V> y[NV], x[NV];
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+      const uint32_t c = me + i * step;
+      const uint64_t at = static_cast<uint64_t>(c) * V;
+      y[i] = x[i] = Piece<T, V>::zero();
+      if (c < pieces) {
+        if (BRANCH) y[i] = Piece<T, V>::load(static_cast<const T*>(p.y) + t * p.y_stride + at);
+        x[i] = Piece<T, V>::load(static_cast<const T*>(p.x) + t * p.x_stride + at);
+      }
+    }
+    float n[NV][V];  // the new x
+    if (BRANCH) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; i++) {
+        float f[V];
+        y[i].get(f);
+#pragma unroll
+        for (int j = 0; j < V; j++) sum = fmaf(f[j], f[j], sum);
+      }
+      const float r = rsqrtf(row_sum(sum) * inv_d + p.eps);
+      const uint64_t gate_row = p.gate ? t / p.gate_tokens : 0;
+      const float gate_one = p.gate && !p.gate_wide ? load_param<T>(p.gate, p.params_f32, gate_row) : 1.f;
+#pragma unroll
+      for (int i = 0; i < NV; i++) {
+        const uint32_t c = me + i * step;
+        const uint64_t at = static_cast<uint64_t>(c) * V;
+        float f[V], w[V], g[V], o[V];
+        y[i].get(f);
+        x[i].get(o);
+#pragma unroll
+        for (int j = 0; j < V; j++) w[j] = 0.f, g[j] = gate_one;
+        if (c < pieces) {
+          load_params<T, V>(p.weight, p.params_f32, at, w);
+          if (p.gate && p.gate_wide) load_params<T, V>(p.gate, p.params_f32, gate_row * p.hidden + at, g);
+        }
+#pragma unroll
+        for (int j = 0; j < V; j++) n[i][j] = fmaf(g[j], f[j] * r * w[j], p.residual_scale * o[j]);
+        if (c < pieces) {
+          Piece<T, V> out;
+          out.set(n[i]);
+          out.store(static_cast<T*>(p.x_new) + t * p.hidden + at);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; i++) x[i].get(n[i]);
+    }
+    if (NEXT) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int j = 0; j < V; j++) sum = fmaf(n[i][j], n[i][j], sum);
+      const float r = rsqrtf(row_sum(sum) * inv_d + p.eps);
+#pragma unroll
+      for (int i = 0; i < NV; i++) {
+        const uint32_t c = me + i * step;
+        const uint64_t at = static_cast<uint64_t>(c) * V;
+        if (c >= pieces) continue;
+        float w[V], h[V];
+        load_params<T, V>(p.next_weight, p.params_f32, at, w);
+#pragma unroll
+        for (int j = 0; j < V; j++) h[j] = n[i][j] * r * w[j];
+        Piece<T, V> out;
+        out.set(h);
+        out.store(static_cast<T*>(p.h) + t * p.hidden + at);
+      }
+    }
+  }
+}
+
+template <typename T, int V, int NV, bool WARP, int THREADS>
+cudaError_t run_shape(NormParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
+  const void* fn = nullptr;
+  if (p.y && p.next_weight)
+    fn = reinterpret_cast<const void*>(norm_kernel<T, V, NV, WARP, true, true, THREADS>);
+  else if (p.y)
+    fn = reinterpret_cast<const void*>(norm_kernel<T, V, NV, WARP, true, false, THREADS>);
+  else
+    fn = reinterpret_cast<const void*>(norm_kernel<T, V, NV, WARP, false, true, THREADS>);
+  const uint64_t units = WARP ? (p.tokens + kNormWarps - 1) / kNormWarps : p.tokens;
+  const uint64_t most = static_cast<uint64_t>(dev.sm_count) * 2048 / static_cast<uint64_t>(threads);
+  void* args[] = {&p};
+  return launch_kernel(fn, dim3(static_cast<unsigned>(units < most ? units : most)), dim3(threads), 0, stream, args,
+                       false);
+}
+
+template <typename T>
+cudaError_t run_typed(NormParams& p, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
+  constexpr int V = kPieceOf<T>;
+  const uint32_t d = p.hidden;
+  auto cta = [&](uint32_t per_thread) { return static_cast<int>((d + per_thread * 32 - 1) / (per_thread * 32) * 32); };
+  if (!vec) {
+    if (d <= kNormWarpWidth) return run_shape<T, 1, 16, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
+    return run_shape<T, 1, 16, false, 1024>(p, cta(16), stream, dev);
+  }
+  if (d <= 256) return run_shape<T, V, 8 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
+  if (d <= kNormWarpWidth) return run_shape<T, V, 16 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
+  if (d <= 4096) return run_shape<T, V, 8 / V, false, 512>(p, cta(8), stream, dev);
+  return run_shape<T, V, 16 / V, false, 1024>(p, cta(16), stream, dev);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormParams& params, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
+  if (params.tokens == 0) return cudaSuccess;
+  NormParams p = params;
+  switch (dtype) {
+    case ZC_BF16: return run_typed<__nv_bfloat16>(p, vec, stream, dev);
+    case ZC_F16: return run_typed<__half>(p, vec, stream, dev);
+    default: return run_typed<float>(p, vec, stream, dev);
+  }
+}
+
+}  // namespace zc
