@@ -131,4 +131,59 @@ __device__ __forceinline__ void block_sum_f32(float (&v)[N], float* red) {
   for (int i = 0; i < N; i++) v[i] = warp_sum_f32(lane < warps ? red[i * 32 + lane] : 0.f);
 }
 
+// As block_sum_f32 for one to four values with fewer shuffles: the lanes of a
+// warp first share the values out among them (lane group g, of 32 / 4 or 32 / 2 lanes,
+// ends with value g), the CTA's partial sums are then added the same
+// way.  `red`: 4 x 32 floats, 16-byte aligned, those of absent warps zero (the caller clears all before
+// the first use); as above, two sums in a row need two buffers.
+template <int N>
+__device__ __forceinline__ void block_sum_shared(float (&v)[N], float* red) {
+  static_assert(N == 2 || N == 4, "lane groups of 16 or 8");
+  const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+  float s;
+  if (N == 4) {
+    const bool up = lane & 16;
+    float a = up ? v[N - 2] : v[0], b = up ? v[N - 1] : v[1];
+    a += __shfl_xor_sync(kFull, up ? v[0] : v[N - 2], 16);
+    b += __shfl_xor_sync(kFull, up ? v[1] : v[N - 1], 16);
+    const bool odd = lane & 8;
+    s = odd ? b : a;
+    s += __shfl_xor_sync(kFull, odd ? a : b, 8);
+  } else {
+    const bool up = lane & 16;
+    s = up ? v[1] : v[0];
+    s += __shfl_xor_sync(kFull, up ? v[0] : v[1], 16);
+    s += __shfl_xor_sync(kFull, s, 8);
+  }
+  s += __shfl_xor_sync(kFull, s, 4);
+  s += __shfl_xor_sync(kFull, s, 2);
+  s += __shfl_xor_sync(kFull, s, 1);
+  constexpr uint32_t kGroup = 32 / N;
+  if ((lane & (kGroup - 1)) == 0) red[(lane / kGroup) * 32 + warp] = s;
+  __syncthreads();
+  if (N == 4) {
+    const float4 p = *reinterpret_cast<const float4*>(red + (lane >> 3) * 32 + (lane & 7) * 4);
+    s = (p.x + p.y) + (p.z + p.w);
+  } else {
+    const float2 p = *reinterpret_cast<const float2*>(red + (lane >> 4) * 32 + (lane & 15) * 2);
+    s = p.x + p.y;
+    s += __shfl_xor_sync(kFull, s, 8);
+  }
+  s += __shfl_xor_sync(kFull, s, 4);
+  s += __shfl_xor_sync(kFull, s, 2);
+  s += __shfl_xor_sync(kFull, s, 1);
+#pragma unroll
+  for (int i = 0; i < N; i++) v[i] = __shfl_sync(kFull, s, i * kGroup);
+}
+
+// 4-byte asynchronous copy, both addresses 4-byte aligned.
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {  // all but the last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 }  // namespace zc

@@ -105,6 +105,91 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(NormParams p) {
   }
 }
 
+constexpr int kFwdStages = 4;
+
+// The ring shape: rows blockIdx.x, blockIdx.x + CTAs, ... stream through shared memory.
+template <typename T, int V, bool BRANCH, bool NEXT>
+__global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormParams p) {
+  constexpr int NV = kNormCols / V, P = kNormCols / 2;
+  using Ring = RowRing<T, V, NV, BRANCH ? 2 : 1, kFwdStages>;
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ __align__(16) float red[2][128];
+  pdl_allow_dependents();
+  for (uint32_t i = threadIdx.x; i < 256; i += blockDim.x) red[i >> 7][i & 127] = 0.f;
+  pdl_wait();
+  const Ring ring{ring_smem, blockDim.x, p.hidden / V};
+  const float inv_d = 1.f / static_cast<float>(p.hidden);
+  const bool wide = BRANCH && p.gate && p.gate_wide, narrow = BRANCH && p.gate && !p.gate_wide;
+  const T *x_at = static_cast<const T*>(p.x), *y_at = static_cast<const T*>(p.y);
+  uint64_t ahead = blockIdx.x;
+  auto issue = [&](int stage) {
+    if (ahead < p.tokens) {
+      ring.copy(stage, 0, x_at + ahead * p.x_stride);
+      if (BRANCH) ring.copy(stage, 1, y_at + ahead * p.y_stride);
+      ahead += gridDim.x;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kFwdStages; s++) issue(s);
+  float2 w[P], w2[P], k[P];
+  if (BRANCH) ring.params(p.weight, p.params_f32, 0, w);
+  if (NEXT) ring.params(p.next_weight, p.params_f32, 0, w2);
+#pragma unroll
+  for (int i = 0; i < P; i++) k[i] = splat(1.f);
+  uint64_t gate_row = ~0ull;  // the gate row that k holds
+  cp_async_wait<kFwdStages - 1>();
+  __syncthreads();
+  int stage = 0, turn = 0;
+  for (uint64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+    float2 x[P];
+    float sums[2];
+    ring.get(stage, 0, x_at + t * p.x_stride, x);
+    if (BRANCH) {
+      float2 y[P], yy = splat(0.f);
+      ring.get(stage, 1, y_at + t * p.y_stride, y);
+#pragma unroll
+      for (int i = 0; i < P; i++) yy = __ffma2_rn(y[i], y[i], yy);
+      sums[0] = yy.x + yy.y;
+      sums[1] = 0.f;
+      cp_async_wait<kFwdStages - 2>();  // the next row, which the barrier below shows to all
+      block_sum_shared<2>(sums, red[turn]);
+      turn ^= 1;
+      issue(stage);
+      const float2 r = splat(rsqrtf(sums[0] * inv_d + p.eps)), a = splat(p.residual_scale);
+      if (wide && t / p.gate_tokens != gate_row) {
+        gate_row = t / p.gate_tokens;
+        ring.params(p.gate, p.params_f32, gate_row * p.hidden, k);
+      } else if (narrow) {
+        const float one = load_param<T>(p.gate, p.params_f32, t / p.gate_tokens);
+#pragma unroll
+        for (int i = 0; i < P; i++) k[i] = splat(one);
+      }
+#pragma unroll
+      for (int i = 0; i < P; i++)
+        x[i] = __ffma2_rn(k[i], __fmul2_rn(__fmul2_rn(y[i], r), w[i]), __fmul2_rn(a, x[i]));
+      ring.put(static_cast<T*>(p.x_new) + t * p.hidden, x);
+    }
+    if (NEXT) {
+      float2 xx = splat(0.f);
+#pragma unroll
+      for (int i = 0; i < P; i++) xx = __ffma2_rn(x[i], x[i], xx);
+      sums[0] = xx.x + xx.y;
+      sums[1] = 0.f;
+      if (!BRANCH) cp_async_wait<kFwdStages - 2>();
+      block_sum_shared<2>(sums, red[turn]);
+      turn ^= 1;
+      if (!BRANCH) issue(stage);
+      const float2 r = splat(rsqrtf(sums[0] * inv_d + p.eps));
+#pragma unroll
+      for (int i = 0; i < P; i++) x[i] = __fmul2_rn(__fmul2_rn(x[i], r), w2[i]);
+      ring.put(static_cast<T*>(p.h) + t * p.hidden, x);
+    }
+    stage = stage + 1 == kFwdStages ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
+}
+
 template <typename T, int V, int NV, bool WARP, int THREADS>
 cudaError_t run_shape(NormParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
   const void* fn = nullptr;
@@ -121,19 +206,39 @@ cudaError_t run_shape(NormParams& p, int threads, cudaStream_t stream, const Dev
                        false);
 }
 
+template <typename T, int V, bool BRANCH, bool NEXT>
+cudaError_t run_ring(NormParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
+  static RingPrep prep;
+  const int smem = static_cast<int>(RowRing<T, V, kNormCols / V, BRANCH ? 2 : 1, kFwdStages>::bytes(threads));
+  const void* fn = reinterpret_cast<const void*>(norm_ring_kernel<T, V, BRANCH, NEXT>);
+  int per_sm = 0;
+  cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, &per_sm);
+  if (e != cudaSuccess) return e;
+  const uint64_t most = static_cast<uint64_t>(per_sm) * static_cast<uint64_t>(dev.sm_count);
+  void* args[] = {&p};
+  return launch_kernel(fn, dim3(static_cast<unsigned>(p.tokens < most ? p.tokens : most)), dim3(threads), smem, stream,
+                       args, false);
+}
+
+template <typename T, int V>
+cudaError_t run_width(NormParams& p, cudaStream_t stream, const DeviceInfo& dev) {
+  const uint32_t d = p.hidden;
+  if (d <= kNormWarpWidth) {
+    if (V > 1 && d <= 256) return run_shape<T, V, V == 1 ? 16 : 8 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
+    return run_shape<T, V, 16 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
+  }
+  const int threads = static_cast<int>((d + kNormCols * 32 - 1) / (kNormCols * 32) * 32);
+  if (threads <= kNormRingThreads && RowRing<T, V, kNormCols / V, 2, kFwdStages>::bytes(threads) <= kNormRingSmem) {
+    if (p.y && p.next_weight) return run_ring<T, V, true, true>(p, threads, stream, dev);
+    if (p.y) return run_ring<T, V, true, false>(p, threads, stream, dev);
+    return run_ring<T, V, false, true>(p, threads, stream, dev);
+  }
+  return run_shape<T, V, 16 / V, false, 1024>(p, static_cast<int>((d + 511) / 512 * 32), stream, dev);
+}
+
 template <typename T>
 cudaError_t run_typed(NormParams& p, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
-  constexpr int V = kPieceOf<T>;
-  const uint32_t d = p.hidden;
-  auto cta = [&](uint32_t per_thread) { return static_cast<int>((d + per_thread * 32 - 1) / (per_thread * 32) * 32); };
-  if (!vec) {
-    if (d <= kNormWarpWidth) return run_shape<T, 1, 16, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
-    return run_shape<T, 1, 16, false, 1024>(p, cta(16), stream, dev);
-  }
-  if (d <= 256) return run_shape<T, V, 8 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
-  if (d <= kNormWarpWidth) return run_shape<T, V, 16 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
-  if (d <= 4096) return run_shape<T, V, 8 / V, false, 512>(p, cta(8), stream, dev);
-  return run_shape<T, V, 16 / V, false, 1024>(p, cta(16), stream, dev);
+  return vec ? run_width<T, kPieceOf<T>>(p, stream, dev) : run_width<T, 1>(p, stream, dev);
 }
 
 }  // namespace

@@ -1,6 +1,8 @@
 // zc_norm.cuh -- what the block norms' forward and backward kernels share.
 #pragma once
 
+#include <atomic>
+
 #include "zc_internal.h"
 #include "zc_layer.cuh"
 
@@ -31,9 +33,104 @@ __device__ __forceinline__ float load_param(const void* base, int is_f32, uint64
   return f[0];
 }
 
-// Launch shapes.  A row is held by a warp (up to kNormWarpWidth values) or by a CTA, each
-// thread keeping 8 or 16 of its values in registers.
+// Launch shapes.  A row of up to kNormWarpWidth values is held by a warp.  Wider rows stream through a CTA's shared
+// memory, one thread for every 8 columns; rows too wide for that ring are held in a CTA's registers.
 constexpr uint32_t kNormWarpWidth = 512;
-constexpr int kNormWarps = 8;  // rows of a CTA in the warp shape
+constexpr int kNormWarps = 8;         // rows of a CTA in the warp shape
+constexpr int kNormCols = 8;          // columns of a thread in the ring shape
+constexpr int kNormRingThreads = 512;
+constexpr int kNormRingSmem = 225 * 1024;  // what the ring may take of the 227 KB a CTA can have
+
+// The ring: the next STAGES rows of ARRAYS matrices, copied asynchronously (16 bytes at a time; 4 where the rows are not
+// so aligned) by the threads of the CTA.  Every thread keeps the same columns in every row, in NV pieces of V
+// values: its pieces lie in slots of its own, so shared memory is read without bank conflicts.  Rows of 16-bit values at odd
+// addresses are copied as the 4-byte words that cover them and read value by value; their first and last
+// word may hold a neighbour's value, which is not used.
+template <typename T, int V, int NV, int ARRAYS, int STAGES>
+struct RowRing {
+  static constexpr bool kWords = V == 1 && sizeof(T) == 2;
+  uint8_t* smem;
+  uint32_t threads, pieces;
+
+  __host__ __device__ static uint32_t region(uint32_t threads) {  // bytes of one row of one matrix
+    return kWords ? (threads * NV * 2 + 4 + 15) / 16 * 16 : threads * NV * V * static_cast<uint32_t>(sizeof(T));
+  }
+  __host__ __device__ static uint32_t bytes(uint32_t threads) { return STAGES * ARRAYS * region(threads); }
+
+  __device__ __forceinline__ uint8_t* at(int stage, int array) const {
+    return smem + (stage * ARRAYS + array) * region(threads);
+  }
+  __device__ __forceinline__ void copy(int stage, int array, const T* row) const {
+    uint8_t* to = at(stage, array);
+    if (kWords) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(row);
+      const uint32_t words = (static_cast<uint32_t>(a & 2) + 2 * pieces + 3) / 4;
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(a & ~static_cast<uintptr_t>(3));
+      for (uint32_t w = threadIdx.x; w < words; w += threads) cp_async_4(to + 4 * w, from + w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; i++) {
+        const uint32_t c = threadIdx.x + i * threads;
+        if (c >= pieces) continue;
+        if (V == 1)
+          cp_async_4(to + c * 4, row + c);
+        else
+          cp_async_16(to + c * 16, row + static_cast<uint64_t>(c) * V, 16);
+      }
+    }
+  }
+  // This thread's columns of a row; zeros beyond the width.
+  __device__ __forceinline__ void get(int stage, int array, const T* row, float2 (&f)[NV * V / 2]) const {
+    const uint8_t* from = at(stage, array);
+    float* flat = reinterpret_cast<float*>(f);
+    if (kWords) from += reinterpret_cast<uintptr_t>(row) & 2;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+      const uint32_t c = threadIdx.x + i * threads;
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; j++) v[j] = 0.f;
+      if (c < pieces) Piece<T, V>::load(reinterpret_cast<const T*>(from) + c * V).get(v);
+#pragma unroll
+      for (int j = 0; j < V; j++) flat[i * V + j] = v[j];
+    }
+  }
+  // Writes this thread's columns of an output row.
+  __device__ __forceinline__ void put(T* row, const float2 (&f)[NV * V / 2]) const {
+    const float* flat = reinterpret_cast<const float*>(f);
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+      const uint32_t c = threadIdx.x + i * threads;
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; j++) v[j] = flat[i * V + j];
+      Piece<T, V> o;
+      o.set(v);
+      if (c < pieces) o.store(row + static_cast<uint64_t>(c) * V);
+    }
+  }
+  // This thread's columns of a parameter row.
+  __device__ __forceinline__ void params(const void* base, int is_f32, uint64_t first, float2 (&f)[NV * V / 2]) const {
+    float* flat = reinterpret_cast<float*>(f);
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+      const uint32_t c = threadIdx.x + i * threads;
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; j++) v[j] = 0.f;
+      if (c < pieces) load_params<T, V>(base, is_f32, first + static_cast<uint64_t>(c) * V, v);
+#pragma unroll
+      for (int j = 0; j < V; j++) flat[i * V + j] = v[j];
+    }
+  }
+};
+
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+// CTAs of a ring kernel on one SM, by CTA size (the ring's size follows from it); looked up once per device and size.
+struct RingPrep {
+  std::atomic<int> per_sm[kMaxDevices][kNormRingThreads / 32 + 1];
+};
+cudaError_t prepare_ring(RingPrep& rp, const void* fn, int threads, int smem_bytes, const DeviceInfo& dev, int* per_sm);
 
 }  // namespace zc

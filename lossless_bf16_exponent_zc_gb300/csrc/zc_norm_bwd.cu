@@ -17,7 +17,196 @@ namespace zc {
 
 namespace {
 
-constexpr uint32_t kNormMaxCtas = 512;
+// Most CTAs whose sums the workspace holds.
+__host__ __device__ constexpr uint32_t norm_max_ctas(uint32_t hidden) { return hidden > 2048 ? 512 : 1024; }
+constexpr int kBwdStages = 3;
+
+// Rows of a CTA, range after range: unit u = blockIdx.x, blockIdx.x + ctas, ...
+struct BwdWalk {
+  uint32_t u;
+  uint64_t t, last;
+  __device__ __forceinline__ void open(const NormBwdParams& p) {
+    const uint64_t size = p.gate && p.gate_wide ? p.gate_tokens : p.tokens;
+    const uint32_t group = u / p.splits, split = u - group * p.splits;
+    t = group * size + size * split / p.splits;
+    last = group * size + size * (split + 1) / p.splits;
+  }
+  __device__ __forceinline__ bool valid(const NormBwdParams& p) const { return u < p.units; }
+  // Moves on by a row; true if that ended the unit.  No unit is empty.
+  __device__ __forceinline__ bool next(const NormBwdParams& p) {
+    if (++t < last) return false;
+    u += p.ctas;
+    if (u < p.units) open(p);
+    return true;
+  }
+};
+
+// The ring shape.  Per row: unpack the thread's 8 columns of the four inputs, sum
+// x'^2, u x' and y^2 over the CTA, take G, dx and the column sums, sum v n over
+// the CTA, write dy.  The copies of the next rows run meanwhile; a stage is
+// refilled once the CTA's first sum shows that every thread has unpacked it.
+template <typename T, int V, bool BRANCH, bool NEXT>
+__global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(NormBwdParams p) {
+  constexpr int NV = kNormCols / V, P = kNormCols / 2;
+  constexpr int kGx = 0, kGh = 1, kX = 2, kY = NEXT ? 3 : 1, kArrays = BRANCH && NEXT ? 4 : NEXT ? 3 : 2;
+  using Ring = RowRing<T, V, NV, kArrays, kBwdStages>;
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ __align__(16) float red[2][128];
+  pdl_allow_dependents();
+  for (uint32_t i = threadIdx.x; i < 256; i += blockDim.x) red[i >> 7][i & 127] = 0.f;
+  pdl_wait();
+  const Ring ring{ring_smem, blockDim.x, p.hidden / V};
+  const float inv_d = 1.f / static_cast<float>(p.hidden);
+  const bool wide = BRANCH && p.gate && p.gate_wide, narrow = BRANCH && p.gate && !p.gate_wide;
+  float* gate_parts = p.parts + static_cast<uint64_t>(p.ctas) * 2 * p.hidden;
+
+  const T *gx_at = static_cast<const T*>(p.dx_new), *gh_at = static_cast<const T*>(p.dh);
+  const T *x_at = static_cast<const T*>(p.x_new), *y_at = static_cast<const T*>(p.y);
+  BwdWalk ahead{blockIdx.x, 0, 0}, now{blockIdx.x, 0, 0};
+  ahead.open(p);
+  now.open(p);
+  auto issue = [&](int stage) {
+    if (ahead.valid(p)) {
+      if (NEXT) {
+        ring.copy(stage, kGh, gh_at + ahead.t * p.dh_stride);
+        ring.copy(stage, kX, x_at + ahead.t * p.x_new_stride);
+      }
+      if (BRANCH) ring.copy(stage, kY, y_at + ahead.t * p.y_stride);
+      if (p.dx_new) ring.copy(stage, kGx, gx_at + ahead.t * p.dx_new_stride);
+      ahead.next(p);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kBwdStages; s++) issue(s);
+
+  float2 w2[P], w[P], k[P], sum_n[P], sum_w[P], sum_g[P];
+  if (NEXT) ring.params(p.next_weight, p.params_f32, 0, w2);
+  if (BRANCH) ring.params(p.weight, p.params_f32, 0, w);
+#pragma unroll
+  for (int i = 0; i < P; i++) k[i] = splat(1.f), sum_n[i] = sum_w[i] = sum_g[i] = splat(0.f);
+  if (wide) ring.params(p.gate, p.params_f32, (now.u / p.splits) * static_cast<uint64_t>(p.hidden), k);
+
+  // This thread's columns of a sum: fp32 to the workspace, or a finished row in the parameters' type.
+  auto flush = [&](const float2(&s)[P], float* parts, void* dst, uint64_t first) {
+    const float* flat = reinterpret_cast<const float*>(s);
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        const uint32_t col = (threadIdx.x + i * blockDim.x) * V + j;
+        if (col >= p.hidden) continue;
+        if (parts)
+          parts[first + col] = flat[i * V + j];
+        else if (p.params_f32)
+          static_cast<float*>(dst)[first + col] = flat[i * V + j];
+        else
+          static_cast<T*>(dst)[first + col] = from_f32<T>(flat[i * V + j]);
+      }
+  };
+
+  cp_async_wait<kBwdStages - 1>();
+  __syncthreads();
+  int stage = 0;
+  while (now.valid(p)) {
+    const uint64_t t = now.t;
+    float2 g[P], h[P], x[P], y[P];
+    float sums[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.dx_new) {
+      ring.get(stage, kGx, gx_at + t * p.dx_new_stride, g);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; i++) g[i] = splat(0.f);
+    }
+    if (NEXT) {
+      ring.get(stage, kGh, gh_at + t * p.dh_stride, h);
+      ring.get(stage, kX, x_at + t * p.x_new_stride, x);
+      float2 xx = splat(0.f), ux = splat(0.f);
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        xx = __ffma2_rn(x[i], x[i], xx);
+        ux = __ffma2_rn(__fmul2_rn(h[i], w2[i]), x[i], ux);
+      }
+      sums[0] = xx.x + xx.y;
+      sums[1] = ux.x + ux.y;
+    }
+    if (BRANCH) {
+      ring.get(stage, kY, y_at + t * p.y_stride, y);
+      float2 yy = splat(0.f);
+#pragma unroll
+      for (int i = 0; i < P; i++) yy = __ffma2_rn(y[i], y[i], yy);
+      sums[2] = yy.x + yy.y;
+    }
+    cp_async_wait<kBwdStages - 2>();  // the next row, which the barrier below shows to all
+    block_sum_shared<4>(sums, red[0]);
+    issue(stage);
+    if (NEXT) {
+      const float r2 = rsqrtf(sums[0] * inv_d + p.eps);
+      const float2 rr = splat(r2), m = splat(-sums[1] * r2 * inv_d);  // -mean(u n2)
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        const float2 n2 = __fmul2_rn(x[i], rr);
+        g[i] = __ffma2_rn(rr, __ffma2_rn(n2, m, __fmul2_rn(h[i], w2[i])), g[i]);
+        sum_n[i] = __ffma2_rn(h[i], n2, sum_n[i]);
+      }
+    }
+    float2 o[P];
+    const float2 a = splat(p.residual_scale);
+#pragma unroll
+    for (int i = 0; i < P; i++) o[i] = __fmul2_rn(a, g[i]);
+    ring.put(static_cast<T*>(p.dx) + t * p.hidden, o);
+    if (BRANCH) {
+      const float r = rsqrtf(sums[2] * inv_d + p.eps);
+      if (narrow) {
+        const float one = load_param<T>(p.gate, p.params_f32, t / p.gate_tokens);
+#pragma unroll
+        for (int i = 0; i < P; i++) k[i] = splat(one);
+      }
+      float2 vn = splat(0.f), en = splat(0.f);
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        const float2 gk = __fmul2_rn(g[i], k[i]);
+        y[i] = __fmul2_rn(y[i], splat(r));  // n
+        if (wide) sum_g[i] = __ffma2_rn(__fmul2_rn(g[i], y[i]), w[i], sum_g[i]);
+        if (narrow) en = __ffma2_rn(__fmul2_rn(g[i], y[i]), w[i], en);
+        sum_w[i] = __ffma2_rn(gk, y[i], sum_w[i]);
+        g[i] = __fmul2_rn(gk, w[i]);  // v
+        vn = __ffma2_rn(g[i], y[i], vn);
+      }
+      float dots[2] = {vn.x + vn.y, en.x + en.y};
+      block_sum_shared<2>(dots, red[1]);
+      const float2 m = splat(-dots[0] * inv_d), rr = splat(r);
+#pragma unroll
+      for (int i = 0; i < P; i++) g[i] = __fmul2_rn(rr, __ffma2_rn(y[i], m, g[i]));
+      ring.put(static_cast<T*>(p.dy) + t * p.hidden, g);
+      if (narrow && threadIdx.x == 0) {
+        if (p.gate_tokens > 1)
+          gate_parts[t] = dots[1];
+        else if (p.params_f32)
+          static_cast<float*>(p.dgate)[t] = dots[1];
+        else
+          static_cast<T*>(p.dgate)[t] = from_f32<T>(dots[1]);
+      }
+    } else {
+      __syncthreads();  // the next row's sums take the same buffer
+    }
+    const uint32_t u = now.u;
+    if (now.next(p) && wide) {
+      if (p.splits > 1)
+        flush(sum_g, gate_parts, nullptr, static_cast<uint64_t>(u) * p.hidden);
+      else
+        flush(sum_g, nullptr, p.dgate, static_cast<uint64_t>(u) * p.hidden);
+#pragma unroll
+      for (int i = 0; i < P; i++) sum_g[i] = splat(0.f);
+      if (now.valid(p)) ring.params(p.gate, p.params_f32, (now.u / p.splits) * static_cast<uint64_t>(p.hidden), k);
+    }
+    stage = stage + 1 == kBwdStages ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
+  const uint64_t mine = static_cast<uint64_t>(blockIdx.x) * 2 * p.hidden;
+  if (BRANCH) flush(sum_w, p.parts, nullptr, mine);
+  if (NEXT) flush(sum_n, p.parts, nullptr, mine + p.hidden);
+}
 
 template <typename T, int V, int NV, bool WARP, bool BRANCH, bool NEXT, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormBwdParams p) {
@@ -288,20 +477,15 @@ __global__ void __launch_bounds__(256) norm_narrow_gate_kernel(NormBwdParams p) 
     static_cast<T*>(p.dgate)[blockIdx.x] = from_f32<T>(s[0]);
 }
 
-template <typename T, int V, int NV, bool WARP, int THREADS>
-cudaError_t run_shape(NormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
-  const void* fn = nullptr;
-  if (p.y && p.next_weight)
-    fn = reinterpret_cast<const void*>(norm_bwd_kernel<T, V, NV, WARP, true, true, THREADS>);
-  else if (p.y)
-    fn = reinterpret_cast<const void*>(norm_bwd_kernel<T, V, NV, WARP, true, false, THREADS>);
-  else
-    fn = reinterpret_cast<const void*>(norm_bwd_kernel<T, V, NV, WARP, false, true, THREADS>);
+// Cuts the rows into ranges for at most `most` CTAs (a range lies in one gate row's tokens; `per_turn` rows are
+// the least worth one), launches `fn` and adds up what it left.
+template <typename T>
+cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint32_t per_turn, int threads, int smem,
+                          cudaStream_t stream) {
   const bool wide = p.gate && p.gate_wide;
-  uint64_t most = 2ull * static_cast<uint64_t>(dev.sm_count);
-  if (most > kNormMaxCtas) most = kNormMaxCtas;
+  if (most > norm_max_ctas(p.hidden)) most = norm_max_ctas(p.hidden);
   const uint64_t groups = wide ? p.gate_rows : 1, size = wide ? p.gate_tokens : p.tokens;
-  const uint64_t turns = WARP ? (size + kNormWarps - 1) / kNormWarps : size;  // most ranges worth making of a group
+  const uint64_t turns = (size + per_turn - 1) / per_turn;
   uint64_t splits = groups >= most ? 1 : most / groups;
   if (splits > turns) splits = turns;  // no tokens: no ranges, and the sums over none of them are zero
   p.splits = static_cast<uint32_t>(splits);
@@ -311,7 +495,7 @@ cudaError_t run_shape(NormBwdParams& p, int threads, cudaStream_t stream, const 
   p.ctas = static_cast<uint32_t>(units < most ? units : most);
   void* args[] = {&p};
   cudaError_t e = cudaSuccess;
-  if (p.ctas) e = launch_kernel(fn, dim3(p.ctas), dim3(threads), 0, stream, args, false);
+  if (p.ctas) e = launch_kernel(fn, dim3(p.ctas), dim3(threads), smem, stream, args, false);
   if (e != cudaSuccess) return e;
   const uint32_t jobs = 2 + (wide && splits != 1 ? static_cast<uint32_t>(groups) : 0u);
   e = launch_kernel(reinterpret_cast<const void*>(norm_parts_kernel<T>), dim3((p.hidden + 31) / 32, jobs), dim3(256), 0,
@@ -321,25 +505,73 @@ cudaError_t run_shape(NormBwdParams& p, int threads, cudaStream_t stream, const 
                        dim3(static_cast<unsigned>(p.gate_rows)), dim3(256), 0, stream, args, false);
 }
 
+template <typename T, int V, int NV, bool WARP, int THREADS>
+cudaError_t run_shape(NormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
+  const void* fn = nullptr;
+  if (p.y && p.next_weight)
+    fn = reinterpret_cast<const void*>(norm_bwd_kernel<T, V, NV, WARP, true, true, THREADS>);
+  else if (p.y)
+    fn = reinterpret_cast<const void*>(norm_bwd_kernel<T, V, NV, WARP, true, false, THREADS>);
+  else
+    fn = reinterpret_cast<const void*>(norm_bwd_kernel<T, V, NV, WARP, false, true, THREADS>);
+  return launch_ranges<T>(p, fn, 2ull * static_cast<uint64_t>(dev.sm_count), WARP ? kNormWarps : 1, threads, 0, stream);
+}
+
+template <typename T, int V, bool BRANCH, bool NEXT>
+cudaError_t run_ring(NormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
+  static RingPrep prep;
+  constexpr int kArrays = BRANCH && NEXT ? 4 : NEXT ? 3 : 2;
+  const int smem = static_cast<int>(RowRing<T, V, kNormCols / V, kArrays, kBwdStages>::bytes(threads));
+  const void* fn = reinterpret_cast<const void*>(norm_bwd_ring_kernel<T, V, BRANCH, NEXT>);
+  int per_sm = 0;
+  cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, &per_sm);
+  if (e != cudaSuccess) return e;
+  return launch_ranges<T>(p, fn, static_cast<uint64_t>(per_sm) * static_cast<uint64_t>(dev.sm_count), 1, threads, smem,
+                          stream);
+}
+
+template <typename T, int V>
+cudaError_t run_width(NormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
+  const uint32_t d = p.hidden;
+  if (d <= kNormWarpWidth) {
+    if (V > 1 && d <= 256) return run_shape<T, V, V == 1 ? 16 : 8 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
+    return run_shape<T, V, 16 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
+  }
+  const int threads = static_cast<int>((d + kNormCols * 32 - 1) / (kNormCols * 32) * 32);
+  if (threads <= kNormRingThreads &&
+      RowRing<T, V, kNormCols / V, 4, kBwdStages>::bytes(threads) <= kNormRingSmem) {
+    if (p.y && p.next_weight) return run_ring<T, V, true, true>(p, threads, stream, dev);
+    if (p.y) return run_ring<T, V, true, false>(p, threads, stream, dev);
+    return run_ring<T, V, false, true>(p, threads, stream, dev);
+  }
+  return run_shape<T, V, 16 / V, false, 1024>(p, static_cast<int>((d + 511) / 512 * 32), stream, dev);
+}
+
 template <typename T>
 cudaError_t run_typed(NormBwdParams& p, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
-  constexpr int V = kPieceOf<T>;
-  const uint32_t d = p.hidden;
-  auto cta = [&](uint32_t per_thread) { return static_cast<int>((d + per_thread * 32 - 1) / (per_thread * 32) * 32); };
-  if (!vec) {
-    if (d <= kNormWarpWidth) return run_shape<T, 1, 16, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
-    return run_shape<T, 1, 16, false, 1024>(p, cta(16), stream, dev);
-  }
-  if (d <= 256) return run_shape<T, V, 8 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
-  if (d <= kNormWarpWidth) return run_shape<T, V, 16 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
-  if (d <= 4096) return run_shape<T, V, 8 / V, false, 512>(p, cta(8), stream, dev);
-  return run_shape<T, V, 16 / V, false, 1024>(p, cta(16), stream, dev);
+  return vec ? run_width<T, kPieceOf<T>>(p, stream, dev) : run_width<T, 1>(p, stream, dev);
 }
 
 }  // namespace
 
+cudaError_t prepare_ring(RingPrep& rp, const void* fn, int threads, int smem_bytes, const DeviceInfo& dev, int* per_sm) {
+  const bool cached = dev.device >= 0 && dev.device < kMaxDevices;
+  std::atomic<int>* known = cached ? &rp.per_sm[dev.device][threads / 32] : nullptr;
+  if (known) {
+    *per_sm = known->load(std::memory_order_acquire);
+    if (*per_sm > 0) return cudaSuccess;
+  }
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingSmem);
+  if (e != cudaSuccess) return e;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, fn, threads, static_cast<size_t>(smem_bytes));
+  if (e != cudaSuccess) return e;
+  if (*per_sm < 1) return cudaErrorInvalidConfiguration;
+  if (known) known->store(*per_sm, std::memory_order_release);
+  return cudaSuccess;
+}
+
 uint64_t norm_workspace_bytes(uint64_t tokens, uint32_t hidden) {
-  const uint64_t ctas = tokens < kNormMaxCtas ? tokens : kNormMaxCtas;
+  const uint64_t ctas = tokens < norm_max_ctas(hidden) ? tokens : norm_max_ctas(hidden);
   return 4 * (3 * ctas * hidden + tokens);
 }
 
