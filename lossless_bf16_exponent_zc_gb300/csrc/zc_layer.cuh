@@ -131,49 +131,52 @@ __device__ __forceinline__ void block_sum_f32(float (&v)[N], float* red) {
   for (int i = 0; i < N; i++) v[i] = warp_sum_f32(lane < warps ? red[i * 32 + lane] : 0.f);
 }
 
-// As block_sum_f32 for one to four values with fewer shuffles: the lanes of a
-// warp first share the values out among them (lane group g, of 32 / 4 or 32 / 2 lanes,
-// ends with value g), the CTA's partial sums are then added the same
-// way.  `red`: 4 x 32 floats, 16-byte aligned, those of absent warps zero (the caller clears all before
-// the first use); as above, two sums in a row need two buffers.
+// As block_sum_f32 for 2, 4 or 8 values with fewer shuffles.  Halving the
+// lanes' groups, every lane keeps half of the values and gives the others to its
+// partner, until the lanes of group g (of 32 / N lanes) hold value g; the
+// rest is a tree inside the group.  The CTA's partial sums are added the
+// same way.  `red`: N x 32 floats, 16-byte aligned, those of absent warps zero
+// (the caller clears them all before the first use); as above, two sums in
+// a row need two buffers.
 template <int N>
 __device__ __forceinline__ void block_sum_shared(float (&v)[N], float* red) {
-  static_assert(N == 2 || N == 4, "lane groups of 16 or 8");
-  const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
-  float s;
-  if (N == 4) {
-    const bool up = lane & 16;
-    float a = up ? v[N - 2] : v[0], b = up ? v[N - 1] : v[1];
-    a += __shfl_xor_sync(kFull, up ? v[0] : v[N - 2], 16);
-    b += __shfl_xor_sync(kFull, up ? v[1] : v[N - 1], 16);
-    const bool odd = lane & 8;
-    s = odd ? b : a;
-    s += __shfl_xor_sync(kFull, odd ? a : b, 8);
-  } else {
-    const bool up = lane & 16;
-    s = up ? v[1] : v[0];
-    s += __shfl_xor_sync(kFull, up ? v[0] : v[1], 16);
-    s += __shfl_xor_sync(kFull, s, 8);
-  }
-  s += __shfl_xor_sync(kFull, s, 4);
-  s += __shfl_xor_sync(kFull, s, 2);
-  s += __shfl_xor_sync(kFull, s, 1);
+  static_assert(N == 2 || N == 4 || N == 8, "lane groups of 16, 8 or 4");
   constexpr uint32_t kGroup = 32 / N;
-  if ((lane & (kGroup - 1)) == 0) red[(lane / kGroup) * 32 + warp] = s;
-  __syncthreads();
-  if (N == 4) {
-    const float4 p = *reinterpret_cast<const float4*>(red + (lane >> 3) * 32 + (lane & 7) * 4);
-    s = (p.x + p.y) + (p.z + p.w);
-  } else {
-    const float2 p = *reinterpret_cast<const float2*>(red + (lane >> 4) * 32 + (lane & 15) * 2);
-    s = p.x + p.y;
-    s += __shfl_xor_sync(kFull, s, 8);
-  }
-  s += __shfl_xor_sync(kFull, s, 4);
-  s += __shfl_xor_sync(kFull, s, 2);
-  s += __shfl_xor_sync(kFull, s, 1);
+  const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+  float s[N];
 #pragma unroll
-  for (int i = 0; i < N; i++) v[i] = __shfl_sync(kFull, s, i * kGroup);
+  for (int i = 0; i < N; i++) s[i] = v[i];
+  int d = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n /= 2, d /= 2) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      const float give = up ? s[i] : s[i + n];
+      s[i] = (up ? s[i + n] : s[i]) + __shfl_xor_sync(kFull, give, d);
+    }
+  }
+#pragma unroll
+  for (; d >= 1; d /= 2) s[0] += __shfl_xor_sync(kFull, s[0], d);
+  if ((lane & (kGroup - 1)) == 0) red[(lane / kGroup) * 32 + warp] = s[0];
+  __syncthreads();
+  const float* part = red + (lane / kGroup) * 32 + (lane & (kGroup - 1)) * N;
+  float sum;
+  if (N == 2) {
+    const float2 a = *reinterpret_cast<const float2*>(part);
+    sum = a.x + a.y;
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(part);
+    sum = (a.x + a.y) + (a.z + a.w);
+    if (N == 8) {
+      const float4 b = *reinterpret_cast<const float4*>(part + 4);
+      sum += (b.x + b.y) + (b.z + b.w);
+    }
+  }
+#pragma unroll
+  for (int i = kGroup / 2; i >= 1; i /= 2) sum += __shfl_xor_sync(kFull, sum, i);
+#pragma unroll
+  for (int i = 0; i < N; i++) v[i] = __shfl_sync(kFull, sum, i * kGroup);
 }
 
 // 4-byte asynchronous copy, both addresses 4-byte aligned.

@@ -105,27 +105,29 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(NormParams p) {
   }
 }
 
-constexpr int kFwdStages = 4;
+constexpr int kFwdStages = 4, kFwdCols = 8;
 
 // The ring shape: rows blockIdx.x, blockIdx.x + CTAs, ... stream through shared memory.
 template <typename T, int V, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormParams p) {
-  constexpr int NV = kNormCols / V, P = kNormCols / 2;
-  using Ring = RowRing<T, V, NV, BRANCH ? 2 : 1, kFwdStages>;
+  constexpr int P = kFwdCols / 2;
+  using Ring = RowRing<T, V, kFwdCols, BRANCH ? 2 : 1, kFwdStages>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ __align__(16) float red[2][128];
   pdl_allow_dependents();
   for (uint32_t i = threadIdx.x; i < 256; i += blockDim.x) red[i >> 7][i & 127] = 0.f;
   pdl_wait();
   const Ring ring{ring_smem, blockDim.x, p.hidden / V};
+#pragma unroll
+  for (int i = 0; i < (BRANCH ? 2 : 1); i++) ring.clear(i, false);
   const float inv_d = 1.f / static_cast<float>(p.hidden);
   const bool wide = BRANCH && p.gate && p.gate_wide, narrow = BRANCH && p.gate && !p.gate_wide;
   const T *x_at = static_cast<const T*>(p.x), *y_at = static_cast<const T*>(p.y);
   uint64_t ahead = blockIdx.x;
   auto issue = [&](int stage) {
     if (ahead < p.tokens) {
-      ring.copy(stage, 0, x_at + ahead * p.x_stride);
-      if (BRANCH) ring.copy(stage, 1, y_at + ahead * p.y_stride);
+      ring.copy(stage, 0, ring.start(x_at, ahead, p.x_stride));
+      if (BRANCH) ring.copy(stage, 1, ring.start(y_at, ahead, p.y_stride));
       ahead += gridDim.x;
     }
     cp_async_commit();
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormPara
       float2 y[P], yy = splat(0.f);
       ring.get(stage, 1, y_at + t * p.y_stride, y);
 #pragma unroll
-      for (int i = 0; i < P; i++) yy = __ffma2_rn(y[i], y[i], yy);
+      for (int i = 0; i < P; i++) yy = fma2(y[i], y[i], yy);
       sums[0] = yy.x + yy.y;
       sums[1] = 0.f;
       cp_async_wait<kFwdStages - 2>();  // the next row, which the barrier below shows to all
@@ -167,13 +169,13 @@ __global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormPara
       }
 #pragma unroll
       for (int i = 0; i < P; i++)
-        x[i] = __ffma2_rn(k[i], __fmul2_rn(__fmul2_rn(y[i], r), w[i]), __fmul2_rn(a, x[i]));
-      ring.put(static_cast<T*>(p.x_new) + t * p.hidden, x);
+        x[i] = fma2(k[i], mul2(mul2(y[i], r), w[i]), mul2(a, x[i]));
+      ring.put(ring.start(static_cast<T*>(p.x_new), t, p.hidden), x);
     }
     if (NEXT) {
       float2 xx = splat(0.f);
 #pragma unroll
-      for (int i = 0; i < P; i++) xx = __ffma2_rn(x[i], x[i], xx);
+      for (int i = 0; i < P; i++) xx = fma2(x[i], x[i], xx);
       sums[0] = xx.x + xx.y;
       sums[1] = 0.f;
       if (!BRANCH) cp_async_wait<kFwdStages - 2>();
@@ -182,8 +184,8 @@ __global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormPara
       if (!BRANCH) issue(stage);
       const float2 r = splat(rsqrtf(sums[0] * inv_d + p.eps));
 #pragma unroll
-      for (int i = 0; i < P; i++) x[i] = __fmul2_rn(__fmul2_rn(x[i], r), w2[i]);
-      ring.put(static_cast<T*>(p.h) + t * p.hidden, x);
+      for (int i = 0; i < P; i++) x[i] = mul2(mul2(x[i], r), w2[i]);
+      ring.put(ring.start(static_cast<T*>(p.h), t, p.hidden), x);
     }
     stage = stage + 1 == kFwdStages ? 0 : stage + 1;
   }
@@ -209,7 +211,7 @@ cudaError_t run_shape(NormParams& p, int threads, cudaStream_t stream, const Dev
 template <typename T, int V, bool BRANCH, bool NEXT>
 cudaError_t run_ring(NormParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
   static RingPrep prep;
-  const int smem = static_cast<int>(RowRing<T, V, kNormCols / V, BRANCH ? 2 : 1, kFwdStages>::bytes(threads));
+  const int smem = static_cast<int>(RowRing<T, V, kFwdCols, BRANCH ? 2 : 1, kFwdStages>::bytes(threads));
   const void* fn = reinterpret_cast<const void*>(norm_ring_kernel<T, V, BRANCH, NEXT>);
   int per_sm = 0;
   cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, &per_sm);
@@ -227,8 +229,8 @@ cudaError_t run_width(NormParams& p, cudaStream_t stream, const DeviceInfo& dev)
     if (V > 1 && d <= 256) return run_shape<T, V, V == 1 ? 16 : 8 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
     return run_shape<T, V, 16 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
   }
-  const int threads = static_cast<int>((d + kNormCols * 32 - 1) / (kNormCols * 32) * 32);
-  if (threads <= kNormRingThreads && RowRing<T, V, kNormCols / V, 2, kFwdStages>::bytes(threads) <= kNormRingSmem) {
+  const int threads = static_cast<int>((d + kFwdCols * 32 - 1) / (kFwdCols * 32) * 32);
+  if (threads <= kNormRingThreads && RowRing<T, V, kFwdCols, 2, kFwdStages>::bytes(threads) <= kNormRingSmem) {
     if (p.y && p.next_weight) return run_ring<T, V, true, true>(p, threads, stream, dev);
     if (p.y) return run_ring<T, V, true, false>(p, threads, stream, dev);
     return run_ring<T, V, false, true>(p, threads, stream, dev);

@@ -34,20 +34,21 @@ __device__ __forceinline__ float load_param(const void* base, int is_f32, uint64
 }
 
 // Launch shapes.  A row of up to kNormWarpWidth values is held by a warp.  Wider rows stream through a CTA's shared
-// memory, one thread for every 8 columns; rows too wide for that ring are held in a CTA's registers.
+// memory, one thread for every 8 or 16 columns; rows too wide for that ring are held in a CTA's registers.
 constexpr uint32_t kNormWarpWidth = 512;
 constexpr int kNormWarps = 8;         // rows of a CTA in the warp shape
-constexpr int kNormCols = 8;          // columns of a thread in the ring shape
 constexpr int kNormRingThreads = 512;
 constexpr int kNormRingSmem = 225 * 1024;  // what the ring may take of the 227 KB a CTA can have
 
 // The ring: the next STAGES rows of ARRAYS matrices, copied asynchronously (16 bytes at a time; 4 where the rows are not
-// so aligned) by the threads of the CTA.  Every thread keeps the same columns in every row, in NV pieces of V
-// values: its pieces lie in slots of its own, so shared memory is read without bank conflicts.  Rows of 16-bit values at odd
-// addresses are copied as the 4-byte words that cover them and read value by value; their first and last
-// word may hold a neighbour's value, which is not used.
-template <typename T, int V, int NV, int ARRAYS, int STAGES>
+// so aligned) by the threads of the CTA.  Every thread keeps the same COLS columns in every row, in NV pieces of V
+// values: its pieces lie in slots of its own, so shared memory is read without bank conflicts and a thread waits for
+// nobody's copies but its own.  Rows of 16-bit values at odd addresses (kWords) are copied as the 4-byte words
+// that cover them and read value by value, by other threads than copied them; their first and last word may hold a
+// neighbour's value, which is not used.
+template <typename T, int V, int COLS, int ARRAYS, int STAGES>
 struct RowRing {
+  static constexpr int NV = COLS / V;
   static constexpr bool kWords = V == 1 && sizeof(T) == 2;
   uint8_t* smem;
   uint32_t threads, pieces;
@@ -60,6 +61,11 @@ struct RowRing {
   __device__ __forceinline__ uint8_t* at(int stage, int array) const {
     return smem + (stage * ARRAYS + array) * region(threads);
   }
+  // Where a thread's walk through a matrix starts: its first column of row t.
+  template <typename U>
+  __device__ __forceinline__ U* start(U* base, uint64_t t, uint64_t stride) const {
+    return base + t * stride + (kWords ? 0 : threadIdx.x * V);
+  }
   __device__ __forceinline__ void copy(int stage, int array, const T* row) const {
     uint8_t* to = at(stage, array);
     if (kWords) {
@@ -68,49 +74,70 @@ struct RowRing {
       const uint32_t* from = reinterpret_cast<const uint32_t*>(a & ~static_cast<uintptr_t>(3));
       for (uint32_t w = threadIdx.x; w < words; w += threads) cp_async_4(to + 4 * w, from + w);
     } else {
+      to += threadIdx.x * V * sizeof(T);
 #pragma unroll
       for (int i = 0; i < NV; i++) {
-        const uint32_t c = threadIdx.x + i * threads;
-        if (c >= pieces) continue;
+        if (threadIdx.x + i * threads >= pieces) continue;
         if (V == 1)
-          cp_async_4(to + c * 4, row + c);
+          cp_async_4(to + i * threads * 4, row + i * threads);
         else
-          cp_async_16(to + c * 16, row + static_cast<uint64_t>(c) * V, 16);
+          cp_async_16(to + i * threads * 16, row + i * threads * V, 16);
       }
     }
   }
-  // This thread's columns of a row; zeros beyond the width.
-  __device__ __forceinline__ void get(int stage, int array, const T* row, float2 (&f)[NV * V / 2]) const {
-    const uint8_t* from = at(stage, array);
-    float* flat = reinterpret_cast<float*>(f);
-    if (kWords) from += reinterpret_cast<uintptr_t>(row) & 2;
+  // Zeroes this thread's slots that no copy ever fills (its columns beyond the width, and all of a matrix that
+  // is not there), so that reading them needs no test.
+  __device__ __forceinline__ void clear(int array, bool all) const {
+    if constexpr (!kWords) {
+      for (int stage = 0; stage < STAGES; stage++)
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-      const uint32_t c = threadIdx.x + i * threads;
-      float v[V];
-#pragma unroll
-      for (int j = 0; j < V; j++) v[j] = 0.f;
-      if (c < pieces) Piece<T, V>::load(reinterpret_cast<const T*>(from) + c * V).get(v);
-#pragma unroll
-      for (int j = 0; j < V; j++) flat[i * V + j] = v[j];
+        for (int i = 0; i < NV; i++) {
+          const uint32_t c = threadIdx.x + i * threads;
+          if (all || c >= pieces) Piece<T, V>::zero().store(reinterpret_cast<T*>(at(stage, array)) + c * V);
+        }
     }
   }
-  // Writes this thread's columns of an output row.
-  __device__ __forceinline__ void put(T* row, const float2 (&f)[NV * V / 2]) const {
-    const float* flat = reinterpret_cast<const float*>(f);
+  // This thread's columns of a row (its address as given to copy()) as they lie in memory; zeros beyond the width.
+  __device__ __forceinline__ void get(int stage, int array, const T* row, Piece<T, V> (&v)[NV]) const {
+    const uint8_t* from = at(stage, array) + (kWords ? reinterpret_cast<uintptr_t>(row) & 2 : 0);
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       const uint32_t c = threadIdx.x + i * threads;
+      v[i] = Piece<T, V>::zero();
+      if (!kWords || c < pieces) v[i] = Piece<T, V>::load(reinterpret_cast<const T*>(from) + c * V);
+    }
+  }
+  __device__ __forceinline__ static void unpack(const Piece<T, V> (&v)[NV], float2 (&f)[COLS / 2]) {
+    float* flat = reinterpret_cast<float*>(f);
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+      float u[V];
+      v[i].get(u);
+#pragma unroll
+      for (int j = 0; j < V; j++) flat[i * V + j] = u[j];
+    }
+  }
+  __device__ __forceinline__ void get(int stage, int array, const T* row, float2 (&f)[COLS / 2]) const {
+    Piece<T, V> v[NV];
+    get(stage, array, row, v);
+    unpack(v, f);
+  }
+  // Writes this thread's columns of an output row, from its address by start().
+  __device__ __forceinline__ void put(T* row, const float2 (&f)[COLS / 2]) const {
+    const float* flat = reinterpret_cast<const float*>(f);
+    if (kWords) row += threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
       float v[V];
 #pragma unroll
       for (int j = 0; j < V; j++) v[j] = flat[i * V + j];
       Piece<T, V> o;
       o.set(v);
-      if (c < pieces) o.store(row + static_cast<uint64_t>(c) * V);
+      if (threadIdx.x + i * threads < pieces) o.store(row + i * threads * V);
     }
   }
   // This thread's columns of a parameter row.
-  __device__ __forceinline__ void params(const void* base, int is_f32, uint64_t first, float2 (&f)[NV * V / 2]) const {
+  __device__ __forceinline__ void params(const void* base, int is_f32, uint64_t first, float2 (&f)[COLS / 2]) const {
     float* flat = reinterpret_cast<float*>(f);
 #pragma unroll
     for (int i = 0; i < NV; i++) {
@@ -126,6 +153,13 @@ struct RowRing {
 };
 
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+#ifdef ZC_SCALAR
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+#else
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+#endif
 
 // CTAs of a ring kernel on one SM, by CTA size (the ring's size follows from it); looked up once per device and size.
 struct RingPrep {

@@ -18,194 +18,276 @@ namespace zc {
 namespace {
 
 // Most CTAs whose sums the workspace holds.
-__host__ __device__ constexpr uint32_t norm_max_ctas(uint32_t hidden) { return hidden > 2048 ? 512 : 1024; }
+__host__ __device__ constexpr uint32_t norm_max_ctas(uint32_t hidden) { return hidden > 2048 ? 608 : 1216; }
 constexpr int kBwdStages = 3;
 
-// Rows of a CTA, range after range: unit u = blockIdx.x, blockIdx.x + ctas, ...
+// Columns of a thread in the ring shape.  With 8 the column sums, the weights and a row fit the 128 registers of a
+// 512-thread CTA; 16 columns in 256 threads, two CTAs an SM, spill 260 bytes a thread and take 170 us instead of 130
+// (16384 x 4096 bf16), and 8 in 64 registers, again for two CTAs, 238 us: the ring leaves the L1 cache too small for
+// spilled registers.
+constexpr int kBwdCols = 8;
+
+// Rows of a CTA, unit after unit: u = blockIdx.x, blockIdx.x + ctas, ...  A unit takes every splits-th row of a gate
+// row's tokens, so that neighbouring CTAs read neighbouring rows at about the same time.
 struct BwdWalk {
   uint32_t u;
   uint64_t t, last;
   __device__ __forceinline__ void open(const NormBwdParams& p) {
     const uint64_t size = p.gate && p.gate_wide ? p.gate_tokens : p.tokens;
-    const uint32_t group = u / p.splits, split = u - group * p.splits;
-    t = group * size + size * split / p.splits;
-    last = group * size + size * (split + 1) / p.splits;
+    const uint32_t group = u / p.splits;
+    t = group * size + (u - group * p.splits);
+    last = group * size + size;
   }
   __device__ __forceinline__ bool valid(const NormBwdParams& p) const { return u < p.units; }
   // Moves on by a row; true if that ended the unit.  No unit is empty.
   __device__ __forceinline__ bool next(const NormBwdParams& p) {
-    if (++t < last) return false;
+    t += p.splits;
+    if (t < last) return false;
     u += p.ctas;
     if (u < p.units) open(p);
     return true;
   }
 };
 
-// The ring shape.  Per row: unpack the thread's 8 columns of the four inputs, sum
-// x'^2, u x' and y^2 over the CTA, take G, dx and the column sums, sum v n over
-// the CTA, write dy.  The copies of the next rows run meanwhile; a stage is
-// refilled once the CTA's first sum shows that every thread has unpacked it.
+// The ring shape.  A row takes two sums over the CTA, of x'^2, u x' and y^2 and then, once G is known, of v y.  The
+// second is taken together with the next row's first, so that a row costs one barrier: between two barriers the CTA
+// writes the last row's dy, takes this row's G, dx, column sums and v y, and the next row's first sums.  The inputs are
+// read from the stage twice rather than held, so that the column sums and the weights stay in registers.
 template <typename T, int V, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(NormBwdParams p) {
-  constexpr int NV = kNormCols / V, P = kNormCols / 2;
+  constexpr int C = kBwdCols, P = C / 2;
   constexpr int kGx = 0, kGh = 1, kX = 2, kY = NEXT ? 3 : 1, kArrays = BRANCH && NEXT ? 4 : NEXT ? 3 : 2;
-  using Ring = RowRing<T, V, NV, kArrays, kBwdStages>;
+  using Ring = RowRing<T, V, C, kArrays, kBwdStages>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ __align__(16) float red[2][128];
   pdl_allow_dependents();
-  for (uint32_t i = threadIdx.x; i < 256; i += blockDim.x) red[i >> 7][i & 127] = 0.f;
+  for (uint32_t i = threadIdx.x; i < 256; i += blockDim.x) red[0][i] = 0.f;
   pdl_wait();
   const Ring ring{ring_smem, blockDim.x, p.hidden / V};
   const float inv_d = 1.f / static_cast<float>(p.hidden);
   const bool wide = BRANCH && p.gate && p.gate_wide, narrow = BRANCH && p.gate && !p.gate_wide;
+  const bool past = p.dx_new != nullptr;
   float* gate_parts = p.parts + static_cast<uint64_t>(p.ctas) * 2 * p.hidden;
+#pragma unroll
+  for (int i = 0; i < kArrays; i++) ring.clear(i, i == kGx && !past);
 
-  const T *gx_at = static_cast<const T*>(p.dx_new), *gh_at = static_cast<const T*>(p.dh);
-  const T *x_at = static_cast<const T*>(p.x_new), *y_at = static_cast<const T*>(p.y);
+  // Addresses of the row to copy next and, for rows at odd addresses, of the row being computed.
+  const T *gx = nullptr, *gh = nullptr, *x = nullptr, *y = nullptr;
   BwdWalk ahead{blockIdx.x, 0, 0}, now{blockIdx.x, 0, 0};
   ahead.open(p);
   now.open(p);
+  auto aim = [&](uint64_t t) {
+    if (past) gx = ring.start(static_cast<const T*>(p.dx_new), t, p.dx_new_stride);
+    if (NEXT) {
+      gh = ring.start(static_cast<const T*>(p.dh), t, p.dh_stride);
+      x = ring.start(static_cast<const T*>(p.x_new), t, p.x_new_stride);
+    }
+    if (BRANCH) y = ring.start(static_cast<const T*>(p.y), t, p.y_stride);
+  };
+  aim(ahead.t);
   auto issue = [&](int stage) {
     if (ahead.valid(p)) {
       if (NEXT) {
-        ring.copy(stage, kGh, gh_at + ahead.t * p.dh_stride);
-        ring.copy(stage, kX, x_at + ahead.t * p.x_new_stride);
+        ring.copy(stage, kGh, gh);
+        ring.copy(stage, kX, x);
+        gh += p.dh_stride * p.splits;
+        x += p.x_new_stride * p.splits;
       }
-      if (BRANCH) ring.copy(stage, kY, y_at + ahead.t * p.y_stride);
-      if (p.dx_new) ring.copy(stage, kGx, gx_at + ahead.t * p.dx_new_stride);
-      ahead.next(p);
+      if (BRANCH) {
+        ring.copy(stage, kY, y);
+        y += p.y_stride * p.splits;
+      }
+      if (past) {
+        ring.copy(stage, kGx, gx);
+        gx += p.dx_new_stride * p.splits;
+      }
+      if (ahead.next(p) && ahead.valid(p)) aim(ahead.t);
     }
     cp_async_commit();
+  };
+  // The address of the row at hand, of which only rows at odd addresses need to know.
+  auto row_of = [&](const void* base, uint64_t t, uint64_t stride) {
+    return Ring::kWords ? static_cast<const T*>(base) + t * stride : nullptr;
   };
 #pragma unroll
   for (int s = 0; s < kBwdStages; s++) issue(s);
 
-  float2 w2[P], w[P], k[P], sum_n[P], sum_w[P], sum_g[P];
+  // w2, and g w of the unit's gate row (w alone under a one-column gate); the sums of dh n2, and of G n over the
+  // unit, which give the weight's gradient times g and the gate's times w when the unit ends.
+  float2 w2[P], gw[P], sum_n[P], sum_b[P];
   if (NEXT) ring.params(p.next_weight, p.params_f32, 0, w2);
-  if (BRANCH) ring.params(p.weight, p.params_f32, 0, w);
+  auto open_unit = [&](uint32_t u) {
+    ring.params(p.weight, p.params_f32, 0, gw);
+    if (wide) {
+      float2 k[P];
+      ring.params(p.gate, p.params_f32, (u / p.splits) * static_cast<uint64_t>(p.hidden), k);
 #pragma unroll
-  for (int i = 0; i < P; i++) k[i] = splat(1.f), sum_n[i] = sum_w[i] = sum_g[i] = splat(0.f);
-  if (wide) ring.params(p.gate, p.params_f32, (now.u / p.splits) * static_cast<uint64_t>(p.hidden), k);
-
-  // This thread's columns of a sum: fp32 to the workspace, or a finished row in the parameters' type.
-  auto flush = [&](const float2(&s)[P], float* parts, void* dst, uint64_t first) {
-    const float* flat = reinterpret_cast<const float*>(s);
+      for (int i = 0; i < P; i++) gw[i] = mul2(gw[i], k[i]);
+    }
 #pragma unroll
-    for (int i = 0; i < NV; i++)
+    for (int i = 0; i < P; i++) sum_b[i] = splat(0.f);
+  };
+  float* mine = p.parts + static_cast<uint64_t>(blockIdx.x) * 2 * p.hidden;
+  auto close_unit = [&](uint32_t u) {
+    const float* fb = reinterpret_cast<const float*>(sum_b);
+#pragma unroll
+    for (int i = 0; i < Ring::NV; i++) {
+      const uint32_t c = threadIdx.x + i * blockDim.x;
+      if (c >= ring.pieces) continue;
+      float k[V], w[V];
+      if (wide) {
+        load_params<T, V>(p.gate, p.params_f32, (u / p.splits) * static_cast<uint64_t>(p.hidden) + c * V, k);
+        load_params<T, V>(p.weight, p.params_f32, c * V, w);
+      }
 #pragma unroll
       for (int j = 0; j < V; j++) {
-        const uint32_t col = (threadIdx.x + i * blockDim.x) * V + j;
-        if (col >= p.hidden) continue;
-        if (parts)
-          parts[first + col] = flat[i * V + j];
+        const float b = fb[i * V + j], dw = wide ? b * k[j] : b;
+        float* sum = mine + c * V + j;
+        *sum = u == blockIdx.x ? dw : *sum + dw;  // the CTA's first unit has its number
+        if (!wide) continue;
+        const uint64_t at = static_cast<uint64_t>(u) * p.hidden + c * V + j;
+        if (p.splits > 1)
+          gate_parts[at] = b * w[j];
         else if (p.params_f32)
-          static_cast<float*>(dst)[first + col] = flat[i * V + j];
+          static_cast<float*>(p.dgate)[at] = b * w[j];
         else
-          static_cast<T*>(dst)[first + col] = from_f32<T>(flat[i * V + j]);
+          static_cast<T*>(p.dgate)[at] = from_f32<T>(b * w[j]);
       }
-  };
-
-  cp_async_wait<kBwdStages - 1>();
-  __syncthreads();
-  int stage = 0;
-  while (now.valid(p)) {
-    const uint64_t t = now.t;
-    float2 g[P], h[P], x[P], y[P];
-    float sums[4] = {0.f, 0.f, 0.f, 0.f};
-    if (p.dx_new) {
-      ring.get(stage, kGx, gx_at + t * p.dx_new_stride, g);
-    } else {
-#pragma unroll
-      for (int i = 0; i < P; i++) g[i] = splat(0.f);
     }
+  };
+#pragma unroll
+  for (int i = 0; i < P; i++) sum_n[i] = splat(0.f);
+  if (BRANCH) open_unit(now.u);
+
+  // Partial sums of row t's x'^2, u x' and y^2.
+  auto first_sums = [&](int stage, uint64_t t, float (&sums)[4]) {
     if (NEXT) {
-      ring.get(stage, kGh, gh_at + t * p.dh_stride, h);
-      ring.get(stage, kX, x_at + t * p.x_new_stride, x);
-      float2 xx = splat(0.f), ux = splat(0.f);
+      float2 h[P], v[P], xx = splat(0.f), ux = splat(0.f);
+      ring.get(stage, kGh, row_of(p.dh, t, p.dh_stride), h);
+      ring.get(stage, kX, row_of(p.x_new, t, p.x_new_stride), v);
 #pragma unroll
       for (int i = 0; i < P; i++) {
-        xx = __ffma2_rn(x[i], x[i], xx);
-        ux = __ffma2_rn(__fmul2_rn(h[i], w2[i]), x[i], ux);
+        xx = fma2(v[i], v[i], xx);
+        ux = fma2(mul2(h[i], w2[i]), v[i], ux);
       }
       sums[0] = xx.x + xx.y;
       sums[1] = ux.x + ux.y;
     }
     if (BRANCH) {
-      ring.get(stage, kY, y_at + t * p.y_stride, y);
-      float2 yy = splat(0.f);
+      float2 v[P], yy = splat(0.f);
+      ring.get(stage, kY, row_of(p.y, t, p.y_stride), v);
 #pragma unroll
-      for (int i = 0; i < P; i++) yy = __ffma2_rn(y[i], y[i], yy);
+      for (int i = 0; i < P; i++) yy = fma2(v[i], v[i], yy);
       sums[2] = yy.x + yy.y;
     }
-    cp_async_wait<kBwdStages - 2>();  // the next row, which the barrier below shows to all
-    block_sum_shared<4>(sums, red[0]);
-    issue(stage);
+  };
+
+  // Between barriers: `t` is the row whose first sums are known; v (in g), y and the scalars of the row before wait for
+  // their last sum.
+  float2 g[P];
+  Piece<T, V> y_row[Ring::NV];
+  uint64_t before = ~0ull;
+  float root = 0.f, one = 1.f;
+  float sums[4] = {0.f, 0.f, 0.f, 0.f};
+  auto finish = [&](float vy) {  // dy of the row before
+    const float2 m = splat(-(vy * root * inv_d) * root), rr = splat(root * one);
+    float2 v[P];
+    Ring::unpack(y_row, v);
+#pragma unroll
+    for (int i = 0; i < P; i++) v[i] = mul2(rr, fma2(v[i], m, g[i]));
+    ring.put(ring.start(static_cast<T*>(p.dy), before, p.hidden), v);
+    if (narrow && threadIdx.x == 0) {
+      const float dg = root * vy;  // sum of G n w
+      if (p.gate_tokens > 1)
+        gate_parts[before] = dg;
+      else if (p.params_f32)
+        static_cast<float*>(p.dgate)[before] = dg;
+      else
+        static_cast<T*>(p.dgate)[before] = from_f32<T>(dg);
+    }
+  };
+
+  int stage = 0, turn = 0;
+  cp_async_wait<kBwdStages - 1>();
+  if (Ring::kWords) __syncthreads();
+  first_sums(0, now.t, sums);
+  block_sum_shared<4>(sums, red[1]);
+  while (now.valid(p)) {
+    const uint64_t t = now.t;
+    if (BRANCH && before != ~0ull) finish(sums[3]);
+    if (!Ring::kWords || past) {
+      ring.get(stage, kGx, row_of(p.dx_new, t, p.dx_new_stride), g);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; i++) g[i] = splat(0.f);
+    }
     if (NEXT) {
       const float r2 = rsqrtf(sums[0] * inv_d + p.eps);
-      const float2 rr = splat(r2), m = splat(-sums[1] * r2 * inv_d);  // -mean(u n2)
+      const float2 rr = splat(r2), m = splat(-(sums[1] * r2 * inv_d) * r2 * r2);  // -r2^2 mean(u n2)
+      float2 h[P], v[P];
+      ring.get(stage, kGh, row_of(p.dh, t, p.dh_stride), h);
+      ring.get(stage, kX, row_of(p.x_new, t, p.x_new_stride), v);
 #pragma unroll
       for (int i = 0; i < P; i++) {
-        const float2 n2 = __fmul2_rn(x[i], rr);
-        g[i] = __ffma2_rn(rr, __ffma2_rn(n2, m, __fmul2_rn(h[i], w2[i])), g[i]);
-        sum_n[i] = __ffma2_rn(h[i], n2, sum_n[i]);
+        g[i] = fma2(rr, mul2(h[i], w2[i]), fma2(v[i], m, g[i]));
+        sum_n[i] = fma2(h[i], mul2(v[i], rr), sum_n[i]);
       }
     }
-    float2 o[P];
-    const float2 a = splat(p.residual_scale);
+    {
+      float2 o[P];
+      const float2 a = splat(p.residual_scale);
 #pragma unroll
-    for (int i = 0; i < P; i++) o[i] = __fmul2_rn(a, g[i]);
-    ring.put(static_cast<T*>(p.dx) + t * p.hidden, o);
+      for (int i = 0; i < P; i++) o[i] = mul2(a, g[i]);
+      ring.put(ring.start(static_cast<T*>(p.dx), t, p.hidden), o);
+    }
+    sums[3] = 0.f;
     if (BRANCH) {
-      const float r = rsqrtf(sums[2] * inv_d + p.eps);
-      if (narrow) {
-        const float one = load_param<T>(p.gate, p.params_f32, t / p.gate_tokens);
-#pragma unroll
-        for (int i = 0; i < P; i++) k[i] = splat(one);
-      }
-      float2 vn = splat(0.f), en = splat(0.f);
+      root = rsqrtf(sums[2] * inv_d + p.eps);
+      one = narrow ? load_param<T>(p.gate, p.params_f32, t / p.gate_tokens) : 1.f;
+      const float2 rr = splat(root * one);
+      float2 v[P], vy = splat(0.f);
+      ring.get(stage, kY, row_of(p.y, t, p.y_stride), y_row);
+      Ring::unpack(y_row, v);
 #pragma unroll
       for (int i = 0; i < P; i++) {
-        const float2 gk = __fmul2_rn(g[i], k[i]);
-        y[i] = __fmul2_rn(y[i], splat(r));  // n
-        if (wide) sum_g[i] = __ffma2_rn(__fmul2_rn(g[i], y[i]), w[i], sum_g[i]);
-        if (narrow) en = __ffma2_rn(__fmul2_rn(g[i], y[i]), w[i], en);
-        sum_w[i] = __ffma2_rn(gk, y[i], sum_w[i]);
-        g[i] = __fmul2_rn(gk, w[i]);  // v
-        vn = __ffma2_rn(g[i], y[i], vn);
+        sum_b[i] = fma2(g[i], mul2(v[i], rr), sum_b[i]);
+        g[i] = mul2(g[i], gw[i]);  // v, but for a one-column gate
+        vy = fma2(g[i], v[i], vy);
       }
-      float dots[2] = {vn.x + vn.y, en.x + en.y};
-      block_sum_shared<2>(dots, red[1]);
-      const float2 m = splat(-dots[0] * inv_d), rr = splat(r);
-#pragma unroll
-      for (int i = 0; i < P; i++) g[i] = __fmul2_rn(rr, __ffma2_rn(y[i], m, g[i]));
-      ring.put(static_cast<T*>(p.dy) + t * p.hidden, g);
-      if (narrow && threadIdx.x == 0) {
-        if (p.gate_tokens > 1)
-          gate_parts[t] = dots[1];
-        else if (p.params_f32)
-          static_cast<float*>(p.dgate)[t] = dots[1];
-        else
-          static_cast<T*>(p.dgate)[t] = from_f32<T>(dots[1]);
-      }
-    } else {
-      __syncthreads();  // the next row's sums take the same buffer
+      sums[3] = vy.x + vy.y;
     }
-    const uint32_t u = now.u;
-    if (now.next(p) && wide) {
-      if (p.splits > 1)
-        flush(sum_g, gate_parts, nullptr, static_cast<uint64_t>(u) * p.hidden);
-      else
-        flush(sum_g, nullptr, p.dgate, static_cast<uint64_t>(u) * p.hidden);
-#pragma unroll
-      for (int i = 0; i < P; i++) sum_g[i] = splat(0.f);
-      if (now.valid(p)) ring.params(p.gate, p.params_f32, (now.u / p.splits) * static_cast<uint64_t>(p.hidden), k);
+    const int done = stage;
+    if (!Ring::kWords) issue(done);
+    before = t;
+    const uint32_t unit = now.u;
+    if (now.next(p) && BRANCH) {
+      close_unit(unit);
+      if (now.valid(p)) open_unit(now.u);
     }
     stage = stage + 1 == kBwdStages ? 0 : stage + 1;
+    sums[0] = sums[1] = sums[2] = 0.f;
+    if (now.valid(p)) {
+      // the next row: all but the copies issued after its own
+      cp_async_wait<Ring::kWords ? kBwdStages - 2 : kBwdStages - 1>();
+      if (Ring::kWords) __syncthreads();
+      first_sums(stage, now.t, sums);
+    }
+    block_sum_shared<4>(sums, red[turn]);
+    turn ^= 1;
+    if (Ring::kWords) issue(done);  // now every thread is past its last reading of the row
   }
+  if (BRANCH) finish(sums[3]);
   cp_async_wait<0>();
-  const uint64_t mine = static_cast<uint64_t>(blockIdx.x) * 2 * p.hidden;
-  if (BRANCH) flush(sum_w, p.parts, nullptr, mine);
-  if (NEXT) flush(sum_n, p.parts, nullptr, mine + p.hidden);
+  if (NEXT) {
+    const float* fn = reinterpret_cast<const float*>(sum_n);
+#pragma unroll
+    for (int i = 0; i < Ring::NV; i++)
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        const uint32_t col = (threadIdx.x + i * blockDim.x) * V + j;
+        if (col < p.hidden) mine[p.hidden + col] = fn[i * V + j];
+      }
+  }
 }
 
 template <typename T, int V, int NV, bool WARP, bool BRANCH, bool NEXT, int THREADS>
@@ -521,7 +603,7 @@ template <typename T, int V, bool BRANCH, bool NEXT>
 cudaError_t run_ring(NormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
   static RingPrep prep;
   constexpr int kArrays = BRANCH && NEXT ? 4 : NEXT ? 3 : 2;
-  const int smem = static_cast<int>(RowRing<T, V, kNormCols / V, kArrays, kBwdStages>::bytes(threads));
+  const int smem = static_cast<int>(RowRing<T, V, kBwdCols, kArrays, kBwdStages>::bytes(threads));
   const void* fn = reinterpret_cast<const void*>(norm_bwd_ring_kernel<T, V, BRANCH, NEXT>);
   int per_sm = 0;
   cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, &per_sm);
@@ -537,9 +619,9 @@ cudaError_t run_width(NormBwdParams& p, cudaStream_t stream, const DeviceInfo& d
     if (V > 1 && d <= 256) return run_shape<T, V, V == 1 ? 16 : 8 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
     return run_shape<T, V, 16 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
   }
-  const int threads = static_cast<int>((d + kNormCols * 32 - 1) / (kNormCols * 32) * 32);
-  if (threads <= kNormRingThreads &&
-      RowRing<T, V, kNormCols / V, 4, kBwdStages>::bytes(threads) <= kNormRingSmem) {
+  constexpr uint32_t kCols = kBwdCols;
+  const int threads = static_cast<int>((d + kCols * 32 - 1) / (kCols * 32) * 32);
+  if (threads <= kNormRingThreads && RowRing<T, V, kCols, 4, kBwdStages>::bytes(threads) <= kNormRingSmem) {
     if (p.y && p.next_weight) return run_ring<T, V, true, true>(p, threads, stream, dev);
     if (p.y) return run_ring<T, V, true, false>(p, threads, stream, dev);
     return run_ring<T, V, false, true>(p, threads, stream, dev);
