@@ -110,8 +110,8 @@ cudaError_t launch_zq_decode(const uint8_t* in, uint64_t in_bytes, uint64_t n, u
 constexpr uint32_t kMoeMaxExperts = ZC_MOE_MAX_EXPERTS;
 constexpr uint32_t kMoeMaxK = ZC_MOE_MAX_K;
 constexpr uint32_t kMoePlaceTokens = 8;    // most tokens one CTA of the dispatch places
-constexpr uint32_t kMoeChunkSlots = 2048;  // most slots of a counting chunk (whole groups of 8 tokens)
-constexpr uint64_t kMoeSingleSlots = 2048; // up to here every CTA counts all slots itself: one launch
+constexpr uint32_t kMoeChunkSlots = 2048;   // slots of a counting chunk
+constexpr uint64_t kMoeSingleSlots = 8192;  // up to here every CTA of a dispatch counts all slots itself
 
 struct RouteParams {
   const void* logits;
@@ -144,8 +144,8 @@ struct DispatchParams {
   const void* ids;
   void* rows;
   int32_t *positions, *slots, *offsets;
-  uint32_t* counts;  // workspace: [experts + 1][chunks], then [experts + 1] totals
-  uint32_t chunks, chunk_tokens, cta_tokens;  // set by the launch
+  uint32_t* counts;  // workspace: [experts + 1][chunks]
+  uint32_t chunks, cta_tokens;  // set by the launch
   int single;
 };
 uint64_t moe_workspace_bytes(uint64_t tokens, uint32_t k, uint32_t experts);

@@ -189,4 +189,16 @@ __device__ __forceinline__ void cp_async_wait() {  // all but the last N groups 
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Thread-block clusters: the barrier of all threads of the cluster in its two halves (release, acquire), and a store to the
+// same variable in the shared memory of the cluster's CTA `cta`.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_shared_of_cta(uint32_t* var, uint32_t cta, uint32_t v) {
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u32 [a], %2;\n\t}" ::"r"(
+          smem_u32(var)),
+      "r"(cta), "r"(v)
+      : "memory");
+}
+
 }  // namespace zc

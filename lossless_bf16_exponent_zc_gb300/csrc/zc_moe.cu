@@ -18,55 +18,147 @@ namespace {
 // ------------------------------------------------------------------ routing
 constexpr int kRouteWarps = 4;  // tokens per CTA, one warp each
 
-// Order-preserving image of a score: larger score, larger key.  0 stands for
-// "cannot be chosen" (minus infinity); NaN is above everything, as a sort has
-// it, so that it shows in the weights; both zeros are equal.
+// Order-preserving image of a score: larger score, larger key.  NaN is above
+// everything, as a sort has it, so that it shows in the weights; both zeros
+// are equal.  Up to kClosed (minus infinity) an expert cannot be chosen.
+constexpr uint32_t kClosed = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t order_key(float f) {
-  if (f != f) return 0xFFFFFFFFu;
-  if (f == -INFINITY) return 0u;
-  const uint32_t b = f == 0.f ? 0u : __float_as_uint(f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const int32_t b = __float_as_int(f + 0.f);
+  const uint32_t key = static_cast<uint32_t>(b) ^ (static_cast<uint32_t>(b >> 31) | 0x80000000u);
+  return f != f ? 0xFFFFFFFFu : key;
 }
 
-__device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-l))); }
+// 1 / (1 + exp(-l)), each step rounded as the plain expression's (a correctly rounded reciprocal is the quotient).
+__device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(__fadd_rn(1.f, expf(-l))); }
 
-// One warp per token, lane l holding experts l, l + 32, ...: K times the
-// largest key (ties: the lowest expert) is found and cleared.  Pick k ends in
-// lane k, which then reads its logit again (an L1 hit) for the weight.
-template <typename T, int NPL>
+// Lane l's N values of a row, N l .. N l + N - 1; minus infinity beyond the width.  VEC: they are whole 4-, 8- or 16-byte
+// pieces.
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void load_row(const T* row, uint32_t width, float (&v)[N]) {
+  const uint32_t first = lane_id() * N;
+  if (VEC && N * sizeof(T) >= 4) {
+    constexpr int kBytes = N * static_cast<int>(sizeof(T));
+    constexpr int kPart = kBytes >= 16 ? 16 : kBytes;  // bytes of a piece
+    constexpr int kOf = kPart / static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int i = 0; i < N; i += kOf) {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (first + i < width) {
+        const T* src = row + first + i;
+        if (kPart == 16) {
+          const uint4 q = *reinterpret_cast<const uint4*>(src);
+          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else if (kPart == 8) {
+          const uint2 q = *reinterpret_cast<const uint2*>(src);
+          w[0] = q.x, w[1] = q.y;
+        } else {
+          w[0] = *reinterpret_cast<const uint32_t*>(src);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kOf; j++) {
+        float f;
+        if constexpr (sizeof(T) == 4) {
+          f = __uint_as_float(w[j & 3]);
+        } else {
+          float lo, hi;
+          unpack2(w[(j / 2) & 3], lo, hi, T());
+          f = j & 1 ? hi : lo;
+        }
+        v[i + j] = first + i < width ? f : -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; j++) v[j] = first + j < width ? to_f32<T>(row[first + j]) : -INFINITY;
+  }
+}
+
+// Sorts N values, largest first: Batcher's odd-even merge sort, unrolled.
+template <int N>
+__device__ __forceinline__ void sort_down(unsigned long long (&q)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; i++)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const unsigned long long a = q[i + j], b = q[i + j + k];
+            q[i + j] = a > b ? a : b;
+            q[i + j + k] = a > b ? b : a;
+          }
+}
+
+// One warp per token, every lane holding N experts next to one another: K
+// times the largest of the lanes' best is taken (on ties the lowest lane's, which
+// is the lowest expert's) and its lane goes on to its next.  A lane
+// sorts up to 8 experts once and then shifts them (256 experts, 8 taken: 600
+// instructions a token; looking for its best again each time, 1040); more than 8 it searches again.  Pick k ends in
+// lane k, which then reads its logit again (an L1 hit) for the weight.  Bound by those
+// instructions: 16384 x 256 fp32 take XXX us, their bytes 2.7.
+template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) {
   pdl_begin();
   const uint32_t lane = lane_id();
   const uint64_t t = static_cast<uint64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (t >= p.tokens) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.stride;
-  float l[NPL];
-  uint32_t key[NPL];
+  float l[N];
+  load_row<T, N, VEC>(row, p.experts, l);
+  unsigned long long q[N];  // key, then the higher for the lower expert
+  {
+    float bias[N];
+    if (p.sigmoid && p.bias) {
+      if (VEC && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0 && p.experts % 4 == 0)
+        load_row<float, N, true>(p.bias, p.experts, bias);
+      else
+        load_row<float, N, false>(p.bias, p.experts, bias);
+    } else {
 #pragma unroll
-  for (int j = 0; j < NPL; j++) {
-    const uint32_t e = j * 32 + lane;
-    l[j] = e < p.experts ? to_f32<T>(row[e]) : -INFINITY;
-  }
+      for (int j = 0; j < N; j++) bias[j] = 0.f;
+    }
 #pragma unroll
-  for (int j = 0; j < NPL; j++) {
-    const uint32_t e = j * 32 + lane;
-    float s = l[j];
-    if (p.sigmoid) s = __fadd_rn(sigmoid(l[j]), p.bias && e < p.experts ? p.bias[e] : 0.f);
-    key[j] = l[j] == -INFINITY ? 0u : order_key(s);
+    for (int j = 0; j < N; j++) {
+      float s = l[j];
+      if (p.sigmoid) s = s == -INFINITY ? s : __fadd_rn(sigmoid(s), bias[j]);
+      q[j] = static_cast<unsigned long long>(order_key(s)) << 32 | static_cast<uint32_t>(N - 1 - j);
+    }
   }
   uint32_t mine = kFull;
+  unsigned long long best = q[0];
+  auto look = [&]() {
+    best = q[0];
+#pragma unroll
+    for (int j = 1; j < N; j++) best = q[j] > best ? q[j] : best;
+  };
+  if (N <= 8)
+    sort_down<N>(q);
+  else
+    look();
   for (uint32_t k = 0; k < p.k; k++) {
-    uint32_t best = key[0], at = 0;
-#pragma unroll
-    for (int j = 1; j < NPL; j++)
-      if (key[j] > best) best = key[j], at = j;
-    const uint32_t top = __reduce_max_sync(kFull, best);
-    if (top == 0) break;
-    const uint32_t e = __reduce_min_sync(kFull, best == top ? at * 32 + lane : kFull);
+    if (N <= 8) best = q[0];
+    const uint32_t key = static_cast<uint32_t>(best >> 32);
+    const uint32_t top = __reduce_max_sync(kFull, key);
+    if (top <= kClosed) break;
+    const uint32_t winner = __ffs(__ballot_sync(kFull, key == top)) - 1;
+    const uint32_t at = N - 1 - static_cast<uint32_t>(best);
+    const uint32_t e = __shfl_sync(kFull, lane * N + at, winner);
     if (lane == k) mine = e;
+    if (lane == winner) {
+      if (N <= 8) {
 #pragma unroll
-    for (int j = 0; j < NPL; j++)
-      if (e == j * 32 + lane) key[j] = 0;
+        for (int j = 0; j + 1 < N; j++) q[j] = q[j + 1];
+        q[N - 1] = 0;
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; j++)
+          if (at == j) q[j] = 0;
+        look();
+      }
+    }
   }
   const bool have = mine != kFull;
   const float lm = have ? to_f32<T>(row[mine]) : -INFINITY;
@@ -83,7 +175,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
     } else {
       sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < NPL; j++) sum += l[j] == -INFINITY ? 0.f : expf(l[j] - top);
+      for (int j = 0; j < N; j++) sum += l[j] == -INFINITY ? 0.f : expf(l[j] - top);
       sum = warp_sum_f32(sum);
     }
     w = have ? w / sum : 0.f;
@@ -97,15 +189,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
 // Gradient of the logits: G_k = scale dw_k for the chosen experts.  A
 // renormalised softmax and both sigmoid forms depend on the chosen logits
 // alone, so only those are read and every other gradient is zero; the plain
-// softmax needs the whole row.
-template <typename T, int NPL>
+// softmax needs the whole row.  The chosen experts' values meet the lanes that hold
+// those experts in a row of shared memory.
+template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(RouteBwdParams p) {
+  __shared__ float rows[kRouteWarps][32 * N];
   pdl_begin();
   const uint32_t lane = lane_id();
   const uint64_t t = static_cast<uint64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (t >= p.tokens) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.stride;
   T* out = static_cast<T*>(p.dlogits) + t * p.experts;
+  float* mid = rows[threadIdx.x >> 5];
+#pragma unroll
+  for (int j = 0; j < N; j++) mid[j * 32 + lane] = 0.f;
   int32_t id = -1;
   float g = 0.f, lm = -INFINITY;
   if (lane < p.k) {
@@ -118,27 +215,24 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(RouteBwdPar
   }
   const bool have = id >= 0;
   const bool whole = !p.sigmoid && !p.renormalize;
-  float prob[NPL];
+  float prob[N];
   float d = 0.f, mean = 0.f;  // this lane's chosen logit's gradient; sum of G p over the row
   if (whole) {
+    load_row<T, N, VEC>(row, p.experts, prob);
     float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NPL; j++) {
-      const uint32_t e = j * 32 + lane;
-      prob[j] = e < p.experts ? to_f32<T>(row[e]) : -INFINITY;
-      top = fmaxf(top, prob[j]);
-    }
+    for (int j = 0; j < N; j++) top = fmaxf(top, prob[j]);
     top = warp_max_f32(top);
     float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < NPL; j++) {
+    for (int j = 0; j < N; j++) {
       prob[j] = prob[j] == -INFINITY ? 0.f : expf(prob[j] - top);
       sum += prob[j];
     }
     sum = warp_sum_f32(sum);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row with every expert masked has no gradient
 #pragma unroll
-    for (int j = 0; j < NPL; j++) prob[j] *= inv;
+    for (int j = 0; j < N; j++) prob[j] *= inv;
     mean = warp_sum_f32(have ? g * (expf(lm - top) * inv) : 0.f);
     d = g;
   } else if (p.sigmoid) {
@@ -155,27 +249,36 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(RouteBwdPar
     f = have ? f / sum : 0.f;
     d = f * (g - warp_sum_f32(g * f));
   }
-  float acc[NPL];
-#pragma unroll
-  for (int j = 0; j < NPL; j++) acc[j] = 0.f;
-  for (uint32_t k = 0; k < p.k; k++) {
-    const int32_t e = __shfl_sync(kFull, id, k);
-    const float dk = __shfl_sync(kFull, d, k);
-    if (e < 0) continue;
-#pragma unroll
-    for (int j = 0; j < NPL; j++)
-      if (static_cast<uint32_t>(e) == j * 32 + lane) acc[j] += dk;
+  __syncwarp();
+  // An expert named more than once (never by the router) gets its gradients one after the other.
+  if (have) mid[id] = __uint_as_float(lane);
+  __syncwarp();
+  const bool alone = !have || __float_as_uint(mid[id]) == lane;
+  if (__all_sync(kFull, alone)) {
+    if (have) mid[id] = d;
+  } else {
+    if (have) mid[id] = 0.f;
+    __syncwarp();
+    for (uint32_t k = 0; k < p.k; k++) {
+      if (lane == k && have) mid[id] += d;
+      __syncwarp();
+    }
+  }
+  __syncwarp();
+  if (!whole) {
+    for (uint32_t e = lane; e < p.experts; e += 32) out[e] = from_f32<T>(mid[e]);
+    return;
   }
 #pragma unroll
-  for (int j = 0; j < NPL; j++) {
-    const uint32_t e = j * 32 + lane;
-    if (whole) acc[j] = prob[j] * (acc[j] - mean);
-    if (e < p.experts) out[e] = from_f32<T>(acc[j]);
+  for (int j = 0; j < N; j++) {
+    const uint32_t e = lane * N + j;
+    if (e < p.experts) out[e] = from_f32<T>(prob[j] * (mid[e] - mean));
   }
 }
 
 // ------------------------------------------------------------------ dispatch
 constexpr int kSortThreads = 256;
+constexpr int kSortWarps = kSortThreads / 32;
 
 // The expert of slot i, or `experts` for a slot that is not routed.
 __device__ __forceinline__ uint32_t slot_key(const DispatchParams& p, uint64_t i) {
@@ -183,9 +286,24 @@ __device__ __forceinline__ uint32_t slot_key(const DispatchParams& p, uint64_t i
   return v >= 0 && v < static_cast<int64_t>(p.experts) ? static_cast<uint32_t>(v) : p.experts;
 }
 
-// Exclusive prefix sums of a[0 .. count), in place; count <= 8 * kSortThreads.
+__device__ __forceinline__ uint32_t lanes_below() { return (1u << lane_id()) - 1u; }
+
+// The lanes whose key equals this one's, by a vote on each of the low `bits` bits.
+__device__ __forceinline__ uint32_t equal_lanes(uint32_t key, int bits) {
+  uint32_t equal = kFull;
+  for (int b = 0; b < bits; b++) {
+    const bool one = (key >> b) & 1u;
+    const uint32_t ones = __ballot_sync(kFull, one);
+    equal &= one ? ones : ~ones;
+  }
+  return equal;
+}
+// Bits that tell 0 .. experts and "no slot" (all ones) apart.
+__device__ __forceinline__ int key_bits(uint32_t experts) { return 32 - __clz(experts + 1); }
+
+// Exclusive prefix sums of a[0 .. count), in place, over a CTA of whole warps.
 __device__ __forceinline__ void block_exclusive_scan(uint32_t* a, uint32_t count, uint32_t* warp_totals) {
-  const uint32_t per = (count + kSortThreads - 1) / kSortThreads, first = threadIdx.x * per;
+  const uint32_t per = (count + blockDim.x - 1) / blockDim.x, first = threadIdx.x * per;
   uint32_t sum = 0;
   for (uint32_t i = first; i < first + per && i < count; i++) sum += a[i];
   const uint32_t upto = warp_inclusive_scan(sum);
@@ -201,85 +319,156 @@ __device__ __forceinline__ void block_exclusive_scan(uint32_t* a, uint32_t count
   __syncthreads();
 }
 
-// First of two passes of the stable counting sort: how many slots of each
-// expert a chunk of tokens holds, counts[expert][chunk].
+// The stable counting sort of a call with many slots, first of three
+// launches.  A CTA takes a chunk of 2048 slots, each warp an eighth of it in
+// order: counts per warp and expert, their prefix over the warps,
+// and then every slot's place among its expert's in the chunk, 32 at a time
+// (its equals among the lanes below it).  positions[] holds that place until the rows are placed.
 __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(DispatchParams p) {
-  __shared__ uint32_t hist[kMoeMaxExperts + 1];
+  extern __shared__ uint32_t hist[];  // [kSortWarps][experts + 1]
   pdl_allow_dependents();
-  for (uint32_t e = threadIdx.x; e <= kMoeMaxExperts; e += kSortThreads) hist[e] = 0;
+  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
   pdl_wait();
+  const uint32_t e1 = p.experts + 1;
+  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kMoeChunkSlots;
+  const uint32_t n = static_cast<uint32_t>(min(static_cast<uint64_t>(kMoeChunkSlots), p.tokens * p.k - first));
+  constexpr uint32_t kTurns = kMoeChunkSlots / kSortThreads;
+  const uint32_t base = warp * (kTurns * 32) + lane;
+  uint32_t key[kTurns];
+#pragma unroll
+  for (uint32_t i = 0; i < kTurns; i++) key[i] = base + i * 32 < n ? slot_key(p, first + base + i * 32) : kFull;
+  uint32_t* own = hist + warp * e1;
+  for (uint32_t e = lane; e < e1; e += 32) own[e] = 0;
+  __syncwarp();
+#pragma unroll
+  for (uint32_t i = 0; i < kTurns; i++)
+    if (key[i] != kFull) atomicAdd(&own[key[i]], 1u);
   __syncthreads();
-  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * p.chunk_tokens * p.k;
-  const uint64_t all = p.tokens * p.k, last = min(all, first + static_cast<uint64_t>(p.chunk_tokens) * p.k);
-  for (uint64_t i = first + threadIdx.x; i < last; i += kSortThreads) atomicAdd(&hist[slot_key(p, i)], 1u);
-  __syncthreads();
-  for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads)
-    p.counts[static_cast<uint64_t>(e) * p.chunks + blockIdx.x] = hist[e];
-}
-
-// Exclusive prefix over the chunks of every expert, in place, one warp per
-// expert; the total goes behind the table.
-__global__ void __launch_bounds__(128) moe_prefix_kernel(DispatchParams p) {
-  pdl_begin();
-  const uint32_t e = blockIdx.x * 4 + (threadIdx.x >> 5), lane = lane_id();
-  if (e > p.experts) return;
-  uint32_t* c = p.counts + static_cast<uint64_t>(e) * p.chunks;
-  uint32_t base = 0;
-  for (uint32_t i = 0; i < p.chunks; i += 32) {
-    const uint32_t v = i + lane < p.chunks ? c[i + lane] : 0;
-    const uint32_t upto = warp_inclusive_scan(v);
-    if (i + lane < p.chunks) c[i + lane] = base + upto - v;
-    base += __shfl_sync(kFull, upto, 31);
+  for (uint32_t e = threadIdx.x; e < e1; e += kSortThreads) {
+    uint32_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; w++) {
+      const uint32_t c = hist[w * e1 + e];
+      hist[w * e1 + e] = sum;
+      sum += c;
+    }
+    p.counts[static_cast<uint64_t>(e) * p.chunks + blockIdx.x] = sum;
   }
-  if (lane == 0) p.counts[static_cast<uint64_t>(p.experts + 1) * p.chunks + e] = base;
+  __syncthreads();
+  const int bits = key_bits(p.experts);
+#pragma unroll
+  for (uint32_t i = 0; i < kTurns; i++) {
+    const uint32_t equal = equal_lanes(key[i], bits);
+    if (key[i] != kFull)
+      p.positions[first + base + i * 32] = static_cast<int32_t>(own[key[i]] + __popc(equal & lanes_below()));
+    __syncwarp();
+    if (key[i] != kFull && (equal & lanes_below()) == 0) own[key[i]] += __popc(equal);
+    __syncwarp();
+  }
 }
 
-// Row of every slot, and the rows themselves.  A CTA places the slots of a
-// few tokens: row = first row of the expert + the expert's slots in earlier
-// chunks + those earlier in this chunk + those earlier among its own.  With
-// one chunk in all (`single`) the CTA counts all slots itself, so small calls are one
-// launch.  Then it reads each token once and writes its K rows.
+// Second: the exclusive prefix over the chunks of every expert, in place, a warp per expert, and from the totals the
+// experts' first rows.  One cluster: its CTAs leave their totals in the first one's shared memory, which adds them up
+// (256 experts, 64 chunks: 5.5 us by itself, in one CTA 13.5).  Letting every CTA of the third launch add up what its slots
+// need instead took longer: 131072 slots of 512 values 58 us against 41, and sorting in one cluster of 8 CTAs 55.
+constexpr uint32_t kPrefixCtas = 8;
+constexpr int kPrefixThreads = 1024;
+__global__ void __launch_bounds__(kPrefixThreads) __cluster_dims__(kPrefixCtas, 1, 1)
+    moe_prefix_kernel(DispatchParams p) {
+  __shared__ uint32_t total[kMoeMaxExperts + 1];
+  __shared__ uint32_t warp_totals[32];
+  pdl_allow_dependents();
+  const uint32_t lane = lane_id(), warps = kPrefixCtas * (kPrefixThreads / 32);
+  cluster_arrive();  // shared memory of the first CTA may be written once it has started, that is after this barrier
+  pdl_wait();
+  cluster_wait();
+  for (uint32_t e = (threadIdx.x >> 5) * kPrefixCtas + blockIdx.x; e <= p.experts; e += warps) {
+    uint32_t* c = p.counts + static_cast<uint64_t>(e) * p.chunks;
+    uint32_t base = 0;
+    for (uint32_t i = 0; i < p.chunks; i += 128) {  // four pieces on their way at once
+      uint32_t v[4];
+#pragma unroll
+      for (uint32_t q = 0; q < 4; q++) v[q] = i + q * 32 + lane < p.chunks ? c[i + q * 32 + lane] : 0;
+#pragma unroll
+      for (uint32_t q = 0; q < 4; q++) {
+        if (i + q * 32 >= p.chunks) break;
+        const uint32_t upto = warp_inclusive_scan(v[q]);
+        if (i + q * 32 + lane < p.chunks) c[i + q * 32 + lane] = base + upto - v[q];
+        base += __shfl_sync(kFull, upto, 31);
+      }
+    }
+    if (lane == 0) st_shared_of_cta(&total[e], 0, base);
+  }
+  cluster_arrive();
+  cluster_wait();
+  if (blockIdx.x) return;
+  block_exclusive_scan(total, p.experts + 1, warp_totals);
+  for (uint32_t e = threadIdx.x; e <= p.experts; e += kPrefixThreads) p.offsets[e] = static_cast<int32_t>(total[e]);
+}
+
+// Third, or alone: the row of every slot, and the rows themselves.  A CTA
+// places the slots of a few tokens, then reads each token once and writes its K
+// rows.  A slot's row is its expert's first + those in earlier chunks + its place in the chunk.  In a call with few
+// slots (`single`) the CTA counts all of them itself, those before its own
+// apart (two counts in a word), and ranks its own as above, so that the call is one
+// launch: with 8192 slots of 128 experts 9.9 us against 10.6 in three, with 1024 3.1 against 8.3, with 16384 18.0
+// against 16.4.  Bound by memory: 16384 x 4096 bf16 to 4 experts each, 1.34 GB, 118 us in all, of which the sort 8.
 template <typename T, int V>
 __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams p) {
-  __shared__ uint32_t start[kMoeMaxExperts + 1];   // first row of each expert
-  __shared__ uint32_t before[kMoeMaxExperts + 1];  // its slots in this chunk before this CTA's
-  __shared__ uint32_t warp_totals[kSortThreads / 32];
-  __shared__ uint32_t own_key[kMoePlaceTokens * kMoeMaxK];
+  __shared__ uint32_t start[kMoeMaxExperts + 1];
+  __shared__ uint32_t before[kMoeMaxExperts + 1];
+  __shared__ uint32_t warp_totals[kSortWarps];
   __shared__ int32_t own_pos[kMoePlaceTokens * kMoeMaxK];
   pdl_allow_dependents();
-  for (uint32_t e = threadIdx.x; e <= kMoeMaxExperts; e += kSortThreads) start[e] = before[e] = 0;
+  const uint32_t lane = lane_id();
   pdl_wait();
-  __syncthreads();
   const uint64_t t0 = static_cast<uint64_t>(blockIdx.x) * p.cta_tokens;
   const uint32_t nt = static_cast<uint32_t>(min(static_cast<uint64_t>(p.cta_tokens), p.tokens - min(p.tokens, t0)));
-  const uint64_t s0 = t0 * p.k, all = p.tokens * p.k;
+  const uint64_t s0 = t0 * p.k;
   const uint32_t own = nt * p.k;
-  const uint32_t chunk = p.single ? 0 : static_cast<uint32_t>(t0 / p.chunk_tokens);
-  const uint64_t c0 = static_cast<uint64_t>(chunk) * p.chunk_tokens * p.k;
-  for (uint32_t i = threadIdx.x; i < own; i += kSortThreads) own_key[i] = slot_key(p, s0 + i);
+  const bool writes = blockIdx.y == 0;  // the CTA that reports its slots' rows
   if (p.single) {
-    for (uint64_t i = threadIdx.x; i < all; i += kSortThreads) {
-      const uint32_t e = slot_key(p, i);
-      atomicAdd(&start[e], 1u);
-      if (i < s0) atomicAdd(&before[e], 1u);
+    const uint32_t all = static_cast<uint32_t>(p.tokens) * p.k, mine = static_cast<uint32_t>(s0);
+    for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads) start[e] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < all; i += kSortThreads)
+      atomicAdd(&start[slot_key(p, i)], i < mine ? 0x10001u : 1u);
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads) {
+      before[e] = start[e] >> 16;
+      start[e] &= 0xFFFFu;
+    }
+    __syncthreads();
+    block_exclusive_scan(start, p.experts + 1, warp_totals);
+    if (blockIdx.x == 0 && writes)
+      for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads) p.offsets[e] = static_cast<int32_t>(start[e]);
+    if (threadIdx.x < 32) {
+      const int bits = key_bits(p.experts);
+      for (uint32_t i = lane; i < (own + 31) / 32 * 32; i += 32) {
+        const uint32_t e = i < own ? slot_key(p, s0 + i) : kFull;
+        const uint32_t equal = equal_lanes(e, bits);
+        uint32_t r = 0;
+        if (e != kFull) r = start[e] + before[e] + __popc(equal & lanes_below());
+        __syncwarp();
+        if (e != kFull && (equal & lanes_below()) == 0) before[e] += __popc(equal);
+        __syncwarp();
+        if (e == kFull) continue;
+        const int32_t pos = e < p.experts ? static_cast<int32_t>(r) : ~static_cast<int32_t>(r);
+        own_pos[i] = pos;
+        if (writes) {
+          p.positions[s0 + i] = pos;
+          p.slots[r] = static_cast<int32_t>(s0 + i);
+        }
+      }
     }
   } else {
-    for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads)
-      start[e] = p.counts[static_cast<uint64_t>(p.experts + 1) * p.chunks + e];
-    for (uint64_t i = c0 + threadIdx.x; i < s0; i += kSortThreads) atomicAdd(&before[slot_key(p, i)], 1u);
-  }
-  __syncthreads();
-  block_exclusive_scan(start, p.experts + 1, warp_totals);
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads) p.offsets[e] = static_cast<int32_t>(start[e]);
-  for (uint32_t i = threadIdx.x; i < own; i += kSortThreads) {
-    const uint32_t e = own_key[i];
-    uint32_t r = start[e] + before[e];
-    if (!p.single) r += p.counts[static_cast<uint64_t>(e) * p.chunks + chunk];
-    for (uint32_t j = 0; j < i; j++) r += own_key[j] == e;
-    const int32_t pos = e < p.experts ? static_cast<int32_t>(r) : ~static_cast<int32_t>(r);
-    own_pos[i] = pos;
-    if (blockIdx.y == 0) {
+    for (uint32_t i = threadIdx.x; i < own; i += kSortThreads) {
+      const uint32_t e = slot_key(p, s0 + i), chunk = static_cast<uint32_t>((s0 + i) / kMoeChunkSlots);
+      const uint32_t r = static_cast<uint32_t>(p.offsets[e]) + p.counts[static_cast<uint64_t>(e) * p.chunks + chunk] +
+                         static_cast<uint32_t>(p.positions[s0 + i]);
+      const int32_t pos = e < p.experts ? static_cast<int32_t>(r) : ~static_cast<int32_t>(r);
+      own_pos[i] = pos;
       p.positions[s0 + i] = pos;
       p.slots[r] = static_cast<int32_t>(s0 + i);
     }
@@ -305,7 +494,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams 
 
 // ------------------------------------------------------------------ combine
 constexpr int kCombineThreads = 256;
-constexpr int kCombineK = 8;  // rows of one token in flight together
+constexpr int kCombineLoads = 8;  // pieces a thread has in flight
 
 // The row of a slot: true if it is routed.  `row` is the row to read (or,
 // unrouted, the one to clear, which the buffer need not hold); a routed row
@@ -317,47 +506,59 @@ __device__ __forceinline__ bool slot_row(int32_t pos, uint64_t n_rows, int32_t* 
   return *inside && pos >= 0;
 }
 
-// out[t] = sum over k, in order, of w[t][k] rows[pos[t][k]], in fp32.  One
-// thread per 16-byte piece of a token: the rows of up to eight slots are
-// loaded before the first is added.
-template <typename T, int V>
+// out[t] = sum over k, in order, of w[t][k] rows[pos[t][k]], in fp32.  A
+// thread has eight 16-byte pieces in flight before it adds the first: those of KU
+// slots of 8 / KU pieces of the output (16384 x 4096 bf16, 4 slots: one piece of 4 slots takes 132 us, two
+// of them 106), kCombineThreads pieces apart.
+template <typename T, int V, int KU>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(CombineParams p) {
+  constexpr int kPieces = kCombineLoads / KU;
   pdl_begin();
   const uint32_t pieces = p.hidden / V;
-  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kCombineThreads + threadIdx.x;
-  const uint64_t t = i / pieces;
-  if (t >= p.tokens) return;
-  const uint64_t c = (i - t * pieces) * V;
-  float acc[V];
+  const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kCombineThreads * kPieces) + threadIdx.x;
+  float acc[kPieces][V];
 #pragma unroll
-  for (int j = 0; j < V; j++) acc[j] = 0.f;
-  for (uint32_t k0 = 0; k0 < p.k; k0 += kCombineK) {
-    Piece<T, V> v[kCombineK];
-    float w[kCombineK];
+  for (int q = 0; q < kPieces; q++)
 #pragma unroll
-    for (int k = 0; k < kCombineK; k++) {
-      w[k] = 0.f;
-      v[k] = Piece<T, V>::zero();
-      if (k0 + k < p.k) {
-        uint64_t row;
-        bool inside;
-        if (slot_row(p.positions[t * p.k + k0 + k], p.n_rows, p.status, &row, &inside)) {
-          w[k] = p.weights ? p.weights[t * p.k + k0 + k] : 1.f;
-          v[k] = Piece<T, V>::load(static_cast<const T*>(p.rows) + row * p.row_stride + c);
+    for (int j = 0; j < V; j++) acc[q][j] = 0.f;
+  for (uint32_t k0 = 0; k0 < p.k; k0 += KU) {
+    Piece<T, V> v[kPieces][KU];
+    float w[kPieces][KU];
+#pragma unroll
+    for (int q = 0; q < kPieces; q++) {
+      const uint64_t i = i0 + q * kCombineThreads, t = i / pieces, c = (i - t * pieces) * V;
+#pragma unroll
+      for (int k = 0; k < KU; k++) {
+        w[q][k] = 0.f;
+        v[q][k] = Piece<T, V>::zero();
+        if (t < p.tokens && k0 + k < p.k) {
+          uint64_t row;
+          bool inside;
+          if (slot_row(p.positions[t * p.k + k0 + k], p.n_rows, p.status, &row, &inside)) {
+            w[q][k] = p.weights ? p.weights[t * p.k + k0 + k] : 1.f;
+            v[q][k] = Piece<T, V>::load(static_cast<const T*>(p.rows) + row * p.row_stride + c);
+          }
         }
       }
     }
 #pragma unroll
-    for (int k = 0; k < kCombineK; k++) {
-      float f[V];
-      v[k].get(f);
+    for (int q = 0; q < kPieces; q++)
 #pragma unroll
-      for (int j = 0; j < V; j++) acc[j] = fmaf(w[k], f[j], acc[j]);
-    }
+      for (int k = 0; k < KU; k++) {
+        float f[V];
+        v[q][k].get(f);
+#pragma unroll
+        for (int j = 0; j < V; j++) acc[q][j] = fmaf(w[q][k], f[j], acc[q][j]);
+      }
   }
-  Piece<T, V> o;
-  o.set(acc);
-  o.store(static_cast<T*>(p.out) + t * p.hidden + c);
+#pragma unroll
+  for (int q = 0; q < kPieces; q++) {
+    const uint64_t i = i0 + q * kCombineThreads, t = i / pieces, c = (i - t * pieces) * V;
+    if (t >= p.tokens) continue;
+    Piece<T, V> o;
+    o.set(acc[q]);
+    o.store(static_cast<T*>(p.out) + t * p.hidden + c);
+  }
 }
 
 // drows[pos] = w dout and dw = <dout, rows[pos]>: dout's row is read once for
@@ -429,34 +630,44 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
 
 // ------------------------------------------------------------------ launches
 template <typename F>
-cudaError_t run(F* kernel, uint64_t grid_x, uint32_t grid_y, int threads, cudaStream_t stream, void* params) {
+cudaError_t run(F* kernel, uint64_t grid_x, uint32_t grid_y, int threads, cudaStream_t stream, void* params,
+                int smem = 0) {
   if (grid_x == 0) return cudaSuccess;
   if (grid_x > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
   void* args[] = {params};
   return launch_kernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<unsigned>(grid_x), grid_y),
-                       dim3(threads), 0, stream, args, false);
+                       dim3(threads), smem, stream, args, false);
 }
 
 uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
+template <typename T, int N, bool VEC, typename P>
+cudaError_t route_shape(P& p, cudaStream_t stream) {
+  const uint64_t grid = ceil_div(p.tokens, kRouteWarps);
+  if constexpr (std::is_same<P, RouteParams>::value)
+    return run(route_kernel<T, N, VEC>, grid, 1, kRouteWarps * 32, stream, &p);
+  else
+    return run(route_bwd_kernel<T, N, VEC>, grid, 1, kRouteWarps * 32, stream, &p);
+}
+
+template <typename T, int N, typename P>
+cudaError_t route_width(P& p, cudaStream_t stream) {
+  // a lane's values as whole pieces: of 16 bytes, or of all its values where those are fewer
+  constexpr uint64_t kPart = N * sizeof(T) < 16 ? N * sizeof(T) : 16;
+  const bool vec = reinterpret_cast<uintptr_t>(p.logits) % kPart == 0 && p.stride * sizeof(T) % kPart == 0 &&
+                   p.experts * sizeof(T) % kPart == 0;
+  return vec ? route_shape<T, N, true>(p, stream) : route_shape<T, N, false>(p, stream);
+}
+
 template <typename T, typename P>
 cudaError_t route_of(const P& params, cudaStream_t stream) {
   P p = params;
-  const uint64_t grid = ceil_div(p.tokens, kRouteWarps);
-#define ZC_ROUTE(NPL)                                                                      \
-  if (p.experts <= 32 * NPL) {                                                             \
-    if constexpr (std::is_same<P, RouteParams>::value)                                     \
-      return run(route_kernel<T, NPL>, grid, 1, kRouteWarps * 32, stream, &p);             \
-    else                                                                                   \
-      return run(route_bwd_kernel<T, NPL>, grid, 1, kRouteWarps * 32, stream, &p);         \
-  }
-  ZC_ROUTE(2)
-  ZC_ROUTE(4)
-  ZC_ROUTE(8)
-  ZC_ROUTE(16)
-  ZC_ROUTE(32)
-#undef ZC_ROUTE
-  return cudaErrorInvalidValue;
+  if (p.experts <= 32) return route_width<T, 1>(p, stream);
+  if (p.experts <= 64) return route_width<T, 2>(p, stream);
+  if (p.experts <= 128) return route_width<T, 4>(p, stream);
+  if (p.experts <= 256) return route_width<T, 8>(p, stream);
+  if (p.experts <= 512) return route_width<T, 16>(p, stream);
+  return route_width<T, 32>(p, stream);
 }
 
 template <typename P>
@@ -474,12 +685,17 @@ cudaError_t place(DispatchParams& p, bool vec, uint64_t grid, uint32_t split, cu
   return run(moe_place_kernel<T, 1>, grid, split, kSortThreads, stream, &p);
 }
 
-template <typename T>
-cudaError_t combine(CombineParams& p, bool vec, cudaStream_t stream) {
-  const uint64_t pieces = p.hidden / (vec ? kPieceOf<T> : 1);
-  const uint64_t grid = ceil_div(p.tokens * pieces, kCombineThreads);
-  if (vec) return run(moe_combine_kernel<T, kPieceOf<T>>, grid, 1, kCombineThreads, stream, &p);
-  return run(moe_combine_kernel<T, 1>, grid, 1, kCombineThreads, stream, &p);
+template <typename T, int V>
+cudaError_t combine(CombineParams& p, cudaStream_t stream) {
+  const uint64_t all = p.tokens * (p.hidden / V);
+  const int ku = p.k <= 1 ? 1 : p.k <= 2 ? 2 : p.k <= 4 ? 4 : 8;
+  const uint64_t grid = ceil_div(all, kCombineThreads * (kCombineLoads / ku));
+  switch (ku) {
+    case 1: return run(moe_combine_kernel<T, V, 1>, grid, 1, kCombineThreads, stream, &p);
+    case 2: return run(moe_combine_kernel<T, V, 2>, grid, 1, kCombineThreads, stream, &p);
+    case 4: return run(moe_combine_kernel<T, V, 4>, grid, 1, kCombineThreads, stream, &p);
+    default: return run(moe_combine_kernel<T, V, 8>, grid, 1, kCombineThreads, stream, &p);
+  }
 }
 
 template <typename T, int V>
@@ -500,25 +716,27 @@ cudaError_t launch_route_bwd(const RouteBwdParams& p, int dtype, cudaStream_t st
   return route_typed(p, dtype, stream);
 }
 
-uint64_t moe_chunks(uint64_t tokens, uint32_t k) {
-  const uint64_t chunk_tokens = kMoeChunkSlots / (k * kMoePlaceTokens) * kMoePlaceTokens;
-  return ceil_div(tokens, chunk_tokens);
-}
-
 uint64_t moe_workspace_bytes(uint64_t tokens, uint32_t k, uint32_t experts) {
-  return 4 * (static_cast<uint64_t>(experts) + 1) * (moe_chunks(tokens, k) + 1);
+  return 4 * (static_cast<uint64_t>(experts) + 1) * (ceil_div(tokens * k, kMoeChunkSlots) + 1);
 }
 
 cudaError_t launch_dispatch(const DispatchParams& params, int dtype, bool vec, cudaStream_t stream,
                             const DeviceInfo& dev) {
   DispatchParams p = params;
-  p.chunk_tokens = kMoeChunkSlots / (p.k * kMoePlaceTokens) * kMoePlaceTokens;
-  p.chunks = static_cast<uint32_t>(moe_chunks(p.tokens, p.k));
-  p.single = p.tokens * p.k <= kMoeSingleSlots;
+  const uint64_t slots = p.tokens * p.k;
+  p.chunks = static_cast<uint32_t>(ceil_div(slots, kMoeChunkSlots));
+  p.single = slots <= kMoeSingleSlots;
   if (!p.single) {
-    cudaError_t e = run(moe_count_kernel, p.chunks, 1, kSortThreads, stream, &p);
+    static KernelPrep prep;
+    constexpr int kMostSmem = kSortWarps * (kMoeMaxExperts + 1) * 4;
+    int per_sm = 0;
+    cudaError_t e = prepare_kernel(prep, reinterpret_cast<const void*>(moe_count_kernel), kSortThreads, kMostSmem, dev,
+                                   &per_sm);
     if (e != cudaSuccess) return e;
-    e = run(moe_prefix_kernel, ceil_div(p.experts + 1, 4), 1, 128, stream, &p);
+    e = run(moe_count_kernel, p.chunks, 1, kSortThreads, stream, &p,
+            kSortWarps * (static_cast<int>(p.experts) + 1) * 4);
+    if (e != cudaSuccess) return e;
+    e = run(moe_prefix_kernel, kPrefixCtas, 1, kPrefixThreads, stream, &p);
     if (e != cudaSuccess) return e;
   }
   // Tokens per CTA: few while the grid does not fill the GPU, up to
@@ -527,7 +745,6 @@ cudaError_t launch_dispatch(const DispatchParams& params, int dtype, bool vec, c
   p.cta_tokens = static_cast<uint32_t>(p.tokens / fill);
   if (p.cta_tokens < 1) p.cta_tokens = 1;
   if (p.cta_tokens > kMoePlaceTokens) p.cta_tokens = kMoePlaceTokens;
-  while (kMoePlaceTokens % p.cta_tokens) p.cta_tokens--;  // a CTA's tokens lie in one chunk
   const uint64_t grid = p.tokens ? ceil_div(p.tokens, p.cta_tokens) : 1;  // no tokens: the offsets are still written
   switch (dtype) {
     case ZC_BF16: return place<__nv_bfloat16>(p, vec, grid, 1, stream);
@@ -539,9 +756,9 @@ cudaError_t launch_dispatch(const DispatchParams& params, int dtype, bool vec, c
 cudaError_t launch_combine(const CombineParams& params, int dtype, bool vec, cudaStream_t stream) {
   CombineParams p = params;
   switch (dtype) {
-    case ZC_BF16: return combine<__nv_bfloat16>(p, vec, stream);
-    case ZC_F16: return combine<__half>(p, vec, stream);
-    default: return combine<float>(p, vec, stream);
+    case ZC_BF16: return vec ? combine<__nv_bfloat16, kPieceOf<__nv_bfloat16>>(p, stream) : combine<__nv_bfloat16, 1>(p, stream);
+    case ZC_F16: return vec ? combine<__half, kPieceOf<__half>>(p, stream) : combine<__half, 1>(p, stream);
+    default: return vec ? combine<float, kPieceOf<float>>(p, stream) : combine<float, 1>(p, stream);
   }
 }
 
