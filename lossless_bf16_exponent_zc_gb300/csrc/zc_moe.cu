@@ -98,7 +98,7 @@ __device__ __forceinline__ void sort_down(unsigned long long (&q)[N]) {
 // sorts up to 8 experts once and then shifts them (256 experts, 8 taken: 600
 // instructions a token; looking for its best again each time, 1040); more than 8 it searches again.  Pick k ends in
 // lane k, which then reads its logit again (an L1 hit) for the weight.  Bound by those
-// instructions: 16384 x 256 fp32 take XXX us, their bytes 2.7.
+// instructions: 16384 x 256 fp32 take 16 us, their bytes 2.7.
 template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) {
   pdl_begin();
@@ -508,25 +508,29 @@ __device__ __forceinline__ bool slot_row(int32_t pos, uint64_t n_rows, int32_t* 
 
 // out[t] = sum over k, in order, of w[t][k] rows[pos[t][k]], in fp32.  A
 // thread has eight 16-byte pieces in flight before it adds the first: those of KU
-// slots of 8 / KU pieces of the output (16384 x 4096 bf16, 4 slots: one piece of 4 slots takes 132 us, two
-// of them 106), kCombineThreads pieces apart.
-template <typename T, int V, int KU>
-__global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(CombineParams p) {
+// slots of 8 / KU pieces of the output, kCombineThreads pieces apart.  More than 8
+// slots (LOOP) are added eight at a time.
+template <typename T, int V, int KU, bool LOOP>
+__global__ void __launch_bounds__(kCombineThreads, 4) moe_combine_kernel(CombineParams p) {
   constexpr int kPieces = kCombineLoads / KU;
   pdl_begin();
   const uint32_t pieces = p.hidden / V;
-  const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kCombineThreads * kPieces) + threadIdx.x;
-  float acc[kPieces][V];
+  // the CTA's first piece: token t0, piece c0 of it
+  const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kCombineThreads * kPieces);
+  const uint64_t t0 = i0 / pieces;
+  const uint32_t c0 = static_cast<uint32_t>(i0 - t0 * pieces) + threadIdx.x;
+  float acc[V];
 #pragma unroll
-  for (int q = 0; q < kPieces; q++)
-#pragma unroll
-    for (int j = 0; j < V; j++) acc[q][j] = 0.f;
-  for (uint32_t k0 = 0; k0 < p.k; k0 += KU) {
+  for (int j = 0; j < V; j++) acc[j] = 0.f;
+  for (uint32_t k0 = 0; k0 < (LOOP ? p.k : 1u); k0 += KU) {
     Piece<T, V> v[kPieces][KU];
     float w[kPieces][KU];
+    uint64_t to[kPieces];
 #pragma unroll
     for (int q = 0; q < kPieces; q++) {
-      const uint64_t i = i0 + q * kCombineThreads, t = i / pieces, c = (i - t * pieces) * V;
+      const uint32_t i = c0 + q * kCombineThreads, dt = i / pieces, c = (i - dt * pieces) * V;
+      const uint64_t t = t0 + dt;
+      to[q] = t < p.tokens ? t * p.hidden + c : ~0ull;
 #pragma unroll
       for (int k = 0; k < KU; k++) {
         w[q][k] = 0.f;
@@ -542,22 +546,24 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(CombinePar
       }
     }
 #pragma unroll
-    for (int q = 0; q < kPieces; q++)
+    for (int q = 0; q < kPieces; q++) {
 #pragma unroll
       for (int k = 0; k < KU; k++) {
         float f[V];
         v[q][k].get(f);
 #pragma unroll
-        for (int j = 0; j < V; j++) acc[q][j] = fmaf(w[q][k], f[j], acc[q][j]);
+        for (int j = 0; j < V; j++) acc[j] = fmaf(w[q][k], f[j], acc[j]);
       }
-  }
+      if ((!LOOP || k0 + KU >= p.k) && to[q] != ~0ull) {
+        Piece<T, V> o;
+        o.set(acc);
+        o.store(static_cast<T*>(p.out) + to[q]);
+      }
+      if (!LOOP) {
 #pragma unroll
-  for (int q = 0; q < kPieces; q++) {
-    const uint64_t i = i0 + q * kCombineThreads, t = i / pieces, c = (i - t * pieces) * V;
-    if (t >= p.tokens) continue;
-    Piece<T, V> o;
-    o.set(acc[q]);
-    o.store(static_cast<T*>(p.out) + t * p.hidden + c);
+        for (int j = 0; j < V; j++) acc[j] = 0.f;
+      }
+    }
   }
 }
 
@@ -690,11 +696,12 @@ cudaError_t combine(CombineParams& p, cudaStream_t stream) {
   const uint64_t all = p.tokens * (p.hidden / V);
   const int ku = p.k <= 1 ? 1 : p.k <= 2 ? 2 : p.k <= 4 ? 4 : 8;
   const uint64_t grid = ceil_div(all, kCombineThreads * (kCombineLoads / ku));
+  if (p.k > 8) return run(moe_combine_kernel<T, V, 8, true>, grid, 1, kCombineThreads, stream, &p);
   switch (ku) {
-    case 1: return run(moe_combine_kernel<T, V, 1>, grid, 1, kCombineThreads, stream, &p);
-    case 2: return run(moe_combine_kernel<T, V, 2>, grid, 1, kCombineThreads, stream, &p);
-    case 4: return run(moe_combine_kernel<T, V, 4>, grid, 1, kCombineThreads, stream, &p);
-    default: return run(moe_combine_kernel<T, V, 8>, grid, 1, kCombineThreads, stream, &p);
+    case 1: return run(moe_combine_kernel<T, V, 1, false>, grid, 1, kCombineThreads, stream, &p);
+    case 2: return run(moe_combine_kernel<T, V, 2, false>, grid, 1, kCombineThreads, stream, &p);
+    case 4: return run(moe_combine_kernel<T, V, 4, false>, grid, 1, kCombineThreads, stream, &p);
+    default: return run(moe_combine_kernel<T, V, 8, false>, grid, 1, kCombineThreads, stream, &p);
   }
 }
 
