@@ -110,7 +110,7 @@ cudaError_t launch_zq_decode(const uint8_t* in, uint64_t in_bytes, uint64_t n, u
 constexpr uint32_t kMoeMaxExperts = ZC_MOE_MAX_EXPERTS;
 constexpr uint32_t kMoeMaxK = ZC_MOE_MAX_K;
 constexpr uint32_t kMoePlaceTokens = 8;    // most tokens one CTA of the dispatch places
-constexpr uint32_t kMoeChunkSlots = 2048;   // slots of a counting chunk
+constexpr uint32_t kMoeChunkSlots = 1024;   // slots of a counting chunk
 constexpr uint64_t kMoeSingleSlots = 8192;  // up to here every CTA of a dispatch counts all slots itself
 
 struct RouteParams {

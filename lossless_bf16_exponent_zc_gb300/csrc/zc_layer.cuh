@@ -102,6 +102,56 @@ struct Piece<T, 8> {
 template <typename T>
 constexpr int kPieceOf = 16 / static_cast<int>(sizeof(T));
 
+// The 16 bytes at any address that T's alignment allows: the two aligned pieces that hold them, shifted together.  Each
+// of the two holds at least one of the values asked for, so nothing is read from where the caller's memory cannot be;
+// neighbouring threads ask for the same pieces, so the second comes from the L1 cache.
+template <typename T>
+__device__ __forceinline__ Piece<T, kPieceOf<T>> load_any(const T* p) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  const uint32_t off = static_cast<uint32_t>(a & 15);
+  const uint4* at = reinterpret_cast<const uint4*>(a & ~static_cast<uintptr_t>(15));
+  const uint4 lo = at[0];
+  uint4 hi = lo;
+  if (off) hi = at[1];
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (off & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; i++) w[i] = w[i + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; i++) w[i] = w[i + 1];
+  }
+  if (sizeof(T) == 2 && (off & 2)) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  return Piece<T, kPieceOf<T>>{make_uint4(w[0], w[1], w[2], w[3])};
+}
+
+// How a row of `width` values that is written at p falls into aligned 16-byte pieces: `head` values before the first
+// piece, `body` pieces, and the rest.  Work on the row is cut into body + 2 units: the head, the pieces, the tail;
+// at most any_units(width) of them.
+template <typename T>
+struct RowCut {
+  uint32_t head, body;
+  __device__ __forceinline__ RowCut(const T* p, uint32_t width) {
+    constexpr uint32_t kV = kPieceOf<T>;
+    head = static_cast<uint32_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T);
+    head = head < width ? head : width;
+    body = (width - head) / kV;
+  }
+  // The values [first, last) of unit u; `whole`: one aligned piece.
+  __device__ __forceinline__ bool unit(uint32_t u, uint32_t width, uint32_t* first, uint32_t* last) const {
+    constexpr uint32_t kV = kPieceOf<T>;
+    *first = u == 0 ? 0 : head + (u - 1) * kV;
+    *last = u == 0 ? head : u <= body ? *first + kV : width;
+    return u >= 1 && u <= body;
+  }
+};
+template <typename T>
+__host__ __device__ constexpr uint32_t any_units(uint32_t width) { return width / kPieceOf<T> + 2; }
+
 __device__ __forceinline__ float warp_sum_f32(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);

@@ -320,7 +320,7 @@ __device__ __forceinline__ void block_exclusive_scan(uint32_t* a, uint32_t count
 }
 
 // The stable counting sort of a call with many slots, first of three
-// launches.  A CTA takes a chunk of 2048 slots, each warp an eighth of it in
+// launches.  A CTA takes a chunk of 1024 slots, each warp an eighth of it in
 // order: counts per warp and expert, their prefix over the warps,
 // and then every slot's place among its expert's in the chunk, 32 at a time
 // (its equals among the lanes below it).  positions[] holds that place until the rows are placed.
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kPrefixThreads) __cluster_dims__(kPrefixCtas, 
 // apart (two counts in a word), and ranks its own as above, so that the call is one
 // launch: with 8192 slots of 128 experts 9.9 us against 10.6 in three, with 1024 3.1 against 8.3, with 16384 18.0
 // against 16.4.  Bound by memory: 16384 x 4096 bf16 to 4 experts each, 1.34 GB, 118 us in all, of which the sort 8.
-template <typename T, int V>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams p) {
   __shared__ uint32_t start[kMoeMaxExperts + 1];
   __shared__ uint32_t before[kMoeMaxExperts + 1];
@@ -426,7 +426,6 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams 
   const uint32_t nt = static_cast<uint32_t>(min(static_cast<uint64_t>(p.cta_tokens), p.tokens - min(p.tokens, t0)));
   const uint64_t s0 = t0 * p.k;
   const uint32_t own = nt * p.k;
-  const bool writes = blockIdx.y == 0;  // the CTA that reports its slots' rows
   if (p.single) {
     const uint32_t all = static_cast<uint32_t>(p.tokens) * p.k, mine = static_cast<uint32_t>(s0);
     for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads) start[e] = 0;
@@ -441,7 +440,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams 
     }
     __syncthreads();
     block_exclusive_scan(start, p.experts + 1, warp_totals);
-    if (blockIdx.x == 0 && writes)
+    if (blockIdx.x == 0)
       for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads) p.offsets[e] = static_cast<int32_t>(start[e]);
     if (threadIdx.x < 32) {
       const int bits = key_bits(p.experts);
@@ -456,10 +455,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams 
         if (e == kFull) continue;
         const int32_t pos = e < p.experts ? static_cast<int32_t>(r) : ~static_cast<int32_t>(r);
         own_pos[i] = pos;
-        if (writes) {
-          p.positions[s0 + i] = pos;
-          p.slots[r] = static_cast<int32_t>(s0 + i);
-        }
+        p.positions[s0 + i] = pos;
+        p.slots[r] = static_cast<int32_t>(s0 + i);
       }
     }
   } else {
@@ -474,19 +471,29 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams 
     }
   }
   __syncthreads();
-  const uint32_t pieces = p.hidden / V;
-  for (uint32_t t = 0; t < nt; t++) {
+  constexpr int V = kPieceOf<T>;
+  const uint32_t pieces = VEC ? p.hidden / V : any_units<T>(p.hidden);
+  const uint64_t all = static_cast<uint64_t>(nt) * pieces;
+#pragma unroll 2
+  for (uint64_t i = threadIdx.x; i < all; i += kSortThreads) {
+    const uint32_t t = all >> 32 ? static_cast<uint32_t>(i / pieces) : static_cast<uint32_t>(i) / pieces;
+    const uint32_t u = static_cast<uint32_t>(i - static_cast<uint64_t>(t) * pieces);
     const T* src = static_cast<const T*>(p.x) + (t0 + t) * p.stride;
-    for (uint32_t c = blockIdx.y * kSortThreads + threadIdx.x; c < pieces; c += gridDim.y * kSortThreads) {
-      const Piece<T, V> v = Piece<T, V>::load(src + static_cast<uint64_t>(c) * V);
-      for (uint32_t k = 0; k < p.k; k++) {
-        const int32_t pos = own_pos[t * p.k + k];
-        const uint64_t row = static_cast<uint64_t>(pos < 0 ? ~pos : pos);
-        T* dst = static_cast<T*>(p.rows) + row * p.hidden + static_cast<uint64_t>(c) * V;
-        if (pos < 0)
-          Piece<T, V>::zero().store(dst);
+    Piece<T, V> v;
+    if (VEC) v = Piece<T, V>::load(src + static_cast<uint64_t>(u) * V);
+    for (uint32_t k = 0; k < p.k; k++) {
+      const int32_t pos = own_pos[t * p.k + k];
+      const uint64_t row = static_cast<uint64_t>(pos < 0 ? ~pos : pos);
+      T* dst = static_cast<T*>(p.rows) + row * p.hidden;
+      if (VEC) {
+        (pos < 0 ? Piece<T, V>::zero() : v).store(dst + static_cast<uint64_t>(u) * V);
+      } else {  // every row in pieces of its own alignment
+        const RowCut<T> cut(dst, p.hidden);
+        uint32_t first, last;
+        if (cut.unit(u, p.hidden, &first, &last))
+          (pos < 0 ? Piece<T, V>::zero() : load_any(src + first)).store(dst + first);
         else
-          v.store(dst);
+          for (uint32_t c = first; c < last; c++) dst[c] = pos < 0 ? from_f32<T>(0.f) : src[c];
       }
     }
   }
@@ -507,14 +514,14 @@ __device__ __forceinline__ bool slot_row(int32_t pos, uint64_t n_rows, int32_t* 
 }
 
 // out[t] = sum over k, in order, of w[t][k] rows[pos[t][k]], in fp32.  A
-// thread has eight 16-byte pieces in flight before it adds the first: those of KU
-// slots of 8 / KU pieces of the output, kCombineThreads pieces apart.  More than 8
-// slots (LOOP) are added eight at a time.
-template <typename T, int V, int KU, bool LOOP>
-__global__ void __launch_bounds__(kCombineThreads, 4) moe_combine_kernel(CombineParams p) {
-  constexpr int kPieces = kCombineLoads / KU;
+// thread has LOADS 16-byte pieces in flight before it adds the first (8; 4 where the rows lie off 16 bytes, each
+// then two loads): those of KU slots of LOADS / KU pieces of the output, kCombineThreads pieces apart.  More than 8
+// slots (LOOP) are added KU at a time.
+template <typename T, bool VEC, int KU, bool LOOP>
+__global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_kernel(CombineParams p) {
+  constexpr int V = kPieceOf<T>, kPieces = (VEC ? kCombineLoads : kCombineLoads / 2) / KU;
   pdl_begin();
-  const uint32_t pieces = p.hidden / V;
+  const uint32_t pieces = VEC ? p.hidden / V : any_units<T>(p.hidden);
   // the CTA's first piece: token t0, piece c0 of it
   const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kCombineThreads * kPieces);
   const uint64_t t0 = i0 / pieces;
@@ -525,23 +532,41 @@ __global__ void __launch_bounds__(kCombineThreads, 4) moe_combine_kernel(Combine
   for (uint32_t k0 = 0; k0 < (LOOP ? p.k : 1u); k0 += KU) {
     Piece<T, V> v[kPieces][KU];
     float w[kPieces][KU];
-    uint64_t to[kPieces];
+    T* to[kPieces];
 #pragma unroll
     for (int q = 0; q < kPieces; q++) {
-      const uint32_t i = c0 + q * kCombineThreads, dt = i / pieces, c = (i - dt * pieces) * V;
+      const uint32_t i = c0 + q * kCombineThreads, dt = i / pieces, u = i - dt * pieces;
       const uint64_t t = t0 + dt;
-      to[q] = t < p.tokens ? t * p.hidden + c : ~0ull;
+      T* out = static_cast<T*>(p.out) + t * p.hidden;
+      uint32_t first = u * V, last = first + V;
+      bool piece = true;
+      if (!VEC) piece = RowCut<T>(out, p.hidden).unit(u, p.hidden, &first, &last);
+      to[q] = t < p.tokens && piece ? out + first : nullptr;
 #pragma unroll
       for (int k = 0; k < KU; k++) {
         w[q][k] = 0.f;
         v[q][k] = Piece<T, V>::zero();
-        if (t < p.tokens && k0 + k < p.k) {
+        if (to[q] && k0 + k < p.k) {
           uint64_t row;
           bool inside;
           if (slot_row(p.positions[t * p.k + k0 + k], p.n_rows, p.status, &row, &inside)) {
             w[q][k] = p.weights ? p.weights[t * p.k + k0 + k] : 1.f;
-            v[q][k] = Piece<T, V>::load(static_cast<const T*>(p.rows) + row * p.row_stride + c);
+            const T* src = static_cast<const T*>(p.rows) + row * p.row_stride + first;
+            v[q][k] = VEC ? Piece<T, V>::load(src) : load_any(src);
           }
+        }
+      }
+      if (!VEC && t < p.tokens && !piece && k0 == 0) {  // a head or a tail, value by value
+        for (uint32_t c = first; c < last; c++) {
+          float sum = 0.f;
+          for (uint32_t k = 0; k < p.k; k++) {
+            uint64_t row;
+            bool inside;
+            if (slot_row(p.positions[t * p.k + k], p.n_rows, p.status, &row, &inside))
+              sum = fmaf(p.weights ? p.weights[t * p.k + k] : 1.f,
+                         to_f32<T>(static_cast<const T*>(p.rows)[row * p.row_stride + c]), sum);
+          }
+          out[c] = from_f32<T>(sum);
         }
       }
     }
@@ -554,10 +579,10 @@ __global__ void __launch_bounds__(kCombineThreads, 4) moe_combine_kernel(Combine
 #pragma unroll
         for (int j = 0; j < V; j++) acc[j] = fmaf(w[q][k], f[j], acc[j]);
       }
-      if ((!LOOP || k0 + KU >= p.k) && to[q] != ~0ull) {
+      if ((!LOOP || k0 + KU >= p.k) && to[q]) {
         Piece<T, V> o;
         o.set(acc);
-        o.store(static_cast<T*>(p.out) + to[q]);
+        o.store(to[q]);
       }
       if (!LOOP) {
 #pragma unroll
@@ -572,52 +597,95 @@ __global__ void __launch_bounds__(kCombineThreads, 4) moe_combine_kernel(Combine
 // thread's pieces, then over the CTA (or the warp, for narrow rows).
 constexpr int kCombineBwdK = 4;
 
-template <typename T, int V, bool WARP>
+template <typename T, bool VEC, bool WARP>
 __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p) {
+  constexpr int V = kPieceOf<T>;
   __shared__ float red[2][kCombineBwdK * 32];
   pdl_begin();
   const uint32_t lane = lane_id(), warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
   const uint64_t t = WARP ? static_cast<uint64_t>(blockIdx.x) * warps + warp : blockIdx.x;
   if (t >= p.tokens) return;
   const uint32_t me = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
-  const uint32_t pieces = p.hidden / V;
+  const uint32_t pieces = VEC ? p.hidden / V : any_units<T>(p.hidden);
   const T* dout = static_cast<const T*>(p.dout) + t * p.dout_stride;
   for (uint32_t k0 = 0, turn = 0; k0 < p.k; k0 += kCombineBwdK, turn ^= 1) {
     float dot[kCombineBwdK], w[kCombineBwdK];
-    uint64_t row[kCombineBwdK];
+    const T* from[kCombineBwdK];
+    T* to[kCombineBwdK];
     bool routed[kCombineBwdK], inside[kCombineBwdK];
 #pragma unroll
     for (int k = 0; k < kCombineBwdK; k++) {
       dot[k] = 0.f;
       w[k] = 0.f;
       routed[k] = inside[k] = false;
+      from[k] = nullptr;
+      to[k] = nullptr;
       if (k0 + k < p.k) {
-        routed[k] = slot_row(p.positions[t * p.k + k0 + k], p.n_rows, p.status, &row[k], &inside[k]);
+        uint64_t row;
+        routed[k] = slot_row(p.positions[t * p.k + k0 + k], p.n_rows, p.status, &row, &inside[k]);
         if (routed[k]) w[k] = p.weights[t * p.k + k0 + k];
+        from[k] = static_cast<const T*>(p.rows) + row * p.row_stride;
+        to[k] = static_cast<T*>(p.drows) + row * p.hidden;
       }
     }
-    for (uint32_t c = me; c < pieces; c += step) {
-      const uint64_t at = static_cast<uint64_t>(c) * V;
-      float g[V];
-      Piece<T, V> v[kCombineBwdK];
+    for (uint32_t u = me; u < pieces; u += step) {
+      if (VEC) {
+        const uint64_t at = static_cast<uint64_t>(u) * V;
+        float g[V];
+        Piece<T, V> v[kCombineBwdK];
 #pragma unroll
-      for (int k = 0; k < kCombineBwdK; k++)
-        v[k] = routed[k] ? Piece<T, V>::load(static_cast<const T*>(p.rows) + row[k] * p.row_stride + at)
-                         : Piece<T, V>::zero();
-      Piece<T, V>::load(dout + at).get(g);
+        for (int k = 0; k < kCombineBwdK; k++)
+          v[k] = routed[k] ? Piece<T, V>::load(from[k] + at) : Piece<T, V>::zero();
+        Piece<T, V>::load(dout + at).get(g);
 #pragma unroll
-      for (int k = 0; k < kCombineBwdK; k++) {
-        if (!inside[k]) continue;
-        float f[V], d[V];
-        v[k].get(f);
+        for (int k = 0; k < kCombineBwdK; k++) {
+          if (!inside[k]) continue;
+          float f[V], d[V];
+          v[k].get(f);
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-          dot[k] = routed[k] ? fmaf(g[j], f[j], dot[k]) : 0.f;
-          d[j] = routed[k] ? w[k] * g[j] : 0.f;
+          for (int j = 0; j < V; j++) {
+            dot[k] = routed[k] ? fmaf(g[j], f[j], dot[k]) : 0.f;
+            d[j] = routed[k] ? w[k] * g[j] : 0.f;
+          }
+          Piece<T, V> o;
+          o.set(d);
+          o.store(to[k] + at);
         }
-        Piece<T, V> o;
-        o.set(d);
-        o.store(static_cast<T*>(p.drows) + row[k] * p.hidden + at);
+      } else {  // every row in pieces of its own alignment
+        Piece<T, V> v[kCombineBwdK], g[kCombineBwdK];
+        uint32_t first[kCombineBwdK], last[kCombineBwdK];
+        bool piece[kCombineBwdK];
+#pragma unroll
+        for (int k = 0; k < kCombineBwdK; k++) {
+          v[k] = g[k] = Piece<T, V>::zero();
+          piece[k] = inside[k] && RowCut<T>(to[k], p.hidden).unit(u, p.hidden, &first[k], &last[k]);
+          if (piece[k] && routed[k]) {
+            v[k] = load_any(from[k] + first[k]);
+            g[k] = load_any(dout + first[k]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kCombineBwdK; k++) {
+          if (piece[k]) {
+            float f[V], d[V];
+            v[k].get(f);
+            g[k].get(d);
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+              dot[k] = fmaf(d[j], f[j], dot[k]);
+              d[j] = routed[k] ? w[k] * d[j] : 0.f;
+            }
+            Piece<T, V> o;
+            o.set(d);
+            o.store(to[k] + first[k]);
+          } else if (inside[k]) {
+            for (uint32_t c = first[k]; c < last[k]; c++) {
+              const float d = routed[k] ? to_f32<T>(dout[c]) : 0.f;
+              if (routed[k]) dot[k] = fmaf(d, to_f32<T>(from[k][c]), dot[k]);
+              to[k][c] = from_f32<T>(routed[k] ? w[k] * d : 0.f);
+            }
+          }
+        }
       }
     }
     if (WARP) {
@@ -686,31 +754,32 @@ cudaError_t route_typed(const P& p, int dtype, cudaStream_t stream) {
 }
 
 template <typename T>
-cudaError_t place(DispatchParams& p, bool vec, uint64_t grid, uint32_t split, cudaStream_t stream) {
-  if (vec) return run(moe_place_kernel<T, kPieceOf<T>>, grid, split, kSortThreads, stream, &p);
-  return run(moe_place_kernel<T, 1>, grid, split, kSortThreads, stream, &p);
+cudaError_t place(DispatchParams& p, bool vec, uint64_t grid, cudaStream_t stream) {
+  if (vec) return run(moe_place_kernel<T, true>, grid, 1, kSortThreads, stream, &p);
+  return run(moe_place_kernel<T, false>, grid, 1, kSortThreads, stream, &p);
 }
 
-template <typename T, int V>
+template <typename T, bool VEC>
 cudaError_t combine(CombineParams& p, cudaStream_t stream) {
-  const uint64_t all = p.tokens * (p.hidden / V);
-  const int ku = p.k <= 1 ? 1 : p.k <= 2 ? 2 : p.k <= 4 ? 4 : 8;
-  const uint64_t grid = ceil_div(all, kCombineThreads * (kCombineLoads / ku));
-  if (p.k > 8) return run(moe_combine_kernel<T, V, 8, true>, grid, 1, kCombineThreads, stream, &p);
+  constexpr int kLoads = VEC ? kCombineLoads : kCombineLoads / 2, kMost = VEC ? 8 : 4;
+  const uint64_t all = p.tokens * (VEC ? p.hidden / kPieceOf<T> : any_units<T>(p.hidden));
+  const int ku = p.k <= 1 ? 1 : p.k <= 2 ? 2 : p.k <= 4 ? 4 : kMost;
+  const uint64_t grid = ceil_div(all, kCombineThreads * (kLoads / ku));
+  if (p.k > kMost) return run(moe_combine_kernel<T, VEC, kMost, true>, grid, 1, kCombineThreads, stream, &p);
   switch (ku) {
-    case 1: return run(moe_combine_kernel<T, V, 1, false>, grid, 1, kCombineThreads, stream, &p);
-    case 2: return run(moe_combine_kernel<T, V, 2, false>, grid, 1, kCombineThreads, stream, &p);
-    case 4: return run(moe_combine_kernel<T, V, 4, false>, grid, 1, kCombineThreads, stream, &p);
-    default: return run(moe_combine_kernel<T, V, 8, false>, grid, 1, kCombineThreads, stream, &p);
+    case 1: return run(moe_combine_kernel<T, VEC, 1, false>, grid, 1, kCombineThreads, stream, &p);
+    case 2: return run(moe_combine_kernel<T, VEC, 2, false>, grid, 1, kCombineThreads, stream, &p);
+    case 4: return run(moe_combine_kernel<T, VEC, 4, false>, grid, 1, kCombineThreads, stream, &p);
+    default: return run(moe_combine_kernel<T, VEC, kMost, false>, grid, 1, kCombineThreads, stream, &p);
   }
 }
 
-template <typename T, int V>
+template <typename T, bool VEC>
 cudaError_t combine_bwd(CombineBwdParams& p, cudaStream_t stream) {
-  const uint64_t pieces = p.hidden / V;
-  if (pieces <= 64) return run(moe_combine_bwd_kernel<T, V, true>, ceil_div(p.tokens, 4), 1, 128, stream, &p);
+  const uint64_t pieces = VEC ? p.hidden / kPieceOf<T> : any_units<T>(p.hidden);
+  if (pieces <= 64) return run(moe_combine_bwd_kernel<T, VEC, true>, ceil_div(p.tokens, 4), 1, 128, stream, &p);
   const int threads = pieces >= 512 ? 256 : static_cast<int>(ceil_div(pieces, 64) * 32);
-  return run(moe_combine_bwd_kernel<T, V, false>, p.tokens, 1, threads, stream, &p);
+  return run(moe_combine_bwd_kernel<T, VEC, false>, p.tokens, 1, threads, stream, &p);
 }
 
 }  // namespace
@@ -754,28 +823,27 @@ cudaError_t launch_dispatch(const DispatchParams& params, int dtype, bool vec, c
   if (p.cta_tokens > kMoePlaceTokens) p.cta_tokens = kMoePlaceTokens;
   const uint64_t grid = p.tokens ? ceil_div(p.tokens, p.cta_tokens) : 1;  // no tokens: the offsets are still written
   switch (dtype) {
-    case ZC_BF16: return place<__nv_bfloat16>(p, vec, grid, 1, stream);
-    case ZC_F16: return place<__half>(p, vec, grid, 1, stream);
-    default: return place<float>(p, vec, grid, 1, stream);
+    case ZC_BF16: return place<__nv_bfloat16>(p, vec, grid, stream);
+    case ZC_F16: return place<__half>(p, vec, grid, stream);
+    default: return place<float>(p, vec, grid, stream);
   }
 }
 
 cudaError_t launch_combine(const CombineParams& params, int dtype, bool vec, cudaStream_t stream) {
   CombineParams p = params;
   switch (dtype) {
-    case ZC_BF16: return vec ? combine<__nv_bfloat16, kPieceOf<__nv_bfloat16>>(p, stream) : combine<__nv_bfloat16, 1>(p, stream);
-    case ZC_F16: return vec ? combine<__half, kPieceOf<__half>>(p, stream) : combine<__half, 1>(p, stream);
-    default: return vec ? combine<float, kPieceOf<float>>(p, stream) : combine<float, 1>(p, stream);
+    case ZC_BF16: return vec ? combine<__nv_bfloat16, true>(p, stream) : combine<__nv_bfloat16, false>(p, stream);
+    case ZC_F16: return vec ? combine<__half, true>(p, stream) : combine<__half, false>(p, stream);
+    default: return vec ? combine<float, true>(p, stream) : combine<float, false>(p, stream);
   }
 }
 
 cudaError_t launch_combine_bwd(const CombineBwdParams& params, int dtype, bool vec, cudaStream_t stream) {
   CombineBwdParams p = params;
   switch (dtype) {
-    case ZC_BF16:
-      return vec ? combine_bwd<__nv_bfloat16, 8>(p, stream) : combine_bwd<__nv_bfloat16, 1>(p, stream);
-    case ZC_F16: return vec ? combine_bwd<__half, 8>(p, stream) : combine_bwd<__half, 1>(p, stream);
-    default: return vec ? combine_bwd<float, 4>(p, stream) : combine_bwd<float, 1>(p, stream);
+    case ZC_BF16: return vec ? combine_bwd<__nv_bfloat16, true>(p, stream) : combine_bwd<__nv_bfloat16, false>(p, stream);
+    case ZC_F16: return vec ? combine_bwd<__half, true>(p, stream) : combine_bwd<__half, false>(p, stream);
+    default: return vec ? combine_bwd<float, true>(p, stream) : combine_bwd<float, false>(p, stream);
   }
 }
 
