@@ -1,4 +1,5 @@
-"""Builds libzc.so in-tree for sm_103a with nvcc (one process per translation unit)."""
+"""Builds libzc.so in-tree for sm_103a with nvcc (one process per translation unit), and with the host compiler the
+Python extension of the operators that take torch tensors natively."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -21,6 +22,7 @@ SAN_LIB = os.path.join(LIBDIR, "libzc_san.so")
 SAN_FLAGS = ["-fsanitize=address", "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer", "-g"]
 SOURCES = ["zc_api.cu", "zc_encode.cu", "zc_decode.cu", "zc_reduce.cu", "zc_hist.cu", "zc_noalloc.cu", "zc_pipeline.cu", "zq.cu",
            "zc_moe.cu", "zc_norm.cu", "zc_norm_bwd.cu"]
+TORCH_SOURCE = "zc_torch.cpp"  # the extension, built against the torch at hand
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
@@ -70,6 +72,62 @@ def build(force: bool = False, verbose_ptxas: bool = False, sanitize: bool = Fal
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
     return lib
+
+
+def torch_extension_path() -> str:
+    import torch
+    return os.path.join(LIBDIR, f"_zc_torch-{torch.__version__}.so")
+
+
+def _compile_extension() -> str:
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "zc_torch.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], cuda, INCLUDE]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f for d in inc for f in ("-isystem" if d != INCLUDE else "-I", d)]
+    r = subprocess.run(cmd + ["-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on {TORCH_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def build_extension(force: bool = False, obj: str | None = None) -> str:
+    """Compile and link the torch extension against libzc.so; skip if up to date."""
+    import torch
+    path = torch_extension_path()
+    if not force and obj is None and os.path.exists(path) and os.path.getmtime(path) >= _deps_mtime():
+        return path
+    build()
+    os.makedirs(BUILD, exist_ok=True)
+    obj = obj or _compile_extension()
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIBDIR, "-lzc", "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the torch extension failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+    return path
+
+
+def build_all() -> None:
+    """libzc.so and the torch extension, compiled side by side."""
+    if os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+        build_extension()
+        return
+    os.makedirs(BUILD, exist_ok=True)
+    os.makedirs(LIBDIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_compile_extension)
+        build()
+        build_extension(obj=obj.result())
 
 
 if __name__ == "__main__":

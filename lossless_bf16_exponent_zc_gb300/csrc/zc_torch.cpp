@@ -1,0 +1,468 @@
+// zc_torch.cpp -- Python entry points of the operators around an
+// expert-parallel exchange (moe.py, norm.py): torch tensors in, checked,
+// outputs allocated by torch, and one call of the C ABI (include/zc.h) on the
+// current torch stream.  Argument marshalling only, as zc.py does with ctypes;
+// native because these operators run for a few microseconds in a decoding
+// step, where five allocations, a dozen attributes and a ctypes call in
+// Python cost more than the kernels (route of 8 tokens: 9.5 us of host time in
+// Python).
+//
+// Errors: a wrong tensor raises ValueError, an error of the C ABI zc.ZcError,
+// torch's own errors (out of memory) as torch raises them.
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <string>
+
+#include "zc.h"
+
+namespace {
+
+using at::Tensor;
+
+PyObject* g_error = nullptr;  // zc.ZcError
+
+// Unwinds to the entry point with a Python exception set.
+struct Raised {};
+
+[[noreturn]] void refuse(const std::string& why) {
+  PyErr_SetString(PyExc_ValueError, why.c_str());
+  throw Raised();
+}
+
+void check(zc_status s, const char* where) {
+  if (s == ZC_OK) return;
+  PyObject* e = PyObject_CallFunction(g_error, "is", static_cast<int>(s), where);
+  if (e) {
+    PyErr_SetObject(g_error, e);
+    Py_DECREF(e);
+  }
+  throw Raised();
+}
+
+std::string shape_of(const Tensor& t) {
+  std::string s = "(";
+  for (int64_t i = 0; i < t.dim(); i++) s += (i ? ", " : "") + std::to_string(t.size(i));
+  return s + ")";
+}
+
+const Tensor& tensor(PyObject* o, const char* what) {
+  if (!THPVariable_Check(o)) {
+    PyErr_Format(PyExc_TypeError, "%s must be a tensor", what);
+    throw Raised();
+  }
+  const Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_cuda()) refuse("libzc takes CUDA tensors");
+  return t;
+}
+
+int dtype_of(const Tensor& t) {
+  switch (t.scalar_type()) {
+    case at::kBFloat16: return ZC_BF16;
+    case at::kHalf: return ZC_F16;
+    case at::kFloat: return ZC_F32;
+    default: refuse("activations are bfloat16, float16 or float32");
+  }
+}
+
+// An input matrix: contiguous columns, rows `stride` values apart.
+struct Matrix {
+  const Tensor& t;
+  uint64_t rows, width, stride;
+  const void* p() const { return t.const_data_ptr(); }
+};
+
+Matrix matrix(PyObject* o, const char* what) {
+  const Tensor& t = tensor(o, what);
+  if (t.dim() != 2) refuse(std::string(what) + " must be a matrix (rows, width), not " + shape_of(t));
+  if (t.stride(1) != 1 && t.size(1) > 1) refuse(std::string(what) + " must have contiguous columns");
+  return {t, static_cast<uint64_t>(t.size(0)), static_cast<uint64_t>(t.size(1)), static_cast<uint64_t>(t.stride(0))};
+}
+
+Matrix same_as(PyObject* o, const Tensor& like, const char* what) {
+  const Matrix m = matrix(o, what);
+  if (m.t.sizes() != like.sizes() || m.t.scalar_type() != like.scalar_type())
+    refuse(std::string(what) + " must have the shape and type of the activations");
+  return m;
+}
+
+// A contiguous table of a given type and shape.
+const Tensor& table(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const char* what) {
+  const Tensor& t = tensor(o, what);
+  if (t.scalar_type() != type || t.sizes() != shape)
+    refuse(std::string(what) + " has the wrong type or shape " + shape_of(t));
+  if (!t.is_contiguous()) refuse("libzc takes contiguous tensors");
+  return t;
+}
+
+// The caller's output tensor, checked, or a new one.
+Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Tensor& like, const char* what) {
+  if (o == Py_None) return at::empty(shape, like.options().dtype(type));
+  return table(o, shape, type, what);
+}
+
+int score_of(PyObject* o) {
+  const char* s = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : nullptr;
+  if (s && std::string(s) == "softmax") return ZC_SOFTMAX;
+  if (s && std::string(s) == "sigmoid") return ZC_SIGMOID;
+  refuse("score must be 'softmax' or 'sigmoid'");
+}
+
+long integer(PyObject* o) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised();
+  return v;
+}
+
+// A count that the C ABI takes as 32 bits; what it refuses as too large stays so.
+uint32_t count(PyObject* o, const char* what) {
+  const long v = integer(o);
+  if (v < 0) refuse(std::string(what) + " must not be negative");
+  return v > 0x7FFFFFFFl ? 0x7FFFFFFFu : static_cast<uint32_t>(v);
+}
+
+float real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised();
+  return static_cast<float>(v);
+}
+
+// The cudaStream_t to launch on: the given torch stream, else the current one of `like`'s device.
+void* stream_of(PyObject* o, const Tensor& like) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(like.device().index()).stream();
+  PyObject* raw = PyObject_GetAttrString(o, "cuda_stream");
+  if (!raw) throw Raised();
+  void* s = PyLong_AsVoidPtr(raw);
+  Py_DECREF(raw);
+  if (PyErr_Occurred()) throw Raised();
+  return s;
+}
+
+PyObject* pack(std::initializer_list<Tensor> ts) {
+  PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
+  if (!r) throw Raised();
+  Py_ssize_t i = 0;
+  for (const Tensor& t : ts) {
+    PyObject* o = Py_None;
+    if (t.defined())
+      o = THPVariable_Wrap(t);
+    else
+      Py_INCREF(o);
+    if (!o) {
+      Py_DECREF(r);
+      throw Raised();
+    }
+    PyTuple_SET_ITEM(r, i++, o);
+  }
+  return r;
+}
+
+template <typename F>
+zc_status without_gil(F&& f) {
+  zc_status s;
+  Py_BEGIN_ALLOW_THREADS
+  s = f();
+  Py_END_ALLOW_THREADS
+  return s;
+}
+
+using Args = PyObject* const*;
+
+// (logits, k, score, bias, renormalize, scale, weights, experts, stream) -> (weights, experts)
+PyObject* moe_route(Args a) {
+  const Matrix l = matrix(a[0], "logits");
+  const int64_t tokens = l.t.size(0);
+  const uint32_t k = count(a[1], "k");
+  const int dtype = dtype_of(l.t), score = score_of(a[2]), renormalize = PyObject_IsTrue(a[4]);
+  const float* bias = nullptr;
+  if (a[3] != Py_None) bias = static_cast<const float*>(table(a[3], {l.t.size(1)}, at::kFloat, "bias").const_data_ptr());
+  const float scale = real(a[5]);
+  if (k > ZC_MOE_MAX_K) check(ZC_ERR_TOO_LARGE, "zc_moe_route");  // before outputs of that size are made
+  Tensor weights = output(a[6], {tokens, k}, at::kFloat, l.t, "weights");
+  Tensor experts = output(a[7], {tokens, k}, at::kInt, l.t, "experts");
+  void* stream = stream_of(a[8], l.t);
+  check(without_gil([&] {
+          return zc_moe_route(l.p(), dtype, l.stride, l.rows, static_cast<uint32_t>(l.width), k, score, bias,
+                              renormalize, scale, static_cast<float*>(weights.mutable_data_ptr()),
+                              static_cast<int32_t*>(experts.mutable_data_ptr()), stream);
+        }),
+        "zc_moe_route");
+  return pack({weights, experts});
+}
+
+// (dweights, logits, experts, score, renormalize, scale, dlogits, stream) -> (dlogits,)
+PyObject* moe_route_backward(Args a) {
+  const Matrix l = matrix(a[1], "logits");
+  const Tensor& experts = tensor(a[2], "experts");
+  if (experts.dim() != 2) refuse("experts must be [tokens, k]");
+  const int64_t tokens = l.t.size(0), k = experts.size(1);
+  table(a[2], {tokens, k}, at::kInt, "experts");
+  const Tensor& dweights = table(a[0], {tokens, k}, at::kFloat, "dweights");
+  const int dtype = dtype_of(l.t), score = score_of(a[3]), renormalize = PyObject_IsTrue(a[4]);
+  const float scale = real(a[5]);
+  Tensor dlogits = output(a[6], l.t.sizes(), l.t.scalar_type(), l.t, "dlogits");
+  void* stream = stream_of(a[7], l.t);
+  check(without_gil([&] {
+          return zc_moe_route_backward(static_cast<const float*>(dweights.const_data_ptr()), l.p(), dtype, l.stride,
+                                       l.rows, static_cast<uint32_t>(l.width), static_cast<uint32_t>(k),
+                                       static_cast<const int32_t*>(experts.const_data_ptr()), score, renormalize,
+                                       scale, dlogits.mutable_data_ptr(), stream);
+        }),
+        "zc_moe_route_backward");
+  return pack({dlogits});
+}
+
+// (x, experts, num_experts, ws, rows, stream) -> (rows, positions, slots, offsets)
+PyObject* moe_dispatch(Args a) {
+  const Matrix x = matrix(a[0], "x");
+  const Tensor& experts = tensor(a[1], "experts");
+  const int64_t tokens = x.t.size(0);
+  if (experts.dim() != 2 || experts.size(0) != tokens ||
+      (experts.scalar_type() != at::kInt && experts.scalar_type() != at::kLong))
+    refuse("experts must be int32 or int64 [tokens, k]");
+  if (!experts.is_contiguous()) refuse("libzc takes contiguous tensors");
+  const int64_t k = experts.size(1);
+  const uint32_t n = count(a[2], "num_experts");
+  const Tensor& ws = tensor(a[3], "ws");
+  if (!ws.is_contiguous()) refuse("libzc takes contiguous tensors");
+  const int dtype = dtype_of(x.t);
+  if (n > ZC_MOE_MAX_EXPERTS || k > ZC_MOE_MAX_K) check(ZC_ERR_TOO_LARGE, "zc_moe_dispatch");
+  Tensor rows = output(a[4], {tokens * k, x.t.size(1)}, x.t.scalar_type(), x.t, "rows");
+  const auto ints = x.t.options().dtype(at::kInt);
+  Tensor positions = at::empty({tokens, k}, ints), slots = at::empty({tokens * k}, ints);
+  Tensor offsets = at::empty({static_cast<int64_t>(n) + 1}, ints);
+  void* stream = stream_of(a[5], x.t);
+  check(without_gil([&] {
+          return zc_moe_dispatch(x.p(), dtype, x.stride, x.rows, static_cast<uint32_t>(x.width),
+                                 experts.const_data_ptr(), experts.scalar_type() == at::kLong,
+                                 static_cast<uint32_t>(k), n, rows.mutable_data_ptr(),
+                                 static_cast<int32_t*>(positions.mutable_data_ptr()),
+                                 static_cast<int32_t*>(slots.mutable_data_ptr()),
+                                 static_cast<int32_t*>(offsets.mutable_data_ptr()), ws.mutable_data_ptr(),
+                                 static_cast<uint64_t>(ws.nbytes()), stream);
+        }),
+        "zc_moe_dispatch");
+  return pack({rows, positions, slots, offsets});
+}
+
+const Tensor& positions_of(PyObject* o) {
+  const Tensor& t = tensor(o, "positions");
+  if (t.dim() != 2 || t.scalar_type() != at::kInt) refuse("positions must be int32 [tokens, k]");
+  if (!t.is_contiguous()) refuse("libzc takes contiguous tensors");
+  return t;
+}
+
+// (rows, weights or None, positions, status, out, stream) -> (out,)
+PyObject* moe_combine(Args a) {
+  const Matrix r = matrix(a[0], "rows");
+  const Tensor& positions = positions_of(a[2]);
+  const int64_t tokens = positions.size(0), k = positions.size(1);
+  const int dtype = dtype_of(r.t);
+  const float* weights = nullptr;
+  if (a[1] != Py_None)
+    weights = static_cast<const float*>(table(a[1], {tokens, k}, at::kFloat, "weights").const_data_ptr());
+  const Tensor& status = table(a[3], {1}, at::kInt, "status");
+  Tensor out = output(a[4], {tokens, r.t.size(1)}, r.t.scalar_type(), r.t, "out");
+  void* stream = stream_of(a[5], r.t);
+  check(without_gil([&] {
+          return zc_moe_combine(r.p(), dtype, r.stride, r.rows, weights,
+                                static_cast<const int32_t*>(positions.const_data_ptr()),
+                                static_cast<uint64_t>(tokens), static_cast<uint32_t>(k),
+                                static_cast<uint32_t>(r.width), out.mutable_data_ptr(),
+                                static_cast<int32_t*>(status.mutable_data_ptr()), stream);
+        }),
+        "zc_moe_combine");
+  return pack({out});
+}
+
+// (dout, rows, weights, positions, status, drows, dweights, stream) -> (drows, dweights)
+PyObject* moe_combine_backward(Args a) {
+  const Matrix r = matrix(a[1], "rows"), g = matrix(a[0], "dout");
+  const Tensor& positions = positions_of(a[3]);
+  const int64_t tokens = positions.size(0), k = positions.size(1);
+  if (g.t.scalar_type() != r.t.scalar_type() || g.t.size(0) != tokens || g.width != r.width)
+    refuse("dout must be [tokens, hidden] in the rows' type");
+  const int dtype = dtype_of(r.t);
+  const Tensor& weights = table(a[2], {tokens, k}, at::kFloat, "weights");
+  const Tensor& status = table(a[4], {1}, at::kInt, "status");
+  Tensor drows = output(a[5], r.t.sizes(), r.t.scalar_type(), r.t, "drows");
+  Tensor dweights = output(a[6], {tokens, k}, at::kFloat, r.t, "dweights");
+  void* stream = stream_of(a[7], r.t);
+  check(without_gil([&] {
+          return zc_moe_combine_backward(
+              g.p(), dtype, g.stride, r.p(), r.stride, r.rows, static_cast<const float*>(weights.const_data_ptr()),
+              static_cast<const int32_t*>(positions.const_data_ptr()), static_cast<uint64_t>(tokens),
+              static_cast<uint32_t>(k), static_cast<uint32_t>(r.width), drows.mutable_data_ptr(),
+              static_cast<float*>(dweights.mutable_data_ptr()), static_cast<int32_t*>(status.mutable_data_ptr()), stream);
+        }),
+        "zc_moe_combine_backward");
+  return pack({drows, dweights});
+}
+
+// Fills in the parameters that zc_norm_args and zc_norm_backward_args share.
+template <typename A>
+void norm_params(A& a, const Tensor& x, PyObject* weight, PyObject* gate, PyObject* next_weight) {
+  a.tokens = static_cast<uint64_t>(x.size(0));
+  a.hidden = x.size(1) > 0x7FFFFFFF ? 0x7FFFFFFFu : static_cast<uint32_t>(x.size(1));
+  a.dtype = dtype_of(x);
+  bool first = true;
+  at::ScalarType kind = x.scalar_type();
+  auto param = [&](PyObject* o, const char* what) -> const Tensor& {
+    const Tensor& t = tensor(o, what);
+    if (first) kind = t.scalar_type();
+    first = false;
+    if (t.scalar_type() != kind || (kind != x.scalar_type() && kind != at::kFloat))
+      refuse("weights and gate must all have the activations' type, or all be float32");
+    if (!t.is_contiguous()) refuse("libzc takes contiguous tensors");
+    return t;
+  };
+  auto vector = [&](PyObject* o, const char* what) -> const void* {
+    if (o == Py_None) return nullptr;
+    const Tensor& t = param(o, what);
+    if (t.dim() != 1 || t.size(0) != x.size(1))
+      refuse(std::string(what) + " must have the activations' width, not " + shape_of(t));
+    return t.const_data_ptr();
+  };
+  a.weight = vector(weight, "weight");
+  a.next_weight = vector(next_weight, "next_weight");
+  if (gate != Py_None) {
+    const Tensor& g = param(gate, "gate");
+    if (g.dim() != 2 || (g.size(1) != 1 && g.size(1) != x.size(1)) || g.size(0) < 1 || x.size(0) % g.size(0))
+      refuse("gate must be [rows, hidden] or [rows, 1] with rows a divisor of the tokens");
+    a.gate = g.const_data_ptr();
+    a.gate_rows = static_cast<uint64_t>(g.size(0));
+    a.gate_wide = g.size(1) == x.size(1);
+  }
+  a.params_f32 = kind == at::kFloat && x.scalar_type() != at::kFloat;
+}
+
+// (y or None, x, weight, gate, residual_scale, next_weight, eps, x_new, h, stream) -> (x_new or None, h or None)
+PyObject* norm_forward(Args a) {
+  zc_norm_args n = {};
+  const bool branch = a[0] != Py_None;
+  const Matrix x = matrix(a[1], "x");
+  if (branch) {
+    const Matrix y = same_as(a[0], x.t, "y");
+    n.y = y.p();
+    n.y_stride = y.stride;
+    if (a[2] == Py_None) refuse("the norm after a block takes a weight");
+  }
+  n.x = x.p();
+  n.x_stride = x.stride;
+  norm_params(n, x.t, a[2], a[3], a[5]);
+  n.residual_scale = real(a[4]);
+  n.eps = real(a[6]);
+  Tensor x_new, h;
+  if (branch) x_new = output(a[7], x.t.sizes(), x.t.scalar_type(), x.t, "x_new");
+  if (a[5] != Py_None) h = output(a[8], x.t.sizes(), x.t.scalar_type(), x.t, branch ? "h" : "out");
+  if (x_new.defined()) n.x_new = x_new.mutable_data_ptr();
+  if (h.defined()) n.h = h.mutable_data_ptr();
+  void* stream = stream_of(a[9], x.t);
+  check(without_gil([&] { return zc_norm(&n, stream); }), "zc_norm");
+  return pack({x_new, h});
+}
+
+// (dx_new, dh, y, x_new, weight, gate, residual_scale, next_weight, eps, ws, stream; any of the first four may be None)
+// -> (dy, dx, dweight, dgate, dnext_weight)
+PyObject* norm_backward(Args a) {
+  zc_norm_backward_args n = {};
+  const bool branch = a[2] != Py_None;
+  const Matrix like = matrix(branch ? a[2] : a[3], branch ? "y" : "x");
+  const Tensor& x = like.t;
+  if (branch) {
+    n.y = like.p();
+    n.y_stride = like.stride;
+  }
+  if (a[0] != Py_None) {
+    const Matrix m = same_as(a[0], x, "dx_new");
+    n.dx_new = m.p();
+    n.dx_new_stride = m.stride;
+  }
+  if (a[1] != Py_None) {
+    const Matrix m = same_as(a[1], x, "dh");
+    n.dh = m.p();
+    n.dh_stride = m.stride;
+  }
+  if (a[3] != Py_None && a[7] != Py_None) {
+    const Matrix m = same_as(a[3], x, "x_new");
+    n.x_new = m.p();
+    n.x_new_stride = m.stride;
+  }
+  norm_params(n, x, a[4], a[5], a[7]);
+  n.residual_scale = real(a[6]);
+  n.eps = real(a[8]);
+  const bool none = x.size(0) == 0;  // no tokens: nothing to launch, and the sums over none of them are zero
+  Tensor dy, dx = at::empty(x.sizes(), x.options()), grads[3];
+  if (branch) dy = at::empty(x.sizes(), x.options());
+  for (int i = 0; i < 3; i++) {
+    PyObject* o = a[i == 0 ? 4 : i == 1 ? 5 : 7];
+    if (o == Py_None) continue;
+    const Tensor& p = THPVariable_Unpack(o);
+    grads[i] = none ? at::zeros(p.sizes(), p.options()) : at::empty(p.sizes(), p.options());
+  }
+  if (!none) {
+    const Tensor& ws = tensor(a[9], "ws");
+    if (!ws.is_contiguous()) refuse("libzc takes contiguous tensors");
+    n.dx = dx.mutable_data_ptr();
+    if (dy.defined()) n.dy = dy.mutable_data_ptr();
+    if (grads[0].defined()) n.dweight = grads[0].mutable_data_ptr();
+    if (grads[1].defined()) n.dgate = grads[1].mutable_data_ptr();
+    if (grads[2].defined()) n.dnext_weight = grads[2].mutable_data_ptr();
+    n.ws = ws.mutable_data_ptr();
+    n.ws_bytes = static_cast<uint64_t>(ws.nbytes());
+    void* stream = stream_of(a[10], x);
+    check(without_gil([&] { return zc_norm_backward(&n, stream); }), "zc_norm_backward");
+  }
+  return pack({dy, dx, grads[0], grads[1], grads[2]});
+}
+
+template <PyObject* (*F)(Args), Py_ssize_t N>
+PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != N) {
+    PyErr_Format(PyExc_TypeError, "%zd arguments, not %zd", N, n);
+    return nullptr;
+  }
+  try {
+    return F(args);
+  } catch (const Raised&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* set_error(PyObject*, PyObject* cls) {
+  Py_INCREF(cls);
+  Py_XDECREF(g_error);
+  g_error = cls;
+  Py_RETURN_NONE;
+}
+
+template <PyObject* (*F)(Args), Py_ssize_t N>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(entry<F, N>)), METH_FASTCALL, nullptr};
+}
+
+PyMethodDef g_methods[] = {
+    method<moe_route, 9>("moe_route"),
+    method<moe_route_backward, 8>("moe_route_backward"),
+    method<moe_dispatch, 6>("moe_dispatch"),
+    method<moe_combine, 6>("moe_combine"),
+    method<moe_combine_backward, 8>("moe_combine_backward"),
+    method<norm_forward, 10>("norm_forward"),
+    method<norm_backward, 11>("norm_backward"),
+    {"set_error", set_error, METH_O, nullptr},
+    {nullptr, nullptr, 0, nullptr},
+};
+
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_zc_torch", "torch entry points of libzc (zc_torch.cpp)", -1, g_methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__zc_torch() { return PyModule_Create(&g_module); }

@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 from dataclasses import dataclass
 from typing import Sequence
@@ -51,24 +53,6 @@ class LinkModel(ctypes.Structure):
 
 class CodecModel(ctypes.Structure):
     _fields_ = [("compress_gbps", ctypes.c_double), ("decompress_gbps", ctypes.c_double), ("ratio", ctypes.c_double)]
-
-
-class NormArgs(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("y", "x")] + [(n, ctypes.c_uint64) for n in
-                ("y_stride", "x_stride", "tokens")] + [(n, ctypes.c_void_p) for n in
-                ("weight", "gate", "next_weight")] + [("gate_rows", ctypes.c_uint64), ("hidden", ctypes.c_uint32),
-                ("dtype", ctypes.c_int32), ("gate_wide", ctypes.c_int32), ("params_f32", ctypes.c_int32),
-                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float), ("x_new", ctypes.c_void_p),
-                ("h", ctypes.c_void_p)]
-
-
-class NormBackwardArgs(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("dx_new", "dh", "y", "x_new")] + [(n, ctypes.c_uint64) for n in
-                ("dx_new_stride", "dh_stride", "y_stride", "x_new_stride", "tokens")] + [(n, ctypes.c_void_p) for n in
-                ("weight", "gate", "next_weight")] + [("gate_rows", ctypes.c_uint64), ("hidden", ctypes.c_uint32),
-                ("dtype", ctypes.c_int32), ("gate_wide", ctypes.c_int32), ("params_f32", ctypes.c_int32),
-                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)] + [(n, ctypes.c_void_p) for n in
-                ("dy", "dx", "dweight", "dgate", "dnext_weight", "ws")] + [("ws_bytes", ctypes.c_uint64)]
 
 
 class ZcTensor(ctypes.Structure):
@@ -131,28 +115,35 @@ def load() -> ctypes.CDLL:
     lib.zc_pipeline_plan_create.argtypes = [vp, u64, vp, vp, u64, vp, u64, vp, i32, ctypes.POINTER(vp)]
     lib.zc_pipeline_plan_launch.argtypes = [vp, vp]
     lib.zc_pipeline_plan_destroy.argtypes = [vp]
-    u32, f32 = ctypes.c_uint32, ctypes.c_float
-    lib.zc_moe_route.argtypes = [vp, i32, u64, u64, u32, u32, i32, vp, i32, f32, vp, vp, vp]
-    lib.zc_moe_route_backward.argtypes = [vp, vp, i32, u64, u64, u32, u32, vp, i32, i32, f32, vp, vp]
+    u32 = ctypes.c_uint32
     lib.zc_moe_workspace_size.argtypes = [u64, u32, u32, u64p]
-    lib.zc_moe_dispatch.argtypes = [vp, i32, u64, u64, u32, vp, i32, u32, u32, vp, vp, vp, vp, vp, u64, vp]
-    lib.zc_moe_combine.argtypes = [vp, i32, u64, u64, vp, vp, u64, u32, u32, vp, vp, vp]
-    lib.zc_moe_combine_backward.argtypes = [vp, i32, u64, vp, u64, u64, vp, vp, u64, u32, u32, vp, vp, vp, vp]
-    lib.zc_norm.argtypes = [ctypes.POINTER(NormArgs), vp]
     lib.zc_norm_workspace_size.argtypes = [u64, u32, u64p]
-    lib.zc_norm_backward.argtypes = [ctypes.POINTER(NormBackwardArgs), vp]
     for name in ("zc_codebook_from_sigma", "zc_compressed_size", "zc_workspace_size", "zc_histogram_topk",
                  "zc_compress", "zc_compress_adaptive", "zc_raw_spill", "zc_decompress", "zc_decompress_reduce",
                  "zc_compress_batched", "zc_compress_batched_adaptive", "zc_decompress_batched",
                  "zc_pipeline_workspace_size", "zc_pipelined_transfer", "zc_pipeline_plan_create",
                  "zc_pipeline_plan_launch", "zc_pipeline_plan_destroy", "zq_default_widths",
                  "zq_table_from_histogram", "zq_max_bytes", "zq_compress", "zq_decompress", "zc_transfer_pays",
-                 "zc_reduce_scatter_choose", "zc_moe_route", "zc_moe_route_backward", "zc_moe_workspace_size",
-                 "zc_moe_dispatch", "zc_moe_combine", "zc_moe_combine_backward", "zc_norm", "zc_norm_workspace_size",
-                 "zc_norm_backward"):
+                 "zc_reduce_scatter_choose", "zc_moe_workspace_size", "zc_norm_workspace_size"):
         getattr(lib, name).restype = i32
     _lib = lib
     return lib
+
+
+_native = None
+
+
+def native():
+    """The extension with the entry points of moe.py and norm.py (csrc/zc_torch.cpp), built first if missing or stale."""
+    global _native
+    if _native is None:
+        loader = importlib.machinery.ExtensionFileLoader("_zc_torch", _build.build_extension())
+        spec = importlib.machinery.ModuleSpec("_zc_torch", loader, origin=loader.path)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.set_error(ZcError)
+        _native = module
+    return _native
 
 
 def status_string(code: int) -> str:
@@ -198,37 +189,6 @@ def _nelem16(x: torch.Tensor) -> int:
     if x.element_size() != 2:
         raise ValueError("bfloat16 data must be a 2-byte dtype (bfloat16, int16 or uint16)")
     return x.numel()
-
-
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # zc_dtype
-
-
-def _dtype(t: torch.Tensor) -> int:
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"activations are bfloat16, float16 or float32, not {t.dtype}")
-    return code
-
-
-def _rows(t: torch.Tensor, what: str) -> tuple[int, int]:
-    """(device pointer, row stride in values) of an input matrix; its columns must be contiguous."""
-    if not t.is_cuda:
-        raise ValueError("libzc takes CUDA tensors")
-    if t.dim() != 2:
-        raise ValueError(f"{what} must be a matrix (rows, width), not {tuple(t.shape)}")
-    row, col = t.stride()
-    if col != 1 and t.shape[1] > 1:
-        raise ValueError(f"{what} must have contiguous columns")
-    return t.data_ptr(), row
-
-
-def _output(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, device, what: str) -> torch.Tensor:
-    """The caller's output tensor, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous CUDA tensor of shape {tuple(shape)} and type {dtype}")
-    return t
 
 
 # ------------------------------------------------------------------ host-side pure functions

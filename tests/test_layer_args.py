@@ -5,6 +5,37 @@ import pytest
 
 from lossless_bf16_exponent_zc_gb300 import moe, norm, zc
 
+class NormArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("y", "x")] + [(n, ctypes.c_uint64) for n in
+                ("y_stride", "x_stride", "tokens")] + [(n, ctypes.c_void_p) for n in
+                ("weight", "gate", "next_weight")] + [("gate_rows", ctypes.c_uint64), ("hidden", ctypes.c_uint32),
+                ("dtype", ctypes.c_int32), ("gate_wide", ctypes.c_int32), ("params_f32", ctypes.c_int32),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float), ("x_new", ctypes.c_void_p),
+                ("h", ctypes.c_void_p)]
+
+
+class NormBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx_new", "dh", "y", "x_new")] + [(n, ctypes.c_uint64) for n in
+                ("dx_new_stride", "dh_stride", "y_stride", "x_new_stride", "tokens")] + [(n, ctypes.c_void_p) for n in
+                ("weight", "gate", "next_weight")] + [("gate_rows", ctypes.c_uint64), ("hidden", ctypes.c_uint32),
+                ("dtype", ctypes.c_int32), ("gate_wide", ctypes.c_int32), ("params_f32", ctypes.c_int32),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)] + [(n, ctypes.c_void_p) for n in
+                ("dy", "dx", "dweight", "dgate", "dnext_weight", "ws")] + [("ws_bytes", ctypes.c_uint64)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def prototypes():
+    lib = zc.load()
+    vp, u64, u32, i32, f32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int, ctypes.c_float
+    lib.zc_moe_route.argtypes = [vp, i32, u64, u64, u32, u32, i32, vp, i32, f32, vp, vp, vp]
+    lib.zc_moe_route_backward.argtypes = [vp, vp, i32, u64, u64, u32, u32, vp, i32, i32, f32, vp, vp]
+    lib.zc_moe_dispatch.argtypes = [vp, i32, u64, u64, u32, vp, i32, u32, u32, vp, vp, vp, vp, vp, u64, vp]
+    lib.zc_moe_combine.argtypes = [vp, i32, u64, u64, vp, vp, u64, u32, u32, vp, vp, vp]
+    lib.zc_moe_combine_backward.argtypes = [vp, i32, u64, vp, u64, u64, vp, vp, u64, u32, u32, vp, vp, vp, vp]
+    lib.zc_norm.argtypes = [ctypes.POINTER(NormArgs), vp]
+    lib.zc_norm_backward.argtypes = [ctypes.POINTER(NormBackwardArgs), vp]
+
+
 F = 0x10000  # an aligned address that is never dereferenced: every call below is refused first
 
 
@@ -104,8 +135,8 @@ def test_norm():
            ({"next_weight": None}, "INVALID_ARG"), ({"h": F + 1}, "ALIGNMENT"), ({"x_new": F + 1}, "ALIGNMENT")]
     for kw, want in COMMON + own:
         kw = {n: v for n, v in kw.items() if n != "dgate"}
-        assert lib.zc_norm(norm_args(zc.NormArgs, **kw), None) == getattr(zc, "ERR_" + want), kw
-    assert lib.zc_norm(norm_args(zc.NormArgs, tokens=0, x=None), None) == zc.OK
+        assert lib.zc_norm(norm_args(NormArgs, **kw), None) == getattr(zc, "ERR_" + want), kw
+    assert lib.zc_norm(norm_args(NormArgs, tokens=0, x=None), None) == zc.OK
 
 
 def test_norm_backward():
@@ -117,7 +148,7 @@ def test_norm_backward():
            ({"dx": F + 1}, "ALIGNMENT"), ({"ws_bytes": norm.workspace_size(4, 16) - 1}, "WORKSPACE"),
            ({"dh": None, "next_weight": None, "dnext_weight": None, "dx_new": None}, "INVALID_ARG")]
     for kw, want in COMMON + own:
-        assert lib.zc_norm_backward(norm_args(zc.NormBackwardArgs, **kw), None) == getattr(zc, "ERR_" + want), kw
+        assert lib.zc_norm_backward(norm_args(NormBackwardArgs, **kw), None) == getattr(zc, "ERR_" + want), kw
 
 
 def test_sizes():
