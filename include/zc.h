@@ -608,7 +608,7 @@ typedef struct zc_norm_args {
 } zc_norm_args;
 zc_status zc_norm(const zc_norm_args* h_args, void* stream);
 
-/* Workspace of zc_norm_backward (bytes; 4-byte aligned). */
+/* Workspace of zc_norm_backward (bytes; 16-byte aligned). */
 zc_status zc_norm_workspace_size(uint64_t tokens, uint32_t hidden, uint64_t* bytes);
 
 /*

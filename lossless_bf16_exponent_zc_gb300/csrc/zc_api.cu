@@ -703,7 +703,9 @@ zc_status zc_moe_combine_backward(const void* d_dout, int dtype, uint64_t dout_s
                         d_weights, d_positions, d_drows,     d_dweights,  d_status, hidden, k};
   const bool vec = in_pieces(d_rows, rows_stride, hidden, size) && in_pieces(d_dout, dout_stride, hidden, size) &&
                    aligned(d_drows, 16);
-  return cuda_status(launch_combine_bwd(p, dtype, vec, as_stream(stream)));
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;
+  return cuda_status(launch_combine_bwd(p, dtype, vec, as_stream(stream), dev));
 }
 
 zc_status zc_norm(const zc_norm_args* h_args, void* stream) {
@@ -770,7 +772,7 @@ zc_status zc_norm_backward(const zc_norm_backward_args* h_args, void* stream) {
     return ZC_ERR_INVALID_ARG;
   const uint32_t psize = a.params_f32 ? 4 : size;
   if (!aligned(a.dx, size) || !aligned(a.dy, size) || !aligned(a.dweight, psize) || !aligned(a.dgate, psize) ||
-      !aligned(a.dnext_weight, psize) || !aligned(a.ws, 4))
+      !aligned(a.dnext_weight, psize) || !aligned(a.ws, 16))
     return ZC_ERR_ALIGNMENT;
   const uint64_t need = norm_workspace_bytes(a.tokens, a.hidden);
   if (!a.ws && need) return ZC_ERR_INVALID_ARG;

@@ -171,7 +171,8 @@ struct CombineBwdParams {
   uint32_t hidden, k;
 };
 cudaError_t launch_combine(const CombineParams& p, int dtype, bool vec, cudaStream_t stream);
-cudaError_t launch_combine_bwd(const CombineBwdParams& p, int dtype, bool vec, cudaStream_t stream);
+cudaError_t launch_combine_bwd(const CombineBwdParams& p, int dtype, bool vec, cudaStream_t stream,
+                               const DeviceInfo& dev);
 
 // Gate of a token: row token / gate_tokens of a table with `hidden` columns, or
 // with one (gate_wide = 0); gate NULL: 1.
@@ -195,7 +196,7 @@ struct NormBwdParams {
   void *dy, *dx, *dweight, *dgate, *dnext_weight;
   float* parts;  // workspace
   uint32_t hidden;
-  uint32_t splits, units, ctas;  // set by the launch: row ranges per gate row, ranges in all, CTAs
+  uint32_t splits, units, walkers, ctas;  // set by the launch: ranges of rows per gate row and in all; who walks them
 };
 uint64_t norm_workspace_bytes(uint64_t tokens, uint32_t hidden);
 cudaError_t launch_norm(const NormParams& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev);

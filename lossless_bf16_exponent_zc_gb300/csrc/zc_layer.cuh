@@ -130,8 +130,8 @@ __device__ __forceinline__ Piece<T, kPieceOf<T>> load_any(const T* p) {
 }
 
 // How a row of `width` values that is written at p falls into aligned 16-byte pieces: `head` values before the first
-// piece, `body` pieces, and the rest.  Work on the row is cut into body + 2 units: the head, the pieces, the tail;
-// at most any_units(width) of them.
+// piece, `body` pieces, and the rest.  Work on the row is cut into units: the pieces, then the values outside them one by
+// one, so that no thread has several of those to take in turn; at most any_units(width) of them.
 template <typename T>
 struct RowCut {
   uint32_t head, body;
@@ -141,16 +141,20 @@ struct RowCut {
     head = head < width ? head : width;
     body = (width - head) / kV;
   }
-  // The values [first, last) of unit u; `whole`: one aligned piece.
-  __device__ __forceinline__ bool unit(uint32_t u, uint32_t width, uint32_t* first, uint32_t* last) const {
+  // Unit u's first value, and how many it has: a piece's, 1, or 0 where the row has no such unit.
+  __device__ __forceinline__ uint32_t unit(uint32_t u, uint32_t width, uint32_t* first) const {
     constexpr uint32_t kV = kPieceOf<T>;
-    *first = u == 0 ? 0 : head + (u - 1) * kV;
-    *last = u == 0 ? head : u <= body ? *first + kV : width;
-    return u >= 1 && u <= body;
+    if (u < body) {
+      *first = head + u * kV;
+      return kV;
+    }
+    const uint32_t e = u - body;
+    *first = e < head ? e : body * kV + e;
+    return *first < width ? 1 : 0;
   }
 };
 template <typename T>
-__host__ __device__ constexpr uint32_t any_units(uint32_t width) { return width / kPieceOf<T> + 2; }
+__host__ __device__ constexpr uint32_t any_units(uint32_t width) { return width / kPieceOf<T> + 2 * (kPieceOf<T> - 1); }
 
 __device__ __forceinline__ float warp_sum_f32(float v) {
 #pragma unroll

@@ -488,12 +488,12 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams 
       if (VEC) {
         (pos < 0 ? Piece<T, V>::zero() : v).store(dst + static_cast<uint64_t>(u) * V);
       } else {  // every row in pieces of its own alignment
-        const RowCut<T> cut(dst, p.hidden);
-        uint32_t first, last;
-        if (cut.unit(u, p.hidden, &first, &last))
+        uint32_t first;
+        const uint32_t n = RowCut<T>(dst, p.hidden).unit(u, p.hidden, &first);
+        if (n == V)
           (pos < 0 ? Piece<T, V>::zero() : load_any(src + first)).store(dst + first);
-        else
-          for (uint32_t c = first; c < last; c++) dst[c] = pos < 0 ? from_f32<T>(0.f) : src[c];
+        else if (n)
+          dst[first] = pos < 0 ? from_f32<T>(0.f) : src[first];
       }
     }
   }
@@ -538,10 +538,9 @@ __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_
       const uint32_t i = c0 + q * kCombineThreads, dt = i / pieces, u = i - dt * pieces;
       const uint64_t t = t0 + dt;
       T* out = static_cast<T*>(p.out) + t * p.hidden;
-      uint32_t first = u * V, last = first + V;
-      bool piece = true;
-      if (!VEC) piece = RowCut<T>(out, p.hidden).unit(u, p.hidden, &first, &last);
-      to[q] = t < p.tokens && piece ? out + first : nullptr;
+      uint32_t first = u * V, values = V;
+      if (!VEC) values = RowCut<T>(out, p.hidden).unit(u, p.hidden, &first);
+      to[q] = t < p.tokens && values == V ? out + first : nullptr;
 #pragma unroll
       for (int k = 0; k < KU; k++) {
         w[q][k] = 0.f;
@@ -556,18 +555,17 @@ __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_
           }
         }
       }
-      if (!VEC && t < p.tokens && !piece && k0 == 0) {  // a head or a tail, value by value
-        for (uint32_t c = first; c < last; c++) {
-          float sum = 0.f;
-          for (uint32_t k = 0; k < p.k; k++) {
-            uint64_t row;
-            bool inside;
-            if (slot_row(p.positions[t * p.k + k], p.n_rows, p.status, &row, &inside))
-              sum = fmaf(p.weights ? p.weights[t * p.k + k] : 1.f,
-                         to_f32<T>(static_cast<const T*>(p.rows)[row * p.row_stride + c]), sum);
-          }
-          out[c] = from_f32<T>(sum);
+      if (!VEC && t < p.tokens && values == 1 && k0 == 0) {  // a value outside the pieces
+        float sum = 0.f;
+#pragma unroll 4
+        for (uint32_t k = 0; k < p.k; k++) {
+          uint64_t row;
+          bool inside;
+          if (slot_row(p.positions[t * p.k + k], p.n_rows, p.status, &row, &inside))
+            sum = fmaf(p.weights ? p.weights[t * p.k + k] : 1.f,
+                       to_f32<T>(static_cast<const T*>(p.rows)[row * p.row_stride + first]), sum);
         }
+        out[first] = from_f32<T>(sum);
       }
     }
 #pragma unroll
@@ -608,7 +606,7 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
   const uint32_t me = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
   const uint32_t pieces = VEC ? p.hidden / V : any_units<T>(p.hidden);
   const T* dout = static_cast<const T*>(p.dout) + t * p.dout_stride;
-  for (uint32_t k0 = 0, turn = 0; k0 < p.k; k0 += kCombineBwdK, turn ^= 1) {
+  for (uint32_t k0 = blockIdx.y * kCombineBwdK, turn = 0; k0 < p.k; k0 += gridDim.y * kCombineBwdK, turn ^= 1) {
     float dot[kCombineBwdK], w[kCombineBwdK];
     const T* from[kCombineBwdK];
     T* to[kCombineBwdK];
@@ -653,20 +651,24 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
         }
       } else {  // every row in pieces of its own alignment
         Piece<T, V> v[kCombineBwdK], g[kCombineBwdK];
-        uint32_t first[kCombineBwdK], last[kCombineBwdK];
-        bool piece[kCombineBwdK];
+        uint32_t first[kCombineBwdK], values[kCombineBwdK];
+        float one_v[kCombineBwdK], one_g[kCombineBwdK];
 #pragma unroll
         for (int k = 0; k < kCombineBwdK; k++) {
           v[k] = g[k] = Piece<T, V>::zero();
-          piece[k] = inside[k] && RowCut<T>(to[k], p.hidden).unit(u, p.hidden, &first[k], &last[k]);
-          if (piece[k] && routed[k]) {
+          one_v[k] = one_g[k] = 0.f;
+          values[k] = inside[k] ? RowCut<T>(to[k], p.hidden).unit(u, p.hidden, &first[k]) : 0;
+          if (values[k] == V && routed[k]) {
             v[k] = load_any(from[k] + first[k]);
             g[k] = load_any(dout + first[k]);
+          } else if (values[k] && routed[k]) {
+            one_v[k] = to_f32<T>(from[k][first[k]]);
+            one_g[k] = to_f32<T>(dout[first[k]]);
           }
         }
 #pragma unroll
         for (int k = 0; k < kCombineBwdK; k++) {
-          if (piece[k]) {
+          if (values[k] == V) {
             float f[V], d[V];
             v[k].get(f);
             g[k].get(d);
@@ -678,12 +680,9 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
             Piece<T, V> o;
             o.set(d);
             o.store(to[k] + first[k]);
-          } else if (inside[k]) {
-            for (uint32_t c = first[k]; c < last[k]; c++) {
-              const float d = routed[k] ? to_f32<T>(dout[c]) : 0.f;
-              if (routed[k]) dot[k] = fmaf(d, to_f32<T>(from[k][c]), dot[k]);
-              to[k][c] = from_f32<T>(routed[k] ? w[k] * d : 0.f);
-            }
+          } else if (values[k]) {
+            dot[k] = fmaf(one_g[k], one_v[k], dot[k]);
+            to[k][first[k]] = from_f32<T>(routed[k] ? w[k] * one_g[k] : 0.f);
           }
         }
       }
@@ -775,11 +774,16 @@ cudaError_t combine(CombineParams& p, cudaStream_t stream) {
 }
 
 template <typename T, bool VEC>
-cudaError_t combine_bwd(CombineBwdParams& p, cudaStream_t stream) {
+cudaError_t combine_bwd(CombineBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   const uint64_t pieces = VEC ? p.hidden / kPieceOf<T> : any_units<T>(p.hidden);
-  if (pieces <= 64) return run(moe_combine_bwd_kernel<T, VEC, true>, ceil_div(p.tokens, 4), 1, 128, stream, &p);
-  const int threads = pieces >= 512 ? 256 : static_cast<int>(ceil_div(pieces, 64) * 32);
-  return run(moe_combine_bwd_kernel<T, VEC, false>, p.tokens, 1, threads, stream, &p);
+  // Few tokens leave SMs idle: their slots, four at a time, then go to CTAs of their own, which hold a piece a thread.
+  const bool few = p.tokens < 2ull * static_cast<uint64_t>(dev.sm_count);
+  const uint32_t split = few ? static_cast<uint32_t>(ceil_div(p.k, kCombineBwdK)) : 1;
+  if (pieces <= 64)
+    return run(moe_combine_bwd_kernel<T, VEC, true>, ceil_div(p.tokens, 4), split, 128, stream, &p);
+  const uint64_t warps = ceil_div(pieces, few ? 32 : 64), most = few ? 16 : 8;
+  return run(moe_combine_bwd_kernel<T, VEC, false>, p.tokens, split, static_cast<int>(32 * (warps < most ? warps : most)),
+             stream, &p);
 }
 
 }  // namespace
@@ -838,12 +842,13 @@ cudaError_t launch_combine(const CombineParams& params, int dtype, bool vec, cud
   }
 }
 
-cudaError_t launch_combine_bwd(const CombineBwdParams& params, int dtype, bool vec, cudaStream_t stream) {
+cudaError_t launch_combine_bwd(const CombineBwdParams& params, int dtype, bool vec, cudaStream_t stream,
+                               const DeviceInfo& dev) {
   CombineBwdParams p = params;
   switch (dtype) {
-    case ZC_BF16: return vec ? combine_bwd<__nv_bfloat16, true>(p, stream) : combine_bwd<__nv_bfloat16, false>(p, stream);
-    case ZC_F16: return vec ? combine_bwd<__half, true>(p, stream) : combine_bwd<__half, false>(p, stream);
-    default: return vec ? combine_bwd<float, true>(p, stream) : combine_bwd<float, false>(p, stream);
+    case ZC_BF16: return vec ? combine_bwd<__nv_bfloat16, true>(p, stream, dev) : combine_bwd<__nv_bfloat16, false>(p, stream, dev);
+    case ZC_F16: return vec ? combine_bwd<__half, true>(p, stream, dev) : combine_bwd<__half, false>(p, stream, dev);
+    default: return vec ? combine_bwd<float, true>(p, stream, dev) : combine_bwd<float, false>(p, stream, dev);
   }
 }
 

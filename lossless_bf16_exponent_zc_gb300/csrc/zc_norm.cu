@@ -13,6 +13,8 @@ namespace zc {
 
 namespace {
 
+constexpr uint32_t kNormWarpWidth = 512;  // widest row that a warp holds
+
 template <typename T, int V, int NV, bool WARP, bool BRANCH, bool NEXT, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_kernel(NormParams p) {
   __shared__ float red[2][32];
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormPara
   pdl_allow_dependents();
   for (uint32_t i = threadIdx.x; i < 256; i += blockDim.x) red[i >> 7][i & 127] = 0.f;
   pdl_wait();
-  const Ring ring{ring_smem, blockDim.x, p.hidden / V};
+  const Ring ring{ring_smem, threadIdx.x, blockDim.x, p.hidden / V};
 #pragma unroll
   for (int i = 0; i < (BRANCH ? 2 : 1); i++) ring.clear(i, false);
   const float inv_d = 1.f / static_cast<float>(p.hidden);

@@ -33,10 +33,34 @@ __device__ __forceinline__ float load_param(const void* base, int is_f32, uint64
   return f[0];
 }
 
-// Launch shapes.  A row of up to kNormWarpWidth values is held by a warp.  Wider rows stream through a CTA's shared
+// V fp32 values at p, 16-byte aligned where V is a multiple of 4.
+template <int V>
+__device__ __forceinline__ void load_f32(const float* p, float (&f)[V]) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + i);
+      f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i++) f[i] = p[i];
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_f32(float* p, const float (&f)[V]) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i++) p[i] = f[i];
+  }
+}
+
+// Launch shapes.  A narrow row is held by a warp.  Wider rows stream through a CTA's shared
 // memory, one thread for every 8 or 16 columns; rows too wide for that ring are held in a CTA's registers.
-constexpr uint32_t kNormWarpWidth = 512;
-constexpr int kNormWarps = 8;         // rows of a CTA in the warp shape
+constexpr int kNormWarps = 8;  // rows of a CTA in the warp shape
 constexpr int kNormRingThreads = 512;
 constexpr int kNormRingSmem = 225 * 1024;  // what the ring may take of the 227 KB a CTA can have
 
@@ -51,7 +75,7 @@ struct RowRing {
   static constexpr int NV = COLS / V;
   static constexpr bool kWords = V == 1 && sizeof(T) == 2;
   uint8_t* smem;
-  uint32_t threads, pieces;
+  uint32_t me, threads, pieces;  // this thread among those that share a row, and the row's pieces
 
   __host__ __device__ static uint32_t region(uint32_t threads) {  // bytes of one row of one matrix
     return kWords ? (threads * NV * 2 + 4 + 15) / 16 * 16 : threads * NV * V * static_cast<uint32_t>(sizeof(T));
@@ -64,7 +88,7 @@ struct RowRing {
   // Where a thread's walk through a matrix starts: its first column of row t.
   template <typename U>
   __device__ __forceinline__ U* start(U* base, uint64_t t, uint64_t stride) const {
-    return base + t * stride + (kWords ? 0 : threadIdx.x * V);
+    return base + t * stride + (kWords ? 0 : me * V);
   }
   __device__ __forceinline__ void copy(int stage, int array, const T* row) const {
     uint8_t* to = at(stage, array);
@@ -72,12 +96,12 @@ struct RowRing {
       const uintptr_t a = reinterpret_cast<uintptr_t>(row);
       const uint32_t words = (static_cast<uint32_t>(a & 2) + 2 * pieces + 3) / 4;
       const uint32_t* from = reinterpret_cast<const uint32_t*>(a & ~static_cast<uintptr_t>(3));
-      for (uint32_t w = threadIdx.x; w < words; w += threads) cp_async_4(to + 4 * w, from + w);
+      for (uint32_t w = me; w < words; w += threads) cp_async_4(to + 4 * w, from + w);
     } else {
-      to += threadIdx.x * V * sizeof(T);
+      to += me * V * sizeof(T);
 #pragma unroll
       for (int i = 0; i < NV; i++) {
-        if (threadIdx.x + i * threads >= pieces) continue;
+        if (me + i * threads >= pieces) continue;
         if (V == 1)
           cp_async_4(to + i * threads * 4, row + i * threads);
         else
@@ -92,7 +116,7 @@ struct RowRing {
       for (int stage = 0; stage < STAGES; stage++)
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-          const uint32_t c = threadIdx.x + i * threads;
+          const uint32_t c = me + i * threads;
           if (all || c >= pieces) Piece<T, V>::zero().store(reinterpret_cast<T*>(at(stage, array)) + c * V);
         }
     }
@@ -102,9 +126,17 @@ struct RowRing {
     const uint8_t* from = at(stage, array) + (kWords ? reinterpret_cast<uintptr_t>(row) & 2 : 0);
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-      const uint32_t c = threadIdx.x + i * threads;
+      const uint32_t c = me + i * threads;
       v[i] = Piece<T, V>::zero();
       if (!kWords || c < pieces) v[i] = Piece<T, V>::load(reinterpret_cast<const T*>(from) + c * V);
+    }
+  }
+  // The same straight from the matrix.
+  __device__ __forceinline__ void load(const T* row, Piece<T, V> (&v)[NV]) const {
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+      v[i] = Piece<T, V>::zero();
+      if (me + i * threads < pieces) v[i] = Piece<T, V>::load(row + (me + i * threads) * V);
     }
   }
   __device__ __forceinline__ static void unpack(const Piece<T, V> (&v)[NV], float2 (&f)[COLS / 2]) {
@@ -125,7 +157,7 @@ struct RowRing {
   // Writes this thread's columns of an output row, from its address by start().
   __device__ __forceinline__ void put(T* row, const float2 (&f)[COLS / 2]) const {
     const float* flat = reinterpret_cast<const float*>(f);
-    if (kWords) row += threadIdx.x;
+    if (kWords) row += me;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       float v[V];
@@ -133,7 +165,7 @@ struct RowRing {
       for (int j = 0; j < V; j++) v[j] = flat[i * V + j];
       Piece<T, V> o;
       o.set(v);
-      if (threadIdx.x + i * threads < pieces) o.store(row + i * threads * V);
+      if (me + i * threads < pieces) o.store(row + i * threads * V);
     }
   }
   // This thread's columns of a parameter row.
@@ -141,7 +173,7 @@ struct RowRing {
     float* flat = reinterpret_cast<float*>(f);
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-      const uint32_t c = threadIdx.x + i * threads;
+      const uint32_t c = me + i * threads;
       float v[V];
 #pragma unroll
       for (int j = 0; j < V; j++) v[j] = 0.f;

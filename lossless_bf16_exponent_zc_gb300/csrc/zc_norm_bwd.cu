@@ -17,18 +17,21 @@ namespace zc {
 
 namespace {
 
-// Most CTAs whose sums the workspace holds.
-__host__ __device__ constexpr uint32_t norm_max_ctas(uint32_t hidden) { return hidden > 2048 ? 608 : 1216; }
+constexpr uint32_t kNormWarpWidth = 256;  // widest row that a warp holds
+// Most ranges of rows, and CTAs, whose sums the workspace holds.
+__host__ __device__ constexpr uint32_t norm_max_units(uint32_t hidden) {
+  return hidden > 2048 ? 608 : hidden > kNormWarpWidth ? 1216 : 4864;
+}
 constexpr int kBwdStages = 3;
 
-// Columns of a thread in the ring shape.  With 8 the column sums, the weights and a row fit the 128 registers of a
-// 512-thread CTA; 16 columns in 256 threads, two CTAs an SM, spill 260 bytes a thread and take 170 us instead of 130
-// (16384 x 4096 bf16), and 8 in 64 registers, again for two CTAs, 238 us: the ring leaves the L1 cache too small for
-// spilled registers.
-constexpr int kBwdCols = 8;
+// Columns of a thread in the ring shape: 8, and 16 for 16-bit rows that 8 of each of 512 threads do not hold.  With 8 the
+// column sums, the weights and a row fit the 128 registers of a 512-thread CTA; 16 columns in 256 threads, two CTAs an
+// SM, spill registers and take 170 us instead of 130 (16384 x 4096 bf16), and 8 in 64 registers, again for two CTAs,
+// 238 us: the ring leaves the L1 cache too small for spilled registers.
+constexpr int kBwdCols = 8, kBwdWideCols = 16;
 
-// Rows of a CTA, unit after unit: u = blockIdx.x, blockIdx.x + ctas, ...  A unit takes every splits-th row of a gate
-// row's tokens, so that neighbouring CTAs read neighbouring rows at about the same time.
+// Rows of a walker (a CTA; a warp in the warp shape), unit after unit: u = its number, number + walkers, ...  A unit takes every splits-th row of a gate
+// row's tokens, so that neighbouring walkers read neighbouring rows at about the same time.
 struct BwdWalk {
   uint32_t u;
   uint64_t t, last;
@@ -43,7 +46,7 @@ struct BwdWalk {
   __device__ __forceinline__ bool next(const NormBwdParams& p) {
     t += p.splits;
     if (t < last) return false;
-    u += p.ctas;
+    u += p.walkers;
     if (u < p.units) open(p);
     return true;
   }
@@ -53,9 +56,9 @@ struct BwdWalk {
 // second is taken together with the next row's first, so that a row costs one barrier: between two barriers the CTA
 // writes the last row's dy, takes this row's G, dx, column sums and v y, and the next row's first sums.  The inputs are
 // read from the stage twice rather than held, so that the column sums and the weights stay in registers.
-template <typename T, int V, bool BRANCH, bool NEXT>
+template <typename T, int V, int C, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(NormBwdParams p) {
-  constexpr int C = kBwdCols, P = C / 2;
+  constexpr int P = C / 2;
   constexpr int kGx = 0, kGh = 1, kX = 2, kY = NEXT ? 3 : 1, kArrays = BRANCH && NEXT ? 4 : NEXT ? 3 : 2;
   using Ring = RowRing<T, V, C, kArrays, kBwdStages>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
@@ -63,7 +66,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
   pdl_allow_dependents();
   for (uint32_t i = threadIdx.x; i < 256; i += blockDim.x) red[0][i] = 0.f;
   pdl_wait();
-  const Ring ring{ring_smem, blockDim.x, p.hidden / V};
+  const Ring ring{ring_smem, threadIdx.x, blockDim.x, p.hidden / V};
   const float inv_d = 1.f / static_cast<float>(p.hidden);
   const bool wide = BRANCH && p.gate && p.gate_wide, narrow = BRANCH && p.gate && !p.gate_wide;
   const bool past = p.dx_new != nullptr;
@@ -139,19 +142,29 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
         load_params<T, V>(p.gate, p.params_f32, (u / p.splits) * static_cast<uint64_t>(p.hidden) + c * V, k);
         load_params<T, V>(p.weight, p.params_f32, c * V, w);
       }
+      float dw[V], dg[V];
 #pragma unroll
       for (int j = 0; j < V; j++) {
-        const float b = fb[i * V + j], dw = wide ? b * k[j] : b;
-        float* sum = mine + c * V + j;
-        *sum = u == blockIdx.x ? dw : *sum + dw;  // the CTA's first unit has its number
-        if (!wide) continue;
-        const uint64_t at = static_cast<uint64_t>(u) * p.hidden + c * V + j;
-        if (p.splits > 1)
-          gate_parts[at] = b * w[j];
-        else if (p.params_f32)
-          static_cast<float*>(p.dgate)[at] = b * w[j];
-        else
-          static_cast<T*>(p.dgate)[at] = from_f32<T>(b * w[j]);
+        dw[j] = wide ? fb[i * V + j] * k[j] : fb[i * V + j];
+        dg[j] = wide ? fb[i * V + j] * w[j] : 0.f;
+      }
+      if (u != blockIdx.x) {  // the CTA's first unit has its number
+        float sum[V];
+        load_f32<V>(mine + c * V, sum);
+#pragma unroll
+        for (int j = 0; j < V; j++) dw[j] += sum[j];
+      }
+      store_f32<V>(mine + c * V, dw);
+      if (!wide) continue;
+      const uint64_t at = static_cast<uint64_t>(u) * p.hidden + c * V;
+      if (p.splits > 1) {
+        store_f32<V>(gate_parts + at, dg);
+      } else if (p.params_f32) {
+#pragma unroll
+        for (int j = 0; j < V; j++) static_cast<float*>(p.dgate)[at + j] = dg[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; j++) static_cast<T*>(p.dgate)[at + j] = from_f32<T>(dg[j]);
       }
     }
   };
@@ -185,14 +198,21 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
   // Between barriers: `t` is the row whose first sums are known; v (in g), y and the scalars of the row before wait for
   // their last sum.
   float2 g[P];
-  Piece<T, V> y_row[Ring::NV];
+  // With few columns a thread holds the row's y and refills the stage at once; with many the registers do not allow
+  // it, y is read again from its stage, and that is refilled after it.
+  constexpr bool kHold = C <= kBwdCols;
+  Piece<T, V> y_row[kHold ? Ring::NV : 1];
+  int y_stage = 0;
   uint64_t before = ~0ull;
   float root = 0.f, one = 1.f;
   float sums[4] = {0.f, 0.f, 0.f, 0.f};
   auto finish = [&](float vy) {  // dy of the row before
     const float2 m = splat(-(vy * root * inv_d) * root), rr = splat(root * one);
     float2 v[P];
-    Ring::unpack(y_row, v);
+    if constexpr (kHold)
+      Ring::unpack(y_row, v);
+    else
+      ring.get(y_stage, kY, row_of(p.y, before, p.y_stride), v);
 #pragma unroll
     for (int i = 0; i < P; i++) v[i] = mul2(rr, fma2(v[i], m, g[i]));
     ring.put(ring.start(static_cast<T*>(p.dy), before, p.hidden), v);
@@ -214,7 +234,10 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
   block_sum_shared<4>(sums, red[1]);
   while (now.valid(p)) {
     const uint64_t t = now.t;
-    if (BRANCH && before != ~0ull) finish(sums[3]);
+    if (BRANCH && before != ~0ull) {
+      finish(sums[3]);
+      if (!kHold) issue(y_stage);
+    }
     if (!Ring::kWords || past) {
       ring.get(stage, kGx, row_of(p.dx_new, t, p.dx_new_stride), g);
     } else {
@@ -246,8 +269,13 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
       one = narrow ? load_param<T>(p.gate, p.params_f32, t / p.gate_tokens) : 1.f;
       const float2 rr = splat(root * one);
       float2 v[P], vy = splat(0.f);
-      ring.get(stage, kY, row_of(p.y, t, p.y_stride), y_row);
-      Ring::unpack(y_row, v);
+      if constexpr (kHold) {
+        ring.get(stage, kY, row_of(p.y, t, p.y_stride), y_row);
+        Ring::unpack(y_row, v);
+      } else {
+        ring.get(stage, kY, row_of(p.y, t, p.y_stride), v);
+        y_stage = stage;
+      }
 #pragma unroll
       for (int i = 0; i < P; i++) {
         sum_b[i] = fma2(g[i], mul2(v[i], rr), sum_b[i]);
@@ -257,7 +285,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
       sums[3] = vy.x + vy.y;
     }
     const int done = stage;
-    if (!Ring::kWords) issue(done);
+    if (!Ring::kWords && (kHold || !BRANCH)) issue(done);
     before = t;
     const uint32_t unit = now.u;
     if (now.next(p) && BRANCH) {
@@ -268,7 +296,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
     sums[0] = sums[1] = sums[2] = 0.f;
     if (now.valid(p)) {
       // the next row: all but the copies issued after its own
-      cp_async_wait<Ring::kWords ? kBwdStages - 2 : kBwdStages - 1>();
+      cp_async_wait<Ring::kWords || (!kHold && BRANCH) ? kBwdStages - 2 : kBwdStages - 1>();
       if (Ring::kWords) __syncthreads();
       first_sums(stage, now.t, sums);
     }
@@ -281,23 +309,201 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
   if (NEXT) {
     const float* fn = reinterpret_cast<const float*>(sum_n);
 #pragma unroll
-    for (int i = 0; i < Ring::NV; i++)
+    for (int i = 0; i < Ring::NV; i++) {
+      const uint32_t c = threadIdx.x + i * blockDim.x;
+      float dn[V];
 #pragma unroll
-      for (int j = 0; j < V; j++) {
-        const uint32_t col = (threadIdx.x + i * blockDim.x) * V + j;
-        if (col < p.hidden) mine[p.hidden + col] = fn[i * V + j];
-      }
+      for (int j = 0; j < V; j++) dn[j] = fn[i * V + j];
+      if (c < ring.pieces) store_f32<V>(mine + p.hidden + c * V, dn);
+    }
   }
 }
 
-template <typename T, int V, int NV, bool WARP, bool BRANCH, bool NEXT, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormBwdParams p) {
-  __shared__ float red[2][3 * 32];
-  __shared__ float cols[WARP ? kNormWarpWidth : 1];
+// The warp shape: every warp walks rows of its own, the next one's loads under way while it computes; a CTA adds its
+// warps' sums of the weights' gradients at the end.
+template <typename T, int V, bool BRANCH, bool NEXT>
+__global__ void __launch_bounds__(kNormWarps * 32, 2) norm_bwd_warp_kernel(NormBwdParams p) {
+  constexpr int C = 8, P = C / 2;
+  using Cols = RowRing<T, V, C, 1, 1>;
+  __shared__ float tile[kNormWarps][kNormWarpWidth];
   pdl_begin();
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
-  const uint32_t me = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
-  const uint32_t pieces = p.hidden / V;
+  const Cols cols{nullptr, lane, 32, p.hidden / V};
+  const float inv_d = 1.f / static_cast<float>(p.hidden);
+  const bool wide = BRANCH && p.gate && p.gate_wide, narrow = BRANCH && p.gate && !p.gate_wide;
+  float* gate_parts = p.parts + static_cast<uint64_t>(p.ctas) * 2 * p.hidden;
+  float2 w2[P], gw[P], sum_n[P], sum_w[P], sum_b[P];  // as in the ring shape; sum_w over the units
+#pragma unroll
+  for (int i = 0; i < P; i++) w2[i] = gw[i] = sum_n[i] = sum_w[i] = sum_b[i] = splat(0.f);
+  if (NEXT) cols.params(p.next_weight, p.params_f32, 0, w2);
+  auto gate_of = [&](uint32_t u, float2(&k)[P]) {
+    cols.params(p.gate, p.params_f32, (u / p.splits) * static_cast<uint64_t>(p.hidden), k);
+  };
+  auto open_unit = [&](uint32_t u) {
+    cols.params(p.weight, p.params_f32, 0, gw);
+    if (!wide) return;
+    float2 k[P];
+    gate_of(u, k);
+#pragma unroll
+    for (int i = 0; i < P; i++) gw[i] = mul2(gw[i], k[i]);
+  };
+  auto close_unit = [&](uint32_t u) {
+    float2 dg[P];
+    if (wide) {
+      gate_of(u, dg);
+#pragma unroll
+      for (int i = 0; i < P; i++) sum_w[i] = fma2(sum_b[i], dg[i], sum_w[i]);
+      cols.params(p.weight, p.params_f32, 0, dg);
+    }
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+      if (wide)
+        dg[i] = mul2(sum_b[i], dg[i]);
+      else
+        sum_w[i] = fma2(sum_b[i], splat(1.f), sum_w[i]);
+      sum_b[i] = splat(0.f);
+    }
+    if (!wide) return;
+    const float* f = reinterpret_cast<const float*>(dg);
+#pragma unroll
+    for (int i = 0; i < Cols::NV; i++) {
+      const uint32_t c = lane + i * 32;
+      if (c >= cols.pieces) continue;
+      const uint64_t at = static_cast<uint64_t>(u) * p.hidden + c * V;
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        if (p.splits > 1)
+          gate_parts[at + j] = f[i * V + j];
+        else if (p.params_f32)
+          static_cast<float*>(p.dgate)[at + j] = f[i * V + j];
+        else
+          static_cast<T*>(p.dgate)[at + j] = from_f32<T>(f[i * V + j]);
+      }
+    }
+  };
+  struct Row {
+    Piece<T, V> gx[Cols::NV], gh[Cols::NV], x[Cols::NV], y[Cols::NV];
+  };
+  auto load = [&](Row& r, uint64_t t) {
+    if (NEXT) {
+      cols.load(static_cast<const T*>(p.dh) + t * p.dh_stride, r.gh);
+      cols.load(static_cast<const T*>(p.x_new) + t * p.x_new_stride, r.x);
+    }
+    if (BRANCH) cols.load(static_cast<const T*>(p.y) + t * p.y_stride, r.y);
+    if (p.dx_new) {
+      cols.load(static_cast<const T*>(p.dx_new) + t * p.dx_new_stride, r.gx);
+    } else {
+#pragma unroll
+      for (int i = 0; i < Cols::NV; i++) r.gx[i] = Piece<T, V>::zero();
+    }
+  };
+  BwdWalk now{blockIdx.x * kNormWarps + warp, 0, 0};
+  Row row, next;
+  if (now.valid(p)) {
+    now.open(p);
+    if (BRANCH) open_unit(now.u);
+    load(row, now.t);
+  }
+  while (now.valid(p)) {
+    const uint64_t t = now.t;
+    const uint32_t unit = now.u;
+    const bool ended = now.next(p);
+    if (now.valid(p)) load(next, now.t);
+    float2 g[P], h[P], x[P], y[P];
+    float sums[3] = {0.f, 0.f, 0.f};
+    Cols::unpack(row.gx, g);
+    if (NEXT) {
+      float2 xx = splat(0.f), ux = splat(0.f);
+      Cols::unpack(row.gh, h);
+      Cols::unpack(row.x, x);
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        xx = fma2(x[i], x[i], xx);
+        ux = fma2(mul2(h[i], w2[i]), x[i], ux);
+      }
+      sums[0] = warp_sum_f32(xx.x + xx.y);
+      sums[1] = warp_sum_f32(ux.x + ux.y);
+    }
+    if (BRANCH) {
+      float2 yy = splat(0.f);
+      Cols::unpack(row.y, y);
+#pragma unroll
+      for (int i = 0; i < P; i++) yy = fma2(y[i], y[i], yy);
+      sums[2] = warp_sum_f32(yy.x + yy.y);
+    }
+    if (NEXT) {
+      const float r2 = rsqrtf(sums[0] * inv_d + p.eps);
+      const float2 rr = splat(r2), m = splat(-(sums[1] * r2 * inv_d) * r2 * r2);  // -r2^2 mean(u n2)
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        g[i] = fma2(rr, mul2(h[i], w2[i]), fma2(x[i], m, g[i]));
+        sum_n[i] = fma2(h[i], mul2(x[i], rr), sum_n[i]);
+      }
+    }
+    float2 o[P];
+    const float2 a = splat(p.residual_scale);
+#pragma unroll
+    for (int i = 0; i < P; i++) o[i] = mul2(a, g[i]);
+    cols.put(cols.start(static_cast<T*>(p.dx), t, p.hidden), o);
+    if (BRANCH) {
+      const float root = rsqrtf(sums[2] * inv_d + p.eps);
+      const float one = narrow ? load_param<T>(p.gate, p.params_f32, t / p.gate_tokens) : 1.f;
+      const float2 rr = splat(root * one);
+      float2 vy = splat(0.f);
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        sum_b[i] = fma2(g[i], mul2(y[i], rr), sum_b[i]);
+        g[i] = mul2(g[i], gw[i]);  // v, but for a one-column gate
+        vy = fma2(g[i], y[i], vy);
+      }
+      const float dot = warp_sum_f32(vy.x + vy.y);
+      const float2 m = splat(-(dot * root * inv_d) * root);
+#pragma unroll
+      for (int i = 0; i < P; i++) g[i] = mul2(rr, fma2(y[i], m, g[i]));
+      cols.put(cols.start(static_cast<T*>(p.dy), t, p.hidden), g);
+      if (narrow && lane == 0) {
+        const float dg = root * dot;  // sum of G n w
+        if (p.gate_tokens > 1)
+          gate_parts[t] = dg;
+        else if (p.params_f32)
+          static_cast<float*>(p.dgate)[t] = dg;
+        else
+          static_cast<T*>(p.dgate)[t] = from_f32<T>(dg);
+      }
+    }
+    if (ended && BRANCH) {
+      close_unit(unit);
+      if (now.valid(p)) open_unit(now.u);
+    }
+    row = next;
+  }
+  float* mine = p.parts + static_cast<uint64_t>(blockIdx.x) * 2 * p.hidden;
+  auto flush = [&](const float2(&s)[P], float* dst) {
+    const float* f = reinterpret_cast<const float*>(s);
+#pragma unroll
+    for (int i = 0; i < Cols::NV; i++)
+#pragma unroll
+      for (int j = 0; j < V; j++)
+        if (lane + i * 32 < cols.pieces) tile[warp][(lane + i * 32) * V + j] = f[i * V + j];
+    __syncthreads();
+    if (threadIdx.x < p.hidden) {
+      float sum = 0.f;
+#pragma unroll
+      for (int q = 0; q < kNormWarps; q++) sum += tile[q][threadIdx.x];
+      dst[threadIdx.x] = sum;
+    }
+    __syncthreads();
+  };
+  if (BRANCH) flush(sum_w, mine);
+  if (NEXT) flush(sum_n, mine + p.hidden);
+}
+
+// Rows wider than the ring holds: a CTA keeps one in registers at a time.
+template <typename T, int V, int NV, bool BRANCH, bool NEXT, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormBwdParams p) {
+  __shared__ float red[2][3 * 32];
+  pdl_begin();
+  const uint32_t me = threadIdx.x, step = blockDim.x, pieces = p.hidden / V;
   const float inv_d = 1.f / static_cast<float>(p.hidden);
   const bool wide = p.gate && p.gate_wide;
   float* gate_parts = p.parts + static_cast<uint64_t>(p.ctas) * 2 * p.hidden;  // one row per unit, or one value per token
@@ -308,50 +514,25 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormBwdParams p) {
 #pragma unroll
     for (int j = 0; j < V; j++) sum_w[i][j] = sum_n[i][j] = sum_g[i][j] = 0.f;
 
-  // The CTA's sum of one column array to dst[0 .. hidden), fp32 or, `last`, a
-  // finished gradient row in the parameters' type.  In the warp shape the
-  // warps add theirs in turn.
+  // This thread's columns of a sum to dst: fp32 or, `last`, a finished gradient row in the parameters' type.
   auto flush = [&](float (&s)[NV][V], void* dst, bool last) {
-    if (WARP) {
-      for (uint32_t w = 0; w < kNormWarps; w++) {
-        if (warp == w) {
 #pragma unroll
-          for (int i = 0; i < NV; i++)
+    for (int i = 0; i < NV; i++)
 #pragma unroll
-            for (int j = 0; j < V; j++) {
-              const uint32_t col = (me + i * step) * V + j;
-              if (col < p.hidden) cols[col] = (w ? cols[col] : 0.f) + s[i][j];
-            }
-        }
-        __syncthreads();
-      }
-      for (uint32_t col = threadIdx.x; col < p.hidden; col += kNormWarps * 32) {
+      for (int j = 0; j < V; j++) {
+        const uint32_t col = (me + i * step) * V + j;
+        if (col >= p.hidden) continue;
         if (last && !p.params_f32)
-          static_cast<T*>(dst)[col] = from_f32<T>(cols[col]);
+          static_cast<T*>(dst)[col] = from_f32<T>(s[i][j]);
         else
-          static_cast<float*>(dst)[col] = cols[col];
+          static_cast<float*>(dst)[col] = s[i][j];
       }
-      __syncthreads();
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; i++)
-#pragma unroll
-        for (int j = 0; j < V; j++) {
-          const uint32_t col = (me + i * step) * V + j;
-          if (col >= p.hidden) continue;
-          if (last && !p.params_f32)
-            static_cast<T*>(dst)[col] = from_f32<T>(s[i][j]);
-          else
-            static_cast<float*>(dst)[col] = s[i][j];
-        }
-    }
   };
 
   for (uint32_t u = blockIdx.x; u < p.units; u += p.ctas) {
     const uint64_t group = u / p.splits, split = u - static_cast<uint32_t>(group) * p.splits;
     const uint64_t size = wide ? p.gate_tokens : p.tokens;
-    const uint64_t first = group * size + size * split / p.splits, last = group * size + size * (split + 1) / p.splits;
-    for (uint64_t t = first + (WARP ? warp : 0); t < last; t += WARP ? kNormWarps : 1) {
+    for (uint64_t t = group * size + split; t < (group + 1) * size; t += p.splits) {
       Piece<T, V> gx[NV], gh[NV], y[NV], x[NV];
 #pragma unroll
       for (int i = 0; i < NV; i++) {
@@ -391,13 +572,8 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormBwdParams p) {
           for (int j = 0; j < V; j++) s[2] = fmaf(f[j], f[j], s[2]);
         }
       }
-      if (WARP) {
-#pragma unroll
-        for (int i = 0; i < 3; i++) s[i] = warp_sum_f32(s[i]);
-      } else {
-        block_sum_f32<3>(s, red[turn]);
-        turn ^= 1;
-      }
+      block_sum_f32<3>(s, red[turn]);
+      turn ^= 1;
       const float r2 = rsqrtf(s[0] * inv_d + p.eps), mean2 = s[1] * r2 * inv_d;  // mean(u n2)
       const float r = rsqrtf(s[2] * inv_d + p.eps);
       const uint64_t gate_row = p.gate ? t / p.gate_tokens : 0;
@@ -453,13 +629,8 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormBwdParams p) {
         }
       }
       if (BRANCH) {
-        if (WARP) {
-          dots[0] = warp_sum_f32(dots[0]);
-          dots[1] = warp_sum_f32(dots[1]);
-        } else {
-          block_sum_f32<2>(dots, red[turn]);
-          turn ^= 1;
-        }
+        block_sum_f32<2>(dots, red[turn]);
+        turn ^= 1;
         const float mean = dots[0] * inv_d;
         if (p.gate && !wide && me == 0) {
           if (p.gate_tokens > 1)
@@ -499,12 +670,12 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormBwdParams p) {
   if (NEXT) flush(sum_n, mine + p.hidden, false);
 }
 
-// Adds the CTAs' sums, in order: 8 threads per column take an eighth of the
-// parts each and thread 0 of the 8 adds theirs.  blockIdx.y: 0 the branch
-// weight's gradient, 1 the next weight's, 2 + g gate row g's.
+// Adds the CTAs' sums, in order: 32 warps take a share of the parts each, a lane a column, and then adds a column's shares.
+// blockIdx.y: 0 the branch weight's gradient, 1 the next weight's, 2 + g gate row g's.
+constexpr uint32_t kPartWarps = 32;
 template <typename T>
-__global__ void __launch_bounds__(256) norm_parts_kernel(NormBwdParams p) {
-  __shared__ float sums[8][32];
+__global__ void __launch_bounds__(kPartWarps * 32) norm_parts_kernel(NormBwdParams p) {
+  __shared__ float sums[kPartWarps][33];
   pdl_begin();
   const uint32_t lane = lane_id(), slice = threadIdx.x >> 5, job = blockIdx.y;
   const uint32_t col = blockIdx.x * 32 + lane;
@@ -525,20 +696,21 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(NormBwdParams p) {
   }
   if (!dst) return;
   float s = 0.f;
-  const uint32_t first = count * slice / 8, last = count * (slice + 1) / 8;
+  const uint32_t first = count * slice / kPartWarps, last = count * (slice + 1) / kPartWarps;
   if (col < p.hidden) {
 #pragma unroll 8
     for (uint32_t i = first; i < last; i++) s += src[i * stride + col];
   }
   sums[slice][lane] = s;
   __syncthreads();
-  if (slice || col >= p.hidden) return;
-#pragma unroll
-  for (int i = 1; i < 8; i++) s += sums[i][lane];
+  // warp w adds the 32 shares of column w
+  s = warp_sum_f32(sums[lane][slice]);
+  const uint32_t mine = blockIdx.x * 32 + slice;
+  if (lane || mine >= p.hidden) return;
   if (p.params_f32)
-    static_cast<float*>(dst)[col] = s;
+    static_cast<float*>(dst)[mine] = s;
   else
-    static_cast<T*>(dst)[col] = from_f32<T>(s);
+    static_cast<T*>(dst)[mine] = from_f32<T>(s);
 }
 
 // A one-column gate's gradient where several tokens share a gate value: one
@@ -559,52 +731,47 @@ __global__ void __launch_bounds__(256) norm_narrow_gate_kernel(NormBwdParams p) 
     static_cast<T*>(p.dgate)[blockIdx.x] = from_f32<T>(s[0]);
 }
 
-// Cuts the rows into ranges for at most `most` CTAs (a range lies in one gate row's tokens; `per_turn` rows are
-// the least worth one), launches `fn` and adds up what it left.
+// Cuts the rows into ranges for at most `most` walkers, `per_cta` of them in a CTA (a range lies in one gate row's
+// tokens), launches `fn` and adds up what it left.
 template <typename T>
-cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint32_t per_turn, int threads, int smem,
+cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint32_t per_cta, int threads, int smem,
                           cudaStream_t stream) {
   const bool wide = p.gate && p.gate_wide;
-  if (most > norm_max_ctas(p.hidden)) most = norm_max_ctas(p.hidden);
+  if (most > norm_max_units(p.hidden)) most = norm_max_units(p.hidden);
   const uint64_t groups = wide ? p.gate_rows : 1, size = wide ? p.gate_tokens : p.tokens;
-  const uint64_t turns = (size + per_turn - 1) / per_turn;
   uint64_t splits = groups >= most ? 1 : most / groups;
-  if (splits > turns) splits = turns;  // no tokens: no ranges, and the sums over none of them are zero
+  if (splits > size) splits = size;  // no tokens: no ranges, and the sums over none of them are zero
   p.splits = static_cast<uint32_t>(splits);
   const uint64_t units = groups * splits;
   if (units > 0xFFFFFFFFull) return cudaErrorInvalidConfiguration;
   p.units = static_cast<uint32_t>(units);
-  p.ctas = static_cast<uint32_t>(units < most ? units : most);
+  p.walkers = static_cast<uint32_t>(units < most ? units : most);
+  p.ctas = (p.walkers + per_cta - 1) / per_cta;
+  p.walkers = p.ctas * per_cta;
   void* args[] = {&p};
   cudaError_t e = cudaSuccess;
   if (p.ctas) e = launch_kernel(fn, dim3(p.ctas), dim3(threads), smem, stream, args, false);
   if (e != cudaSuccess) return e;
   const uint32_t jobs = 2 + (wide && splits != 1 ? static_cast<uint32_t>(groups) : 0u);
-  e = launch_kernel(reinterpret_cast<const void*>(norm_parts_kernel<T>), dim3((p.hidden + 31) / 32, jobs), dim3(256), 0,
-                    stream, args, false);
+  e = launch_kernel(reinterpret_cast<const void*>(norm_parts_kernel<T>), dim3((p.hidden + 31) / 32, jobs),
+                    dim3(kPartWarps * 32), 0, stream, args, false);
   if (e != cudaSuccess || !p.gate || wide || p.gate_tokens == 1) return e;
   return launch_kernel(reinterpret_cast<const void*>(norm_narrow_gate_kernel<T>),
                        dim3(static_cast<unsigned>(p.gate_rows)), dim3(256), 0, stream, args, false);
 }
 
-template <typename T, int V, int NV, bool WARP, int THREADS>
-cudaError_t run_shape(NormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
-  const void* fn = nullptr;
-  if (p.y && p.next_weight)
-    fn = reinterpret_cast<const void*>(norm_bwd_kernel<T, V, NV, WARP, true, true, THREADS>);
-  else if (p.y)
-    fn = reinterpret_cast<const void*>(norm_bwd_kernel<T, V, NV, WARP, true, false, THREADS>);
-  else
-    fn = reinterpret_cast<const void*>(norm_bwd_kernel<T, V, NV, WARP, false, true, THREADS>);
-  return launch_ranges<T>(p, fn, 2ull * static_cast<uint64_t>(dev.sm_count), WARP ? kNormWarps : 1, threads, 0, stream);
-}
+// fn<BRANCH, NEXT> of a kernel template by what the call has.
+#define ZC_NORM_MODE(KERNEL, ...)                                                                       \
+  (p.y && p.next_weight ? reinterpret_cast<const void*>(KERNEL<__VA_ARGS__, true, true>)                \
+   : p.y                ? reinterpret_cast<const void*>(KERNEL<__VA_ARGS__, true, false>)               \
+                        : reinterpret_cast<const void*>(KERNEL<__VA_ARGS__, false, true>))
 
-template <typename T, int V, bool BRANCH, bool NEXT>
+template <typename T, int V, int C, bool BRANCH, bool NEXT>
 cudaError_t run_ring(NormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
   static RingPrep prep;
   constexpr int kArrays = BRANCH && NEXT ? 4 : NEXT ? 3 : 2;
-  const int smem = static_cast<int>(RowRing<T, V, kBwdCols, kArrays, kBwdStages>::bytes(threads));
-  const void* fn = reinterpret_cast<const void*>(norm_bwd_ring_kernel<T, V, BRANCH, NEXT>);
+  const int smem = static_cast<int>(RowRing<T, V, C, kArrays, kBwdStages>::bytes(threads));
+  const void* fn = reinterpret_cast<const void*>(norm_bwd_ring_kernel<T, V, C, BRANCH, NEXT>);
   int per_sm = 0;
   cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, &per_sm);
   if (e != cudaSuccess) return e;
@@ -612,22 +779,39 @@ cudaError_t run_ring(NormBwdParams& p, int threads, cudaStream_t stream, const D
                           stream);
 }
 
+template <typename T, int V, int C>
+cudaError_t run_ring(NormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
+  if (p.y && p.next_weight) return run_ring<T, V, C, true, true>(p, threads, stream, dev);
+  if (p.y) return run_ring<T, V, C, true, false>(p, threads, stream, dev);
+  return run_ring<T, V, C, false, true>(p, threads, stream, dev);
+}
+
 template <typename T, int V>
 cudaError_t run_width(NormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   const uint32_t d = p.hidden;
-  if (d <= kNormWarpWidth) {
-    if (V > 1 && d <= 256) return run_shape<T, V, V == 1 ? 16 : 8 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
-    return run_shape<T, V, 16 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
+  const uint64_t sms = static_cast<uint64_t>(dev.sm_count);
+  if (d <= kNormWarpWidth)
+    return launch_ranges<T>(p, ZC_NORM_MODE(norm_bwd_warp_kernel, T, V), 4 * kNormWarps * sms, kNormWarps,
+                            kNormWarps * 32, 0, stream);
+  auto threads = [&](int cols) { return static_cast<int>((d + cols * 32 - 1) / (cols * 32) * 32); };
+  if (threads(kBwdCols) <= kNormRingThreads &&
+      RowRing<T, V, kBwdCols, 4, kBwdStages>::bytes(threads(kBwdCols)) <= kNormRingSmem)
+    return run_ring<T, V, kBwdCols>(p, threads(kBwdCols), stream, dev);
+  if constexpr (sizeof(T) == 2 && V > 1) {
+    if (threads(kBwdWideCols) <= kNormRingThreads &&
+        RowRing<T, V, kBwdWideCols, 4, kBwdStages>::bytes(threads(kBwdWideCols)) <= kNormRingSmem)
+      return run_ring<T, V, kBwdWideCols>(p, threads(kBwdWideCols), stream, dev);
   }
-  constexpr uint32_t kCols = kBwdCols;
-  const int threads = static_cast<int>((d + kCols * 32 - 1) / (kCols * 32) * 32);
-  if (threads <= kNormRingThreads && RowRing<T, V, kCols, 4, kBwdStages>::bytes(threads) <= kNormRingSmem) {
-    if (p.y && p.next_weight) return run_ring<T, V, true, true>(p, threads, stream, dev);
-    if (p.y) return run_ring<T, V, true, false>(p, threads, stream, dev);
-    return run_ring<T, V, false, true>(p, threads, stream, dev);
-  }
-  return run_shape<T, V, 16 / V, false, 1024>(p, static_cast<int>((d + 511) / 512 * 32), stream, dev);
+  if (p.y && p.next_weight)
+    return launch_ranges<T>(p, reinterpret_cast<const void*>(norm_bwd_kernel<T, V, 16 / V, true, true, 1024>), 2 * sms, 1,
+                            threads(16), 0, stream);
+  if (p.y)
+    return launch_ranges<T>(p, reinterpret_cast<const void*>(norm_bwd_kernel<T, V, 16 / V, true, false, 1024>), 2 * sms, 1,
+                            threads(16), 0, stream);
+  return launch_ranges<T>(p, reinterpret_cast<const void*>(norm_bwd_kernel<T, V, 16 / V, false, true, 1024>), 2 * sms, 1,
+                          threads(16), 0, stream);
 }
+#undef ZC_NORM_MODE
 
 template <typename T>
 cudaError_t run_typed(NormBwdParams& p, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
@@ -653,8 +837,9 @@ cudaError_t prepare_ring(RingPrep& rp, const void* fn, int threads, int smem_byt
 }
 
 uint64_t norm_workspace_bytes(uint64_t tokens, uint32_t hidden) {
-  const uint64_t ctas = tokens < norm_max_ctas(hidden) ? tokens : norm_max_ctas(hidden);
-  return 4 * (3 * ctas * hidden + tokens);
+  // two sums a CTA, and one a range or a value a token for the gate
+  const uint64_t units = tokens < norm_max_units(hidden) ? tokens : norm_max_units(hidden);
+  return 4 * (3 * units * hidden + tokens);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdParams& params, int dtype, bool vec, cudaStream_t stream,
