@@ -13,8 +13,6 @@ namespace zc {
 
 namespace {
 
-constexpr uint32_t kNormWarpWidth = 512;  // widest row that a warp holds
-
 template <typename T, int V, int NV, bool WARP, bool BRANCH, bool NEXT, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_kernel(NormParams p) {
   __shared__ float red[2][32];
@@ -107,13 +105,16 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(NormParams p) {
   }
 }
 
-constexpr int kFwdStages = 4, kFwdCols = 8;
+// Columns of a thread and stages of the ring: 8 columns, and 16 for rows that 8 of each of 512 threads do not hold.
+constexpr int kFwdCols = 8, kFwdWideCols = 16;
+template <int C>
+constexpr int kFwdStages = C == kFwdCols ? 4 : 3;
 
 // The ring shape: rows blockIdx.x, blockIdx.x + CTAs, ... stream through shared memory.
-template <typename T, int V, bool BRANCH, bool NEXT>
-__global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormParams p) {
-  constexpr int P = kFwdCols / 2;
-  using Ring = RowRing<T, V, kFwdCols, BRANCH ? 2 : 1, kFwdStages>;
+template <typename T, int V, int C, bool BRANCH, bool NEXT>
+__global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_ring_kernel(NormParams p) {
+  constexpr int P = C / 2, kStages = kFwdStages<C>;
+  using Ring = RowRing<T, V, C, BRANCH ? 2 : 1, kStages>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ __align__(16) float red[2][128];
   pdl_allow_dependents();
@@ -135,14 +136,14 @@ __global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormPara
     cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < kFwdStages; s++) issue(s);
+  for (int s = 0; s < kStages; s++) issue(s);
   float2 w[P], w2[P], k[P];
   if (BRANCH) ring.params(p.weight, p.params_f32, 0, w);
   if (NEXT) ring.params(p.next_weight, p.params_f32, 0, w2);
 #pragma unroll
   for (int i = 0; i < P; i++) k[i] = splat(1.f);
   uint64_t gate_row = ~0ull;  // the gate row that k holds
-  cp_async_wait<kFwdStages - 1>();
+  cp_async_wait<kStages - 1>();
   __syncthreads();
   int stage = 0, turn = 0;
   for (uint64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormPara
       for (int i = 0; i < P; i++) yy = fma2(y[i], y[i], yy);
       sums[0] = yy.x + yy.y;
       sums[1] = 0.f;
-      cp_async_wait<kFwdStages - 2>();  // the next row, which the barrier below shows to all
+      cp_async_wait<kStages - 2>();  // the next row, which the barrier below shows to all
       block_sum_shared<2>(sums, red[turn]);
       turn ^= 1;
       issue(stage);
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormPara
       for (int i = 0; i < P; i++) xx = fma2(x[i], x[i], xx);
       sums[0] = xx.x + xx.y;
       sums[1] = 0.f;
-      if (!BRANCH) cp_async_wait<kFwdStages - 2>();
+      if (!BRANCH) cp_async_wait<kStages - 2>();
       block_sum_shared<2>(sums, red[turn]);
       turn ^= 1;
       if (!BRANCH) issue(stage);
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 2) norm_ring_kernel(NormPara
       for (int i = 0; i < P; i++) x[i] = mul2(mul2(x[i], r), w2[i]);
       ring.put(ring.start(static_cast<T*>(p.h), t, p.hidden), x);
     }
-    stage = stage + 1 == kFwdStages ? 0 : stage + 1;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   cp_async_wait<0>();
 }
@@ -210,11 +211,11 @@ cudaError_t run_shape(NormParams& p, int threads, cudaStream_t stream, const Dev
                        false);
 }
 
-template <typename T, int V, bool BRANCH, bool NEXT>
+template <typename T, int V, int C, bool BRANCH, bool NEXT>
 cudaError_t run_ring(NormParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
   static RingPrep prep;
-  const int smem = static_cast<int>(RowRing<T, V, kFwdCols, BRANCH ? 2 : 1, kFwdStages>::bytes(threads));
-  const void* fn = reinterpret_cast<const void*>(norm_ring_kernel<T, V, BRANCH, NEXT>);
+  const int smem = static_cast<int>(RowRing<T, V, C, BRANCH ? 2 : 1, kFwdStages<C>>::bytes(threads));
+  const void* fn = reinterpret_cast<const void*>(norm_ring_kernel<T, V, C, BRANCH, NEXT>);
   int per_sm = 0;
   cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, &per_sm);
   if (e != cudaSuccess) return e;
@@ -224,18 +225,38 @@ cudaError_t run_ring(NormParams& p, int threads, cudaStream_t stream, const Devi
                        args, false);
 }
 
+// Runs the ring with C columns a thread if it holds such rows.
+template <typename T, int V, int C>
+bool run_ring(NormParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e) {
+  const int threads = static_cast<int>((p.hidden + C * 32 - 1) / (C * 32) * 32);
+  if (threads > kNormRingThreads || RowRing<T, V, C, 2, kFwdStages<C>>::bytes(threads) > kNormRingSmem) return false;
+  if (p.y && p.next_weight)
+    *e = run_ring<T, V, C, true, true>(p, threads, stream, dev);
+  else if (p.y)
+    *e = run_ring<T, V, C, true, false>(p, threads, stream, dev);
+  else
+    *e = run_ring<T, V, C, false, true>(p, threads, stream, dev);
+  return true;
+}
+
 template <typename T, int V>
 cudaError_t run_width(NormParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   const uint32_t d = p.hidden;
-  if (d <= kNormWarpWidth) {
-    if (V > 1 && d <= 256) return run_shape<T, V, V == 1 ? 16 : 8 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
-    return run_shape<T, V, 16 / V, true, kNormWarps * 32>(p, kNormWarps * 32, stream, dev);
+  // A warp holds up to 512 values, in 16-byte pieces 1024 if the rows keep all SMs busy: then it beats the ring's four
+  // warps a row (65536 x 1024 bf16 93 us against 100), with few rows it is slower (8 x 1024 3.5 us against 2.2).
+  constexpr int kWarp = kNormWarps * 32;
+  if constexpr (V > 1) {
+    if (d <= 256) return run_shape<T, V, 8 / V, true, kWarp>(p, kWarp, stream, dev);
+    if (d <= 512) return run_shape<T, V, 16 / V, true, kWarp>(p, kWarp, stream, dev);
+    if (d <= 1024 && p.tokens >= 16ull * static_cast<uint64_t>(dev.sm_count))
+      return run_shape<T, V, 32 / V, true, kWarp>(p, kWarp, stream, dev);
+  } else if (d <= 512) {
+    return run_shape<T, V, 16, true, kWarp>(p, kWarp, stream, dev);
   }
-  const int threads = static_cast<int>((d + kFwdCols * 32 - 1) / (kFwdCols * 32) * 32);
-  if (threads <= kNormRingThreads && RowRing<T, V, kFwdCols, 2, kFwdStages>::bytes(threads) <= kNormRingSmem) {
-    if (p.y && p.next_weight) return run_ring<T, V, true, true>(p, threads, stream, dev);
-    if (p.y) return run_ring<T, V, true, false>(p, threads, stream, dev);
-    return run_ring<T, V, false, true>(p, threads, stream, dev);
+  cudaError_t e;
+  if (run_ring<T, V, kFwdCols>(p, stream, dev, &e)) return e;
+  if constexpr (V > 1) {
+    if (run_ring<T, V, kFwdWideCols>(p, stream, dev, &e)) return e;
   }
   return run_shape<T, V, 16 / V, false, 1024>(p, static_cast<int>((d + 511) / 512 * 32), stream, dev);
 }

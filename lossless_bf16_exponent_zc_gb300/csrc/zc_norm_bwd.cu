@@ -670,12 +670,11 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormBwdParams p) {
   if (NEXT) flush(sum_n, mine + p.hidden, false);
 }
 
-// Adds the CTAs' sums, in order: 32 warps take a share of the parts each, a lane a column, and then adds a column's shares.
-// blockIdx.y: 0 the branch weight's gradient, 1 the next weight's, 2 + g gate row g's.
-constexpr uint32_t kPartWarps = 32;
-template <typename T>
-__global__ void __launch_bounds__(kPartWarps * 32) norm_parts_kernel(NormBwdParams p) {
-  __shared__ float sums[kPartWarps][33];
+// Adds the CTAs' sums, in order: the warps take a share of the parts each, a lane a column, and then half a warp, or a
+// warp, adds a column's shares.  blockIdx.y: 0 the branch weight's gradient, 1 the next weight's, 2 + g gate row g's.
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) norm_parts_kernel(NormBwdParams p) {
+  __shared__ float sums[WARPS][33];
   pdl_begin();
   const uint32_t lane = lane_id(), slice = threadIdx.x >> 5, job = blockIdx.y;
   const uint32_t col = blockIdx.x * 32 + lane;
@@ -696,21 +695,23 @@ __global__ void __launch_bounds__(kPartWarps * 32) norm_parts_kernel(NormBwdPara
   }
   if (!dst) return;
   float s = 0.f;
-  const uint32_t first = count * slice / kPartWarps, last = count * (slice + 1) / kPartWarps;
+  const uint32_t first = count * slice / WARPS, last = count * (slice + 1) / WARPS;
   if (col < p.hidden) {
 #pragma unroll 8
     for (uint32_t i = first; i < last; i++) s += src[i * stride + col];
   }
   sums[slice][lane] = s;
   __syncthreads();
-  // warp w adds the 32 shares of column w
-  s = warp_sum_f32(sums[lane][slice]);
-  const uint32_t mine = blockIdx.x * 32 + slice;
-  if (lane || mine >= p.hidden) return;
+  constexpr uint32_t kEach = 32 / WARPS;  // columns of a warp
+  const uint32_t mine = slice * kEach + lane / WARPS;
+  s = sums[lane % WARPS][mine];
+#pragma unroll
+  for (int d = WARPS / 2; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+  if (lane % WARPS || blockIdx.x * 32 + mine >= p.hidden) return;
   if (p.params_f32)
-    static_cast<float*>(dst)[mine] = s;
+    static_cast<float*>(dst)[blockIdx.x * 32 + mine] = s;
   else
-    static_cast<T*>(dst)[mine] = from_f32<T>(s);
+    static_cast<T*>(dst)[blockIdx.x * 32 + mine] = from_f32<T>(s);
 }
 
 // A one-column gate's gradient where several tokens share a gate value: one
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(256) norm_narrow_gate_kernel(NormBwdParams p) 
 // tokens), launches `fn` and adds up what it left.
 template <typename T>
 cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint32_t per_cta, int threads, int smem,
-                          cudaStream_t stream) {
+                          cudaStream_t stream, const DeviceInfo& dev) {
   const bool wide = p.gate && p.gate_wide;
   if (most > norm_max_units(p.hidden)) most = norm_max_units(p.hidden);
   const uint64_t groups = wide ? p.gate_rows : 1, size = wide ? p.gate_tokens : p.tokens;
@@ -753,8 +754,13 @@ cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint3
   if (p.ctas) e = launch_kernel(fn, dim3(p.ctas), dim3(threads), smem, stream, args, false);
   if (e != cudaSuccess) return e;
   const uint32_t jobs = 2 + (wide && splits != 1 ? static_cast<uint32_t>(groups) : 0u);
-  e = launch_kernel(reinterpret_cast<const void*>(norm_parts_kernel<T>), dim3((p.hidden + 31) / 32, jobs),
-                    dim3(kPartWarps * 32), 0, stream, args, false);
+  // 32 warps a CTA while the GPU holds all such CTAs at once, two an SM (4452 x 704 fp32 18.1 us in all against 22.9
+  // with 16); beyond that 16, four an SM (512 x 4096 bf16 10.8 against 13.0).
+  const dim3 parts((p.hidden + 31) / 32, jobs);
+  if (static_cast<uint64_t>(parts.x) * parts.y <= 2ull * static_cast<uint64_t>(dev.sm_count))
+    e = launch_kernel(reinterpret_cast<const void*>(norm_parts_kernel<T, 32>), parts, dim3(1024), 0, stream, args, false);
+  else
+    e = launch_kernel(reinterpret_cast<const void*>(norm_parts_kernel<T, 16>), parts, dim3(512), 0, stream, args, false);
   if (e != cudaSuccess || !p.gate || wide || p.gate_tokens == 1) return e;
   return launch_kernel(reinterpret_cast<const void*>(norm_narrow_gate_kernel<T>),
                        dim3(static_cast<unsigned>(p.gate_rows)), dim3(256), 0, stream, args, false);
@@ -776,7 +782,7 @@ cudaError_t run_ring(NormBwdParams& p, int threads, cudaStream_t stream, const D
   cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, &per_sm);
   if (e != cudaSuccess) return e;
   return launch_ranges<T>(p, fn, static_cast<uint64_t>(per_sm) * static_cast<uint64_t>(dev.sm_count), 1, threads, smem,
-                          stream);
+                          stream, dev);
 }
 
 template <typename T, int V, int C>
@@ -792,7 +798,7 @@ cudaError_t run_width(NormBwdParams& p, cudaStream_t stream, const DeviceInfo& d
   const uint64_t sms = static_cast<uint64_t>(dev.sm_count);
   if (d <= kNormWarpWidth)
     return launch_ranges<T>(p, ZC_NORM_MODE(norm_bwd_warp_kernel, T, V), 4 * kNormWarps * sms, kNormWarps,
-                            kNormWarps * 32, 0, stream);
+                            kNormWarps * 32, 0, stream, dev);
   auto threads = [&](int cols) { return static_cast<int>((d + cols * 32 - 1) / (cols * 32) * 32); };
   if (threads(kBwdCols) <= kNormRingThreads &&
       RowRing<T, V, kBwdCols, 4, kBwdStages>::bytes(threads(kBwdCols)) <= kNormRingSmem)
@@ -804,12 +810,12 @@ cudaError_t run_width(NormBwdParams& p, cudaStream_t stream, const DeviceInfo& d
   }
   if (p.y && p.next_weight)
     return launch_ranges<T>(p, reinterpret_cast<const void*>(norm_bwd_kernel<T, V, 16 / V, true, true, 1024>), 2 * sms, 1,
-                            threads(16), 0, stream);
+                            threads(16), 0, stream, dev);
   if (p.y)
     return launch_ranges<T>(p, reinterpret_cast<const void*>(norm_bwd_kernel<T, V, 16 / V, true, false, 1024>), 2 * sms, 1,
-                            threads(16), 0, stream);
+                            threads(16), 0, stream, dev);
   return launch_ranges<T>(p, reinterpret_cast<const void*>(norm_bwd_kernel<T, V, 16 / V, false, true, 1024>), 2 * sms, 1,
-                          threads(16), 0, stream);
+                          threads(16), 0, stream, dev);
 }
 #undef ZC_NORM_MODE
 
