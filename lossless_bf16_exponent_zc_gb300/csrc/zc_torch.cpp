@@ -11,6 +11,7 @@
 // torch's own errors (out of memory) as torch raises them.
 #include <Python.h>
 
+#include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
@@ -430,6 +431,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   try {
+    // Outputs are new tensors outside autograd: their creation goes straight to the allocation.
+    at::AutoDispatchBelowADInplaceOrView plain;
     return F(args);
   } catch (const Raised&) {
     return nullptr;
