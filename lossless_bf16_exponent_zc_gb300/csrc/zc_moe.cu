@@ -6,8 +6,6 @@
 // Everything here is bound by memory: each value is read or written once and
 // takes a few operations.  No kernel uses atomics on global memory and every
 // sum has a fixed order, so the same inputs give the same bits.
-#include <type_traits>
-
 #include "zc_internal.h"
 #include "zc_layer.cuh"
 
@@ -17,6 +15,8 @@ namespace {
 
 // ------------------------------------------------------------------ routing
 constexpr int kRouteWarps = 4;  // tokens per CTA, one warp each
+
+__device__ __forceinline__ uint32_t lanes_below() { return (1u << lane_id()) - 1u; }
 
 // Order-preserving image of a score: larger score, larger key.  NaN is above
 // everything, as a sort has it, so that it shows in the weights; both zeros
@@ -74,90 +74,87 @@ __device__ __forceinline__ void load_row(const T* row, uint32_t width, float (&v
   }
 }
 
-// Sorts N values, largest first: Batcher's odd-even merge sort, unrolled.
-template <int N>
-__device__ __forceinline__ void sort_down(unsigned long long (&q)[N]) {
-#pragma unroll
-  for (int p = 1; p < N; p *= 2)
-#pragma unroll
-    for (int k = p; k >= 1; k /= 2)
-#pragma unroll
-      for (int j = k % p; j + k < N; j += 2 * k)
-#pragma unroll
-        for (int i = 0; i < k; i++)
-          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
-            const unsigned long long a = q[i + j], b = q[i + j + k];
-            q[i + j] = a > b ? a : b;
-            q[i + j + k] = a > b ? b : a;
-          }
-}
-
-// One warp per token, every lane holding N experts next to one another: K
-// times the largest of the lanes' best is taken (on ties the lowest lane's, which
-// is the lowest expert's) and its lane goes on to its next.  A lane
-// sorts up to 8 experts once and then shifts them (256 experts, 8 taken: 600
-// instructions a token; looking for its best again each time, 1040); more than 8 it searches again.  Pick k ends in
-// lane k, which then reads its logit again (an L1 hit) for the weight.  Bound by those
-// instructions: 16384 x 256 fp32 take 16 us, their bytes 2.7.
+// One warp per token, every lane holding N experts next to one another.
+// The K-th largest of the lanes' best keys is a bound that at least K experts
+// reach and few more do: those are gathered in shared memory, a lane each, and
+// every lane counts the ones before its own.  Where more than 32 reach it
+// (equal logits, or too few lanes left open) the largest is taken K times instead, the lowest expert on ties.  Expert k ends in
+// lane k, which then reads its logit again (an L1 hit) for the weight.  Bound by instructions: 16384 x 256 fp32, 8
+// taken, 14.8 us, its bytes 2.7; sorting each lane's experts and taking the largest 8 times took 16.5 (512 experts: 23 against
+// 41), warps that stay and load the next token ahead 18.3, with fewer of them on an SM.
 template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) {
+  __shared__ unsigned long long found[kRouteWarps][32];
+  __shared__ uint32_t order[kRouteWarps][32];
   pdl_begin();
-  const uint32_t lane = lane_id();
-  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
+  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * kRouteWarps + warp;
   if (t >= p.tokens) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.stride;
   float l[N];
+  uint32_t key[N];
+  float bias[N];
+#pragma unroll
+  for (int j = 0; j < N; j++) bias[j] = 0.f;
+  if (p.sigmoid && p.bias) {
+    if (VEC && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0 && p.experts % 4 == 0)
+      load_row<float, N, true>(p.bias, p.experts, bias);
+    else
+      load_row<float, N, false>(p.bias, p.experts, bias);
+  }
   load_row<T, N, VEC>(row, p.experts, l);
-  unsigned long long q[N];  // key, then the higher for the lower expert
+#pragma unroll
+  for (int j = 0; j < N; j++) {
+    float s = l[j];
+    if (p.sigmoid) s = s == -INFINITY ? s : __fadd_rn(sigmoid(s), bias[j]);
+    key[j] = order_key(s);
+  }
+  uint32_t bound;
   {
-    float bias[N];
-    if (p.sigmoid && p.bias) {
-      if (VEC && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0 && p.experts % 4 == 0)
-        load_row<float, N, true>(p.bias, p.experts, bias);
-      else
-        load_row<float, N, false>(p.bias, p.experts, bias);
-    } else {
+    uint32_t best = key[0];
 #pragma unroll
-      for (int j = 0; j < N; j++) bias[j] = 0.f;
+    for (int j = 1; j < N; j++) best = max(best, key[j]);
+    uint32_t lanes = 0;
+    while (true) {
+      bound = __reduce_max_sync(kFull, best);
+      if (bound <= kClosed) break;
+      lanes += __popc(__ballot_sync(kFull, best == bound));
+      if (lanes >= p.k) break;
+      best = best == bound ? 0 : best;
     }
+    bound = max(bound, kClosed + 1);
+  }
+  uint32_t n = 0;  // experts that reach it
 #pragma unroll
-    for (int j = 0; j < N; j++) {
-      float s = l[j];
-      if (p.sigmoid) s = s == -INFINITY ? s : __fadd_rn(sigmoid(s), bias[j]);
-      q[j] = static_cast<unsigned long long>(order_key(s)) << 32 | static_cast<uint32_t>(N - 1 - j);
-    }
+  for (int j = 0; j < N; j++) {
+    const bool in = key[j] >= bound;
+    const uint32_t lanes = __ballot_sync(kFull, in), at = n + __popc(lanes & lanes_below());
+    if (in && at < 32) found[warp][at] = static_cast<unsigned long long>(key[j]) << 32 | (kFull - (lane * N + j));
+    n += __popc(lanes);
   }
   uint32_t mine = kFull;
-  unsigned long long best = q[0];
-  auto look = [&]() {
-    best = q[0];
+  __syncwarp();
+  if (n <= 32) {
+    const unsigned long long own = lane < n ? found[warp][lane] : 0;
+    uint32_t before = 0;
+    for (uint32_t i = 0; i < n; i++) before += found[warp][i] > own;
+    if (lane < n) order[warp][before] = kFull - static_cast<uint32_t>(own);
+    __syncwarp();
+    if (lane < n && lane < p.k) mine = order[warp][lane];
+  } else {
+    for (uint32_t k = 0; k < p.k; k++) {
+      uint32_t best = key[0], at = 0;
 #pragma unroll
-    for (int j = 1; j < N; j++) best = q[j] > best ? q[j] : best;
-  };
-  if (N <= 8)
-    sort_down<N>(q);
-  else
-    look();
-  for (uint32_t k = 0; k < p.k; k++) {
-    if (N <= 8) best = q[0];
-    const uint32_t key = static_cast<uint32_t>(best >> 32);
-    const uint32_t top = __reduce_max_sync(kFull, key);
-    if (top <= kClosed) break;
-    const uint32_t winner = __ffs(__ballot_sync(kFull, key == top)) - 1;
-    const uint32_t at = N - 1 - static_cast<uint32_t>(best);
-    const uint32_t e = __shfl_sync(kFull, lane * N + at, winner);
-    if (lane == k) mine = e;
-    if (lane == winner) {
-      if (N <= 8) {
+      for (int j = 1; j < N; j++)
+        if (key[j] > best) best = key[j], at = j;
+      const uint32_t top = __reduce_max_sync(kFull, best);
+      if (top <= kClosed) break;
+      const uint32_t winner = __ffs(__ballot_sync(kFull, best == top)) - 1;
+      const uint32_t e = __shfl_sync(kFull, lane * N + at, winner);
+      if (lane == k) mine = e;
 #pragma unroll
-        for (int j = 0; j + 1 < N; j++) q[j] = q[j + 1];
-        q[N - 1] = 0;
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; j++)
-          if (at == j) q[j] = 0;
-        look();
-      }
+      for (int j = 0; j < N; j++)
+        if (lane == winner && at == j) key[j] = 0;
     }
   }
   const bool have = mine != kFull;
@@ -191,7 +188,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
 // alone, so only those are read and every other gradient is zero; the plain
 // softmax needs the whole row.  The chosen experts' values meet the lanes that hold
 // those experts in a row of shared memory.
-template <typename T, int N, bool VEC>
+template <typename T, int N>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(RouteBwdParams p) {
   __shared__ float rows[kRouteWarps][32 * N];
   pdl_begin();
@@ -218,10 +215,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(RouteBwdPar
   float prob[N];
   float d = 0.f, mean = 0.f;  // this lane's chosen logit's gradient; sum of G p over the row
   if (whole) {
-    load_row<T, N, VEC>(row, p.experts, prob);
     float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < N; j++) top = fmaxf(top, prob[j]);
+    for (int j = 0; j < N; j++) {  // lane l's experts: l, l + 32, ...
+      const uint32_t e = j * 32 + lane;
+      prob[j] = e < p.experts ? to_f32<T>(row[e]) : -INFINITY;
+      top = fmaxf(top, prob[j]);
+    }
     top = warp_max_f32(top);
     float sum = 0.f;
 #pragma unroll
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(RouteBwdPar
   }
 #pragma unroll
   for (int j = 0; j < N; j++) {
-    const uint32_t e = lane * N + j;
+    const uint32_t e = j * 32 + lane;
     if (e < p.experts) out[e] = from_f32<T>(prob[j] * (mid[e] - mean));
   }
 }
@@ -285,8 +285,6 @@ __device__ __forceinline__ uint32_t slot_key(const DispatchParams& p, uint64_t i
   const int64_t v = p.ids64 ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
   return v >= 0 && v < static_cast<int64_t>(p.experts) ? static_cast<uint32_t>(v) : p.experts;
 }
-
-__device__ __forceinline__ uint32_t lanes_below() { return (1u << lane_id()) - 1u; }
 
 // The lanes whose key equals this one's, by a vote on each of the low `bits` bits.
 __device__ __forceinline__ uint32_t equal_lanes(uint32_t key, int bits) {
@@ -714,22 +712,19 @@ cudaError_t run(F* kernel, uint64_t grid_x, uint32_t grid_y, int threads, cudaSt
 
 uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
-template <typename T, int N, bool VEC, typename P>
-cudaError_t route_shape(P& p, cudaStream_t stream) {
-  const uint64_t grid = ceil_div(p.tokens, kRouteWarps);
-  if constexpr (std::is_same<P, RouteParams>::value)
-    return run(route_kernel<T, N, VEC>, grid, 1, kRouteWarps * 32, stream, &p);
-  else
-    return run(route_bwd_kernel<T, N, VEC>, grid, 1, kRouteWarps * 32, stream, &p);
-}
-
-template <typename T, int N, typename P>
-cudaError_t route_width(P& p, cudaStream_t stream) {
+template <typename T, int N>
+cudaError_t route_width(RouteParams& p, cudaStream_t stream) {
   // a lane's values as whole pieces: of 16 bytes, or of all its values where those are fewer
   constexpr uint64_t kPart = N * sizeof(T) < 16 ? N * sizeof(T) : 16;
   const bool vec = reinterpret_cast<uintptr_t>(p.logits) % kPart == 0 && p.stride * sizeof(T) % kPart == 0 &&
                    p.experts * sizeof(T) % kPart == 0;
-  return vec ? route_shape<T, N, true>(p, stream) : route_shape<T, N, false>(p, stream);
+  const uint64_t grid = ceil_div(p.tokens, kRouteWarps);
+  if (vec) return run(route_kernel<T, N, true>, grid, 1, kRouteWarps * 32, stream, &p);
+  return run(route_kernel<T, N, false>, grid, 1, kRouteWarps * 32, stream, &p);
+}
+template <typename T, int N>
+cudaError_t route_width(RouteBwdParams& p, cudaStream_t stream) {
+  return run(route_bwd_kernel<T, N>, ceil_div(p.tokens, kRouteWarps), 1, kRouteWarps * 32, stream, &p);
 }
 
 template <typename T, typename P>

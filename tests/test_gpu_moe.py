@@ -142,6 +142,29 @@ def test_route_ties_and_special_values(moe):
     assert torch.equal(d[2], torch.zeros(6, device="cuda"))
 
 
+@pytest.mark.parametrize("experts", [40, 64, 300, 1024])
+@pytest.mark.parametrize("k", [1, 8, 32])
+def test_route_many_equal_or_few_open(moe, experts, k):
+    """More experts tie for the last place than a warp has lanes; all that are open stand next to one another."""
+    logits = torch.zeros((4, experts), device="cuda")
+    logits[1, experts // 2:] = 1.0                 # ties above ties
+    logits[2, experts // 4:] = -math.inf           # few open, all equal
+    logits[3] = -math.inf
+    logits[3, -39:] = torch.arange(39.0)           # few open, in the last lanes alone
+    w, e = moe.route(logits, k)
+    half, quarter = experts // 2, experts // 4
+
+    def padded(ids):
+        return (ids + [-1] * k)[:k]
+
+    assert e[0].tolist() == list(range(k))
+    upper = list(range(half, experts))
+    assert e[1].tolist() == (upper + list(range(half)))[:k]
+    assert e[2].tolist() == padded(list(range(quarter)))
+    assert e[3].tolist() == padded(list(range(experts - 1, experts - 40, -1)))
+    assert torch.allclose(w.sum(1), torch.ones(4, device="cuda"), rtol=0, atol=2.0 ** -20)
+
+
 def test_route_strides_bias_and_empty(moe):
     g = torch.Generator().manual_seed(3)
     base = torch.randn((40, 100), generator=g).cuda()
