@@ -64,8 +64,9 @@ cudaError_t prepare_kernel(KernelPrep& kp, const void* fn, int threads, int smem
 // Launches kernel `fn` (args: pointers to its parameters) on `stream` as a
 // programmatic dependent of the work before it (the kernel begins with
 // pdl_begin()), and cooperatively -- every CTA resident at once -- if asked.
+// cluster > 1: in clusters of so many CTAs.
 cudaError_t launch_kernel(const void* fn, dim3 grid, dim3 block, int smem_bytes, cudaStream_t stream, void** args,
-                          bool cooperative);
+                          bool cooperative, unsigned cluster = 1);
 
 // count <= kMaxBatch; flags = workspace flag array (one per tile of the launch).
 // adaptive: the raw bypass in the same launch -- each tensor whose coded form
@@ -196,7 +197,7 @@ struct NormBwdParams {
   void *dy, *dx, *dweight, *dgate, *dnext_weight;
   float* parts;  // workspace
   uint32_t hidden;
-  uint32_t splits, units, walkers, ctas;  // set by the launch: ranges of rows per gate row and in all; who walks them
+  uint32_t splits, units, walkers, ctas, cluster;  // set by the launch: ranges of rows per gate row and in all; who walks them
 };
 uint64_t norm_workspace_bytes(uint64_t tokens, uint32_t hidden);
 cudaError_t launch_norm(const NormParams& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev);

@@ -168,6 +168,23 @@ __device__ __forceinline__ float warp_max_f32(float v) {
   return v;
 }
 
+// Thread-block clusters: the barrier of all threads of the cluster in its two halves (release, acquire), and a store to the
+// same variable in the shared memory of the cluster's CTA `cta`.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void st_shared_of_cta(uint32_t* var, uint32_t cta, uint32_t v) {
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u32 [a], %2;\n\t}" ::"r"(
+          smem_u32(var)),
+      "r"(cta), "r"(v)
+      : "memory");
+}
+
 // Sums of N values over a CTA of whole warps, every thread getting all of
 // them.  `red` holds N x 32 floats; a caller that sums again before a
 // __syncthreads of its own passes another buffer.
@@ -185,16 +202,19 @@ __device__ __forceinline__ void block_sum_f32(float (&v)[N], float* red) {
   for (int i = 0; i < N; i++) v[i] = warp_sum_f32(lane < warps ? red[i * 32 + lane] : 0.f);
 }
 
-// As block_sum_f32 for 2, 4 or 8 values with fewer shuffles.  Halving the
+// As block_sum_f32 for 2 or 4 values with fewer shuffles.  Halving the
 // lanes' groups, every lane keeps half of the values and gives the others to its
 // partner, until the lanes of group g (of 32 / N lanes) hold value g; the
 // rest is a tree inside the group.  The CTA's partial sums are added the
-// same way.  `red`: N x 32 floats, 16-byte aligned, those of absent warps zero
+// same way.  `red`: N x kSumSlots floats, 16-byte aligned, those of absent warps zero
 // (the caller clears them all before the first use); as above, two sums in
-// a row need two buffers.
-template <int N>
-__device__ __forceinline__ void block_sum_shared(float (&v)[N], float* red) {
-  static_assert(N == 2 || N == 4 || N == 8, "lane groups of 16, 8 or 4");
+// a row need two buffers.  CLUSTER: over all `ctas` CTAs of the cluster, this one being `rank`; every CTA
+// leaves its partial sums in all of them (a sum of two barriers, the CTA's and the
+// cluster's, would wait twice).  kSumSlots: 16 warps each of up to 4 CTAs, or 32 of one.
+constexpr int kSumSlots = 64;
+template <int N, bool CLUSTER = false>
+__device__ __forceinline__ void block_sum_shared(float (&v)[N], float* red, uint32_t rank = 0, uint32_t ctas = 1) {
+  static_assert(N == 2 || N == 4, "lane groups of 16 or 8");
   constexpr uint32_t kGroup = 32 / N;
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
   float s[N];
@@ -212,19 +232,29 @@ __device__ __forceinline__ void block_sum_shared(float (&v)[N], float* red) {
   }
 #pragma unroll
   for (; d >= 1; d /= 2) s[0] += __shfl_xor_sync(kFull, s[0], d);
-  if ((lane & (kGroup - 1)) == 0) red[(lane / kGroup) * 32 + warp] = s[0];
-  __syncthreads();
-  const float* part = red + (lane / kGroup) * 32 + (lane & (kGroup - 1)) * N;
-  float sum;
-  if (N == 2) {
+  float* slot = red + (lane / kGroup) * kSumSlots + warp;
+  if constexpr (CLUSTER) {
+    if ((lane & (kGroup - 1)) == 0)
+      for (uint32_t c = 0; c < ctas; c++)
+        st_shared_of_cta(reinterpret_cast<uint32_t*>(slot + 16 * rank), c, __float_as_uint(s[0]));
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    if ((lane & (kGroup - 1)) == 0) *slot = s[0];
+    __syncthreads();
+  }
+  // slots of a lane: all 64 of a cluster, or the first 32
+  constexpr uint32_t kOf = (CLUSTER ? kSumSlots : 32) / kGroup;
+  const float* part = red + (lane / kGroup) * kSumSlots + (lane & (kGroup - 1)) * kOf;
+  float sum = 0.f;
+  if constexpr (kOf == 2) {
     const float2 a = *reinterpret_cast<const float2*>(part);
     sum = a.x + a.y;
   } else {
-    const float4 a = *reinterpret_cast<const float4*>(part);
-    sum = (a.x + a.y) + (a.z + a.w);
-    if (N == 8) {
-      const float4 b = *reinterpret_cast<const float4*>(part + 4);
-      sum += (b.x + b.y) + (b.z + b.w);
+#pragma unroll
+    for (uint32_t i = 0; i < kOf; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(part + i);
+      sum += (a.x + a.y) + (a.z + a.w);
     }
   }
 #pragma unroll
@@ -241,18 +271,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {  // all but the last N groups have landed
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Thread-block clusters: the barrier of all threads of the cluster in its two halves (release, acquire), and a store to the
-// same variable in the shared memory of the cluster's CTA `cta`.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_shared_of_cta(uint32_t* var, uint32_t cta, uint32_t v) {
-  asm volatile(
-      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u32 [a], %2;\n\t}" ::"r"(
-          smem_u32(var)),
-      "r"(cta), "r"(v)
-      : "memory");
 }
 
 }  // namespace zc

@@ -116,9 +116,9 @@ __global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_
   constexpr int P = C / 2, kStages = kFwdStages<C>;
   using Ring = RowRing<T, V, C, BRANCH ? 2 : 1, kStages>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
-  __shared__ __align__(16) float red[2][128];
+  __shared__ __align__(16) float red[2][2 * kSumSlots];
   pdl_allow_dependents();
-  for (uint32_t i = threadIdx.x; i < 256; i += blockDim.x) red[i >> 7][i & 127] = 0.f;
+  for (uint32_t i = threadIdx.x; i < 4 * kSumSlots; i += blockDim.x) red[0][i] = 0.f;
   pdl_wait();
   const Ring ring{ring_smem, threadIdx.x, blockDim.x, p.hidden / V};
 #pragma unroll
@@ -216,10 +216,10 @@ cudaError_t run_ring(NormParams& p, int threads, cudaStream_t stream, const Devi
   static RingPrep prep;
   const int smem = static_cast<int>(RowRing<T, V, C, BRANCH ? 2 : 1, kFwdStages<C>>::bytes(threads));
   const void* fn = reinterpret_cast<const void*>(norm_ring_kernel<T, V, C, BRANCH, NEXT>);
-  int per_sm = 0;
-  cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, &per_sm);
+  int fit = 0;
+  cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, 1, &fit);
   if (e != cudaSuccess) return e;
-  const uint64_t most = static_cast<uint64_t>(per_sm) * static_cast<uint64_t>(dev.sm_count);
+  const uint64_t most = static_cast<uint64_t>(fit);
   void* args[] = {&p};
   return launch_kernel(fn, dim3(static_cast<unsigned>(p.tokens < most ? p.tokens : most)), dim3(threads), smem, stream,
                        args, false);

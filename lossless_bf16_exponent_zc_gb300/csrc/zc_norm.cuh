@@ -59,7 +59,8 @@ __device__ __forceinline__ void store_f32(float* p, const float (&f)[V]) {
 }
 
 // Launch shapes.  A narrow row is held by a warp.  Wider rows stream through a CTA's shared
-// memory, one thread for every 8 or 16 columns; rows too wide for that ring are held in a CTA's registers.
+// memory, one thread for every 8 or 16 columns; for rows too wide for one CTA the gradient takes a cluster, the forward
+// pass holds them in registers.
 constexpr int kNormWarps = 8;  // rows of a CTA in the warp shape
 constexpr int kNormRingThreads = 512;
 constexpr int kNormRingSmem = 225 * 1024;  // what the ring may take of the 227 KB a CTA can have
@@ -75,7 +76,8 @@ struct RowRing {
   static constexpr int NV = COLS / V;
   static constexpr bool kWords = V == 1 && sizeof(T) == 2;
   uint8_t* smem;
-  uint32_t me, threads, pieces;  // this thread among those that share a row, and the row's pieces
+  uint32_t me, threads, pieces;  // this thread among those that share a row (or its part of a cluster's), and its pieces
+  uint32_t first = 0;            // column that the part starts at
 
   __host__ __device__ static uint32_t region(uint32_t threads) {  // bytes of one row of one matrix
     return kWords ? (threads * NV * 2 + 4 + 15) / 16 * 16 : threads * NV * V * static_cast<uint32_t>(sizeof(T));
@@ -88,7 +90,7 @@ struct RowRing {
   // Where a thread's walk through a matrix starts: its first column of row t.
   template <typename U>
   __device__ __forceinline__ U* start(U* base, uint64_t t, uint64_t stride) const {
-    return base + t * stride + (kWords ? 0 : me * V);
+    return base + t * stride + first + (kWords ? 0 : me * V);
   }
   __device__ __forceinline__ void copy(int stage, int array, const T* row) const {
     uint8_t* to = at(stage, array);
@@ -169,7 +171,7 @@ struct RowRing {
     }
   }
   // This thread's columns of a parameter row.
-  __device__ __forceinline__ void params(const void* base, int is_f32, uint64_t first, float2 (&f)[COLS / 2]) const {
+  __device__ __forceinline__ void params(const void* base, int is_f32, uint64_t row, float2 (&f)[COLS / 2]) const {
     float* flat = reinterpret_cast<float*>(f);
 #pragma unroll
     for (int i = 0; i < NV; i++) {
@@ -177,7 +179,7 @@ struct RowRing {
       float v[V];
 #pragma unroll
       for (int j = 0; j < V; j++) v[j] = 0.f;
-      if (c < pieces) load_params<T, V>(base, is_f32, first + static_cast<uint64_t>(c) * V, v);
+      if (c < pieces) load_params<T, V>(base, is_f32, row + first + static_cast<uint64_t>(c) * V, v);
 #pragma unroll
       for (int j = 0; j < V; j++) flat[i * V + j] = v[j];
     }
@@ -193,10 +195,12 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 #endif
 
-// CTAs of a ring kernel on one SM, by CTA size (the ring's size follows from it); looked up once per device and size.
+// CTAs of a ring kernel (clusters of them) that the GPU holds, by CTA size (the ring's size follows from it); looked up
+// once per device, size and cluster.
 struct RingPrep {
-  std::atomic<int> per_sm[kMaxDevices][kNormRingThreads / 32 + 1];
+  std::atomic<int> fit[kMaxDevices][kNormRingThreads / 32 + 1];
 };
-cudaError_t prepare_ring(RingPrep& rp, const void* fn, int threads, int smem_bytes, const DeviceInfo& dev, int* per_sm);
+cudaError_t prepare_ring(RingPrep& rp, const void* fn, int threads, int smem_bytes, const DeviceInfo& dev, int cluster,
+                         int* fit);
 
 }  // namespace zc

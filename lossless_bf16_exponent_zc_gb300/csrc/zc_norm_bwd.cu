@@ -24,7 +24,8 @@ __host__ __device__ constexpr uint32_t norm_max_units(uint32_t hidden) {
 }
 constexpr int kBwdStages = 3;
 
-// Columns of a thread in the ring shape: 8, and 16 for 16-bit rows that 8 of each of 512 threads do not hold.  With 8 the
+// Columns of a thread in the ring shape: 8, and 16 for 16-bit rows that 8 of each of 512 threads do not hold; still wider
+// rows are shared by a cluster of 2 or 4 CTAs.  With 8 the
 // column sums, the weights and a row fit the 128 registers of a 512-thread CTA; 16 columns in 256 threads, two CTAs an
 // SM, spill registers and take 170 us instead of 130 (16384 x 4096 bf16), and 8 in 64 registers, again for two CTAs,
 // 238 us: the ring leaves the L1 cache too small for spilled registers.
@@ -56,17 +57,25 @@ struct BwdWalk {
 // second is taken together with the next row's first, so that a row costs one barrier: between two barriers the CTA
 // writes the last row's dy, takes this row's G, dx, column sums and v y, and the next row's first sums.  The inputs are
 // read from the stage twice rather than held, so that the column sums and the weights stay in registers.
-template <typename T, int V, int C, bool BRANCH, bool NEXT>
+template <typename T, int V, int C, bool CLUSTER, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(NormBwdParams p) {
   constexpr int P = C / 2;
   constexpr int kGx = 0, kGh = 1, kX = 2, kY = NEXT ? 3 : 1, kArrays = BRANCH && NEXT ? 4 : NEXT ? 3 : 2;
   using Ring = RowRing<T, V, C, kArrays, kBwdStages>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
-  __shared__ __align__(16) float red[2][128];
+  __shared__ __align__(16) float red[2][4 * kSumSlots];
   pdl_allow_dependents();
-  for (uint32_t i = threadIdx.x; i < 256; i += blockDim.x) red[0][i] = 0.f;
+  for (uint32_t i = threadIdx.x; i < 8 * kSumSlots; i += blockDim.x) red[0][i] = 0.f;
+  if (CLUSTER) {  // every CTA's sums are cleared before another writes there
+    cluster_arrive();
+    cluster_wait();
+  }
   pdl_wait();
-  const Ring ring{ring_smem, threadIdx.x, blockDim.x, p.hidden / V};
+  // this CTA's part of the rows, and who walks them: the CTA or its cluster
+  const uint32_t rank = CLUSTER ? cluster_rank() : 0, walker = CLUSTER ? blockIdx.x / p.cluster : blockIdx.x;
+  const uint32_t part = blockDim.x * C;
+  const uint32_t width = CLUSTER ? min(part, p.hidden - rank * part) : p.hidden;
+  const Ring ring{ring_smem, threadIdx.x, blockDim.x, width / V, rank * part};
   const float inv_d = 1.f / static_cast<float>(p.hidden);
   const bool wide = BRANCH && p.gate && p.gate_wide, narrow = BRANCH && p.gate && !p.gate_wide;
   const bool past = p.dx_new != nullptr;
@@ -76,7 +85,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
 
   // Addresses of the row to copy next and, for rows at odd addresses, of the row being computed.
   const T *gx = nullptr, *gh = nullptr, *x = nullptr, *y = nullptr;
-  BwdWalk ahead{blockIdx.x, 0, 0}, now{blockIdx.x, 0, 0};
+  BwdWalk ahead{walker, 0, 0}, now{walker, 0, 0};
   ahead.open(p);
   now.open(p);
   auto aim = [&](uint64_t t) {
@@ -110,7 +119,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
   };
   // The address of the row at hand, of which only rows at odd addresses need to know.
   auto row_of = [&](const void* base, uint64_t t, uint64_t stride) {
-    return Ring::kWords ? static_cast<const T*>(base) + t * stride : nullptr;
+    return Ring::kWords ? static_cast<const T*>(base) + t * stride + ring.first : nullptr;
   };
 #pragma unroll
   for (int s = 0; s < kBwdStages; s++) issue(s);
@@ -130,7 +139,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
 #pragma unroll
     for (int i = 0; i < P; i++) sum_b[i] = splat(0.f);
   };
-  float* mine = p.parts + static_cast<uint64_t>(blockIdx.x) * 2 * p.hidden;
+  float* mine = p.parts + static_cast<uint64_t>(walker) * 2 * p.hidden + ring.first;
   auto close_unit = [&](uint32_t u) {
     const float* fb = reinterpret_cast<const float*>(sum_b);
 #pragma unroll
@@ -139,8 +148,8 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
       if (c >= ring.pieces) continue;
       float k[V], w[V];
       if (wide) {
-        load_params<T, V>(p.gate, p.params_f32, (u / p.splits) * static_cast<uint64_t>(p.hidden) + c * V, k);
-        load_params<T, V>(p.weight, p.params_f32, c * V, w);
+        load_params<T, V>(p.gate, p.params_f32, (u / p.splits) * static_cast<uint64_t>(p.hidden) + ring.first + c * V, k);
+        load_params<T, V>(p.weight, p.params_f32, ring.first + c * V, w);
       }
       float dw[V], dg[V];
 #pragma unroll
@@ -148,7 +157,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
         dw[j] = wide ? fb[i * V + j] * k[j] : fb[i * V + j];
         dg[j] = wide ? fb[i * V + j] * w[j] : 0.f;
       }
-      if (u != blockIdx.x) {  // the CTA's first unit has its number
+      if (u != walker) {  // a walker's first unit has its number
         float sum[V];
         load_f32<V>(mine + c * V, sum);
 #pragma unroll
@@ -156,7 +165,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
       }
       store_f32<V>(mine + c * V, dw);
       if (!wide) continue;
-      const uint64_t at = static_cast<uint64_t>(u) * p.hidden + c * V;
+      const uint64_t at = static_cast<uint64_t>(u) * p.hidden + ring.first + c * V;
       if (p.splits > 1) {
         store_f32<V>(gate_parts + at, dg);
       } else if (p.params_f32) {
@@ -216,7 +225,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
 #pragma unroll
     for (int i = 0; i < P; i++) v[i] = mul2(rr, fma2(v[i], m, g[i]));
     ring.put(ring.start(static_cast<T*>(p.dy), before, p.hidden), v);
-    if (narrow && threadIdx.x == 0) {
+    if (narrow && threadIdx.x == 0 && rank == 0) {
       const float dg = root * vy;  // sum of G n w
       if (p.gate_tokens > 1)
         gate_parts[before] = dg;
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
   cp_async_wait<kBwdStages - 1>();
   if (Ring::kWords) __syncthreads();
   first_sums(0, now.t, sums);
-  block_sum_shared<4>(sums, red[1]);
+  block_sum_shared<4, CLUSTER>(sums, red[1], rank, p.cluster);
   while (now.valid(p)) {
     const uint64_t t = now.t;
     if (BRANCH && before != ~0ull) {
@@ -300,7 +309,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
       if (Ring::kWords) __syncthreads();
       first_sums(stage, now.t, sums);
     }
-    block_sum_shared<4>(sums, red[turn]);
+    block_sum_shared<4, CLUSTER>(sums, red[turn], rank, p.cluster);
     turn ^= 1;
     if (Ring::kWords) issue(done);  // now every thread is past its last reading of the row
   }
@@ -498,178 +507,6 @@ __global__ void __launch_bounds__(kNormWarps * 32, 2) norm_bwd_warp_kernel(NormB
   if (NEXT) flush(sum_n, mine + p.hidden);
 }
 
-// Rows wider than the ring holds: a CTA keeps one in registers at a time.
-template <typename T, int V, int NV, bool BRANCH, bool NEXT, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormBwdParams p) {
-  __shared__ float red[2][3 * 32];
-  pdl_begin();
-  const uint32_t me = threadIdx.x, step = blockDim.x, pieces = p.hidden / V;
-  const float inv_d = 1.f / static_cast<float>(p.hidden);
-  const bool wide = p.gate && p.gate_wide;
-  float* gate_parts = p.parts + static_cast<uint64_t>(p.ctas) * 2 * p.hidden;  // one row per unit, or one value per token
-  int turn = 0;
-  float sum_w[NV][V], sum_n[NV][V], sum_g[NV][V];
-#pragma unroll
-  for (int i = 0; i < NV; i++)
-#pragma unroll
-    for (int j = 0; j < V; j++) sum_w[i][j] = sum_n[i][j] = sum_g[i][j] = 0.f;
-
-  // This thread's columns of a sum to dst: fp32 or, `last`, a finished gradient row in the parameters' type.
-  auto flush = [&](float (&s)[NV][V], void* dst, bool last) {
-#pragma unroll
-    for (int i = 0; i < NV; i++)
-#pragma unroll
-      for (int j = 0; j < V; j++) {
-        const uint32_t col = (me + i * step) * V + j;
-        if (col >= p.hidden) continue;
-        if (last && !p.params_f32)
-          static_cast<T*>(dst)[col] = from_f32<T>(s[i][j]);
-        else
-          static_cast<float*>(dst)[col] = s[i][j];
-      }
-  };
-
-  for (uint32_t u = blockIdx.x; u < p.units; u += p.ctas) {
-    const uint64_t group = u / p.splits, split = u - static_cast<uint32_t>(group) * p.splits;
-    const uint64_t size = wide ? p.gate_tokens : p.tokens;
-    for (uint64_t t = group * size + split; t < (group + 1) * size; t += p.splits) {
-      Piece<T, V> gx[NV], gh[NV], y[NV], x[NV];
-#pragma unroll
-      for (int i = 0; i < NV; i++) {
-        const uint32_t c = me + i * step;
-        const uint64_t at = static_cast<uint64_t>(c) * V;
-        gx[i] = gh[i] = y[i] = x[i] = Piece<T, V>::zero();
-        if (c < pieces) {
-          if (NEXT) {
-            x[i] = Piece<T, V>::load(static_cast<const T*>(p.x_new) + t * p.x_new_stride + at);
-            gh[i] = Piece<T, V>::load(static_cast<const T*>(p.dh) + t * p.dh_stride + at);
-          }
-          if (BRANCH) y[i] = Piece<T, V>::load(static_cast<const T*>(p.y) + t * p.y_stride + at);
-          if (p.dx_new) gx[i] = Piece<T, V>::load(static_cast<const T*>(p.dx_new) + t * p.dx_new_stride + at);
-        }
-      }
-      float s[3] = {0.f, 0.f, 0.f};  // sums of x'^2, u x', y^2
-#pragma unroll
-      for (int i = 0; i < NV; i++) {
-        const uint32_t c = me + i * step;
-        float f[V];
-        if (NEXT) {
-          float h[V], w[V];
-          x[i].get(f);
-          gh[i].get(h);
-#pragma unroll
-          for (int j = 0; j < V; j++) w[j] = 0.f;
-          if (c < pieces) load_params<T, V>(p.next_weight, p.params_f32, static_cast<uint64_t>(c) * V, w);
-#pragma unroll
-          for (int j = 0; j < V; j++) {
-            s[0] = fmaf(f[j], f[j], s[0]);
-            s[1] = fmaf(h[j] * w[j], f[j], s[1]);
-          }
-        }
-        if (BRANCH) {
-          y[i].get(f);
-#pragma unroll
-          for (int j = 0; j < V; j++) s[2] = fmaf(f[j], f[j], s[2]);
-        }
-      }
-      block_sum_f32<3>(s, red[turn]);
-      turn ^= 1;
-      const float r2 = rsqrtf(s[0] * inv_d + p.eps), mean2 = s[1] * r2 * inv_d;  // mean(u n2)
-      const float r = rsqrtf(s[2] * inv_d + p.eps);
-      const uint64_t gate_row = p.gate ? t / p.gate_tokens : 0;
-      const float gate_one = p.gate && !p.gate_wide ? load_param<T>(p.gate, p.params_f32, gate_row) : 1.f;
-      float v[NV][V];  // G g w
-      float dots[2] = {0.f, 0.f};  // sums of v n and of G n w
-#pragma unroll
-      for (int i = 0; i < NV; i++) {
-        const uint32_t c = me + i * step;
-        const uint64_t at = static_cast<uint64_t>(c) * V;
-        float g[V];
-        gx[i].get(g);
-        if (NEXT) {
-          float f[V], h[V], w[V];
-          x[i].get(f);
-          gh[i].get(h);
-#pragma unroll
-          for (int j = 0; j < V; j++) w[j] = 0.f;
-          if (c < pieces) load_params<T, V>(p.next_weight, p.params_f32, at, w);
-#pragma unroll
-          for (int j = 0; j < V; j++) {
-            const float n2 = f[j] * r2;
-            g[j] += r2 * (h[j] * w[j] - n2 * mean2);
-            sum_n[i][j] = fmaf(h[j], n2, sum_n[i][j]);
-          }
-        }
-        if (c < pieces) {
-          float o[V];
-#pragma unroll
-          for (int j = 0; j < V; j++) o[j] = p.residual_scale * g[j];
-          Piece<T, V> out;
-          out.set(o);
-          out.store(static_cast<T*>(p.dx) + t * p.hidden + at);
-        }
-        if (BRANCH) {
-          float f[V], w[V], k[V];
-          y[i].get(f);
-#pragma unroll
-          for (int j = 0; j < V; j++) w[j] = 0.f, k[j] = gate_one;
-          if (c < pieces) {
-            load_params<T, V>(p.weight, p.params_f32, at, w);
-            if (wide) load_params<T, V>(p.gate, p.params_f32, gate_row * p.hidden + at, k);
-          }
-#pragma unroll
-          for (int j = 0; j < V; j++) {
-            const float n = f[j] * r, e = g[j] * n;  // e w: the gate's gradient; e k: the weight's
-            sum_w[i][j] = fmaf(e, k[j], sum_w[i][j]);
-            if (wide) sum_g[i][j] = fmaf(e, w[j], sum_g[i][j]);
-            v[i][j] = g[j] * k[j] * w[j];
-            dots[0] = fmaf(v[i][j], n, dots[0]);
-            dots[1] = fmaf(e, w[j], dots[1]);
-          }
-        }
-      }
-      if (BRANCH) {
-        block_sum_f32<2>(dots, red[turn]);
-        turn ^= 1;
-        const float mean = dots[0] * inv_d;
-        if (p.gate && !wide && me == 0) {
-          if (p.gate_tokens > 1)
-            gate_parts[t] = dots[1];
-          else if (p.params_f32)
-            static_cast<float*>(p.dgate)[t] = dots[1];
-          else
-            static_cast<T*>(p.dgate)[t] = from_f32<T>(dots[1]);
-        }
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-          const uint32_t c = me + i * step;
-          if (c >= pieces) continue;
-          float f[V], o[V];
-          y[i].get(f);
-#pragma unroll
-          for (int j = 0; j < V; j++) o[j] = r * (v[i][j] - f[j] * r * mean);
-          Piece<T, V> out;
-          out.set(o);
-          out.store(static_cast<T*>(p.dy) + t * p.hidden + static_cast<uint64_t>(c) * V);
-        }
-      }
-    }
-    if (BRANCH && wide) {
-      if (p.splits > 1)
-        flush(sum_g, gate_parts + static_cast<uint64_t>(u) * p.hidden, false);
-      else
-        flush(sum_g, static_cast<uint8_t*>(p.dgate) + group * p.hidden * (p.params_f32 ? 4 : sizeof(T)), true);
-#pragma unroll
-      for (int i = 0; i < NV; i++)
-#pragma unroll
-        for (int j = 0; j < V; j++) sum_g[i][j] = 0.f;
-    }
-  }
-  float* mine = p.parts + static_cast<uint64_t>(blockIdx.x) * 2 * p.hidden;
-  if (BRANCH) flush(sum_w, mine, false);
-  if (NEXT) flush(sum_n, mine + p.hidden, false);
-}
-
 // Adds the CTAs' sums, in order: the warps take a share of the parts each, a lane a column, and then half a warp, or a
 // warp, adds a column's shares.  blockIdx.y: 0 the branch weight's gradient, 1 the next weight's, 2 + g gate row g's.
 template <typename T, int WARPS>
@@ -732,8 +569,8 @@ __global__ void __launch_bounds__(256) norm_narrow_gate_kernel(NormBwdParams p) 
     static_cast<T*>(p.dgate)[blockIdx.x] = from_f32<T>(s[0]);
 }
 
-// Cuts the rows into ranges for at most `most` walkers, `per_cta` of them in a CTA (a range lies in one gate row's
-// tokens), launches `fn` and adds up what it left.
+// Cuts the rows into ranges for at most `most` walkers, `per_cta` of them in a CTA or each a cluster of p.cluster CTAs (a
+// range lies in one gate row's tokens), launches `fn` and adds up what it left.
 template <typename T>
 cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint32_t per_cta, int threads, int smem,
                           cudaStream_t stream, const DeviceInfo& dev) {
@@ -751,7 +588,7 @@ cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint3
   p.walkers = p.ctas * per_cta;
   void* args[] = {&p};
   cudaError_t e = cudaSuccess;
-  if (p.ctas) e = launch_kernel(fn, dim3(p.ctas), dim3(threads), smem, stream, args, false);
+  if (p.ctas) e = launch_kernel(fn, dim3(p.ctas * p.cluster), dim3(threads), smem, stream, args, false, p.cluster);
   if (e != cudaSuccess) return e;
   const uint32_t jobs = 2 + (wide && splits != 1 ? static_cast<uint32_t>(groups) : 0u);
   // 32 warps a CTA while the GPU holds all such CTAs at once, two an SM (4452 x 704 fp32 18.1 us in all against 22.9
@@ -772,50 +609,49 @@ cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint3
    : p.y                ? reinterpret_cast<const void*>(KERNEL<__VA_ARGS__, true, false>)               \
                         : reinterpret_cast<const void*>(KERNEL<__VA_ARGS__, false, true>))
 
-template <typename T, int V, int C, bool BRANCH, bool NEXT>
+template <typename T, int V, int C, bool CLUSTER, bool BRANCH, bool NEXT>
 cudaError_t run_ring(NormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
-  static RingPrep prep;
+  static RingPrep prep[2];  // for clusters of 2 and 4
   constexpr int kArrays = BRANCH && NEXT ? 4 : NEXT ? 3 : 2;
   const int smem = static_cast<int>(RowRing<T, V, C, kArrays, kBwdStages>::bytes(threads));
-  const void* fn = reinterpret_cast<const void*>(norm_bwd_ring_kernel<T, V, C, BRANCH, NEXT>);
-  int per_sm = 0;
-  cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, &per_sm);
+  const void* fn = reinterpret_cast<const void*>(norm_bwd_ring_kernel<T, V, C, CLUSTER, BRANCH, NEXT>);
+  int fit = 0;
+  cudaError_t e = prepare_ring(prep[p.cluster == 4], fn, threads, smem, dev, static_cast<int>(p.cluster), &fit);
   if (e != cudaSuccess) return e;
-  return launch_ranges<T>(p, fn, static_cast<uint64_t>(per_sm) * static_cast<uint64_t>(dev.sm_count), 1, threads, smem,
-                          stream, dev);
+  return launch_ranges<T>(p, fn, static_cast<uint64_t>(fit), 1, threads, smem, stream, dev);
 }
 
-template <typename T, int V, int C>
-cudaError_t run_ring(NormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
-  if (p.y && p.next_weight) return run_ring<T, V, C, true, true>(p, threads, stream, dev);
-  if (p.y) return run_ring<T, V, C, true, false>(p, threads, stream, dev);
-  return run_ring<T, V, C, false, true>(p, threads, stream, dev);
+// Runs the ring with C columns a thread and so many CTAs a row if it holds such rows.
+template <typename T, int V, int C, bool CLUSTER>
+bool run_ring(NormBwdParams& p, uint32_t cluster, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e) {
+  const uint32_t all = cluster * C * 32;
+  const int threads = static_cast<int>((p.hidden + all - 1) / all * 32);
+  if (threads > kNormRingThreads || RowRing<T, V, C, 4, kBwdStages>::bytes(threads) > kNormRingSmem) return false;
+  p.cluster = cluster;
+  if (p.y && p.next_weight)
+    *e = run_ring<T, V, C, CLUSTER, true, true>(p, threads, stream, dev);
+  else if (p.y)
+    *e = run_ring<T, V, C, CLUSTER, true, false>(p, threads, stream, dev);
+  else
+    *e = run_ring<T, V, C, CLUSTER, false, true>(p, threads, stream, dev);
+  return true;
 }
 
 template <typename T, int V>
 cudaError_t run_width(NormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
-  const uint32_t d = p.hidden;
-  const uint64_t sms = static_cast<uint64_t>(dev.sm_count);
-  if (d <= kNormWarpWidth)
-    return launch_ranges<T>(p, ZC_NORM_MODE(norm_bwd_warp_kernel, T, V), 4 * kNormWarps * sms, kNormWarps,
-                            kNormWarps * 32, 0, stream, dev);
-  auto threads = [&](int cols) { return static_cast<int>((d + cols * 32 - 1) / (cols * 32) * 32); };
-  if (threads(kBwdCols) <= kNormRingThreads &&
-      RowRing<T, V, kBwdCols, 4, kBwdStages>::bytes(threads(kBwdCols)) <= kNormRingSmem)
-    return run_ring<T, V, kBwdCols>(p, threads(kBwdCols), stream, dev);
-  if constexpr (sizeof(T) == 2 && V > 1) {
-    if (threads(kBwdWideCols) <= kNormRingThreads &&
-        RowRing<T, V, kBwdWideCols, 4, kBwdStages>::bytes(threads(kBwdWideCols)) <= kNormRingSmem)
-      return run_ring<T, V, kBwdWideCols>(p, threads(kBwdWideCols), stream, dev);
+  p.cluster = 1;
+  if (p.hidden <= kNormWarpWidth)
+    return launch_ranges<T>(p, ZC_NORM_MODE(norm_bwd_warp_kernel, T, V), 4ull * kNormWarps * static_cast<uint64_t>(dev.sm_count),
+                            kNormWarps, kNormWarps * 32, 0, stream, dev);
+  cudaError_t e;
+  constexpr int kWide = sizeof(T) == 2 && V > 1 ? kBwdWideCols : kBwdCols;
+  if (run_ring<T, V, kBwdCols, false>(p, 1, stream, dev, &e)) return e;
+  if constexpr (kWide != kBwdCols) {
+    if (run_ring<T, V, kWide, false>(p, 1, stream, dev, &e)) return e;
   }
-  if (p.y && p.next_weight)
-    return launch_ranges<T>(p, reinterpret_cast<const void*>(norm_bwd_kernel<T, V, 16 / V, true, true, 1024>), 2 * sms, 1,
-                            threads(16), 0, stream, dev);
-  if (p.y)
-    return launch_ranges<T>(p, reinterpret_cast<const void*>(norm_bwd_kernel<T, V, 16 / V, true, false, 1024>), 2 * sms, 1,
-                            threads(16), 0, stream, dev);
-  return launch_ranges<T>(p, reinterpret_cast<const void*>(norm_bwd_kernel<T, V, 16 / V, false, true, 1024>), 2 * sms, 1,
-                          threads(16), 0, stream, dev);
+  if (run_ring<T, V, kWide, true>(p, 2, stream, dev, &e)) return e;
+  if (run_ring<T, V, kWide, true>(p, 4, stream, dev, &e)) return e;
+  return cudaErrorInvalidValue;  // wider than ZC_NORM_MAX_HIDDEN
 }
 #undef ZC_NORM_MODE
 
@@ -826,19 +662,35 @@ cudaError_t run_typed(NormBwdParams& p, bool vec, cudaStream_t stream, const Dev
 
 }  // namespace
 
-cudaError_t prepare_ring(RingPrep& rp, const void* fn, int threads, int smem_bytes, const DeviceInfo& dev, int* per_sm) {
+cudaError_t prepare_ring(RingPrep& rp, const void* fn, int threads, int smem_bytes, const DeviceInfo& dev, int cluster,
+                         int* fit) {
   const bool cached = dev.device >= 0 && dev.device < kMaxDevices;
-  std::atomic<int>* known = cached ? &rp.per_sm[dev.device][threads / 32] : nullptr;
+  std::atomic<int>* known = cached ? &rp.fit[dev.device][threads / 32] : nullptr;
   if (known) {
-    *per_sm = known->load(std::memory_order_acquire);
-    if (*per_sm > 0) return cudaSuccess;
+    *fit = known->load(std::memory_order_acquire);
+    if (*fit > 0) return cudaSuccess;
   }
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingSmem);
   if (e != cudaSuccess) return e;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, fn, threads, static_cast<size_t>(smem_bytes));
+  if (cluster == 1) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(fit, fn, threads, static_cast<size_t>(smem_bytes));
+    *fit *= dev.sm_count;
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / cluster * cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(fit, fn, &cfg);
+  }
   if (e != cudaSuccess) return e;
-  if (*per_sm < 1) return cudaErrorInvalidConfiguration;
-  if (known) known->store(*per_sm, std::memory_order_release);
+  if (*fit < 1) return cudaErrorInvalidConfiguration;
+  if (known) known->store(*fit, std::memory_order_release);
   return cudaSuccess;
 }
 

@@ -144,6 +144,13 @@ def test_gates(norm, gate, tokens, hidden):
     check(norm, make(tokens, tokens, hidden, "f32", "f32", gate, False))
 
 
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full", "sequence", "narrow"])
+@pytest.mark.parametrize("hidden", [4099, 8200, 12288])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gates_of_wide_rows(norm, gate, hidden, dtype):
+    check(norm, make(hidden, 402, hidden, dtype, "f32", gate, True))
+
+
 @pytest.mark.parametrize("tokens", [1, 2, 151, 305, 2049])
 def test_token_counts_and_a_reused_workspace(norm, tokens):
     """The workspace holds whatever an earlier call left there."""
