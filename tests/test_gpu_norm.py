@@ -212,6 +212,29 @@ def test_views_expanded_gradients_and_in_place(norm):
     assert got[0] is x and torch.equal(x, want[0]) and torch.equal(got[1], want[1])
 
 
+def test_offsets_past_32_bits(norm):
+    """More than 2^32 bytes and 2^31 values: the last rows are those of a call with them alone."""
+    tokens, hidden = 140000, 16384
+    g = torch.Generator(device="cuda").manual_seed(13)
+    one = torch.randn((7, hidden), device="cuda", generator=g).to(torch.bfloat16)
+    x = torch.empty((tokens, hidden), dtype=torch.bfloat16, device="cuda")
+    x.zero_()
+    x[-7:] = one
+    w = torch.rand(hidden, device="cuda", generator=g) + 0.5
+    assert x.numel() > 2 ** 31
+    got, want = norm.post_norm(x, x, w, next_weight=w), norm.post_norm(one, one, w, next_weight=w)
+    for a, b in zip(got, want):
+        assert torch.equal(a[-7:], b) and not a[:-7].any()
+    del got
+    ws = norm.workspace(tokens, hidden)
+    a = norm.post_norm_backward(x, x, x, x, w, ws, next_weight=w)
+    b = norm.post_norm_backward(one, one, one, one, w, ws, next_weight=w)
+    assert torch.equal(a.dy[-7:], b.dy) and torch.equal(a.dx[-7:], b.dx)
+    # the rows of zeros add nothing; the seven are shared out among other CTAs, so their sums have another order
+    for u, v in ((a.dweight, b.dweight), (a.dnext_weight, b.dnext_weight)):
+        assert float((u - v).abs().max()) <= 32 * E32 * float(v.abs().max())
+
+
 def test_zeros_infinities_and_nan(norm):
     """A row of zeros norms to zero; a row with an infinity or NaN spoils itself alone."""
     d = make(6, 12, 128, "f32", "f32", "token", True)
