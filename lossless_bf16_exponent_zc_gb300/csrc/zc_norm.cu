@@ -13,6 +13,7 @@ namespace zc {
 
 namespace {
 
+// Rows held in registers, NV pieces a thread: by a warp (WARP), or the widest by a CTA.
 template <typename T, int V, int NV, bool WARP, bool BRANCH, bool NEXT, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_kernel(NormParams p) {
   __shared__ float red[2][32];
@@ -110,8 +111,8 @@ constexpr int kFwdCols = 8, kFwdWideCols = 16;
 template <int C>
 constexpr int kFwdStages = C == kFwdCols ? 4 : 3;
 
-// The ring shape: rows blockIdx.x, blockIdx.x + CTAs, ... stream through shared memory.
-template <typename T, int V, int C, bool BRANCH, bool NEXT>
+// The ring shape: rows walker, walker + walkers, ... stream through the shared memory of a CTA or a cluster of two.
+template <typename T, int V, int C, int CTAS, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_ring_kernel(NormParams p) {
   constexpr int P = C / 2, kStages = kFwdStages<C>;
   using Ring = RowRing<T, V, C, BRANCH ? 2 : 1, kStages>;
@@ -119,19 +120,26 @@ __global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_
   __shared__ __align__(16) float red[2][2 * kSumSlots];
   pdl_allow_dependents();
   for (uint32_t i = threadIdx.x; i < 4 * kSumSlots; i += blockDim.x) red[0][i] = 0.f;
+  if (CTAS > 1) {  // every CTA's sums are cleared before another writes there
+    cluster_arrive();
+    cluster_wait();
+  }
   pdl_wait();
-  const Ring ring{ring_smem, threadIdx.x, blockDim.x, p.hidden / V};
+  const uint32_t rank = CTAS > 1 ? cluster_rank() : 0, part = blockDim.x * C;
+  const uint32_t width = CTAS > 1 ? min(part, p.hidden - rank * part) : p.hidden;
+  const Ring ring{ring_smem, threadIdx.x, blockDim.x, width / V, rank * part};
+  const uint64_t walker = blockIdx.x / CTAS, walkers = gridDim.x / CTAS;
 #pragma unroll
   for (int i = 0; i < (BRANCH ? 2 : 1); i++) ring.clear(i, false);
   const float inv_d = 1.f / static_cast<float>(p.hidden);
   const bool wide = BRANCH && p.gate && p.gate_wide, narrow = BRANCH && p.gate && !p.gate_wide;
   const T *x_at = static_cast<const T*>(p.x), *y_at = static_cast<const T*>(p.y);
-  uint64_t ahead = blockIdx.x;
+  uint64_t ahead = walker;
   auto issue = [&](int stage) {
     if (ahead < p.tokens) {
       ring.copy(stage, 0, ring.start(x_at, ahead, p.x_stride));
       if (BRANCH) ring.copy(stage, 1, ring.start(y_at, ahead, p.y_stride));
-      ahead += gridDim.x;
+      ahead += walkers;
     }
     cp_async_commit();
   };
@@ -146,19 +154,19 @@ __global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_
   cp_async_wait<kStages - 1>();
   __syncthreads();
   int stage = 0, turn = 0;
-  for (uint64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+  for (uint64_t t = walker; t < p.tokens; t += walkers) {
     float2 x[P];
     float sums[2];
-    ring.get(stage, 0, x_at + t * p.x_stride, x);
+    ring.get(stage, 0, x_at + t * p.x_stride + ring.first, x);
     if (BRANCH) {
       float2 y[P], yy = splat(0.f);
-      ring.get(stage, 1, y_at + t * p.y_stride, y);
+      ring.get(stage, 1, y_at + t * p.y_stride + ring.first, y);
 #pragma unroll
       for (int i = 0; i < P; i++) yy = fma2(y[i], y[i], yy);
       sums[0] = yy.x + yy.y;
       sums[1] = 0.f;
       cp_async_wait<kStages - 2>();  // the next row, which the barrier below shows to all
-      block_sum_shared<2>(sums, red[turn]);
+      block_sum_shared<2, (CTAS > 1)>(sums, red[turn], rank, CTAS);
       turn ^= 1;
       issue(stage);
       const float2 r = splat(rsqrtf(sums[0] * inv_d + p.eps)), a = splat(p.residual_scale);
@@ -171,8 +179,7 @@ __global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_
         for (int i = 0; i < P; i++) k[i] = splat(one);
       }
 #pragma unroll
-      for (int i = 0; i < P; i++)
-        x[i] = fma2(k[i], mul2(mul2(y[i], r), w[i]), mul2(a, x[i]));
+      for (int i = 0; i < P; i++) x[i] = fma2(k[i], mul2(mul2(y[i], r), w[i]), mul2(a, x[i]));
       ring.put(ring.start(static_cast<T*>(p.x_new), t, p.hidden), x);
     }
     if (NEXT) {
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_
       sums[0] = xx.x + xx.y;
       sums[1] = 0.f;
       if (!BRANCH) cp_async_wait<kStages - 2>();
-      block_sum_shared<2>(sums, red[turn]);
+      block_sum_shared<2, (CTAS > 1)>(sums, red[turn], rank, CTAS);
       turn ^= 1;
       if (!BRANCH) issue(stage);
       const float2 r = splat(rsqrtf(sums[0] * inv_d + p.eps));
@@ -211,31 +218,31 @@ cudaError_t run_shape(NormParams& p, int threads, cudaStream_t stream, const Dev
                        false);
 }
 
-template <typename T, int V, int C, bool BRANCH, bool NEXT>
+template <typename T, int V, int C, int CTAS, bool BRANCH, bool NEXT>
 cudaError_t run_ring(NormParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
   static RingPrep prep;
   const int smem = static_cast<int>(RowRing<T, V, C, BRANCH ? 2 : 1, kFwdStages<C>>::bytes(threads));
-  const void* fn = reinterpret_cast<const void*>(norm_ring_kernel<T, V, C, BRANCH, NEXT>);
+  const void* fn = reinterpret_cast<const void*>(norm_ring_kernel<T, V, C, CTAS, BRANCH, NEXT>);
   int fit = 0;
-  cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, 1, &fit);
+  cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, CTAS, &fit);
   if (e != cudaSuccess) return e;
-  const uint64_t most = static_cast<uint64_t>(fit);
+  const uint64_t walkers = p.tokens < static_cast<uint64_t>(fit) ? p.tokens : static_cast<uint64_t>(fit);
   void* args[] = {&p};
-  return launch_kernel(fn, dim3(static_cast<unsigned>(p.tokens < most ? p.tokens : most)), dim3(threads), smem, stream,
-                       args, false);
+  return launch_kernel(fn, dim3(static_cast<unsigned>(walkers) * CTAS), dim3(threads), smem, stream, args, false, CTAS);
 }
 
-// Runs the ring with C columns a thread if it holds such rows.
-template <typename T, int V, int C>
+// Runs the ring with C columns a thread and CTAS CTAs a row if it holds such rows.
+template <typename T, int V, int C, int CTAS>
 bool run_ring(NormParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e) {
-  const int threads = static_cast<int>((p.hidden + C * 32 - 1) / (C * 32) * 32);
+  constexpr uint32_t kAll = CTAS * C * 32;
+  const int threads = static_cast<int>((p.hidden + kAll - 1) / kAll * 32);
   if (threads > kNormRingThreads || RowRing<T, V, C, 2, kFwdStages<C>>::bytes(threads) > kNormRingSmem) return false;
   if (p.y && p.next_weight)
-    *e = run_ring<T, V, C, true, true>(p, threads, stream, dev);
+    *e = run_ring<T, V, C, CTAS, true, true>(p, threads, stream, dev);
   else if (p.y)
-    *e = run_ring<T, V, C, true, false>(p, threads, stream, dev);
+    *e = run_ring<T, V, C, CTAS, true, false>(p, threads, stream, dev);
   else
-    *e = run_ring<T, V, C, false, true>(p, threads, stream, dev);
+    *e = run_ring<T, V, C, CTAS, false, true>(p, threads, stream, dev);
   return true;
 }
 
@@ -254,11 +261,16 @@ cudaError_t run_width(NormParams& p, cudaStream_t stream, const DeviceInfo& dev)
     return run_shape<T, V, 16, true, kWarp>(p, kWarp, stream, dev);
   }
   cudaError_t e;
-  if (run_ring<T, V, kFwdCols>(p, stream, dev, &e)) return e;
+  if (run_ring<T, V, kFwdCols, 1>(p, stream, dev, &e)) return e;
+  if (run_ring<T, V, kFwdWideCols, 1>(p, stream, dev, &e)) return e;
+  // Wider still: in 16-byte pieces a CTA holds a row in registers (4096 x 16384 bf16 114 us; a cluster of two through the
+  // ring 152, its two cluster barriers a row wait too long), otherwise the cluster takes it.
   if constexpr (V > 1) {
-    if (run_ring<T, V, kFwdWideCols>(p, stream, dev, &e)) return e;
+    return run_shape<T, V, 16 / V, false, 1024>(p, static_cast<int>((d + 511) / 512 * 32), stream, dev);
+  } else {
+    if (run_ring<T, V, kFwdWideCols, 2>(p, stream, dev, &e)) return e;
+    return cudaErrorInvalidValue;  // wider than ZC_NORM_MAX_HIDDEN
   }
-  return run_shape<T, V, 16 / V, false, 1024>(p, static_cast<int>((d + 511) / 512 * 32), stream, dev);
 }
 
 template <typename T>

@@ -59,8 +59,7 @@ __device__ __forceinline__ void store_f32(float* p, const float (&f)[V]) {
 }
 
 // Launch shapes.  A narrow row is held by a warp.  Wider rows stream through a CTA's shared
-// memory, one thread for every 8 or 16 columns; for rows too wide for one CTA the gradient takes a cluster, the forward
-// pass holds them in registers.
+// memory, one thread for every 8 or 16 columns, the widest through a cluster's or, in the forward pass, a CTA's registers.
 constexpr int kNormWarps = 8;  // rows of a CTA in the warp shape
 constexpr int kNormRingThreads = 512;
 constexpr int kNormRingSmem = 225 * 1024;  // what the ring may take of the 227 KB a CTA can have
