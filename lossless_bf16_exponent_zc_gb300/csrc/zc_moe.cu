@@ -3,9 +3,9 @@
 // pieces, bringing the experts' outputs back weighted, and their gradients.
 // Definitions in include/zc.h.
 //
-// Everything here is bound by memory: each value is read or written once and
-// takes a few operations.  No kernel uses atomics on global memory and every
-// sum has a fixed order, so the same inputs give the same bits.
+// All but the router are bound by memory: each value is read or written once
+// and takes a few operations.  No result depends on the order of atomics
+// (counts are whole numbers) and every sum has a fixed order, so the same inputs give the same bits.
 #include "zc_internal.h"
 #include "zc_layer.cuh"
 
@@ -74,18 +74,31 @@ __device__ __forceinline__ void load_row(const T* row, uint32_t width, float (&v
   }
 }
 
+// An expert's choice: its logit, or its sigmoid plus its bias; minus infinity if it is closed.
+__device__ __forceinline__ float choice_of(const RouteParams& p, float l, uint32_t e, float* prob) {
+  if (!p.sigmoid || l == -INFINITY) return l;
+  *prob = sigmoid(l);
+  return p.bias ? __fadd_rn(*prob, p.bias[e]) : *prob;
+}
+
 // One warp per token, every lane holding N experts next to one another.
-// The K-th largest of the lanes' best keys is a bound that at least K experts
-// reach and few more do: those are gathered in shared memory, a lane each, and
-// every lane counts the ones before its own.  Where more than 32 reach it
-// (equal logits, or too few lanes left open) the largest is taken K times instead, the lowest expert on ties.  Expert k ends in
-// lane k, which then reads its logit again (an L1 hit) for the weight.  Bound by instructions: 16384 x 256 fp32, 8
-// taken, 14.8 us, its bytes 2.7; sorting each lane's experts and taking the largest 8 times took 16.5 (512 experts: 23 against
-// 41), warps that stay and load the next token ahead 18.3, with fewer of them on an SM.
+// The K-th largest of the lanes' best choices is a bound that at least K
+// experts reach and few more do: those are gathered in shared memory, a lane
+// each, and every lane counts the ones before its own.  Where more than 32
+// reach it (equal logits, or too few lanes left open) the largest is taken K
+// times instead, the lowest expert on ties.
+// For the bound a sigmoid is good enough to 2^-20 (the fast exponential's and
+// divide's stated errors make 2^-21 of a value in 0..1, the exact one's own 2^-22): with the bound lowered by twice
+// that and the sums' rounding, no expert that belongs among the K stays out, and
+// the exact sigmoid is taken of those gathered alone, one a lane.
+// Bound by instructions: 16384 x 256 fp32, 8 taken with a bias, 12.6 us (softmax 10.3), its
+// bytes 2.7.  With exact sigmoids of all experts it took 15.0; sorting each
+// lane's experts and taking the largest 8 times 16.5 (512 experts: 41 against
+// 23); warps that stay and load the next token ahead 18.3, for fewer of them fit an SM.
 template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) {
   __shared__ unsigned long long found[kRouteWarps][32];
-  __shared__ uint32_t order[kRouteWarps][32];
+  __shared__ float2 order[kRouteWarps][32];  // by rank: the expert, and its logit or its sigmoid
   pdl_begin();
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
   const uint64_t t = static_cast<uint64_t>(blockIdx.x) * kRouteWarps + warp;
@@ -93,21 +106,23 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
   const T* row = static_cast<const T*>(p.logits) + t * p.stride;
   float l[N];
   uint32_t key[N];
-  float bias[N];
-#pragma unroll
-  for (int j = 0; j < N; j++) bias[j] = 0.f;
-  if (p.sigmoid && p.bias) {
-    if (VEC && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0 && p.experts % 4 == 0)
-      load_row<float, N, true>(p.bias, p.experts, bias);
-    else
-      load_row<float, N, false>(p.bias, p.experts, bias);
-  }
   load_row<T, N, VEC>(row, p.experts, l);
+  if (p.sigmoid) {
+    float bias[N];
 #pragma unroll
-  for (int j = 0; j < N; j++) {
-    float s = l[j];
-    if (p.sigmoid) s = s == -INFINITY ? s : __fadd_rn(sigmoid(s), bias[j]);
-    key[j] = order_key(s);
+    for (int j = 0; j < N; j++) bias[j] = 0.f;
+    if (p.bias) {
+      if (VEC && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0 && p.experts % 4 == 0)
+        load_row<float, N, true>(p.bias, p.experts, bias);
+      else
+        load_row<float, N, false>(p.bias, p.experts, bias);
+    }
+#pragma unroll
+    for (int j = 0; j < N; j++)
+      key[j] = order_key(l[j] == -INFINITY ? l[j] : __fdividef(1.f, 1.f + __expf(-l[j])) + bias[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; j++) key[j] = order_key(l[j]);
   }
   uint32_t bound;
   {
@@ -122,6 +137,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
       if (lanes >= p.k) break;
       best = best == bound ? 0 : best;
     }
+    if (p.sigmoid && bound > kClosed) {
+      const float b = __uint_as_float(bound & 0x80000000u ? bound ^ 0x80000000u : ~bound);  // order_key undone
+      if (fabsf(b) < INFINITY) bound = order_key(b - 0x1p-18f - fabsf(b) * 0x1p-20f);
+    }
     bound = max(bound, kClosed + 1);
   }
   uint32_t n = 0;  // experts that reach it
@@ -129,19 +148,36 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
   for (int j = 0; j < N; j++) {
     const bool in = key[j] >= bound;
     const uint32_t lanes = __ballot_sync(kFull, in), at = n + __popc(lanes & lanes_below());
-    if (in && at < 32) found[warp][at] = static_cast<unsigned long long>(key[j]) << 32 | (kFull - (lane * N + j));
+    if (in && at < 32) found[warp][at] = lane * N + j;
     n += __popc(lanes);
   }
   uint32_t mine = kFull;
+  float value = -INFINITY;  // of expert `mine`: its logit, or its sigmoid
   __syncwarp();
   if (n <= 32) {
-    const unsigned long long own = lane < n ? found[warp][lane] : 0;
+    const uint32_t e = lane < n ? static_cast<uint32_t>(found[warp][lane]) : 0;
+    float v = lane < n ? to_f32<T>(row[e]) : -INFINITY, prob = 0.f;
+    const uint32_t exact = order_key(choice_of(p, v, e, &prob));
+    if (p.sigmoid) v = prob;
+    const unsigned long long own = lane < n ? static_cast<unsigned long long>(exact) << 32 | (kFull - e) : 0;
+    __syncwarp();
+    found[warp][lane] = own;
+    __syncwarp();
     uint32_t before = 0;
     for (uint32_t i = 0; i < n; i++) before += found[warp][i] > own;
-    if (lane < n) order[warp][before] = kFull - static_cast<uint32_t>(own);
+    if (lane < n) order[warp][before] = make_float2(__uint_as_float(e), v);
     __syncwarp();
-    if (lane < n && lane < p.k) mine = order[warp][lane];
+    if (lane < n && lane < p.k) {
+      mine = __float_as_uint(order[warp][lane].x);
+      value = order[warp][lane].y;
+    }
   } else {
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      float prob;
+      const uint32_t e = lane * N + j;
+      key[j] = e < p.experts ? order_key(choice_of(p, l[j], e, &prob)) : 0;
+    }
     for (uint32_t k = 0; k < p.k; k++) {
       uint32_t best = key[0], at = 0;
 #pragma unroll
@@ -156,16 +192,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
       for (int j = 0; j < N; j++)
         if (lane == winner && at == j) key[j] = 0;
     }
+    if (mine != kFull) {
+      value = to_f32<T>(row[mine]);
+      if (p.sigmoid) value = sigmoid(value);
+    }
   }
   const bool have = mine != kFull;
-  const float lm = have ? to_f32<T>(row[mine]) : -INFINITY;
   float w;
   if (p.sigmoid) {
-    w = have ? sigmoid(lm) : 0.f;
+    w = have ? value : 0.f;
     if (p.renormalize) w = w / (warp_sum_f32(w) + 1e-20f);
   } else {
-    const float top = __shfl_sync(kFull, lm, 0);  // the first pick is the row's largest logit
-    w = have ? expf(lm - top) : 0.f;
+    const float top = __shfl_sync(kFull, value, 0);  // the first pick is the row's largest logit
+    w = have ? expf(value - top) : 0.f;
     float sum;
     if (p.renormalize) {
       sum = warp_sum_f32(w);
@@ -408,9 +447,10 @@ __global__ void __launch_bounds__(kPrefixThreads) __cluster_dims__(kPrefixCtas, 
 // places the slots of a few tokens, then reads each token once and writes its K
 // rows.  A slot's row is its expert's first + those in earlier chunks + its place in the chunk.  In a call with few
 // slots (`single`) the CTA counts all of them itself, those before its own
-// apart (two counts in a word), and ranks its own as above, so that the call is one
-// launch: with 8192 slots of 128 experts 9.9 us against 10.6 in three, with 1024 3.1 against 8.3, with 16384 18.0
-// against 16.4.  Bound by memory: 16384 x 4096 bf16 to 4 experts each, 1.34 GB, 118 us in all, of which the sort 8.
+// apart (two counts in a word), and ranks its own as above, so that the call
+// is one launch: with 8192 slots of 128 experts 9.9 us against 10.6 in three,
+// with 1024 3.1 against 8.3, with 16384 18.0 against 16.4.  Bound by memory,
+// mostly writes: 16384 x 4096 bf16 to 4 experts each, 0.67 GB, 116 us in all, of which the sort about 7.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams p) {
   __shared__ uint32_t start[kMoeMaxExperts + 1];
@@ -512,9 +552,11 @@ __device__ __forceinline__ bool slot_row(int32_t pos, uint64_t n_rows, int32_t* 
 }
 
 // out[t] = sum over k, in order, of w[t][k] rows[pos[t][k]], in fp32.  A
-// thread has LOADS 16-byte pieces in flight before it adds the first (8; 4 where the rows lie off 16 bytes, each
-// then two loads): those of KU slots of LOADS / KU pieces of the output, kCombineThreads pieces apart.  More than 8
-// slots (LOOP) are added KU at a time.
+// thread has 8 16-byte pieces in flight before it adds the first (4 where the
+// rows lie off 16 bytes, each then two loads): those of KU slots of 8 / KU
+// pieces of the output, kCombineThreads pieces apart.  More than 8 slots
+// (LOOP) are added KU at a time.  Bound by memory: 16384 x 4096 bf16 from 4
+// slots each, 0.67 GB, 101 us, the measured copy's rate; one piece of 4 slots at a time 132.
 template <typename T, bool VEC, int KU, bool LOOP>
 __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_kernel(CombineParams p) {
   constexpr int V = kPieceOf<T>, kPieces = (VEC ? kCombineLoads : kCombineLoads / 2) / KU;
@@ -590,7 +632,8 @@ __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_
 
 // drows[pos] = w dout and dw = <dout, rows[pos]>: dout's row is read once for
 // four slots, each row once; the products are summed in registers over a
-// thread's pieces, then over the CTA (or the warp, for narrow rows).
+// thread's pieces, then over the CTA (or the warp, for narrow rows).  Bound by
+// memory: 16384 x 4096 bf16, 4 slots each, 1.21 GB, 181 us, the measured copy's rate.
 constexpr int kCombineBwdK = 4;
 
 template <typename T, bool VEC, bool WARP>
@@ -841,7 +884,8 @@ cudaError_t launch_combine_bwd(const CombineBwdParams& params, int dtype, bool v
                                const DeviceInfo& dev) {
   CombineBwdParams p = params;
   switch (dtype) {
-    case ZC_BF16: return vec ? combine_bwd<__nv_bfloat16, true>(p, stream, dev) : combine_bwd<__nv_bfloat16, false>(p, stream, dev);
+    case ZC_BF16:
+      return vec ? combine_bwd<__nv_bfloat16, true>(p, stream, dev) : combine_bwd<__nv_bfloat16, false>(p, stream, dev);
     case ZC_F16: return vec ? combine_bwd<__half, true>(p, stream, dev) : combine_bwd<__half, false>(p, stream, dev);
     default: return vec ? combine_bwd<float, true>(p, stream, dev) : combine_bwd<float, false>(p, stream, dev);
   }

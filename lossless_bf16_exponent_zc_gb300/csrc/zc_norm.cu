@@ -3,10 +3,12 @@
 //
 //   x' = a x + g * (y r(y) w),   h = x' r(x') w2,   r(z) = 1 / sqrt(mean(z^2) + eps)
 //
-// One pass: a row of y and x is read once into registers, both sums of
-// squares are taken there, and x' and the next block's input h are written.
-// h is the norm of x' before its rounding to the stored type, so each output
-// is rounded once.  Bound by memory: 4 values moved per 11 operations.
+// One pass: a row of y and x is read once, both sums of squares are taken on
+// chip, and x' and the next block's input h are written.  h is the norm of
+// x' before its rounding to the stored type, so each output is rounded once.
+// Bound by memory, 4 values moved per 11 operations: 16384 x 4096 bf16, 0.54
+// GB, 86 us, 94% of the measured copy's rate (with a CTA per row and no copies
+// ahead of it 133; with one barrier a row instead of two, as in the gradient, 93).
 #include "zc_norm.cuh"
 
 namespace zc {

@@ -142,6 +142,25 @@ def test_route_ties_and_special_values(moe):
     assert torch.equal(d[2], torch.zeros(6, device="cuda"))
 
 
+@pytest.mark.parametrize("experts", [8, 61, 256, 1000])
+@pytest.mark.parametrize("width", [0.001, 1.0, 30.0])
+@pytest.mark.parametrize("bias_scale", [None, 0.0, 0.05, 100.0])
+def test_route_chooses_as_a_stable_sort_of_the_fp32_scores(moe, experts, width, bias_scale):
+    """The choice is by sigmoid + bias rounded to fp32, however near the scores are."""
+    g = torch.Generator(device="cuda").manual_seed(experts)
+    logits = torch.randn((3000, experts), device="cuda", generator=g) * width
+    k = min(8, experts)
+    if bias_scale is None:
+        bias, scores = None, 1 / (1 + torch.exp(-logits))
+    else:
+        bias = torch.randn(experts, device="cuda", generator=g) * bias_scale
+        scores = 1 / (1 + torch.exp(-logits)) + bias
+    order = torch.sort(scores, dim=1, descending=True, stable=True).indices[:, :k]
+    w, e = moe.route(logits, k, score="sigmoid", bias=bias, renormalize=False)
+    assert torch.equal(e.long(), order)
+    assert torch.equal(w, (1 / (1 + torch.exp(-logits))).gather(1, order))
+
+
 @pytest.mark.parametrize("experts", [40, 64, 300, 1024])
 @pytest.mark.parametrize("k", [1, 8, 32])
 def test_route_many_equal_or_few_open(moe, experts, k):
