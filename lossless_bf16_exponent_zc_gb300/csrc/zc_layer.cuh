@@ -1,7 +1,6 @@
-// zc_layer.cuh -- device building blocks of the operators around an
-// expert-parallel layer (zc_moe.cu, zc_norm.cu): values of three types moved
-// in 16-byte pieces or one at a time, computed in fp32, and sums over a warp
-// or a CTA whose order is fixed (the same inputs give the same bits).
+// zc_layer.cuh -- device building blocks of the operators around an expert-parallel layer
+// (zc_moe.cu, zc_norm.cu): values of three types moved in 16-byte pieces or one at a time, computed
+// in fp32, and sums over a warp or a CTA whose order is fixed (the same inputs give the same bits).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -30,9 +29,8 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// V values of T as they lie in memory: one 16-byte piece (V = 16 / sizeof(T))
-// or a single value (V = 1, for widths, strides and addresses that 16 bytes
-// do not divide).
+// V values of T as they lie in memory: one 16-byte piece (V = 16 / sizeof(T)) or a single value (V
+// = 1, for widths, strides and addresses that 16 bytes do not divide).
 template <typename T, int V>
 struct Piece;
 
@@ -102,9 +100,10 @@ struct Piece<T, 8> {
 template <typename T>
 constexpr int kPieceOf = 16 / static_cast<int>(sizeof(T));
 
-// The 16 bytes at any address that T's alignment allows: the two aligned pieces that hold them, shifted together.  Each
-// of the two holds at least one of the values asked for, so nothing is read from where the caller's memory cannot be;
-// neighbouring threads ask for the same pieces, so the second comes from the L1 cache.
+// The 16 bytes at any address that T's alignment allows: the two aligned pieces that hold them,
+// shifted together.  Each of the two holds at least one of the values asked for, so nothing is read
+// from where the caller's memory cannot be; neighbouring threads ask for the same pieces, so the
+// second comes from the L1 cache.
 template <typename T>
 __device__ __forceinline__ Piece<T, kPieceOf<T>> load_any(const T* p) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
@@ -129,9 +128,10 @@ __device__ __forceinline__ Piece<T, kPieceOf<T>> load_any(const T* p) {
   return Piece<T, kPieceOf<T>>{make_uint4(w[0], w[1], w[2], w[3])};
 }
 
-// How a row of `width` values that is written at p falls into aligned 16-byte pieces: `head` values before the first
-// piece, `body` pieces, and the rest.  Work on the row is cut into units: the pieces, then the values outside them one by
-// one, so that no thread has several of those to take in turn; at most any_units(width) of them.
+// How a row of `width` values that is written at p falls into aligned 16-byte pieces: `head` values
+// before the first piece, `body` pieces, and the rest.  Work on the row is cut into units: the
+// pieces, then the values outside them one by one, so that no thread has several of those to take
+// in turn; at most any_units(width) of them.
 template <typename T>
 struct RowCut {
   uint32_t head, body;
@@ -168,8 +168,8 @@ __device__ __forceinline__ float warp_max_f32(float v) {
   return v;
 }
 
-// Thread-block clusters: the barrier of all threads of the cluster in its two halves (release, acquire), and a store to the
-// same variable in the shared memory of the cluster's CTA `cta`.
+// Thread-block clusters: the barrier of all threads of the cluster in its two halves (release,
+// acquire), and a store to the same variable in the shared memory of the cluster's CTA `cta`.
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -185,9 +185,8 @@ __device__ __forceinline__ void st_shared_of_cta(uint32_t* var, uint32_t cta, ui
       : "memory");
 }
 
-// Sums of N values over a CTA of whole warps, every thread getting all of
-// them.  `red` holds N x 32 floats; a caller that sums again before a
-// __syncthreads of its own passes another buffer.
+// Sums of N values over a CTA of whole warps, every thread getting all of them.  `red` holds N x 32
+// floats; a caller that sums again before a __syncthreads of its own passes another buffer.
 template <int N>
 __device__ __forceinline__ void block_sum_f32(float (&v)[N], float* red) {
   const uint32_t warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = lane_id();
@@ -202,15 +201,14 @@ __device__ __forceinline__ void block_sum_f32(float (&v)[N], float* red) {
   for (int i = 0; i < N; i++) v[i] = warp_sum_f32(lane < warps ? red[i * 32 + lane] : 0.f);
 }
 
-// As block_sum_f32 for 2 or 4 values with fewer shuffles.  Halving the
-// lanes' groups, every lane keeps half of the values and gives the others to its
-// partner, until the lanes of group g (of 32 / N lanes) hold value g; the
-// rest is a tree inside the group.  The CTA's partial sums are added the
-// same way.  `red`: N x kSumSlots floats, 16-byte aligned, those of absent warps zero
-// (the caller clears them all before the first use); as above, two sums in
-// a row need two buffers.  CLUSTER: over all `ctas` CTAs of the cluster, this one being `rank`; every CTA
-// leaves its partial sums in all of them (a sum of two barriers, the CTA's and the
-// cluster's, would wait twice).  kSumSlots: 16 warps each of up to 4 CTAs, or 32 of one.
+// As block_sum_f32 for 2 or 4 values with fewer shuffles.  Halving the lanes' groups, every lane
+// keeps half of the values and gives the others to its partner, until the lanes of group g (of 32 /
+// N lanes) hold value g; the rest is a tree inside the group.  The CTA's partial sums are added the
+// same way.  `red`: N x kSumSlots floats, 16-byte aligned, those of absent warps zero (the caller
+// clears them all before the first use); as above, two sums in a row need two buffers.  CLUSTER:
+// over all `ctas` CTAs of the cluster, this one being `rank`; every CTA leaves its partial sums in
+// all of them (a sum of two barriers, the CTA's and the cluster's, would wait twice).  kSumSlots:
+// 16 warps each of up to 4 CTAs, or 32 of one.
 constexpr int kSumSlots = 64;
 template <int N, bool CLUSTER = false>
 __device__ __forceinline__ void block_sum_shared(float (&v)[N], float* red, uint32_t rank = 0, uint32_t ctas = 1) {

@@ -1,11 +1,10 @@
-// zc_moe.cu -- the operators on both sides of an expert-parallel exchange:
-// choosing experts for every token, sorting tokens by expert into contiguous
-// pieces, bringing the experts' outputs back weighted, and their gradients.
-// Definitions in include/zc.h.
+// zc_moe.cu -- the operators on both sides of an expert-parallel exchange: choosing experts for
+// every token, sorting tokens by expert into contiguous pieces, bringing the experts' outputs back
+// weighted, and their gradients.  Definitions in include/zc.h.
 //
-// All but the router are bound by memory: each value is read or written once
-// and takes a few operations.  No result depends on the order of atomics
-// (counts are whole numbers) and every sum has a fixed order, so the same inputs give the same bits.
+// All but the router are bound by memory: each value is read or written once and takes a few
+// operations.  No result depends on the order of atomics (counts are whole numbers) and every sum
+// has a fixed order, so the same inputs give the same bits.
 #include "zc_internal.h"
 #include "zc_layer.cuh"
 
@@ -18,9 +17,9 @@ constexpr int kRouteWarps = 4;  // tokens per CTA, one warp each
 
 __device__ __forceinline__ uint32_t lanes_below() { return (1u << lane_id()) - 1u; }
 
-// Order-preserving image of a score: larger score, larger key.  NaN is above
-// everything, as a sort has it, so that it shows in the weights; both zeros
-// are equal.  Up to kClosed (minus infinity) an expert cannot be chosen.
+// Order-preserving image of a score: larger score, larger key.  NaN is above everything, as a sort
+// has it, so that it shows in the weights; both zeros are equal.  Up to kClosed (minus infinity) an
+// expert cannot be chosen.
 constexpr uint32_t kClosed = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t order_key(float f) {
   const int32_t b = __float_as_int(f + 0.f);
@@ -28,11 +27,12 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return f != f ? 0xFFFFFFFFu : key;
 }
 
-// 1 / (1 + exp(-l)), each step rounded as the plain expression's (a correctly rounded reciprocal is the quotient).
+// 1 / (1 + exp(-l)), each step rounded as the plain expression's (a correctly rounded reciprocal is
+// the quotient).
 __device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(__fadd_rn(1.f, expf(-l))); }
 
-// Lane l's N values of a row, N l .. N l + N - 1; minus infinity beyond the width.  VEC: they are whole 4-, 8- or 16-byte
-// pieces.
+// Lane l's N values of a row, N l .. N l + N - 1; minus infinity beyond the width.  VEC: they are
+// whole 4-, 8- or 16-byte pieces.
 template <typename T, int N, bool VEC>
 __device__ __forceinline__ void load_row(const T* row, uint32_t width, float (&v)[N]) {
   const uint32_t first = lane_id() * N;
@@ -81,20 +81,18 @@ __device__ __forceinline__ float choice_of(const RouteParams& p, float l, uint32
   return p.bias ? __fadd_rn(*prob, p.bias[e]) : *prob;
 }
 
-// One warp per token, every lane holding N experts next to one another.
-// The K-th largest of the lanes' best choices is a bound that at least K
-// experts reach and few more do: those are gathered in shared memory, a lane
-// each, and every lane counts the ones before its own.  Where more than 32
-// reach it (equal logits, or too few lanes left open) the largest is taken K
-// times instead, the lowest expert on ties.
-// For the bound a sigmoid is good enough to 2^-20 (the fast exponential's and
-// divide's stated errors make 2^-21 of a value in 0..1, the exact one's own 2^-22): with the bound lowered by twice
-// that and the sums' rounding, no expert that belongs among the K stays out, and
-// the exact sigmoid is taken of those gathered alone, one a lane.
-// Bound by instructions: 16384 x 256 fp32, 8 taken with a bias, 12.6 us (softmax 10.3), its
-// bytes 2.7.  With exact sigmoids of all experts it took 15.0; sorting each
-// lane's experts and taking the largest 8 times 16.5 (512 experts: 41 against
-// 23); warps that stay and load the next token ahead 18.3, for fewer of them fit an SM.
+// One warp per token, every lane holding N experts next to one another.  The K-th largest of the
+// lanes' best choices is a bound that at least K experts reach and few more do: those are gathered
+// in shared memory, a lane each, and every lane counts the ones before its own.  Where more than 32
+// reach it (equal logits, or too few lanes left open) the largest is taken K times instead, the
+// lowest expert on ties.  For the bound a sigmoid is good enough to 2^-20 (the fast exponential's
+// and divide's stated errors make 2^-21 of a value in 0..1, the exact one's own 2^-22): with the
+// bound lowered by twice that and the sums' rounding, no expert that belongs among the K stays out,
+// and the exact sigmoid is taken of those gathered alone, one a lane.  Bound by instructions: 16384
+// x 256 fp32, 8 taken with a bias, 12.6 us (softmax 10.3), its bytes 2.7.  With exact sigmoids of
+// all experts it took 15.0; sorting each lane's experts and taking the largest 8 times 16.5 (512
+// experts: 41 against 23); warps that stay and load the next token ahead 18.3, for fewer of them
+// fit an SM.
 template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) {
   __shared__ unsigned long long found[kRouteWarps][32];
@@ -222,11 +220,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
   }
 }
 
-// Gradient of the logits: G_k = scale dw_k for the chosen experts.  A
-// renormalised softmax and both sigmoid forms depend on the chosen logits
-// alone, so only those are read and every other gradient is zero; the plain
-// softmax needs the whole row.  The chosen experts' values meet the lanes that hold
-// those experts in a row of shared memory.
+// Gradient of the logits: G_k = scale dw_k for the chosen experts.  A renormalised softmax and both
+// sigmoid forms depend on the chosen logits alone, so only those are read and every other gradient
+// is zero; the plain softmax needs the whole row.  The chosen experts' values meet the lanes that
+// hold those experts in a row of shared memory.
 template <typename T, int N>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(RouteBwdParams p) {
   __shared__ float rows[kRouteWarps][32 * N];
@@ -356,11 +353,10 @@ __device__ __forceinline__ void block_exclusive_scan(uint32_t* a, uint32_t count
   __syncthreads();
 }
 
-// The stable counting sort of a call with many slots, first of three
-// launches.  A CTA takes a chunk of 1024 slots, each warp an eighth of it in
-// order: counts per warp and expert, their prefix over the warps,
-// and then every slot's place among its expert's in the chunk, 32 at a time
-// (its equals among the lanes below it).  positions[] holds that place until the rows are placed.
+// The stable counting sort of a call with many slots, first of three launches.  A CTA takes a chunk
+// of 1024 slots, each warp an eighth of it in order: counts per warp and expert, their prefix over
+// the warps, and then every slot's place among its expert's in the chunk, 32 at a time (its equals
+// among the lanes below it).  positions[] holds that place until the rows are placed.
 __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(DispatchParams p) {
   extern __shared__ uint32_t hist[];  // [kSortWarps][experts + 1]
   pdl_allow_dependents();
@@ -404,10 +400,11 @@ __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(DispatchParams 
   }
 }
 
-// Second: the exclusive prefix over the chunks of every expert, in place, a warp per expert, and from the totals the
-// experts' first rows.  One cluster: its CTAs leave their totals in the first one's shared memory, which adds them up
-// (256 experts, 64 chunks: 5.5 us by itself, in one CTA 13.5).  Letting every CTA of the third launch add up what its slots
-// need instead took longer: 131072 slots of 512 values 58 us against 41, and sorting in one cluster of 8 CTAs 55.
+// Second: the exclusive prefix over the chunks of every expert, in place, a warp per expert, and
+// from the totals the experts' first rows.  One cluster: its CTAs leave their totals in the first
+// one's shared memory, which adds them up (256 experts, 64 chunks: 5.5 us by itself, in one CTA
+// 13.5).  Letting every CTA of the third launch add up what its slots need instead took longer:
+// 131072 slots of 512 values 58 us against 41, and sorting in one cluster of 8 CTAs 55.
 constexpr uint32_t kPrefixCtas = 8;
 constexpr int kPrefixThreads = 1024;
 __global__ void __launch_bounds__(kPrefixThreads) __cluster_dims__(kPrefixCtas, 1, 1)
@@ -443,14 +440,13 @@ __global__ void __launch_bounds__(kPrefixThreads) __cluster_dims__(kPrefixCtas, 
   for (uint32_t e = threadIdx.x; e <= p.experts; e += kPrefixThreads) p.offsets[e] = static_cast<int32_t>(total[e]);
 }
 
-// Third, or alone: the row of every slot, and the rows themselves.  A CTA
-// places the slots of a few tokens, then reads each token once and writes its K
-// rows.  A slot's row is its expert's first + those in earlier chunks + its place in the chunk.  In a call with few
-// slots (`single`) the CTA counts all of them itself, those before its own
-// apart (two counts in a word), and ranks its own as above, so that the call
-// is one launch: with 8192 slots of 128 experts 9.9 us against 10.6 in three,
-// with 1024 3.1 against 8.3, with 16384 18.0 against 16.4.  Bound by memory,
-// mostly writes: 16384 x 4096 bf16 to 4 experts each, 0.67 GB, 116 us in all, of which the sort about 7.
+// Third, or alone: the row of every slot, and the rows themselves.  A CTA places the slots of a few
+// tokens, then reads each token once and writes its K rows.  A slot's row is its expert's first +
+// those in earlier chunks + its place in the chunk.  In a call with few slots (`single`) the CTA
+// counts all of them itself, those before its own apart (two counts in a word), and ranks its own
+// as above, so that the call is one launch: with 8192 slots of 128 experts 9.9 us against 10.6 in
+// three, with 1024 3.1 against 8.3, with 16384 18.0 against 16.4.  Bound by memory, mostly writes:
+// 16384 x 4096 bf16 to 4 experts each, 0.67 GB, 116 us in all, of which the sort about 7.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams p) {
   __shared__ uint32_t start[kMoeMaxExperts + 1];
@@ -541,9 +537,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams 
 constexpr int kCombineThreads = 256;
 constexpr int kCombineLoads = 8;  // pieces a thread has in flight
 
-// The row of a slot: true if it is routed.  `row` is the row to read (or,
-// unrouted, the one to clear, which the buffer need not hold); a routed row
-// outside the buffer is reported and skipped.
+// The row of a slot: true if it is routed.  `row` is the row to read (or, unrouted, the one to
+// clear, which the buffer need not hold); a routed row outside the buffer is reported and skipped.
 __device__ __forceinline__ bool slot_row(int32_t pos, uint64_t n_rows, int32_t* status, uint64_t* row, bool* inside) {
   *row = static_cast<uint64_t>(pos < 0 ? ~pos : pos);
   *inside = *row < n_rows;
@@ -551,12 +546,11 @@ __device__ __forceinline__ bool slot_row(int32_t pos, uint64_t n_rows, int32_t* 
   return *inside && pos >= 0;
 }
 
-// out[t] = sum over k, in order, of w[t][k] rows[pos[t][k]], in fp32.  A
-// thread has 8 16-byte pieces in flight before it adds the first (4 where the
-// rows lie off 16 bytes, each then two loads): those of KU slots of 8 / KU
-// pieces of the output, kCombineThreads pieces apart.  More than 8 slots
-// (LOOP) are added KU at a time.  Bound by memory: 16384 x 4096 bf16 from 4
-// slots each, 0.67 GB, 101 us, the measured copy's rate; one piece of 4 slots at a time 132.
+// out[t] = sum over k, in order, of w[t][k] rows[pos[t][k]], in fp32.  A thread has 8 16-byte
+// pieces in flight before it adds the first (4 where the rows lie off 16 bytes, each then two
+// loads): those of KU slots of 8 / KU pieces of the output, kCombineThreads pieces apart.  More
+// than 8 slots (LOOP) are added KU at a time.  Bound by memory: 16384 x 4096 bf16 from 4 slots
+// each, 0.67 GB, 101 us, the measured copy's rate; one piece of 4 slots at a time 132.
 template <typename T, bool VEC, int KU, bool LOOP>
 __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_kernel(CombineParams p) {
   constexpr int V = kPieceOf<T>, kPieces = (VEC ? kCombineLoads : kCombineLoads / 2) / KU;
@@ -630,10 +624,10 @@ __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_
   }
 }
 
-// drows[pos] = w dout and dw = <dout, rows[pos]>: dout's row is read once for
-// four slots, each row once; the products are summed in registers over a
-// thread's pieces, then over the CTA (or the warp, for narrow rows).  Bound by
-// memory: 16384 x 4096 bf16, 4 slots each, 1.21 GB, 181 us, the measured copy's rate.
+// drows[pos] = w dout and dw = <dout, rows[pos]>: dout's row is read once for four slots, each row
+// once; the products are summed in registers over a thread's pieces, then over the CTA (or the
+// warp, for narrow rows).  Bound by memory: 16384 x 4096 bf16, 4 slots each, 1.21 GB, 181 us, the
+// measured copy's rate.
 constexpr int kCombineBwdK = 4;
 
 template <typename T, bool VEC, bool WARP>
@@ -814,7 +808,8 @@ cudaError_t combine(CombineParams& p, cudaStream_t stream) {
 template <typename T, bool VEC>
 cudaError_t combine_bwd(CombineBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   const uint64_t pieces = VEC ? p.hidden / kPieceOf<T> : any_units<T>(p.hidden);
-  // Few tokens leave SMs idle: their slots, four at a time, then go to CTAs of their own, which hold a piece a thread.
+  // Few tokens leave SMs idle: their slots, four at a time, then go to CTAs of their own, which
+  // hold a piece a thread.
   const bool few = p.tokens < 2ull * static_cast<uint64_t>(dev.sm_count);
   const uint32_t split = few ? static_cast<uint32_t>(ceil_div(p.k, kCombineBwdK)) : 1;
   if (pieces <= 64)
@@ -857,8 +852,8 @@ cudaError_t launch_dispatch(const DispatchParams& params, int dtype, bool vec, c
     e = run(moe_prefix_kernel, kPrefixCtas, 1, kPrefixThreads, stream, &p);
     if (e != cudaSuccess) return e;
   }
-  // Tokens per CTA: few while the grid does not fill the GPU, up to
-  // kMoePlaceTokens once it does (the ranking is then shared by more rows).
+  // Tokens per CTA: few while the grid does not fill the GPU, up to kMoePlaceTokens once it does
+  // (the ranking is then shared by more rows).
   const uint64_t fill = 4ull * static_cast<uint64_t>(dev.sm_count);
   p.cta_tokens = static_cast<uint32_t>(p.tokens / fill);
   if (p.cta_tokens < 1) p.cta_tokens = 1;

@@ -1,14 +1,13 @@
-// zc_norm.cu -- the norms before and after a block, with the block's gate and
-// residual scale, forward (the gradient is in zc_norm_bwd.cu).
+// zc_norm.cu -- the norms before and after a block, with the block's gate and residual scale,
+// forward (the gradient is in zc_norm_bwd.cu).
 //
 //   x' = a x + g * (y r(y) w),   h = x' r(x') w2,   r(z) = 1 / sqrt(mean(z^2) + eps)
 //
-// One pass: a row of y and x is read once, both sums of squares are taken on
-// chip, and x' and the next block's input h are written.  h is the norm of
-// x' before its rounding to the stored type, so each output is rounded once.
-// Bound by memory, 4 values moved per 11 operations: 16384 x 4096 bf16, 0.54
-// GB, 86 us, 94% of the measured copy's rate (with a CTA per row and no copies
-// ahead of it 133; with one barrier a row instead of two, as in the gradient, 93).
+// One pass: a row of y and x is read once, both sums of squares are taken on chip, and x' and the
+// next block's input h are written.  h is the norm of x' before its rounding to the stored type, so
+// each output is rounded once.  Bound by memory, 4 values moved per 11 operations: 16384 x 4096
+// bf16, 0.54 GB, 86 us, 94% of the measured copy's rate (with a CTA per row and no copies ahead of
+// it 133; with one barrier a row instead of two, as in the gradient, 93).
 #include "zc_norm.cuh"
 
 namespace zc {
@@ -108,12 +107,14 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(NormParams p) {
   }
 }
 
-// Columns of a thread and stages of the ring: 8 columns, and 16 for rows that 8 of each of 512 threads do not hold.
+// Columns of a thread and stages of the ring: 8 columns, and 16 for rows that 8 of each of 512
+// threads do not hold.
 constexpr int kFwdCols = 8, kFwdWideCols = 16;
 template <int C>
 constexpr int kFwdStages = C == kFwdCols ? 4 : 3;
 
-// The ring shape: rows walker, walker + walkers, ... stream through the shared memory of a CTA or a cluster of two.
+// The ring shape: rows walker, walker + walkers, ... stream through the shared memory of a CTA or a
+// cluster of two.
 template <typename T, int V, int C, int CTAS, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_ring_kernel(NormParams p) {
   constexpr int P = C / 2, kStages = kFwdStages<C>;
@@ -251,8 +252,9 @@ bool run_ring(NormParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaErr
 template <typename T, int V>
 cudaError_t run_width(NormParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   const uint32_t d = p.hidden;
-  // A warp holds up to 512 values, in 16-byte pieces 1024 if the rows keep all SMs busy: then it beats the ring's four
-  // warps a row (65536 x 1024 bf16 93 us against 100), with few rows it is slower (8 x 1024 3.5 us against 2.2).
+  // A warp holds up to 512 values, in 16-byte pieces 1024 if the rows keep all SMs busy: then it
+  // beats the ring's four warps a row (65536 x 1024 bf16 93 us against 100), with few rows it is
+  // slower (8 x 1024 3.5 us against 2.2).
   constexpr int kWarp = kNormWarps * 32;
   if constexpr (V > 1) {
     if (d <= 256) return run_shape<T, V, 8 / V, true, kWarp>(p, kWarp, stream, dev);
@@ -265,8 +267,9 @@ cudaError_t run_width(NormParams& p, cudaStream_t stream, const DeviceInfo& dev)
   cudaError_t e;
   if (run_ring<T, V, kFwdCols, 1>(p, stream, dev, &e)) return e;
   if (run_ring<T, V, kFwdWideCols, 1>(p, stream, dev, &e)) return e;
-  // Wider still: in 16-byte pieces a CTA holds a row in registers (4096 x 16384 bf16 114 us; a cluster of two through the
-  // ring 152, its two cluster barriers a row wait too long), otherwise the cluster takes it.
+  // Wider still: in 16-byte pieces a CTA holds a row in registers (4096 x 16384 bf16 114 us; a
+  // cluster of two through the ring 152, its two cluster barriers a row wait too long), otherwise
+  // the cluster takes it.
   if constexpr (V > 1) {
     return run_shape<T, V, 16 / V, false, 1024>(p, static_cast<int>((d + 511) / 512 * 32), stream, dev);
   } else {

@@ -8,8 +8,8 @@
 
 namespace zc {
 
-// V parameters (norm weights or a gate row) from column `col` on: in the
-// values' type, or in fp32 next to 16-bit values.
+// V parameters (norm weights or a gate row) from column `col` on: in the values' type, or in fp32
+// next to 16-bit values.
 template <typename T, int V>
 __device__ __forceinline__ void load_params(const void* base, int is_f32, uint64_t col, float (&f)[V]) {
   if (sizeof(T) == 4 || !is_f32) {
@@ -58,17 +58,19 @@ __device__ __forceinline__ void store_f32(float* p, const float (&f)[V]) {
   }
 }
 
-// Launch shapes.  A narrow row is held by a warp.  Wider rows stream through a CTA's shared
-// memory, one thread for every 8 or 16 columns, the widest through a cluster's or, in the forward pass, a CTA's registers.
+// Launch shapes.  A narrow row is held by a warp.  Wider rows stream through a CTA's shared memory,
+// one thread for every 8 or 16 columns, the widest through a cluster's or, in the forward pass, a
+// CTA's registers.
 constexpr int kNormWarps = 8;  // rows of a CTA in the warp shape
 constexpr int kNormRingThreads = 512;
 constexpr int kNormRingSmem = 225 * 1024;  // what the ring may take of the 227 KB a CTA can have
 
-// The ring: the next STAGES rows of ARRAYS matrices, copied asynchronously (16 bytes at a time; 4 where the rows are not
-// so aligned) by the threads of the CTA.  Every thread keeps the same COLS columns in every row, in NV pieces of V
-// values: its pieces lie in slots of its own, so shared memory is read without bank conflicts and a thread waits for
-// nobody's copies but its own.  Rows of 16-bit values at odd addresses (kWords) are copied as the 4-byte words
-// that cover them and read value by value, by other threads than copied them; their first and last word may hold a
+// The ring: the next STAGES rows of ARRAYS matrices, copied asynchronously (16 bytes at a time; 4
+// where the rows are not so aligned) by the threads of the CTA.  Every thread keeps the same COLS
+// columns in every row, in NV pieces of V values: its pieces lie in slots of its own, so shared
+// memory is read without bank conflicts and a thread waits for nobody's copies but its own.  Rows
+// of 16-bit values at odd addresses (kWords) are copied as the 4-byte words that cover them and
+// read value by value, by other threads than copied them; their first and last word may hold a
 // neighbour's value, which is not used.
 template <typename T, int V, int COLS, int ARRAYS, int STAGES>
 struct RowRing {
@@ -110,8 +112,8 @@ struct RowRing {
       }
     }
   }
-  // Zeroes this thread's slots that no copy ever fills (its columns beyond the width, and all of a matrix that
-  // is not there), so that reading them needs no test.
+  // Zeroes this thread's slots that no copy ever fills (its columns beyond the width, and all of a
+  // matrix that is not there), so that reading them needs no test.
   __device__ __forceinline__ void clear(int array, bool all) const {
     if constexpr (!kWords) {
       for (int stage = 0; stage < STAGES; stage++)
@@ -122,7 +124,8 @@ struct RowRing {
         }
     }
   }
-  // This thread's columns of a row (its address as given to copy()) as they lie in memory; zeros beyond the width.
+  // This thread's columns of a row (its address as given to copy()) as they lie in memory; zeros
+  // beyond the width.
   __device__ __forceinline__ void get(int stage, int array, const T* row, Piece<T, V> (&v)[NV]) const {
     const uint8_t* from = at(stage, array) + (kWords ? reinterpret_cast<uintptr_t>(row) & 2 : 0);
 #pragma unroll
@@ -185,17 +188,13 @@ struct RowRing {
   }
 };
 
+// Two fp32 operations of one instruction each.
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
-#ifdef ZC_SCALAR
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
-#else
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-#endif
 
-// CTAs of a ring kernel (clusters of them) that the GPU holds, by CTA size (the ring's size follows from it); looked up
-// once per device, size and cluster.
+// CTAs of a ring kernel (clusters of them) that the GPU holds, by CTA size (the ring's size follows
+// from it); looked up once per device, size and cluster.
 struct RingPrep {
   std::atomic<int> fit[kMaxDevices][kNormRingThreads / 32 + 1];
 };

@@ -6,14 +6,13 @@
 //   dy  = r(y) (v - n mean(v n))
 // and over the rows  dw2 = sum dh n2,  dw = sum G g n,  dg = sum G n w.
 //
-// One pass over the data: a row's four inputs are read once, r(y) and r(x')
-// are taken again from them instead of being saved, and a thread adds up the
-// column sums of its own columns in registers over all rows of its walker.
-// (The weight's and the gate's gradient share the sum of G n while the gate row
-// stays the same.)  Every walker then writes its sums to the workspace and a
-// second, small kernel adds them in order, so no result depends on timing.
-// Bound by memory: 16384 x 4096 bf16, 0.81 GB, 125 us, 97% of the measured
-// copy's rate; rows off 16 bytes by the instructions that take them value by value (16384 x 4095 bf16 284 us).
+// One pass over the data: a row's four inputs are read once, r(y) and r(x') are taken again from
+// them instead of being saved, and a thread adds up the column sums of its own columns in registers
+// over all rows of its walker. (The weight's and the gate's gradient share the sum of G n while the
+// gate row stays the same.)  Every walker then writes its sums to the workspace and a second, small
+// kernel adds them in order, so no result depends on timing.  Bound by memory: 16384 x 4096 bf16,
+// 0.81 GB, 125 us, 97% of the measured copy's rate; rows off 16 bytes by the instructions that take
+// them value by value (16384 x 4095 bf16 284 us).
 #include "zc_norm.cuh"
 
 namespace zc {
@@ -27,15 +26,16 @@ __host__ __device__ constexpr uint32_t norm_max_units(uint32_t hidden) {
 }
 constexpr int kBwdStages = 3;
 
-// Columns of a thread in the ring shape: 8, and 16 for 16-bit rows that 8 of each of 512 threads do not hold; still wider
-// rows are shared by a cluster of 2 or 4 CTAs.  With 8 the
-// column sums, the weights and a row fit the 128 registers of a 512-thread CTA; 16 columns in 256 threads, two CTAs an
-// SM, spill registers and take 170 us instead of 130 (16384 x 4096 bf16), and 8 in 64 registers, again for two CTAs,
-// 238 us: the ring leaves the L1 cache too small for spilled registers.
+// Columns of a thread in the ring shape: 8, and 16 for 16-bit rows that 8 of each of 512 threads do
+// not hold; still wider rows are shared by a cluster of 2 or 4 CTAs.  With 8 the column sums, the
+// weights and a row fit the 128 registers of a 512-thread CTA; 16 columns in 256 threads, two CTAs
+// an SM, spill registers and take 170 us instead of 130 (16384 x 4096 bf16), and 8 in 64 registers,
+// again for two CTAs, 238 us: the ring leaves the L1 cache too small for spilled registers.
 constexpr int kBwdCols = 8, kBwdWideCols = 16;
 
-// Rows of a walker (a CTA; a warp in the warp shape), unit after unit: u = its number, number + walkers, ...  A unit takes every splits-th row of a gate
-// row's tokens, so that neighbouring walkers read neighbouring rows at about the same time.
+// Rows of a walker (a CTA; a warp in the warp shape), unit after unit: u = its number, number +
+// walkers, ...  A unit takes every splits-th row of a gate row's tokens, so that neighbouring
+// walkers read neighbouring rows at about the same time.
 struct BwdWalk {
   uint32_t u;
   uint64_t t, last;
@@ -56,10 +56,11 @@ struct BwdWalk {
   }
 };
 
-// The ring shape.  A row takes two sums over the CTA, of x'^2, u x' and y^2 and then, once G is known, of v y.  The
-// second is taken together with the next row's first, so that a row costs one barrier: between two barriers the CTA
-// writes the last row's dy, takes this row's G, dx, column sums and v y, and the next row's first sums.  The inputs are
-// read from the stage twice rather than held, so that the column sums and the weights stay in registers.
+// The ring shape.  A row takes two sums over the CTA, of x'^2, u x' and y^2 and then, once G is
+// known, of v y.  The second is taken together with the next row's first, so that a row costs one
+// barrier: between two barriers the CTA writes the last row's dy, takes this row's G, dx, column
+// sums and v y, and the next row's first sums.  The inputs are read from the stage twice rather
+// than held, so that the column sums and the weights stay in registers.
 template <typename T, int V, int C, bool CLUSTER, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(NormBwdParams p) {
   constexpr int P = C / 2;
@@ -127,8 +128,9 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
 #pragma unroll
   for (int s = 0; s < kBwdStages; s++) issue(s);
 
-  // w2, and g w of the unit's gate row (w alone under a one-column gate); the sums of dh n2, and of G n over the
-  // unit, which give the weight's gradient times g and the gate's times w when the unit ends.
+  // w2, and g w of the unit's gate row (w alone under a one-column gate); the sums of dh n2, and of
+  // G n over the unit, which give the weight's gradient times g and the gate's times w when the
+  // unit ends.
   float2 w2[P], gw[P], sum_n[P], sum_b[P];
   if (NEXT) ring.params(p.next_weight, p.params_f32, 0, w2);
   auto open_unit = [&](uint32_t u) {
@@ -207,11 +209,11 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
     }
   };
 
-  // Between barriers: `t` is the row whose first sums are known; v (in g), y and the scalars of the row before wait for
-  // their last sum.
+  // Between barriers: `t` is the row whose first sums are known; v (in g), y and the scalars of the
+  // row before wait for their last sum.
   float2 g[P];
-  // With few columns a thread holds the row's y and refills the stage at once; with many the registers do not allow
-  // it, y is read again from its stage, and that is refilled after it.
+  // With few columns a thread holds the row's y and refills the stage at once; with many the
+  // registers do not allow it, y is read again from its stage, and that is refilled after it.
   constexpr bool kHold = C <= kBwdCols;
   Piece<T, V> y_row[kHold ? Ring::NV : 1];
   int y_stage = 0;
@@ -331,8 +333,8 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
   }
 }
 
-// The warp shape: every warp walks rows of its own, the next one's loads under way while it computes; a CTA adds its
-// warps' sums of the weights' gradients at the end.
+// The warp shape: every warp walks rows of its own, the next one's loads under way while it
+// computes; a CTA adds its warps' sums of the weights' gradients at the end.
 template <typename T, int V, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kNormWarps * 32, 2) norm_bwd_warp_kernel(NormBwdParams p) {
   constexpr int C = 8, P = C / 2;
@@ -510,8 +512,9 @@ __global__ void __launch_bounds__(kNormWarps * 32, 2) norm_bwd_warp_kernel(NormB
   if (NEXT) flush(sum_n, mine + p.hidden);
 }
 
-// Adds the CTAs' sums, in order: the warps take a share of the parts each, a lane a column, and then half a warp, or a
-// warp, adds a column's shares.  blockIdx.y: 0 the branch weight's gradient, 1 the next weight's, 2 + g gate row g's.
+// Adds the CTAs' sums, in order: the warps take a share of the parts each, a lane a column, and
+// then half a warp, or a warp, adds a column's shares.  blockIdx.y: 0 the branch weight's gradient,
+// 1 the next weight's, 2 + g gate row g's.
 template <typename T, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) norm_parts_kernel(NormBwdParams p) {
   __shared__ float sums[WARPS][33];
@@ -554,8 +557,7 @@ __global__ void __launch_bounds__(WARPS * 32) norm_parts_kernel(NormBwdParams p)
     static_cast<T*>(dst)[blockIdx.x * 32 + mine] = from_f32<T>(s);
 }
 
-// A one-column gate's gradient where several tokens share a gate value: one
-// CTA per value.
+// A one-column gate's gradient where several tokens share a gate value: one CTA per value.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_narrow_gate_kernel(NormBwdParams p) {
   __shared__ float red[32];
@@ -572,8 +574,9 @@ __global__ void __launch_bounds__(256) norm_narrow_gate_kernel(NormBwdParams p) 
     static_cast<T*>(p.dgate)[blockIdx.x] = from_f32<T>(s[0]);
 }
 
-// Cuts the rows into ranges for at most `most` walkers, `per_cta` of them in a CTA or each a cluster of p.cluster CTAs (a
-// range lies in one gate row's tokens), launches `fn` and adds up what it left.
+// Cuts the rows into ranges for at most `most` walkers, `per_cta` of them in a CTA or each a
+// cluster of p.cluster CTAs (a range lies in one gate row's tokens), launches `fn` and adds up what
+// it left.
 template <typename T>
 cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint32_t per_cta, int threads, int smem,
                           cudaStream_t stream, const DeviceInfo& dev) {
@@ -594,8 +597,8 @@ cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint3
   if (p.ctas) e = launch_kernel(fn, dim3(p.ctas * p.cluster), dim3(threads), smem, stream, args, false, p.cluster);
   if (e != cudaSuccess) return e;
   const uint32_t jobs = 2 + (wide && splits != 1 ? static_cast<uint32_t>(groups) : 0u);
-  // 32 warps a CTA while the GPU holds all such CTAs at once, two an SM (4452 x 704 fp32 18.1 us in all against 22.9
-  // with 16); beyond that 16, four an SM (512 x 4096 bf16 10.8 against 13.0).
+  // 32 warps a CTA while the GPU holds all such CTAs at once, two an SM (4452 x 704 fp32 18.1 us in
+  // all against 22.9 with 16); beyond that 16, four an SM (512 x 4096 bf16 10.8 against 13.0).
   const dim3 parts((p.hidden + 31) / 32, jobs);
   if (static_cast<uint64_t>(parts.x) * parts.y <= 2ull * static_cast<uint64_t>(dev.sm_count))
     e = launch_kernel(reinterpret_cast<const void*>(norm_parts_kernel<T, 32>), parts, dim3(1024), 0, stream, args, false);

@@ -1,14 +1,12 @@
-// zc_torch.cpp -- Python entry points of the operators around an
-// expert-parallel exchange (moe.py, norm.py): torch tensors in, checked,
-// outputs allocated by torch, and one call of the C ABI (include/zc.h) on the
-// current torch stream.  Argument marshalling only, as zc.py does with ctypes;
-// native because these operators run for a few microseconds in a decoding
-// step, where five allocations, a dozen attributes and a ctypes call in
-// Python cost more than the kernels (route of 8 tokens: 9.5 us of host time in
-// Python).
+// zc_torch.cpp -- Python entry points of the operators around an expert-parallel exchange (moe.py,
+// norm.py): torch tensors in, checked, outputs allocated by torch, and one call of the C ABI
+// (include/zc.h) on the current torch stream.  Argument marshalling only, as zc.py does with
+// ctypes; native because these operators run for a few microseconds in a decoding step, where five
+// allocations, a dozen attributes and a ctypes call in Python cost more than the kernels (route of
+// 8 tokens: 9.5 us of host time in Python).
 //
-// Errors: a wrong tensor raises ValueError, an error of the C ABI zc.ZcError,
-// torch's own errors (out of memory) as torch raises them.
+// Errors: a wrong tensor raises ValueError, an error of the C ABI zc.ZcError, torch's own errors
+// (out of memory) as torch raises them.
 #include <Python.h>
 
 #include <ATen/core/LegacyTypeDispatch.h>
@@ -343,7 +341,8 @@ void norm_params(A& a, const Tensor& x, PyObject* weight, PyObject* gate, PyObje
   a.params_f32 = kind == at::kFloat && x.scalar_type() != at::kFloat;
 }
 
-// (y or None, x, weight, gate, residual_scale, next_weight, eps, x_new, h, stream) -> (x_new or None, h or None)
+// (y or None, x, weight, gate, residual_scale, next_weight, eps, x_new, h, stream) -> (x_new or
+// None, h or None)
 PyObject* norm_forward(Args a) {
   zc_norm_args n = {};
   const bool branch = a[0] != Py_None;
@@ -369,8 +368,8 @@ PyObject* norm_forward(Args a) {
   return pack({x_new, h});
 }
 
-// (dx_new, dh, y, x_new, weight, gate, residual_scale, next_weight, eps, ws, stream; any of the first four may be None)
-// -> (dy, dx, dweight, dgate, dnext_weight)
+// (dx_new, dh, y, x_new, weight, gate, residual_scale, next_weight, eps, ws, stream; any of the
+// first four may be None) -> (dy, dx, dweight, dgate, dnext_weight)
 PyObject* norm_backward(Args a) {
   zc_norm_backward_args n = {};
   const bool branch = a[2] != Py_None;
