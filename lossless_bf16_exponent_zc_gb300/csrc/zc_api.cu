@@ -689,7 +689,9 @@ zc_status zc_moe_combine(const void* d_rows, int dtype, uint64_t rows_stride, ui
     return ZC_ERR_ALIGNMENT;
   CombineParams p = {d_rows, rows_stride, n_rows, tokens, d_weights, d_positions, d_out, d_status, hidden, k};
   const bool vec = in_pieces(d_rows, rows_stride, hidden, size) && aligned(d_out, 16);
-  return cuda_status(launch_combine(p, dtype, vec, as_stream(stream)));
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;
+  return cuda_status(launch_combine(p, dtype, vec, as_stream(stream), dev));
 }
 
 zc_status zc_moe_combine_backward(const void* d_dout, int dtype, uint64_t dout_stride, const void* d_rows,

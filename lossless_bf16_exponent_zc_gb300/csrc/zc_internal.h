@@ -112,7 +112,7 @@ constexpr uint32_t kMoeMaxExperts = ZC_MOE_MAX_EXPERTS;
 constexpr uint32_t kMoeMaxK = ZC_MOE_MAX_K;
 constexpr uint32_t kMoePlaceTokens = 8;    // most tokens one CTA of the dispatch places
 constexpr uint32_t kMoeChunkSlots = 1024;   // slots of a counting chunk
-constexpr uint64_t kMoeSingleSlots = 8192;  // up to here every CTA of a dispatch counts all slots itself
+constexpr uint64_t kMoeSingleSlots = 2048;  // up to here (half with k < 4) every CTA of a dispatch counts all slots
 
 struct RouteParams {
   const void* logits;
@@ -147,7 +147,7 @@ struct DispatchParams {
   int32_t *positions, *slots, *offsets;
   uint32_t* counts;  // workspace: [experts + 1][chunks]
   uint32_t chunks, cta_tokens;  // set by the launch
-  int single;
+  int single, few_counts;
 };
 uint64_t moe_workspace_bytes(uint64_t tokens, uint32_t k, uint32_t experts);
 cudaError_t launch_dispatch(const DispatchParams& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev);
@@ -171,7 +171,7 @@ struct CombineBwdParams {
   int32_t* status;
   uint32_t hidden, k;
 };
-cudaError_t launch_combine(const CombineParams& p, int dtype, bool vec, cudaStream_t stream);
+cudaError_t launch_combine(const CombineParams& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev);
 cudaError_t launch_combine_bwd(const CombineBwdParams& p, int dtype, bool vec, cudaStream_t stream,
                                const DeviceInfo& dev);
 

@@ -100,18 +100,12 @@ struct Piece<T, 8> {
 template <typename T>
 constexpr int kPieceOf = 16 / static_cast<int>(sizeof(T));
 
-// The 16 bytes at any address that T's alignment allows: the two aligned pieces that hold them,
-// shifted together.  Each of the two holds at least one of the values asked for, so nothing is read
-// from where the caller's memory cannot be; neighbouring threads ask for the same pieces, so the
-// second comes from the L1 cache.
+// The 16 bytes from byte `off` (0 .. 15, a multiple of T's size) of two neighbouring pieces on: values
+// at any address are read as the aligned pieces that hold them, shifted together.  A piece that holds
+// at least one value of the caller's is never where its memory cannot be; neighbouring threads ask
+// for the same pieces, so the second comes from the L1 cache.
 template <typename T>
-__device__ __forceinline__ Piece<T, kPieceOf<T>> load_any(const T* p) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  const uint32_t off = static_cast<uint32_t>(a & 15);
-  const uint4* at = reinterpret_cast<const uint4*>(a & ~static_cast<uintptr_t>(15));
-  const uint4 lo = at[0];
-  uint4 hi = lo;
-  if (off) hi = at[1];
+__device__ __forceinline__ uint4 shift_pieces(uint4 lo, uint4 hi, uint32_t off) {
   uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   if (off & 8) {
 #pragma unroll
@@ -125,7 +119,20 @@ __device__ __forceinline__ Piece<T, kPieceOf<T>> load_any(const T* p) {
 #pragma unroll
     for (int i = 0; i < 4; i++) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
   }
-  return Piece<T, kPieceOf<T>>{make_uint4(w[0], w[1], w[2], w[3])};
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Pairs of neighbouring pieces that a row of `width` values can touch wherever it starts, the first
+// with nothing before its second.
+template <typename T>
+__host__ __device__ constexpr uint32_t any_pairs(uint32_t width) {
+  return (width + 2 * (kPieceOf<T> - 1)) / kPieceOf<T> + 1;
+}
+
+// True if the kPieceOf<T> values from `first` (taken modulo 2^32) on all lie in a row of `width`.
+template <typename T>
+__device__ __forceinline__ bool whole_piece(uint32_t first, uint32_t width) {
+  return width >= kPieceOf<T> && first <= width - kPieceOf<T>;
 }
 
 // How a row of `width` values that is written at p falls into aligned 16-byte pieces: `head` values

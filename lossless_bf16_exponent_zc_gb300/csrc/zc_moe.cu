@@ -372,10 +372,15 @@ __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(DispatchParams 
   for (uint32_t i = 0; i < kTurns; i++) key[i] = base + i * 32 < n ? slot_key(p, first + base + i * 32) : kFull;
   uint32_t* own = hist + warp * e1;
   for (uint32_t e = lane; e < e1; e += 32) own[e] = 0;
+  const int bits = key_bits(p.experts);
+  uint32_t equal[kTurns];
   __syncwarp();
 #pragma unroll
-  for (uint32_t i = 0; i < kTurns; i++)
-    if (key[i] != kFull) atomicAdd(&own[key[i]], 1u);
+  for (uint32_t i = 0; i < kTurns; i++) {
+    equal[i] = equal_lanes(key[i], bits);
+    if (key[i] != kFull && (equal[i] & lanes_below()) == 0) own[key[i]] += __popc(equal[i]);
+    __syncwarp();
+  }
   __syncthreads();
   for (uint32_t e = threadIdx.x; e < e1; e += kSortThreads) {
     uint32_t sum = 0;
@@ -388,22 +393,20 @@ __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(DispatchParams 
     p.counts[static_cast<uint64_t>(e) * p.chunks + blockIdx.x] = sum;
   }
   __syncthreads();
-  const int bits = key_bits(p.experts);
 #pragma unroll
   for (uint32_t i = 0; i < kTurns; i++) {
-    const uint32_t equal = equal_lanes(key[i], bits);
-    if (key[i] != kFull)
-      p.positions[first + base + i * 32] = static_cast<int32_t>(own[key[i]] + __popc(equal & lanes_below()));
+    const uint32_t below = equal[i] & lanes_below();
+    if (key[i] != kFull) p.positions[first + base + i * 32] = static_cast<int32_t>(own[key[i]] + __popc(below));
     __syncwarp();
-    if (key[i] != kFull && (equal & lanes_below()) == 0) own[key[i]] += __popc(equal);
+    if (key[i] != kFull && below == 0) own[key[i]] += __popc(equal[i]);
     __syncwarp();
   }
 }
 
-// Second: the exclusive prefix over the chunks of every expert, in place, a warp per expert, and
+// With many counts: the exclusive prefix over the chunks of every expert, in place, a warp per expert, and
 // from the totals the experts' first rows.  One cluster: its CTAs leave their totals in the first
 // one's shared memory, which adds them up (256 experts, 64 chunks: 5.5 us by itself, in one CTA
-// 13.5).  Letting every CTA of the third launch add up what its slots need instead took longer:
+// 13.5).  Letting every CTA of the last launch add up what its slots need instead took longer:
 // 131072 slots of 512 values 58 us against 41, and sorting in one cluster of 8 CTAs 55.
 constexpr uint32_t kPrefixCtas = 8;
 constexpr int kPrefixThreads = 1024;
@@ -440,19 +443,33 @@ __global__ void __launch_bounds__(kPrefixThreads) __cluster_dims__(kPrefixCtas, 
   for (uint32_t e = threadIdx.x; e <= p.experts; e += kPrefixThreads) p.offsets[e] = static_cast<int32_t>(total[e]);
 }
 
-// Third, or alone: the row of every slot, and the rows themselves.  A CTA places the slots of a few
-// tokens, then reads each token once and writes its K rows.  A slot's row is its expert's first +
-// those in earlier chunks + its place in the chunk.  In a call with few slots (`single`) the CTA
-// counts all of them itself, those before its own apart (two counts in a word), and ranks its own
-// as above, so that the call is one launch: with 8192 slots of 128 experts 9.9 us against 10.6 in
-// three, with 1024 3.1 against 8.3, with 16384 18.0 against 16.4.  Bound by memory, mostly writes:
-// 16384 x 4096 bf16 to 4 experts each, 0.67 GB, 116 us in all, of which the sort about 7.
+// Last: the row of every slot, and the rows themselves.  A CTA places the slots of a few tokens,
+// then reads each token once and writes its K rows.  A slot's row is its expert's first + those in
+// earlier chunks + its place in the chunk.  Where there are few counts (`few_counts`) the CTA adds
+// them up itself and the launch of the prefix falls away: 4096 slots of 128 experts 6.7 us against
+// 7.8, 12288 8.3 against 9.4; 16384 of 128, 2064 counts, 12.4 against 10.5.  With few slots
+// (`single`) it counts all of them itself, those before its own apart (two counts in a word), and
+// ranks its own by ballots, so that the call is one launch: 1024 slots 3.2 us against 5.2 in two,
+// 2048 4.2 against 5.6, 4096 7.3 against 6.6.  Slots of the same token never meet in a bin of this
+// count, with fewer than four a token more lanes may: 2048 skewed slots, one a token, 10.4 against
+// 7.6.  (Clusters of 8 CTAs that share this count: 4096 slots 8.2, 8192 9.8.)  Bound by memory,
+// mostly writes: 16384 x 4096 bf16 to 4 experts each, 0.67 GB, 115 us in all, of which the sort
+// about 7.  Rows off 16 bytes are read once, in pairs of pieces, and shifted for every slot: 16384 x
+// 4095 131 us; with a read for every slot, cut at that row's own pieces, 174.
+// Where a slot's row goes.  A token's row is read in its own aligned pieces; off bytes into every
+// pair of neighbours lie the 16 bytes of an aligned piece of the row to write.
+struct PlaceRow {
+  uint64_t at;   // address of the piece that pair 0 holds
+  uint32_t off;  // 0 .. 15
+  uint32_t routed;
+};
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams p) {
   __shared__ uint32_t start[kMoeMaxExperts + 1];
   __shared__ uint32_t before[kMoeMaxExperts + 1];
   __shared__ uint32_t warp_totals[kSortWarps];
-  __shared__ int32_t own_pos[kMoePlaceTokens * kMoeMaxK];
+  __shared__ PlaceRow own_row[kMoePlaceTokens * kMoeMaxK];
   pdl_allow_dependents();
   const uint32_t lane = lane_id();
   pdl_wait();
@@ -460,13 +477,31 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams 
   const uint32_t nt = static_cast<uint32_t>(min(static_cast<uint64_t>(p.cta_tokens), p.tokens - min(p.tokens, t0)));
   const uint64_t s0 = t0 * p.k;
   const uint32_t own = nt * p.k;
+  auto token = [&](uint32_t t) { return static_cast<const T*>(p.x) + (t0 + t) * p.stride; };
+  // Row r is that of the CTA's slot i.
+  auto place = [&](uint32_t i, uint32_t r, bool routed) {
+    const int32_t pos = routed ? static_cast<int32_t>(r) : ~static_cast<int32_t>(r);
+    const uint64_t dst = reinterpret_cast<uint64_t>(static_cast<T*>(p.rows) + static_cast<uint64_t>(r) * p.hidden);
+    const uint32_t lead = VEC ? 0 : reinterpret_cast<uintptr_t>(token(i / p.k)) & 15;
+    const uint32_t off = VEC ? 0 : (lead - static_cast<uint32_t>(dst)) & 15;
+    own_row[i] = PlaceRow{dst - lead + off, off, routed};
+    p.positions[s0 + i] = pos;
+    p.slots[r] = static_cast<int32_t>(s0 + i);
+  };
   if (p.single) {
     const uint32_t all = static_cast<uint32_t>(p.tokens) * p.k, mine = static_cast<uint32_t>(s0);
     for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads) start[e] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (uint32_t i = threadIdx.x; i < all; i += kSortThreads)
-      atomicAdd(&start[slot_key(p, i)], i < mine ? 0x10001u : 1u);
+    constexpr uint32_t kTurns = 8;  // keys on their way at once
+    for (uint32_t i = threadIdx.x; i < all; i += kTurns * kSortThreads) {
+      uint32_t key[kTurns];
+#pragma unroll
+      for (uint32_t q = 0; q < kTurns; q++)
+        key[q] = i + q * kSortThreads < all ? slot_key(p, i + q * kSortThreads) : kFull;
+#pragma unroll
+      for (uint32_t q = 0; q < kTurns; q++)
+        if (key[q] != kFull) atomicAdd(&start[key[q]], i + q * kSortThreads < mine ? 0x10001u : 1u);
+    }
     __syncthreads();
     for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads) {
       before[e] = start[e] >> 16;
@@ -487,47 +522,71 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams 
         if (e != kFull && (equal & lanes_below()) == 0) before[e] += __popc(equal);
         __syncwarp();
         if (e == kFull) continue;
-        const int32_t pos = e < p.experts ? static_cast<int32_t>(r) : ~static_cast<int32_t>(r);
-        own_pos[i] = pos;
-        p.positions[s0 + i] = pos;
-        p.slots[r] = static_cast<int32_t>(s0 + i);
+        place(i, r, e < p.experts);
       }
     }
   } else {
+    if (p.few_counts) {
+      for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads) {
+        uint32_t sum = 0;
+#pragma unroll 8
+        for (uint32_t c = 0; c < p.chunks; c++) sum += p.counts[e * p.chunks + c];
+        start[e] = sum;
+      }
+      __syncthreads();
+      block_exclusive_scan(start, p.experts + 1, warp_totals);
+      if (blockIdx.x == 0)
+        for (uint32_t e = threadIdx.x; e <= p.experts; e += kSortThreads) p.offsets[e] = static_cast<int32_t>(start[e]);
+    }
     for (uint32_t i = threadIdx.x; i < own; i += kSortThreads) {
       const uint32_t e = slot_key(p, s0 + i), chunk = static_cast<uint32_t>((s0 + i) / kMoeChunkSlots);
-      const uint32_t r = static_cast<uint32_t>(p.offsets[e]) + p.counts[static_cast<uint64_t>(e) * p.chunks + chunk] +
-                         static_cast<uint32_t>(p.positions[s0 + i]);
-      const int32_t pos = e < p.experts ? static_cast<int32_t>(r) : ~static_cast<int32_t>(r);
-      own_pos[i] = pos;
-      p.positions[s0 + i] = pos;
-      p.slots[r] = static_cast<int32_t>(s0 + i);
+      const uint32_t* counts = p.counts + static_cast<uint64_t>(e) * p.chunks;
+      uint32_t r = static_cast<uint32_t>(p.positions[s0 + i]);
+      if (p.few_counts) {
+        r += start[e];
+#pragma unroll 8
+        for (uint32_t c = 0; c < chunk; c++) r += counts[c];
+      } else {
+        r += static_cast<uint32_t>(p.offsets[e]) + counts[chunk];
+      }
+      place(i, r, e < p.experts);
     }
   }
   __syncthreads();
-  constexpr int V = kPieceOf<T>;
-  const uint32_t pieces = VEC ? p.hidden / V : any_units<T>(p.hidden);
+  constexpr uint32_t V = kPieceOf<T>;
+  const uint32_t pieces = VEC ? p.hidden / V : any_pairs<T>(p.hidden);
   const uint64_t all = static_cast<uint64_t>(nt) * pieces;
 #pragma unroll 2
   for (uint64_t i = threadIdx.x; i < all; i += kSortThreads) {
     const uint32_t t = all >> 32 ? static_cast<uint32_t>(i / pieces) : static_cast<uint32_t>(i) / pieces;
-    const uint32_t u = static_cast<uint32_t>(i - static_cast<uint64_t>(t) * pieces);
-    const T* src = static_cast<const T*>(p.x) + (t0 + t) * p.stride;
-    Piece<T, V> v;
-    if (VEC) v = Piece<T, V>::load(src + static_cast<uint64_t>(u) * V);
+    const uint32_t u = static_cast<uint32_t>(i) - t * pieces - (VEC ? 0 : 1);  // -1: the pair before the row's pieces
+    const uint64_t src = reinterpret_cast<uint64_t>(token(t));
+    const PlaceRow* rows = own_row + t * p.k;
+    const uint32_t lead = VEC ? 0 : src & 15, held = (lead / static_cast<uint32_t>(sizeof(T)) + p.hidden + V - 1) / V;
+    const uint4* from = reinterpret_cast<const uint4*>(src - lead) + static_cast<int32_t>(u);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 lo = zero, hi = zero;
+    if (VEC || u < held) lo = from[0];
+    if (!VEC && u + 1 < held) hi = from[1];
     for (uint32_t k = 0; k < p.k; k++) {
-      const int32_t pos = own_pos[t * p.k + k];
-      const uint64_t row = static_cast<uint64_t>(pos < 0 ? ~pos : pos);
-      T* dst = static_cast<T*>(p.rows) + row * p.hidden;
-      if (VEC) {
-        (pos < 0 ? Piece<T, V>::zero() : v).store(dst + static_cast<uint64_t>(u) * V);
-      } else {  // every row in pieces of its own alignment
-        uint32_t first;
-        const uint32_t n = RowCut<T>(dst, p.hidden).unit(u, p.hidden, &first);
-        if (n == V)
-          (pos < 0 ? Piece<T, V>::zero() : load_any(src + first)).store(dst + first);
-        else if (n)
-          dst[first] = pos < 0 ? from_f32<T>(0.f) : src[first];
+      const PlaceRow row = rows[k];
+      uint4* to = reinterpret_cast<uint4*>(row.at) + static_cast<int32_t>(u);
+      const uint4 v = !row.routed ? zero : VEC ? lo : shift_pieces<T>(lo, hi, row.off);
+      // the piece's first value; it wraps below 0
+      const uint32_t first = u * V + static_cast<uint32_t>((static_cast<int32_t>(row.off) - static_cast<int32_t>(lead)) /
+                                                             static_cast<int32_t>(sizeof(T)));
+      if (VEC || whole_piece<T>(first, p.hidden)) {
+        *to = v;
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (uint32_t j = 0; j < V; j++) {
+          if (first + j >= p.hidden) continue;
+          if (sizeof(T) == 4)
+            reinterpret_cast<uint32_t*>(to)[j] = w[j & 3];
+          else
+            reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(w[j / 2 & 3] >> (j & 1) * 16);
+        }
       }
     }
   }
@@ -547,15 +606,15 @@ __device__ __forceinline__ bool slot_row(int32_t pos, uint64_t n_rows, int32_t* 
 }
 
 // out[t] = sum over k, in order, of w[t][k] rows[pos[t][k]], in fp32.  A thread has 8 16-byte
-// pieces in flight before it adds the first (4 where the rows lie off 16 bytes, each then two
-// loads): those of KU slots of 8 / KU pieces of the output, kCombineThreads pieces apart.  More
-// than 8 slots (LOOP) are added KU at a time.  Bound by memory: 16384 x 4096 bf16 from 4 slots
-// each, 0.67 GB, 101 us, the measured copy's rate; one piece of 4 slots at a time 132.
-template <typename T, bool VEC, int KU, bool LOOP>
+// pieces in flight before it adds the first: those of KU slots of 8 / KU pieces of the output,
+// kCombineThreads pieces apart.  More than 8 slots (LOOP) are added KU at a time.  Bound by memory:
+// 16384 x 4096 bf16 from 4 slots each, 0.67 GB, 101 us, the measured copy's rate; one piece of 4
+// slots at a time 132.
+template <typename T, int KU, bool LOOP>
 __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_kernel(CombineParams p) {
-  constexpr int V = kPieceOf<T>, kPieces = (VEC ? kCombineLoads : kCombineLoads / 2) / KU;
+  constexpr int V = kPieceOf<T>, kPieces = kCombineLoads / KU;
   pdl_begin();
-  const uint32_t pieces = VEC ? p.hidden / V : any_units<T>(p.hidden);
+  const uint32_t pieces = p.hidden / V;
   // the CTA's first piece: token t0, piece c0 of it
   const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kCombineThreads * kPieces);
   const uint64_t t0 = i0 / pieces;
@@ -569,12 +628,9 @@ __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_
     T* to[kPieces];
 #pragma unroll
     for (int q = 0; q < kPieces; q++) {
-      const uint32_t i = c0 + q * kCombineThreads, dt = i / pieces, u = i - dt * pieces;
+      const uint32_t i = c0 + q * kCombineThreads, dt = i / pieces, first = (i - dt * pieces) * V;
       const uint64_t t = t0 + dt;
-      T* out = static_cast<T*>(p.out) + t * p.hidden;
-      uint32_t first = u * V, values = V;
-      if (!VEC) values = RowCut<T>(out, p.hidden).unit(u, p.hidden, &first);
-      to[q] = t < p.tokens && values == V ? out + first : nullptr;
+      to[q] = t < p.tokens ? static_cast<T*>(p.out) + t * p.hidden + first : nullptr;
 #pragma unroll
       for (int k = 0; k < KU; k++) {
         w[q][k] = 0.f;
@@ -584,22 +640,9 @@ __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_
           bool inside;
           if (slot_row(p.positions[t * p.k + k0 + k], p.n_rows, p.status, &row, &inside)) {
             w[q][k] = p.weights ? p.weights[t * p.k + k0 + k] : 1.f;
-            const T* src = static_cast<const T*>(p.rows) + row * p.row_stride + first;
-            v[q][k] = VEC ? Piece<T, V>::load(src) : load_any(src);
+            v[q][k] = Piece<T, V>::load(static_cast<const T*>(p.rows) + row * p.row_stride + first);
           }
         }
-      }
-      if (!VEC && t < p.tokens && values == 1 && k0 == 0) {  // a value outside the pieces
-        float sum = 0.f;
-#pragma unroll 4
-        for (uint32_t k = 0; k < p.k; k++) {
-          uint64_t row;
-          bool inside;
-          if (slot_row(p.positions[t * p.k + k], p.n_rows, p.status, &row, &inside))
-            sum = fmaf(p.weights ? p.weights[t * p.k + k] : 1.f,
-                       to_f32<T>(static_cast<const T*>(p.rows)[row * p.row_stride + first]), sum);
-        }
-        out[first] = from_f32<T>(sum);
       }
     }
 #pragma unroll
@@ -624,6 +667,87 @@ __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_
   }
 }
 
+// The same for rows that lie off 16 bytes: a warp takes some of the units of a token's output
+// (RowCut).  Each slot's row has its own place relative to those pieces, found once by a lane and
+// kept in shared memory: the piece that output piece 0 starts in, and at which byte.  Bound by the
+// instructions that shift the pieces: 16384 x 4095 bf16 from 4 slots each 150 us, fp32, with half the
+// values a piece, 206, the copy's rate; with all of this found by every thread for itself 225 and 436.
+constexpr uint32_t kAnySlots = 4;  // slots read at once
+constexpr uint32_t kAnyTurns = 4;  // units of a lane, where there are many
+struct AnyRow {
+  uint64_t at;  // 0: nothing to add
+  uint32_t off;
+  float w;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kCombineThreads) moe_combine_any_kernel(CombineParams p, uint32_t turns) {
+  constexpr int V = kPieceOf<T>;
+  __shared__ AnyRow rows_of[kCombineThreads / 32][kMoeMaxK];
+  pdl_begin();
+  const uint32_t lane = lane_id(), units = any_units<T>(p.hidden), shares = (units + 32 * turns - 1) / (32 * turns);
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kCombineThreads / 32) + (threadIdx.x >> 5), t = i / shares;
+  if (t >= p.tokens) return;
+  const uint32_t share = static_cast<uint32_t>(i - t * shares);
+  AnyRow* rows = rows_of[threadIdx.x >> 5];
+  T* out = static_cast<T*>(p.out) + t * p.hidden;
+  const RowCut<T> cut(out, p.hidden);
+  if (lane < p.k) {
+    AnyRow r{0, 0, 0.f};
+    uint64_t row;
+    bool inside;
+    if (slot_row(p.positions[t * p.k + lane], p.n_rows, p.status, &row, &inside)) {
+      const uint64_t at =
+          reinterpret_cast<uint64_t>(static_cast<const T*>(p.rows) + row * p.row_stride + cut.head);
+      r = AnyRow{at & ~15ull, static_cast<uint32_t>(at & 15), p.weights ? p.weights[t * p.k + lane] : 1.f};
+    }
+    rows[lane] = r;
+  }
+  __syncwarp();
+  for (uint32_t turn = 0; turn < turns; turn++) {
+    const uint32_t u = (share * turns + turn) * 32 + lane;
+    uint32_t first;
+    const uint32_t values = cut.unit(u, p.hidden, &first);
+    if (values == V) {
+      float acc[V];
+#pragma unroll
+      for (int j = 0; j < V; j++) acc[j] = 0.f;
+      for (uint32_t k0 = 0; k0 < p.k; k0 += kAnySlots) {
+        uint4 lo[kAnySlots], hi[kAnySlots];
+        AnyRow r[kAnySlots];
+#pragma unroll
+        for (uint32_t k = 0; k < kAnySlots; k++) {
+          r[k] = k0 + k < p.k ? rows[k0 + k] : AnyRow{0, 0, 0.f};
+          lo[k] = hi[k] = make_uint4(0u, 0u, 0u, 0u);
+          const uint4* from = reinterpret_cast<const uint4*>(r[k].at) + u;
+          if (r[k].at) lo[k] = from[0];
+          if (r[k].off) hi[k] = from[1];
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kAnySlots; k++) {
+          float f[V];
+          Piece<T, V>{shift_pieces<T>(lo[k], hi[k], r[k].off)}.get(f);
+#pragma unroll
+          for (int j = 0; j < V; j++) acc[j] = fmaf(r[k].w, f[j], acc[j]);
+        }
+      }
+      Piece<T, V> o;
+      o.set(acc);
+      o.store(out + first);
+    } else if (values) {  // a value outside the pieces
+      float sum = 0.f;
+#pragma unroll 4
+      for (uint32_t k = 0; k < p.k; k++) {
+        const AnyRow r = rows[k];
+        if (!r.at) continue;
+        const T* from = reinterpret_cast<const T*>(r.at + r.off) + (static_cast<int64_t>(first) - cut.head);
+        sum = fmaf(r.w, to_f32<T>(*from), sum);
+      }
+      out[first] = from_f32<T>(sum);
+    }
+  }
+}
+
 // drows[pos] = w dout and dw = <dout, rows[pos]>: dout's row is read once for four slots, each row
 // once; the products are summed in registers over a thread's pieces, then over the CTA (or the
 // warp, for narrow rows).  Bound by memory: 16384 x 4096 bf16, 4 slots each, 1.21 GB, 181 us, the
@@ -639,7 +763,7 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
   const uint64_t t = WARP ? static_cast<uint64_t>(blockIdx.x) * warps + warp : blockIdx.x;
   if (t >= p.tokens) return;
   const uint32_t me = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
-  const uint32_t pieces = VEC ? p.hidden / V : any_units<T>(p.hidden);
+  const uint32_t pieces = VEC ? p.hidden / V : any_pairs<T>(p.hidden);
   const T* dout = static_cast<const T*>(p.dout) + t * p.dout_stride;
   for (uint32_t k0 = blockIdx.y * kCombineBwdK, turn = 0; k0 < p.k; k0 += gridDim.y * kCombineBwdK, turn ^= 1) {
     float dot[kCombineBwdK], w[kCombineBwdK];
@@ -661,9 +785,26 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
         to[k] = static_cast<T*>(p.drows) + row * p.hidden;
       }
     }
-    for (uint32_t u = me; u < pieces; u += step) {
+    // Off 16 bytes: dout is read in pairs of its own pieces; `off` bytes into each lies a piece of the
+    // gradient's row k to write, which takes the values of the row itself that start at byte `foff`
+    // of a piece (none, where both rows lie alike).
+    uint32_t off[kCombineBwdK], foff[kCombineBwdK];
+    const uint32_t lead = VEC ? 0 : reinterpret_cast<uintptr_t>(dout) & 15;
+    const uint32_t held = (lead / static_cast<uint32_t>(sizeof(T)) + p.hidden + V - 1) / V;
+    if (!VEC) {
+#pragma unroll
+      for (int k = 0; k < kCombineBwdK; k++) {
+        off[k] = (lead - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to[k]))) & 15;
+        const int64_t move = static_cast<int64_t>(off[k]) - lead;
+        to[k] = reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(to[k]) + move);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(from[k]) + move;
+        foff[k] = at & 15;
+        from[k] = reinterpret_cast<const T*>(at - foff[k]);
+      }
+    }
+    for (uint32_t i = me; i < pieces; i += step) {
       if (VEC) {
-        const uint64_t at = static_cast<uint64_t>(u) * V;
+        const uint64_t at = static_cast<uint64_t>(i) * V;
         float g[V];
         Piece<T, V> v[kCombineBwdK];
 #pragma unroll
@@ -684,40 +825,51 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
           o.set(d);
           o.store(to[k] + at);
         }
-      } else {  // every row in pieces of its own alignment
-        Piece<T, V> v[kCombineBwdK], g[kCombineBwdK];
-        uint32_t first[kCombineBwdK], values[kCombineBwdK];
-        float one_v[kCombineBwdK], one_g[kCombineBwdK];
+      } else {
+        const uint32_t u = i - 1;  // -1: the pair before dout's pieces
+        const int64_t at = static_cast<int64_t>(static_cast<int32_t>(u)) * V;
+        const uint4* g_at = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(dout) - lead) +
+                            static_cast<int32_t>(u);
+        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo, vlo[kCombineBwdK], vhi[kCombineBwdK];
+        uint32_t first[kCombineBwdK];
+        if (u < held) lo = g_at[0];
+        if (u + 1 < held) hi = g_at[1];
 #pragma unroll
         for (int k = 0; k < kCombineBwdK; k++) {
-          v[k] = g[k] = Piece<T, V>::zero();
-          one_v[k] = one_g[k] = 0.f;
-          values[k] = inside[k] ? RowCut<T>(to[k], p.hidden).unit(u, p.hidden, &first[k]) : 0;
-          if (values[k] == V && routed[k]) {
-            v[k] = load_any(from[k] + first[k]);
-            g[k] = load_any(dout + first[k]);
-          } else if (values[k] && routed[k]) {
-            one_v[k] = to_f32<T>(from[k][first[k]]);
-            one_g[k] = to_f32<T>(dout[first[k]]);
+          first[k] = u * V + static_cast<uint32_t>((static_cast<int32_t>(off[k]) - static_cast<int32_t>(lead)) /
+                                                   static_cast<int32_t>(sizeof(T)));
+          vlo[k] = vhi[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (routed[k] && whole_piece<T>(first[k], p.hidden)) {
+            const uint4* v_at = reinterpret_cast<const uint4*>(from[k] + at);
+            vlo[k] = v_at[0];
+            if (foff[k]) vhi[k] = v_at[1];
           }
         }
 #pragma unroll
         for (int k = 0; k < kCombineBwdK; k++) {
-          if (values[k] == V) {
-            float f[V], d[V];
-            v[k].get(f);
-            g[k].get(d);
+          if (!inside[k]) continue;
+          float f[V], d[V];
+          Piece<T, V>{shift_pieces<T>(lo, hi, off[k])}.get(d);
+          if (whole_piece<T>(first[k], p.hidden)) {
+            if (foff[k]) vlo[k] = shift_pieces<T>(vlo[k], vhi[k], foff[k]);
+            Piece<T, V>{vlo[k]}.get(f);
 #pragma unroll
             for (int j = 0; j < V; j++) {
-              dot[k] = fmaf(d[j], f[j], dot[k]);
+              dot[k] = routed[k] ? fmaf(d[j], f[j], dot[k]) : 0.f;
               d[j] = routed[k] ? w[k] * d[j] : 0.f;
             }
             Piece<T, V> o;
             o.set(d);
-            o.store(to[k] + first[k]);
-          } else if (values[k]) {
-            dot[k] = fmaf(one_g[k], one_v[k], dot[k]);
-            to[k][first[k]] = from_f32<T>(routed[k] ? w[k] * one_g[k] : 0.f);
+            o.store(to[k] + at);
+          } else {  // a piece that the row does not fill
+            const T* v_at =
+                reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(from[k]) + foff[k]) + at;
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+              if (first[k] + j >= p.hidden) continue;
+              if (routed[k]) dot[k] = fmaf(d[j], to_f32<T>(v_at[j]), dot[k]);
+              to[k][at + j] = from_f32<T>(routed[k] ? w[k] * d[j] : 0.f);
+            }
           }
         }
       }
@@ -790,24 +942,36 @@ cudaError_t place(DispatchParams& p, bool vec, uint64_t grid, cudaStream_t strea
   return run(moe_place_kernel<T, false>, grid, 1, kSortThreads, stream, &p);
 }
 
-template <typename T, bool VEC>
-cudaError_t combine(CombineParams& p, cudaStream_t stream) {
-  constexpr int kLoads = VEC ? kCombineLoads : kCombineLoads / 2, kMost = VEC ? 8 : 4;
-  const uint64_t all = p.tokens * (VEC ? p.hidden / kPieceOf<T> : any_units<T>(p.hidden));
-  const int ku = p.k <= 1 ? 1 : p.k <= 2 ? 2 : p.k <= 4 ? 4 : kMost;
-  const uint64_t grid = ceil_div(all, kCombineThreads * (kLoads / ku));
-  if (p.k > kMost) return run(moe_combine_kernel<T, VEC, kMost, true>, grid, 1, kCombineThreads, stream, &p);
+template <typename T>
+cudaError_t combine(CombineParams& p, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
+  if (!vec) {
+    // one unit a lane until the warps fill the GPU
+    const uint64_t turns_all = ceil_div(any_units<T>(p.hidden), 32);
+    uint64_t turns = p.tokens * turns_all / (64ull * static_cast<uint64_t>(dev.sm_count));
+    turns = turns < 1 ? 1 : turns > kAnyTurns ? kAnyTurns : turns;
+    uint32_t each = static_cast<uint32_t>(turns);
+    const uint64_t grid = ceil_div(p.tokens * ceil_div(turns_all, turns), kCombineThreads / 32);
+    if (grid == 0) return cudaSuccess;
+    if (grid > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+    void* args[] = {&p, &each};
+    return launch_kernel(reinterpret_cast<const void*>(moe_combine_any_kernel<T>), dim3(static_cast<unsigned>(grid)),
+                         dim3(kCombineThreads), 0, stream, args, false);
+  }
+  const uint64_t all = p.tokens * (p.hidden / kPieceOf<T>);
+  const int ku = p.k <= 1 ? 1 : p.k <= 2 ? 2 : p.k <= 4 ? 4 : 8;
+  const uint64_t grid = ceil_div(all, kCombineThreads * (kCombineLoads / ku));
+  if (p.k > 8) return run(moe_combine_kernel<T, 8, true>, grid, 1, kCombineThreads, stream, &p);
   switch (ku) {
-    case 1: return run(moe_combine_kernel<T, VEC, 1, false>, grid, 1, kCombineThreads, stream, &p);
-    case 2: return run(moe_combine_kernel<T, VEC, 2, false>, grid, 1, kCombineThreads, stream, &p);
-    case 4: return run(moe_combine_kernel<T, VEC, 4, false>, grid, 1, kCombineThreads, stream, &p);
-    default: return run(moe_combine_kernel<T, VEC, kMost, false>, grid, 1, kCombineThreads, stream, &p);
+    case 1: return run(moe_combine_kernel<T, 1, false>, grid, 1, kCombineThreads, stream, &p);
+    case 2: return run(moe_combine_kernel<T, 2, false>, grid, 1, kCombineThreads, stream, &p);
+    case 4: return run(moe_combine_kernel<T, 4, false>, grid, 1, kCombineThreads, stream, &p);
+    default: return run(moe_combine_kernel<T, 8, false>, grid, 1, kCombineThreads, stream, &p);
   }
 }
 
 template <typename T, bool VEC>
 cudaError_t combine_bwd(CombineBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
-  const uint64_t pieces = VEC ? p.hidden / kPieceOf<T> : any_units<T>(p.hidden);
+  const uint64_t pieces = VEC ? p.hidden / kPieceOf<T> : any_pairs<T>(p.hidden);
   // Few tokens leave SMs idle: their slots, four at a time, then go to CTAs of their own, which
   // hold a piece a thread.
   const bool few = p.tokens < 2ull * static_cast<uint64_t>(dev.sm_count);
@@ -838,7 +1002,7 @@ cudaError_t launch_dispatch(const DispatchParams& params, int dtype, bool vec, c
   DispatchParams p = params;
   const uint64_t slots = p.tokens * p.k;
   p.chunks = static_cast<uint32_t>(ceil_div(slots, kMoeChunkSlots));
-  p.single = slots <= kMoeSingleSlots;
+  p.single = slots <= (p.k < 4 ? kMoeSingleSlots / 2 : kMoeSingleSlots);
   if (!p.single) {
     static KernelPrep prep;
     constexpr int kMostSmem = kSortWarps * (kMoeMaxExperts + 1) * 4;
@@ -849,7 +1013,8 @@ cudaError_t launch_dispatch(const DispatchParams& params, int dtype, bool vec, c
     e = run(moe_count_kernel, p.chunks, 1, kSortThreads, stream, &p,
             kSortWarps * (static_cast<int>(p.experts) + 1) * 4);
     if (e != cudaSuccess) return e;
-    e = run(moe_prefix_kernel, kPrefixCtas, 1, kPrefixThreads, stream, &p);
+    p.few_counts = p.chunks <= 16 && (p.experts + 1) * p.chunks <= 1600;
+    if (!p.few_counts) e = run(moe_prefix_kernel, kPrefixCtas, 1, kPrefixThreads, stream, &p);
     if (e != cudaSuccess) return e;
   }
   // Tokens per CTA: few while the grid does not fill the GPU, up to kMoePlaceTokens once it does
@@ -866,12 +1031,13 @@ cudaError_t launch_dispatch(const DispatchParams& params, int dtype, bool vec, c
   }
 }
 
-cudaError_t launch_combine(const CombineParams& params, int dtype, bool vec, cudaStream_t stream) {
+cudaError_t launch_combine(const CombineParams& params, int dtype, bool vec, cudaStream_t stream,
+                           const DeviceInfo& dev) {
   CombineParams p = params;
   switch (dtype) {
-    case ZC_BF16: return vec ? combine<__nv_bfloat16, true>(p, stream) : combine<__nv_bfloat16, false>(p, stream);
-    case ZC_F16: return vec ? combine<__half, true>(p, stream) : combine<__half, false>(p, stream);
-    default: return vec ? combine<float, true>(p, stream) : combine<float, false>(p, stream);
+    case ZC_BF16: return combine<__nv_bfloat16>(p, vec, stream, dev);
+    case ZC_F16: return combine<__half>(p, vec, stream, dev);
+    default: return combine<float>(p, vec, stream, dev);
   }
 }
 
