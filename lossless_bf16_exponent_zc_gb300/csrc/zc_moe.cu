@@ -751,13 +751,15 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_any_kernel(Combin
 // drows[pos] = w dout and dw = <dout, rows[pos]>: dout's row is read once for four slots, each row
 // once; the products are summed in registers over a thread's pieces, then over the CTA (or the
 // warp, for narrow rows).  Bound by memory: 16384 x 4096 bf16, 4 slots each, 1.21 GB, 181 us, the
-// measured copy's rate.
-constexpr int kCombineBwdK = 4;
+// measured copy's rate; off 16 bytes by the instructions that shift the pieces, 4095 wide 254 us (two
+// slots at once in 64 registers; four in 124 423).
+template <bool VEC>
+constexpr int kCombineBwdK = VEC ? 4 : 2;  // slots at once; off 16 bytes four take twice the registers
 
 template <typename T, bool VEC, bool WARP>
-__global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p) {
-  constexpr int V = kPieceOf<T>;
-  __shared__ float red[2][kCombineBwdK * 32];
+__global__ void __launch_bounds__(512, 2) moe_combine_bwd_kernel(CombineBwdParams p) {
+  constexpr int V = kPieceOf<T>, KU = kCombineBwdK<VEC>;
+  __shared__ float red[2][KU * 32];
   pdl_begin();
   const uint32_t lane = lane_id(), warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
   const uint64_t t = WARP ? static_cast<uint64_t>(blockIdx.x) * warps + warp : blockIdx.x;
@@ -765,13 +767,13 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
   const uint32_t me = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
   const uint32_t pieces = VEC ? p.hidden / V : any_pairs<T>(p.hidden);
   const T* dout = static_cast<const T*>(p.dout) + t * p.dout_stride;
-  for (uint32_t k0 = blockIdx.y * kCombineBwdK, turn = 0; k0 < p.k; k0 += gridDim.y * kCombineBwdK, turn ^= 1) {
-    float dot[kCombineBwdK], w[kCombineBwdK];
-    const T* from[kCombineBwdK];
-    T* to[kCombineBwdK];
-    bool routed[kCombineBwdK], inside[kCombineBwdK];
+  for (uint32_t k0 = blockIdx.y * KU, turn = 0; k0 < p.k; k0 += gridDim.y * KU, turn ^= 1) {
+    float dot[KU], w[KU];
+    const T* from[KU];
+    T* to[KU];
+    bool routed[KU], inside[KU];
 #pragma unroll
-    for (int k = 0; k < kCombineBwdK; k++) {
+    for (int k = 0; k < KU; k++) {
       dot[k] = 0.f;
       w[k] = 0.f;
       routed[k] = inside[k] = false;
@@ -788,12 +790,12 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
     // Off 16 bytes: dout is read in pairs of its own pieces; `off` bytes into each lies a piece of the
     // gradient's row k to write, which takes the values of the row itself that start at byte `foff`
     // of a piece (none, where both rows lie alike).
-    uint32_t off[kCombineBwdK], foff[kCombineBwdK];
+    uint32_t off[KU], foff[KU];
     const uint32_t lead = VEC ? 0 : reinterpret_cast<uintptr_t>(dout) & 15;
     const uint32_t held = (lead / static_cast<uint32_t>(sizeof(T)) + p.hidden + V - 1) / V;
     if (!VEC) {
 #pragma unroll
-      for (int k = 0; k < kCombineBwdK; k++) {
+      for (int k = 0; k < KU; k++) {
         off[k] = (lead - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to[k]))) & 15;
         const int64_t move = static_cast<int64_t>(off[k]) - lead;
         to[k] = reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(to[k]) + move);
@@ -806,13 +808,13 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
       if (VEC) {
         const uint64_t at = static_cast<uint64_t>(i) * V;
         float g[V];
-        Piece<T, V> v[kCombineBwdK];
+        Piece<T, V> v[KU];
 #pragma unroll
-        for (int k = 0; k < kCombineBwdK; k++)
+        for (int k = 0; k < KU; k++)
           v[k] = routed[k] ? Piece<T, V>::load(from[k] + at) : Piece<T, V>::zero();
         Piece<T, V>::load(dout + at).get(g);
 #pragma unroll
-        for (int k = 0; k < kCombineBwdK; k++) {
+        for (int k = 0; k < KU; k++) {
           if (!inside[k]) continue;
           float f[V], d[V];
           v[k].get(f);
@@ -830,12 +832,12 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
         const int64_t at = static_cast<int64_t>(static_cast<int32_t>(u)) * V;
         const uint4* g_at = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(dout) - lead) +
                             static_cast<int32_t>(u);
-        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo, vlo[kCombineBwdK], vhi[kCombineBwdK];
-        uint32_t first[kCombineBwdK];
+        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo, vlo[KU], vhi[KU];
+        uint32_t first[KU];
         if (u < held) lo = g_at[0];
         if (u + 1 < held) hi = g_at[1];
 #pragma unroll
-        for (int k = 0; k < kCombineBwdK; k++) {
+        for (int k = 0; k < KU; k++) {
           first[k] = u * V + static_cast<uint32_t>((static_cast<int32_t>(off[k]) - static_cast<int32_t>(lead)) /
                                                    static_cast<int32_t>(sizeof(T)));
           vlo[k] = vhi[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -846,7 +848,7 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
           }
         }
 #pragma unroll
-        for (int k = 0; k < kCombineBwdK; k++) {
+        for (int k = 0; k < KU; k++) {
           if (!inside[k]) continue;
           float f[V], d[V];
           Piece<T, V>{shift_pieces<T>(lo, hi, off[k])}.get(d);
@@ -876,13 +878,13 @@ __global__ void __launch_bounds__(512) moe_combine_bwd_kernel(CombineBwdParams p
     }
     if (WARP) {
 #pragma unroll
-      for (int k = 0; k < kCombineBwdK; k++) dot[k] = warp_sum_f32(dot[k]);
+      for (int k = 0; k < KU; k++) dot[k] = warp_sum_f32(dot[k]);
     } else {
-      block_sum_f32<kCombineBwdK>(dot, red[turn]);
+      block_sum_f32<KU>(dot, red[turn]);
     }
     if (me == 0) {
 #pragma unroll
-      for (int k = 0; k < kCombineBwdK; k++)
+      for (int k = 0; k < KU; k++)
         if (k0 + k < p.k) p.dweights[t * p.k + k0 + k] = dot[k];
     }
   }
@@ -972,14 +974,16 @@ cudaError_t combine(CombineParams& p, bool vec, cudaStream_t stream, const Devic
 template <typename T, bool VEC>
 cudaError_t combine_bwd(CombineBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   const uint64_t pieces = VEC ? p.hidden / kPieceOf<T> : any_pairs<T>(p.hidden);
-  // Few tokens leave SMs idle: their slots, four at a time, then go to CTAs of their own, which
+  // Few tokens leave SMs idle: their slots, a few at a time, then go to CTAs of their own, which
   // hold a piece a thread.
   const bool few = p.tokens < 2ull * static_cast<uint64_t>(dev.sm_count);
-  const uint32_t split = few ? static_cast<uint32_t>(ceil_div(p.k, kCombineBwdK)) : 1;
+  const uint32_t split = few ? static_cast<uint32_t>(ceil_div(p.k, kCombineBwdK<VEC>)) : 1;
   if (pieces <= 64)
     return run(moe_combine_bwd_kernel<T, VEC, true>, ceil_div(p.tokens, 4), split, 128, stream, &p);
-  const uint64_t warps = ceil_div(pieces, few ? 32 : 64), most = few ? 16 : 8;
-  return run(moe_combine_bwd_kernel<T, VEC, false>, p.tokens, split, static_cast<int>(32 * (warps < most ? warps : most)),
+  // a piece a thread up to 16 warps, or 8 warps in whole turns; off 16 bytes 4 (16384 x 4095 bf16 254 us
+  // against 303)
+  const uint64_t turns = few ? ceil_div(pieces, 512) : pieces < 512 ? 2 : pieces / (VEC ? 256 : 128);
+  return run(moe_combine_bwd_kernel<T, VEC, false>, p.tokens, split, static_cast<int>(32 * ceil_div(pieces, 32 * turns)),
              stream, &p);
 }
 
