@@ -122,6 +122,20 @@ __device__ __forceinline__ uint4 shift_pieces(uint4 lo, uint4 hi, uint32_t off) 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Stores those of a piece's values, the first of them number `first` of the row, that lie in it.
+template <typename T>
+__device__ __forceinline__ void store_part(T* p, Piece<T, kPieceOf<T>> v, uint32_t first, uint32_t width) {
+  const uint32_t w[4] = {v.v.x, v.v.y, v.v.z, v.v.w};
+#pragma unroll
+  for (uint32_t j = 0; j < kPieceOf<T>; j++) {
+    if (first + j >= width) continue;
+    if (sizeof(T) == 4)
+      reinterpret_cast<uint32_t*>(p)[j] = w[j & 3];
+    else
+      reinterpret_cast<uint16_t*>(p)[j] = static_cast<uint16_t>(w[j / 2 & 3] >> (j & 1) * 16);
+  }
+}
+
 // Pairs of neighbouring pieces that a row of `width` values can touch wherever it starts, the first
 // with nothing before its second.
 template <typename T>

@@ -578,15 +578,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams 
       if (VEC || whole_piece<T>(first, p.hidden)) {
         *to = v;
       } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (uint32_t j = 0; j < V; j++) {
-          if (first + j >= p.hidden) continue;
-          if (sizeof(T) == 4)
-            reinterpret_cast<uint32_t*>(to)[j] = w[j & 3];
-          else
-            reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(w[j / 2 & 3] >> (j & 1) * 16);
-        }
+        store_part<T>(reinterpret_cast<T*>(to), Piece<T, V>{v}, first, p.hidden);
       }
     }
   }
@@ -868,10 +860,12 @@ __global__ void __launch_bounds__(512, 2) moe_combine_bwd_kernel(CombineBwdParam
                 reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(from[k]) + foff[k]) + at;
 #pragma unroll
             for (int j = 0; j < V; j++) {
-              if (first[k] + j >= p.hidden) continue;
-              if (routed[k]) dot[k] = fmaf(d[j], to_f32<T>(v_at[j]), dot[k]);
-              to[k][at + j] = from_f32<T>(routed[k] ? w[k] * d[j] : 0.f);
+              if (routed[k] && first[k] + j < p.hidden) dot[k] = fmaf(d[j], to_f32<T>(v_at[j]), dot[k]);
+              d[j] = routed[k] ? w[k] * d[j] : 0.f;
             }
+            Piece<T, V> o;
+            o.set(d);
+            store_part<T>(to[k] + at, o, first[k], p.hidden);
           }
         }
       }

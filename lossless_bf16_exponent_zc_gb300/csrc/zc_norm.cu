@@ -115,10 +115,10 @@ constexpr int kFwdStages = C == kFwdCols ? 4 : 3;
 
 // The ring shape: rows walker, walker + walkers, ... stream through the shared memory of a CTA or a
 // cluster of two.
-template <typename T, int V, int C, int CTAS, bool BRANCH, bool NEXT>
+template <typename T, int V, int C, int CTAS, bool SHIFT, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_ring_kernel(NormParams p) {
   constexpr int P = C / 2, kStages = kFwdStages<C>;
-  using Ring = RowRing<T, V, C, BRANCH ? 2 : 1, kStages>;
+  using Ring = RowRing<T, V, C, BRANCH ? 2 : 1, kStages, SHIFT>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ __align__(16) float red[2][2 * kSumSlots];
   pdl_allow_dependents();
@@ -130,8 +130,11 @@ __global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_
   pdl_wait();
   const uint32_t rank = CTAS > 1 ? cluster_rank() : 0, part = blockDim.x * C;
   const uint32_t width = CTAS > 1 ? min(part, p.hidden - rank * part) : p.hidden;
-  const Ring ring{ring_smem, threadIdx.x, blockDim.x, width / V, rank * part};
   const uint64_t walker = blockIdx.x / CTAS, walkers = gridDim.x / CTAS;
+  const T* row0 = static_cast<const T*>(p.x) + walker * p.x_stride;
+  const uint32_t lead = SHIFT ? (reinterpret_cast<uintptr_t>(row0) & 15) / static_cast<uint32_t>(sizeof(T)) : 0;
+  const Ring ring{ring_smem, threadIdx.x, blockDim.x, SHIFT ? (lead + width + V - 1) / V : width / V, rank * part, lead,
+                  width};
 #pragma unroll
   for (int i = 0; i < (BRANCH ? 2 : 1); i++) ring.clear(i, false);
   const float inv_d = 1.f / static_cast<float>(p.hidden);
@@ -160,6 +163,7 @@ __global__ void __launch_bounds__(kNormRingThreads, C == kFwdCols ? 2 : 1) norm_
   for (uint64_t t = walker; t < p.tokens; t += walkers) {
     float2 x[P];
     float sums[2];
+    ring.cut(stage);
     ring.get(stage, 0, x_at + t * p.x_stride + ring.first, x);
     if (BRANCH) {
       float2 y[P], yy = splat(0.f);
@@ -221,31 +225,33 @@ cudaError_t run_shape(NormParams& p, int threads, cudaStream_t stream, const Dev
                        false);
 }
 
-template <typename T, int V, int C, int CTAS, bool BRANCH, bool NEXT>
-cudaError_t run_ring(NormParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
+template <typename T, int V, int C, int CTAS, bool SHIFT, bool BRANCH, bool NEXT>
+cudaError_t run_ring(NormParams& p, int threads, uint64_t period, cudaStream_t stream, const DeviceInfo& dev) {
   static RingPrep prep;
   const int smem = static_cast<int>(RowRing<T, V, C, BRANCH ? 2 : 1, kFwdStages<C>>::bytes(threads));
-  const void* fn = reinterpret_cast<const void*>(norm_ring_kernel<T, V, C, CTAS, BRANCH, NEXT>);
+  const void* fn = reinterpret_cast<const void*>(norm_ring_kernel<T, V, C, CTAS, SHIFT, BRANCH, NEXT>);
   int fit = 0;
   cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, CTAS, &fit);
   if (e != cudaSuccess) return e;
-  const uint64_t walkers = p.tokens < static_cast<uint64_t>(fit) ? p.tokens : static_cast<uint64_t>(fit);
+  uint64_t walkers = static_cast<uint64_t>(fit);
+  if (walkers > period) walkers -= walkers % period;
+  if (p.tokens < walkers) walkers = p.tokens;
   void* args[] = {&p};
   return launch_kernel(fn, dim3(static_cast<unsigned>(walkers) * CTAS), dim3(threads), smem, stream, args, false, CTAS);
 }
 
 // Runs the ring with C columns a thread and CTAS CTAs a row if it holds such rows.
-template <typename T, int V, int C, int CTAS>
-bool run_ring(NormParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e) {
+template <typename T, int V, int C, int CTAS, bool SHIFT = false>
+bool run_ring(NormParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e, uint64_t period = 1) {
   constexpr uint32_t kAll = CTAS * C * 32;
-  const int threads = static_cast<int>((p.hidden + kAll - 1) / kAll * 32);
+  const int threads = static_cast<int>((p.hidden + (SHIFT ? V - 1 : 0) + kAll - 1) / kAll * 32);
   if (threads > kNormRingThreads || RowRing<T, V, C, 2, kFwdStages<C>>::bytes(threads) > kNormRingSmem) return false;
   if (p.y && p.next_weight)
-    *e = run_ring<T, V, C, CTAS, true, true>(p, threads, stream, dev);
+    *e = run_ring<T, V, C, CTAS, SHIFT, true, true>(p, threads, period, stream, dev);
   else if (p.y)
-    *e = run_ring<T, V, C, CTAS, true, false>(p, threads, stream, dev);
+    *e = run_ring<T, V, C, CTAS, SHIFT, true, false>(p, threads, period, stream, dev);
   else
-    *e = run_ring<T, V, C, CTAS, false, true>(p, threads, stream, dev);
+    *e = run_ring<T, V, C, CTAS, SHIFT, false, true>(p, threads, period, stream, dev);
   return true;
 }
 
@@ -265,6 +271,17 @@ cudaError_t run_width(NormParams& p, cudaStream_t stream, const DeviceInfo& dev)
     return run_shape<T, V, 16, true, kWarp>(p, kWarp, stream, dev);
   }
   cudaError_t e;
+  if constexpr (V == 1) {
+    RowPlaces rows;
+    rows.add(p.x, p.x_stride * sizeof(T));
+    rows.add(p.y, p.y_stride * sizeof(T));
+    rows.add(p.x_new, static_cast<uint64_t>(d) * sizeof(T));
+    rows.add(p.h, static_cast<uint64_t>(d) * sizeof(T));
+    if (rows.alike) {
+      if (run_ring<T, kPieceOf<T>, kFwdCols, 1, true>(p, stream, dev, &e, rows.period())) return e;
+      if (run_ring<T, kPieceOf<T>, kFwdWideCols, 1, true>(p, stream, dev, &e, rows.period())) return e;
+    }
+  }
   if (run_ring<T, V, kFwdCols, 1>(p, stream, dev, &e)) return e;
   if (run_ring<T, V, kFwdWideCols, 1>(p, stream, dev, &e)) return e;
   // Wider still: in 16-byte pieces a CTA holds a row in registers (4096 x 16384 bf16 114 us; a

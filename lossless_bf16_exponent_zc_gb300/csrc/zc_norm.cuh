@@ -72,13 +72,17 @@ constexpr int kNormRingSmem = 225 * 1024;  // what the ring may take of the 227 
 // of 16-bit values at odd addresses (kWords) are copied as the 4-byte words that cover them and
 // read value by value, by other threads than copied them; their first and last word may hold a
 // neighbour's value, which is not used.
-template <typename T, int V, int COLS, int ARRAYS, int STAGES>
+// SHIFT: rows off 16 bytes, but all of a walker's rows in all matrices equally so, by `lead` values.
+// They are then copied as the aligned pieces that cover them: a thread's columns start `lead` before
+// those of its pieces, and what the first and the last piece hold of other rows becomes zero.
+template <typename T, int V, int COLS, int ARRAYS, int STAGES, bool SHIFT = false>
 struct RowRing {
   static constexpr int NV = COLS / V;
   static constexpr bool kWords = V == 1 && sizeof(T) == 2;
   uint8_t* smem;
   uint32_t me, threads, pieces;  // this thread among those that share a row (or its part of a cluster's), and its pieces
   uint32_t first = 0;            // column that the part starts at
+  uint32_t lead = 0, width = 0;  // SHIFT: values before a row in its first piece, and of the row
 
   __host__ __device__ static uint32_t region(uint32_t threads) {  // bytes of one row of one matrix
     return kWords ? (threads * NV * 2 + 4 + 15) / 16 * 16 : threads * NV * V * static_cast<uint32_t>(sizeof(T));
@@ -91,6 +95,7 @@ struct RowRing {
   // Where a thread's walk through a matrix starts: its first column of row t.
   template <typename U>
   __device__ __forceinline__ U* start(U* base, uint64_t t, uint64_t stride) const {
+    if (SHIFT) return base + t * stride + me * V - lead;
     return base + t * stride + first + (kWords ? 0 : me * V);
   }
   __device__ __forceinline__ void copy(int stage, int array, const T* row) const {
@@ -107,6 +112,9 @@ struct RowRing {
         if (me + i * threads >= pieces) continue;
         if (V == 1)
           cp_async_4(to + i * threads * 4, row + i * threads);
+        else if (SHIFT)  // zeros after the row's end
+          cp_async_16(to + i * threads * 16, row + i * threads * V,
+                      min(16u, (lead + width - (me + i * threads) * V) * static_cast<uint32_t>(sizeof(T))));
         else
           cp_async_16(to + i * threads * 16, row + i * threads * V, 16);
       }
@@ -122,6 +130,22 @@ struct RowRing {
           const uint32_t c = me + i * threads;
           if (all || c >= pieces) Piece<T, V>::zero().store(reinterpret_cast<T*>(at(stage, array)) + c * V);
         }
+    }
+  }
+  // Zeroes what the first piece of a row that has landed holds of the row before.
+  __device__ __forceinline__ void cut(int stage) const {
+    if constexpr (SHIFT) {
+      if (me || !lead) return;
+      uint4 head[ARRAYS];
+#pragma unroll
+      for (int a = 0; a < ARRAYS; a++) head[a] = *reinterpret_cast<const uint4*>(at(stage, a));
+      const uint32_t bits = lead * 8 * static_cast<uint32_t>(sizeof(T));  // to clear, in front
+      auto mask = [&](uint32_t word) { return bits >= 32 * word + 32 ? 0u : bits > 32 * word ? 0xFFFF0000u : kFull; };
+      const uint4 m = make_uint4(mask(0), mask(1), mask(2), mask(3));
+#pragma unroll
+      for (int a = 0; a < ARRAYS; a++)
+        *reinterpret_cast<uint4*>(at(stage, a)) =
+            make_uint4(head[a].x & m.x, head[a].y & m.y, head[a].z & m.z, head[a].w & m.w);
     }
   }
   // This thread's columns of a row (its address as given to copy()) as they lie in memory; zeros
@@ -169,7 +193,16 @@ struct RowRing {
       for (int j = 0; j < V; j++) v[j] = flat[i * V + j];
       Piece<T, V> o;
       o.set(v);
-      if (me + i * threads < pieces) o.store(row + i * threads * V);
+      if constexpr (SHIFT) {
+        const uint32_t c = me + i * threads, col = c * V - lead;
+        if (whole_piece<T>(col, width)) {
+          o.store(row + i * threads * V);
+        } else if (c < pieces) {
+          store_part<T>(row + i * threads * V, o, col, width);
+        }
+      } else {
+        if (me + i * threads < pieces) o.store(row + i * threads * V);
+      }
     }
   }
   // This thread's columns of a parameter row.
@@ -181,7 +214,13 @@ struct RowRing {
       float v[V];
 #pragma unroll
       for (int j = 0; j < V; j++) v[j] = 0.f;
-      if (c < pieces) load_params<T, V>(base, is_f32, row + first + static_cast<uint64_t>(c) * V, v);
+      if constexpr (SHIFT) {
+#pragma unroll
+        for (int j = 0; j < V; j++)
+          if (c * V + j - lead < width) v[j] = load_param<T>(base, is_f32, row + (c * V + j - lead));
+      } else {
+        if (c < pieces) load_params<T, V>(base, is_f32, row + first + static_cast<uint64_t>(c) * V, v);
+      }
 #pragma unroll
       for (int j = 0; j < V; j++) flat[i * V + j] = v[j];
     }
@@ -192,6 +231,20 @@ struct RowRing {
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
+// How the rows of a call's matrices lie relative to 16 bytes: alike if they start equally far into a
+// piece in all of them, and then rows `period` apart do.
+struct RowPlaces {
+  bool any = false, alike = true;
+  uint64_t base = 0, step = 0;
+  void add(const void* p, uint64_t stride_bytes) {
+    if (!p) return;
+    const uint64_t b = reinterpret_cast<uintptr_t>(p) & 15, s = stride_bytes & 15;
+    if (any && (b != base || s != step)) alike = false;
+    any = true, base = b, step = s;
+  }
+  uint64_t period() const { return step ? 16 / (step & (~step + 1)) : 1; }
+};
 
 // CTAs of a ring kernel (clusters of them) that the GPU holds, by CTA size (the ring's size follows
 // from it); looked up once per device, size and cluster.

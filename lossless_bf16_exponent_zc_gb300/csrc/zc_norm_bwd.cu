@@ -61,11 +61,11 @@ struct BwdWalk {
 // barrier: between two barriers the CTA writes the last row's dy, takes this row's G, dx, column
 // sums and v y, and the next row's first sums.  The inputs are read from the stage twice rather
 // than held, so that the column sums and the weights stay in registers.
-template <typename T, int V, int C, bool CLUSTER, bool BRANCH, bool NEXT>
+template <typename T, int V, int C, bool CLUSTER, bool SHIFT, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(NormBwdParams p) {
   constexpr int P = C / 2;
   constexpr int kGx = 0, kGh = 1, kX = 2, kY = NEXT ? 3 : 1, kArrays = BRANCH && NEXT ? 4 : NEXT ? 3 : 2;
-  using Ring = RowRing<T, V, C, kArrays, kBwdStages>;
+  using Ring = RowRing<T, V, C, kArrays, kBwdStages, SHIFT>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ __align__(16) float red[2][4 * kSumSlots];
   pdl_allow_dependents();
@@ -79,7 +79,13 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
   const uint32_t rank = CLUSTER ? cluster_rank() : 0, walker = CLUSTER ? blockIdx.x / p.cluster : blockIdx.x;
   const uint32_t part = blockDim.x * C;
   const uint32_t width = CLUSTER ? min(part, p.hidden - rank * part) : p.hidden;
-  const Ring ring{ring_smem, threadIdx.x, blockDim.x, width / V, rank * part};
+  BwdWalk ahead{walker, 0, 0}, now{walker, 0, 0};
+  ahead.open(p);
+  now.open(p);
+  const T* row0 = static_cast<const T*>(p.dx) + now.t * p.hidden;
+  const uint32_t lead = SHIFT ? (reinterpret_cast<uintptr_t>(row0) & 15) / static_cast<uint32_t>(sizeof(T)) : 0;
+  const Ring ring{ring_smem, threadIdx.x, blockDim.x, SHIFT ? (lead + width + V - 1) / V : width / V, rank * part, lead,
+                  width};
   const float inv_d = 1.f / static_cast<float>(p.hidden);
   const bool wide = BRANCH && p.gate && p.gate_wide, narrow = BRANCH && p.gate && !p.gate_wide;
   const bool past = p.dx_new != nullptr;
@@ -89,9 +95,6 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
 
   // Addresses of the row to copy next and, for rows at odd addresses, of the row being computed.
   const T *gx = nullptr, *gh = nullptr, *x = nullptr, *y = nullptr;
-  BwdWalk ahead{walker, 0, 0}, now{walker, 0, 0};
-  ahead.open(p);
-  now.open(p);
   auto aim = [&](uint64_t t) {
     if (past) gx = ring.start(static_cast<const T*>(p.dx_new), t, p.dx_new_stride);
     if (NEXT) {
@@ -151,6 +154,27 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
     for (int i = 0; i < Ring::NV; i++) {
       const uint32_t c = threadIdx.x + i * blockDim.x;
       if (c >= ring.pieces) continue;
+      if constexpr (SHIFT) {  // a walker has one unit only
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+          const uint32_t col = c * V + j - lead;
+          if (col >= width) continue;
+          const uint64_t at = static_cast<uint64_t>(u) * p.hidden + col;
+          float dw = fb[i * V + j];
+          if (wide) {
+            const float dg = dw * load_param<T>(p.weight, p.params_f32, col);
+            dw *= load_param<T>(p.gate, p.params_f32, (u / p.splits) * static_cast<uint64_t>(p.hidden) + col);
+            if (p.splits > 1)
+              gate_parts[at] = dg;
+            else if (p.params_f32)
+              static_cast<float*>(p.dgate)[at] = dg;
+            else
+              static_cast<T*>(p.dgate)[at] = from_f32<T>(dg);
+          }
+          mine[col] = dw;
+        }
+        continue;
+      }
       float k[V], w[V];
       if (wide) {
         load_params<T, V>(p.gate, p.params_f32, (u / p.splits) * static_cast<uint64_t>(p.hidden) + ring.first + c * V, k);
@@ -244,6 +268,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
   int stage = 0, turn = 0;
   cp_async_wait<kBwdStages - 1>();
   if (Ring::kWords) __syncthreads();
+  ring.cut(0);
   first_sums(0, now.t, sums);
   block_sum_shared<4, CLUSTER>(sums, red[1], rank, p.cluster);
   while (now.valid(p)) {
@@ -312,6 +337,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
       // the next row: all but the copies issued after its own
       cp_async_wait<Ring::kWords || (!kHold && BRANCH) ? kBwdStages - 2 : kBwdStages - 1>();
       if (Ring::kWords) __syncthreads();
+      ring.cut(stage);
       first_sums(stage, now.t, sums);
     }
     block_sum_shared<4, CLUSTER>(sums, red[turn], rank, p.cluster);
@@ -328,7 +354,13 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
       float dn[V];
 #pragma unroll
       for (int j = 0; j < V; j++) dn[j] = fn[i * V + j];
-      if (c < ring.pieces) store_f32<V>(mine + p.hidden + c * V, dn);
+      if constexpr (SHIFT) {
+#pragma unroll
+        for (int j = 0; j < V; j++)
+          if (c * V + j - lead < width) mine[p.hidden + (c * V + j - lead)] = dn[j];
+      } else {
+        if (c < ring.pieces) store_f32<V>(mine + p.hidden + c * V, dn);
+      }
     }
   }
 }
@@ -574,17 +606,23 @@ __global__ void __launch_bounds__(256) norm_narrow_gate_kernel(NormBwdParams p) 
     static_cast<T*>(p.dgate)[blockIdx.x] = from_f32<T>(s[0]);
 }
 
+// Ranges of a gate row's `size` tokens, of `groups` gate rows for `most` walkers.
+uint64_t row_splits(uint64_t groups, uint64_t size, uint64_t most, uint64_t period) {
+  uint64_t splits = groups >= most ? 1 : most / groups;
+  if (splits >= size) return size;  // no tokens: no ranges, and the sums over none of them are zero
+  return splits > period ? splits - splits % period : splits;
+}
+
 // Cuts the rows into ranges for at most `most` walkers, `per_cta` of them in a CTA or each a
 // cluster of p.cluster CTAs (a range lies in one gate row's tokens), launches `fn` and adds up what
-// it left.
+// it left.  With a period, a range's rows are a multiple of it apart, and there is one a walker.
 template <typename T>
 cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint32_t per_cta, int threads, int smem,
-                          cudaStream_t stream, const DeviceInfo& dev) {
+                          cudaStream_t stream, const DeviceInfo& dev, uint64_t period = 1) {
   const bool wide = p.gate && p.gate_wide;
   if (most > norm_max_units(p.hidden)) most = norm_max_units(p.hidden);
   const uint64_t groups = wide ? p.gate_rows : 1, size = wide ? p.gate_tokens : p.tokens;
-  uint64_t splits = groups >= most ? 1 : most / groups;
-  if (splits > size) splits = size;  // no tokens: no ranges, and the sums over none of them are zero
+  const uint64_t splits = row_splits(groups, size, most, period);
   p.splits = static_cast<uint32_t>(splits);
   const uint64_t units = groups * splits;
   if (units > 0xFFFFFFFFull) return cudaErrorInvalidConfiguration;
@@ -615,32 +653,56 @@ cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint3
    : p.y                ? reinterpret_cast<const void*>(KERNEL<__VA_ARGS__, true, false>)               \
                         : reinterpret_cast<const void*>(KERNEL<__VA_ARGS__, false, true>))
 
-template <typename T, int V, int C, bool CLUSTER, bool BRANCH, bool NEXT>
-cudaError_t run_ring(NormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
+template <typename T, int V, int C, bool CLUSTER, bool SHIFT, bool BRANCH, bool NEXT>
+cudaError_t run_ring(NormBwdParams& p, int threads, uint64_t period, cudaStream_t stream, const DeviceInfo& dev) {
   static RingPrep prep[2];  // for clusters of 2 and 4
   constexpr int kArrays = BRANCH && NEXT ? 4 : NEXT ? 3 : 2;
   const int smem = static_cast<int>(RowRing<T, V, C, kArrays, kBwdStages>::bytes(threads));
-  const void* fn = reinterpret_cast<const void*>(norm_bwd_ring_kernel<T, V, C, CLUSTER, BRANCH, NEXT>);
+  const void* fn = reinterpret_cast<const void*>(norm_bwd_ring_kernel<T, V, C, CLUSTER, SHIFT, BRANCH, NEXT>);
   int fit = 0;
   cudaError_t e = prepare_ring(prep[p.cluster == 4], fn, threads, smem, dev, static_cast<int>(p.cluster), &fit);
   if (e != cudaSuccess) return e;
-  return launch_ranges<T>(p, fn, static_cast<uint64_t>(fit), 1, threads, smem, stream, dev);
+  return launch_ranges<T>(p, fn, static_cast<uint64_t>(fit), 1, threads, smem, stream, dev, period);
 }
 
 // Runs the ring with C columns a thread and so many CTAs a row if it holds such rows.
-template <typename T, int V, int C, bool CLUSTER>
-bool run_ring(NormBwdParams& p, uint32_t cluster, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e) {
+template <typename T, int V, int C, bool CLUSTER, bool SHIFT = false>
+bool run_ring(NormBwdParams& p, uint32_t cluster, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e,
+              uint64_t period = 1) {
   const uint32_t all = cluster * C * 32;
-  const int threads = static_cast<int>((p.hidden + all - 1) / all * 32);
+  const int threads = static_cast<int>((p.hidden + (SHIFT ? V - 1 : 0) + all - 1) / all * 32);
   if (threads > kNormRingThreads || RowRing<T, V, C, 4, kBwdStages>::bytes(threads) > kNormRingSmem) return false;
   p.cluster = cluster;
   if (p.y && p.next_weight)
-    *e = run_ring<T, V, C, CLUSTER, true, true>(p, threads, stream, dev);
+    *e = run_ring<T, V, C, CLUSTER, SHIFT, true, true>(p, threads, period, stream, dev);
   else if (p.y)
-    *e = run_ring<T, V, C, CLUSTER, true, false>(p, threads, stream, dev);
+    *e = run_ring<T, V, C, CLUSTER, SHIFT, true, false>(p, threads, period, stream, dev);
   else
-    *e = run_ring<T, V, C, CLUSTER, false, true>(p, threads, stream, dev);
+    *e = run_ring<T, V, C, CLUSTER, SHIFT, false, true>(p, threads, period, stream, dev);
   return true;
+}
+
+// The ring on rows off 16 bytes, but alike in all matrices, if its walkers can keep to rows that lie
+// alike and hold them.
+template <typename T>
+bool run_shifted(NormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e) {
+  RowPlaces rows;
+  rows.add(p.y, p.y_stride * sizeof(T));
+  if (p.next_weight) rows.add(p.x_new, p.x_new_stride * sizeof(T));
+  rows.add(p.dh, p.dh_stride * sizeof(T));
+  rows.add(p.dx_new, p.dx_new_stride * sizeof(T));
+  rows.add(p.dx, static_cast<uint64_t>(p.hidden) * sizeof(T));
+  rows.add(p.dy, static_cast<uint64_t>(p.hidden) * sizeof(T));
+  if (!rows.alike) return false;
+  const bool wide = p.gate && p.gate_wide;
+  const uint64_t groups = wide ? p.gate_rows : 1, size = wide ? p.gate_tokens : p.tokens, period = rows.period();
+  const uint64_t most = static_cast<uint64_t>(dev.sm_count), splits = row_splits(groups, size, most, period);
+  // at least a walker an SM; a few fewer where the period wants it, but not many
+  if (groups * splits > most || (splits < size && (splits % period || 2 * groups * splits < most))) return false;
+  constexpr int V = kPieceOf<T>;
+  if (run_ring<T, V, kBwdCols, false, true>(p, 1, stream, dev, e, period)) return true;
+  if constexpr (sizeof(T) == 2) return run_ring<T, V, kBwdWideCols, false, true>(p, 1, stream, dev, e, period);
+  return false;
 }
 
 template <typename T, int V>
@@ -650,6 +712,9 @@ cudaError_t run_width(NormBwdParams& p, cudaStream_t stream, const DeviceInfo& d
     return launch_ranges<T>(p, ZC_NORM_MODE(norm_bwd_warp_kernel, T, V), 4ull * kNormWarps * static_cast<uint64_t>(dev.sm_count),
                             kNormWarps, kNormWarps * 32, 0, stream, dev);
   cudaError_t e;
+  if constexpr (V == 1) {
+    if (run_shifted<T>(p, stream, dev, &e)) return e;
+  }
   constexpr int kWide = sizeof(T) == 2 && V > 1 ? kBwdWideCols : kBwdCols;
   if (run_ring<T, V, kBwdCols, false>(p, 1, stream, dev, &e)) return e;
   if constexpr (kWide != kBwdCols) {
