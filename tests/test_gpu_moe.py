@@ -262,6 +262,22 @@ def test_dispatch(moe, zc, tokens, experts, k, hidden, dtype, dropped):
     assert zc.status_value(st) == 0
 
 
+@pytest.mark.parametrize("tokens,experts,k", [(1024, 8, 1), (1025, 8, 1), (512, 64, 4), (513, 64, 4), (341, 40, 3),
+                                              (342, 40, 3), (16384, 8, 1), (16385, 8, 1), (1900, 100, 8),
+                                              (2000, 100, 8)])
+def test_dispatch_around_its_choices(moe, tokens, experts, k):
+    """Numbers of slots and of counts on both sides of where the sort takes another way, skewed experts."""
+    g = torch.Generator().manual_seed(tokens)
+    scores = torch.randn((tokens, experts), generator=g) - torch.arange(experts).add(1).log()
+    ids = torch.topk(scores, k, dim=1).indices.int()
+    x = torch.randn((tokens, 8), generator=g).to(torch.bfloat16)
+    rows, plan = moe.dispatch(x.cuda(), ids.cuda(), experts, moe.workspace(tokens, k, experts))
+    positions, slots, offsets = place(ids, experts)
+    assert plan.positions.reshape(-1).tolist() == positions and plan.slots.tolist() == slots
+    assert plan.offsets.tolist() == offsets
+    assert torch.equal(rows.cpu(), x[torch.tensor(slots) // k])
+
+
 def test_dispatch_equal_ids_and_one_expert(moe):
     """Everything to one expert, and the same expert several times in a token: the order is the slots' own."""
     x = torch.arange(3000, device="cuda", dtype=torch.float32)[:, None].repeat(1, 4)
@@ -315,6 +331,56 @@ def test_strided_and_misaligned_inputs(moe, zc, cut, k):
 
 
 # ------------------------------------------------------------------ combine
+@pytest.mark.parametrize("hidden", [1, 2, 3, 6, 9, 15, 17, 23, 33, 255, 1021, 4095])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("before,after", [(0, 0), (1, 2), (3, 8)])
+def test_rows_off_sixteen_bytes(moe, zc, hidden, dtype, before, after):
+    """All four moves of rows that start anywhere, NaN beside them."""
+    g = torch.Generator().manual_seed(hidden)
+
+    def matrix(n):
+        wide = torch.full((n, before + hidden + after), math.nan, dtype=TYPES[dtype])
+        wide[:, before:before + hidden] = torch.randn((n, hidden), generator=g).to(TYPES[dtype])
+        return wide.cuda()[:, before:before + hidden]
+
+    tokens, k, experts = 37, 5, 9
+    ids = ids_of(g, tokens, k, experts, 0.2).cuda()
+    x, rows, dout = matrix(tokens), matrix(tokens * k), matrix(tokens)
+    w = torch.rand((tokens, k), generator=g).cuda()
+    st = zc.new_status()
+    sent, plan = moe.dispatch(x, ids, experts, moe.workspace(tokens, k, experts))
+    at = plan.positions.long()
+    routed = at >= 0
+    want = torch.zeros_like(sent)
+    want[at[routed]] = x[:, None].expand(tokens, k, hidden)[routed]
+    assert torch.equal(sent, want)
+    picked = torch.where(routed[..., None], rows[at.clamp(min=0)].double(), 0)
+    within(moe.dispatch_backward(rows, plan.positions, st), picked.sum(1), picked.abs().sum(1), k)
+    terms = picked * w.double()[..., None]
+    within(moe.combine(rows, w, plan.positions, st), terms.sum(1), terms.abs().sum(1), k + 1)
+    drows, dw = moe.combine_backward(dout, rows, w, plan.positions, st)
+    grad = torch.zeros_like(drows, dtype=torch.float64)
+    grad[at[routed]] = (w.double()[..., None] * dout.double()[:, None])[routed]
+    within(drows, grad, grad.abs(), 1)
+    prod = picked * dout.double()[:, None]
+    within(dw, prod.sum(2), prod.abs().sum(2), hidden // 8 + 32)
+    assert zc.status_value(st) == 0
+
+
+def test_a_row_of_more_than_two_to_the_31_bytes(moe, zc):
+    hidden = 2 ** 30 + 5
+    x = torch.randint(0, 2 ** 20, (1, hidden), device="cuda", dtype=torch.int32).float()
+    ids = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    rows, plan = moe.dispatch(x, ids, 1, moe.workspace(1, 1, 1))
+    assert torch.equal(rows, x)
+    st, w = zc.new_status(), torch.full((1, 1), 0.5, device="cuda")
+    out = moe.combine(rows, w, plan.positions, st)
+    assert torch.equal(out, x / 2)
+    drows, _ = moe.combine_backward(out, rows, w, plan.positions, st)
+    assert torch.equal(drows, x / 4)
+    assert zc.status_value(st) == 0
+
+
 @pytest.mark.parametrize("tokens,experts,k,hidden", [s for s in SHAPES if s[0] < 2000])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("dropped", [0.0, 0.3, 1.0])

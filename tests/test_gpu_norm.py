@@ -5,6 +5,8 @@ the magnitudes that make up a value, ops x 2^-24 x S.  A row's sums run over at 
 10 levels (27 roundings, halved by the square root), which with the products around them gives the ops below; sums
 over tokens add one rounding for each token.
 """
+import math
+
 import pytest
 import torch
 
@@ -210,6 +212,43 @@ def test_views_expanded_gradients_and_in_place(norm):
     want = norm.post_norm(d["y"], d["x"], d["w"], gate=d["gate"], next_weight=d["w2"])
     got = norm.post_norm(d["y"], x, d["w"], gate=d["gate"], next_weight=d["w2"], x_new=x)
     assert got[0] is x and torch.equal(x, want[0]) and torch.equal(got[1], want[1])
+
+
+def inside(t, before, after):
+    """The same matrix as columns of a wider one that holds NaN elsewhere."""
+    wide = torch.full((t.shape[0], before + t.shape[1] + after), math.nan, dtype=t.dtype, device=t.device)
+    wide[:, before:before + t.shape[1]] = t
+    return wide[:, before:before + t.shape[1]]
+
+
+@pytest.mark.parametrize("before,after", [(0, 0), (0, 16), (8, 24), (0, 3), (1, 0), (5, 8)])
+@pytest.mark.parametrize("hidden", [259, 515, 1018, 1531, 4085, 4095])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_off_sixteen_bytes(norm, hidden, dtype, before, after):
+    """Rows that start in the same place as the outputs' and others; what lies beside them is not looked at."""
+    d = make(hidden + before, 700, hidden, dtype, "f32", "channel", True)
+    d["gate"] = 1 + 0.3 * torch.randn(7, hidden, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    for name in ("y", "x", "gx", "gh"):
+        d[name] = inside(d[name], before, after)
+    check(norm, d)
+
+
+@pytest.mark.parametrize("hidden", [515, 1531, 4085])
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_a_row_of_nan_stays_alone(norm, hidden, dtype):
+    d = make(hidden, 610, hidden, dtype, "f32", "none", True)
+
+    def rows(d):
+        x_new, h = norm.post_norm(d["y"], d["x"], d["w"], residual_scale=0.5, next_weight=d["w2"])
+        dy, dx = norm.post_norm_backward(d["gx"], d["gh"], d["y"], d["x"], d["w"], norm.workspace(610, hidden),
+                                         residual_scale=0.5, next_weight=d["w2"])[:2]
+        return [m[::2] for m in (x_new, h, dy, dx)]
+
+    want = rows(d)
+    for name in ("y", "x", "gx", "gh"):
+        d[name][1::2] = math.nan
+    for g, w in zip(rows(d), want):
+        assert torch.equal(g, w)
 
 
 def test_offsets_past_32_bits(norm):
