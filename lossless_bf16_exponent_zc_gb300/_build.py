@@ -109,7 +109,7 @@ def build_extension(force: bool = False, obj: str | None = None) -> str:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIBDIR, "-lzc", "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
-           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+           "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the torch extension failed:\n{r.stdout}\n{r.stderr}")

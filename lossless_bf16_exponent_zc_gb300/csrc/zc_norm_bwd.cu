@@ -11,8 +11,9 @@
 // over all rows of its walker. (The weight's and the gate's gradient share the sum of G n while the
 // gate row stays the same.)  Every walker then writes its sums to the workspace and a second, small
 // kernel adds them in order, so no result depends on timing.  Bound by memory: 16384 x 4096 bf16,
-// 0.81 GB, 125 us, 97% of the measured copy's rate; rows off 16 bytes by the instructions that take
-// them value by value (16384 x 4095 bf16 284 us).
+// 0.81 GB, 125 us, 97% of the measured copy's rate; off 16 bytes it waits a row for the two warps
+// that cut its first and last piece (16384 x 4081 bf16 155 us, 173 with a slower cut; with every
+// row taken value by value 284).
 #include "zc_norm.cuh"
 
 namespace zc {
@@ -682,8 +683,8 @@ bool run_ring(NormBwdParams& p, uint32_t cluster, cudaStream_t stream, const Dev
   return true;
 }
 
-// The ring on rows off 16 bytes, but alike in all matrices, if its walkers can keep to rows that lie
-// alike and hold them.
+// The ring on rows off 16 bytes, but alike in all matrices, if its walkers can keep to rows that
+// lie alike and hold them.
 template <typename T>
 bool run_shifted(NormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e) {
   RowPlaces rows;

@@ -11,7 +11,7 @@
 
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -100,9 +100,15 @@ const Tensor& table(PyObject* o, at::IntArrayRef shape, at::ScalarType type, con
   return t;
 }
 
+// A new tensor, straight from torch's allocator of device memory: the way there through torch's
+// dispatcher takes 0.25 us more (a dispatch of 8 tokens 7.8 us of host time instead of 6.8).
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
+  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+}
+
 // The caller's output tensor, checked, or a new one.
 Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Tensor& like, const char* what) {
-  if (o == Py_None) return at::empty(shape, like.options().dtype(type));
+  if (o == Py_None) return fresh(shape, type, like);
   return table(o, shape, type, what);
 }
 
@@ -233,9 +239,8 @@ PyObject* moe_dispatch(Args a) {
   const int dtype = dtype_of(x.t);
   if (n > ZC_MOE_MAX_EXPERTS || k > ZC_MOE_MAX_K) check(ZC_ERR_TOO_LARGE, "zc_moe_dispatch");
   Tensor rows = output(a[4], {tokens * k, x.t.size(1)}, x.t.scalar_type(), x.t, "rows");
-  const auto ints = x.t.options().dtype(at::kInt);
-  Tensor positions = at::empty({tokens, k}, ints), slots = at::empty({tokens * k}, ints);
-  Tensor offsets = at::empty({static_cast<int64_t>(n) + 1}, ints);
+  Tensor positions = fresh({tokens, k}, at::kInt, x.t), slots = fresh({tokens * k}, at::kInt, x.t);
+  Tensor offsets = fresh({static_cast<int64_t>(n) + 1}, at::kInt, x.t);
   void* stream = stream_of(a[5], x.t);
   check(without_gil([&] {
           return zc_moe_dispatch(x.p(), dtype, x.stride, x.rows, static_cast<uint32_t>(x.width),
@@ -398,13 +403,13 @@ PyObject* norm_backward(Args a) {
   n.residual_scale = real(a[6]);
   n.eps = real(a[8]);
   const bool none = x.size(0) == 0;  // no tokens: nothing to launch, and the sums over none of them are zero
-  Tensor dy, dx = at::empty(x.sizes(), x.options()), grads[3];
-  if (branch) dy = at::empty(x.sizes(), x.options());
+  Tensor dy, dx = fresh(x.sizes(), x.scalar_type(), x), grads[3];
+  if (branch) dy = fresh(x.sizes(), x.scalar_type(), x);
   for (int i = 0; i < 3; i++) {
     PyObject* o = a[i == 0 ? 4 : i == 1 ? 5 : 7];
     if (o == Py_None) continue;
     const Tensor& p = THPVariable_Unpack(o);
-    grads[i] = none ? at::zeros(p.sizes(), p.options()) : at::empty(p.sizes(), p.options());
+    grads[i] = none ? at::zeros(p.sizes(), p.options()) : fresh(p.sizes(), p.scalar_type(), x);
   }
   if (!none) {
     const Tensor& ws = tensor(a[9], "ws");
