@@ -5,6 +5,8 @@
 // All but the router are bound by memory: each value is read or written once and takes a few
 // operations.  No result depends on the order of atomics (counts are whole numbers) and every sum
 // has a fixed order, so the same inputs give the same bits.
+#include <cfloat>
+
 #include "zc_internal.h"
 #include "zc_layer.cuh"
 
@@ -30,6 +32,20 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 // 1 / (1 + exp(-l)), each step rounded as the plain expression's (a correctly rounded reciprocal is
 // the quotient).
 __device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(__fadd_rn(1.f, expf(-l))); }
+
+// The hyperbolic tangent, good to 2^-11 of it (the instruction's stated error).
+__device__ __forceinline__ float tanh_estimate(float x) {
+  float y;
+  asm("tanh.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The largest of the warp's values, none of them NaN.
+__device__ __forceinline__ float warp_max_of(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // Lane l's N values of a row, N l .. N l + N - 1; minus infinity beyond the width.  VEC: they are
 // whole 4-, 8- or 16-byte pieces.
@@ -85,25 +101,24 @@ __device__ __forceinline__ float choice_of(const RouteParams& p, float l, uint32
 // lanes' best choices is a bound that at least K experts reach and few more do: those are gathered
 // in shared memory, a lane each, and every lane counts the ones before its own.  Where more than 32
 // reach it (equal logits, or too few lanes left open) the largest is taken K times instead, the
-// lowest expert on ties.  For the bound a sigmoid is good enough to 2^-20 (the fast exponential's
-// and divide's stated errors make 2^-21 of a value in 0..1, the exact one's own 2^-22): with the
-// bound lowered by twice that and the sums' rounding, no expert that belongs among the K stays out,
-// and the exact sigmoid is taken of those gathered alone, one a lane.  Bound by instructions: 16384
-// x 256 fp32, 8 taken with a bias, 12.6 us (softmax 10.3), its bytes 2.7.  With exact sigmoids of
-// all experts it took 15.0; sorting each lane's experts and taking the largest 8 times 16.5 (512
-// experts: 41 against 23); warps that stay and load the next token ahead 18.3, for fewer of them
-// fit an SM.
+// lowest expert on ties.  For the bound a sigmoid (1 + tanh(l / 2)) / 2 by the tanh instruction will
+// do, at most 2^-12 off: with the bound lowered by four times that and the sums' rounding, no expert
+// that belongs among the K stays out, and the exact sigmoid is taken of those gathered alone, one a
+// lane.  Bound by instructions, 560 a warp at 70% of the issue slots: 16384 x 256 fp32, 8 taken with
+// a bias, 10.8 us (softmax 9.5), its bytes 2.7.  With sigmoids good to 2^-20 for the bound and
+// choices compared as whole numbers it took 12.6, with exact sigmoids of all experts 15.0; sorting
+// each lane's experts and taking the largest 8 times 16.5 (512 experts: 41 against 15); warps that
+// stay and load the next token ahead 18.3, for fewer of them fit an SM.
 template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) {
-  __shared__ unsigned long long found[kRouteWarps][32];
+  __shared__ __align__(16) unsigned long long found[kRouteWarps][32];
   __shared__ float2 order[kRouteWarps][32];  // by rank: the expert, and its logit or its sigmoid
   pdl_begin();
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
   const uint64_t t = static_cast<uint64_t>(blockIdx.x) * kRouteWarps + warp;
   if (t >= p.tokens) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.stride;
-  float l[N];
-  uint32_t key[N];
+  float l[N], v[N];  // logits; choices, the sigmoid's estimated, NaN as infinity
   load_row<T, N, VEC>(row, p.experts, l);
   if (p.sigmoid) {
     float bias[N];
@@ -117,59 +132,65 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
     }
 #pragma unroll
     for (int j = 0; j < N; j++)
-      key[j] = order_key(l[j] == -INFINITY ? l[j] : __fdividef(1.f, 1.f + __expf(-l[j])) + bias[j]);
+      v[j] = l[j] == -INFINITY ? l[j] : fminf(fmaf(0.5f, tanh_estimate(0.5f * l[j]), 0.5f + bias[j]), INFINITY);
   } else {
 #pragma unroll
-    for (int j = 0; j < N; j++) key[j] = order_key(l[j]);
+    for (int j = 0; j < N; j++) v[j] = fminf(l[j], INFINITY);
   }
-  uint32_t bound;
+  float bound;
   {
-    uint32_t best = key[0];
+    float best = v[0];
 #pragma unroll
-    for (int j = 1; j < N; j++) best = max(best, key[j]);
+    for (int j = 1; j < N; j++) best = fmaxf(best, v[j]);
     uint32_t lanes = 0;
     while (true) {
-      bound = __reduce_max_sync(kFull, best);
-      if (bound <= kClosed) break;
+      bound = warp_max_of(best);
+      if (bound == -INFINITY) break;
       lanes += __popc(__ballot_sync(kFull, best == bound));
       if (lanes >= p.k) break;
-      best = best == bound ? 0 : best;
+      best = best == bound ? -INFINITY : best;
     }
-    if (p.sigmoid && bound > kClosed) {
-      const float b = __uint_as_float(bound & 0x80000000u ? bound ^ 0x80000000u : ~bound);  // order_key undone
-      if (fabsf(b) < INFINITY) bound = order_key(b - 0x1p-18f - fabsf(b) * 0x1p-20f);
-    }
-    bound = max(bound, kClosed + 1);
+    if (p.sigmoid && bound < INFINITY) bound -= 0x1p-10f + fabsf(bound) * 0x1p-20f;
+    bound = fmaxf(bound, -FLT_MAX);
   }
-  uint32_t n = 0;  // experts that reach it
+  uint32_t reach = 0;  // this lane's experts that reach it
 #pragma unroll
-  for (int j = 0; j < N; j++) {
-    const bool in = key[j] >= bound;
-    const uint32_t lanes = __ballot_sync(kFull, in), at = n + __popc(lanes & lanes_below());
-    if (in && at < 32) found[warp][at] = lane * N + j;
-    n += __popc(lanes);
+  for (int j = 0; j < N; j++) reach |= v[j] >= bound ? 1u << j : 0u;
+  uint32_t n = 0, at = 0;  // of the warp, and of the lanes below
+#pragma unroll
+  for (int b = 1; b <= N; b *= 2) {
+    const uint32_t lanes = __ballot_sync(kFull, __popc(reach) & b);
+    n += b * __popc(lanes);
+    at += b * __popc(lanes & lanes_below());
+  }
+  if (n <= 32) {
+    for (; reach; reach &= reach - 1) found[warp][at++] = lane * N + __ffs(reach) - 1;
   }
   uint32_t mine = kFull;
   float value = -INFINITY;  // of expert `mine`: its logit, or its sigmoid
   __syncwarp();
   if (n <= 32) {
     const uint32_t e = lane < n ? static_cast<uint32_t>(found[warp][lane]) : 0;
-    float v = lane < n ? to_f32<T>(row[e]) : -INFINITY, prob = 0.f;
-    const uint32_t exact = order_key(choice_of(p, v, e, &prob));
-    if (p.sigmoid) v = prob;
+    float mid = lane < n ? to_f32<T>(row[e]) : -INFINITY, prob = 0.f;
+    const uint32_t exact = order_key(choice_of(p, mid, e, &prob));
+    if (p.sigmoid) mid = prob;
     const unsigned long long own = lane < n ? static_cast<unsigned long long>(exact) << 32 | (kFull - e) : 0;
     __syncwarp();
     found[warp][lane] = own;
     __syncwarp();
     uint32_t before = 0;
-    for (uint32_t i = 0; i < n; i++) before += found[warp][i] > own;
-    if (lane < n) order[warp][before] = make_float2(__uint_as_float(e), v);
+    for (uint32_t i = 0; i < n; i += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&found[warp][i]);
+      before += (two.x > own) + (two.y > own);
+    }
+    if (lane < n) order[warp][before] = make_float2(__uint_as_float(e), mid);
     __syncwarp();
     if (lane < n && lane < p.k) {
       mine = __float_as_uint(order[warp][lane].x);
       value = order[warp][lane].y;
     }
   } else {
+    uint32_t key[N];
 #pragma unroll
     for (int j = 0; j < N; j++) {
       float prob;
