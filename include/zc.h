@@ -494,9 +494,8 @@ zc_status zq_decompress(const void* d_in, uint64_t in_bytes, uint64_t n, void* d
  * gradient.
  *   - Matrices are row-major; a *_stride is the distance of two rows of an
  *     input in values (0: every row is the same one); columns are contiguous.
- *     Outputs are contiguous.  Any alignment of the type is accepted; where every address,
- *     stride and width is a multiple of 16 bytes, values move in 16-byte
- *     pieces.
+ *     Outputs are contiguous.  Any alignment of the type is accepted; rows whose
+ *     addresses, strides and widths are multiples of 16 bytes are the fastest.
  *   - dtype (zc_dtype) is the type of the activations; computation is in fp32
  *     and each result is rounded once, to nearest even.
  *   - Sums have a fixed order: the same inputs give the same bits.
