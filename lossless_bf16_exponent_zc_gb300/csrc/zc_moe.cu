@@ -683,10 +683,11 @@ __global__ void __launch_bounds__(kCombineThreads, KU <= 2 ? 3 : 4) moe_combine_
 // The same for rows that lie off 16 bytes: a warp takes some of the units of a token's output
 // (RowCut).  Each slot's row has its own place relative to those pieces, found once by a lane and
 // kept in shared memory: the piece that output piece 0 starts in, and at which byte.  Bound by the
-// instructions that shift the pieces: 16384 x 4095 bf16 from 4 slots each 150 us, fp32, with half the
-// values a piece, 206, the copy's rate; with all of this found by every thread for itself 225 and 436.
+// instructions that shift the pieces: 16384 x 4095 bf16 from 4 slots each 138 us in 32 registers,
+// 154 in 40; fp32, with half the values a piece, 208, the copy's rate; with all of this found by
+// every thread for itself 225 and 436.
 constexpr uint32_t kAnySlots = 4;  // slots read at once
-constexpr uint32_t kAnyTurns = 4;  // units of a lane, where there are many
+constexpr uint32_t kAnyTurns = 4;  // units of a lane, where there are many (8: 164 us against 152)
 struct AnyRow {
   uint64_t at;  // 0: nothing to add
   uint32_t off;
@@ -694,7 +695,7 @@ struct AnyRow {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kCombineThreads) moe_combine_any_kernel(CombineParams p, uint32_t turns) {
+__global__ void __launch_bounds__(kCombineThreads, 8) moe_combine_any_kernel(CombineParams p, uint32_t turns) {
   constexpr int V = kPieceOf<T>;
   __shared__ AnyRow rows_of[kCombineThreads / 32][kMoeMaxK];
   pdl_begin();
@@ -966,6 +967,7 @@ cudaError_t combine(CombineParams& p, bool vec, cudaStream_t stream, const Devic
     const uint64_t turns_all = ceil_div(any_units<T>(p.hidden), 32);
     uint64_t turns = p.tokens * turns_all / (64ull * static_cast<uint64_t>(dev.sm_count));
     turns = turns < 1 ? 1 : turns > kAnyTurns ? kAnyTurns : turns;
+    turns = ceil_div(turns_all, ceil_div(turns_all, turns));  // evenly over a token's warps
     uint32_t each = static_cast<uint32_t>(turns);
     const uint64_t grid = ceil_div(p.tokens * ceil_div(turns_all, turns), kCombineThreads / 32);
     if (grid == 0) return cudaSuccess;
@@ -993,7 +995,9 @@ cudaError_t combine_bwd(CombineBwdParams& p, cudaStream_t stream, const DeviceIn
   // hold a piece a thread.
   const bool few = p.tokens < 2ull * static_cast<uint64_t>(dev.sm_count);
   const uint32_t split = few ? static_cast<uint32_t>(ceil_div(p.k, kCombineBwdK<VEC>)) : 1;
-  if (pieces <= 64)
+  // a warp a token while that is a few turns: 16384 x 640 bf16 32.8 us against 38.1 by two warps, 2048 92.4
+  // against 90.8 by four
+  if (pieces <= (few ? 64 : 128))
     return run(moe_combine_bwd_kernel<T, VEC, true>, ceil_div(p.tokens, 4), split, 128, stream, &p);
   // a piece a thread up to 16 warps, or 8 warps in whole turns; off 16 bytes 4 (16384 x 4095 bf16 254 us
   // against 303)

@@ -233,6 +233,16 @@ def test_rows_off_sixteen_bytes(norm, hidden, dtype, before, after):
     check(norm, d)
 
 
+@pytest.mark.parametrize("hidden", [515, 1531, 4081, 4095])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_in_place_off_sixteen_bytes(norm, hidden, dtype):
+    """x_new over x where neighbouring rows share 16 bytes."""
+    d = make(hidden, 2000, hidden, dtype, "f32", "token", True)
+    want = norm.post_norm(d["y"], d["x"], d["w"], gate=d["gate"], next_weight=d["w2"])
+    got = norm.post_norm(d["y"], d["x"], d["w"], gate=d["gate"], next_weight=d["w2"], x_new=d["x"])
+    assert got[0] is d["x"] and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("hidden", [515, 1531, 4085])
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 def test_a_row_of_nan_stays_alone(norm, hidden, dtype):
