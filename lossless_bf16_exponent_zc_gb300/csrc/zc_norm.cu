@@ -268,8 +268,9 @@ cudaError_t run_width(NormParams& p, cudaStream_t stream, const DeviceInfo& dev)
     if (d <= 512) return run_shape<T, V, 16 / V, true, kWarp>(p, kWarp, stream, dev);
     if (d <= 1024 && p.tokens >= 16ull * static_cast<uint64_t>(dev.sm_count))
       return run_shape<T, V, 32 / V, true, kWarp>(p, kWarp, stream, dev);
-  } else if (d <= 512) {
-    return run_shape<T, V, 16, true, kWarp>(p, kWarp, stream, dev);
+  } else {
+    if (d <= 256) return run_shape<T, V, 8, true, kWarp>(p, kWarp, stream, dev);
+    if (d <= 512) return run_shape<T, V, 16, true, kWarp>(p, kWarp, stream, dev);
   }
   cudaError_t e;
   if constexpr (V == 1) {

@@ -214,6 +214,13 @@ def test_views_expanded_gradients_and_in_place(norm):
     assert got[0] is x and torch.equal(x, want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("hidden", [1, 3, 65, 129, 255])
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "narrow"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_narrow_odd_rows(norm, hidden, gate, dtype):
+    check(norm, make(hidden, 6000, hidden, dtype, "f32", gate, True))
+
+
 def inside(t, before, after):
     """The same matrix as columns of a wider one that holds NaN elsewhere."""
     wide = torch.full((t.shape[0], before + t.shape[1] + after), math.nan, dtype=t.dtype, device=t.device)
