@@ -226,10 +226,11 @@ __device__ __forceinline__ void block_sum_f32(float (&v)[N], float* red) {
 // keeps half of the values and gives the others to its partner, until the lanes of group g (of 32 /
 // N lanes) hold value g; the rest is a tree inside the group.  The CTA's partial sums are added the
 // same way.  `red`: N x kSumSlots floats, 16-byte aligned, those of absent warps zero (the caller
-// clears them all before the first use); as above, two sums in a row need two buffers.  CLUSTER:
-// over all `ctas` CTAs of the cluster, this one being `rank`; every CTA leaves its partial sums in
-// all of them (a sum of two barriers, the CTA's and the cluster's, would wait twice).  kSumSlots:
-// 16 warps each of up to 4 CTAs, or 32 of one.
+// clears them all before the first use, with a barrier of the CTA or the cluster in between,
+// whatever the instance: the slots of a warp are cleared by others); as above, two sums in a row
+// need two buffers.  CLUSTER: over all `ctas` CTAs of the cluster, this one being `rank`; every CTA
+// leaves its partial sums in all of them (a sum of two barriers, the CTA's and the cluster's, would
+// wait twice).  kSumSlots: 16 warps each of up to 4 CTAs, or 32 of one.
 constexpr int kSumSlots = 64;
 template <int N, bool CLUSTER = false>
 __device__ __forceinline__ void block_sum_shared(float (&v)[N], float* red, uint32_t rank = 0, uint32_t ctas = 1) {

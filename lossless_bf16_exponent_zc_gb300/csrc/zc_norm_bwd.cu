@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_bwd_ring_kernel(Norm
   __shared__ __align__(16) float red[2][4 * kSumSlots];
   pdl_allow_dependents();
   for (uint32_t i = threadIdx.x; i < 8 * kSumSlots; i += blockDim.x) red[0][i] = 0.f;
+  __syncthreads();  // a warp's slots are cleared by others, and the first sum may be next
   if (CLUSTER) {  // every CTA's sums are cleared before another writes there
     cluster_arrive();
     cluster_wait();
