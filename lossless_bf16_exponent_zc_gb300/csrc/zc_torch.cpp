@@ -13,10 +13,13 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <string>
 
 #include "zc.h"
@@ -100,18 +103,6 @@ const Tensor& table(PyObject* o, at::IntArrayRef shape, at::ScalarType type, con
   return t;
 }
 
-// A new tensor, straight from torch's allocator of device memory: the way there through torch's
-// dispatcher takes 0.25 us more (a dispatch of 8 tokens 7.8 us of host time instead of 6.8).
-Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
-  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
-}
-
-// The caller's output tensor, checked, or a new one.
-Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Tensor& like, const char* what) {
-  if (o == Py_None) return fresh(shape, type, like);
-  return table(o, shape, type, what);
-}
-
 int score_of(PyObject* o) {
   const char* s = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : nullptr;
   if (s && std::string(s) == "softmax") return ZC_SOFTMAX;
@@ -138,16 +129,55 @@ float real(PyObject* o) {
   return static_cast<float>(v);
 }
 
-// The cudaStream_t to launch on: the given torch stream, else the current one of `like`'s device.
-void* stream_of(PyObject* o, const Tensor& like) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(like.device().index()).stream();
-  PyObject* raw = PyObject_GetAttrString(o, "cuda_stream");
-  if (!raw) throw Raised();
-  void* s = PyLong_AsVoidPtr(raw);
-  Py_DECREF(raw);
-  if (PyErr_Occurred()) throw Raised();
-  return s;
-}
+// Where a call launches: on the given torch stream, else on the current one of the activations'
+// device.  Its outputs come from the allocator for that stream, for a block is only safe to write on
+// the stream that it was last used on: a given stream is the current one while the call lasts.  What
+// it makes there is also recorded on the stream that was current before, so that the caller may use
+// and drop it on either (once ordered behind the launch).
+class Launch {
+ public:
+  Launch(PyObject* stream, const Tensor& like) : device_(like.device()) {
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(device_.index());
+    stream_ = current.stream();
+    if (stream == Py_None) return;
+    PyObject* raw = PyObject_GetAttrString(stream, "cuda_stream");
+    if (!raw) throw Raised();
+    void* s = PyLong_AsVoidPtr(raw);
+    Py_DECREF(raw);
+    if (PyErr_Occurred()) throw Raised();
+    if (s == stream_) return;
+    stream_ = s;
+    caller_ = current;
+    given_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), device_.index()));
+  }
+
+  void* stream() const { return stream_; }
+
+  // A new tensor, straight from torch's allocator of device memory: the way there through torch's
+  // dispatcher takes 0.25 us more (a dispatch of 8 tokens 7.8 us of host time instead of 6.8).
+  Tensor fresh(at::IntArrayRef shape, at::ScalarType type) const {
+    return kept(at::detail::empty_cuda(shape, type, device_, std::nullopt));
+  }
+  Tensor zeros(at::IntArrayRef shape, at::ScalarType type) const {
+    return kept(at::zeros(shape, at::TensorOptions(type).device(device_)));
+  }
+  // The caller's output tensor, checked, or a new one.
+  Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const char* what) const {
+    if (o == Py_None) return fresh(shape, type);
+    return table(o, shape, type, what);
+  }
+
+ private:
+  Tensor kept(Tensor t) const {
+    if (caller_) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *caller_);
+    return t;
+  }
+
+  c10::Device device_;
+  void* stream_;
+  std::optional<c10::cuda::CUDAStream> caller_;  // with a given stream: the current one before
+  std::optional<c10::cuda::CUDAStreamGuard> given_;
+};
 
 PyObject* pack(std::initializer_list<Tensor> ts) {
   PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
@@ -189,13 +219,13 @@ PyObject* moe_route(Args a) {
   if (a[3] != Py_None) bias = static_cast<const float*>(table(a[3], {l.t.size(1)}, at::kFloat, "bias").const_data_ptr());
   const float scale = real(a[5]);
   if (k > ZC_MOE_MAX_K) check(ZC_ERR_TOO_LARGE, "zc_moe_route");  // before outputs of that size are made
-  Tensor weights = output(a[6], {tokens, k}, at::kFloat, l.t, "weights");
-  Tensor experts = output(a[7], {tokens, k}, at::kInt, l.t, "experts");
-  void* stream = stream_of(a[8], l.t);
+  const Launch on(a[8], l.t);
+  Tensor weights = on.output(a[6], {tokens, k}, at::kFloat, "weights");
+  Tensor experts = on.output(a[7], {tokens, k}, at::kInt, "experts");
   check(without_gil([&] {
           return zc_moe_route(l.p(), dtype, l.stride, l.rows, static_cast<uint32_t>(l.width), k, score, bias,
                               renormalize, scale, static_cast<float*>(weights.mutable_data_ptr()),
-                              static_cast<int32_t*>(experts.mutable_data_ptr()), stream);
+                              static_cast<int32_t*>(experts.mutable_data_ptr()), on.stream());
         }),
         "zc_moe_route");
   return pack({weights, experts});
@@ -211,13 +241,13 @@ PyObject* moe_route_backward(Args a) {
   const Tensor& dweights = table(a[0], {tokens, k}, at::kFloat, "dweights");
   const int dtype = dtype_of(l.t), score = score_of(a[3]), renormalize = PyObject_IsTrue(a[4]);
   const float scale = real(a[5]);
-  Tensor dlogits = output(a[6], l.t.sizes(), l.t.scalar_type(), l.t, "dlogits");
-  void* stream = stream_of(a[7], l.t);
+  const Launch on(a[7], l.t);
+  Tensor dlogits = on.output(a[6], l.t.sizes(), l.t.scalar_type(), "dlogits");
   check(without_gil([&] {
           return zc_moe_route_backward(static_cast<const float*>(dweights.const_data_ptr()), l.p(), dtype, l.stride,
                                        l.rows, static_cast<uint32_t>(l.width), static_cast<uint32_t>(k),
                                        static_cast<const int32_t*>(experts.const_data_ptr()), score, renormalize,
-                                       scale, dlogits.mutable_data_ptr(), stream);
+                                       scale, dlogits.mutable_data_ptr(), on.stream());
         }),
         "zc_moe_route_backward");
   return pack({dlogits});
@@ -238,10 +268,10 @@ PyObject* moe_dispatch(Args a) {
   if (!ws.is_contiguous()) refuse("libzc takes contiguous tensors");
   const int dtype = dtype_of(x.t);
   if (n > ZC_MOE_MAX_EXPERTS || k > ZC_MOE_MAX_K) check(ZC_ERR_TOO_LARGE, "zc_moe_dispatch");
-  Tensor rows = output(a[4], {tokens * k, x.t.size(1)}, x.t.scalar_type(), x.t, "rows");
-  Tensor positions = fresh({tokens, k}, at::kInt, x.t), slots = fresh({tokens * k}, at::kInt, x.t);
-  Tensor offsets = fresh({static_cast<int64_t>(n) + 1}, at::kInt, x.t);
-  void* stream = stream_of(a[5], x.t);
+  const Launch on(a[5], x.t);
+  Tensor rows = on.output(a[4], {tokens * k, x.t.size(1)}, x.t.scalar_type(), "rows");
+  Tensor positions = on.fresh({tokens, k}, at::kInt), slots = on.fresh({tokens * k}, at::kInt);
+  Tensor offsets = on.fresh({static_cast<int64_t>(n) + 1}, at::kInt);
   check(without_gil([&] {
           return zc_moe_dispatch(x.p(), dtype, x.stride, x.rows, static_cast<uint32_t>(x.width),
                                  experts.const_data_ptr(), experts.scalar_type() == at::kLong,
@@ -249,7 +279,7 @@ PyObject* moe_dispatch(Args a) {
                                  static_cast<int32_t*>(positions.mutable_data_ptr()),
                                  static_cast<int32_t*>(slots.mutable_data_ptr()),
                                  static_cast<int32_t*>(offsets.mutable_data_ptr()), ws.mutable_data_ptr(),
-                                 static_cast<uint64_t>(ws.nbytes()), stream);
+                                 static_cast<uint64_t>(ws.nbytes()), on.stream());
         }),
         "zc_moe_dispatch");
   return pack({rows, positions, slots, offsets});
@@ -272,14 +302,14 @@ PyObject* moe_combine(Args a) {
   if (a[1] != Py_None)
     weights = static_cast<const float*>(table(a[1], {tokens, k}, at::kFloat, "weights").const_data_ptr());
   const Tensor& status = table(a[3], {1}, at::kInt, "status");
-  Tensor out = output(a[4], {tokens, r.t.size(1)}, r.t.scalar_type(), r.t, "out");
-  void* stream = stream_of(a[5], r.t);
+  const Launch on(a[5], r.t);
+  Tensor out = on.output(a[4], {tokens, r.t.size(1)}, r.t.scalar_type(), "out");
   check(without_gil([&] {
           return zc_moe_combine(r.p(), dtype, r.stride, r.rows, weights,
                                 static_cast<const int32_t*>(positions.const_data_ptr()),
                                 static_cast<uint64_t>(tokens), static_cast<uint32_t>(k),
                                 static_cast<uint32_t>(r.width), out.mutable_data_ptr(),
-                                static_cast<int32_t*>(status.mutable_data_ptr()), stream);
+                                static_cast<int32_t*>(status.mutable_data_ptr()), on.stream());
         }),
         "zc_moe_combine");
   return pack({out});
@@ -295,15 +325,16 @@ PyObject* moe_combine_backward(Args a) {
   const int dtype = dtype_of(r.t);
   const Tensor& weights = table(a[2], {tokens, k}, at::kFloat, "weights");
   const Tensor& status = table(a[4], {1}, at::kInt, "status");
-  Tensor drows = output(a[5], r.t.sizes(), r.t.scalar_type(), r.t, "drows");
-  Tensor dweights = output(a[6], {tokens, k}, at::kFloat, r.t, "dweights");
-  void* stream = stream_of(a[7], r.t);
+  const Launch on(a[7], r.t);
+  Tensor drows = on.output(a[5], r.t.sizes(), r.t.scalar_type(), "drows");
+  Tensor dweights = on.output(a[6], {tokens, k}, at::kFloat, "dweights");
   check(without_gil([&] {
           return zc_moe_combine_backward(
               g.p(), dtype, g.stride, r.p(), r.stride, r.rows, static_cast<const float*>(weights.const_data_ptr()),
               static_cast<const int32_t*>(positions.const_data_ptr()), static_cast<uint64_t>(tokens),
               static_cast<uint32_t>(k), static_cast<uint32_t>(r.width), drows.mutable_data_ptr(),
-              static_cast<float*>(dweights.mutable_data_ptr()), static_cast<int32_t*>(status.mutable_data_ptr()), stream);
+              static_cast<float*>(dweights.mutable_data_ptr()), static_cast<int32_t*>(status.mutable_data_ptr()),
+              on.stream());
         }),
         "zc_moe_combine_backward");
   return pack({drows, dweights});
@@ -363,13 +394,13 @@ PyObject* norm_forward(Args a) {
   norm_params(n, x.t, a[2], a[3], a[5]);
   n.residual_scale = real(a[4]);
   n.eps = real(a[6]);
+  const Launch on(a[9], x.t);
   Tensor x_new, h;
-  if (branch) x_new = output(a[7], x.t.sizes(), x.t.scalar_type(), x.t, "x_new");
-  if (a[5] != Py_None) h = output(a[8], x.t.sizes(), x.t.scalar_type(), x.t, branch ? "h" : "out");
+  if (branch) x_new = on.output(a[7], x.t.sizes(), x.t.scalar_type(), "x_new");
+  if (a[5] != Py_None) h = on.output(a[8], x.t.sizes(), x.t.scalar_type(), branch ? "h" : "out");
   if (x_new.defined()) n.x_new = x_new.mutable_data_ptr();
   if (h.defined()) n.h = h.mutable_data_ptr();
-  void* stream = stream_of(a[9], x.t);
-  check(without_gil([&] { return zc_norm(&n, stream); }), "zc_norm");
+  check(without_gil([&] { return zc_norm(&n, on.stream()); }), "zc_norm");
   return pack({x_new, h});
 }
 
@@ -403,13 +434,14 @@ PyObject* norm_backward(Args a) {
   n.residual_scale = real(a[6]);
   n.eps = real(a[8]);
   const bool none = x.size(0) == 0;  // no tokens: nothing to launch, and the sums over none of them are zero
-  Tensor dy, dx = fresh(x.sizes(), x.scalar_type(), x), grads[3];
-  if (branch) dy = fresh(x.sizes(), x.scalar_type(), x);
+  const Launch on(a[10], x);
+  Tensor dy, dx = on.fresh(x.sizes(), x.scalar_type()), grads[3];
+  if (branch) dy = on.fresh(x.sizes(), x.scalar_type());
   for (int i = 0; i < 3; i++) {
     PyObject* o = a[i == 0 ? 4 : i == 1 ? 5 : 7];
     if (o == Py_None) continue;
     const Tensor& p = THPVariable_Unpack(o);
-    grads[i] = none ? at::zeros(p.sizes(), p.options()) : fresh(p.sizes(), p.scalar_type(), x);
+    grads[i] = none ? on.zeros(p.sizes(), p.scalar_type()) : on.fresh(p.sizes(), p.scalar_type());
   }
   if (!none) {
     const Tensor& ws = tensor(a[9], "ws");
@@ -421,8 +453,7 @@ PyObject* norm_backward(Args a) {
     if (grads[2].defined()) n.dnext_weight = grads[2].mutable_data_ptr();
     n.ws = ws.mutable_data_ptr();
     n.ws_bytes = static_cast<uint64_t>(ws.nbytes());
-    void* stream = stream_of(a[10], x);
-    check(without_gil([&] { return zc_norm_backward(&n, stream); }), "zc_norm_backward");
+    check(without_gil([&] { return zc_norm_backward(&n, on.stream()); }), "zc_norm_backward");
   }
   return pack({dy, dx, grads[0], grads[1], grads[2]});
 }

@@ -6,9 +6,13 @@
     out = moe.combine(rows_back, weights, plan.positions, status)
 
 and the gradients of all three (``torch.ops.zc.moe_*`` has them with autograd).  Every step runs in libzc's kernels
-(zc_moe_* in include/zc.h, where the operators are defined) on the current torch stream, or the one given; arguments are
-checked, and outputs that are not given allocated, in the native extension (csrc/zc_torch.cpp).  Activations are bfloat16, float16 or float32 matrices whose rows may be strided; weights are float32,
-expert ids int32 (or int64, in dispatch).
+(zc_moe_* in include/zc.h, where the operators are defined); arguments are checked, and outputs that are not given
+allocated, in the native extension (csrc/zc_torch.cpp).  Activations are bfloat16, float16 or float32 matrices whose rows
+may be strided; weights are float32, expert ids int32 (or int64, in dispatch).
+
+Calls run on the current torch stream, or on the one given as ``stream``.  On a given stream, what it reads and the
+outputs it is handed must be ready there (``stream.wait_stream(...)``) and stay alive until it has run; outputs it makes
+are that stream's, to be used elsewhere once that place waits for it.
 """
 from __future__ import annotations
 
@@ -22,6 +26,7 @@ from . import zc
 
 MAX_K = 32
 MAX_EXPERTS = 1024
+
 
 class DispatchPlan(NamedTuple):
     """Where dispatch put every slot (token * k + j) of the token-to-expert assignment."""

@@ -6,10 +6,13 @@
 post_norm closes one block and opens the next: x_new = a x + gate * rmsnorm(y) * weight, and h = rmsnorm(x_new) *
 next_weight (None: no h).  A gate has one row for all tokens, or a row for each run of tokens / rows of them (a
 sequence each, say), of hidden values or of one.  The kernels are zc_norm and zc_norm_backward (include/zc.h, where the
-operators are defined), on the current torch stream or the one given; arguments are checked, and outputs that are
-not given allocated, in the native extension (csrc/zc_torch.cpp).  Activations are
-bfloat16, float16 or float32 matrices whose rows may be strided; weights and gate share a type, the activations' or
-float32.
+operators are defined); arguments are checked, and outputs that are not given allocated, in the native extension
+(csrc/zc_torch.cpp).  Activations are bfloat16, float16 or float32 matrices whose rows may be strided; weights and gate
+share a type, the activations' or float32.
+
+Calls run on the current torch stream, or on the one given as ``stream``.  On a given stream, what it reads and the
+outputs it is handed must be ready there (``stream.wait_stream(...)``) and stay alive until it has run; outputs it makes
+are that stream's, to be used elsewhere once that place waits for it.
 """
 from __future__ import annotations
 
