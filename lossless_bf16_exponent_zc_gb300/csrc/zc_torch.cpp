@@ -54,14 +54,29 @@ std::string shape_of(const Tensor& t) {
   return s + ")";
 }
 
+// A torch.Tensor or of a class derived from it (isinstance() would ask the metaclass, 0.1 us a float).
+bool is_tensor(PyObject* o) { return PyObject_TypeCheck(o, reinterpret_cast<PyTypeObject*>(THPVariableClass)); }
+
 const Tensor& tensor(PyObject* o, const char* what) {
-  if (!THPVariable_Check(o)) {
+  if (!is_tensor(o)) {
     PyErr_Format(PyExc_TypeError, "%s must be a tensor", what);
     throw Raised();
   }
-  const Tensor& t = THPVariable_Unpack(o);
-  if (!t.is_cuda()) refuse("libzc takes CUDA tensors");
-  return t;
+  return THPVariable_Unpack(o);
+}
+
+// The kernels read and write all of a call's tensors on one device (checked before anything else).
+void one_device(PyObject* const* args, Py_ssize_t n) {
+  const Tensor* first = nullptr;
+  for (Py_ssize_t i = 0; i < n; i++) {
+    if (!is_tensor(args[i])) continue;
+    const Tensor& t = THPVariable_Unpack(args[i]);
+    if (!t.is_cuda()) refuse("libzc takes CUDA tensors");
+    if (!first)
+      first = &t;
+    else if (t.device() != first->device())
+      refuse("the tensors are on more than one device: " + first->device().str() + " and " + t.device().str());
+  }
 }
 
 int dtype_of(const Tensor& t) {
@@ -129,14 +144,15 @@ float real(PyObject* o) {
   return static_cast<float>(v);
 }
 
-// Where a call launches: on the given torch stream, else on the current one of the activations'
-// device.  Its outputs come from the allocator for that stream, for a block is only safe to write on
+// Where a call launches: on the activations' device, which is the current one while the call lasts,
+// and there on the given torch stream, else on the current one.  Its outputs come from the allocator for that stream, for a block is only safe to write on
 // the stream that it was last used on: a given stream is the current one while the call lasts.  What
 // it makes there is also recorded on the stream that was current before, so that the caller may use
 // and drop it on either (once ordered behind the launch).
 class Launch {
  public:
   Launch(PyObject* stream, const Tensor& like) : device_(like.device()) {
+    if (c10::cuda::current_device() != device_.index()) current_.set_device(device_);
     const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(device_.index());
     stream_ = current.stream();
     if (stream == Py_None) return;
@@ -145,6 +161,12 @@ class Launch {
     void* s = PyLong_AsVoidPtr(raw);
     Py_DECREF(raw);
     if (PyErr_Occurred()) throw Raised();
+    PyObject* index = PyObject_GetAttrString(stream, "device_index");
+    if (!index) PyErr_Clear();  // a handle alone
+    const long on = index ? PyLong_AsLong(index) : device_.index();
+    Py_XDECREF(index);
+    if (PyErr_Occurred()) throw Raised();
+    if (on != device_.index()) refuse("the stream is on another device than the tensors");
     if (s == stream_) return;
     stream_ = s;
     caller_ = current;
@@ -174,6 +196,7 @@ class Launch {
   }
 
   c10::Device device_;
+  c10::cuda::OptionalCUDAGuard current_;
   void* stream_;
   std::optional<c10::cuda::CUDAStream> caller_;  // with a given stream: the current one before
   std::optional<c10::cuda::CUDAStreamGuard> given_;
@@ -468,6 +491,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
     // Outputs are new tensors outside autograd: their creation goes straight to the allocation.
     at::AutoDispatchBelowADInplaceOrView plain;
+    one_device(args, n);
     return F(args);
   } catch (const Raised&) {
     return nullptr;
