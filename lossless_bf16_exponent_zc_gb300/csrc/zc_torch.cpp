@@ -138,6 +138,12 @@ uint32_t count(PyObject* o, const char* what) {
   return v > 0x7FFFFFFFl ? 0x7FFFFFFFu : static_cast<uint32_t>(v);
 }
 
+// A size that the C ABI takes as 32 bits and refuses as too large from 2^31 on.
+uint32_t narrow(uint64_t size, const char* where) {
+  if (size > 0x7FFFFFFFull) check(ZC_ERR_TOO_LARGE, where);
+  return static_cast<uint32_t>(size);
+}
+
 float real(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Raised();
@@ -145,10 +151,11 @@ float real(PyObject* o) {
 }
 
 // Where a call launches: on the activations' device, which is the current one while the call lasts,
-// and there on the given torch stream, else on the current one.  Its outputs come from the allocator for that stream, for a block is only safe to write on
-// the stream that it was last used on: a given stream is the current one while the call lasts.  What
-// it makes there is also recorded on the stream that was current before, so that the caller may use
-// and drop it on either (once ordered behind the launch).
+// and there on the given torch stream, else on the current one.  Its outputs come from the
+// allocator for that stream, for a block is only safe to write on the stream that it was last used
+// on: a given stream is the current one while the call lasts.  What it makes there is also recorded
+// on the stream that was current before, so that the caller may use and drop it on either (once
+// ordered behind the launch).
 class Launch {
  public:
   Launch(PyObject* stream, const Tensor& like) : device_(like.device()) {
@@ -241,13 +248,14 @@ PyObject* moe_route(Args a) {
   const float* bias = nullptr;
   if (a[3] != Py_None) bias = static_cast<const float*>(table(a[3], {l.t.size(1)}, at::kFloat, "bias").const_data_ptr());
   const float scale = real(a[5]);
+  const uint32_t width = narrow(l.width, "zc_moe_route");
   if (k > ZC_MOE_MAX_K) check(ZC_ERR_TOO_LARGE, "zc_moe_route");  // before outputs of that size are made
   const Launch on(a[8], l.t);
   Tensor weights = on.output(a[6], {tokens, k}, at::kFloat, "weights");
   Tensor experts = on.output(a[7], {tokens, k}, at::kInt, "experts");
   check(without_gil([&] {
-          return zc_moe_route(l.p(), dtype, l.stride, l.rows, static_cast<uint32_t>(l.width), k, score, bias,
-                              renormalize, scale, static_cast<float*>(weights.mutable_data_ptr()),
+          return zc_moe_route(l.p(), dtype, l.stride, l.rows, width, k, score, bias, renormalize, scale,
+                              static_cast<float*>(weights.mutable_data_ptr()),
                               static_cast<int32_t*>(experts.mutable_data_ptr()), on.stream());
         }),
         "zc_moe_route");
@@ -264,11 +272,13 @@ PyObject* moe_route_backward(Args a) {
   const Tensor& dweights = table(a[0], {tokens, k}, at::kFloat, "dweights");
   const int dtype = dtype_of(l.t), score = score_of(a[3]), renormalize = PyObject_IsTrue(a[4]);
   const float scale = real(a[5]);
+  const uint32_t width = narrow(l.width, "zc_moe_route_backward");
+  const uint32_t slots = narrow(static_cast<uint64_t>(k), "zc_moe_route_backward");
   const Launch on(a[7], l.t);
   Tensor dlogits = on.output(a[6], l.t.sizes(), l.t.scalar_type(), "dlogits");
   check(without_gil([&] {
           return zc_moe_route_backward(static_cast<const float*>(dweights.const_data_ptr()), l.p(), dtype, l.stride,
-                                       l.rows, static_cast<uint32_t>(l.width), static_cast<uint32_t>(k),
+                                       l.rows, width, slots,
                                        static_cast<const int32_t*>(experts.const_data_ptr()), score, renormalize,
                                        scale, dlogits.mutable_data_ptr(), on.stream());
         }),
@@ -290,16 +300,16 @@ PyObject* moe_dispatch(Args a) {
   const Tensor& ws = tensor(a[3], "ws");
   if (!ws.is_contiguous()) refuse("libzc takes contiguous tensors");
   const int dtype = dtype_of(x.t);
+  const uint32_t hidden = narrow(x.width, "zc_moe_dispatch");
   if (n > ZC_MOE_MAX_EXPERTS || k > ZC_MOE_MAX_K) check(ZC_ERR_TOO_LARGE, "zc_moe_dispatch");
   const Launch on(a[5], x.t);
   Tensor rows = on.output(a[4], {tokens * k, x.t.size(1)}, x.t.scalar_type(), "rows");
   Tensor positions = on.fresh({tokens, k}, at::kInt), slots = on.fresh({tokens * k}, at::kInt);
   Tensor offsets = on.fresh({static_cast<int64_t>(n) + 1}, at::kInt);
   check(without_gil([&] {
-          return zc_moe_dispatch(x.p(), dtype, x.stride, x.rows, static_cast<uint32_t>(x.width),
-                                 experts.const_data_ptr(), experts.scalar_type() == at::kLong,
-                                 static_cast<uint32_t>(k), n, rows.mutable_data_ptr(),
-                                 static_cast<int32_t*>(positions.mutable_data_ptr()),
+          return zc_moe_dispatch(x.p(), dtype, x.stride, x.rows, hidden, experts.const_data_ptr(),
+                                 experts.scalar_type() == at::kLong, static_cast<uint32_t>(k), n,
+                                 rows.mutable_data_ptr(), static_cast<int32_t*>(positions.mutable_data_ptr()),
                                  static_cast<int32_t*>(slots.mutable_data_ptr()),
                                  static_cast<int32_t*>(offsets.mutable_data_ptr()), ws.mutable_data_ptr(),
                                  static_cast<uint64_t>(ws.nbytes()), on.stream());
@@ -321,6 +331,7 @@ PyObject* moe_combine(Args a) {
   const Tensor& positions = positions_of(a[2]);
   const int64_t tokens = positions.size(0), k = positions.size(1);
   const int dtype = dtype_of(r.t);
+  const uint32_t hidden = narrow(r.width, "zc_moe_combine"), slots = narrow(static_cast<uint64_t>(k), "zc_moe_combine");
   const float* weights = nullptr;
   if (a[1] != Py_None)
     weights = static_cast<const float*>(table(a[1], {tokens, k}, at::kFloat, "weights").const_data_ptr());
@@ -330,8 +341,7 @@ PyObject* moe_combine(Args a) {
   check(without_gil([&] {
           return zc_moe_combine(r.p(), dtype, r.stride, r.rows, weights,
                                 static_cast<const int32_t*>(positions.const_data_ptr()),
-                                static_cast<uint64_t>(tokens), static_cast<uint32_t>(k),
-                                static_cast<uint32_t>(r.width), out.mutable_data_ptr(),
+                                static_cast<uint64_t>(tokens), slots, hidden, out.mutable_data_ptr(),
                                 static_cast<int32_t*>(status.mutable_data_ptr()), on.stream());
         }),
         "zc_moe_combine");
@@ -346,6 +356,8 @@ PyObject* moe_combine_backward(Args a) {
   if (g.t.scalar_type() != r.t.scalar_type() || g.t.size(0) != tokens || g.width != r.width)
     refuse("dout must be [tokens, hidden] in the rows' type");
   const int dtype = dtype_of(r.t);
+  const uint32_t hidden = narrow(r.width, "zc_moe_combine_backward");
+  const uint32_t slots = narrow(static_cast<uint64_t>(k), "zc_moe_combine_backward");
   const Tensor& weights = table(a[2], {tokens, k}, at::kFloat, "weights");
   const Tensor& status = table(a[4], {1}, at::kInt, "status");
   const Launch on(a[7], r.t);
@@ -355,9 +367,8 @@ PyObject* moe_combine_backward(Args a) {
           return zc_moe_combine_backward(
               g.p(), dtype, g.stride, r.p(), r.stride, r.rows, static_cast<const float*>(weights.const_data_ptr()),
               static_cast<const int32_t*>(positions.const_data_ptr()), static_cast<uint64_t>(tokens),
-              static_cast<uint32_t>(k), static_cast<uint32_t>(r.width), drows.mutable_data_ptr(),
-              static_cast<float*>(dweights.mutable_data_ptr()), static_cast<int32_t*>(status.mutable_data_ptr()),
-              on.stream());
+              slots, hidden, drows.mutable_data_ptr(), static_cast<float*>(dweights.mutable_data_ptr()),
+              static_cast<int32_t*>(status.mutable_data_ptr()), on.stream());
         }),
         "zc_moe_combine_backward");
   return pack({drows, dweights});
