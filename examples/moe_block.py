@@ -22,16 +22,19 @@ ops = torch.ops.zc
 
 
 class ZippedExchange(torch.autograd.Function):
-    """Rows sorted by destination rank to their ranks, compressed with the exact histogram's codebook of what is sent."""
+    """Rows sorted by destination rank to their ranks, compressed with the exact histogram's codebook of what is sent.
+    Rows behind those (of slots that are not routed) stay here and get no gradient."""
 
     @staticmethod
     def forward(ctx, rows, send, recv, status):
-        ctx.send, ctx.recv, ctx.status = send, recv, status
+        ctx.send, ctx.recv, ctx.status, ctx.rows = send, recv, status, rows.shape[0]
         return ZippedExchange.move(rows, send, recv, status)
 
     @staticmethod
     def backward(ctx, drows):
-        return ZippedExchange.move(drows.contiguous(), ctx.recv, ctx.send, ctx.status), None, None, None
+        back = ZippedExchange.move(drows.contiguous(), ctx.recv, ctx.send, ctx.status)
+        kept = back.new_zeros((ctx.rows - back.shape[0], back.shape[1]))
+        return torch.cat([back, kept]) if len(kept) else back, None, None, None
 
     @staticmethod
     def move(rows, send, recv, status):
