@@ -26,22 +26,23 @@ class ZippedExchange(torch.autograd.Function):
     Rows behind those (of slots that are not routed) stay here and get no gradient."""
 
     @staticmethod
-    def forward(ctx, rows, send, recv, status):
-        ctx.send, ctx.recv, ctx.status, ctx.rows = send, recv, status, rows.shape[0]
-        return ZippedExchange.move(rows, send, recv, status)
+    def forward(ctx, rows, send, recv, status, group=None):
+        ctx.send, ctx.recv, ctx.status, ctx.group, ctx.rows = send, recv, status, group, rows.shape[0]
+        return ZippedExchange.move(rows, send, recv, status, group)
 
     @staticmethod
     def backward(ctx, drows):
-        back = ZippedExchange.move(drows.contiguous(), ctx.recv, ctx.send, ctx.status)
+        back = ZippedExchange.move(drows.contiguous(), ctx.recv, ctx.send, ctx.status, ctx.group)
         kept = back.new_zeros((ctx.rows - back.shape[0], back.shape[1]))
-        return torch.cat([back, kept]) if len(kept) else back, None, None, None
+        return torch.cat([back, kept]) if len(kept) else back, None, None, None, None
 
     @staticmethod
-    def move(rows, send, recv, status):
+    def move(rows, send, recv, status, group=None):
         hidden = rows.shape[1]
         bits = rows[:sum(send)].reshape(-1).view(torch.int16)
         cb, _ = zc.histogram_topk(bits, zc.workspace(bits.numel(), rows.device), status)
-        pieces = zipped_all_to_all(list(bits.split([n * hidden for n in send])), [n * hidden for n in recv], cb, status)
+        pieces = zipped_all_to_all(list(bits.split([n * hidden for n in send])), [n * hidden for n in recv], cb, status,
+                                   group=group)
         return torch.cat(pieces).view(torch.bfloat16).view(-1, hidden)
 
 
@@ -93,8 +94,8 @@ class MoEBlock(torch.nn.Module):
         send = [sum(counts[rank][r * per:(r + 1) * per]) for r in range(self.world)]
         here = [c[rank * per:(rank + 1) * per] for c in counts]
         recv = [sum(c) for c in here]
-        got = ZippedExchange.apply(rows, send, recv, self.status)
-        back = ZippedExchange.apply(self.run_experts(got, here), recv, send, self.status)
+        got = ZippedExchange.apply(rows, send, recv, self.status, self.group)
+        back = ZippedExchange.apply(self.run_experts(got, here), recv, send, self.status, self.group)
         y, combined = ops.moe_combine(back, weights, positions)
         torch.maximum(self.status, combined, out=self.status)
         return ops.post_pre_norm(y, x, self.norm_weight, self.gate, self.next_weight, self.residual_scale, self.eps)
