@@ -1,7 +1,10 @@
 """Thin Python binding of libzc (the C ABI in include/zc.h).
 
 Argument marshalling only: every step runs in libzc's CUDA kernels on the
-caller's current torch stream.  Tensors are passed as raw device pointers;
+caller's current torch stream, or on the one given as ``stream``.  What a call
+on a given stream reads, and the outputs it is handed, must be ready there and
+stay alive until it has run; outputs it makes are that stream's, to be used
+elsewhere once that place waits for it.  Tensors are passed as raw device pointers;
 bfloat16 data may be given as ``torch.bfloat16``, ``torch.int16`` or
 ``torch.uint16`` tensors (the bits are what matters).  There is no CPU path:
 if libzc cannot be loaded, every call raises.
@@ -185,6 +188,22 @@ def _stream(stream: torch.cuda.Stream | None = None, like: torch.Tensor | None =
     return _current_raw_stream(index)
 
 
+def _empty(n: int, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
+    """A new output of a call on `stream` (default: the current one).  It comes from the memory of the stream that
+    writes it -- a block of another one may still have a reader queued there -- and is recorded on the current
+    stream, so that the caller may use and drop it there (once ordered behind the call)."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # a handle alone
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(n, dtype=dtype, device=device)
+    if stream != current:
+        t.record_stream(current)
+    return t
+
+
 def _nelem16(x: torch.Tensor) -> int:
     if x.element_size() != 2:
         raise ValueError("bfloat16 data must be a 2-byte dtype (bfloat16, int16 or uint16)")
@@ -239,7 +258,7 @@ def histogram_topk(x: torch.Tensor, ws: torch.Tensor, status: torch.Tensor, cb_o
     """Exact exponent histogram -> device codebook (7 x uint8) [+ 256 x int32 counts]."""
     n = _nelem16(x)
     if cb_out is None:
-        cb_out = torch.empty(7, dtype=torch.uint8, device=x.device)
+        cb_out = _empty(7, torch.uint8, x.device, stream)
     rc = load().zc_histogram_topk(_ptr(x), n, _ptr(cb_out), _ptr(hist_out), _ptr(ws), ws.numel(), _ptr(status),
                                   _stream(stream, status))
     _check(rc, "zc_histogram_topk")
@@ -252,9 +271,9 @@ def compress(x: torch.Tensor, cb: torch.Tensor, ws: torch.Tensor, status: torch.
     n = _nelem16(x)
     mb, eb = compressed_size(n)
     if main is None:
-        main = torch.empty(mb, dtype=torch.uint8, device=x.device)
+        main = _empty(mb, torch.uint8, x.device, stream)
     if esc is None:
-        esc = torch.empty(max(eb, 16), dtype=torch.uint8, device=x.device)
+        esc = _empty(max(eb, 16), torch.uint8, x.device, stream)
     rc = load().zc_compress(_ptr(x), n, _ptr(cb), _ptr(main), _ptr(esc), esc.numel(), _ptr(ws), ws.numel(),
                             _ptr(status), _stream(stream, status))
     _check(rc, "zc_compress")
@@ -270,9 +289,9 @@ def compress_adaptive(x: torch.Tensor, cb: torch.Tensor, ws: torch.Tensor, statu
     n = _nelem16(x)
     mb, _ = compressed_size(n)
     if main is None:
-        main = torch.empty(mb, dtype=torch.uint8, device=x.device)
+        main = _empty(mb, torch.uint8, x.device, stream)
     if esc is None:
-        esc = torch.empty(max(raw_spill(n), 16), dtype=torch.uint8, device=x.device)
+        esc = _empty(max(raw_spill(n), 16), torch.uint8, x.device, stream)
     rc = load().zc_compress_adaptive(_ptr(x), n, _ptr(cb), _ptr(main), _ptr(esc), esc.numel(), _ptr(ws),
                                      ws.numel(), _ptr(status), _stream(stream, status))
     _check(rc, "zc_compress_adaptive")
@@ -282,7 +301,7 @@ def compress_adaptive(x: torch.Tensor, cb: torch.Tensor, ws: torch.Tensor, statu
 def decompress(main: torch.Tensor, esc: torch.Tensor, n: int, status: torch.Tensor,
                out: torch.Tensor | None = None, esc_bytes: int | None = None, stream=None) -> torch.Tensor:
     if out is None:
-        out = torch.empty(n, dtype=torch.int16, device=main.device)
+        out = _empty(n, torch.int16, main.device, stream)
     eb = esc.numel() if esc_bytes is None else int(esc_bytes)
     rc = load().zc_decompress(_ptr(main), _ptr(esc) if esc is not None else None, eb, int(n), _ptr(out),
                               _ptr(status), _stream(stream, status))
@@ -298,13 +317,13 @@ def decompress_reduce(mains: Sequence[torch.Tensor], escs: Sequence[torch.Tensor
     P = len(mains)
     dev = mains[0].device
     if out is None and want_out:
-        out = torch.empty(n, dtype=torch.int16, device=dev)
+        out = _empty(n, torch.int16, dev, stream)
     if out_cb is not None:
         mb, eb = compressed_size(n)
         if out_main is None:
-            out_main = torch.empty(mb, dtype=torch.uint8, device=dev)
+            out_main = _empty(mb, torch.uint8, dev, stream)
         if out_esc is None:
-            out_esc = torch.empty(max(eb, 16), dtype=torch.uint8, device=dev)
+            out_esc = _empty(max(eb, 16), torch.uint8, dev, stream)
     mp = (ctypes.c_void_p * P)(*[_ptr(m) for m in mains])
     ep = (ctypes.c_void_p * P)(*[_ptr(e) for e in escs])
     sizes = [e.numel() for e in escs] if esc_bytes is None else list(esc_bytes)
@@ -396,8 +415,8 @@ def pipelined_transfer(x: torch.Tensor, cb: torch.Tensor, chunk_elems: int, ws: 
     reaches this point.
     """
     n = _nelem16(x)
-    if out is None:
-        out = torch.empty(n, dtype=torch.int16, device=x.device)
+    if out is None:  # the link and decompress streams write it behind events of the compress stream
+        out = _empty(n, torch.int16, x.device, streams[0] if streams is not None else None)
     if streams is None:
         cur = torch.cuda.current_stream()
         streams = (cur, torch.cuda.Stream(device=x.device), torch.cuda.Stream(device=x.device))
@@ -490,7 +509,7 @@ def zq_compress(x: torch.Tensor, table: ZqTable, ws: torch.Tensor, status: torch
         raise ValueError("QLC codes 1-byte symbols (uint8 or float8 tensors)")
     n = x.numel()
     if out is None:
-        out = torch.empty(zq_max_bytes(n), dtype=torch.uint8, device=x.device)
+        out = _empty(zq_max_bytes(n), torch.uint8, x.device, stream)
     rc = load().zq_compress(_ptr(x), n, ctypes.byref(table), _ptr(out), out.numel(), _ptr(ws), ws.numel(),
                             _ptr(status), _stream(stream, status))
     _check(rc, "zq_compress")
@@ -508,7 +527,7 @@ def zq_stream_bytes(stream_buf: torch.Tensor) -> int:
 def zq_decompress(stream_buf: torch.Tensor, n: int, status: torch.Tensor, out: torch.Tensor | None = None,
                   in_bytes: int | None = None, stream=None) -> torch.Tensor:
     if out is None:
-        out = torch.empty(n, dtype=torch.uint8, device=stream_buf.device)
+        out = _empty(n, torch.uint8, stream_buf.device, stream)
     nb = stream_buf.numel() if in_bytes is None else int(in_bytes)
     rc = load().zq_decompress(_ptr(stream_buf), nb, int(n), _ptr(out), _ptr(status), _stream(stream, status))
     _check(rc, "zq_decompress")
