@@ -3,6 +3,8 @@ Python extension of the operators that take torch tensors natively."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
+import fcntl
 import os
 import shutil
 import subprocess
@@ -39,6 +41,20 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _fresh(target: str) -> bool:
+    return os.path.exists(target) and os.path.getmtime(target) >= _deps_mtime()
+
+
+@contextlib.contextmanager
+def _builder_of(target: str):
+    """Held while a target is built: of several ranks that find it stale one builds (objects lie in one place), the
+    others wait and look again.  The lock goes with its process."""
+    os.makedirs(os.path.dirname(target), exist_ok=True)
+    with open(target + ".lock", "w") as f:
+        fcntl.flock(f, fcntl.LOCK_EX)
+        yield
+
+
 def _compile(src: str, extra: list[str], outdir: str = BUILD) -> str:
     obj = os.path.join(outdir, os.path.splitext(src)[0] + ".o")
     cmd = [nvcc()] + NVCC_FLAGS + extra + ["-c", os.path.join(CSRC, src), "-o", obj]
@@ -57,20 +73,22 @@ def build(force: bool = False, verbose_ptxas: bool = False, sanitize: bool = Fal
     code instrumented by AddressSanitizer and UndefinedBehaviorSanitizer.  A
     process that loads it must load the ASan runtime first (LD_PRELOAD)."""
     lib, outdir = (SAN_LIB, SAN_BUILD) if sanitize else (LIB, BUILD)
-    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime():
+    if not force and _fresh(lib):
         return lib
-    os.makedirs(outdir, exist_ok=True)
-    os.makedirs(LIBDIR, exist_ok=True)
-    extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    host = [f for flag in SAN_FLAGS for f in ("-Xcompiler", flag)] if sanitize else []
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra + host, outdir), SOURCES))
-    tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc()] + ARCH + host + ["-shared", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, lib)
+    with _builder_of(lib):
+        if not force and _fresh(lib):
+            return lib
+        os.makedirs(outdir, exist_ok=True)
+        extra = ["-Xptxas", "-v"] if verbose_ptxas else []
+        host = [f for flag in SAN_FLAGS for f in ("-Xcompiler", flag)] if sanitize else []
+        with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+            objs = list(ex.map(lambda s: _compile(s, extra + host, outdir), SOURCES))
+        tmp = lib + f".tmp{os.getpid()}"
+        cmd = [nvcc()] + ARCH + host + ["-shared", "-o", tmp] + objs
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, lib)
     return lib
 
 
@@ -97,37 +115,34 @@ def _compile_extension() -> str:
     return obj
 
 
-def build_extension(force: bool = False, obj: str | None = None) -> str:
-    """Compile and link the torch extension against libzc.so; skip if up to date."""
+def build_extension(force: bool = False) -> str:
+    """Compile and link the torch extension against libzc.so, which is built beside it if stale; skip if up to date."""
     import torch
     path = torch_extension_path()
-    if not force and obj is None and os.path.exists(path) and os.path.getmtime(path) >= _deps_mtime():
+    if not force and _fresh(path) and _fresh(LIB):
         return path
-    build()
-    os.makedirs(BUILD, exist_ok=True)
-    obj = obj or _compile_extension()
-    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = path + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIBDIR, "-lzc", "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
-           "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of the torch extension failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, path)
+    with _builder_of(path):
+        if not force and _fresh(path) and _fresh(LIB):
+            return path
+        os.makedirs(BUILD, exist_ok=True)
+        with cf.ThreadPoolExecutor(max_workers=1) as ex:
+            compiled = ex.submit(_compile_extension)
+            build()
+            obj = compiled.result()
+        lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+        tmp = path + f".tmp{os.getpid()}"
+        cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIBDIR, "-lzc", "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+               "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link of the torch extension failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, path)
     return path
 
 
 def build_all() -> None:
     """libzc.so and the torch extension, compiled side by side."""
-    if os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
-        build_extension()
-        return
-    os.makedirs(BUILD, exist_ok=True)
-    os.makedirs(LIBDIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        obj = ex.submit(_compile_extension)
-        build()
-        build_extension(obj=obj.result())
+    build_extension()
 
 
 if __name__ == "__main__":
