@@ -93,8 +93,11 @@ def build(force: bool = False, verbose_ptxas: bool = False, sanitize: bool = Fal
 
 
 def torch_extension_path() -> str:
+    """The extension is good for one torch, one Python and one kind of machine; its name says which."""
+    import sysconfig
+
     import torch
-    return os.path.join(LIBDIR, f"_zc_torch-{torch.__version__}.so")
+    return os.path.join(LIBDIR, f"_zc_torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _compile_extension() -> str:

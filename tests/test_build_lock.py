@@ -1,6 +1,7 @@
 """Several ranks that find the library stale build it once: one compiles, the others wait for it and take what it made
 (no GPU; the compilers are stand-ins)."""
 import os
+import sysconfig
 import threading
 import time
 import types
@@ -85,3 +86,8 @@ def test_a_failed_build_lets_the_next_one_try(compilers, monkeypatch):
         with pytest.raises(RuntimeError):
             _build.build_extension()
     assert os.path.exists(_build.build_extension())
+
+
+def test_the_extension_is_named_for_its_interpreter_and_machine():
+    """An extension module loads into one Python on one kind of machine only."""
+    assert _build.torch_extension_path().endswith(sysconfig.get_config_var("EXT_SUFFIX"))
