@@ -528,8 +528,9 @@ zc_status zc_moe_route(const void* d_logits, int dtype, uint64_t logits_stride, 
                        int32_t* d_experts, void* stream);
 
 /* Gradient of the logits (tokens x experts, their type) from d_dweights
- * (tokens x k fp32), for the experts that zc_moe_route chose (others, -1
- * among them, pass nothing on).  The choice itself has no gradient. */
+ * (tokens x k fp32), for the experts that zc_moe_route chose (others pass
+ * nothing on: -1, ids out of range, and experts whose logit is minus
+ * infinity).  The choice itself has no gradient. */
 zc_status zc_moe_route_backward(const float* d_dweights, const void* d_logits, int dtype, uint64_t logits_stride,
                                 uint64_t tokens, uint32_t experts, uint32_t k, const int32_t* d_experts, int score,
                                 int renormalize, float scale, void* d_dlogits, void* stream);

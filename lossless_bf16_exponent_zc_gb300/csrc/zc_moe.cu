@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(RouteBwdPar
     if (id >= 0) {
       g = p.scale * p.dweights[t * p.k + lane];
       lm = to_f32<T>(row[id]);
+      if (lm == -INFINITY) id = -1, g = 0.f;  // the router cannot have chosen it
     }
   }
   const bool have = id >= 0;
