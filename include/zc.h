@@ -615,7 +615,8 @@ zc_status zc_norm_workspace_size(uint64_t tokens, uint32_t hidden, uint64_t* byt
  * Gradient of zc_norm: from dx_new (the gradient of x_new that does not come through h; NULL =
  * zero) and dh (with next_weight), the saved y and x_new (x where y is NULL):
  * dy, dx, and in the parameters' type dweight, dgate, dnext_weight (summed
- * over the tokens in fp32).  Outputs without their input are NULL.
+ * over the tokens in fp32; without tokens those that are given become zero).
+ * Outputs without their input are NULL.
  */
 typedef struct zc_norm_backward_args {
   const void* dx_new;

@@ -767,7 +767,22 @@ zc_status zc_norm_backward(const zc_norm_backward_args* h_args, void* stream) {
   const ApiRange range_("zc_norm_backward");
   if (!h_args) return ZC_ERR_INVALID_ARG;
   const zc_norm_backward_args& a = *h_args;
-  const uint32_t size = dtype_bytes(a.dtype);
+  const uint32_t size = dtype_bytes(a.dtype), psize = a.params_f32 ? 4 : size;
+  // without tokens the tensors may be NULL, and the sums over none of them are zero
+  if (size && a.tokens == 0) {
+    if (a.hidden < 1) return ZC_ERR_INVALID_ARG;
+    if (a.hidden > ZC_NORM_MAX_HIDDEN) return ZC_ERR_TOO_LARGE;
+    if (!aligned(a.dweight, psize) || !aligned(a.dgate, psize) || !aligned(a.dnext_weight, psize))
+      return ZC_ERR_ALIGNMENT;
+    const uint64_t row = static_cast<uint64_t>(a.hidden) * psize;
+    auto clear = [&](void* p, uint64_t bytes) {
+      return p && bytes ? cudaMemsetAsync(p, 0, bytes, as_stream(stream)) : cudaSuccess;
+    };
+    cudaError_t e = clear(a.dweight, row);
+    if (e == cudaSuccess) e = clear(a.dnext_weight, row);
+    if (e == cudaSuccess) e = clear(a.dgate, a.gate_rows * (a.gate_wide ? row : psize));
+    return cuda_status(e);
+  }
   if (zc_status s = check_norm(a, size)) return s;
   if (!a.dh != !a.next_weight || (!a.dh && !a.dx_new)) return ZC_ERR_INVALID_ARG;
   if (a.next_weight)
@@ -780,12 +795,11 @@ zc_status zc_norm_backward(const zc_norm_backward_args* h_args, void* stream) {
     if (zc_status s = check_rows(a.y, a.tokens, a.y_stride, size)) return s;
   if (!a.dx || !a.dy != !a.y || !a.dweight != !a.weight || !a.dgate != !a.gate || !a.dnext_weight != !a.next_weight)
     return ZC_ERR_INVALID_ARG;
-  const uint32_t psize = a.params_f32 ? 4 : size;
   if (!aligned(a.dx, size) || !aligned(a.dy, size) || !aligned(a.dweight, psize) || !aligned(a.dgate, psize) ||
       !aligned(a.dnext_weight, psize) || !aligned(a.ws, 16))
     return ZC_ERR_ALIGNMENT;
   const uint64_t need = norm_workspace_bytes(a.tokens, a.hidden);
-  if (!a.ws && need) return ZC_ERR_INVALID_ARG;
+  if (!a.ws) return ZC_ERR_INVALID_ARG;
   if (a.ws_bytes < need) return ZC_ERR_WORKSPACE;
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;

@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(256) norm_narrow_gate_kernel(NormBwdParams p) 
 // Ranges of a gate row's `size` tokens, of `groups` gate rows for `most` walkers.
 uint64_t row_splits(uint64_t groups, uint64_t size, uint64_t most, uint64_t period) {
   uint64_t splits = groups >= most ? 1 : most / groups;
-  if (splits >= size) return size;  // no tokens: no ranges, and the sums over none of them are zero
+  if (splits >= size) return size;
   return splits > period ? splits - splits % period : splits;
 }
 
@@ -633,10 +633,9 @@ cudaError_t launch_ranges(NormBwdParams& p, const void* fn, uint64_t most, uint3
   p.ctas = (p.walkers + per_cta - 1) / per_cta;
   p.walkers = p.ctas * per_cta;
   void* args[] = {&p};
-  cudaError_t e = cudaSuccess;
-  if (p.ctas) e = launch_kernel(fn, dim3(p.ctas * p.cluster), dim3(threads), smem, stream, args, false, p.cluster);
+  cudaError_t e = launch_kernel(fn, dim3(p.ctas * p.cluster), dim3(threads), smem, stream, args, false, p.cluster);
   if (e != cudaSuccess) return e;
-  const uint32_t jobs = 2 + (wide && splits != 1 ? static_cast<uint32_t>(groups) : 0u);
+  const uint32_t jobs = 2 + (wide && splits > 1 ? static_cast<uint32_t>(groups) : 0u);
   // 32 warps a CTA while the GPU holds all such CTAs at once, two an SM (4452 x 704 fp32 18.1 us in
   // all against 22.9 with 16); beyond that 16, four an SM (512 x 4096 bf16 10.8 against 13.0).
   const dim3 parts((p.hidden + 31) / 32, jobs);
