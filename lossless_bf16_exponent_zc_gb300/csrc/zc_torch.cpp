@@ -98,8 +98,10 @@ struct Matrix {
 Matrix matrix(PyObject* o, const char* what) {
   const Tensor& t = tensor(o, what);
   if (t.dim() != 2) refuse(std::string(what) + " must be a matrix (rows, width), not " + shape_of(t));
-  if (t.stride(1) != 1 && t.size(1) > 1) refuse(std::string(what) + " must have contiguous columns");
-  return {t, static_cast<uint64_t>(t.size(0)), static_cast<uint64_t>(t.size(1)), static_cast<uint64_t>(t.stride(0))};
+  const bool none = t.size(0) == 0;  // of no rows the strides are anything
+  if (t.stride(1) != 1 && t.size(1) > 1 && !none) refuse(std::string(what) + " must have contiguous columns");
+  return {t, static_cast<uint64_t>(t.size(0)), static_cast<uint64_t>(t.size(1)),
+          static_cast<uint64_t>(none ? t.size(1) : t.stride(0))};
 }
 
 Matrix same_as(PyObject* o, const Tensor& like, const char* what) {
