@@ -465,6 +465,14 @@ __global__ void __launch_bounds__(kPrefixThreads) __cluster_dims__(kPrefixCtas, 
   for (uint32_t e = threadIdx.x; e <= p.experts; e += kPrefixThreads) p.offsets[e] = static_cast<int32_t>(total[e]);
 }
 
+// Where a slot's row goes.  A token's row is read in its own aligned pieces; off bytes into every
+// pair of neighbours lie the 16 bytes of an aligned piece of the row to write.
+struct PlaceRow {
+  uint64_t at;   // address of the piece that pair 0 holds
+  uint32_t off;  // 0 .. 15
+  uint32_t routed;
+};
+
 // Last: the row of every slot, and the rows themselves.  A CTA places the slots of a few tokens,
 // then reads each token once and writes its K rows.  A slot's row is its expert's first + those in
 // earlier chunks + its place in the chunk.  Where there are few counts (`few_counts`) the CTA adds
@@ -478,14 +486,6 @@ __global__ void __launch_bounds__(kPrefixThreads) __cluster_dims__(kPrefixCtas, 
 // mostly writes: 16384 x 4096 bf16 to 4 experts each, 0.67 GB, 115 us in all, of which the sort
 // about 7.  Rows off 16 bytes are read once, in pairs of pieces, and shifted for every slot: 16384 x
 // 4095 131 us; with a read for every slot, cut at that row's own pieces, 174.
-// Where a slot's row goes.  A token's row is read in its own aligned pieces; off bytes into every
-// pair of neighbours lie the 16 bytes of an aligned piece of the row to write.
-struct PlaceRow {
-  uint64_t at;   // address of the piece that pair 0 holds
-  uint32_t off;  // 0 .. 15
-  uint32_t routed;
-};
-
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(DispatchParams p) {
   __shared__ uint32_t start[kMoeMaxExperts + 1];

@@ -6,7 +6,7 @@
 // One pass: a row of y and x is read once, both sums of squares are taken on chip, and x' and the
 // next block's input h are written.  h is the norm of x' before its rounding to the stored type, so
 // each output is rounded once.  Bound by memory, 4 values moved per 11 operations: 16384 x 4096
-// bf16, 0.54 GB, 86 us, 94% of the measured copy's rate (with a CTA per row and no copies ahead of
+// bf16, 0.54 GB, 87 us, 93% of the measured copy's rate (with a CTA per row and no copies ahead of
 // it 133; with one barrier a row instead of two, as in the gradient, 93).  Rows off 16 bytes, 4081
 // wide, 100 us as the pieces that cover them, 168 value by value.
 #include "zc_norm.cuh"

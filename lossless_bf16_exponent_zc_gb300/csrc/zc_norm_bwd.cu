@@ -11,7 +11,7 @@
 // over all rows of its walker. (The weight's and the gate's gradient share the sum of G n while the
 // gate row stays the same.)  Every walker then writes its sums to the workspace and a second, small
 // kernel adds them in order, so no result depends on timing.  Bound by memory: 16384 x 4096 bf16,
-// 0.81 GB, 125 us, 97% of the measured copy's rate; off 16 bytes it waits a row for the two warps
+// 0.81 GB, 124 us, 97% of the measured copy's rate; off 16 bytes it waits a row for the two warps
 // that cut its first and last piece (16384 x 4081 bf16 155 us, 173 with a slower cut; with every
 // row taken value by value 284).
 #include "zc_norm.cuh"

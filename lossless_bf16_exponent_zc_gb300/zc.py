@@ -4,7 +4,8 @@ Argument marshalling only: every step runs in libzc's CUDA kernels on the
 caller's current torch stream, or on the one given as ``stream``.  What a call
 on a given stream reads, and the outputs it is handed, must be ready there and
 stay alive until it has run; outputs it makes are that stream's, to be used
-elsewhere once that place waits for it.  Tensors are passed as raw device pointers;
+elsewhere once that place waits for it.  Tensors have to be on the current
+device; they are passed as raw device pointers;
 bfloat16 data may be given as ``torch.bfloat16``, ``torch.int16`` or
 ``torch.uint16`` tensors (the bits are what matters).  There is no CPU path:
 if libzc cannot be loaded, every call raises.
