@@ -1,9 +1,9 @@
 // zc_torch.cpp -- Python entry points of the operators around an expert-parallel exchange (moe.py,
 // norm.py): torch tensors in, checked, outputs allocated by torch, and one call of the C ABI
-// (include/zc.h) on the current torch stream.  Argument marshalling only, as zc.py does with
-// ctypes; native because these operators run for a few microseconds in a decoding step, where five
-// allocations, a dozen attributes and a ctypes call in Python cost more than the kernels (route of
-// 8 tokens: 9.5 us of host time in Python).
+// (include/zc.h) on the current torch stream or the one given.  Argument marshalling only, as zc.py
+// does with ctypes; native because these operators run for a few microseconds in a decoding step,
+// where five allocations, a dozen attributes and a ctypes call in Python cost more than the kernels
+// (route of 8 tokens: 9.5 us of host time in Python).
 //
 // Errors: a wrong tensor raises ValueError, an error of the C ABI zc.ZcError, torch's own errors
 // (out of memory) as torch raises them.
