@@ -648,6 +648,156 @@ typedef struct zc_norm_backward_args {
 } zc_norm_backward_args;
 zc_status zc_norm_backward(const zc_norm_backward_args* h_args, void* stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * The other operators of a training step around such a block
+ * ------------------------------------------------------------------------
+ * The loss that keeps the router's load even, layer norms in place of the ones
+ * above, dropout, and the embedding that starts the residual stream.
+ * Conventions as for the operators around an expert-parallel exchange: rows of
+ * any alignment, fp32 inside, one rounding, sums in a fixed order, workspaces
+ * that need no initialisation.
+ */
+
+/*
+ * The balance loss of a router, and its experts' counts.  tokens lie in
+ * `sequences` equal runs (a divisor of tokens); a token counts if d_mask (one
+ * byte a token, NULL: all) has it and one of its logits is above minus
+ * infinity; T_s is the number of those in run s.  p is the softmax of a token's
+ * logits, or with ZC_SIGMOID its sigmoids divided by their sum + 1e-20.
+ *   d_counts  int32[sequences][experts]: slots of d_experts (tokens x k, as
+ *             zc_moe_route gives them; ids outside [0, experts) are none) of tokens that count
+ *   d_slope   fp32[sequences][experts]: experts * count / (sequences * k * T_s^2), 0 where T_s is 0
+ *   d_loss    fp32: sum over s and e of slope[s][e] * (sum of p[t][e] over the run's tokens that count)
+ * that is the mean over the runs of experts * sum_e (fraction of the slots) *
+ * (mean probability): 1 for an even load.  Logits of tokens that the mask
+ * leaves out are not read.
+ */
+zc_status zc_moe_balance_workspace_size(uint64_t tokens, uint32_t experts, uint64_t sequences, uint64_t* bytes);
+zc_status zc_moe_balance(const void* d_logits, int dtype, uint64_t logits_stride, uint64_t tokens, uint32_t experts,
+                         uint32_t k, const int32_t* d_experts, int score, uint64_t sequences, const uint8_t* d_mask,
+                         float* d_loss, int32_t* d_counts, float* d_slope, void* d_ws, uint64_t ws_bytes,
+                         void* stream);
+
+/* Gradient of the logits (tokens x experts, their type; zero for tokens that do
+ * not count) from that of the loss, d_dloss (fp32, on the device), and
+ * d_slope.  The counts have no gradient. */
+zc_status zc_moe_balance_backward(const float* d_dloss, const void* d_logits, int dtype, uint64_t logits_stride,
+                                  uint64_t tokens, uint32_t experts, int score, uint64_t sequences,
+                                  const uint8_t* d_mask, const float* d_slope, void* d_dlogits, void* stream);
+
+/*
+ * Dropout: a value is kept, and multiplied by 65536 / (65536 - limit), or
+ * becomes zero; limit = floor(p * 65536 + 1/2).  It is kept if its 16 bits of a
+ * counter-based generator are at least limit, so the mask is never stored:
+ * Philox-4x32-10 (Salmon, Moraes, Dror and Shaw, 2011) with the seed's low and
+ * high word as its key and the counter (column / 8, row, call, offset modulo
+ * 2^32); output word j / 2 holds the bits of column 8 * group + j, in its low
+ * half for even j.  d_rng: int64[2] on the device, seed and offset, so that a
+ * captured graph draws anew when they change.  `call` tells the dropouts of a
+ * step apart; a step changes the offset.
+ *   zc_dropout: d_out = residual_scale * residual + dropout(x); d_residual NULL:
+ *   none.  d_out may be d_x or d_residual where that is contiguous.  The gradient
+ *   of x is the dropout of d_out's with the same p, rng and call.
+ * 0 <= p <= 1, tokens < 2^32, width < 2^31.
+ */
+zc_status zc_dropout(const void* d_x, int dtype, uint64_t x_stride, const void* d_residual, uint64_t residual_stride,
+                     float residual_scale, uint64_t tokens, uint32_t width, double p, const int64_t* d_rng,
+                     uint32_t call, void* d_out, void* stream);
+
+/*
+ * Layer norm.  With m = mean(z) and r(z) = 1 / sqrt(mean((z - m)^2) + eps) over a row:
+ *   x_new = residual_scale * x + dropout(y)
+ *   h     = (x_new - m) * r(x_new) * weight + bias
+ * h is taken from x_new before x_new is rounded.
+ *   - y NULL (then x_new is NULL too): h of x itself.  bias NULL: none.
+ *   - rng NULL: no dropout (p must be 0); otherwise as zc_dropout, and only with y.
+ *   - weight and bias have the activations' type, or fp32 with params_f32.
+ *   - stats, fp32[tokens][2] or NULL, gets m and r(x_new): the gradient needs them.
+ *   - x_new may be x or y, and h may be x where there is no y, if contiguous.
+ */
+typedef struct zc_layer_norm_args {
+  const void* y;
+  const void* x;
+  uint64_t y_stride;
+  uint64_t x_stride;
+  uint64_t tokens;
+  const void* weight;
+  const void* bias;
+  const int64_t* rng;
+  double p;
+  uint32_t call;
+  uint32_t hidden;
+  int32_t dtype;
+  int32_t params_f32;
+  float residual_scale;
+  float eps;
+  void* x_new;
+  void* h;
+  float* stats;
+} zc_layer_norm_args;
+zc_status zc_layer_norm(const zc_layer_norm_args* h_args, void* stream);
+
+/*
+ * Gradient of zc_layer_norm: from dx_new (the gradient of x_new that does not come through h; NULL =
+ * zero) and dh, the saved x_new (x where there was no y) and stats: dx, dy
+ * (NULL: not wanted; without dropout and a residual_scale of 1 it is dx), and
+ * in the parameters' type dweight and dbias (NULL: not wanted), summed over the
+ * tokens in fp32.  residual_scale is 1 where there was no y.  Workspace:
+ * zc_norm_workspace_size bytes, 16-byte aligned.  Without tokens dweight and
+ * dbias become zero.
+ */
+typedef struct zc_layer_norm_backward_args {
+  const void* dx_new;
+  const void* dh;
+  const void* x_new;
+  uint64_t dx_new_stride;
+  uint64_t dh_stride;
+  uint64_t x_new_stride;
+  uint64_t tokens;
+  const float* stats;
+  const void* weight;
+  const int64_t* rng;
+  double p;
+  uint32_t call;
+  uint32_t hidden;
+  int32_t dtype;
+  int32_t params_f32;
+  float residual_scale;
+  void* dy;
+  void* dx;
+  void* dweight;
+  void* dbias;
+  void* ws;
+  uint64_t ws_bytes;
+} zc_layer_norm_backward_args;
+zc_status zc_layer_norm_backward(const zc_layer_norm_backward_args* h_args, void* stream);
+
+/*
+ * Embedding: d_out[t] = scale * row d_ids[t] of d_table (vocab x hidden), in
+ * type dtype; the table has that type, or fp32 with table_f32.  ids are int32,
+ * or int64 with ids_are_int64.  A negative id is no token: a row of zeros.  An
+ * id >= vocab sets ZC_ERR_BAD_INDEX and counts as none.
+ * tokens < 2^31, vocab < 2^31, hidden < 2^31.
+ */
+zc_status zc_embedding(const void* d_ids, int ids_are_int64, uint64_t tokens, const void* d_table, int dtype,
+                       int table_f32, uint64_t table_stride, uint64_t vocab, uint32_t hidden, float scale, void* d_out,
+                       int32_t* d_status, void* stream);
+
+/* Workspace of zc_embedding_backward (bytes; 16-byte aligned). */
+zc_status zc_embedding_workspace_size(uint64_t tokens, uint64_t vocab, uint32_t hidden, uint64_t* bytes);
+
+/*
+ * Gradient of the table, d_dtable (vocab x hidden, contiguous, of the table's
+ * type): scale * the sum of d_dout's rows of every id's tokens, zero for ids
+ * without one.  With accumulate the sums are added to what d_dtable holds, and
+ * rows of other ids are neither read nor written.
+ */
+zc_status zc_embedding_backward(const void* d_dout, int dtype, uint64_t dout_stride, const void* d_ids,
+                                int ids_are_int64, uint64_t tokens, uint64_t vocab, uint32_t hidden, float scale,
+                                int table_f32, int accumulate, void* d_dtable, void* d_ws, uint64_t ws_bytes,
+                                int32_t* d_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

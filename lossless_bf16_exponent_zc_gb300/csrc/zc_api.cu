@@ -118,6 +118,26 @@ zc_status check_experts(uint32_t experts, uint32_t k) {
   return k > experts ? ZC_ERR_INVALID_ARG : ZC_OK;
 }
 
+// Runs of tokens of equal length.
+zc_status check_sequences(uint64_t tokens, uint64_t sequences) {
+  if (sequences < 1 || tokens % sequences) return ZC_ERR_INVALID_ARG;
+  return sequences > 0x7FFFFFFFull ? ZC_ERR_TOO_LARGE : ZC_OK;
+}
+
+// A dropout's arguments, and from them what its kernels take.
+zc_status check_dropout(double p, const int64_t* rng, uint32_t call, uint64_t tokens, Dropout* out) {
+  if (!(p >= 0.0 && p <= 1.0) || (!rng && tokens)) return ZC_ERR_INVALID_ARG;
+  if (!aligned(rng, 8)) return ZC_ERR_ALIGNMENT;
+  const uint32_t limit = static_cast<uint32_t>(p * 65536.0 + 0.5);
+  *out = Dropout{rng, call, limit, limit < 65536u ? static_cast<float>(65536.0 / (65536.0 - limit)) : 0.f};
+  return ZC_OK;
+}
+
+zc_status check_table(uint64_t tokens, uint64_t vocab, uint32_t hidden) {
+  if (hidden < 1) return ZC_ERR_INVALID_ARG;
+  return hidden > 0x7FFFFFFFu || tokens > 0x7FFFFFFFull || vocab > 0x7FFFFFFFull ? ZC_ERR_TOO_LARGE : ZC_OK;
+}
+
 // What the norms' forward and backward arguments have in common.
 template <typename A>
 zc_status check_norm(const A& a, uint32_t size) {
@@ -835,6 +855,247 @@ zc_status zc_norm_backward(const zc_norm_backward_args* h_args, void* stream) {
                    (!a.y || in_pieces(a.y, a.y_stride, a.hidden, size)) && aligned(a.dx, 16) && aligned(a.dy, 16) &&
                    aligned(a.weight, 16) && aligned(a.gate, 16) && aligned(a.next_weight, 16);
   return cuda_status(launch_norm_bwd(p, a.dtype, vec, as_stream(stream), dev));
+}
+
+// ---- the other operators of a training step ---------------------------------
+zc_status zc_moe_balance_workspace_size(uint64_t tokens, uint32_t experts, uint64_t sequences, uint64_t* bytes) {
+  if (!bytes) return ZC_ERR_INVALID_ARG;
+  if (zc_status s = check_slots(tokens, 1)) return s;
+  if (zc_status s = check_experts(experts, 1)) return s;
+  if (zc_status s = check_sequences(tokens, sequences)) return s;
+  *bytes = balance_workspace_bytes(tokens, experts, sequences);
+  return ZC_OK;
+}
+
+zc_status zc_moe_balance(const void* d_logits, int dtype, uint64_t logits_stride, uint64_t tokens, uint32_t experts,
+                         uint32_t k, const int32_t* d_experts, int score, uint64_t sequences, const uint8_t* d_mask,
+                         float* d_loss, int32_t* d_counts, float* d_slope, void* d_ws, uint64_t ws_bytes,
+                         void* stream) {
+  const ApiRange range_("zc_moe_balance");
+  const uint32_t size = dtype_bytes(dtype);
+  if (!size || (score != ZC_SOFTMAX && score != ZC_SIGMOID)) return ZC_ERR_INVALID_ARG;
+  if (zc_status s = check_slots(tokens, k)) return s;
+  if (zc_status s = check_experts(experts, k)) return s;
+  if (zc_status s = check_sequences(tokens, sequences)) return s;
+  if (zc_status s = check_rows(d_logits, tokens, logits_stride, size)) return s;
+  if ((tokens && !d_experts) || !d_loss || !d_counts || !d_slope || !d_ws) return ZC_ERR_INVALID_ARG;
+  if (!aligned(d_experts, 4) || !aligned(d_loss, 4) || !aligned(d_counts, 4) || !aligned(d_slope, 4) ||
+      !aligned(d_ws, 16))
+    return ZC_ERR_ALIGNMENT;
+  if (ws_bytes < balance_workspace_bytes(tokens, experts, sequences)) return ZC_ERR_WORKSPACE;
+  BalanceParams p = {};
+  p.logits = d_logits;
+  p.stride = logits_stride;
+  p.tokens = tokens;
+  p.sequences = sequences;
+  p.experts = experts;
+  p.k = k;
+  p.sigmoid = score == ZC_SIGMOID;
+  p.ids = d_experts;
+  p.mask = d_mask;
+  p.loss = d_loss;
+  p.counts = d_counts;
+  p.slope = d_slope;
+  return cuda_status(launch_balance(p, dtype, d_ws, as_stream(stream)));
+}
+
+zc_status zc_moe_balance_backward(const float* d_dloss, const void* d_logits, int dtype, uint64_t logits_stride,
+                                  uint64_t tokens, uint32_t experts, int score, uint64_t sequences,
+                                  const uint8_t* d_mask, const float* d_slope, void* d_dlogits, void* stream) {
+  const ApiRange range_("zc_moe_balance_backward");
+  const uint32_t size = dtype_bytes(dtype);
+  if (!size || (score != ZC_SOFTMAX && score != ZC_SIGMOID)) return ZC_ERR_INVALID_ARG;
+  if (zc_status s = check_slots(tokens, 1)) return s;
+  if (zc_status s = check_experts(experts, 1)) return s;
+  if (zc_status s = check_sequences(tokens, sequences)) return s;
+  if (zc_status s = check_rows(d_logits, tokens, logits_stride, size)) return s;
+  if (tokens && (!d_dloss || !d_slope || !d_dlogits)) return ZC_ERR_INVALID_ARG;
+  if (!aligned(d_dloss, 4) || !aligned(d_slope, 4) || !aligned(d_dlogits, size)) return ZC_ERR_ALIGNMENT;
+  BalanceBwdParams p = {d_dloss, d_logits, logits_stride, tokens, tokens / sequences, experts, score == ZC_SIGMOID,
+                        d_mask,  d_slope,  d_dlogits};
+  return cuda_status(launch_balance_bwd(p, dtype, as_stream(stream)));
+}
+
+zc_status zc_dropout(const void* d_x, int dtype, uint64_t x_stride, const void* d_residual, uint64_t residual_stride,
+                     float residual_scale, uint64_t tokens, uint32_t width, double p, const int64_t* d_rng,
+                     uint32_t call, void* d_out, void* stream) {
+  const ApiRange range_("zc_dropout");
+  const uint32_t size = dtype_bytes(dtype);
+  if (!size || width < 1) return ZC_ERR_INVALID_ARG;
+  if (width > 0x7FFFFFFFu || tokens > 0xFFFFFFFFull) return ZC_ERR_TOO_LARGE;
+  DropoutParams a = {};
+  if (zc_status s = check_dropout(p, d_rng, call, tokens, &a.drop)) return s;
+  if (zc_status s = check_rows(d_x, tokens, x_stride, size)) return s;
+  if (d_residual)
+    if (zc_status s = check_rows(d_residual, tokens, residual_stride, size)) return s;
+  if (tokens && !d_out) return ZC_ERR_INVALID_ARG;
+  if (!aligned(d_out, size)) return ZC_ERR_ALIGNMENT;
+  a.x = d_x;
+  a.residual = d_residual;
+  a.x_stride = x_stride;
+  a.residual_stride = residual_stride;
+  a.tokens = tokens;
+  a.width = width;
+  a.residual_scale = residual_scale;
+  a.out = d_out;
+  const bool vec = in_pieces(d_x, x_stride, width, size) &&
+                   (!d_residual || in_pieces(d_residual, residual_stride, width, size)) && aligned(d_out, 16);
+  return cuda_status(launch_dropout(a, dtype, vec, as_stream(stream)));
+}
+
+zc_status zc_layer_norm(const zc_layer_norm_args* h_args, void* stream) {
+  const ApiRange range_("zc_layer_norm");
+  if (!h_args) return ZC_ERR_INVALID_ARG;
+  const zc_layer_norm_args& a = *h_args;
+  const uint32_t size = dtype_bytes(a.dtype), psize = a.params_f32 ? 4 : size;
+  if (!size || a.hidden < 1) return ZC_ERR_INVALID_ARG;
+  if (a.hidden > ZC_NORM_MAX_HIDDEN || a.tokens > 0x7FFFFFFFull) return ZC_ERR_TOO_LARGE;
+  LayerNormParams p = {};
+  if (a.rng) {
+    if (zc_status s = check_dropout(a.p, a.rng, a.call, a.tokens, &p.drop)) return s;
+  } else if (a.p != 0.0) {
+    return ZC_ERR_INVALID_ARG;
+  }
+  // without tokens the tensors may be NULL, so which of them the call is about does not matter
+  if (a.tokens == 0) return ZC_OK;
+  if (zc_status s = check_rows(a.x, a.tokens, a.x_stride, size)) return s;
+  if (a.y)
+    if (zc_status s = check_rows(a.y, a.tokens, a.y_stride, size)) return s;
+  if (!a.weight || !a.h || !a.x_new != !a.y || (a.rng && !a.y)) return ZC_ERR_INVALID_ARG;
+  if (!aligned(a.weight, psize) || !aligned(a.bias, psize) || !aligned(a.x_new, size) || !aligned(a.h, size) ||
+      !aligned(a.stats, 8))
+    return ZC_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;
+  p.y = a.y;
+  p.x = a.x;
+  p.y_stride = a.y_stride;
+  p.x_stride = a.x_stride;
+  p.tokens = a.tokens;
+  p.weight = a.weight;
+  p.bias = a.bias;
+  p.hidden = a.hidden;
+  p.params_f32 = a.params_f32 != 0;
+  p.residual_scale = a.residual_scale;
+  p.eps = a.eps;
+  p.x_new = a.x_new;
+  p.h = a.h;
+  p.stats = a.stats;
+  const bool vec = in_pieces(a.x, a.x_stride, a.hidden, size) && (!a.y || in_pieces(a.y, a.y_stride, a.hidden, size)) &&
+                   aligned(a.x_new, 16) && aligned(a.h, 16) && aligned(a.weight, 16) && aligned(a.bias, 16);
+  return cuda_status(launch_layer_norm(p, a.dtype, vec, as_stream(stream), dev));
+}
+
+zc_status zc_layer_norm_backward(const zc_layer_norm_backward_args* h_args, void* stream) {
+  const ApiRange range_("zc_layer_norm_backward");
+  if (!h_args) return ZC_ERR_INVALID_ARG;
+  const zc_layer_norm_backward_args& a = *h_args;
+  const uint32_t size = dtype_bytes(a.dtype), psize = a.params_f32 ? 4 : size;
+  if (!size || a.hidden < 1) return ZC_ERR_INVALID_ARG;
+  if (a.hidden > ZC_NORM_MAX_HIDDEN || a.tokens > 0x7FFFFFFFull) return ZC_ERR_TOO_LARGE;
+  LayerNormBwdParams p = {};
+  if (a.rng) {
+    if (zc_status s = check_dropout(a.p, a.rng, a.call, a.tokens, &p.drop)) return s;
+  } else if (a.p != 0.0) {
+    return ZC_ERR_INVALID_ARG;
+  }
+  if (!aligned(a.dweight, psize) || !aligned(a.dbias, psize)) return ZC_ERR_ALIGNMENT;
+  // without tokens the tensors may be NULL, and the sums over none of them are zero
+  if (a.tokens == 0) {
+    const uint64_t row = static_cast<uint64_t>(a.hidden) * psize;
+    cudaError_t e = a.dweight ? cudaMemsetAsync(a.dweight, 0, row, as_stream(stream)) : cudaSuccess;
+    if (e == cudaSuccess && a.dbias) e = cudaMemsetAsync(a.dbias, 0, row, as_stream(stream));
+    return cuda_status(e);
+  }
+  if (zc_status s = check_rows(a.dh, a.tokens, a.dh_stride, size)) return s;
+  if (zc_status s = check_rows(a.x_new, a.tokens, a.x_new_stride, size)) return s;
+  if (a.dx_new)
+    if (zc_status s = check_rows(a.dx_new, a.tokens, a.dx_new_stride, size)) return s;
+  if (!a.stats || !a.weight || !a.dx || !a.dweight || !a.ws || (a.rng && !a.dy)) return ZC_ERR_INVALID_ARG;
+  if (!aligned(a.stats, 8) || !aligned(a.weight, psize) || !aligned(a.dx, size) || !aligned(a.dy, size) ||
+      !aligned(a.ws, 16))
+    return ZC_ERR_ALIGNMENT;
+  if (a.ws_bytes < norm_workspace_bytes(a.tokens, a.hidden)) return ZC_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;
+  p.dx_new = a.dx_new;
+  p.dh = a.dh;
+  p.x_new = a.x_new;
+  p.dx_new_stride = a.dx_new_stride;
+  p.dh_stride = a.dh_stride;
+  p.x_new_stride = a.x_new_stride;
+  p.tokens = a.tokens;
+  p.stats = a.stats;
+  p.weight = a.weight;
+  p.hidden = a.hidden;
+  p.params_f32 = a.params_f32 != 0;
+  p.residual_scale = a.residual_scale;
+  p.dy = a.dy;
+  p.dx = a.dx;
+  p.dweight = a.dweight;
+  p.dbias = a.dbias;
+  p.parts = static_cast<float*>(a.ws);
+  const bool vec = in_pieces(a.dh, a.dh_stride, a.hidden, size) && in_pieces(a.x_new, a.x_new_stride, a.hidden, size) &&
+                   (!a.dx_new || in_pieces(a.dx_new, a.dx_new_stride, a.hidden, size)) && aligned(a.dx, 16) &&
+                   aligned(a.dy, 16) && aligned(a.weight, 16);
+  return cuda_status(launch_layer_norm_bwd(p, a.dtype, vec, as_stream(stream), dev));
+}
+
+zc_status zc_embedding(const void* d_ids, int ids_are_int64, uint64_t tokens, const void* d_table, int dtype,
+                       int table_f32, uint64_t table_stride, uint64_t vocab, uint32_t hidden, float scale, void* d_out,
+                       int32_t* d_status, void* stream) {
+  const ApiRange range_("zc_embedding");
+  const uint32_t size = dtype_bytes(dtype), tsize = table_f32 ? 4 : size;
+  if (!size || !d_status) return ZC_ERR_INVALID_ARG;
+  if (zc_status s = check_table(tokens, vocab, hidden)) return s;
+  if (zc_status s = check_rows(d_table, vocab, table_stride, tsize)) return s;
+  if (tokens && (!d_ids || !d_out)) return ZC_ERR_INVALID_ARG;
+  if (!aligned(d_ids, ids_are_int64 ? 8 : 4) || !aligned(d_out, size) || !aligned(d_status, 4))
+    return ZC_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;
+  EmbedParams p = {d_ids, ids_are_int64 != 0, d_table, table_stride, tokens, vocab, hidden, scale, d_out, d_status};
+  const bool vec = in_pieces(d_table, table_stride, hidden, tsize) && in_pieces(d_out, hidden, hidden, size);
+  return cuda_status(launch_embed(p, dtype, table_f32 != 0, vec, as_stream(stream), dev));
+}
+
+zc_status zc_embedding_workspace_size(uint64_t tokens, uint64_t vocab, uint32_t hidden, uint64_t* bytes) {
+  if (!bytes) return ZC_ERR_INVALID_ARG;
+  if (zc_status s = check_table(tokens, vocab, hidden)) return s;
+  *bytes = embed_workspace_bytes(tokens, vocab, hidden);
+  return ZC_OK;
+}
+
+zc_status zc_embedding_backward(const void* d_dout, int dtype, uint64_t dout_stride, const void* d_ids,
+                                int ids_are_int64, uint64_t tokens, uint64_t vocab, uint32_t hidden, float scale,
+                                int table_f32, int accumulate, void* d_dtable, void* d_ws, uint64_t ws_bytes,
+                                int32_t* d_status, void* stream) {
+  const ApiRange range_("zc_embedding_backward");
+  const uint32_t size = dtype_bytes(dtype), tsize = table_f32 ? 4 : size;
+  if (!size || !d_status) return ZC_ERR_INVALID_ARG;
+  if (zc_status s = check_table(tokens, vocab, hidden)) return s;
+  if (zc_status s = check_rows(d_dout, tokens, dout_stride, size)) return s;
+  if ((tokens && !d_ids) || (vocab && !d_dtable) || !d_ws) return ZC_ERR_INVALID_ARG;
+  if (!aligned(d_ids, ids_are_int64 ? 8 : 4) || !aligned(d_dtable, tsize) || !aligned(d_ws, 16) ||
+      !aligned(d_status, 4))
+    return ZC_ERR_ALIGNMENT;
+  if (ws_bytes < embed_workspace_bytes(tokens, vocab, hidden)) return ZC_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;
+  EmbedBwdParams p = {};
+  p.dout = d_dout;
+  p.ids = d_ids;
+  p.ids64 = ids_are_int64 != 0;
+  p.dout_stride = dout_stride;
+  p.tokens = tokens;
+  p.vocab = vocab;
+  p.hidden = hidden;
+  p.scale = scale;
+  p.accumulate = accumulate != 0;
+  p.dtable = d_dtable;
+  p.status = d_status;
+  const bool vec = in_pieces(d_dout, dout_stride, hidden, size) && in_pieces(d_dtable, hidden, hidden, tsize);
+  return cuda_status(launch_embed_bwd(p, dtype, table_f32 != 0, vec, d_ws, as_stream(stream), dev));
 }
 
 }  // extern "C"

@@ -1,0 +1,196 @@
+// zc_dropout.cu -- dropout with a mask that is never stored (zc_dropout.cuh), and the residual
+// addition behind it in the same pass:  out = a residual + D(x),  D(x) = x / (1 - p) where kept.
+//
+// The gradient of x is the dropout of out's gradient with the same seed, offset and call.  Bound by
+// memory, and next by the generator's instructions.
+#include "zc_dropout.cuh"
+#include "zc_internal.h"
+
+namespace zc {
+
+namespace {
+
+constexpr int kDropThreads = 256;
+
+// Rows whose addresses, strides and widths are multiples of 16 bytes: a thread takes UNITS groups of
+// eight columns, kDropThreads apart, all loads before the first use.
+template <typename T, int UNITS, bool RESIDUAL>
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(DropoutParams p) {
+  constexpr int V = kPieceOf<T>, NP = 8 / V;
+  pdl_begin();
+  const KeepRng rng(p.drop);
+  const uint32_t groups = (p.width + 7) / 8;
+  const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kDropThreads * UNITS), t0 = i0 / groups;
+  const uint32_t c0 = static_cast<uint32_t>(i0 - t0 * groups) + threadIdx.x;
+  Piece<T, V> x[UNITS][NP], r[UNITS][NP];
+  uint64_t row[UNITS];
+  uint32_t group[UNITS];
+#pragma unroll
+  for (int q = 0; q < UNITS; q++) {
+    const uint32_t i = c0 + q * kDropThreads, dt = i / groups;
+    group[q] = i - dt * groups;
+    row[q] = t0 + dt;
+#pragma unroll
+    for (int k = 0; k < NP; k++) {
+      const uint32_t col = group[q] * 8 + k * V;
+      const bool there = row[q] < p.tokens && col < p.width;
+      x[q][k] = r[q][k] = Piece<T, V>::zero();
+      if (there) x[q][k] = Piece<T, V>::load(static_cast<const T*>(p.x) + row[q] * p.x_stride + col);
+      if (there && RESIDUAL)
+        r[q][k] = Piece<T, V>::load(static_cast<const T*>(p.residual) + row[q] * p.residual_stride + col);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < UNITS; q++) {
+    if (row[q] >= p.tokens) continue;
+    const uint4 g = rng.group(static_cast<uint32_t>(row[q]), group[q]);
+    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int k = 0; k < NP; k++) {
+      const uint32_t col = group[q] * 8 + k * V;
+      if (col >= p.width) continue;
+      float f[V], o[V];
+      uint32_t bits[V / 2];
+#pragma unroll
+      for (int j = 0; j < V / 2; j++) bits[j] = w[k * V / 2 + j];
+      x[q][k].get(f);
+      rng.template apply<V>(f, bits);
+      if (RESIDUAL) {
+        r[q][k].get(o);
+#pragma unroll
+        for (int j = 0; j < V; j++) f[j] = fmaf(p.residual_scale, o[j], f[j]);
+      }
+      Piece<T, V> out;
+      out.set(f);
+      out.store(static_cast<T*>(p.out) + row[q] * p.width + col);
+    }
+  }
+}
+
+// 8 values at p, which lies anywhere, as the pieces that hold them.
+template <typename T>
+struct AnyEight {
+  static constexpr int NP = 8 / kPieceOf<T>;
+  uint4 w[NP + 1];
+  uint32_t off;
+  __device__ __forceinline__ void load(const T* p) {
+    off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
+#pragma unroll
+    for (int k = 0; k < NP; k++) w[k] = from[k];
+    w[NP] = off ? from[NP] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    constexpr int V = kPieceOf<T>;
+#pragma unroll
+    for (int k = 0; k < NP; k++) {
+      float v[V];
+      Piece<T, V>{shift_pieces<T>(w[k], w[k + 1], off)}.get(v);
+#pragma unroll
+      for (int j = 0; j < V; j++) f[k * V + j] = v[j];
+    }
+  }
+};
+
+// Rows off 16 bytes.  A warp takes 31 units of a row of the output: eight columns from an aligned
+// piece on, or a column outside those (the ones behind the last piece, then the ones before the
+// first).  Eight such columns lie in two of the generator's groups: every lane draws one and takes
+// the second from the lane above, the last lane drawing for its neighbour alone.
+constexpr uint32_t kDropAnyUnits = 31;
+template <typename T, bool RESIDUAL>
+__global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(DropoutParams p, uint32_t shares) {
+  constexpr int V = kPieceOf<T>, NP = 8 / V;
+  pdl_begin();
+  const KeepRng rng(p.drop);
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kDropThreads / 32) + (threadIdx.x >> 5), t = i / shares;
+  if (t >= p.tokens) return;
+  const uint32_t u = static_cast<uint32_t>(i - t * shares) * kDropAnyUnits + lane_id();
+  T* out = static_cast<T*>(p.out) + t * p.width;
+  const T* x = static_cast<const T*>(p.x) + t * p.x_stride;
+  const T* r = RESIDUAL ? static_cast<const T*>(p.residual) + t * p.residual_stride : nullptr;
+  uint32_t head = static_cast<uint32_t>((16 - (reinterpret_cast<uintptr_t>(out) & 15)) & 15) / sizeof(T);
+  head = head < p.width ? head : p.width;
+  const uint32_t body = (p.width - head) / 8, tail = p.width - head - body * 8;
+  const bool whole = u < body && lane_id() < kDropAnyUnits;
+  // behind the last piece one unit at the least, which draws the group of that piece's last columns
+  const uint32_t behind = tail ? tail : 1, e = u - body;
+  const bool last = u >= body && e >= behind;
+  const uint32_t col = last ? e - behind : head + body * 8 + (u < body ? (u - body) * 8 : e);
+  const bool single = u >= body && lane_id() < kDropAnyUnits && (last ? col < head : e < tail);
+  AnyEight<T> xs, rs;
+  if (whole) {
+    xs.load(x + col);
+    if (RESIDUAL) rs.load(r + col);
+  }
+  const uint4 own = rng.group(static_cast<uint32_t>(t), col / 8);
+  uint4 above;
+  above.x = __shfl_down_sync(kFull, own.x, 1);
+  above.y = __shfl_down_sync(kFull, own.y, 1);
+  above.z = __shfl_down_sync(kFull, own.z, 1);
+  above.w = __shfl_down_sync(kFull, own.w, 1);
+  if (whole) {
+    const uint4 g = shift_pieces<__half>(own, above, (col & 7) * 2);
+    const uint32_t bits[4] = {g.x, g.y, g.z, g.w};
+    float f[8], o[8];
+    xs.get(f);
+    rng.template apply<8>(f, bits);
+    if (RESIDUAL) {
+      rs.get(o);
+#pragma unroll
+      for (int j = 0; j < 8; j++) f[j] = fmaf(p.residual_scale, o[j], f[j]);
+    }
+#pragma unroll
+    for (int k = 0; k < NP; k++) {
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; j++) v[j] = f[k * V + j];
+      Piece<T, V> piece;
+      piece.set(v);
+      piece.store(out + col + k * V);
+    }
+  } else if (single) {
+    float f = rng.keeps(own, col & 7) ? to_f32<T>(x[col]) * rng.factor : 0.f;
+    if (RESIDUAL) f = fmaf(p.residual_scale, to_f32<T>(r[col]), f);
+    out[col] = from_f32<T>(f);
+  }
+}
+
+template <typename T, bool RESIDUAL>
+cudaError_t run(DropoutParams& p, bool vec, cudaStream_t stream) {
+  constexpr int kUnits = sizeof(T) == 2 ? 4 : 2;
+  uint64_t grid;
+  uint32_t shares = 0;
+  const void* fn;
+  if (vec) {
+    grid = (p.tokens * ((p.width + 7) / 8) + kDropThreads * kUnits - 1) / (kDropThreads * kUnits);
+    fn = reinterpret_cast<const void*>(dropout_kernel<T, kUnits, RESIDUAL>);
+  } else {
+    // at most 7 columns on either side of the pieces
+    const uint32_t units = p.width / 8 + 14;
+    shares = (units + kDropAnyUnits - 1) / kDropAnyUnits;
+    grid = (p.tokens * shares + kDropThreads / 32 - 1) / (kDropThreads / 32);
+    fn = reinterpret_cast<const void*>(dropout_any_kernel<T, RESIDUAL>);
+  }
+  if (grid > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+  void* args[] = {&p, &shares};  // dropout_kernel takes the first alone
+  return launch_kernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kDropThreads), 0, stream, args, false);
+}
+
+template <typename T>
+cudaError_t run_typed(DropoutParams& p, bool vec, cudaStream_t stream) {
+  return p.residual ? run<T, true>(p, vec, stream) : run<T, false>(p, vec, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_dropout(const DropoutParams& params, int dtype, bool vec, cudaStream_t stream) {
+  if (params.tokens == 0) return cudaSuccess;
+  DropoutParams p = params;
+  switch (dtype) {
+    case ZC_BF16: return run_typed<__nv_bfloat16>(p, vec, stream);
+    case ZC_F16: return run_typed<__half>(p, vec, stream);
+    default: return run_typed<float>(p, vec, stream);
+  }
+}
+
+}  // namespace zc

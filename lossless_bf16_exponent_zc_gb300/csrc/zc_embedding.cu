@@ -1,0 +1,601 @@
+// zc_embedding.cu -- rows of an embedding table for a run of token ids, scaled, and the table's
+// gradient.  Definitions in include/zc.h.
+//
+//   out[t] = scale table[id_t],    dtable[v] = scale (sum over t with id_t = v, in order, of dout[t])
+//
+// The gradient sorts the tokens by id (a stable radix sort), so that every row of the table is
+// summed in fp32 in the order of its tokens and written once: no sum depends on timing, and no
+// memory is read back.  All parts but the sort are bound by memory.
+#include "zc_internal.h"
+#include "zc_layer.cuh"
+
+namespace zc {
+
+namespace {
+
+constexpr int kEmbedThreads = 256;
+
+__device__ __forceinline__ int64_t id_at(const void* ids, int ids64, uint64_t t) {
+  return ids64 ? static_cast<const int64_t*>(ids)[t] : static_cast<const int32_t*>(ids)[t];
+}
+
+// True if a token has a row: its id is reported if it is beyond the table.
+__device__ __forceinline__ bool has_row(int64_t id, uint64_t vocab, int32_t* status) {
+  if (id >= static_cast<int64_t>(vocab)) set_status(status, ZC_ERR_BAD_INDEX);
+  return id >= 0 && id < static_cast<int64_t>(vocab);
+}
+
+// N values of TT at p, which lies anywhere, as the 16-byte pieces that hold them (ALIGNED: it lies
+// on one), read now and taken apart later.
+template <typename TT, int N, bool ALIGNED>
+struct AnyValues {
+  static constexpr int V = kPieceOf<TT>, NP = N / V;
+  uint4 w[ALIGNED ? NP : NP + 1];
+  uint32_t off;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < (ALIGNED ? NP : NP + 1); k++) w[k] = make_uint4(0u, 0u, 0u, 0u);
+    off = 0;
+  }
+  __device__ __forceinline__ void load(const TT* p) {
+    off = ALIGNED ? 0 : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
+#pragma unroll
+    for (int k = 0; k < NP; k++) w[k] = from[k];
+    if constexpr (!ALIGNED) w[NP] = off ? from[NP] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void get(float (&f)[N]) const {
+#pragma unroll
+    for (int k = 0; k < NP; k++) {
+      float v[V];
+      if constexpr (ALIGNED)
+        Piece<TT, V>{w[k]}.get(v);
+      else
+        Piece<TT, V>{shift_pieces<TT>(w[k], w[k + 1], off)}.get(v);
+#pragma unroll
+      for (int j = 0; j < V; j++) f[k * V + j] = v[j];
+    }
+  }
+};
+
+// ------------------------------------------------------------------ lookup
+// A thread takes UNITS 16-byte pieces of the output, kEmbedThreads apart, all loads before the first
+// store.
+template <typename T, typename TT, int UNITS>
+__global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedParams p) {
+  constexpr int V = kPieceOf<T>;
+  pdl_begin();
+  const uint32_t pieces = p.hidden / V;
+  const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads * UNITS), t0 = i0 / pieces;
+  const uint32_t c0 = static_cast<uint32_t>(i0 - t0 * pieces) + threadIdx.x;
+  AnyValues<TT, V, true> v[UNITS];
+  T* to[UNITS];
+#pragma unroll
+  for (int q = 0; q < UNITS; q++) {
+    const uint32_t i = c0 + q * kEmbedThreads, dt = i / pieces, first = (i - dt * pieces) * V;
+    const uint64_t t = t0 + dt;
+    to[q] = t < p.tokens ? static_cast<T*>(p.out) + t * p.hidden + first : nullptr;
+    v[q].clear();
+    if (!to[q]) continue;
+    const int64_t id = id_at(p.ids, p.ids64, t);
+    if (has_row(id, p.vocab, p.status))
+      v[q].load(static_cast<const TT*>(p.table) + static_cast<uint64_t>(id) * p.table_stride + first);
+  }
+#pragma unroll
+  for (int q = 0; q < UNITS; q++) {
+    if (!to[q]) continue;
+    float f[V];
+    v[q].get(f);
+#pragma unroll
+    for (int j = 0; j < V; j++) f[j] *= p.scale;
+    Piece<T, V> o;
+    o.set(f);
+    o.store(to[q]);
+  }
+}
+
+// The same off 16 bytes: a lane takes a unit of a token's output (RowCut).
+template <typename T, typename TT>
+__global__ void __launch_bounds__(kEmbedThreads) embed_any_kernel(EmbedParams p, uint32_t shares) {
+  constexpr int V = kPieceOf<T>;
+  pdl_begin();
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads / 32) + (threadIdx.x >> 5), t = i / shares;
+  if (t >= p.tokens) return;
+  T* out = static_cast<T*>(p.out) + t * p.hidden;
+  const RowCut<T> cut(out, p.hidden);
+  uint32_t first;
+  const uint32_t values = cut.unit(static_cast<uint32_t>(i - t * shares) * 32 + lane_id(), p.hidden, &first);
+  const int64_t id = id_at(p.ids, p.ids64, t);
+  const bool there = has_row(id, p.vocab, p.status);
+  const TT* row = static_cast<const TT*>(p.table) + (there ? static_cast<uint64_t>(id) * p.table_stride : 0);
+  if (values == V) {
+    AnyValues<TT, V, false> v;
+    v.clear();
+    if (there) v.load(row + first);
+    float f[V];
+    v.get(f);
+#pragma unroll
+    for (int j = 0; j < V; j++) f[j] *= p.scale;
+    Piece<T, V> o;
+    o.set(f);
+    o.store(out + first);
+  } else if (values) {
+    out[first] = from_f32<T>(there ? p.scale * to_f32<TT>(row[first]) : 0.f);
+  }
+}
+
+// ------------------------------------------------------------------ the tokens sorted by id
+// A stable radix sort, a digit of up to 10 bits a pass: counts of every chunk's digits, their prefix
+// over the chunks, then the places.  Tokens without a row have key `vocab` and come last.
+constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
+constexpr uint32_t kSortBins = 1u << kEmbedDigitBits;
+
+__device__ __forceinline__ uint32_t sort_key(const EmbedBwdParams& p, uint64_t i) {
+  if (p.keys_in) return p.keys_in[i];
+  const int64_t id = id_at(p.ids, p.ids64, i);
+  return static_cast<uint32_t>(has_row(id, p.vocab, p.status) ? id : static_cast<int64_t>(p.vocab));
+}
+
+__global__ void __launch_bounds__(kSortThreads) embed_count_kernel(EmbedBwdParams p) {
+  __shared__ uint32_t hist[kSortBins];
+  pdl_allow_dependents();
+  for (uint32_t e = threadIdx.x; e < kSortBins; e += kSortThreads) hist[e] = 0;
+  __syncthreads();
+  pdl_wait();
+  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kEmbedSortChunk;
+  const uint32_t n = static_cast<uint32_t>(min(static_cast<uint64_t>(kEmbedSortChunk), p.tokens - first));
+  const uint32_t bins = 1u << p.digit_bits;
+  for (uint32_t i = threadIdx.x; i < n; i += kSortThreads) {
+    const uint32_t key = sort_key(p, first + i);
+    atomicAdd(&hist[(key >> p.shift) & (bins - 1)], 1u);
+    if (!p.keys_in && key < p.vocab && p.present) atomicOr(&p.present[key >> 5], 1u << (key & 31));
+  }
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e < bins; e += kSortThreads)
+    p.counts[static_cast<uint64_t>(e) * p.sort_chunks + blockIdx.x] = hist[e];
+}
+
+// The exclusive prefix over the chunks of a digit's counts, in place, and their total: a warp a digit.
+__global__ void __launch_bounds__(kSortThreads) embed_prefix_kernel(EmbedBwdParams p) {
+  pdl_begin();
+  const uint32_t digit = blockIdx.x * kSortWarps + (threadIdx.x >> 5), lane = lane_id();
+  if (digit >= 1u << p.digit_bits) return;
+  uint32_t* c = p.counts + static_cast<uint64_t>(digit) * p.sort_chunks;
+  uint32_t base = 0;
+  for (uint32_t i = 0; i < p.sort_chunks; i += 128) {  // four pieces on their way at once
+    uint32_t v[4];
+#pragma unroll
+    for (uint32_t q = 0; q < 4; q++) v[q] = i + q * 32 + lane < p.sort_chunks ? c[i + q * 32 + lane] : 0;
+#pragma unroll
+    for (uint32_t q = 0; q < 4; q++) {
+      const uint32_t upto = warp_inclusive_scan(v[q]);
+      if (i + q * 32 + lane < p.sort_chunks) c[i + q * 32 + lane] = base + upto - v[q];
+      base += __shfl_sync(kFull, upto, 31);
+    }
+  }
+  if (lane == 0) p.totals[digit] = base;
+}
+
+__device__ __forceinline__ uint32_t lanes_below_mask() { return (1u << lane_id()) - 1u; }
+
+// The lanes whose digit equals this one's.
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit, uint32_t bits) {
+  uint32_t equal = kFull;
+  for (uint32_t b = 0; b < bits; b++) {
+    const bool one = (digit >> b) & 1u;
+    const uint32_t ones = __ballot_sync(kFull, one);
+    equal &= one ? ones : ~ones;
+  }
+  return equal;
+}
+
+// Places a chunk's keys: each warp an eighth of it in order, 32 keys at a time.
+__global__ void __launch_bounds__(kSortThreads) embed_place_kernel(EmbedBwdParams p) {
+  extern __shared__ uint32_t sort_smem[];  // [kSortWarps][bins], then the digits' first places [bins]
+  __shared__ uint32_t warp_totals[kSortWarps];
+  pdl_begin();
+  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, bins = 1u << p.digit_bits;
+  uint32_t* start = sort_smem + kSortWarps * bins;
+  uint32_t* own = sort_smem + warp * bins;
+  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kEmbedSortChunk;
+  const uint32_t n = static_cast<uint32_t>(min(static_cast<uint64_t>(kEmbedSortChunk), p.tokens - first));
+  constexpr uint32_t kTurns = kEmbedSortChunk / kSortThreads;
+  const uint32_t base = warp * (kTurns * 32) + lane;
+  uint32_t key[kTurns], token[kTurns], equal[kTurns];
+#pragma unroll
+  for (uint32_t i = 0; i < kTurns; i++) {
+    const bool there = base + i * 32 < n;
+    key[i] = there ? sort_key(p, first + base + i * 32) : 0xFFFFFFFFu;
+    token[i] = static_cast<uint32_t>(first + base + i * 32);
+    if (there && p.keys_in) token[i] = p.tokens_in[first + base + i * 32];
+  }
+  // where each digit starts: the totals' exclusive prefix
+  const uint32_t per = (bins + kSortThreads - 1) / kSortThreads;
+  uint32_t sum = 0;
+  for (uint32_t i = 0; i < per; i++)
+    if (threadIdx.x * per + i < bins) sum += p.totals[threadIdx.x * per + i];
+  const uint32_t upto = warp_inclusive_scan(sum);
+  if (lane == 31) warp_totals[warp] = upto;
+  for (uint32_t e = lane; e < bins; e += 32) own[e] = 0;
+  __syncthreads();
+  uint32_t at = upto - sum;
+  for (uint32_t w = 0; w < warp; w++) at += warp_totals[w];
+  for (uint32_t i = 0; i < per; i++) {
+    const uint32_t e = threadIdx.x * per + i;
+    if (e >= bins) break;
+    start[e] = at + p.counts[static_cast<uint64_t>(e) * p.sort_chunks + blockIdx.x];
+    at += p.totals[e];
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < kTurns; i++) {
+    const bool there = base + i * 32 < n;
+    const uint32_t digit = there ? (key[i] >> p.shift) & (bins - 1) : bins;  // its own class beyond the end
+    equal[i] = same_digit(digit, p.digit_bits + 1);
+    if (there && (equal[i] & lanes_below_mask()) == 0) own[digit] += __popc(equal[i]);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e < bins; e += kSortThreads) {
+    uint32_t before = start[e];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; w++) {
+      const uint32_t c = sort_smem[w * bins + e];
+      sort_smem[w * bins + e] = before;
+      before += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (uint32_t i = 0; i < kTurns; i++) {
+    const bool there = base + i * 32 < n;
+    const uint32_t below = equal[i] & lanes_below_mask();
+    const uint32_t digit = (key[i] >> p.shift) & (bins - 1);
+    if (there) {
+      const uint32_t to = own[digit] + __popc(below);
+      p.keys_out[to] = key[i];
+      p.tokens_out[to] = token[i];
+    }
+    __syncwarp();
+    if (there && below == 0) own[digit] += __popc(equal[i]);
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------ sums
+// A warp adds up kEmbedRun tokens of the sorted order over 256 columns, a lane eight of them (8 /
+// V pieces, 32 apart).  Where a row's tokens all lie in the run, the row is written; where they
+// go on in a neighbouring run, the sum is left in the workspace: slot 0 of the run for the tokens of
+// a row that began before it, slot 1 for one that begins in it and goes on.
+constexpr uint32_t kSlab = 256;
+constexpr int kRowLoads = 4;  // rows on their way at once
+
+template <typename T, typename TT, bool VEC>
+struct EmbedCols {
+  static constexpr int V = kPieceOf<T>, NP = 8 / V;
+  AnyValues<T, V, VEC> w[NP];
+  __device__ __forceinline__ static uint32_t col(uint32_t slab, int i) {
+    return slab * kSlab + (i * 32 + lane_id()) * V;
+  }
+  __device__ __forceinline__ void load(const T* row, uint32_t slab, uint32_t hidden) {
+#pragma unroll
+    for (int i = 0; i < NP; i++) {
+      const uint32_t c = col(slab, i);
+      w[i].clear();
+      if (whole_piece<T>(c, hidden)) {
+        w[i].load(row + c);
+      } else if (c < hidden) {  // the last values of the row, one by one
+        uint32_t part[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+          if (c + j >= hidden) continue;
+          if constexpr (sizeof(T) == 4)
+            part[j] = reinterpret_cast<const uint32_t*>(row)[c + j];
+          else
+            part[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[c + j]) << (j & 1) * 16;
+        }
+        w[i].w[0] = make_uint4(part[0], part[1], part[2], part[3]);
+      }
+    }
+  }
+  __device__ __forceinline__ void add(float (&acc)[8]) const {
+#pragma unroll
+    for (int i = 0; i < NP; i++) {
+      float f[V];
+      w[i].get(f);
+#pragma unroll
+      for (int j = 0; j < V; j++) acc[i * V + j] += f[j];
+    }
+  }
+};
+
+// Writes (or adds) scale acc to the lane's columns of a table row.
+template <typename T, typename TT, bool VEC>
+__device__ __forceinline__ void put_row(const EmbedBwdParams& p, uint64_t row, uint32_t slab, const float (&acc)[8]) {
+  constexpr int V = kPieceOf<T>, W = kPieceOf<TT>;
+  TT* to = static_cast<TT*>(p.dtable) + row * p.hidden;
+#pragma unroll
+  for (int i = 0; i < 8 / V; i++) {
+    const uint32_t c = EmbedCols<T, TT, VEC>::col(slab, i);
+    if (VEC && !p.accumulate) {
+      if (c >= p.hidden) continue;
+#pragma unroll
+      for (int k = 0; k < V; k += W) {
+        float f[W];
+#pragma unroll
+        for (int j = 0; j < W; j++) f[j] = p.scale * acc[i * V + (k + j) % V];
+        Piece<TT, W> o;
+        o.set(f);
+        o.store(to + c + k);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        if (c + j >= p.hidden) continue;
+        const float old = p.accumulate ? to_f32<TT>(to[c + j]) : 0.f;
+        to[c + j] = from_f32<TT>(fmaf(p.scale, acc[i * V + j], old));
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float* part_of(const EmbedBwdParams& p, uint64_t run, uint32_t slot, uint32_t slab) {
+  return p.parts + ((run * 2 + slot) * p.slabs + slab) * kSlab;
+}
+
+template <typename T, typename TT, bool VEC>
+__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(EmbedBwdParams p) {
+  pdl_begin();
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads / 32) + (threadIdx.x >> 5), run = i / p.slabs;
+  if (run >= p.runs) return;
+  const uint32_t lane = lane_id(), slab = static_cast<uint32_t>(i - run * p.slabs);
+  const uint64_t first = run * kEmbedRun;
+  const uint32_t none = static_cast<uint32_t>(p.vocab);
+  const uint32_t key = first + lane < p.tokens ? p.keys_in[first + lane] : none;
+  const uint32_t token = first + lane < p.tokens ? p.tokens_in[first + lane] : 0;
+  const uint32_t before = first ? p.keys_in[first - 1] : none;
+  const uint32_t after = first + kEmbedRun < p.tokens ? p.keys_in[first + kEmbedRun] : none;
+  const uint32_t n = __popc(__ballot_sync(kFull, key != none));  // those with a row come first
+  const uint32_t next = __shfl_down_sync(kFull, key, 1);
+  const uint32_t ends = __ballot_sync(kFull, lane == 31 || next != key);
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; j++) acc[j] = 0.f;
+  bool began = __shfl_sync(kFull, key, 0) == before;  // the row at hand began before the run
+  for (uint32_t r0 = 0; r0 < n; r0 += kRowLoads) {
+    EmbedCols<T, TT, VEC> v[kRowLoads];
+#pragma unroll
+    for (int q = 0; q < kRowLoads; q++) {
+      const uint64_t t = __shfl_sync(kFull, token, (r0 + q) & 31);
+      if (r0 + q < n) v[q].load(static_cast<const T*>(p.dout) + t * p.dout_stride, slab, p.hidden);
+    }
+#pragma unroll
+    for (int q = 0; q < kRowLoads; q++) {
+      const uint32_t r = r0 + q;
+      if (r >= n) break;
+      v[q].add(acc);
+      if (!(ends >> r & 1)) continue;
+      const uint32_t row = __shfl_sync(kFull, key, r);
+      const bool goes_on = r == 31 && after == row;
+      if (began || goes_on) {
+        float* to = part_of(p, run, began ? 0 : 1, slab) + lane * 8;
+        *reinterpret_cast<float4*>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      } else {
+        put_row<T, TT, VEC>(p, row, slab, acc);
+      }
+      began = false;
+#pragma unroll
+      for (int j = 0; j < 8; j++) acc[j] = 0.f;
+    }
+  }
+}
+
+// Rows whose tokens lie in several runs: the CTA of the run that such a row begins in, and of one
+// slab, adds the parts, each warp a share of them in order.
+template <typename T, typename TT, bool VEC>
+__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedBwdParams p) {
+  __shared__ float sums[kEmbedThreads / 32][kSlab];
+  pdl_begin();
+  const uint64_t run = blockIdx.x / p.slabs;
+  const uint32_t slab = static_cast<uint32_t>(blockIdx.x - run * p.slabs), lane = lane_id(), warp = threadIdx.x >> 5;
+  const uint64_t first = run * kEmbedRun, next = first + kEmbedRun;
+  if (next >= p.tokens) return;
+  const uint32_t row = p.keys_in[next - 1];
+  if (row == p.vocab || p.keys_in[next] != row) return;               // no row goes on behind the run
+  if (p.keys_in[first] == row && first && p.keys_in[first - 1] == row) return;  // it began before the run
+  uint64_t last = run + 1;  // the last run with tokens of the row
+  for (;; last += 32) {
+    const uint64_t at = (last + lane + 1) * kEmbedRun;
+    const uint32_t more = __ballot_sync(kFull, at < p.tokens && p.keys_in[at] == row);
+    if (more != kFull) {
+      last += __ffs(~more) - 1;
+      break;
+    }
+  }
+  const uint64_t count = last - run + 1;
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; j++) acc[j] = 0.f;
+  const uint64_t to = count * (warp + 1) / (kEmbedThreads / 32);
+#pragma unroll 4
+  for (uint64_t i = count * warp / (kEmbedThreads / 32); i < to; i++) {
+    const float* from = part_of(p, run + i, i ? 0 : 1, slab) + lane * 8;
+    const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
+    acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
+    acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; j++) sums[warp][j * 32 + lane] = acc[j];
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    acc[j] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kEmbedThreads / 32; w++) acc[j] += sums[w][j * 32 + lane];
+  }
+  put_row<T, TT, VEC>(p, row, slab, acc);
+}
+
+// Zeroes the rows that no token asks for, a warp a row.
+__global__ void __launch_bounds__(kEmbedThreads) embed_fill_kernel(EmbedBwdParams p, uint32_t size) {
+  pdl_begin();
+  const uint32_t lane = lane_id();
+  const uint64_t warps = static_cast<uint64_t>(gridDim.x) * (kEmbedThreads / 32), bytes = static_cast<uint64_t>(p.hidden) * size;
+  for (uint64_t v = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads / 32) + (threadIdx.x >> 5); v < p.vocab; v += warps) {
+    if (p.present[v >> 5] >> (v & 31) & 1) continue;
+    uint8_t* row = static_cast<uint8_t*>(p.dtable) + v * bytes;
+    const uint64_t head = min(bytes, static_cast<uint64_t>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15));
+    const uint64_t body = (bytes - head) / 16;
+    uint4* pieces = reinterpret_cast<uint4*>(row + head);
+    for (uint64_t i = lane; i < body; i += 32) pieces[i] = make_uint4(0u, 0u, 0u, 0u);
+    const uint64_t rest = bytes - body * 16;  // bytes outside the pieces
+    if (lane * 2 < rest) {
+      const uint64_t at = lane * 2 < head ? lane * 2 : body * 16 + lane * 2;
+      *reinterpret_cast<uint16_t*>(row + at) = 0;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launches
+uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+cudaError_t run(const void* fn, uint64_t grid, int threads, int smem, cudaStream_t stream, void** args) {
+  if (grid == 0) return cudaSuccess;
+  if (grid > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+  return launch_kernel(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, stream, args, false);
+}
+
+template <typename T, typename TT>
+cudaError_t lookup(EmbedParams& p, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
+  if (!vec) {
+    uint32_t shares = static_cast<uint32_t>(ceil_div(any_units<T>(p.hidden), 32));
+    void* args[] = {&p, &shares};
+    return run(reinterpret_cast<const void*>(embed_any_kernel<T, TT>), ceil_div(p.tokens * shares, kEmbedThreads / 32),
+               kEmbedThreads, 0, stream, args);
+  }
+  const uint64_t all = p.tokens * (p.hidden / kPieceOf<T>);
+  void* args[] = {&p};
+  if (all <= 2ull * kEmbedThreads * static_cast<uint64_t>(dev.sm_count))
+    return run(reinterpret_cast<const void*>(embed_kernel<T, TT, 1>), ceil_div(all, kEmbedThreads), kEmbedThreads, 0,
+               stream, args);
+  return run(reinterpret_cast<const void*>(embed_kernel<T, TT, 4>), ceil_div(all, 4 * kEmbedThreads), kEmbedThreads, 0,
+             stream, args);
+}
+
+template <typename T, typename TT, bool VEC>
+cudaError_t sums(EmbedBwdParams& p, cudaStream_t stream) {
+  void* args[] = {&p};
+  cudaError_t e = run(reinterpret_cast<const void*>(embed_sum_kernel<T, TT, VEC>),
+                      ceil_div(p.runs * p.slabs, kEmbedThreads / 32), kEmbedThreads, 0, stream, args);
+  if (e != cudaSuccess || p.runs < 2) return e;
+  return run(reinterpret_cast<const void*>(embed_join_kernel<T, TT, VEC>), p.runs * p.slabs, kEmbedThreads, 0, stream,
+             args);
+}
+template <typename T, typename TT>
+cudaError_t sums(EmbedBwdParams& p, bool vec, cudaStream_t stream) {
+  return vec ? sums<T, TT, true>(p, stream) : sums<T, TT, false>(p, stream);
+}
+
+// Where a gradient's workspace holds what.
+struct EmbedWork {
+  uint64_t keys, tokens, counts, totals, present, parts, bytes;  // byte offsets; keys and tokens have two halves
+  EmbedWork(uint64_t n, uint64_t vocab, uint32_t hidden) {
+    const uint64_t chunks = ceil_div(n, kEmbedSortChunk), runs = ceil_div(n, kEmbedRun);
+    uint64_t at = 0;
+    auto take = [&](uint64_t words) {
+      const uint64_t here = at;
+      at += ceil_div(words * 4, 16) * 16;
+      return here;
+    };
+    parts = take(runs * 2 * ceil_div(hidden, kSlab) * kSlab);
+    keys = take(2 * n);
+    tokens = take(2 * n);
+    counts = take(kSortBins * chunks);
+    totals = take(kSortBins);
+    present = take(ceil_div(vocab, 32));
+    bytes = at;
+  }
+};
+
+}  // namespace
+
+cudaError_t launch_embed(const EmbedParams& params, int dtype, int table_f32, bool vec, cudaStream_t stream,
+                         const DeviceInfo& dev) {
+  if (params.tokens == 0) return cudaSuccess;
+  EmbedParams p = params;
+  switch (dtype) {
+    case ZC_BF16:
+      return table_f32 ? lookup<__nv_bfloat16, float>(p, vec, stream, dev)
+                       : lookup<__nv_bfloat16, __nv_bfloat16>(p, vec, stream, dev);
+    case ZC_F16:
+      return table_f32 ? lookup<__half, float>(p, vec, stream, dev) : lookup<__half, __half>(p, vec, stream, dev);
+    default: return lookup<float, float>(p, vec, stream, dev);
+  }
+}
+
+uint64_t embed_workspace_bytes(uint64_t tokens, uint64_t vocab, uint32_t hidden) {
+  return EmbedWork(tokens, vocab, hidden).bytes;
+}
+
+cudaError_t launch_embed_bwd(const EmbedBwdParams& params, int dtype, int table_f32, bool vec, void* ws,
+                             cudaStream_t stream, const DeviceInfo& dev) {
+  EmbedBwdParams p = params;
+  const EmbedWork at(p.tokens, p.vocab, p.hidden);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(base + at.keys), reinterpret_cast<uint32_t*>(base + at.keys) + p.tokens};
+  uint32_t* tokens[2] = {reinterpret_cast<uint32_t*>(base + at.tokens),
+                         reinterpret_cast<uint32_t*>(base + at.tokens) + p.tokens};
+  p.counts = reinterpret_cast<uint32_t*>(base + at.counts);
+  p.totals = reinterpret_cast<uint32_t*>(base + at.totals);
+  p.present = p.accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + at.present);
+  p.parts = reinterpret_cast<float*>(base + at.parts);
+  p.sort_chunks = static_cast<uint32_t>(ceil_div(p.tokens, kEmbedSortChunk));
+  p.runs = ceil_div(p.tokens, kEmbedRun);
+  p.slabs = static_cast<uint32_t>(ceil_div(p.hidden, kSlab));
+  cudaError_t e = cudaSuccess;
+  if (p.present) e = cudaMemsetAsync(p.present, 0, ceil_div(p.vocab, 32) * 4, stream);
+  if (e != cudaSuccess) return e;
+  uint32_t bits = 1;  // of the keys 0 .. vocab
+  while (p.vocab >> bits) bits++;
+  const uint32_t passes = static_cast<uint32_t>(ceil_div(bits, kEmbedDigitBits));
+  static KernelPrep prep;
+  int per_sm = 0;
+  constexpr int kMostSmem = (kSortWarps + 1) * static_cast<int>(kSortBins) * 4;
+  e = prepare_kernel(prep, reinterpret_cast<const void*>(embed_place_kernel), kSortThreads, kMostSmem, dev, &per_sm);
+  void* args[] = {&p};
+  for (uint32_t pass = 0; pass < passes && e == cudaSuccess && p.tokens; pass++) {
+    p.shift = bits * pass / passes;
+    p.digit_bits = bits * (pass + 1) / passes - p.shift;
+    p.keys_in = pass ? keys[pass + 1 & 1] : nullptr;
+    p.tokens_in = pass ? tokens[pass + 1 & 1] : nullptr;
+    p.keys_out = keys[pass & 1];
+    p.tokens_out = tokens[pass & 1];
+    e = run(reinterpret_cast<const void*>(embed_count_kernel), p.sort_chunks, kSortThreads, 0, stream, args);
+    if (e == cudaSuccess)
+      e = run(reinterpret_cast<const void*>(embed_prefix_kernel), ceil_div(1u << p.digit_bits, kSortWarps),
+              kSortThreads, 0, stream, args);
+    if (e == cudaSuccess)
+      e = run(reinterpret_cast<const void*>(embed_place_kernel), p.sort_chunks, kSortThreads,
+              (kSortWarps + 1) * (4 << p.digit_bits), stream, args);
+  }
+  if (e != cudaSuccess) return e;
+  p.keys_in = keys[passes + 1 & 1];
+  p.tokens_in = tokens[passes + 1 & 1];
+  if (p.present) {
+    uint32_t size = dtype == ZC_F32 || table_f32 ? 4 : 2;
+    void* fill[] = {&p, &size};
+    const uint64_t most = 8ull * static_cast<uint64_t>(dev.sm_count), all = ceil_div(p.vocab, kEmbedThreads / 32);
+    e = run(reinterpret_cast<const void*>(embed_fill_kernel), all < most ? all : most, kEmbedThreads, 0, stream, fill);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.tokens == 0) return e;
+  switch (dtype) {
+    case ZC_BF16:
+      return table_f32 ? sums<__nv_bfloat16, float>(p, vec, stream) : sums<__nv_bfloat16, __nv_bfloat16>(p, vec, stream);
+    case ZC_F16: return table_f32 ? sums<__half, float>(p, vec, stream) : sums<__half, __half>(p, vec, stream);
+    default: return sums<float, float>(p, vec, stream);
+  }
+}
+
+}  // namespace zc

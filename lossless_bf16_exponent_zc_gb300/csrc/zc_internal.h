@@ -203,6 +203,125 @@ uint64_t norm_workspace_bytes(uint64_t tokens, uint32_t hidden);
 cudaError_t launch_norm(const NormParams& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev);
 cudaError_t launch_norm_bwd(const NormBwdParams& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev);
 
+// ---- the other operators of a training step (zc_balance.cu, zc_layer_norm.cu, zc_dropout.cu,
+// zc_embedding.cu); conventions as above.
+struct BalanceParams {
+  const void* logits;
+  uint64_t stride, tokens, sequences;
+  uint32_t experts, k;
+  int sigmoid;
+  const int32_t* ids;
+  const uint8_t* mask;  // NULL: every token counts
+  float* loss;
+  int32_t* counts;
+  float* slope;
+  // set by the launch: each sequence's tokens in chunks, and the workspace
+  uint32_t chunks;
+  uint64_t chunk_tokens;
+  uint32_t* ticket;
+  float* part_sums;
+  int32_t* part_counts;
+  uint32_t* part_tokens;
+  float* part_loss;
+};
+struct BalanceBwdParams {
+  const float* dloss;
+  const void* logits;
+  uint64_t stride, tokens, seq_tokens;
+  uint32_t experts;
+  int sigmoid;
+  const uint8_t* mask;
+  const float* slope;
+  void* dlogits;
+};
+uint64_t balance_workspace_bytes(uint64_t tokens, uint32_t experts, uint64_t sequences);
+cudaError_t launch_balance(const BalanceParams& p, int dtype, void* ws, cudaStream_t stream);
+cudaError_t launch_balance_bwd(const BalanceBwdParams& p, int dtype, cudaStream_t stream);
+
+// What a dropout keeps (zc_dropout.cuh); rng NULL: everything.
+struct Dropout {
+  const int64_t* rng;  // seed, offset
+  uint32_t call;
+  uint32_t limit;  // kept: 16 bits that are at least this
+  float factor;
+};
+struct DropoutParams {
+  const void *x, *residual;  // residual NULL: none
+  uint64_t x_stride, residual_stride, tokens;
+  uint32_t width;
+  float residual_scale;
+  Dropout drop;
+  void* out;
+};
+cudaError_t launch_dropout(const DropoutParams& p, int dtype, bool vec, cudaStream_t stream);
+
+struct LayerNormParams {
+  const void *y, *x;  // y NULL: the norm of x alone
+  uint64_t y_stride, x_stride, tokens;
+  const void *weight, *bias;  // bias NULL: none
+  uint32_t hidden;
+  int params_f32;
+  float residual_scale, eps;
+  Dropout drop;
+  void *x_new, *h;
+  float* stats;  // NULL: not wanted
+};
+struct LayerNormBwdParams {
+  const void *dx_new, *dh, *x_new;  // dx_new NULL: zero
+  uint64_t dx_new_stride, dh_stride, x_new_stride, tokens;
+  const float* stats;
+  const void* weight;
+  uint32_t hidden;
+  int params_f32;
+  float residual_scale;
+  Dropout drop;
+  void *dy, *dx, *dweight, *dbias;  // dy, dbias NULL: not wanted
+  float* parts;                     // workspace: two sums of the columns for every walker
+  uint32_t ctas;                    // set by the launch
+};
+uint64_t norm_max_walkers(uint32_t hidden);  // that the norms' workspace has room for
+cudaError_t launch_layer_norm(const LayerNormParams& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev);
+cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int dtype, bool vec, cudaStream_t stream,
+                                  const DeviceInfo& dev);
+
+struct EmbedParams {
+  const void* ids;
+  int ids64;
+  const void* table;
+  uint64_t table_stride, tokens, vocab;
+  uint32_t hidden;
+  float scale;
+  void* out;
+  int32_t* status;
+};
+constexpr uint32_t kEmbedDigitBits = 10;    // of the gradient's radix sort, at most
+constexpr uint32_t kEmbedSortChunk = 1024;  // keys of a CTA there
+constexpr uint32_t kEmbedRun = 32;          // sorted tokens that a warp adds up
+struct EmbedBwdParams {
+  const void* dout;
+  const void* ids;
+  int ids64;
+  uint64_t dout_stride, tokens, vocab;
+  uint32_t hidden;
+  float scale;
+  int accumulate;
+  void* dtable;
+  int32_t* status;
+  // set by the launch: the workspace, the pass of the sort, and the sums' cut
+  const uint32_t *keys_in, *tokens_in;  // of the pass; NULL in the first, which reads the ids
+  uint32_t *keys_out, *tokens_out, *counts, *totals;
+  uint32_t* present;  // a bit for every row that a token asks for; NULL with accumulate
+  uint32_t sort_chunks, shift, digit_bits;
+  float* parts;
+  uint64_t runs;
+  uint32_t slabs;
+};
+uint64_t embed_workspace_bytes(uint64_t tokens, uint64_t vocab, uint32_t hidden);
+cudaError_t launch_embed(const EmbedParams& p, int dtype, int table_f32, bool vec, cudaStream_t stream,
+                         const DeviceInfo& dev);
+cudaError_t launch_embed_bwd(const EmbedBwdParams& p, int dtype, int table_f32, bool vec, void* ws, cudaStream_t stream,
+                             const DeviceInfo& dev);
+
 cudaError_t launch_histogram(const uint16_t* in, uint64_t n, uint8_t* cb_out, uint32_t* hist_out, WsHeader* ws,
                              int32_t* status, cudaStream_t stream, const DeviceInfo& dev);
 

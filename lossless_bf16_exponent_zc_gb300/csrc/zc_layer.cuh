@@ -1,5 +1,5 @@
 // zc_layer.cuh -- device building blocks of the operators around an expert-parallel layer
-// (zc_moe.cu, zc_norm.cu): values of three types moved in 16-byte pieces or one at a time, computed
+// (zc_moe.cu, zc_norm.cu) and next to it: values of three types moved in 16-byte pieces or one at a time, computed
 // in fp32, and sums over a warp or a CTA whose order is fixed (the same inputs give the same bits).
 #pragma once
 
@@ -187,6 +187,53 @@ __device__ __forceinline__ float warp_max_f32(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
   return v;
+}
+
+// 1 / (1 + exp(-l)), each step rounded as the plain expression's (a correctly rounded reciprocal is
+// the quotient).
+__device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(__fadd_rn(1.f, expf(-l))); }
+
+// Lane l's N values of a row, N l .. N l + N - 1; minus infinity beyond the width.  VEC: they are
+// whole 4-, 8- or 16-byte pieces.
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void load_row(const T* row, uint32_t width, float (&v)[N]) {
+  const uint32_t first = lane_id() * N;
+  if (VEC && N * sizeof(T) >= 4) {
+    constexpr int kBytes = N * static_cast<int>(sizeof(T));
+    constexpr int kPart = kBytes >= 16 ? 16 : kBytes;  // bytes of a piece
+    constexpr int kOf = kPart / static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int i = 0; i < N; i += kOf) {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (first + i < width) {
+        const T* src = row + first + i;
+        if (kPart == 16) {
+          const uint4 q = *reinterpret_cast<const uint4*>(src);
+          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else if (kPart == 8) {
+          const uint2 q = *reinterpret_cast<const uint2*>(src);
+          w[0] = q.x, w[1] = q.y;
+        } else {
+          w[0] = *reinterpret_cast<const uint32_t*>(src);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kOf; j++) {
+        float f;
+        if constexpr (sizeof(T) == 4) {
+          f = __uint_as_float(w[j & 3]);
+        } else {
+          float lo, hi;
+          unpack2(w[(j / 2) & 3], lo, hi, T());
+          f = j & 1 ? hi : lo;
+        }
+        v[i + j] = first + i < width ? f : -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; j++) v[j] = first + j < width ? to_f32<T>(row[first + j]) : -INFINITY;
+  }
 }
 
 // Thread-block clusters: the barrier of all threads of the cluster in its two halves (release,

@@ -29,10 +29,6 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return f != f ? 0xFFFFFFFFu : key;
 }
 
-// 1 / (1 + exp(-l)), each step rounded as the plain expression's (a correctly rounded reciprocal is
-// the quotient).
-__device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(__fadd_rn(1.f, expf(-l))); }
-
 // The hyperbolic tangent, good to 2^-11 of it (the instruction's stated error).
 __device__ __forceinline__ float tanh_estimate(float x) {
   float y;
@@ -45,49 +41,6 @@ __device__ __forceinline__ float warp_max_of(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// Lane l's N values of a row, N l .. N l + N - 1; minus infinity beyond the width.  VEC: they are
-// whole 4-, 8- or 16-byte pieces.
-template <typename T, int N, bool VEC>
-__device__ __forceinline__ void load_row(const T* row, uint32_t width, float (&v)[N]) {
-  const uint32_t first = lane_id() * N;
-  if (VEC && N * sizeof(T) >= 4) {
-    constexpr int kBytes = N * static_cast<int>(sizeof(T));
-    constexpr int kPart = kBytes >= 16 ? 16 : kBytes;  // bytes of a piece
-    constexpr int kOf = kPart / static_cast<int>(sizeof(T));
-#pragma unroll
-    for (int i = 0; i < N; i += kOf) {
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-      if (first + i < width) {
-        const T* src = row + first + i;
-        if (kPart == 16) {
-          const uint4 q = *reinterpret_cast<const uint4*>(src);
-          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-        } else if (kPart == 8) {
-          const uint2 q = *reinterpret_cast<const uint2*>(src);
-          w[0] = q.x, w[1] = q.y;
-        } else {
-          w[0] = *reinterpret_cast<const uint32_t*>(src);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kOf; j++) {
-        float f;
-        if constexpr (sizeof(T) == 4) {
-          f = __uint_as_float(w[j & 3]);
-        } else {
-          float lo, hi;
-          unpack2(w[(j / 2) & 3], lo, hi, T());
-          f = j & 1 ? hi : lo;
-        }
-        v[i + j] = first + i < width ? f : -INFINITY;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; j++) v[j] = first + j < width ? to_f32<T>(row[first + j]) : -INFINITY;
-  }
 }
 
 // An expert's choice: its logit, or its sigmoid plus its bias; minus infinity if it is closed.

@@ -772,6 +772,8 @@ cudaError_t prepare_ring(RingPrep& rp, const void* fn, int threads, int smem_byt
   return cudaSuccess;
 }
 
+uint64_t norm_max_walkers(uint32_t hidden) { return norm_max_units(hidden); }
+
 uint64_t norm_workspace_bytes(uint64_t tokens, uint32_t hidden) {
   // two sums a CTA, and one a range or a value a token for the gate
   const uint64_t units = tokens < norm_max_units(hidden) ? tokens : norm_max_units(hidden);

@@ -1,5 +1,5 @@
-// zc_torch.cpp -- Python entry points of the operators around an expert-parallel exchange (moe.py,
-// norm.py): torch tensors in, checked, outputs allocated by torch, and one call of the C ABI
+// zc_torch.cpp -- Python entry points of the operators around an expert-parallel exchange and of the
+// training step around it (moe.py, norm.py, dropout.py, embedding.py): torch tensors in, checked, outputs allocated by torch, and one call of the C ABI
 // (include/zc.h) on the current torch stream or the one given.  Argument marshalling only, as zc.py
 // does with ctypes; native because these operators run for a few microseconds in a decoding step,
 // where five allocations, a dozen attributes and a ctypes call in Python cost more than the kernels
@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -494,6 +495,284 @@ PyObject* norm_backward(Args a) {
   return pack({dy, dx, grads[0], grads[1], grads[2]});
 }
 
+// A mask of one byte a token, or NULL.
+const uint8_t* mask_of(PyObject* o, int64_t tokens) {
+  if (o == Py_None) return nullptr;
+  const Tensor& t = tensor(o, "mask");
+  if ((t.scalar_type() != at::kBool && t.scalar_type() != at::kByte) || t.dim() != 1 || t.size(0) != tokens)
+    refuse("mask must be bool or uint8 [tokens], not " + shape_of(t));
+  if (!t.is_contiguous()) refuse("libzc takes contiguous tensors");
+  return static_cast<const uint8_t*>(t.const_data_ptr());
+}
+
+// (logits, experts, ws, score, sequences, mask, stream) -> (loss, counts, slope)
+PyObject* moe_balance(Args a) {
+  const Matrix l = matrix(a[0], "logits");
+  const Tensor& experts = tensor(a[1], "experts");
+  const int64_t tokens = l.t.size(0), width = l.t.size(1);
+  if (experts.dim() != 2) refuse("experts must be [tokens, k]");
+  const int64_t k = experts.size(1);
+  table(a[1], {tokens, k}, at::kInt, "experts");
+  const Tensor& ws = tensor(a[2], "ws");
+  if (!ws.is_contiguous()) refuse("libzc takes contiguous tensors");
+  const int dtype = dtype_of(l.t), score = score_of(a[3]);
+  const int64_t sequences = integer(a[4]);
+  if (sequences < 1 || tokens % sequences) refuse("sequences must be a divisor of the tokens");
+  const uint8_t* mask = mask_of(a[5], tokens);
+  const uint32_t n = narrow(l.width, "zc_moe_balance"), slots = narrow(static_cast<uint64_t>(k), "zc_moe_balance");
+  if (n > ZC_MOE_MAX_EXPERTS || sequences > 0x7FFFFFFF) check(ZC_ERR_TOO_LARGE, "zc_moe_balance");
+  const Launch on(a[6], l.t);
+  Tensor loss = on.fresh({}, at::kFloat), counts = on.fresh({sequences, width}, at::kInt);
+  Tensor slope = on.fresh({sequences, width}, at::kFloat);
+  check(without_gil([&] {
+          return zc_moe_balance(l.p(), dtype, l.stride, l.rows, n, slots,
+                                static_cast<const int32_t*>(experts.const_data_ptr()), score,
+                                static_cast<uint64_t>(sequences), mask, static_cast<float*>(loss.mutable_data_ptr()),
+                                static_cast<int32_t*>(counts.mutable_data_ptr()),
+                                static_cast<float*>(slope.mutable_data_ptr()), ws.mutable_data_ptr(),
+                                static_cast<uint64_t>(ws.nbytes()), on.stream());
+        }),
+        "zc_moe_balance");
+  return pack({loss, counts, slope});
+}
+
+// (dloss, logits, slope, score, mask, dlogits, stream) -> (dlogits,)
+PyObject* moe_balance_backward(Args a) {
+  const Matrix l = matrix(a[1], "logits");
+  const Tensor& dloss = tensor(a[0], "dloss");
+  if (dloss.numel() != 1 || dloss.scalar_type() != at::kFloat) refuse("dloss must be one float32 value");
+  const int64_t tokens = l.t.size(0);
+  const Tensor& slope = tensor(a[2], "slope");
+  if (slope.dim() != 2 || slope.size(0) < 1 || tokens % slope.size(0))
+    refuse("slope must be [sequences, experts] with sequences a divisor of the tokens");
+  table(a[2], {slope.size(0), l.t.size(1)}, at::kFloat, "slope");
+  const int dtype = dtype_of(l.t), score = score_of(a[3]);
+  const uint8_t* mask = mask_of(a[4], tokens);
+  const uint32_t n = narrow(l.width, "zc_moe_balance_backward");
+  const Launch on(a[6], l.t);
+  Tensor dlogits = on.output(a[5], l.t.sizes(), l.t.scalar_type(), "dlogits");
+  check(without_gil([&] {
+          return zc_moe_balance_backward(static_cast<const float*>(dloss.const_data_ptr()), l.p(), dtype, l.stride,
+                                         l.rows, n, score, static_cast<uint64_t>(slope.size(0)), mask,
+                                         static_cast<const float*>(slope.const_data_ptr()), dlogits.mutable_data_ptr(),
+                                         on.stream());
+        }),
+        "zc_moe_balance_backward");
+  return pack({dlogits});
+}
+
+// What a dropout draws from.
+struct Draw {
+  double p;
+  const int64_t* rng = nullptr;
+  uint32_t call;
+  Draw(PyObject* p_, PyObject* rng_, PyObject* call_) : p(PyFloat_AsDouble(p_)) {
+    if (p == -1.0 && PyErr_Occurred()) throw Raised();
+    if (!(p >= 0.0 && p <= 1.0)) refuse("p must be a probability");
+    const long c = integer(call_);
+    if (c < 0 || c > 0xFFFFFFFFl) refuse("call must be a number of 32 bits");
+    call = static_cast<uint32_t>(c);
+    if (rng_ != Py_None) rng = static_cast<const int64_t*>(table(rng_, {2}, at::kLong, "rng").const_data_ptr());
+  }
+};
+
+// (x, p, rng, call, residual, residual_scale, out, stream) -> (out,)
+PyObject* dropout(Args a) {
+  const Matrix x = matrix(a[0], "x");
+  const int dtype = dtype_of(x.t);
+  const Draw draw(a[1], a[2], a[3]);
+  if (!draw.rng) refuse("dropout takes a generator's state");
+  const void* residual = nullptr;
+  uint64_t residual_stride = 0;
+  if (a[4] != Py_None) {
+    const Matrix r = same_as(a[4], x.t, "residual");
+    residual = r.p();
+    residual_stride = r.stride;
+  }
+  const float scale = real(a[5]);
+  const uint32_t width = narrow(x.width, "zc_dropout");
+  const Launch on(a[7], x.t);
+  Tensor out = on.output(a[6], x.t.sizes(), x.t.scalar_type(), "out");
+  check(without_gil([&] {
+          return zc_dropout(x.p(), dtype, x.stride, residual, residual_stride, scale, x.rows, width, draw.p, draw.rng,
+                            draw.call, out.mutable_data_ptr(), on.stream());
+        }),
+        "zc_dropout");
+  return pack({out});
+}
+
+// A weight or bias of a layer norm, of the activations' type or float32; NULL for None.
+const void* norm_vector(PyObject* o, const Tensor& x, at::ScalarType kind, const char* what) {
+  if (o == Py_None) return nullptr;
+  const Tensor& t = tensor(o, what);
+  if (t.scalar_type() != kind || (kind != x.scalar_type() && kind != at::kFloat))
+    refuse("weight and bias must both have the activations' type, or both be float32");
+  if (t.dim() != 1 || t.size(0) != x.size(1))
+    refuse(std::string(what) + " must have the activations' width, not " + shape_of(t));
+  if (!t.is_contiguous()) refuse("libzc takes contiguous tensors");
+  return t.const_data_ptr();
+}
+
+// (y or None, x, weight, bias or None, p, rng, call, residual_scale, eps, x_new, h, save, stream) ->
+// (x_new or None, h, stats or None)
+PyObject* layer_norm(Args a) {
+  zc_layer_norm_args n = {};
+  const bool branch = a[0] != Py_None;
+  const Matrix x = matrix(a[1], "x");
+  if (branch) {
+    const Matrix y = same_as(a[0], x.t, "y");
+    n.y = y.p();
+    n.y_stride = y.stride;
+  }
+  const Draw draw(a[4], a[5], a[6]);
+  if (draw.p > 0 && !draw.rng) refuse("dropout takes a generator's state");
+  if (draw.p > 0) n.rng = draw.rng, n.p = draw.p, n.call = draw.call;
+  n.x = x.p();
+  n.x_stride = x.stride;
+  n.tokens = x.rows;
+  n.hidden = narrow(x.width, "zc_layer_norm");
+  n.dtype = dtype_of(x.t);
+  const at::ScalarType kind = tensor(a[2], "weight").scalar_type();
+  n.weight = norm_vector(a[2], x.t, kind, "weight");
+  n.bias = norm_vector(a[3], x.t, kind, "bias");
+  n.params_f32 = kind == at::kFloat && x.t.scalar_type() != at::kFloat;
+  n.residual_scale = real(a[7]);
+  n.eps = real(a[8]);
+  const int save = PyObject_IsTrue(a[11]);
+  const Launch on(a[12], x.t);
+  Tensor x_new, stats;
+  if (branch) x_new = on.output(a[9], x.t.sizes(), x.t.scalar_type(), "x_new");
+  Tensor h = on.output(a[10], x.t.sizes(), x.t.scalar_type(), branch ? "h" : "out");
+  if (save) stats = on.fresh({x.t.size(0), 2}, at::kFloat);
+  if (branch) n.x_new = x_new.mutable_data_ptr();
+  n.h = h.mutable_data_ptr();
+  if (save) n.stats = static_cast<float*>(stats.mutable_data_ptr());
+  check(without_gil([&] { return zc_layer_norm(&n, on.stream()); }), "zc_layer_norm");
+  return pack({x_new, h, stats});
+}
+
+// (dx_new or None, dh, x_new, stats, weight, bias wanted, p, rng, call, residual_scale, branch, ws,
+// stream) -> (dy or None, dx, dweight, dbias or None); dy is dx where they are the same
+PyObject* layer_norm_backward(Args a) {
+  zc_layer_norm_backward_args n = {};
+  const Matrix x = matrix(a[2], "x_new"), dh = same_as(a[1], x.t, "dh");
+  n.dh = dh.p();
+  n.dh_stride = dh.stride;
+  n.x_new = x.p();
+  n.x_new_stride = x.stride;
+  if (a[0] != Py_None) {
+    const Matrix m = same_as(a[0], x.t, "dx_new");
+    n.dx_new = m.p();
+    n.dx_new_stride = m.stride;
+  }
+  n.stats = static_cast<const float*>(table(a[3], {x.t.size(0), 2}, at::kFloat, "stats").const_data_ptr());
+  const Draw draw(a[6], a[7], a[8]);
+  if (draw.p > 0 && !draw.rng) refuse("dropout takes a generator's state");
+  if (draw.p > 0) n.rng = draw.rng, n.p = draw.p, n.call = draw.call;
+  n.tokens = x.rows;
+  n.hidden = narrow(x.width, "zc_layer_norm_backward");
+  n.dtype = dtype_of(x.t);
+  const at::ScalarType kind = tensor(a[4], "weight").scalar_type();
+  n.weight = norm_vector(a[4], x.t, kind, "weight");
+  if (!n.weight && x.t.size(1)) refuse("the norm takes a weight");
+  n.params_f32 = kind == at::kFloat && x.t.scalar_type() != at::kFloat;
+  n.residual_scale = real(a[9]);
+  const bool branch = PyObject_IsTrue(a[10]) == 1;
+  if (!branch) n.residual_scale = 1.f;
+  const Tensor& ws = tensor(a[11], "ws");
+  if (!ws.is_contiguous()) refuse("libzc takes contiguous tensors");
+  const Launch on(a[12], x.t);
+  Tensor dx = on.fresh(x.t.sizes(), x.t.scalar_type()), dy, dbias;
+  if (branch) dy = n.rng || n.residual_scale != 1.f ? on.fresh(x.t.sizes(), x.t.scalar_type()) : dx;
+  Tensor dweight = on.fresh({x.t.size(1)}, kind);
+  if (PyObject_IsTrue(a[5]) == 1) dbias = on.fresh({x.t.size(1)}, kind);
+  n.dx = dx.mutable_data_ptr();
+  if (branch && !dy.is_same(dx)) n.dy = dy.mutable_data_ptr();
+  n.dweight = dweight.mutable_data_ptr();
+  if (dbias.defined()) n.dbias = dbias.mutable_data_ptr();
+  n.ws = ws.mutable_data_ptr();
+  n.ws_bytes = static_cast<uint64_t>(ws.nbytes());
+  check(without_gil([&] { return zc_layer_norm_backward(&n, on.stream()); }), "zc_layer_norm_backward");
+  return pack({dy, dx, dweight, dbias});
+}
+
+// Token ids, int32 or int64.
+const Tensor& ids_of(PyObject* o) {
+  const Tensor& t = tensor(o, "ids");
+  if (t.dim() != 1 || (t.scalar_type() != at::kInt && t.scalar_type() != at::kLong))
+    refuse("ids must be int32 or int64 [tokens]");
+  if (!t.is_contiguous()) refuse("libzc takes contiguous tensors");
+  return t;
+}
+
+// A torch.dtype, or `otherwise` for None; of two types that go together, the activations' `type` and
+// the table's: the same, or float32 for the table.
+at::ScalarType kind_of(PyObject* o, at::ScalarType otherwise) {
+  if (o == Py_None) return otherwise;
+  if (!THPDtype_Check(o)) refuse("dtype must be a torch.dtype");
+  return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+int check_kinds(at::ScalarType rows, at::ScalarType table) {
+  if (rows != table && table != at::kFloat) refuse("the table must have the rows' type, or be float32");
+  switch (rows) {
+    case at::kBFloat16: return ZC_BF16;
+    case at::kHalf: return ZC_F16;
+    case at::kFloat: return ZC_F32;
+    default: refuse("rows are bfloat16, float16 or float32");
+  }
+}
+
+// (ids, table, status, scale, dtype, out, stream) -> (out,)
+PyObject* embedding(Args a) {
+  const Tensor& ids = ids_of(a[0]);
+  const Matrix t = matrix(a[1], "table");
+  const Tensor& status = table(a[2], {1}, at::kInt, "status");
+  const float scale = real(a[3]);
+  const at::ScalarType kind = kind_of(a[4], t.t.scalar_type());
+  const int dtype = check_kinds(kind, t.t.scalar_type());
+  const uint32_t hidden = narrow(t.width, "zc_embedding");
+  const Launch on(a[6], t.t);
+  Tensor out = on.output(a[5], {ids.size(0), t.t.size(1)}, kind, "out");
+  check(without_gil([&] {
+          return zc_embedding(ids.const_data_ptr(), ids.scalar_type() == at::kLong,
+                              static_cast<uint64_t>(ids.size(0)), t.p(), dtype, t.t.scalar_type() == at::kFloat,
+                              t.stride, t.rows, hidden, scale, out.mutable_data_ptr(),
+                              static_cast<int32_t*>(status.mutable_data_ptr()), on.stream());
+        }),
+        "zc_embedding");
+  return pack({out});
+}
+
+// (dout, ids, vocab, ws, status, scale, dtype, dtable or None, accumulate, stream) -> (dtable,)
+PyObject* embedding_backward(Args a) {
+  const Matrix g = matrix(a[0], "dout");
+  const Tensor& ids = ids_of(a[1]);
+  if (ids.size(0) != g.t.size(0)) refuse("dout must be [tokens, hidden]");
+  const int64_t vocab = integer(a[2]);
+  if (vocab < 0) refuse("vocab must not be negative");
+  const Tensor& ws = tensor(a[3], "ws");
+  if (!ws.is_contiguous()) refuse("libzc takes contiguous tensors");
+  const Tensor& status = table(a[4], {1}, at::kInt, "status");
+  const float scale = real(a[5]);
+  const bool given = a[7] != Py_None, accumulate = PyObject_IsTrue(a[8]) == 1;
+  if (accumulate && !given) refuse("accumulate adds to a given dtable");
+  at::ScalarType kind = kind_of(a[6], given ? tensor(a[7], "dtable").scalar_type() : g.t.scalar_type());
+  const int dtype = check_kinds(g.t.scalar_type(), kind);
+  const uint32_t hidden = narrow(g.width, "zc_embedding_backward");
+  if (vocab > 0x7FFFFFFF) check(ZC_ERR_TOO_LARGE, "zc_embedding_backward");
+  const Launch on(a[9], g.t);
+  Tensor dtable = on.output(a[7], {vocab, g.t.size(1)}, kind, "dtable");
+  check(without_gil([&] {
+          return zc_embedding_backward(g.p(), dtype, g.stride, ids.const_data_ptr(), ids.scalar_type() == at::kLong,
+                                       g.rows, static_cast<uint64_t>(vocab), hidden, scale, kind == at::kFloat,
+                                       accumulate, dtable.mutable_data_ptr(), ws.mutable_data_ptr(),
+                                       static_cast<uint64_t>(ws.nbytes()),
+                                       static_cast<int32_t*>(status.mutable_data_ptr()), on.stream());
+        }),
+        "zc_embedding_backward");
+  return pack({dtable});
+}
+
 template <PyObject* (*F)(Args), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -532,6 +811,13 @@ PyMethodDef g_methods[] = {
     method<moe_combine_backward, 8>("moe_combine_backward"),
     method<norm_forward, 10>("norm_forward"),
     method<norm_backward, 11>("norm_backward"),
+    method<moe_balance, 7>("moe_balance"),
+    method<moe_balance_backward, 7>("moe_balance_backward"),
+    method<dropout, 8>("dropout"),
+    method<layer_norm, 13>("layer_norm"),
+    method<layer_norm_backward, 13>("layer_norm_backward"),
+    method<embedding, 7>("embedding"),
+    method<embedding_backward, 10>("embedding_backward"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -5,7 +5,9 @@
     ... exchange.zipped_all_to_all, the experts, and back ...
     out = moe.combine(rows_back, weights, plan.positions, status)
 
-and the gradients of all three (``torch.ops.zc.moe_*`` has them with autograd).  Every step runs in libzc's kernels
+    b = moe.balance_loss(logits, experts, bws)                   # a loss that keeps the experts' load even, and their counts
+
+and the gradients of all of them (``torch.ops.zc.moe_*`` has them with autograd).  Every step runs in libzc's kernels
 (zc_moe_* in include/zc.h, where the operators are defined); arguments are checked, and outputs that are not given
 allocated, in the native extension (csrc/zc_torch.cpp).  Activations are bfloat16, float16 or float32 matrices whose rows
 may be strided; weights are float32, expert ids int32 (or int64, in dispatch).
@@ -96,3 +98,43 @@ def dispatch_backward(drows: torch.Tensor, positions: torch.Tensor, status: torc
                       dx: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of dispatch's x: every token gets the sum of its rows' gradients, added in the order of its slots."""
     return zc.native().moe_combine(drows, None, positions, status, dx, stream)[0]
+
+
+class BalanceLoss(NamedTuple):
+    """What balance_loss gives."""
+
+    loss: torch.Tensor    # float32, one value
+    counts: torch.Tensor  # int32 [sequences, experts]: slots of every expert, of the tokens that count
+    slope: torch.Tensor   # float32 [sequences, experts]: the loss's derivative by the sums of p; the gradient needs it
+
+
+@functools.lru_cache(maxsize=4096)
+def balance_workspace_size(tokens: int, num_experts: int, sequences: int = 1) -> int:
+    out = ctypes.c_uint64()
+    zc._check(zc.load().zc_moe_balance_workspace_size(int(tokens), int(num_experts), int(sequences), ctypes.byref(out)),
+              "zc_moe_balance_workspace_size")
+    return out.value
+
+
+def balance_workspace(tokens: int, num_experts: int, sequences: int = 1, device="cuda") -> torch.Tensor:
+    """A workspace for the balance loss of so many tokens; calls that share it must be ordered on one stream."""
+    return torch.empty(balance_workspace_size(tokens, num_experts, sequences), dtype=torch.uint8, device=device)
+
+
+def balance_loss(logits: torch.Tensor, experts: torch.Tensor, ws: torch.Tensor, *, score: str = "softmax",
+                 sequences: int = 1, mask: torch.Tensor | None = None, stream=None) -> BalanceLoss:
+    """The loss that keeps the experts' load even: the mean over the sequences (equal runs of the tokens) of num_experts *
+    sum over the experts of (fraction of the slots) * (mean probability), which is 1 for an even load.
+
+    logits: [tokens, experts]; experts: int32 [tokens, k], as route returned them (-1: none).  p is the softmax of the
+    logits, or with score "sigmoid" the sigmoids over their sum.  mask: bool or uint8 [tokens], the tokens that count
+    (None: all); a token whose logits are all -inf does not.  The counts of the experts (their sums move route's bias)
+    have no gradient."""
+    return BalanceLoss(*zc.native().moe_balance(logits, experts, ws, score, sequences, mask, stream))
+
+
+def balance_loss_backward(dloss: torch.Tensor, logits: torch.Tensor, slope: torch.Tensor, *, score: str = "softmax",
+                          mask: torch.Tensor | None = None, dlogits: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """Gradient of the logits, in their type, from that of the loss (float32, one value on the device)."""
+    return zc.native().moe_balance_backward(dloss, logits, slope, score, mask, dlogits, stream)[0]

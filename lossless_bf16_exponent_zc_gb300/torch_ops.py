@@ -33,12 +33,19 @@ mutate its inputs:
   zc::pre_norm(x, weight, eps) -> h
   zc::post_norm(y, x, weight, gate, residual_scale, eps) -> x_new
   zc::post_pre_norm(y, x, weight, gate, next_weight, residual_scale, eps) -> (x_new, h)
+and those of the training step around it (moe.py, norm.py, dropout.py, embedding.py), likewise; a dropout's generator
+state must not change between a call and its gradient (autograd notices):
+  zc::moe_balance_loss(logits, experts, mask, score, sequences) -> (loss, counts, slope)
+  zc::dropout(x, rng, residual, p, call, residual_scale) -> out
+  zc::layer_norm(x, weight, bias, eps) -> (h, stats)
+  zc::add_layer_norm(y, x, weight, bias, rng, p, call, residual_scale, eps) -> (x_new, h, stats)
+  zc::embedding(ids, table, scale, dtype) -> (rows, status)
 """
 from __future__ import annotations
 
 import torch
 
-from . import moe, norm, zc
+from . import dropout, embedding, moe, norm, zc
 
 
 @torch.library.custom_op("zc::compress", mutates_args=("ws", "status"))
@@ -336,3 +343,198 @@ def _post_pre_backward(ctx, dx_new, dh):
 
 
 post_pre_norm.register_autograd(_post_pre_backward, setup_context=_post_pre_context)
+
+
+# ------------------------------------------------------------------ balance loss
+@torch.library.custom_op("zc::moe_balance_loss", mutates_args=())
+def moe_balance_loss(logits: torch.Tensor, experts: torch.Tensor, mask: torch.Tensor | None, score: str,
+                     sequences: int) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    ws = moe.balance_workspace(*logits.shape, sequences, device=logits.device)
+    return tuple(moe.balance_loss(logits, experts, ws, score=score, sequences=sequences, mask=mask))
+
+
+@moe_balance_loss.register_fake
+def _(logits, experts, mask, score, sequences):
+    shape = (sequences, logits.shape[1])
+    f32 = dict(dtype=torch.float32)
+    return logits.new_empty((), **f32), logits.new_empty(shape, dtype=torch.int32), logits.new_empty(shape, **f32)
+
+
+@torch.library.custom_op("zc::moe_balance_loss_backward", mutates_args=())
+def moe_balance_loss_backward(dloss: torch.Tensor, logits: torch.Tensor, slope: torch.Tensor,
+                              mask: torch.Tensor | None, score: str) -> torch.Tensor:
+    return moe.balance_loss_backward(dloss, logits, slope, score=score, mask=mask)
+
+
+@moe_balance_loss_backward.register_fake
+def _(dloss, logits, slope, mask, score):
+    return logits.new_empty(logits.shape)
+
+
+def _balance_context(ctx, inputs, output):
+    logits, _, mask, ctx.score, _ = inputs
+    ctx.save_for_backward(logits, output[2], mask)
+    ctx.mark_non_differentiable(*output[1:])
+
+
+def _balance_backward(ctx, dloss, *_):
+    return moe_balance_loss_backward(dloss, *ctx.saved_tensors, ctx.score), None, None, None, None
+
+
+moe_balance_loss.register_autograd(_balance_backward, setup_context=_balance_context)
+
+
+# ------------------------------------------------------------------ dropout
+@torch.library.custom_op("zc::dropout", mutates_args=())
+def dropout_op(x: torch.Tensor, rng: torch.Tensor, residual: torch.Tensor | None, p: float, call: int,
+               residual_scale: float) -> torch.Tensor:
+    return dropout.dropout(x, p, rng, call, residual=residual, residual_scale=residual_scale)
+
+
+@dropout_op.register_fake
+def _(x, rng, residual, p, call, residual_scale):
+    return x.new_empty(x.shape)
+
+
+def _dropout_context(ctx, inputs, output):
+    _, rng, residual, ctx.p, ctx.call, ctx.residual_scale = inputs
+    ctx.residual = residual is not None
+    ctx.save_for_backward(rng)  # a state that moved on before the gradient is an error
+
+
+def _dropout_backward(ctx, dout):
+    rng, = ctx.saved_tensors
+    dresidual = None
+    if ctx.residual:
+        dresidual = dout if ctx.residual_scale == 1.0 else dout * ctx.residual_scale
+    return dropout_op(_dense(dout), rng, None, ctx.p, ctx.call, 1.0), None, dresidual, None, None, None
+
+
+dropout_op.register_autograd(_dropout_backward, setup_context=_dropout_context)
+
+
+# ------------------------------------------------------------------ layer norms
+@torch.library.custom_op("zc::layer_norm", mutates_args=())
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None,
+               eps: float) -> tuple[torch.Tensor, torch.Tensor]:
+    return norm.layer_norm(x, weight, bias, eps=eps, save=True)
+
+
+@layer_norm.register_fake
+def _(x, weight, bias, eps):
+    return x.new_empty(x.shape), x.new_empty((x.shape[0], 2), dtype=torch.float32)
+
+
+@torch.library.custom_op("zc::add_layer_norm", mutates_args=())
+def add_layer_norm(y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None,
+                   rng: torch.Tensor | None, p: float, call: int, residual_scale: float,
+                   eps: float) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    return norm.add_layer_norm(y, x, weight, bias, p=p, rng=rng, call=call, residual_scale=residual_scale, eps=eps,
+                               save=True)
+
+
+@add_layer_norm.register_fake
+def _(y, x, weight, bias, rng, p, call, residual_scale, eps):
+    return x.new_empty(x.shape), x.new_empty(x.shape), x.new_empty((x.shape[0], 2), dtype=torch.float32)
+
+
+@torch.library.custom_op("zc::layer_norm_backward", mutates_args=())
+def layer_norm_backward(dx_new: torch.Tensor | None, dh: torch.Tensor, x_new: torch.Tensor, stats: torch.Tensor,
+                        weight: torch.Tensor, bias: bool, rng: torch.Tensor | None, p: float, call: int,
+                        residual_scale: float) -> list[torch.Tensor]:
+    """[dx, dweight], then dy where it is not dx, and dbias where there is one."""
+    ws = norm.workspace(*x_new.shape, device=x_new.device)
+    g = norm.add_layer_norm_backward(dx_new, dh, x_new, stats, weight, ws, bias=bias, p=p, rng=rng, call=call,
+                                     residual_scale=residual_scale)
+    return [t for t in (g.dx, g.dweight, g.dy if g.dy is not g.dx else None, g.dbias) if t is not None]
+
+
+def _own_dy(p, residual_scale):
+    return p > 0 or residual_scale != 1.0
+
+
+@layer_norm_backward.register_fake
+def _(dx_new, dh, x_new, stats, weight, bias, rng, p, call, residual_scale):
+    like = [x_new, weight] + [x_new] * _own_dy(p, residual_scale) + [weight] * bias
+    return [t.new_empty(t.shape) for t in like]
+
+
+def _layer_context(ctx, inputs, output):
+    x, weight, bias, _ = inputs
+    ctx.bias = bias is not None
+    ctx.save_for_backward(x, output[1], weight)
+    ctx.mark_non_differentiable(output[1])
+
+
+def _layer_backward(ctx, dh, _):
+    x, stats, weight = ctx.saved_tensors
+    dx, dw, *db = layer_norm_backward(None, _dense(dh), x, stats, weight, ctx.bias, None, 0.0, 0, 1.0)
+    return dx, dw, db[0] if db else None, None
+
+
+layer_norm.register_autograd(_layer_backward, setup_context=_layer_context)
+
+
+def _add_layer_context(ctx, inputs, output):
+    _, _, weight, bias, rng, ctx.p, ctx.call, ctx.residual_scale, _ = inputs
+    ctx.bias = bias is not None
+    ctx.save_for_backward(output[0], output[2], weight, rng)
+    ctx.mark_non_differentiable(output[2])
+    ctx.set_materialize_grads(False)
+
+
+def _add_layer_backward(ctx, dx_new, dh, _):
+    x_new, stats, weight, rng = ctx.saved_tensors
+    if dx_new is None and dh is None:
+        return (None,) * 9
+    if dh is None:  # nothing came through the norm
+        g = _dense(dx_new)
+        dy = dropout_op(g, rng, None, ctx.p, ctx.call, 1.0) if ctx.p > 0 else g
+        return dy, g if ctx.residual_scale == 1.0 else g * ctx.residual_scale, *(None,) * 7
+    dx, dw, *rest = layer_norm_backward(_dense(dx_new), _dense(dh), x_new, stats, weight, ctx.bias, rng, ctx.p, ctx.call,
+                                        ctx.residual_scale)
+    dy = rest[0] if _own_dy(ctx.p, ctx.residual_scale) else dx
+    return dy, dx, dw, rest[-1] if ctx.bias else None, *(None,) * 5
+
+
+add_layer_norm.register_autograd(_add_layer_backward, setup_context=_add_layer_context)
+
+
+# ------------------------------------------------------------------ embedding
+@torch.library.custom_op("zc::embedding", mutates_args=())
+def embedding_op(ids: torch.Tensor, table: torch.Tensor, scale: float,
+                 dtype: torch.dtype | None) -> tuple[torch.Tensor, torch.Tensor]:
+    status = zc.new_status(table.device)
+    return embedding.lookup(ids, table, status, scale=scale, dtype=dtype), status
+
+
+@embedding_op.register_fake
+def _(ids, table, scale, dtype):
+    return (table.new_empty((ids.shape[0], table.shape[1]), dtype=dtype or table.dtype),
+            table.new_empty(1, dtype=torch.int32))
+
+
+@torch.library.custom_op("zc::embedding_backward", mutates_args=())
+def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float,
+                       dtype: torch.dtype) -> torch.Tensor:
+    ws = embedding.workspace(ids.shape[0], vocab, dout.shape[1], device=dout.device)
+    return embedding.lookup_backward(dout, ids, vocab, ws, zc.new_status(dout.device), scale=scale, dtype=dtype)
+
+
+@embedding_backward.register_fake
+def _(dout, ids, vocab, scale, dtype):
+    return dout.new_empty((vocab, dout.shape[1]), dtype=dtype)
+
+
+def _embedding_context(ctx, inputs, output):
+    ids, table, ctx.scale, _ = inputs
+    ctx.vocab, ctx.dtype = table.shape[0], table.dtype
+    ctx.save_for_backward(ids)
+    ctx.mark_non_differentiable(output[1])
+
+
+def _embedding_backward(ctx, dout, _):
+    return None, embedding_backward(_dense(dout), *ctx.saved_tensors, ctx.vocab, ctx.scale, ctx.dtype), None, None
+
+
+embedding_op.register_autograd(_embedding_backward, setup_context=_embedding_context)

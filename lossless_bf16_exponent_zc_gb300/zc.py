@@ -122,6 +122,8 @@ def load() -> ctypes.CDLL:
     u32 = ctypes.c_uint32
     lib.zc_moe_workspace_size.argtypes = [u64, u32, u32, u64p]
     lib.zc_norm_workspace_size.argtypes = [u64, u32, u64p]
+    lib.zc_moe_balance_workspace_size.argtypes = [u64, u32, u64, u64p]
+    lib.zc_embedding_workspace_size.argtypes = [u64, u64, u32, u64p]
     for name in ("zc_codebook_from_sigma", "zc_compressed_size", "zc_workspace_size", "zc_histogram_topk",
                  "zc_compress", "zc_compress_adaptive", "zc_raw_spill", "zc_decompress", "zc_decompress_reduce",
                  "zc_compress_batched", "zc_compress_batched_adaptive", "zc_decompress_batched",
@@ -138,7 +140,8 @@ _native = None
 
 
 def native():
-    """The extension with the entry points of moe.py and norm.py (csrc/zc_torch.cpp), built first if missing or stale."""
+    """The extension with the entry points of moe.py, norm.py, dropout.py and embedding.py (csrc/zc_torch.cpp), built first
+    if missing or stale."""
     global _native
     if _native is None:
         loader = importlib.machinery.ExtensionFileLoader("_zc_torch", _build.build_extension())
