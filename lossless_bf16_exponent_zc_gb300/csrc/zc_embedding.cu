@@ -62,17 +62,17 @@ struct AnyValues {
 // A thread takes UNITS 16-byte pieces of the output, kEmbedThreads apart, all loads before the first
 // store.
 template <typename T, typename TT, int UNITS>
-__global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedParams p) {
+__global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedParams p, Divisor pieces) {
   constexpr int V = kPieceOf<T>;
   pdl_begin();
-  const uint32_t pieces = p.hidden / V;
-  const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads * UNITS), t0 = i0 / pieces;
-  const uint32_t c0 = static_cast<uint32_t>(i0 - t0 * pieces) + threadIdx.x;
+  const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads * UNITS);
+  const uint64_t t0 = i0 >> 31 ? i0 / pieces.d : pieces(static_cast<uint32_t>(i0));
+  const uint32_t c0 = static_cast<uint32_t>(i0 - t0 * pieces.d) + threadIdx.x;
   AnyValues<TT, V, true> v[UNITS];
   T* to[UNITS];
 #pragma unroll
   for (int q = 0; q < UNITS; q++) {
-    const uint32_t i = c0 + q * kEmbedThreads, dt = i / pieces, first = (i - dt * pieces) * V;
+    const uint32_t i = c0 + q * kEmbedThreads, dt = pieces(i), first = (i - dt * pieces.d) * V;
     const uint64_t t = t0 + dt;
     to[q] = t < p.tokens ? static_cast<T*>(p.out) + t * p.hidden + first : nullptr;
     v[q].clear();
@@ -261,13 +261,166 @@ __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(EmbedBwdParam
   }
 }
 
+// Up to kEmbedClusterTokens tokens are sorted in the shared memory of one cluster, and the other
+// clusters of the same launch zero the table's rows that no token asks for meanwhile: each looks
+// through all ids for those of its own rows, which takes less time than the sort.  A warp of the
+// sort holds 32 `items` keys in order; a pass counts its digits warp by warp, the CTAs tell one
+// another their counts, and every key goes to its place in the shared memory of the CTA that it
+// falls to, in the last pass to the workspace.
+constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
+constexpr uint32_t kMostItems = kEmbedClusterTokens / (kEmbedClusterCtas * kClusterThreads);
+constexpr uint32_t kClusterBins = 512;
+constexpr uint32_t kFillRows = 32768;  // rows whose presence a CTA keeps at once
+
+struct ClusterSort {
+  uint32_t items, ctas, bits, passes, size, fill;  // fill: CTAs that zero rows
+  uint64_t fill_rows;                                // rows of each of them
+};
+
+__device__ __forceinline__ void zero_row(uint8_t* row, uint64_t bytes) {
+  const uint32_t lane = lane_id();
+  const uint64_t head = min(bytes, static_cast<uint64_t>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15));
+  const uint64_t body = (bytes - head) / 16, rest = bytes - body * 16;  // rest: bytes outside the pieces
+  uint4* pieces = reinterpret_cast<uint4*>(row + head);
+  for (uint64_t i = lane; i < body; i += 32) pieces[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (lane * 2 < rest) {
+    const uint64_t at = lane * 2 < head ? lane * 2 : body * 16 + lane * 2;
+    *reinterpret_cast<uint16_t*>(row + at) = 0;
+  }
+}
+
+// Zeroes the rows of `first` .. `last` that no token asks for; `present` holds a bit for kFillRows.
+__device__ __forceinline__ void fill_rows(const EmbedBwdParams& p, uint64_t first, uint64_t last, uint32_t size,
+                                          uint32_t* present) {
+  const uint64_t bytes = static_cast<uint64_t>(p.hidden) * size;
+  for (uint64_t v0 = first; v0 < last; v0 += kFillRows) {
+    const uint32_t n = static_cast<uint32_t>(min(static_cast<uint64_t>(kFillRows), last - v0));
+    for (uint32_t i = threadIdx.x; i < (n + 31) / 32; i += kClusterThreads) present[i] = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (uint64_t i = threadIdx.x; i < p.tokens; i += kClusterThreads) {
+      const int64_t at = id_at(p.ids, p.ids64, i) - static_cast<int64_t>(v0);
+      if (at >= 0 && at < n) atomicOr(&present[at >> 5], 1u << (at & 31));
+    }
+    __syncthreads();
+    for (uint32_t r = threadIdx.x >> 5; r < n; r += kClusterWarps)
+      if (!(present[r >> 5] >> (r & 31) & 1)) zero_row(static_cast<uint8_t*>(p.dtable) + (v0 + r) * bytes, bytes);
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(kClusterThreads) embed_cluster_kernel(EmbedBwdParams p, ClusterSort c, Divisor cap) {
+  extern __shared__ __align__(16) uint8_t cluster_smem[];
+  __shared__ uint32_t warp_totals[kClusterWarps];
+  pdl_begin();
+  if (blockIdx.x >= c.ctas) {
+    const uint64_t first = (blockIdx.x - c.ctas) * c.fill_rows;
+    if (blockIdx.x - c.ctas < c.fill && first < p.vocab)
+      fill_rows(p, first, min(p.vocab, first + c.fill_rows), c.size, reinterpret_cast<uint32_t*>(cluster_smem));
+    return;
+  }
+  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, rank = blockIdx.x;
+  uint16_t* hist = reinterpret_cast<uint16_t*>(cluster_smem);            // [warps][bins]
+  uint32_t* totals = reinterpret_cast<uint32_t*>(hist + kClusterWarps * kClusterBins);  // [ctas][bins]
+  uint32_t* start = totals + kEmbedClusterCtas * kClusterBins;           // [bins]
+  uint32_t* buffers = start + kClusterBins;                              // keys and tokens, once or twice
+  cluster_arrive();  // shared memory of another CTA may be written once it has started
+  cluster_wait();
+  const uint32_t base = warp * 32 * c.items + lane;
+  uint32_t key[kMostItems], token[kMostItems], place[kMostItems];
+#pragma unroll
+  for (uint32_t i = 0; i < kMostItems; i++) {
+    token[i] = rank * cap.d + base + i * 32;
+    key[i] = 0xFFFFFFFFu;
+    if (i < c.items && token[i] < p.tokens) key[i] = sort_key(p, token[i]);
+  }
+  for (uint32_t pass = 0; pass < c.passes; pass++) {
+    const uint32_t shift = c.bits * pass / c.passes, bits = c.bits * (pass + 1) / c.passes - shift, bins = 1u << bits;
+    uint16_t* own = hist + warp * bins;
+    for (uint32_t i = threadIdx.x; i < kClusterWarps * bins / 2; i += kClusterThreads)
+      reinterpret_cast<uint32_t*>(hist)[i] = 0;
+    if (pass) {
+      const uint32_t* from = buffers + ((pass + 1) & 1) * 2 * cap.d;
+#pragma unroll
+      for (uint32_t i = 0; i < kMostItems; i++) {
+        if (i >= c.items) break;
+        key[i] = from[base + i * 32];
+        token[i] = from[cap.d + base + i * 32];
+      }
+    }
+    __syncthreads();
+    // a key's place among its digit's in the warp
+#pragma unroll
+    for (uint32_t i = 0; i < kMostItems; i++) {
+      if (i >= c.items) break;
+      const bool there = rank * cap.d + base + i * 32 < p.tokens;
+      const uint32_t digit = there ? (key[i] >> shift) & (bins - 1) : bins;  // its own class beyond the end
+      const uint32_t equal = same_digit(digit, bits + 1), below = equal & lanes_below_mask();
+      const uint32_t before = there ? own[digit] : 0;
+      place[i] = before + __popc(below);
+      __syncwarp();
+      if (there && below == 0) own[digit] = static_cast<uint16_t>(before + __popc(equal));
+      __syncwarp();
+    }
+    __syncthreads();
+    // the digits' prefix over the warps; every CTA gets to know all CTAs' totals
+    for (uint32_t e = threadIdx.x; e < bins; e += kClusterThreads) {
+      uint32_t sum = 0;
+#pragma unroll 8
+      for (int w = 0; w < kClusterWarps; w++) {
+        const uint32_t n = hist[w * bins + e];
+        hist[w * bins + e] = static_cast<uint16_t>(sum);
+        sum += n;
+      }
+      for (uint32_t k = 0; k < c.ctas; k++) st_shared_of_cta(&totals[rank * kClusterBins + e], k, sum);
+    }
+    cluster_arrive();
+    cluster_wait();
+    uint32_t all = 0, before = 0;
+    if (threadIdx.x < bins) {
+      for (uint32_t k = 0; k < c.ctas; k++) {
+        const uint32_t n = totals[k * kClusterBins + threadIdx.x];
+        before += k < rank ? n : 0;
+        all += n;
+      }
+    }
+    const uint32_t upto = warp_inclusive_scan(all);
+    if (lane == 31) warp_totals[warp] = upto;
+    __syncthreads();
+    uint32_t at = upto - all + before;
+    for (uint32_t w = 0; w < warp; w++) at += warp_totals[w];
+    if (threadIdx.x < bins) start[threadIdx.x] = at;
+    __syncthreads();
+    const bool last = pass + 1 == c.passes;
+    uint32_t* to = buffers + (pass & 1) * 2 * cap.d;
+#pragma unroll
+    for (uint32_t i = 0; i < kMostItems; i++) {
+      if (i >= c.items || rank * cap.d + base + i * 32 >= p.tokens) break;
+      const uint32_t digit = (key[i] >> shift) & (bins - 1), r = start[digit] + own[digit] + place[i];
+      if (last) {
+        p.keys_out[r] = key[i];
+        p.tokens_out[r] = token[i];
+      } else {
+        const uint32_t cta = cap(r), k = r - cta * cap.d;
+        st_shared_of_cta(&to[k], cta, key[i]);
+        st_shared_of_cta(&to[cap.d + k], cta, token[i]);
+      }
+    }
+    if (!last) {
+      cluster_arrive();
+      cluster_wait();
+    }
+  }
+}
+
 // ------------------------------------------------------------------ sums
-// A warp adds up kEmbedRun tokens of the sorted order over 256 columns, a lane eight of them (8 /
-// V pieces, 32 apart).  Where a row's tokens all lie in the run, the row is written; where they
+// A warp adds up a run of up to 32 tokens of the sorted order over 256 columns, a lane eight of them
+// (8 / V pieces, 32 apart).  Where a row's tokens all lie in the run, the row is written; where they
 // go on in a neighbouring run, the sum is left in the workspace: slot 0 of the run for the tokens of
 // a row that began before it, slot 1 for one that begins in it and goes on.
 constexpr uint32_t kSlab = 256;
-constexpr int kRowLoads = 4;  // rows on their way at once
+template <bool VEC>
+constexpr int kRowLoads = VEC ? 8 : 4;  // rows on their way at once
 
 template <typename T, typename TT, bool VEC>
 struct EmbedCols {
@@ -316,13 +469,16 @@ __device__ __forceinline__ void put_row(const EmbedBwdParams& p, uint64_t row, u
 #pragma unroll
   for (int i = 0; i < 8 / V; i++) {
     const uint32_t c = EmbedCols<T, TT, VEC>::col(slab, i);
-    if (VEC && !p.accumulate) {
+    if (VEC) {
       if (c >= p.hidden) continue;
 #pragma unroll
       for (int k = 0; k < V; k += W) {
         float f[W];
 #pragma unroll
-        for (int j = 0; j < W; j++) f[j] = p.scale * acc[i * V + (k + j) % V];
+        for (int j = 0; j < W; j++) f[j] = 0.f;
+        if (p.accumulate) Piece<TT, W>::load(to + c + k).get(f);
+#pragma unroll
+        for (int j = 0; j < W; j++) f[j] = fmaf(p.scale, acc[i * V + (k + j) % V], f[j]);
         Piece<TT, W> o;
         o.set(f);
         o.store(to + c + k);
@@ -348,12 +504,13 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(EmbedBwdParams
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads / 32) + (threadIdx.x >> 5), run = i / p.slabs;
   if (run >= p.runs) return;
   const uint32_t lane = lane_id(), slab = static_cast<uint32_t>(i - run * p.slabs);
-  const uint64_t first = run * kEmbedRun;
+  const uint64_t first = run * p.run;
   const uint32_t none = static_cast<uint32_t>(p.vocab);
-  const uint32_t key = first + lane < p.tokens ? p.keys_in[first + lane] : none;
-  const uint32_t token = first + lane < p.tokens ? p.tokens_in[first + lane] : 0;
+  const bool there = lane < p.run && first + lane < p.tokens;
+  const uint32_t key = there ? p.keys_in[first + lane] : none;
+  const uint32_t token = there ? p.tokens_in[first + lane] : 0;
   const uint32_t before = first ? p.keys_in[first - 1] : none;
-  const uint32_t after = first + kEmbedRun < p.tokens ? p.keys_in[first + kEmbedRun] : none;
+  const uint32_t after = first + p.run < p.tokens ? p.keys_in[first + p.run] : none;
   const uint32_t n = __popc(__ballot_sync(kFull, key != none));  // those with a row come first
   const uint32_t next = __shfl_down_sync(kFull, key, 1);
   const uint32_t ends = __ballot_sync(kFull, lane == 31 || next != key);
@@ -361,21 +518,21 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(EmbedBwdParams
 #pragma unroll
   for (int j = 0; j < 8; j++) acc[j] = 0.f;
   bool began = __shfl_sync(kFull, key, 0) == before;  // the row at hand began before the run
-  for (uint32_t r0 = 0; r0 < n; r0 += kRowLoads) {
-    EmbedCols<T, TT, VEC> v[kRowLoads];
+  for (uint32_t r0 = 0; r0 < n; r0 += kRowLoads<VEC>) {
+    EmbedCols<T, TT, VEC> v[kRowLoads<VEC>];
 #pragma unroll
-    for (int q = 0; q < kRowLoads; q++) {
+    for (int q = 0; q < kRowLoads<VEC>; q++) {
       const uint64_t t = __shfl_sync(kFull, token, (r0 + q) & 31);
       if (r0 + q < n) v[q].load(static_cast<const T*>(p.dout) + t * p.dout_stride, slab, p.hidden);
     }
 #pragma unroll
-    for (int q = 0; q < kRowLoads; q++) {
+    for (int q = 0; q < kRowLoads<VEC>; q++) {
       const uint32_t r = r0 + q;
       if (r >= n) break;
       v[q].add(acc);
       if (!(ends >> r & 1)) continue;
       const uint32_t row = __shfl_sync(kFull, key, r);
-      const bool goes_on = r == 31 && after == row;
+      const bool goes_on = r + 1 == p.run && after == row;
       if (began || goes_on) {
         float* to = part_of(p, run, began ? 0 : 1, slab) + lane * 8;
         *reinterpret_cast<float4*>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -398,14 +555,14 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedBwdParam
   pdl_begin();
   const uint64_t run = blockIdx.x / p.slabs;
   const uint32_t slab = static_cast<uint32_t>(blockIdx.x - run * p.slabs), lane = lane_id(), warp = threadIdx.x >> 5;
-  const uint64_t first = run * kEmbedRun, next = first + kEmbedRun;
+  const uint64_t first = run * p.run, next = first + p.run;
   if (next >= p.tokens) return;
   const uint32_t row = p.keys_in[next - 1];
   if (row == p.vocab || p.keys_in[next] != row) return;               // no row goes on behind the run
   if (p.keys_in[first] == row && first && p.keys_in[first - 1] == row) return;  // it began before the run
   uint64_t last = run + 1;  // the last run with tokens of the row
   for (;; last += 32) {
-    const uint64_t at = (last + lane + 1) * kEmbedRun;
+    const uint64_t at = (last + lane + 1) * p.run;
     const uint32_t more = __ballot_sync(kFull, at < p.tokens && p.keys_in[at] == row);
     if (more != kFull) {
       last += __ffs(~more) - 1;
@@ -440,20 +597,10 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedBwdParam
 // Zeroes the rows that no token asks for, a warp a row.
 __global__ void __launch_bounds__(kEmbedThreads) embed_fill_kernel(EmbedBwdParams p, uint32_t size) {
   pdl_begin();
-  const uint32_t lane = lane_id();
   const uint64_t warps = static_cast<uint64_t>(gridDim.x) * (kEmbedThreads / 32), bytes = static_cast<uint64_t>(p.hidden) * size;
   for (uint64_t v = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads / 32) + (threadIdx.x >> 5); v < p.vocab; v += warps) {
     if (p.present[v >> 5] >> (v & 31) & 1) continue;
-    uint8_t* row = static_cast<uint8_t*>(p.dtable) + v * bytes;
-    const uint64_t head = min(bytes, static_cast<uint64_t>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15));
-    const uint64_t body = (bytes - head) / 16;
-    uint4* pieces = reinterpret_cast<uint4*>(row + head);
-    for (uint64_t i = lane; i < body; i += 32) pieces[i] = make_uint4(0u, 0u, 0u, 0u);
-    const uint64_t rest = bytes - body * 16;  // bytes outside the pieces
-    if (lane * 2 < rest) {
-      const uint64_t at = lane * 2 < head ? lane * 2 : body * 16 + lane * 2;
-      *reinterpret_cast<uint16_t*>(row + at) = 0;
-    }
+    zero_row(static_cast<uint8_t*>(p.dtable) + v * bytes, bytes);
   }
 }
 
@@ -474,8 +621,9 @@ cudaError_t lookup(EmbedParams& p, bool vec, cudaStream_t stream, const DeviceIn
     return run(reinterpret_cast<const void*>(embed_any_kernel<T, TT>), ceil_div(p.tokens * shares, kEmbedThreads / 32),
                kEmbedThreads, 0, stream, args);
   }
-  const uint64_t all = p.tokens * (p.hidden / kPieceOf<T>);
-  void* args[] = {&p};
+  Divisor pieces(p.hidden / kPieceOf<T>);
+  const uint64_t all = p.tokens * pieces.d;
+  void* args[] = {&p, &pieces};
   if (all <= 2ull * kEmbedThreads * static_cast<uint64_t>(dev.sm_count))
     return run(reinterpret_cast<const void*>(embed_kernel<T, TT, 1>), ceil_div(all, kEmbedThreads), kEmbedThreads, 0,
                stream, args);
@@ -497,11 +645,26 @@ cudaError_t sums(EmbedBwdParams& p, bool vec, cudaStream_t stream) {
   return vec ? sums<T, TT, true>(p, stream) : sums<T, TT, false>(p, stream);
 }
 
+// Tokens of a run: 32 where there are many, fewer while the warps would not fill the GPU.
+uint32_t embed_run(uint64_t tokens, uint32_t hidden) {
+  const uint64_t slabs = ceil_div(hidden, kSlab);
+  uint32_t run = 32;
+  while (run > 4 && tokens * slabs < 4096ull * run) run /= 2;
+  return run;
+}
+// At most so many runs of `tokens` tokens or fewer.
+uint64_t embed_runs(uint64_t tokens, uint32_t hidden) {
+  const uint64_t few = 8192 / ceil_div(hidden, kSlab) + 1;  // while runs are short there are no more of them
+  const uint64_t runs = ceil_div(tokens, 32);
+  const uint64_t most = runs > few ? runs : few, all = ceil_div(tokens, 4);
+  return most < all ? most : all;
+}
+
 // Where a gradient's workspace holds what.
 struct EmbedWork {
   uint64_t keys, tokens, counts, totals, present, parts, bytes;  // byte offsets; keys and tokens have two halves
   EmbedWork(uint64_t n, uint64_t vocab, uint32_t hidden) {
-    const uint64_t chunks = ceil_div(n, kEmbedSortChunk), runs = ceil_div(n, kEmbedRun);
+    const uint64_t chunks = ceil_div(n, kEmbedSortChunk), runs = embed_runs(n, hidden);
     uint64_t at = 0;
     auto take = [&](uint64_t words) {
       const uint64_t here = at;
@@ -517,6 +680,72 @@ struct EmbedWork {
     bytes = at;
   }
 };
+
+cudaError_t sort_in_cluster(EmbedBwdParams& p, uint32_t bits, uint32_t size, cudaStream_t stream,
+                            const DeviceInfo& dev) {
+  static KernelPrep prep;
+  ClusterSort c = {};
+  c.bits = bits;
+  c.passes = static_cast<uint32_t>(ceil_div(bits, 9));
+  c.size = size;
+  // one CTA holds a few tokens, and more of them a cluster, with as few a thread as that allows
+  c.ctas = p.tokens <= 2 * kClusterThreads ? 1 : kEmbedClusterCtas;
+  c.items = static_cast<uint32_t>(ceil_div(p.tokens, static_cast<uint64_t>(c.ctas) * kClusterThreads));
+  if (c.items < 1) c.items = 1;
+  Divisor cap(c.items * kClusterThreads);
+  const uint32_t buffers = c.passes > 2 ? 2 : c.passes - 1;
+  const int smem = static_cast<int>(kClusterWarps * kClusterBins * 2 + (kEmbedClusterCtas + 1) * kClusterBins * 4 +
+                                    buffers * 2 * cap.d * 4);
+  constexpr int kMostSmem = static_cast<int>(kClusterWarps * kClusterBins * 2 + (kEmbedClusterCtas + 1) * kClusterBins * 4 +
+                                             4 * kMostItems * kClusterThreads * 4);
+  int per_sm = 0;
+  const void* fn = reinterpret_cast<const void*>(embed_cluster_kernel);
+  cudaError_t e = prepare_kernel(prep, fn, kClusterThreads, kMostSmem, dev, &per_sm);
+  if (e != cudaSuccess) return e;
+  if (!p.accumulate && p.vocab) {
+    const uint64_t most = 2ull * static_cast<uint64_t>(dev.sm_count), rows = ceil_div(p.vocab, kClusterWarps);
+    c.fill = static_cast<uint32_t>(rows < most ? rows : most);
+    c.fill_rows = ceil_div(p.vocab, c.fill);
+  }
+  const uint32_t grid = c.ctas + static_cast<uint32_t>(ceil_div(c.fill, c.ctas)) * c.ctas;
+  void* args[] = {&p, &c, &cap};
+  return launch_kernel(fn, dim3(grid), dim3(kClusterThreads), smem, stream, args, false, c.ctas);
+}
+
+cudaError_t sort_in_launches(EmbedBwdParams& p, uint32_t bits, uint32_t size, uint32_t* const (&keys)[2],
+                             uint32_t* const (&tokens)[2], cudaStream_t stream, const DeviceInfo& dev) {
+  cudaError_t e = cudaSuccess;
+  if (p.present) e = cudaMemsetAsync(p.present, 0, ceil_div(p.vocab, 32) * 4, stream);
+  if (e != cudaSuccess) return e;
+  const uint32_t passes = static_cast<uint32_t>(ceil_div(bits, kEmbedDigitBits));
+  static KernelPrep prep;
+  int per_sm = 0;
+  constexpr int kMostSmem = (kSortWarps + 1) * static_cast<int>(kSortBins) * 4;
+  e = prepare_kernel(prep, reinterpret_cast<const void*>(embed_place_kernel), kSortThreads, kMostSmem, dev, &per_sm);
+  void* args[] = {&p};
+  for (uint32_t pass = 0; pass < passes && e == cudaSuccess; pass++) {
+    p.shift = bits * pass / passes;
+    p.digit_bits = bits * (pass + 1) / passes - p.shift;
+    p.keys_in = pass ? keys[(pass + 1) & 1] : nullptr;
+    p.tokens_in = pass ? tokens[(pass + 1) & 1] : nullptr;
+    p.keys_out = keys[pass & 1];
+    p.tokens_out = tokens[pass & 1];
+    e = run(reinterpret_cast<const void*>(embed_count_kernel), p.sort_chunks, kSortThreads, 0, stream, args);
+    if (e == cudaSuccess)
+      e = run(reinterpret_cast<const void*>(embed_prefix_kernel), ceil_div(1u << p.digit_bits, kSortWarps),
+              kSortThreads, 0, stream, args);
+    if (e == cudaSuccess)
+      e = run(reinterpret_cast<const void*>(embed_place_kernel), p.sort_chunks, kSortThreads,
+              (kSortWarps + 1) * (4 << p.digit_bits), stream, args);
+  }
+  if (e != cudaSuccess) return e;
+  p.keys_in = keys[(passes + 1) & 1];
+  p.tokens_in = tokens[(passes + 1) & 1];
+  if (!p.present) return e;
+  void* fill[] = {&p, &size};
+  const uint64_t most = 8ull * static_cast<uint64_t>(dev.sm_count), all = ceil_div(p.vocab, kEmbedThreads / 32);
+  return run(reinterpret_cast<const void*>(embed_fill_kernel), all < most ? all : most, kEmbedThreads, 0, stream, fill);
+}
 
 }  // namespace
 
@@ -551,44 +780,23 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams& params, int dtype, int table_
   p.present = p.accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + at.present);
   p.parts = reinterpret_cast<float*>(base + at.parts);
   p.sort_chunks = static_cast<uint32_t>(ceil_div(p.tokens, kEmbedSortChunk));
-  p.runs = ceil_div(p.tokens, kEmbedRun);
+  p.run = embed_run(p.tokens, p.hidden);
+  p.runs = ceil_div(p.tokens, p.run);
   p.slabs = static_cast<uint32_t>(ceil_div(p.hidden, kSlab));
-  cudaError_t e = cudaSuccess;
-  if (p.present) e = cudaMemsetAsync(p.present, 0, ceil_div(p.vocab, 32) * 4, stream);
-  if (e != cudaSuccess) return e;
+  const uint32_t size = dtype == ZC_F32 || table_f32 ? 4 : 2;
   uint32_t bits = 1;  // of the keys 0 .. vocab
   while (p.vocab >> bits) bits++;
-  const uint32_t passes = static_cast<uint32_t>(ceil_div(bits, kEmbedDigitBits));
-  static KernelPrep prep;
-  int per_sm = 0;
-  constexpr int kMostSmem = (kSortWarps + 1) * static_cast<int>(kSortBins) * 4;
-  e = prepare_kernel(prep, reinterpret_cast<const void*>(embed_place_kernel), kSortThreads, kMostSmem, dev, &per_sm);
-  void* args[] = {&p};
-  for (uint32_t pass = 0; pass < passes && e == cudaSuccess && p.tokens; pass++) {
-    p.shift = bits * pass / passes;
-    p.digit_bits = bits * (pass + 1) / passes - p.shift;
-    p.keys_in = pass ? keys[pass + 1 & 1] : nullptr;
-    p.tokens_in = pass ? tokens[pass + 1 & 1] : nullptr;
-    p.keys_out = keys[pass & 1];
-    p.tokens_out = tokens[pass & 1];
-    e = run(reinterpret_cast<const void*>(embed_count_kernel), p.sort_chunks, kSortThreads, 0, stream, args);
-    if (e == cudaSuccess)
-      e = run(reinterpret_cast<const void*>(embed_prefix_kernel), ceil_div(1u << p.digit_bits, kSortWarps),
-              kSortThreads, 0, stream, args);
-    if (e == cudaSuccess)
-      e = run(reinterpret_cast<const void*>(embed_place_kernel), p.sort_chunks, kSortThreads,
-              (kSortWarps + 1) * (4 << p.digit_bits), stream, args);
+  cudaError_t e;
+  if (p.tokens <= kEmbedClusterTokens) {
+    p.keys_out = keys[0];
+    p.tokens_out = tokens[0];
+    e = sort_in_cluster(p, bits, size, stream, dev);
+    p.keys_in = keys[0];
+    p.tokens_in = tokens[0];
+  } else {
+    e = sort_in_launches(p, bits, size, keys, tokens, stream, dev);
   }
   if (e != cudaSuccess) return e;
-  p.keys_in = keys[passes + 1 & 1];
-  p.tokens_in = tokens[passes + 1 & 1];
-  if (p.present) {
-    uint32_t size = dtype == ZC_F32 || table_f32 ? 4 : 2;
-    void* fill[] = {&p, &size};
-    const uint64_t most = 8ull * static_cast<uint64_t>(dev.sm_count), all = ceil_div(p.vocab, kEmbedThreads / 32);
-    e = run(reinterpret_cast<const void*>(embed_fill_kernel), all < most ? all : most, kEmbedThreads, 0, stream, fill);
-    if (e != cudaSuccess) return e;
-  }
   if (p.tokens == 0) return e;
   switch (dtype) {
     case ZC_BF16:

@@ -296,7 +296,8 @@ struct EmbedParams {
 };
 constexpr uint32_t kEmbedDigitBits = 10;    // of the gradient's radix sort, at most
 constexpr uint32_t kEmbedSortChunk = 1024;  // keys of a CTA there
-constexpr uint32_t kEmbedRun = 32;          // sorted tokens that a warp adds up
+constexpr uint32_t kEmbedClusterCtas = 8;
+constexpr uint32_t kEmbedClusterTokens = 65536;  // that one cluster sorts
 struct EmbedBwdParams {
   const void* dout;
   const void* ids;
@@ -314,7 +315,7 @@ struct EmbedBwdParams {
   uint32_t sort_chunks, shift, digit_bits;
   float* parts;
   uint64_t runs;
-  uint32_t slabs;
+  uint32_t run, slabs;  // sorted tokens that a warp adds up, and pieces of a row's columns
 };
 uint64_t embed_workspace_bytes(uint64_t tokens, uint64_t vocab, uint32_t hidden);
 cudaError_t launch_embed(const EmbedParams& p, int dtype, int table_f32, bool vec, cudaStream_t stream,

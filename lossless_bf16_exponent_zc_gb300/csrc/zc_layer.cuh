@@ -236,6 +236,19 @@ __device__ __forceinline__ void load_row(const T* row, uint32_t width, float (&v
   }
 }
 
+// Division of 32-bit numbers below 2^31 by a divisor that the host knows: the quotient is the upper
+// half of n * ceil(2^(31 + bits) / d), shifted, bits = ceil(log2 d) (Granlund and Montgomery, 1994).
+struct Divisor {
+  uint32_t d, mul, shift;
+  __host__ explicit Divisor(uint32_t divisor) : d(divisor) {
+    uint32_t bits = 0;
+    while (bits < 31 && (1u << bits) < d) bits++;
+    shift = bits ? bits - 1 : 0;
+    mul = bits ? static_cast<uint32_t>(((1ull << (31 + bits)) + d - 1) / d) : 0;
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return d == 1 ? n : __umulhi(n, mul) >> shift; }
+};
+
 // Thread-block clusters: the barrier of all threads of the cluster in its two halves (release,
 // acquire), and a store to the same variable in the shared memory of the cluster's CTA `cta`.
 __device__ __forceinline__ uint32_t cluster_rank() {
