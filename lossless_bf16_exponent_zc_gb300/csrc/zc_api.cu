@@ -953,6 +953,7 @@ zc_status zc_layer_norm(const zc_layer_norm_args* h_args, void* stream) {
   LayerNormParams p = {};
   if (a.rng) {
     if (zc_status s = check_dropout(a.p, a.rng, a.call, a.tokens, &p.drop)) return s;
+    if (p.drop.limit == 0) p.drop.rng = nullptr;  // keeps everything
   } else if (a.p != 0.0) {
     return ZC_ERR_INVALID_ARG;
   }
@@ -996,6 +997,7 @@ zc_status zc_layer_norm_backward(const zc_layer_norm_backward_args* h_args, void
   LayerNormBwdParams p = {};
   if (a.rng) {
     if (zc_status s = check_dropout(a.p, a.rng, a.call, a.tokens, &p.drop)) return s;
+    if (p.drop.limit == 0) p.drop.rng = nullptr;  // keeps everything
   } else if (a.p != 0.0) {
     return ZC_ERR_INVALID_ARG;
   }

@@ -15,20 +15,21 @@ constexpr int kDropThreads = 256;
 // Rows whose addresses, strides and widths are multiples of 16 bytes: a thread takes UNITS groups of
 // eight columns, kDropThreads apart, all loads before the first use.
 template <typename T, int UNITS, bool RESIDUAL>
-__global__ void __launch_bounds__(kDropThreads) dropout_kernel(DropoutParams p) {
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(DropoutParams p, Divisor groups) {
   constexpr int V = kPieceOf<T>, NP = 8 / V;
   pdl_begin();
   const KeepRng rng(p.drop);
-  const uint32_t groups = (p.width + 7) / 8;
-  const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kDropThreads * UNITS), t0 = i0 / groups;
-  const uint32_t c0 = static_cast<uint32_t>(i0 - t0 * groups) + threadIdx.x;
+  const bool drops = p.drop.limit != 0;
+  const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kDropThreads * UNITS);
+  const uint64_t t0 = i0 >> 31 ? i0 / groups.d : groups(static_cast<uint32_t>(i0));
+  const uint32_t c0 = static_cast<uint32_t>(i0 - t0 * groups.d) + threadIdx.x;
   Piece<T, V> x[UNITS][NP], r[UNITS][NP];
   uint64_t row[UNITS];
   uint32_t group[UNITS];
 #pragma unroll
   for (int q = 0; q < UNITS; q++) {
-    const uint32_t i = c0 + q * kDropThreads, dt = i / groups;
-    group[q] = i - dt * groups;
+    const uint32_t i = c0 + q * kDropThreads, dt = groups(i);
+    group[q] = i - dt * groups.d;
     row[q] = t0 + dt;
 #pragma unroll
     for (int k = 0; k < NP; k++) {
@@ -43,7 +44,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(DropoutParams p) 
 #pragma unroll
   for (int q = 0; q < UNITS; q++) {
     if (row[q] >= p.tokens) continue;
-    const uint4 g = rng.group(static_cast<uint32_t>(row[q]), group[q]);
+    uint4 g = make_uint4(0u, 0u, 0u, 0u);
+    if (drops) g = rng.group(static_cast<uint32_t>(row[q]), group[q]);
     const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
     for (int k = 0; k < NP; k++) {
@@ -54,7 +56,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(DropoutParams p) 
 #pragma unroll
       for (int j = 0; j < V / 2; j++) bits[j] = w[k * V / 2 + j];
       x[q][k].get(f);
-      rng.template apply<V>(f, bits);
+      if (drops) rng.template apply<V>(f, bits);
       if (RESIDUAL) {
         r[q][k].get(o);
 #pragma unroll
@@ -102,6 +104,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(DropoutParams
   constexpr int V = kPieceOf<T>, NP = 8 / V;
   pdl_begin();
   const KeepRng rng(p.drop);
+  const bool drops = p.drop.limit != 0;
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kDropThreads / 32) + (threadIdx.x >> 5), t = i / shares;
   if (t >= p.tokens) return;
   const uint32_t u = static_cast<uint32_t>(i - t * shares) * kDropAnyUnits + lane_id();
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(DropoutParams
     const uint32_t bits[4] = {g.x, g.y, g.z, g.w};
     float f[8], o[8];
     xs.get(f);
-    rng.template apply<8>(f, bits);
+    if (drops) rng.template apply<8>(f, bits);
     if (RESIDUAL) {
       rs.get(o);
 #pragma unroll
@@ -149,31 +152,31 @@ __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(DropoutParams
       piece.store(out + col + k * V);
     }
   } else if (single) {
-    float f = rng.keeps(own, col & 7) ? to_f32<T>(x[col]) * rng.factor : 0.f;
+    float f = !drops ? to_f32<T>(x[col]) : rng.keeps(own, col & 7) ? to_f32<T>(x[col]) * rng.factor : 0.f;
     if (RESIDUAL) f = fmaf(p.residual_scale, to_f32<T>(r[col]), f);
     out[col] = from_f32<T>(f);
   }
 }
 
+cudaError_t launch(const void* fn, uint64_t grid, cudaStream_t stream, void** args) {
+  if (grid > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+  return launch_kernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kDropThreads), 0, stream, args, false);
+}
+
 template <typename T, bool RESIDUAL>
 cudaError_t run(DropoutParams& p, bool vec, cudaStream_t stream) {
   constexpr int kUnits = sizeof(T) == 2 ? 4 : 2;
-  uint64_t grid;
-  uint32_t shares = 0;
-  const void* fn;
   if (vec) {
-    grid = (p.tokens * ((p.width + 7) / 8) + kDropThreads * kUnits - 1) / (kDropThreads * kUnits);
-    fn = reinterpret_cast<const void*>(dropout_kernel<T, kUnits, RESIDUAL>);
-  } else {
-    // at most 7 columns on either side of the pieces
-    const uint32_t units = p.width / 8 + 14;
-    shares = (units + kDropAnyUnits - 1) / kDropAnyUnits;
-    grid = (p.tokens * shares + kDropThreads / 32 - 1) / (kDropThreads / 32);
-    fn = reinterpret_cast<const void*>(dropout_any_kernel<T, RESIDUAL>);
+    Divisor groups((p.width + 7) / 8);
+    void* args[] = {&p, &groups};
+    return launch(reinterpret_cast<const void*>(dropout_kernel<T, kUnits, RESIDUAL>),
+                  (p.tokens * groups.d + kDropThreads * kUnits - 1) / (kDropThreads * kUnits), stream, args);
   }
-  if (grid > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
-  void* args[] = {&p, &shares};  // dropout_kernel takes the first alone
-  return launch_kernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kDropThreads), 0, stream, args, false);
+  // at most 7 columns on either side of the pieces
+  uint32_t shares = (p.width / 8 + 14 + kDropAnyUnits - 1) / kDropAnyUnits;
+  void* args[] = {&p, &shares};
+  return launch(reinterpret_cast<const void*>(dropout_any_kernel<T, RESIDUAL>),
+                (p.tokens * shares + kDropThreads / 32 - 1) / (kDropThreads / 32), stream, args);
 }
 
 template <typename T>

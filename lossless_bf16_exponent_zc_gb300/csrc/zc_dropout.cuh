@@ -26,11 +26,14 @@ __device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
   return c;
 }
 
-// The generator of a call, its seed and offset read.
+// The generator of a call, its seed and offset read.  A value's bits, at the top of a word with
+// anything behind them, are at least the limit if the word is above `below` (a limit of zero drops
+// nothing and needs no generator; one of 2^16 keeps nothing, nothing being above 2^32 - 1).
 struct KeepRng {
-  uint32_t k0, k1, call, offset, limit;
+  uint32_t k0, k1, call, offset, below;
   float factor;
-  __device__ __forceinline__ explicit KeepRng(const Dropout& d) : call(d.call), limit(d.limit), factor(d.factor) {
+  __device__ __forceinline__ explicit KeepRng(const Dropout& d)
+      : call(d.call), below((d.limit << 16) - 1u), factor(d.factor) {
     const uint64_t seed = static_cast<uint64_t>(d.rng[0]);
     k0 = static_cast<uint32_t>(seed);
     k1 = static_cast<uint32_t>(seed >> 32);
@@ -40,19 +43,22 @@ struct KeepRng {
   __device__ __forceinline__ uint4 group(uint32_t row, uint32_t group) const {
     return philox(make_uint4(group, row, call, offset), k0, k1);
   }
-  __device__ __forceinline__ bool keeps(uint32_t bits) const { return bits >= limit; }
+  // The first and the second of the two values that share a word.
+  __device__ __forceinline__ bool keeps_low(uint32_t w) const { return w << 16 > below; }
+  __device__ __forceinline__ bool keeps_high(uint32_t w) const { return w > below; }
   // Column j (0 .. 7) of a group.
   __device__ __forceinline__ bool keeps(uint4 g, uint32_t j) const {
     const uint32_t w = j & 4 ? (j & 2 ? g.w : g.z) : (j & 2 ? g.y : g.x);
-    return keeps(j & 1 ? w >> 16 : w & 0xFFFFu);
+    return j & 1 ? keeps_high(w) : keeps_low(w);
   }
   // Drops out N values, N even, by their 16 bits each.
   template <int N>
   __device__ __forceinline__ void apply(float (&v)[N], const uint32_t (&bits)[N / 2]) const {
 #pragma unroll
-    for (int j = 0; j < N; j++) {
-      const uint32_t b = j & 1 ? bits[j / 2] >> 16 : bits[j / 2] & 0xFFFFu;
-      v[j] = keeps(b) ? v[j] * factor : 0.f;
+    for (int j = 0; j < N; j += 2) {
+      const float2 f = __fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(factor, factor));
+      v[j] = keeps_low(bits[j / 2]) ? f.x : 0.f;
+      v[j + 1] = keeps_high(bits[j / 2]) ? f.y : 0.f;
     }
   }
   // Drops out the V values of a row from column `col` on, a multiple of V.
@@ -69,6 +75,95 @@ struct KeepRng {
     } else {
       v[0] = keeps(g, col & 7) ? v[0] * factor : 0.f;
     }
+  }
+};
+
+// The same for a thread's columns of a ring of rows (RowRing, zc_norm.cuh): NV pieces of V, piece me +
+// i threads, each starting `lead` columns early, V / 2 words of bits a piece; `threads` is a multiple
+// of 32.  No group is drawn twice where that can be helped: a piece of four columns is half a group,
+// so of two neighbouring lanes each draws for one of two pieces and they trade halves; and a piece
+// that starts early takes the bits of the piece before it from the lane below.  What lane 0 needs
+// from the warp below it draws itself, the 32 lanes for the next 32 rows at once.
+template <int V, int NV, bool SHIFT>
+struct KeepColumns {
+  static constexpr int W = V / 2;
+  KeepRng rng;
+  uint32_t me, threads, first_group, lead;
+  uint32_t edge[SHIFT ? NV : 1][W];  // of the piece before lane 0's, of the lane's row of 32
+  uint32_t turn = 0;
+  __device__ __forceinline__ KeepColumns(const Dropout& d, uint32_t me_, uint32_t threads_, uint32_t first,
+                                         uint32_t lead_)
+      : rng(d), me(me_), threads(threads_), first_group(first / 8), lead(lead_) {}
+
+  // Draws the bits of row `row`, to be followed by row + step.
+  __device__ __forceinline__ void draw(uint32_t row, uint32_t step, uint32_t (&bits)[NV][W]) {
+    const uint32_t lane = lane_id();
+    uint32_t own[NV][W];
+    if constexpr (V == 8) {
+#pragma unroll
+      for (int i = 0; i < NV; i++) {
+        const uint4 g = rng.group(row, first_group + me + i * threads);
+        own[i][0] = g.x, own[i][1] = g.y, own[i][2] = g.z, own[i][3] = g.w;
+      }
+    } else {
+      static_assert(V == 4 && NV % 2 == 0, "pairs of pieces");
+      const bool odd = lane & 1;
+#pragma unroll
+      for (int i = 0; i < NV; i += 2) {
+        const uint4 g = rng.group(row, first_group + (me + (odd ? i + 1 : i) * threads) / 2);
+        const uint32_t a = __shfl_xor_sync(kFull, odd ? g.x : g.z, 1), b = __shfl_xor_sync(kFull, odd ? g.y : g.w, 1);
+        own[i][0] = odd ? a : g.x, own[i][1] = odd ? b : g.y;
+        own[i + 1][0] = odd ? g.z : a, own[i + 1][1] = odd ? g.w : b;
+      }
+    }
+    if constexpr (!SHIFT) {
+#pragma unroll
+      for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int j = 0; j < W; j++) bits[i][j] = own[i][j];
+    } else {
+      if (turn == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+          const uint32_t piece = me - lane + i * threads - 1;  // of 8 or 4 columns; it may lie before the row
+          const uint4 g = rng.group(row + lane * step, V == 8 ? piece : piece / 2);
+          edge[i][0] = V == 8 ? g.x : g.z;  // a half before an even piece is a second one
+          edge[i][1] = V == 8 ? g.y : g.w;
+          if constexpr (V == 8) edge[i][2] = g.z, edge[i][3] = g.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NV; i++) {
+        uint32_t before[W];
+#pragma unroll
+        for (int j = 0; j < W; j++) {
+          before[j] = __shfl_up_sync(kFull, own[i][j], 1);
+          const uint32_t e = __shfl_sync(kFull, edge[i][j], turn);
+          before[j] = lane ? before[j] : e;
+        }
+        uint4 w;
+        if constexpr (V == 8)  // 0 .. 7 columns early
+          w = lead ? shift_pieces<__half>(make_uint4(before[0], before[1], before[2], before[3]),
+                                          make_uint4(own[i][0], own[i][1], own[i][2], own[i][3]), 16 - 2 * lead)
+                   : make_uint4(own[i][0], own[i][1], own[i][2], own[i][3]);
+        else
+          w = shift_pieces<__half>(make_uint4(before[0], before[1], own[i][0], own[i][1]), make_uint4(0u, 0u, 0u, 0u),
+                                   8 - 2 * lead);
+        bits[i][0] = w.x, bits[i][1] = w.y;
+        if constexpr (V == 8) bits[i][2] = w.z, bits[i][3] = w.w;
+      }
+      turn = (turn + 1) & 31;
+    }
+  }
+  // Drops out the thread's columns of a row.
+  __device__ __forceinline__ void apply(float2 (&v)[NV * V / 2], const uint32_t (&bits)[NV][W]) const {
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+      for (int j = 0; j < W; j++) {
+        const float2 f = __fmul2_rn(v[i * W + j], make_float2(rng.factor, rng.factor));
+        v[i * W + j] = make_float2(rng.keeps_low(bits[i][j]) ? f.x : 0.f, rng.keeps_high(bits[i][j]) ? f.y : 0.f);
+      }
   }
 };
 
