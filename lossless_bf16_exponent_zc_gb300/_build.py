@@ -23,7 +23,8 @@ SAN_BUILD = os.path.join(BUILD, "san")
 SAN_LIB = os.path.join(LIBDIR, "libzc_san.so")
 SAN_FLAGS = ["-fsanitize=address", "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer", "-g"]
 SOURCES = ["zc_api.cu", "zc_encode.cu", "zc_decode.cu", "zc_reduce.cu", "zc_hist.cu", "zc_noalloc.cu", "zc_pipeline.cu", "zq.cu",
-           "zc_moe.cu", "zc_norm.cu", "zc_norm_bwd.cu", "zc_balance.cu", "zc_layer_norm.cu", "zc_dropout.cu", "zc_embedding.cu"]
+           "zc_moe.cu", "zc_norm.cu", "zc_norm_bwd.cu", "zc_balance.cu", "zc_layer_norm.cu", "zc_layer_norm_bwd.cu", "zc_dropout.cu",
+           "zc_embedding.cu"]
 TORCH_SOURCE = "zc_torch.cpp"  # the extension, built against the torch at hand
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -13,8 +13,9 @@ namespace {
 constexpr int kDropThreads = 256;
 
 // Rows whose addresses, strides and widths are multiples of 16 bytes: a thread takes UNITS groups of
-// eight columns, kDropThreads apart, all loads before the first use.
-template <typename T, int UNITS, bool RESIDUAL>
+// eight columns, kDropThreads apart, all loads before the first use, and draws for all of them
+// together.  FLAT: all matrices are contiguous, and their rows whole groups.
+template <typename T, int UNITS, bool RESIDUAL, bool FLAT>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(DropoutParams p, Divisor groups) {
   constexpr int V = kPieceOf<T>, NP = 8 / V;
   pdl_begin();
@@ -24,33 +25,38 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(DropoutParams p, 
   const uint64_t t0 = i0 >> 31 ? i0 / groups.d : groups(static_cast<uint32_t>(i0));
   const uint32_t c0 = static_cast<uint32_t>(i0 - t0 * groups.d) + threadIdx.x;
   Piece<T, V> x[UNITS][NP], r[UNITS][NP];
-  uint64_t row[UNITS];
-  uint32_t group[UNITS];
+  uint32_t row[UNITS], group[UNITS];
+  bool there[UNITS];
+  // where the values of unit q, a row's group, lie in a matrix
+  auto at = [&](int q, int k, uint32_t of_row, uint32_t of_group, uint64_t stride) {
+    if (FLAT) return (i0 + threadIdx.x + q * kDropThreads) * 8 + k * V;
+    return of_row * stride + of_group * 8 + k * V;
+  };
 #pragma unroll
   for (int q = 0; q < UNITS; q++) {
     const uint32_t i = c0 + q * kDropThreads, dt = groups(i);
     group[q] = i - dt * groups.d;
-    row[q] = t0 + dt;
+    there[q] = t0 + dt < p.tokens;
+    row[q] = static_cast<uint32_t>(t0 + dt);
 #pragma unroll
     for (int k = 0; k < NP; k++) {
-      const uint32_t col = group[q] * 8 + k * V;
-      const bool there = row[q] < p.tokens && col < p.width;
+      const bool here = there[q] && (FLAT || group[q] * 8 + k * V < p.width);
       x[q][k] = r[q][k] = Piece<T, V>::zero();
-      if (there) x[q][k] = Piece<T, V>::load(static_cast<const T*>(p.x) + row[q] * p.x_stride + col);
-      if (there && RESIDUAL)
-        r[q][k] = Piece<T, V>::load(static_cast<const T*>(p.residual) + row[q] * p.residual_stride + col);
+      if (here) x[q][k] = Piece<T, V>::load(static_cast<const T*>(p.x) + at(q, k, row[q], group[q], p.x_stride));
+      if (here && RESIDUAL)
+        r[q][k] =
+            Piece<T, V>::load(static_cast<const T*>(p.residual) + at(q, k, row[q], group[q], p.residual_stride));
     }
   }
+  uint4 g[UNITS];
+#pragma unroll
+  for (int q = 0; q < UNITS; q++) g[q] = make_uint4(0u, 0u, 0u, 0u);
+  if (drops) rng.template groups<UNITS>(row, group, g);
 #pragma unroll
   for (int q = 0; q < UNITS; q++) {
-    if (row[q] >= p.tokens) continue;
-    uint4 g = make_uint4(0u, 0u, 0u, 0u);
-    if (drops) g = rng.group(static_cast<uint32_t>(row[q]), group[q]);
-    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+    const uint32_t w[4] = {g[q].x, g[q].y, g[q].z, g[q].w};
 #pragma unroll
     for (int k = 0; k < NP; k++) {
-      const uint32_t col = group[q] * 8 + k * V;
-      if (col >= p.width) continue;
       float f[V], o[V];
       uint32_t bits[V / 2];
 #pragma unroll
@@ -64,7 +70,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(DropoutParams p, 
       }
       Piece<T, V> out;
       out.set(f);
-      out.store(static_cast<T*>(p.out) + row[q] * p.width + col);
+      if (there[q] && (FLAT || group[q] * 8 + k * V < p.width))
+        out.store(static_cast<T*>(p.out) + at(q, k, row[q], group[q], p.width));
     }
   }
 }
@@ -165,11 +172,13 @@ cudaError_t launch(const void* fn, uint64_t grid, cudaStream_t stream, void** ar
 
 template <typename T, bool RESIDUAL>
 cudaError_t run(DropoutParams& p, bool vec, cudaStream_t stream) {
-  constexpr int kUnits = sizeof(T) == 2 ? 4 : 2;
   if (vec) {
     Divisor groups((p.width + 7) / 8);
     void* args[] = {&p, &groups};
-    return launch(reinterpret_cast<const void*>(dropout_kernel<T, kUnits, RESIDUAL>),
+    constexpr int kUnits = sizeof(T) == 2 ? 4 : 2;
+    const bool flat = p.width % 8 == 0 && p.x_stride == p.width && (!RESIDUAL || p.residual_stride == p.width);
+    return launch(flat ? reinterpret_cast<const void*>(dropout_kernel<T, kUnits, RESIDUAL, true>)
+                       : reinterpret_cast<const void*>(dropout_kernel<T, kUnits, RESIDUAL, false>),
                   (p.tokens * groups.d + kDropThreads * kUnits - 1) / (kDropThreads * kUnits), stream, args);
   }
   // at most 7 columns on either side of the pieces

@@ -14,16 +14,20 @@
 
 namespace zc {
 
-__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
+// N counters at once: they share the rounds' keys.
+template <int N>
+__device__ __forceinline__ void philox(uint4 (&c)[N], uint32_t k0, uint32_t k1) {
 #pragma unroll
   for (int i = 0; i < 10; i++) {
-    const uint64_t a = static_cast<uint64_t>(c.x) * 0xD2511F53u, b = static_cast<uint64_t>(c.z) * 0xCD9E8D57u;
-    c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ k0, static_cast<uint32_t>(b),
-                   static_cast<uint32_t>(a >> 32) ^ c.w ^ k1, static_cast<uint32_t>(a));
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+      const uint64_t a = static_cast<uint64_t>(c[n].x) * 0xD2511F53u, b = static_cast<uint64_t>(c[n].z) * 0xCD9E8D57u;
+      c[n] = make_uint4(static_cast<uint32_t>(b >> 32) ^ c[n].y ^ k0, static_cast<uint32_t>(b),
+                        static_cast<uint32_t>(a >> 32) ^ c[n].w ^ k1, static_cast<uint32_t>(a));
+    }
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
-  return c;
 }
 
 // The generator of a call, its seed and offset read.  A value's bits, at the top of a word with
@@ -41,7 +45,16 @@ struct KeepRng {
   }
   // 16 bits for each of the columns 8 group .. 8 group + 7 of a row.
   __device__ __forceinline__ uint4 group(uint32_t row, uint32_t group) const {
-    return philox(make_uint4(group, row, call, offset), k0, k1);
+    uint4 c[1] = {make_uint4(group, row, call, offset)};
+    philox<1>(c, k0, k1);
+    return c[0];
+  }
+  // The same for N groups.
+  template <int N>
+  __device__ __forceinline__ void groups(const uint32_t (&row)[N], const uint32_t (&group)[N], uint4 (&g)[N]) const {
+#pragma unroll
+    for (int n = 0; n < N; n++) g[n] = make_uint4(group[n], row[n], call, offset);
+    philox<N>(g, k0, k1);
   }
   // The first and the second of the two values that share a word.
   __device__ __forceinline__ bool keeps_low(uint32_t w) const { return w << 16 > below; }
@@ -100,11 +113,13 @@ struct KeepColumns {
     const uint32_t lane = lane_id();
     uint32_t own[NV][W];
     if constexpr (V == 8) {
+      uint4 g[NV];
+      uint32_t rows[NV], at[NV];
 #pragma unroll
-      for (int i = 0; i < NV; i++) {
-        const uint4 g = rng.group(row, first_group + me + i * threads);
-        own[i][0] = g.x, own[i][1] = g.y, own[i][2] = g.z, own[i][3] = g.w;
-      }
+      for (int i = 0; i < NV; i++) rows[i] = row, at[i] = first_group + me + i * threads;
+      rng.template groups<NV>(rows, at, g);
+#pragma unroll
+      for (int i = 0; i < NV; i++) own[i][0] = g[i].x, own[i][1] = g[i].y, own[i][2] = g[i].z, own[i][3] = g[i].w;
     } else {
       static_assert(V == 4 && NV % 2 == 0, "pairs of pieces");
       const bool odd = lane & 1;

@@ -1,17 +1,12 @@
 // zc_layer_norm.cu -- layer norm, by itself and behind a block whose output is dropped out and added
-// to the residual stream in the same pass, and its gradient.
+// to the residual stream in the same pass (the gradient is in zc_layer_norm_bwd.cu).
 //
 //   x' = a x + D(y),   m = mean(x'),  r = 1 / sqrt(mean((x' - m)^2) + eps),   h = (x' - m) r w + b
 //
-// With n = (x' - m) r and u = dh w the gradient is, per row,
-//   G  = dx' + r (u - mean(u) - n mean(u n)),   dx = a G,   dy = D(G)
-// and over the rows  dw = sum dh n,  db = sum dh.  D keeps the same values both times, drawn again
-// from the counters (zc_dropout.cuh).  The mean is taken before the squares of what differs from
-// it, so that a large mean costs no bits; the backward pass gets both from the forward one.
-#include <type_traits>
-
-#include "zc_dropout.cuh"
-#include "zc_norm.cuh"
+// One pass: a row is read once and everything else happens on chip.  h is taken from x' before its
+// rounding to the stored type, so each output is rounded once.  The mean is taken before the squares
+// of what differs from it, so that a large mean costs no bits.
+#include "zc_layer_norm.cuh"
 
 namespace zc {
 
@@ -87,51 +82,13 @@ __global__ void __launch_bounds__(THREADS) layer_norm_kernel(LayerNormParams p) 
   }
 }
 
-// Columns of a thread and stages of the ring, forward: 8 columns, and 16 for rows that 8 of each of
-// 512 threads do not hold.
-constexpr int kLayerCols = 8, kLayerWideCols = 16;
-template <int C>
-constexpr int kLayerStages = C == kLayerCols ? 4 : 3;
-
-// Which of a thread's columns lie in the row; a warp whose columns all do skips the test.
-template <int V, int C, bool SHIFT, typename Ring>
-struct InRow {
-  uint32_t bits = 0;
-  __device__ __forceinline__ explicit InRow(const Ring& r) {
-#pragma unroll
-    for (int i = 0; i < C / V; i++)
-#pragma unroll
-      for (int j = 0; j < V; j++) {
-        const uint32_t c = r.me + i * r.threads;
-        if (SHIFT ? c * V + j - r.lead < r.width : c < r.pieces) bits |= 1u << (i * V + j);
-      }
-  }
-  __device__ __forceinline__ void keep(float2 (&v)[C / 2]) const {
-    if (bits == (C == 32 ? kFull : (1u << (C & 31)) - 1u)) return;
-#pragma unroll
-    for (int i = 0; i < C / 2; i++) {
-      if (!(bits >> (2 * i) & 1)) v[i].x = 0.f;
-      if (!(bits >> (2 * i + 1) & 1)) v[i].y = 0.f;
-    }
-  }
-};
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
-
-// The sum over 16 lanes, the same 16 values lying in both halves of the warp.
-__device__ __forceinline__ float half_warp_sum_f32(float v) {
-#pragma unroll
-  for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
-  return v;
-}
-
 // The ring shape: rows walker, walker + walkers, ... stream through the shared memory of a CTA.  A
 // warp takes its columns' sum and their squares about their own mean; between warps, squares about
 // the row's mean are those plus (columns) (the warp's mean - the row's)^2.  So no squares of a mean
 // are ever subtracted, and a row costs one barrier.
 template <typename T, int V, int C, bool SHIFT, bool BRANCH, bool DROP>
-__global__ void __launch_bounds__(kNormRingThreads, C == kLayerCols ? 2 : 1) layer_norm_ring_kernel(LayerNormParams p) {
-  constexpr int P = C / 2, kStages = kLayerStages<C>;
+__global__ void __launch_bounds__(kNormRingThreads, C == 8 ? 2 : 1) layer_norm_ring_kernel(LayerNormParams p) {
+  constexpr int P = C / 2, kStages = kLayerStages<C, BRANCH>;
   using Ring = RowRing<T, V, C, BRANCH ? 2 : 1, kStages, SHIFT>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ float2 red[2][16];
@@ -174,10 +131,7 @@ __global__ void __launch_bounds__(kNormRingThreads, C == kLayerCols ? 2 : 1) lay
   __syncthreads();
   if (threadIdx.x < 16) red[0][threadIdx.x] = make_float2(0.f, 0.f);
   __syncthreads();
-  struct None {
-    __device__ None(const Dropout&, uint32_t, uint32_t, uint32_t, uint32_t) {}
-  };
-  typename std::conditional<DROP, KeepColumns<V, C / V, SHIFT>, None>::type keep(p.drop, threadIdx.x, blockDim.x, 0, lead);
+  ColumnsOf<V, C / V, SHIFT, DROP> keep(p.drop, threadIdx.x, blockDim.x, 0, lead);
   int stage = 0, turn = 0;
   for (uint64_t t = walker; t < p.tokens; t += walkers) {
     float2 x[P];
@@ -226,315 +180,6 @@ __global__ void __launch_bounds__(kNormRingThreads, C == kLayerCols ? 2 : 1) lay
   cp_async_wait<0>();
 }
 
-// Columns of a thread in NV pieces, over all rows of its CTA; the sums of its columns stay in
-// registers until the end.
-template <typename T, int V, int NV, bool DROP, int THREADS>
-__global__ void __launch_bounds__(THREADS) layer_norm_bwd_kernel(LayerNormBwdParams p) {
-  __shared__ float red[2][2 * 32];
-  pdl_begin();
-  const uint32_t me = threadIdx.x, step = blockDim.x, pieces = p.hidden / V;
-  const float inv_d = 1.f / static_cast<float>(p.hidden);
-  float dw[NV][V], db[NV][V];
-#pragma unroll
-  for (int i = 0; i < NV; i++)
-#pragma unroll
-    for (int j = 0; j < V; j++) dw[i][j] = db[i][j] = 0.f;
-  int turn = 0;
-  for (uint64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    const float2 stats = *reinterpret_cast<const float2*>(p.stats + 2 * t);
-    float u[NV][V], n[NV][V], sums[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-      const uint32_t c = me + i * step;
-      const uint64_t at = static_cast<uint64_t>(c) * V;
-      if (c >= pieces) continue;
-      float w[V];
-      Piece<T, V>::load(static_cast<const T*>(p.dh) + t * p.dh_stride + at).get(u[i]);
-      Piece<T, V>::load(static_cast<const T*>(p.x_new) + t * p.x_new_stride + at).get(n[i]);
-      load_params<T, V>(p.weight, p.params_f32, at, w);
-#pragma unroll
-      for (int j = 0; j < V; j++) {
-        n[i][j] = (n[i][j] - stats.x) * stats.y;
-        dw[i][j] = fmaf(u[i][j], n[i][j], dw[i][j]);
-        db[i][j] += u[i][j];
-        u[i][j] *= w[j];
-        sums[0] += u[i][j];
-        sums[1] = fmaf(u[i][j], n[i][j], sums[1]);
-      }
-    }
-    block_sum_f32<2>(sums, red[turn]);
-    turn ^= 1;
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-      const uint32_t c = me + i * step;
-      const uint64_t at = static_cast<uint64_t>(c) * V;
-      if (c >= pieces) continue;
-      float g[V], o[V];
-#pragma unroll
-      for (int j = 0; j < V; j++) g[j] = 0.f;
-      if (p.dx_new) Piece<T, V>::load(static_cast<const T*>(p.dx_new) + t * p.dx_new_stride + at).get(g);
-#pragma unroll
-      for (int j = 0; j < V; j++) {
-        g[j] = fmaf(stats.y, u[i][j] - sums[0] * inv_d - n[i][j] * (sums[1] * inv_d), g[j]);
-        o[j] = p.residual_scale * g[j];
-      }
-      Piece<T, V> out;
-      out.set(o);
-      out.store(static_cast<T*>(p.dx) + t * p.hidden + at);
-      if (p.dy) {
-        if (DROP) KeepRng(p.drop).template apply<V>(g, static_cast<uint32_t>(t), c * V);
-        out.set(g);
-        out.store(static_cast<T*>(p.dy) + t * p.hidden + at);
-      }
-    }
-  }
-  float* mine = p.parts + static_cast<uint64_t>(blockIdx.x) * 2 * p.hidden;
-#pragma unroll
-  for (int i = 0; i < NV; i++)
-#pragma unroll
-    for (int j = 0; j < V; j++) {
-      const uint32_t c = (me + i * step) * V + j;
-      if (c >= pieces * V) continue;
-      mine[c] = dw[i][j];
-      mine[p.hidden + c] = db[i][j];
-    }
-}
-
-// The gradient's ring: three matrices, or two where nothing reaches x' but through h.
-constexpr int kLayerBwdStages = 4;
-
-template <typename T, int V, int C, bool SHIFT, bool DROP>
-__global__ void __launch_bounds__(kNormRingThreads, 1) layer_norm_bwd_ring_kernel(LayerNormBwdParams p) {
-  constexpr int P = C / 2, kStages = kLayerBwdStages;
-  constexpr int kH = 0, kX = 1, kPast = 2;
-  using Ring = RowRing<T, V, C, 3, kStages, SHIFT>;
-  extern __shared__ __align__(16) uint8_t ring_smem[];
-  __shared__ float red[2][2 * 32];
-  pdl_begin();
-  const uint64_t walker = blockIdx.x, walkers = gridDim.x;
-  const T *h_at = static_cast<const T*>(p.dh), *x_at = static_cast<const T*>(p.x_new),
-          *past_at = static_cast<const T*>(p.dx_new);
-  const uint32_t lead =
-      SHIFT ? (reinterpret_cast<uintptr_t>(x_at + walker * p.x_new_stride) & 15) / static_cast<uint32_t>(sizeof(T)) : 0;
-  const Ring ring{ring_smem, threadIdx.x, blockDim.x, SHIFT ? (lead + p.hidden + V - 1) / V : p.hidden / V, 0, lead,
-                  p.hidden};
-#pragma unroll
-  for (int i = 0; i < 3; i++) ring.clear(i, i == kPast && !p.dx_new);
-  const float inv_d = 1.f / static_cast<float>(p.hidden);
-  uint64_t ahead = walker;
-  auto issue = [&](int stage) {
-    if (ahead < p.tokens) {
-      ring.copy(stage, kH, ring.start(h_at, ahead, p.dh_stride));
-      ring.copy(stage, kX, ring.start(x_at, ahead, p.x_new_stride));
-      if (p.dx_new) ring.copy(stage, kPast, ring.start(past_at, ahead, p.dx_new_stride));
-      ahead += walkers;
-    }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < kStages; s++) issue(s);
-  float2 w[P], dw[P], db[P];
-  ring.params(p.weight, p.params_f32, 0, w);
-#pragma unroll
-  for (int i = 0; i < P; i++) dw[i] = db[i] = splat(0.f);
-  const InRow<V, C, SHIFT, Ring> in_row(ring);
-  struct None {
-    __device__ None(const Dropout&, uint32_t, uint32_t, uint32_t, uint32_t) {}
-  };
-  typename std::conditional<DROP, KeepColumns<V, C / V, SHIFT>, None>::type keep(p.drop, threadIdx.x, blockDim.x, 0, lead);
-  const float2* stats = reinterpret_cast<const float2*>(p.stats);
-  float2 of_row = stats[walker];
-  int stage = 0, turn = 0;
-  for (uint64_t t = walker; t < p.tokens; t += walkers) {
-    const float2 mine = of_row;
-    if (t + walkers < p.tokens) of_row = stats[t + walkers];
-    float2 u[P], n[P], g[P], a = splat(0.f), b = splat(0.f);
-    cp_async_wait<kStages - 1>();
-    ring.cut(stage);
-    ring.get(stage, kH, h_at, u);
-    ring.get(stage, kX, x_at, n);
-#pragma unroll
-    for (int i = 0; i < P; i++) n[i] = mul2(add2(n[i], splat(-mine.x)), splat(mine.y));
-    in_row.keep(n);
-#pragma unroll
-    for (int i = 0; i < P; i++) {
-      dw[i] = fma2(u[i], n[i], dw[i]);
-      db[i] = add2(db[i], u[i]);
-      u[i] = mul2(u[i], w[i]);
-      a = add2(a, u[i]);
-      b = fma2(u[i], n[i], b);
-    }
-    float sums[2] = {a.x + a.y, b.x + b.y};
-    ring.get(stage, kPast, past_at, g);
-    issue(stage);
-    uint32_t bits[C / V][V / 2];
-    if constexpr (DROP) keep.draw(static_cast<uint32_t>(t), static_cast<uint32_t>(walkers), bits);
-    block_sum_f32<2>(sums, red[turn]);
-    turn ^= 1;
-    const float2 ma = splat(-sums[0] * inv_d), mb = splat(-sums[1] * inv_d), root = splat(mine.y);
-#pragma unroll
-    for (int i = 0; i < P; i++)
-      g[i] = fma2(root, fma2(n[i], mb, add2(u[i], ma)), g[i]);
-    {
-      const float2 scale = splat(p.residual_scale);
-#pragma unroll
-      for (int i = 0; i < P; i++) u[i] = mul2(scale, g[i]);
-      ring.put(ring.start(static_cast<T*>(p.dx), t, p.hidden), u);
-    }
-    if (p.dy) {
-      if constexpr (DROP) keep.apply(g, bits);
-      ring.put(ring.start(static_cast<T*>(p.dy), t, p.hidden), g);
-    }
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-  }
-  cp_async_wait<0>();
-  float* mine = p.parts + walker * 2 * p.hidden;
-  const float *fw = reinterpret_cast<const float*>(dw), *fb = reinterpret_cast<const float*>(db);
-#pragma unroll
-  for (int i = 0; i < Ring::NV; i++) {
-    const uint32_t c = threadIdx.x + i * blockDim.x;
-    float ow[V], ob[V];
-#pragma unroll
-    for (int j = 0; j < V; j++) ow[j] = fw[i * V + j], ob[j] = fb[i * V + j];
-    if constexpr (SHIFT) {
-#pragma unroll
-      for (int j = 0; j < V; j++) {
-        const uint32_t col = c * V + j - lead;
-        if (col >= p.hidden) continue;
-        mine[col] = ow[j];
-        mine[p.hidden + col] = ob[j];
-      }
-    } else if (c < ring.pieces) {
-      store_f32<V>(mine + c * V, ow);
-      store_f32<V>(mine + p.hidden + c * V, ob);
-    }
-  }
-}
-
-// Narrow rows: every warp walks rows of its own, the next one's loads under way while it computes; a
-// CTA adds its warps' sums at the end.
-constexpr uint32_t kLayerWarpWidth = 256;
-template <typename T, int V, bool DROP>
-__global__ void __launch_bounds__(kNormWarps * 32) layer_norm_bwd_warp_kernel(LayerNormBwdParams p) {
-  constexpr int NV = 8 / V;
-  __shared__ float tile[kNormWarps][kLayerWarpWidth];
-  pdl_begin();
-  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, pieces = p.hidden / V;
-  const float inv_d = 1.f / static_cast<float>(p.hidden);
-  const uint64_t walkers = static_cast<uint64_t>(gridDim.x) * kNormWarps;
-  float w[NV][V], dw[NV][V], db[NV][V];
-#pragma unroll
-  for (int i = 0; i < NV; i++) {
-#pragma unroll
-    for (int j = 0; j < V; j++) w[i][j] = dw[i][j] = db[i][j] = 0.f;
-    if (lane + i * 32 < pieces) load_params<T, V>(p.weight, p.params_f32, (lane + i * 32) * V, w[i]);
-  }
-  struct Row {
-    Piece<T, V> h[NV], x[NV], past[NV];
-    float2 stats;
-  };
-  auto load = [&](Row& r, uint64_t t) {
-    r.stats = reinterpret_cast<const float2*>(p.stats)[t];
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-      const uint32_t c = lane + i * 32;
-      r.h[i] = r.x[i] = r.past[i] = Piece<T, V>::zero();
-      if (c >= pieces) continue;
-      r.h[i] = Piece<T, V>::load(static_cast<const T*>(p.dh) + t * p.dh_stride + c * V);
-      r.x[i] = Piece<T, V>::load(static_cast<const T*>(p.x_new) + t * p.x_new_stride + c * V);
-      if (p.dx_new) r.past[i] = Piece<T, V>::load(static_cast<const T*>(p.dx_new) + t * p.dx_new_stride + c * V);
-    }
-  };
-  uint64_t t = static_cast<uint64_t>(blockIdx.x) * kNormWarps + warp;
-  Row row, next;
-  if (t < p.tokens) load(row, t);
-  for (; t < p.tokens; t += walkers) {
-    if (t + walkers < p.tokens) load(next, t + walkers);
-    float u[NV][V], n[NV][V], a = 0.f, b = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-      row.h[i].get(u[i]);
-      row.x[i].get(n[i]);
-#pragma unroll
-      for (int j = 0; j < V; j++) {
-        n[i][j] = (n[i][j] - row.stats.x) * row.stats.y;  // beyond the width u is zero
-        dw[i][j] = fmaf(u[i][j], n[i][j], dw[i][j]);
-        db[i][j] += u[i][j];
-        u[i][j] *= w[i][j];
-        a += u[i][j];
-        b = fmaf(u[i][j], n[i][j], b);
-      }
-    }
-    a = warp_sum_f32(a) * inv_d;
-    b = warp_sum_f32(b) * inv_d;
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-      const uint32_t c = lane + i * 32;
-      const uint64_t at = t * p.hidden + c * V;
-      float g[V], o[V];
-      row.past[i].get(g);
-#pragma unroll
-      for (int j = 0; j < V; j++) {
-        g[j] = fmaf(row.stats.y, u[i][j] - a - n[i][j] * b, g[j]);
-        o[j] = p.residual_scale * g[j];
-      }
-      if (c >= pieces) continue;
-      Piece<T, V> out;
-      out.set(o);
-      out.store(static_cast<T*>(p.dx) + at);
-      if (!p.dy) continue;
-      if (DROP) KeepRng(p.drop).template apply<V>(g, static_cast<uint32_t>(t), c * V);
-      out.set(g);
-      out.store(static_cast<T*>(p.dy) + at);
-    }
-    row = next;
-  }
-  float* mine = p.parts + static_cast<uint64_t>(blockIdx.x) * 2 * p.hidden;
-  auto flush = [&](const float (&s)[NV][V], float* dst) {
-#pragma unroll
-    for (int i = 0; i < NV; i++)
-#pragma unroll
-      for (int j = 0; j < V; j++)
-        if (lane + i * 32 < pieces) tile[warp][(lane + i * 32) * V + j] = s[i][j];
-    __syncthreads();
-    if (threadIdx.x < p.hidden) {
-      float sum = 0.f;
-#pragma unroll
-      for (int q = 0; q < kNormWarps; q++) sum += tile[q][threadIdx.x];
-      dst[threadIdx.x] = sum;
-    }
-    __syncthreads();
-  };
-  flush(dw, mine);
-  flush(db, mine + p.hidden);
-}
-
-// Adds the CTAs' sums, in order: the warps take a share of the parts each, a lane a column.
-// blockIdx.y: 0 the weight's gradient, 1 the bias's.
-template <typename T>
-__global__ void __launch_bounds__(1024) layer_norm_parts_kernel(LayerNormBwdParams p) {
-  __shared__ float sums[32][33];
-  pdl_begin();
-  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
-  void* dst = blockIdx.y ? p.dbias : p.dweight;
-  if (!dst) return;
-  float s = 0.f;
-  const uint32_t first = p.ctas * warp / 32, last = p.ctas * (warp + 1) / 32;
-  if (col < p.hidden) {
-#pragma unroll 8
-    for (uint32_t i = first; i < last; i++) s += p.parts[(2ull * i + blockIdx.y) * p.hidden + col];
-  }
-  sums[warp][lane] = s;
-  __syncthreads();
-  s = warp_sum_f32(sums[lane][warp]);
-  const uint32_t mine = blockIdx.x * 32 + warp;
-  if (lane || mine >= p.hidden) return;
-  if (p.params_f32)
-    static_cast<float*>(dst)[mine] = s;
-  else
-    static_cast<T*>(dst)[mine] = from_f32<T>(s);
-}
-
 template <typename T, int V, int NV, bool WARP, int THREADS>
 cudaError_t run_shape(LayerNormParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
   const void* fn = nullptr;
@@ -551,11 +196,13 @@ cudaError_t run_shape(LayerNormParams& p, int threads, cudaStream_t stream, cons
                        false);
 }
 
-template <typename T, int V, int C, bool SHIFT, bool BRANCH, bool DROP>
+template <typename T, int C, bool SHIFT, bool BRANCH, bool DROP>
 cudaError_t run_ring(LayerNormParams& p, int threads, uint64_t period, cudaStream_t stream, const DeviceInfo& dev) {
   static RingPrep prep;
-  const int smem = static_cast<int>(RowRing<T, V, C, BRANCH ? 2 : 1, kLayerStages<C>>::bytes(threads));
+  constexpr int V = kPieceOf<T>;
+  const int smem = static_cast<int>(RowRing<T, V, C, BRANCH ? 2 : 1, kLayerStages<C, BRANCH>>::bytes(threads));
   const void* fn = reinterpret_cast<const void*>(layer_norm_ring_kernel<T, V, C, SHIFT, BRANCH, DROP>);
+  static_assert(kLayerStages<C, BRANCH> * (BRANCH ? 2 : 1) * kNormRingThreads * C * sizeof(T) <= kNormRingSmem, "shared memory");
   int fit = 0;
   cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, 1, &fit);
   if (e != cudaSuccess) return e;
@@ -569,15 +216,14 @@ cudaError_t run_ring(LayerNormParams& p, int threads, uint64_t period, cudaStrea
 // Runs the ring with C columns a thread if it holds such rows.
 template <typename T, int C, bool SHIFT>
 bool run_ring(LayerNormParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e, uint64_t period = 1) {
-  constexpr int V = kPieceOf<T>;
-  const int threads = static_cast<int>((p.hidden + (SHIFT ? V - 1 : 0) + C * 32 - 1) / (C * 32) * 32);
-  if (threads > kNormRingThreads || RowRing<T, V, C, 2, kLayerStages<C>>::bytes(threads) > kNormRingSmem) return false;
+  const int threads = static_cast<int>((p.hidden + (SHIFT ? kPieceOf<T> - 1 : 0) + C * 32 - 1) / (C * 32) * 32);
+  if (threads > kNormRingThreads) return false;
   if (p.drop.rng)
-    *e = run_ring<T, V, C, SHIFT, true, true>(p, threads, period, stream, dev);
+    *e = run_ring<T, C, SHIFT, true, true>(p, threads, period, stream, dev);
   else if (p.y)
-    *e = run_ring<T, V, C, SHIFT, true, false>(p, threads, period, stream, dev);
+    *e = run_ring<T, C, SHIFT, true, false>(p, threads, period, stream, dev);
   else
-    *e = run_ring<T, V, C, SHIFT, false, false>(p, threads, period, stream, dev);
+    *e = run_ring<T, C, SHIFT, false, false>(p, threads, period, stream, dev);
   return true;
 }
 
@@ -591,8 +237,10 @@ cudaError_t run_width(LayerNormParams& p, cudaStream_t stream, const DeviceInfo&
   if constexpr (V > 1) {
     if (d <= 1024 && p.tokens >= 16ull * static_cast<uint64_t>(dev.sm_count))
       return run_shape<T, V, 32 / V, true, kWarp>(p, kWarp, stream, dev);
-    if (run_ring<T, kLayerCols, false>(p, stream, dev, &e)) return e;
-    if (run_ring<T, kLayerWideCols, false>(p, stream, dev, &e)) return e;
+    if (run_ring<T, kLayerCols<T>, false>(p, stream, dev, &e)) return e;
+    if constexpr (kLayerCols<T> != kLayerWideCols) {
+      if (run_ring<T, kLayerWideCols, false>(p, stream, dev, &e)) return e;
+    }
   } else {
     RowPlaces rows;
     rows.add(p.x, p.x_stride * sizeof(T));
@@ -600,8 +248,10 @@ cudaError_t run_width(LayerNormParams& p, cudaStream_t stream, const DeviceInfo&
     rows.add(p.x_new, static_cast<uint64_t>(d) * sizeof(T));
     rows.add(p.h, static_cast<uint64_t>(d) * sizeof(T));
     if (rows.alike) {
-      if (run_ring<T, kLayerCols, true>(p, stream, dev, &e, rows.period())) return e;
-      if (run_ring<T, kLayerWideCols, true>(p, stream, dev, &e, rows.period())) return e;
+      if (run_ring<T, kLayerCols<T>, true>(p, stream, dev, &e, rows.period())) return e;
+      if constexpr (kLayerCols<T> != kLayerWideCols) {
+        if (run_ring<T, kLayerWideCols, true>(p, stream, dev, &e, rows.period())) return e;
+      }
     }
   }
   // Wider still, or rows that start elsewhere in one matrix than in another: a CTA holds a row in
@@ -611,105 +261,20 @@ cudaError_t run_width(LayerNormParams& p, cudaStream_t stream, const DeviceInfo&
 }
 
 template <typename T>
-cudaError_t add_parts(LayerNormBwdParams& p, cudaStream_t stream) {
-  void* args[] = {&p};
-  return launch_kernel(reinterpret_cast<const void*>(layer_norm_parts_kernel<T>),
-                       dim3((p.hidden + 31) / 32, p.dbias ? 2 : 1), dim3(1024), 0, stream, args, false);
-}
-
-template <typename T>
-cudaError_t run_walkers(LayerNormBwdParams& p, const void* fn, uint64_t most, uint64_t rows_a_cta, int threads, int smem,
-                        cudaStream_t stream) {
-  if (most > norm_max_walkers(p.hidden)) most = norm_max_walkers(p.hidden);
-  const uint64_t ctas = (p.tokens + rows_a_cta - 1) / rows_a_cta;
-  p.ctas = static_cast<uint32_t>(ctas < most ? ctas : most);
-  void* args[] = {&p};
-  cudaError_t e = launch_kernel(fn, dim3(p.ctas), dim3(threads), smem, stream, args, false);
-  return e == cudaSuccess ? add_parts<T>(p, stream) : e;
-}
-
-template <typename T, int V, int NV, int THREADS>
-cudaError_t run_shape(LayerNormBwdParams& p, int threads, cudaStream_t stream, const DeviceInfo& dev) {
-  const void* fn = p.drop.rng ? reinterpret_cast<const void*>(layer_norm_bwd_kernel<T, V, NV, true, THREADS>)
-                              : reinterpret_cast<const void*>(layer_norm_bwd_kernel<T, V, NV, false, THREADS>);
-  const uint64_t most = static_cast<uint64_t>(dev.sm_count) * (threads > 256 ? 1024u / static_cast<unsigned>(threads) : 4u);
-  return run_walkers<T>(p, fn, most, 1, threads, 0, stream);
-}
-
-template <typename T, int C, bool SHIFT>
-bool run_ring(LayerNormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e, uint64_t period = 1) {
-  constexpr int V = kPieceOf<T>;
-  const int threads = static_cast<int>((p.hidden + (SHIFT ? V - 1 : 0) + C * 32 - 1) / (C * 32) * 32);
-  const int smem = static_cast<int>(RowRing<T, V, C, 3, kLayerBwdStages>::bytes(threads));
-  if (threads > kNormRingThreads || smem > kNormRingSmem) return false;
-  static RingPrep prep[2];
-  const bool drop = p.drop.rng != nullptr;
-  const void* fn = drop ? reinterpret_cast<const void*>(layer_norm_bwd_ring_kernel<T, V, C, SHIFT, true>)
-                        : reinterpret_cast<const void*>(layer_norm_bwd_ring_kernel<T, V, C, SHIFT, false>);
-  int fit = 0;
-  *e = prepare_ring(prep[drop], fn, threads, smem, dev, 1, &fit);
-  if (*e != cudaSuccess) return true;
-  uint64_t most = static_cast<uint64_t>(fit);
-  if (most > norm_max_walkers(p.hidden)) most = norm_max_walkers(p.hidden);
-  if (most > period) most -= most % period;
-  *e = run_walkers<T>(p, fn, most, 1, threads, smem, stream);
-  return true;
-}
-
-template <typename T, int V>
-cudaError_t run_width(LayerNormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
-  const uint32_t d = p.hidden;
-  cudaError_t e;
-  if (d <= kLayerWarpWidth) {
-    const void* fn = p.drop.rng ? reinterpret_cast<const void*>(layer_norm_bwd_warp_kernel<T, V, true>)
-                                : reinterpret_cast<const void*>(layer_norm_bwd_warp_kernel<T, V, false>);
-    return run_walkers<T>(p, fn, 4ull * static_cast<uint64_t>(dev.sm_count), kNormWarps, kNormWarps * 32, 0, stream);
-  }
-  if constexpr (V > 1) {
-    if (run_ring<T, kLayerCols, false>(p, stream, dev, &e)) return e;
-    if (run_ring<T, kLayerWideCols, false>(p, stream, dev, &e)) return e;
-  } else {
-    RowPlaces rows;
-    rows.add(p.dh, p.dh_stride * sizeof(T));
-    rows.add(p.x_new, p.x_new_stride * sizeof(T));
-    rows.add(p.dx_new, p.dx_new_stride * sizeof(T));
-    rows.add(p.dx, static_cast<uint64_t>(d) * sizeof(T));
-    rows.add(p.dy, static_cast<uint64_t>(d) * sizeof(T));
-    if (rows.alike) {
-      if (run_ring<T, kLayerCols, true>(p, stream, dev, &e, rows.period())) return e;
-      if (run_ring<T, kLayerWideCols, true>(p, stream, dev, &e, rows.period())) return e;
-    }
-  }
-  if (d <= 4096) return run_shape<T, V, 8 / V, 512>(p, static_cast<int>((d + 255) / 256 * 32), stream, dev);
-  return run_shape<T, V, 16 / V, 1024>(p, static_cast<int>((d + 511) / 512 * 32), stream, dev);
-}
-
-template <typename T, typename P>
-cudaError_t run_typed(P& p, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
+cudaError_t run_typed(LayerNormParams& p, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
   return vec ? run_width<T, kPieceOf<T>>(p, stream, dev) : run_width<T, 1>(p, stream, dev);
 }
-template <typename P>
-cudaError_t run_dtype(P& p, int dtype, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
-  switch (dtype) {
-    case ZC_BF16: return run_typed<__nv_bfloat16>(p, vec, stream, dev);
-    case ZC_F16: return run_typed<__half>(p, vec, stream, dev);
-    default: return run_typed<float>(p, vec, stream, dev);
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_layer_norm(const LayerNormParams& params, int dtype, bool vec, cudaStream_t stream,
                               const DeviceInfo& dev) {
   if (params.tokens == 0) return cudaSuccess;
   LayerNormParams p = params;
-  return run_dtype(p, dtype, vec, stream, dev);
-}
-
-cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& params, int dtype, bool vec, cudaStream_t stream,
-                                  const DeviceInfo& dev) {
-  LayerNormBwdParams p = params;
-  return run_dtype(p, dtype, vec, stream, dev);
+  switch (dtype) {
+    case ZC_BF16: return run_typed<__nv_bfloat16>(p, vec, stream, dev);
+    case ZC_F16: return run_typed<__half>(p, vec, stream, dev);
+    default: return run_typed<float>(p, vec, stream, dev);
+  }
 }
 
 }  // namespace zc
