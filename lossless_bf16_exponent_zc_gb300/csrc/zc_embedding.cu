@@ -8,6 +8,7 @@
 // memory is read back.  All parts but the sort are bound by memory.
 #include "zc_internal.h"
 #include "zc_layer.cuh"
+#include "zc_norm.cuh"
 
 namespace zc {
 
@@ -267,14 +268,15 @@ __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(EmbedBwdParam
 // sort holds 32 `items` keys in order; a pass counts its digits warp by warp, the CTAs tell one
 // another their counts, and every key goes to its place in the shared memory of the CTA that it
 // falls to, in the last pass to the workspace.
-constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterThreads = 512, kClusterWarps = kClusterThreads / 32;
 constexpr uint32_t kMostItems = kEmbedClusterTokens / (kEmbedClusterCtas * kClusterThreads);
 constexpr uint32_t kClusterBins = 512;
 constexpr uint32_t kFillRows = 32768;  // rows whose presence a CTA keeps at once
 
 struct ClusterSort {
-  uint32_t items, ctas, bits, passes, size, fill;  // fill: CTAs that zero rows
-  uint64_t fill_rows;                                // rows of each of them
+  uint32_t items, ctas, bits, passes, size;
+  uint32_t fill, late;           // CTAs that zero rows: those beside the sort, and those that follow it on its SMs
+  uint64_t fill_rows, late_rows;  // rows of each of them
 };
 
 __device__ __forceinline__ void zero_row(uint8_t* row, uint64_t bytes) {
@@ -309,14 +311,17 @@ __device__ __forceinline__ void fill_rows(const EmbedBwdParams& p, uint64_t firs
   }
 }
 
-__global__ void __launch_bounds__(kClusterThreads) embed_cluster_kernel(EmbedBwdParams p, ClusterSort c, Divisor cap) {
+__global__ void __launch_bounds__(kClusterThreads, 2) embed_cluster_kernel(EmbedBwdParams p, ClusterSort c, Divisor cap) {
   extern __shared__ __align__(16) uint8_t cluster_smem[];
   __shared__ uint32_t warp_totals[kClusterWarps];
   pdl_begin();
   if (blockIdx.x >= c.ctas) {
-    const uint64_t first = (blockIdx.x - c.ctas) * c.fill_rows;
-    if (blockIdx.x - c.ctas < c.fill && first < p.vocab)
-      fill_rows(p, first, min(p.vocab, first + c.fill_rows), c.size, reinterpret_cast<uint32_t*>(cluster_smem));
+    const uint32_t i = blockIdx.x - c.ctas;
+    if (i >= c.fill + c.late) return;
+    const uint64_t rows = i < c.fill ? c.fill_rows : c.late_rows;
+    const uint64_t first = i < c.fill ? i * rows : c.fill * c.fill_rows + (i - c.fill) * rows;
+    if (first < p.vocab)
+      fill_rows(p, first, min(p.vocab, first + rows), c.size, reinterpret_cast<uint32_t*>(cluster_smem));
     return;
   }
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, rank = blockIdx.x;
@@ -419,8 +424,9 @@ __global__ void __launch_bounds__(kClusterThreads) embed_cluster_kernel(EmbedBwd
 // go on in a neighbouring run, the sum is left in the workspace: slot 0 of the run for the tokens of
 // a row that began before it, slot 1 for one that begins in it and goes on.
 constexpr uint32_t kSlab = 256;
-template <bool VEC>
-constexpr int kRowLoads = VEC ? 8 : 4;  // rows on their way at once
+// Rows on their way at once, as many as 80 registers hold; ADD: with the table's rows that they end in.
+template <typename T, bool VEC, bool ADD>
+constexpr int kSumRows = (VEC && !ADD ? 8 : 4) / (sizeof(T) / 2);
 
 template <typename T, typename TT, bool VEC>
 struct EmbedCols {
@@ -461,9 +467,36 @@ struct EmbedCols {
   }
 };
 
-// Writes (or adds) scale acc to the lane's columns of a table row.
+// The lane's columns of a table row that the sums are added to, read ahead of them.
+template <typename T, typename TT>
+struct OldCols {
+  static constexpr int V = kPieceOf<T>, W = kPieceOf<TT>;
+  uint4 w[8 / W];
+  __device__ __forceinline__ void load(const EmbedBwdParams& p, uint64_t row, uint32_t slab) {
+    const TT* from = static_cast<const TT*>(p.dtable) + row * p.hidden;
+#pragma unroll
+    for (int i = 0; i < 8 / V; i++) {
+      const uint32_t c = EmbedCols<T, TT, true>::col(slab, i);
+      if (c >= p.hidden) continue;
+#pragma unroll
+      for (int k = 0; k < V / W; k++) w[i * (V / W) + k] = *reinterpret_cast<const uint4*>(from + c + k * W);
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8 / W; i++) {
+      float v[W];
+      Piece<TT, W>{w[i]}.get(v);
+#pragma unroll
+      for (int j = 0; j < W; j++) f[i * W + j] = v[j];
+    }
+  }
+};
+
+// Writes scale acc + old to the lane's columns of a table row; off 16 bytes `old` is read here.
 template <typename T, typename TT, bool VEC>
-__device__ __forceinline__ void put_row(const EmbedBwdParams& p, uint64_t row, uint32_t slab, const float (&acc)[8]) {
+__device__ __forceinline__ void put_row(const EmbedBwdParams& p, uint64_t row, uint32_t slab, const float (&acc)[8],
+                                        const float (&old)[8]) {
   constexpr int V = kPieceOf<T>, W = kPieceOf<TT>;
   TT* to = static_cast<TT*>(p.dtable) + row * p.hidden;
 #pragma unroll
@@ -475,10 +508,7 @@ __device__ __forceinline__ void put_row(const EmbedBwdParams& p, uint64_t row, u
       for (int k = 0; k < V; k += W) {
         float f[W];
 #pragma unroll
-        for (int j = 0; j < W; j++) f[j] = 0.f;
-        if (p.accumulate) Piece<TT, W>::load(to + c + k).get(f);
-#pragma unroll
-        for (int j = 0; j < W; j++) f[j] = fmaf(p.scale, acc[i * V + (k + j) % V], f[j]);
+        for (int j = 0; j < W; j++) f[j] = fmaf(p.scale, acc[i * V + (k + j) % V], old[i * V + (k + j) % V]);
         Piece<TT, W> o;
         o.set(f);
         o.store(to + c + k);
@@ -487,8 +517,8 @@ __device__ __forceinline__ void put_row(const EmbedBwdParams& p, uint64_t row, u
 #pragma unroll
       for (int j = 0; j < V; j++) {
         if (c + j >= p.hidden) continue;
-        const float old = p.accumulate ? to_f32<TT>(to[c + j]) : 0.f;
-        to[c + j] = from_f32<TT>(fmaf(p.scale, acc[i * V + j], old));
+        const float before = p.accumulate ? to_f32<TT>(to[c + j]) : 0.f;
+        to[c + j] = from_f32<TT>(fmaf(p.scale, acc[i * V + j], before));
       }
     }
   }
@@ -498,8 +528,9 @@ __device__ __forceinline__ float* part_of(const EmbedBwdParams& p, uint64_t run,
   return p.parts + ((run * 2 + slot) * p.slabs + slab) * kSlab;
 }
 
-template <typename T, typename TT, bool VEC>
-__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(EmbedBwdParams p) {
+template <typename T, typename TT, bool VEC, bool ADD>
+__global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedBwdParams p) {
+  constexpr int kRowLoads = kSumRows<T, VEC, ADD>;
   pdl_begin();
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads / 32) + (threadIdx.x >> 5), run = i / p.slabs;
   if (run >= p.runs) return;
@@ -518,27 +549,34 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(EmbedBwdParams
 #pragma unroll
   for (int j = 0; j < 8; j++) acc[j] = 0.f;
   bool began = __shfl_sync(kFull, key, 0) == before;  // the row at hand began before the run
-  for (uint32_t r0 = 0; r0 < n; r0 += kRowLoads<VEC>) {
-    EmbedCols<T, TT, VEC> v[kRowLoads<VEC>];
+  const bool leaves = n == p.run && __shfl_sync(kFull, key, p.run - 1) == after;  // its last row goes on behind the run
+  for (uint32_t r0 = 0; r0 < n; r0 += kRowLoads) {
+    EmbedCols<T, TT, VEC> v[kRowLoads];
+    OldCols<T, TT> old[ADD ? kRowLoads : 1];
 #pragma unroll
-    for (int q = 0; q < kRowLoads<VEC>; q++) {
+    for (int q = 0; q < kRowLoads; q++) {
       const uint64_t t = __shfl_sync(kFull, token, (r0 + q) & 31);
-      if (r0 + q < n) v[q].load(static_cast<const T*>(p.dout) + t * p.dout_stride, slab, p.hidden);
+      const uint32_t row = __shfl_sync(kFull, key, (r0 + q) & 31);
+      if (r0 + q >= n) continue;
+      v[q].load(static_cast<const T*>(p.dout) + t * p.dout_stride, slab, p.hidden);
+      if constexpr (ADD)
+        if (ends >> (r0 + q) & 1) old[q].load(p, row, slab);
     }
 #pragma unroll
-    for (int q = 0; q < kRowLoads<VEC>; q++) {
+    for (int q = 0; q < kRowLoads; q++) {
       const uint32_t r = r0 + q;
       if (r >= n) break;
       v[q].add(acc);
       if (!(ends >> r & 1)) continue;
       const uint32_t row = __shfl_sync(kFull, key, r);
-      const bool goes_on = r + 1 == p.run && after == row;
-      if (began || goes_on) {
+      if (began || (leaves && r + 1 == p.run)) {
         float* to = part_of(p, run, began ? 0 : 1, slab) + lane * 8;
         *reinterpret_cast<float4*>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         *reinterpret_cast<float4*>(to + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
       } else {
-        put_row<T, TT, VEC>(p, row, slab, acc);
+        float before[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if constexpr (ADD) old[q].get(before);
+        put_row<T, TT, VEC>(p, row, slab, acc, before);
       }
       began = false;
 #pragma unroll
@@ -547,51 +585,68 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(EmbedBwdParams
   }
 }
 
-// Rows whose tokens lie in several runs: the CTA of the run that such a row begins in, and of one
-// slab, adds the parts, each warp a share of them in order.
+// Rows whose tokens lie in several runs.  A CTA looks at kJoinRuns runs, and for each that such a row
+// begins in adds the row's parts of one slab, each warp a share of them in order.
+constexpr uint32_t kJoinRuns = 4;
 template <typename T, typename TT, bool VEC>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedBwdParams p) {
   __shared__ float sums[kEmbedThreads / 32][kSlab];
   pdl_begin();
-  const uint64_t run = blockIdx.x / p.slabs;
-  const uint32_t slab = static_cast<uint32_t>(blockIdx.x - run * p.slabs), lane = lane_id(), warp = threadIdx.x >> 5;
-  const uint64_t first = run * p.run, next = first + p.run;
-  if (next >= p.tokens) return;
-  const uint32_t row = p.keys_in[next - 1];
-  if (row == p.vocab || p.keys_in[next] != row) return;               // no row goes on behind the run
-  if (p.keys_in[first] == row && first && p.keys_in[first - 1] == row) return;  // it began before the run
-  uint64_t last = run + 1;  // the last run with tokens of the row
-  for (;; last += 32) {
-    const uint64_t at = (last + lane + 1) * p.run;
-    const uint32_t more = __ballot_sync(kFull, at < p.tokens && p.keys_in[at] == row);
-    if (more != kFull) {
-      last += __ffs(~more) - 1;
-      break;
+  const uint64_t group = blockIdx.x / p.slabs;
+  const uint32_t slab = static_cast<uint32_t>(blockIdx.x - group * p.slabs), lane = lane_id(), warp = threadIdx.x >> 5;
+  // lane i's run, and the row that goes on behind it if it began there
+  const uint64_t mine = group * kJoinRuns + lane, first = mine * p.run, next = first + p.run;
+  uint32_t row = static_cast<uint32_t>(p.vocab);
+  if (lane < kJoinRuns && next < p.tokens) {
+    const uint32_t last = p.keys_in[next - 1], before = first ? p.keys_in[first - 1] : row;
+    if (p.keys_in[next] == last && (p.keys_in[first] != last || before != last)) row = last;
+  }
+  uint32_t todo = __ballot_sync(kFull, row != p.vocab);
+  for (; todo; todo &= todo - 1) {
+    const uint32_t which = __ffs(todo) - 1;
+    const uint32_t of = __shfl_sync(kFull, row, which);
+    const uint64_t run = group * kJoinRuns + which;
+    uint64_t last = run + 1;  // the last run with tokens of the row
+    for (;; last += 32) {
+      const uint64_t at = (last + lane + 1) * p.run;
+      const uint32_t more = __ballot_sync(kFull, at < p.tokens && p.keys_in[at] == of);
+      if (more != kFull) {
+        last += __ffs(~more) - 1;
+        break;
+      }
     }
-  }
-  const uint64_t count = last - run + 1;
-  float acc[8];
+    const uint64_t count = last - run + 1;
+    float acc[8];
 #pragma unroll
-  for (int j = 0; j < 8; j++) acc[j] = 0.f;
-  const uint64_t to = count * (warp + 1) / (kEmbedThreads / 32);
+    for (int j = 0; j < 8; j++) acc[j] = 0.f;
+    const uint64_t to = count * (warp + 1) / (kEmbedThreads / 32);
 #pragma unroll 4
-  for (uint64_t i = count * warp / (kEmbedThreads / 32); i < to; i++) {
-    const float* from = part_of(p, run + i, i ? 0 : 1, slab) + lane * 8;
-    const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
-    acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
-    acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
+    for (uint64_t i = count * warp / (kEmbedThreads / 32); i < to; i++) {
+      const float* from = part_of(p, run + i, i ? 0 : 1, slab) + lane * 8;
+      const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
+      acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
+      acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) sums[warp][j * 32 + lane] = acc[j];
+    __syncthreads();
+    if (warp == 0) {
+      float old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (VEC && p.accumulate) {
+        OldCols<T, TT> cols;
+        cols.load(p, of, slab);
+        cols.get(old);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        acc[j] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kEmbedThreads / 32; w++) acc[j] += sums[w][j * 32 + lane];
+      }
+      put_row<T, TT, VEC>(p, of, slab, acc, old);
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int j = 0; j < 8; j++) sums[warp][j * 32 + lane] = acc[j];
-  __syncthreads();
-  if (warp) return;
-#pragma unroll
-  for (int j = 0; j < 8; j++) {
-    acc[j] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kEmbedThreads / 32; w++) acc[j] += sums[w][j * 32 + lane];
-  }
-  put_row<T, TT, VEC>(p, row, slab, acc);
 }
 
 // Zeroes the rows that no token asks for, a warp a row.
@@ -634,11 +689,12 @@ cudaError_t lookup(EmbedParams& p, bool vec, cudaStream_t stream, const DeviceIn
 template <typename T, typename TT, bool VEC>
 cudaError_t sums(EmbedBwdParams& p, cudaStream_t stream) {
   void* args[] = {&p};
-  cudaError_t e = run(reinterpret_cast<const void*>(embed_sum_kernel<T, TT, VEC>),
-                      ceil_div(p.runs * p.slabs, kEmbedThreads / 32), kEmbedThreads, 0, stream, args);
+  const void* fn = VEC && p.accumulate ? reinterpret_cast<const void*>(embed_sum_kernel<T, TT, VEC, VEC>)
+                                       : reinterpret_cast<const void*>(embed_sum_kernel<T, TT, VEC, false>);
+  cudaError_t e = run(fn, ceil_div(p.runs * p.slabs, kEmbedThreads / 32), kEmbedThreads, 0, stream, args);
   if (e != cudaSuccess || p.runs < 2) return e;
-  return run(reinterpret_cast<const void*>(embed_join_kernel<T, TT, VEC>), p.runs * p.slabs, kEmbedThreads, 0, stream,
-             args);
+  return run(reinterpret_cast<const void*>(embed_join_kernel<T, TT, VEC>), ceil_div(p.runs, kJoinRuns) * p.slabs,
+             kEmbedThreads, 0, stream, args);
 }
 template <typename T, typename TT>
 cudaError_t sums(EmbedBwdParams& p, bool vec, cudaStream_t stream) {
@@ -703,11 +759,24 @@ cudaError_t sort_in_cluster(EmbedBwdParams& p, uint32_t bits, uint32_t size, cud
   cudaError_t e = prepare_kernel(prep, fn, kClusterThreads, kMostSmem, dev, &per_sm);
   if (e != cudaSuccess) return e;
   if (!p.accumulate && p.vocab) {
-    const uint64_t most = 2ull * static_cast<uint64_t>(dev.sm_count), rows = ceil_div(p.vocab, kClusterWarps);
-    c.fill = static_cast<uint32_t>(rows < most ? rows : most);
-    c.fill_rows = ceil_div(p.vocab, c.fill);
+    // One wave of CTAs, two an SM where clusters fit.  The table is cut so that those that take the
+    // sort's place after it end with the others: the sort's time, about 10 us and 4 more with every
+    // 16384 tokens, at 20 KB a microsecond.
+    int fit = 0;
+    static RingPrep fits[2];
+    e = prepare_ring(fits[c.ctas > 1], fn, kClusterThreads, kMostSmem, dev, static_cast<int>(c.ctas), &fit);
+    if (e != cudaSuccess) return e;
+    const uint64_t beside = fit > 1 ? (static_cast<uint64_t>(fit) - 1) * c.ctas : 1;
+    const uint64_t row = static_cast<uint64_t>(p.hidden) * size;
+    const uint64_t lost = (10 + p.tokens / 4096) * 20480 / row;
+    c.fill = static_cast<uint32_t>(beside);
+    c.late = c.ctas;
+    const uint64_t all = p.vocab + c.late * lost;
+    c.fill_rows = ceil_div(all, beside + c.late);
+    if (c.fill_rows <= lost || c.fill_rows * beside >= p.vocab) c.late = 0, c.fill_rows = ceil_div(p.vocab, beside);
+    if (c.late) c.late_rows = ceil_div(p.vocab - c.fill_rows * beside, c.late);
   }
-  const uint32_t grid = c.ctas + static_cast<uint32_t>(ceil_div(c.fill, c.ctas)) * c.ctas;
+  const uint32_t grid = c.ctas + static_cast<uint32_t>(ceil_div(c.fill + c.late, c.ctas)) * c.ctas;
   void* args[] = {&p, &c, &cap};
   return launch_kernel(fn, dim3(grid), dim3(kClusterThreads), smem, stream, args, false, c.ctas);
 }

@@ -297,7 +297,7 @@ struct EmbedParams {
 constexpr uint32_t kEmbedDigitBits = 10;    // of the gradient's radix sort, at most
 constexpr uint32_t kEmbedSortChunk = 1024;  // keys of a CTA there
 constexpr uint32_t kEmbedClusterCtas = 8;
-constexpr uint32_t kEmbedClusterTokens = 65536;  // that one cluster sorts
+constexpr uint32_t kEmbedClusterTokens = 32768;  // that one cluster sorts
 struct EmbedBwdParams {
   const void* dout;
   const void* ids;
