@@ -493,16 +493,18 @@ struct OldCols {
   }
 };
 
-// Writes scale acc + old to the lane's columns of a table row; off 16 bytes `old` is read here.
+// Writes scale acc + old to the lane's columns of a table row.  Off 16 bytes the warp's columns go
+// through shared memory (`tile`, its own), so that the lanes write, and read what they add to,
+// neighbouring values.
 template <typename T, typename TT, bool VEC>
 __device__ __forceinline__ void put_row(const EmbedBwdParams& p, uint64_t row, uint32_t slab, const float (&acc)[8],
-                                        const float (&old)[8]) {
+                                        const float (&old)[8], float* tile) {
   constexpr int V = kPieceOf<T>, W = kPieceOf<TT>;
   TT* to = static_cast<TT*>(p.dtable) + row * p.hidden;
+  if constexpr (VEC) {
 #pragma unroll
-  for (int i = 0; i < 8 / V; i++) {
-    const uint32_t c = EmbedCols<T, TT, VEC>::col(slab, i);
-    if (VEC) {
+    for (int i = 0; i < 8 / V; i++) {
+      const uint32_t c = EmbedCols<T, TT, VEC>::col(slab, i);
       if (c >= p.hidden) continue;
 #pragma unroll
       for (int k = 0; k < V; k += W) {
@@ -513,13 +515,20 @@ __device__ __forceinline__ void put_row(const EmbedBwdParams& p, uint64_t row, u
         o.set(f);
         o.store(to + c + k);
       }
-    } else {
+    }
+  } else {
+    const uint32_t lane = lane_id(), first = slab * kSlab;
+    __syncwarp();  // the last row's values have been read
 #pragma unroll
-      for (int j = 0; j < V; j++) {
-        if (c + j >= p.hidden) continue;
-        const float before = p.accumulate ? to_f32<TT>(to[c + j]) : 0.f;
-        to[c + j] = from_f32<TT>(fmaf(p.scale, acc[i * V + j], before));
-      }
+    for (int i = 0; i < 8 / V; i++)
+      store_f32<V>(tile + (i * 32 + lane) * V, *reinterpret_cast<const float(*)[V]>(acc + i * V));
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const uint32_t c = first + j * 32 + lane;
+      if (c >= p.hidden) continue;
+      const float before = p.accumulate ? to_f32<TT>(to[c]) : 0.f;
+      to[c] = from_f32<TT>(fmaf(p.scale, tile[j * 32 + lane], before));
     }
   }
 }
@@ -531,6 +540,8 @@ __device__ __forceinline__ float* part_of(const EmbedBwdParams& p, uint64_t run,
 template <typename T, typename TT, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedBwdParams p) {
   constexpr int kRowLoads = kSumRows<T, VEC, ADD>;
+  __shared__ __align__(16) float tiles[VEC ? 1 : kEmbedThreads / 32][VEC ? 4 : kSlab];
+  float* tile = tiles[VEC ? 0 : threadIdx.x >> 5];
   pdl_begin();
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads / 32) + (threadIdx.x >> 5), run = i / p.slabs;
   if (run >= p.runs) return;
@@ -576,7 +587,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedBwdPar
       } else {
         float before[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if constexpr (ADD) old[q].get(before);
-        put_row<T, TT, VEC>(p, row, slab, acc, before);
+        put_row<T, TT, VEC>(p, row, slab, acc, before, tile);
       }
       began = false;
 #pragma unroll
@@ -585,65 +596,85 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedBwdPar
   }
 }
 
-// Rows whose tokens lie in several runs.  A CTA looks at kJoinRuns runs, and for each that such a row
-// begins in adds the row's parts of one slab, each warp a share of them in order.
-constexpr uint32_t kJoinRuns = 4;
+// Rows whose tokens lie in several runs, of one slab.  Each warp looks at one run, and adds the parts of
+// the row that begins there and goes on; where those are many the warps of the CTA share them.
+constexpr uint32_t kJoinAlone = 16;  // parts that a warp adds by itself
 template <typename T, typename TT, bool VEC>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedBwdParams p) {
-  __shared__ float sums[kEmbedThreads / 32][kSlab];
+  constexpr uint32_t kWarps = kEmbedThreads / 32;
+  __shared__ __align__(16) float sums[kWarps][kSlab];
+  __shared__ uint32_t many[kWarps];  // parts of a warp's row that are for all, or 0
+  __shared__ uint32_t rows[kWarps];
   pdl_begin();
   const uint64_t group = blockIdx.x / p.slabs;
   const uint32_t slab = static_cast<uint32_t>(blockIdx.x - group * p.slabs), lane = lane_id(), warp = threadIdx.x >> 5;
-  // lane i's run, and the row that goes on behind it if it began there
-  const uint64_t mine = group * kJoinRuns + lane, first = mine * p.run, next = first + p.run;
-  uint32_t row = static_cast<uint32_t>(p.vocab);
-  if (lane < kJoinRuns && next < p.tokens) {
-    const uint32_t last = p.keys_in[next - 1], before = first ? p.keys_in[first - 1] : row;
-    if (p.keys_in[next] == last && (p.keys_in[first] != last || before != last)) row = last;
-  }
-  uint32_t todo = __ballot_sync(kFull, row != p.vocab);
-  for (; todo; todo &= todo - 1) {
-    const uint32_t which = __ffs(todo) - 1;
-    const uint32_t of = __shfl_sync(kFull, row, which);
-    const uint64_t run = group * kJoinRuns + which;
-    uint64_t last = run + 1;  // the last run with tokens of the row
-    for (;; last += 32) {
-      const uint64_t at = (last + lane + 1) * p.run;
-      const uint32_t more = __ballot_sync(kFull, at < p.tokens && p.keys_in[at] == of);
-      if (more != kFull) {
-        last += __ffs(~more) - 1;
-        break;
+  const uint64_t run = group * kWarps + warp, first = run * p.run, next = first + p.run;
+  uint32_t count = 0, row = 0;
+  if (next < p.tokens) {
+    const uint32_t none = static_cast<uint32_t>(p.vocab);
+    // lane i: the first key of run + 1 + i; with it the last one here, the first one, and the one before
+    const uint64_t at = next + static_cast<uint64_t>(lane) * p.run;
+    const uint32_t key = at < p.tokens ? p.keys_in[at] : none;
+    const uint32_t last = p.keys_in[next - 1], begin = p.keys_in[first], before = first ? p.keys_in[first - 1] : none;
+    row = last;
+    if (last != none && (begin != last || before != last)) {
+      uint32_t more = __ballot_sync(kFull, key == last);
+      count = more ? 1 : 0;
+      while (more == kFull) {  // 32 runs more
+        count += 32;
+        const uint64_t far = next + (static_cast<uint64_t>(lane) + count - 1) * p.run;
+        more = __ballot_sync(kFull, far < p.tokens && p.keys_in[far] == last);
       }
+      count += __popc(more);  // the row's runs come one after another
     }
-    const uint64_t count = last - run + 1;
-    float acc[8];
+  }
+  // adds parts from .. to of the row that begins in run `of`
+  auto add = [&](uint64_t of, uint32_t from, uint32_t to, float (&acc)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; j++) acc[j] = 0.f;
-    const uint64_t to = count * (warp + 1) / (kEmbedThreads / 32);
 #pragma unroll 4
-    for (uint64_t i = count * warp / (kEmbedThreads / 32); i < to; i++) {
-      const float* from = part_of(p, run + i, i ? 0 : 1, slab) + lane * 8;
-      const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
+    for (uint32_t i = from; i < to; i++) {
+      const float* part = part_of(p, of + i, i ? 0 : 1, slab) + lane * 8;
+      const float4 a = *reinterpret_cast<const float4*>(part), b = *reinterpret_cast<const float4*>(part + 4);
       acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
       acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
     }
+  };
+  auto put = [&](uint32_t of, const float (&acc)[8]) {
+    float old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (VEC && p.accumulate) {
+      OldCols<T, TT> cols;
+      cols.load(p, of, slab);
+      cols.get(old);
+    }
+    put_row<T, TT, VEC>(p, of, slab, acc, old, sums[warp]);
+  };
+  float acc[8];
+  if (count && count <= kJoinAlone) {
+    add(run, 0, count, acc);
+    put(row, acc);
+  }
+  if (lane == 0) {
+    many[warp] = count > kJoinAlone ? count : 0;
+    rows[warp] = row;
+  }
+  __syncthreads();
+  for (uint32_t w = 0; w < kWarps; w++) {
+    const uint32_t n = many[w];
+    if (n == 0) continue;
+    add(group * kWarps + w, static_cast<uint32_t>(static_cast<uint64_t>(n) * warp / kWarps),
+        static_cast<uint32_t>(static_cast<uint64_t>(n) * (warp + 1) / kWarps), acc);
 #pragma unroll
     for (int j = 0; j < 8; j++) sums[warp][j * 32 + lane] = acc[j];
     __syncthreads();
     if (warp == 0) {
-      float old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (VEC && p.accumulate) {
-        OldCols<T, TT> cols;
-        cols.load(p, of, slab);
-        cols.get(old);
-      }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         acc[j] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kEmbedThreads / 32; w++) acc[j] += sums[w][j * 32 + lane];
+        for (uint32_t q = 0; q < kWarps; q++) acc[j] += sums[q][j * 32 + lane];
       }
-      put_row<T, TT, VEC>(p, of, slab, acc, old);
+      put(rows[w], acc);
     }
     __syncthreads();
   }
@@ -693,7 +724,7 @@ cudaError_t sums(EmbedBwdParams& p, cudaStream_t stream) {
                                        : reinterpret_cast<const void*>(embed_sum_kernel<T, TT, VEC, false>);
   cudaError_t e = run(fn, ceil_div(p.runs * p.slabs, kEmbedThreads / 32), kEmbedThreads, 0, stream, args);
   if (e != cudaSuccess || p.runs < 2) return e;
-  return run(reinterpret_cast<const void*>(embed_join_kernel<T, TT, VEC>), ceil_div(p.runs, kJoinRuns) * p.slabs,
+  return run(reinterpret_cast<const void*>(embed_join_kernel<T, TT, VEC>), ceil_div(p.runs, kEmbedThreads / 32) * p.slabs,
              kEmbedThreads, 0, stream, args);
 }
 template <typename T, typename TT>
@@ -701,17 +732,26 @@ cudaError_t sums(EmbedBwdParams& p, bool vec, cudaStream_t stream) {
   return vec ? sums<T, TT, true>(p, stream) : sums<T, TT, false>(p, stream);
 }
 
-// Tokens of a run: 32 where there are many, fewer while the warps would not fill the GPU.
-uint32_t embed_run(uint64_t tokens, uint32_t hidden) {
-  const uint64_t slabs = ceil_div(hidden, kSlab);
-  uint32_t run = 32;
-  while (run > 4 && tokens * slabs < 4096ull * run) run /= 2;
-  return run;
+// Tokens of a run: those that make the waves of warps, three CTAs an SM, take the least time, a warp
+// as long as its run and six rows more (16384 tokens of 4096 columns: 24 of them fill three waves,
+// with 32 the third is a quarter full); but no more than kMostShort warps of short runs, whose sums
+// take workspace.
+constexpr uint64_t kMostShort = 16384;
+uint32_t embed_run(uint64_t tokens, uint32_t hidden, const DeviceInfo& dev) {
+  const uint64_t slabs = ceil_div(hidden, kSlab), wave = 24ull * static_cast<uint64_t>(dev.sm_count);
+  uint64_t least = ~0ull;
+  uint32_t best = 32;
+  for (uint32_t run = 32; run >= 4; run--) {
+    const uint64_t warps = ceil_div(tokens, run) * slabs, time = ceil_div(warps, wave) * (run + 6);
+    if ((run < 32 && warps > kMostShort) || time >= least) continue;
+    least = time;
+    best = run;
+  }
+  return best;
 }
-// At most so many runs of `tokens` tokens or fewer.
+// At most so many runs of `tokens` tokens or fewer, on any device.
 uint64_t embed_runs(uint64_t tokens, uint32_t hidden) {
-  const uint64_t few = 8192 / ceil_div(hidden, kSlab) + 1;  // while runs are short there are no more of them
-  const uint64_t runs = ceil_div(tokens, 32);
+  const uint64_t few = kMostShort / ceil_div(hidden, kSlab) + 1, runs = ceil_div(tokens, 32);
   const uint64_t most = runs > few ? runs : few, all = ceil_div(tokens, 4);
   return most < all ? most : all;
 }
@@ -849,7 +889,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams& params, int dtype, int table_
   p.present = p.accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + at.present);
   p.parts = reinterpret_cast<float*>(base + at.parts);
   p.sort_chunks = static_cast<uint32_t>(ceil_div(p.tokens, kEmbedSortChunk));
-  p.run = embed_run(p.tokens, p.hidden);
+  p.run = embed_run(p.tokens, p.hidden, dev);
   p.runs = ceil_div(p.tokens, p.run);
   p.slabs = static_cast<uint32_t>(ceil_div(p.hidden, kSlab));
   const uint32_t size = dtype == ZC_F32 || table_f32 ? 4 : 2;
