@@ -16,75 +16,107 @@ namespace zc {
 
 namespace {
 
-constexpr int kBalanceWarps = 8;
+// Warps of a CTA: 16, whose sums are half as much to add up as twice 8 warps', while shared memory
+// has room for them.  A warp takes 4 tokens where there are not too many.
+template <int N>
+constexpr int kBalanceWarps = N <= 8 ? 16 : 8;
+constexpr int kBackWarps = 8;
 
 // A row's p, from its logits in l; false, and p all zero, where no logit is above minus infinity.
-// `raw` gets the sigmoids, `inv` the reciprocal of their sum.
+// `raw` gets the exponentials or the sigmoids, `inv` the reciprocal of their sum.
 template <int N>
 __device__ __forceinline__ bool probabilities(float (&l)[N], bool sigmoid_score, float (&raw)[N], float* inv) {
-  bool open = false;
+  float best = l[0];
 #pragma unroll
-  for (int j = 0; j < N; j++) open |= l[j] != -INFINITY;
-  const bool any = __any_sync(kFull, open);
+  for (int j = 1; j < N; j++) best = fmaxf(best, l[j]);  // of those that are not NaN
+  const float top = warp_max_of(best);
   float sum = 0.f;
   if (sigmoid_score) {
 #pragma unroll
-    for (int j = 0; j < N; j++) raw[j] = l[j] == -INFINITY ? 0.f : sigmoid(l[j]);
+    for (int j = 0; j < N; j++) raw[j] = __fdividef(1.f, 1.f + expf(-l[j]));  // 1 / infinity: zero
   } else {
-    float top = l[0];
-#pragma unroll
-    for (int j = 1; j < N; j++) top = fmaxf(top, l[j]);
-    top = warp_max_f32(top);
 #pragma unroll
     for (int j = 0; j < N; j++) raw[j] = l[j] == -INFINITY ? 0.f : expf(l[j] - top);
   }
 #pragma unroll
   for (int j = 0; j < N; j++) sum += raw[j];
   sum = warp_sum_f32(sum) + (sigmoid_score ? 1e-20f : 0.f);
+  const bool any = top > -INFINITY || sum != sum;
   *inv = any ? 1.f / sum : 0.f;
 #pragma unroll
   for (int j = 0; j < N; j++) l[j] = any ? raw[j] * *inv : 0.f;
   return any;
 }
 
+// A warp's tokens first, first + step, ... below last: adds their p to acc and their slots to the CTA's
+// counts, and returns how many count.  The next token's row is on its way meanwhile, if there is room for it.
 template <typename T, int N, bool VEC>
-__global__ void __launch_bounds__(kBalanceWarps * 32) balance_kernel(BalanceParams p) {
-  __shared__ float sums[kBalanceWarps][N * 32];
-  __shared__ int32_t counts[N * 32];
-  __shared__ uint32_t counted;
-  pdl_begin();
-  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
-  for (uint32_t e = threadIdx.x; e < N * 32; e += kBalanceWarps * 32) counts[e] = 0;
-  if (threadIdx.x == 0) counted = 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
-  __syncthreads();
-  const uint64_t n = p.tokens / p.sequences, seq = blockIdx.x / p.chunks, chunk = blockIdx.x - seq * p.chunks;
-  const uint64_t last = min(n, (chunk + 1) * p.chunk_tokens);
-  float acc[N];
+__device__ __forceinline__ uint32_t add_tokens(const BalanceParams& p, uint64_t first, uint64_t last, uint32_t step,
+                                               float (&acc)[N], int32_t* counts) {
+  const uint32_t lane = lane_id();
+  float next[N];
+  int32_t next_id = -1;
+  bool next_in = false;
+  constexpr bool kAhead = N <= 8;  // more experts a lane leave no registers for it
+  auto load = [&](uint64_t t) {
+    next_in = t < last && (!p.mask || p.mask[t]);
+    if (!next_in) return;
+    load_row<T, N, VEC>(static_cast<const T*>(p.logits) + t * p.stride, p.experts, next);
+    next_id = lane < p.k ? p.ids[t * p.k + lane] : -1;
+  };
 #pragma unroll
-  for (int j = 0; j < N; j++) acc[j] = 0.f;
-  uint32_t mine = 0;
-  for (uint64_t i = chunk * p.chunk_tokens + warp; i < last; i += kBalanceWarps) {
-    const uint64_t t = seq * n + i;
-    if (p.mask && !p.mask[t]) continue;
+  for (int j = 0; j < N; j++) acc[j] = next[j] = 0.f;
+  if (kAhead) load(first);
+  uint32_t counted = 0;
+  for (uint64_t t = first; t < last; t += step) {
     float l[N], raw[N], inv;
-    load_row<T, N, VEC>(static_cast<const T*>(p.logits) + t * p.stride, p.experts, l);
-    const int32_t id = lane < p.k ? p.ids[t * p.k + lane] : -1;
-    if (!probabilities<N>(l, p.sigmoid, raw, &inv)) continue;
-    mine++;
+    if (!kAhead) load(t);
+#pragma unroll
+    for (int j = 0; j < N; j++) l[j] = next[j];
+    const int32_t id = next_id;
+    const bool in = next_in;
+    if (kAhead) load(t + step);
+    if (!in || !probabilities<N>(l, p.sigmoid, raw, &inv)) continue;
+    counted++;
 #pragma unroll
     for (int j = 0; j < N; j++) acc[j] += l[j];
     if (static_cast<uint32_t>(id) < p.experts) atomicAdd(&counts[id], 1);
   }
+  return counted;
+}
+
+__device__ __forceinline__ float slope_of(const BalanceParams& p, int32_t count, uint32_t counted) {
+  const float tokens = static_cast<float>(counted);
+  return counted ? static_cast<float>(count) * static_cast<float>(p.experts) /
+                       (static_cast<float>(p.sequences) * static_cast<float>(p.k) * tokens * tokens)
+                 : 0.f;
+}
+
+template <typename T, int N, bool VEC>
+__global__ void __launch_bounds__(kBalanceWarps<N> * 32) balance_kernel(BalanceParams p) {
+  constexpr int kWarps = kBalanceWarps<N>;
+  __shared__ float sums[kWarps][N * 32];
+  __shared__ int32_t counts[N * 32];
+  __shared__ uint32_t counted;
+  pdl_begin();
+  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
+  for (uint32_t e = threadIdx.x; e < N * 32; e += kWarps * 32) counts[e] = 0;
+  if (threadIdx.x == 0) counted = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+  __syncthreads();
+  const uint64_t n = p.tokens / p.sequences, seq = blockIdx.x / p.chunks, chunk = blockIdx.x - seq * p.chunks;
+  float acc[N];
+  const uint32_t mine = add_tokens<T, N, VEC>(p, seq * n + chunk * p.chunk_tokens + warp,
+                                              seq * n + min(n, (chunk + 1) * p.chunk_tokens), kWarps, acc, counts);
   if (lane == 0) atomicAdd(&counted, mine);
 #pragma unroll
   for (int j = 0; j < N; j++) sums[warp][lane * N + j] = acc[j];
   __syncthreads();
   const uint64_t at = static_cast<uint64_t>(blockIdx.x) * p.experts;
-  for (uint32_t e = threadIdx.x; e < p.experts; e += kBalanceWarps * 32) {
+  for (uint32_t e = threadIdx.x; e < p.experts; e += kWarps * 32) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kBalanceWarps; w++) s += sums[w][e];
+    for (int w = 0; w < kWarps; w++) s += sums[w][e];
     p.part_sums[at + e] = s;
     p.part_counts[at + e] = counts[e];
   }
@@ -92,7 +124,8 @@ __global__ void __launch_bounds__(kBalanceWarps * 32) balance_kernel(BalancePara
 }
 
 // Adds the CTAs' sums of a sequence, 32 experts a CTA (blockIdx.y): a lane an expert, the warps a
-// share of the CTAs each.  The last CTA to finish adds up the parts of the loss in order.
+// share of the CTAs each, and then a warp an expert.  The last CTA to finish adds up the parts of
+// the loss in order.
 __global__ void __launch_bounds__(1024) balance_sum_kernel(BalanceParams p) {
   __shared__ float sums[32][33];
   __shared__ int32_t counts[32][33];
@@ -103,6 +136,8 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(BalanceParams p) {
   const uint64_t seq = blockIdx.x, first = seq * p.chunks;
   const uint32_t from = static_cast<uint32_t>(static_cast<uint64_t>(p.chunks) * warp / 32),
                  to = static_cast<uint32_t>(static_cast<uint64_t>(p.chunks) * (warp + 1) / 32);
+  uint32_t n = 0;
+  for (uint32_t i = threadIdx.x; i < p.chunks; i += 1024) n += p.part_tokens[first + i];
   float s = 0.f;
   int32_t c = 0;
   if (e < p.experts) {
@@ -112,27 +147,26 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(BalanceParams p) {
       c += p.part_counts[(first + i) * p.experts + e];
     }
   }
-  uint32_t n = 0;
-  for (uint32_t i = threadIdx.x; i < p.chunks; i += 1024) n += p.part_tokens[first + i];
   n = __reduce_add_sync(kFull, n);
   sums[warp][lane] = s;
   counts[warp][lane] = c;
   if (lane == 0) tokens_of[warp] = n;
   __syncthreads();
+  // from here on warp w has expert w
+  const uint32_t mine = blockIdx.y * 32 + warp;
+  s = warp_sum_f32(sums[lane][warp]);
+  c = __reduce_add_sync(kFull, counts[lane][warp]);
+  n = __reduce_add_sync(kFull, tokens_of[lane]);
+  const float slope = slope_of(p, c, n);
+  if (lane == 0 && mine < p.experts) {
+    p.counts[seq * p.experts + mine] = c;
+    p.slope[seq * p.experts + mine] = slope;
+  }
+  __syncthreads();
+  if (lane == 0) sums[0][warp] = mine < p.experts ? slope * s : 0.f;
+  __syncthreads();
   if (warp == 0) {
-    s = 0.f, c = 0;
-#pragma unroll 8
-    for (int w = 0; w < 32; w++) s += sums[w][lane], c += counts[w][lane];
-    n = __reduce_add_sync(kFull, tokens_of[lane]);
-    const float tokens = static_cast<float>(n);
-    const float slope = n ? static_cast<float>(c) * static_cast<float>(p.experts) /
-                                (static_cast<float>(p.sequences) * static_cast<float>(p.k) * tokens * tokens)
-                          : 0.f;
-    if (e < p.experts) {
-      p.counts[seq * p.experts + e] = c;
-      p.slope[seq * p.experts + e] = slope;
-    }
-    const float part = warp_sum_f32(e < p.experts ? slope * s : 0.f);
+    const float part = warp_sum_f32(sums[0][lane]);
     if (lane == 0) {
       p.part_loss[seq * gridDim.y + blockIdx.y] = part;
       __threadfence();
@@ -147,6 +181,66 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(BalanceParams p) {
   for (uint64_t i = threadIdx.x; i < parts; i += 1024) loss[0] += __ldcg(p.part_loss + i);
   block_sum_f32<1>(loss, sums[0]);
   if (threadIdx.x == 0) *p.loss = loss[0];
+}
+
+// Few tokens in 1, 2, 4 or 8 sequences: one cluster, so one launch, 8 / sequences CTAs a sequence.  The
+// first of those adds up what the others have in shared memory.
+constexpr uint32_t kBalanceCtas = 8;
+constexpr int kClusterWarps = 32;
+template <typename T, int N, bool VEC>
+__global__ void __launch_bounds__(kClusterWarps * 32) balance_cluster_kernel(BalanceParams p) {
+  extern __shared__ float warp_sums[];  // [warps][32 N], of which the first row takes the CTA's sums
+  __shared__ int32_t counts[N * 32];
+  __shared__ uint32_t counted;
+  __shared__ float red[32];
+  __shared__ float losses[kBalanceCtas];
+  pdl_begin();
+  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, rank = blockIdx.x;
+  for (uint32_t e = threadIdx.x; e < N * 32; e += kClusterWarps * 32) counts[e] = 0;
+  if (threadIdx.x == 0) counted = 0;
+  __syncthreads();
+  const uint32_t group = kBalanceCtas / static_cast<uint32_t>(p.sequences), seq = rank / group, share = rank - seq * group;
+  const uint64_t n = p.tokens / p.sequences;
+  float acc[N];
+  const uint32_t mine = add_tokens<T, N, VEC>(p, seq * n + share * kClusterWarps + warp, (seq + 1) * n,
+                                              group * kClusterWarps, acc, counts);
+  if (lane == 0) atomicAdd(&counted, mine);
+#pragma unroll
+  for (int j = 0; j < N; j++) warp_sums[warp * (N * 32) + lane * N + j] = acc[j];
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e < p.experts; e += kClusterWarps * 32) {
+    float s = 0.f;
+#pragma unroll 8
+    for (int w = 0; w < kClusterWarps; w++) s += warp_sums[w * (N * 32) + e];
+    warp_sums[e] = s;  // read by this thread alone so far
+  }
+  cluster_arrive();
+  cluster_wait();
+  if (share == 0) {
+    uint32_t all = 0;
+    for (uint32_t r = 0; r < group; r++) all += ld_shared_of_cta(&counted, rank + r);
+    float loss[1] = {0.f};
+    for (uint32_t e = threadIdx.x; e < p.experts; e += kClusterWarps * 32) {
+      float s = 0.f;
+      int32_t c = 0;
+      for (uint32_t r = 0; r < group; r++) {
+        s += __uint_as_float(ld_shared_of_cta(reinterpret_cast<const uint32_t*>(warp_sums + e), rank + r));
+        c += static_cast<int32_t>(ld_shared_of_cta(reinterpret_cast<const uint32_t*>(counts + e), rank + r));
+      }
+      const float slope = slope_of(p, c, all);
+      p.counts[seq * p.experts + e] = c;
+      p.slope[seq * p.experts + e] = slope;
+      loss[0] = fmaf(slope, s, loss[0]);
+    }
+    block_sum_f32<1>(loss, red);
+    if (threadIdx.x == 0) st_shared_of_cta(reinterpret_cast<uint32_t*>(&losses[seq]), 0, __float_as_uint(loss[0]));
+  }
+  cluster_arrive();
+  cluster_wait();
+  if (rank || threadIdx.x) return;
+  float loss = 0.f;
+  for (uint32_t q = 0; q < p.sequences; q++) loss += losses[q];
+  *p.loss = loss;
 }
 
 // Lane l's N values of a row of the output.
@@ -173,9 +267,9 @@ __device__ __forceinline__ void store_row(T* row, uint32_t width, const float (&
 }
 
 template <typename T, int N, bool VEC>
-__global__ void __launch_bounds__(kBalanceWarps * 32) balance_bwd_kernel(BalanceBwdParams p) {
+__global__ void __launch_bounds__(kBackWarps * 32) balance_bwd_kernel(BalanceBwdParams p) {
   pdl_begin();
-  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * kBalanceWarps + (threadIdx.x >> 5);
+  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * kBackWarps + (threadIdx.x >> 5);
   if (t >= p.tokens) return;
   T* out = static_cast<T*>(p.dlogits) + t * p.experts;
   float l[N], c[N], raw[N], inv = 0.f;
@@ -204,15 +298,32 @@ __global__ void __launch_bounds__(kBalanceWarps * 32) balance_bwd_kernel(Balance
   store_row<T, N, VEC>(out, p.experts, l);
 }
 
+constexpr uint64_t kBalanceFew = 2048;  // tokens that one cluster takes, of up to 256 experts (more spill its registers)
+
 template <typename T, int N>
 cudaError_t run_width(BalanceParams& p, cudaStream_t stream) {
   constexpr uint64_t kPart = N * sizeof(T) < 16 ? N * sizeof(T) : 16;
   const bool vec = reinterpret_cast<uintptr_t>(p.logits) % kPart == 0 && p.stride * sizeof(T) % kPart == 0 &&
                    p.experts * sizeof(T) % kPart == 0;
+  void* args[] = {&p};
+  if constexpr (N <= 8) {
+    if (p.tokens <= kBalanceFew && kBalanceCtas % p.sequences == 0) {
+      static KernelPrep prep[2];
+      const void* fn = vec ? reinterpret_cast<const void*>(balance_cluster_kernel<T, N, true>)
+                           : reinterpret_cast<const void*>(balance_cluster_kernel<T, N, false>);
+      constexpr int kSmem = kClusterWarps * N * 32 * 4;
+      DeviceInfo dev;
+      int per_sm = 0;
+      cudaError_t e = device_info(&dev);
+      if (e == cudaSuccess) e = prepare_kernel(prep[vec], fn, kClusterWarps * 32, kSmem, dev, &per_sm);
+      if (e != cudaSuccess) return e;
+      return launch_kernel(fn, dim3(kBalanceCtas), dim3(kClusterWarps * 32), kSmem, stream, args, false, kBalanceCtas);
+    }
+  }
   const void* fn = vec ? reinterpret_cast<const void*>(balance_kernel<T, N, true>)
                        : reinterpret_cast<const void*>(balance_kernel<T, N, false>);
-  void* args[] = {&p};
-  cudaError_t e = launch_kernel(fn, dim3(static_cast<unsigned>(p.sequences * p.chunks)), dim3(kBalanceWarps * 32), 0,
+  cudaError_t e = launch_kernel(fn, dim3(static_cast<unsigned>(p.sequences * p.chunks)),
+                                dim3(kBalanceWarps<N> * 32), 0,
                                 stream, args, false);
   if (e != cudaSuccess) return e;
   return launch_kernel(reinterpret_cast<const void*>(balance_sum_kernel),
@@ -227,9 +338,9 @@ cudaError_t run_width(BalanceBwdParams& p, cudaStream_t stream) {
                    reinterpret_cast<uintptr_t>(p.slope) % 16 == 0;
   const void* fn = vec ? reinterpret_cast<const void*>(balance_bwd_kernel<T, N, true>)
                        : reinterpret_cast<const void*>(balance_bwd_kernel<T, N, false>);
-  const uint64_t grid = (p.tokens + kBalanceWarps - 1) / kBalanceWarps;
+  const uint64_t grid = (p.tokens + kBackWarps - 1) / kBackWarps;
   void* args[] = {&p};
-  return launch_kernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kBalanceWarps * 32), 0, stream, args, false);
+  return launch_kernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kBackWarps * 32), 0, stream, args, false);
 }
 
 template <typename T, typename P>
@@ -257,8 +368,8 @@ struct BalanceCut {
   uint32_t chunks;
   uint64_t chunk_tokens;
 };
-BalanceCut balance_cut(uint64_t tokens, uint64_t sequences) {
-  constexpr uint64_t kTokens = 4 * kBalanceWarps, kMost = 1216;
+BalanceCut balance_cut(uint64_t tokens, uint32_t experts, uint64_t sequences) {
+  const uint64_t kTokens = 4 * (experts <= 256 ? kBalanceWarps<8> : kBalanceWarps<16>), kMost = 1216;
   const uint64_t n = tokens / sequences, most = sequences < kMost ? kMost / sequences : 1;
   uint64_t each = (n + most - 1) / most;
   each = each < kTokens ? kTokens : each;
@@ -269,13 +380,13 @@ BalanceCut balance_cut(uint64_t tokens, uint64_t sequences) {
 }  // namespace
 
 uint64_t balance_workspace_bytes(uint64_t tokens, uint32_t experts, uint64_t sequences) {
-  const uint64_t units = sequences * balance_cut(tokens, sequences).chunks;
+  const uint64_t units = sequences * balance_cut(tokens, experts, sequences).chunks;
   return 16 + 4 * (2 * units * experts + units + sequences * ((experts + 31) / 32));
 }
 
 cudaError_t launch_balance(const BalanceParams& params, int dtype, void* ws, cudaStream_t stream) {
   BalanceParams p = params;
-  const BalanceCut cut = balance_cut(p.tokens, p.sequences);
+  const BalanceCut cut = balance_cut(p.tokens, p.experts, p.sequences);
   p.chunks = cut.chunks;
   p.chunk_tokens = cut.chunk_tokens;
   const uint64_t units = p.sequences * p.chunks;

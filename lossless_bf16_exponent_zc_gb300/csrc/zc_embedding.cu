@@ -63,7 +63,7 @@ struct AnyValues {
 // A thread takes UNITS 16-byte pieces of the output, kEmbedThreads apart, all loads before the first
 // store.
 template <typename T, typename TT, int UNITS>
-__global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedParams p, Divisor pieces) {
+__global__ void __launch_bounds__(kEmbedThreads, 8) embed_kernel(EmbedParams p, Divisor pieces) {
   constexpr int V = kPieceOf<T>;
   pdl_begin();
   const uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads * UNITS);
@@ -713,7 +713,7 @@ cudaError_t lookup(EmbedParams& p, bool vec, cudaStream_t stream, const DeviceIn
   if (all <= 2ull * kEmbedThreads * static_cast<uint64_t>(dev.sm_count))
     return run(reinterpret_cast<const void*>(embed_kernel<T, TT, 1>), ceil_div(all, kEmbedThreads), kEmbedThreads, 0,
                stream, args);
-  return run(reinterpret_cast<const void*>(embed_kernel<T, TT, 4>), ceil_div(all, 4 * kEmbedThreads), kEmbedThreads, 0,
+  return run(reinterpret_cast<const void*>(embed_kernel<T, TT, 2>), ceil_div(all, 2 * kEmbedThreads), kEmbedThreads, 0,
              stream, args);
 }
 

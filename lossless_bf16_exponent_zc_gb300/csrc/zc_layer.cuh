@@ -249,6 +249,13 @@ struct Divisor {
   __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return d == 1 ? n : __umulhi(n, mul) >> shift; }
 };
 
+// The largest of the warp's values that are not NaN.
+__device__ __forceinline__ float warp_max_of(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Thread-block clusters: the barrier of all threads of the cluster in its two halves (release,
 // acquire), and a store to the same variable in the shared memory of the cluster's CTA `cta`.
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -264,6 +271,16 @@ __device__ __forceinline__ void st_shared_of_cta(uint32_t* var, uint32_t cta, ui
           smem_u32(var)),
       "r"(cta), "r"(v)
       : "memory");
+}
+
+// The same variable of the cluster's CTA `cta`.
+__device__ __forceinline__ uint32_t ld_shared_of_cta(const uint32_t* var, uint32_t cta) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.u32 %0, [a];\n\t}"
+               : "=r"(v)
+               : "r"(smem_u32(var)), "r"(cta)
+               : "memory");
+  return v;
 }
 
 // Sums of N values over a CTA of whole warps, every thread getting all of them.  `red` holds N x 32

@@ -36,13 +36,6 @@ __device__ __forceinline__ float tanh_estimate(float x) {
   return y;
 }
 
-// The largest of the warp's values, none of them NaN.
-__device__ __forceinline__ float warp_max_of(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // An expert's choice: its logit, or its sigmoid plus its bias; minus infinity if it is closed.
 __device__ __forceinline__ float choice_of(const RouteParams& p, float l, uint32_t e, float* prob) {
   if (!p.sigmoid || l == -INFINITY) return l;
