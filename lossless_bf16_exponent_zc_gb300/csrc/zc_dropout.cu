@@ -76,92 +76,114 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(DropoutParams p, 
   }
 }
 
-// 8 values at p, which lies anywhere, as the pieces that hold them.
-template <typename T>
+// 8 values at p, which lies anywhere (or, with ALIKE, on a piece), as the pieces that hold them.
+template <typename T, bool ALIKE>
 struct AnyEight {
   static constexpr int NP = 8 / kPieceOf<T>;
-  uint4 w[NP + 1];
+  uint4 w[ALIKE ? NP : NP + 1];
   uint32_t off;
   __device__ __forceinline__ void load(const T* p) {
-    off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
+    off = ALIKE ? 0 : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
     const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
 #pragma unroll
     for (int k = 0; k < NP; k++) w[k] = from[k];
-    w[NP] = off ? from[NP] : make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (!ALIKE) w[NP] = off ? from[NP] : make_uint4(0u, 0u, 0u, 0u);
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     constexpr int V = kPieceOf<T>;
 #pragma unroll
     for (int k = 0; k < NP; k++) {
       float v[V];
-      Piece<T, V>{shift_pieces<T>(w[k], w[k + 1], off)}.get(v);
+      if constexpr (ALIKE)
+        Piece<T, V>{w[k]}.get(v);
+      else
+        Piece<T, V>{shift_pieces<T>(w[k], w[k + 1], off)}.get(v);
 #pragma unroll
       for (int j = 0; j < V; j++) f[k * V + j] = v[j];
     }
   }
 };
 
-// Rows off 16 bytes.  A warp takes 31 units of a row of the output: eight columns from an aligned
-// piece on, or a column outside those (the ones behind the last piece, then the ones before the
-// first).  Eight such columns lie in two of the generator's groups: every lane draws one and takes
-// the second from the lane above, the last lane drawing for its neighbour alone.
+// Rows off 16 bytes.  A warp takes TURNS times 31 units of a row of the output: eight columns from an
+// aligned piece on, or a column outside those (the ones behind the last piece, then the ones before
+// the first).  Eight such columns lie in two of the generator's groups: every lane draws one and
+// takes the second from the lane above, through shared memory, the last lane drawing for its
+// neighbour alone.  ALIKE: the
+// rows of all matrices start equally far into a piece.
 constexpr uint32_t kDropAnyUnits = 31;
-template <typename T, bool RESIDUAL>
-__global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(DropoutParams p, uint32_t shares) {
+template <typename T, bool RESIDUAL, bool ALIKE, int TURNS>
+__global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(DropoutParams p, Divisor shares) {
   constexpr int V = kPieceOf<T>, NP = 8 / V;
+  __shared__ uint4 groups_of[kDropThreads / 32][TURNS][33];  // the last is only read past the others
   pdl_begin();
   const KeepRng rng(p.drop);
   const bool drops = p.drop.limit != 0;
-  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kDropThreads / 32) + (threadIdx.x >> 5), t = i / shares;
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kDropThreads / 32) + (threadIdx.x >> 5);
+  const uint64_t t = i >> 31 ? i / shares.d : shares(static_cast<uint32_t>(i));
   if (t >= p.tokens) return;
-  const uint32_t u = static_cast<uint32_t>(i - t * shares) * kDropAnyUnits + lane_id();
+  const uint32_t lane = lane_id();
+  const uint32_t u0 = static_cast<uint32_t>(i - t * shares.d) * (TURNS * kDropAnyUnits) + lane;
   T* out = static_cast<T*>(p.out) + t * p.width;
   const T* x = static_cast<const T*>(p.x) + t * p.x_stride;
   const T* r = RESIDUAL ? static_cast<const T*>(p.residual) + t * p.residual_stride : nullptr;
   uint32_t head = static_cast<uint32_t>((16 - (reinterpret_cast<uintptr_t>(out) & 15)) & 15) / sizeof(T);
   head = head < p.width ? head : p.width;
-  const uint32_t body = (p.width - head) / 8, tail = p.width - head - body * 8;
-  const bool whole = u < body && lane_id() < kDropAnyUnits;
   // behind the last piece one unit at the least, which draws the group of that piece's last columns
-  const uint32_t behind = tail ? tail : 1, e = u - body;
-  const bool last = u >= body && e >= behind;
-  const uint32_t col = last ? e - behind : head + body * 8 + (u < body ? (u - body) * 8 : e);
-  const bool single = u >= body && lane_id() < kDropAnyUnits && (last ? col < head : e < tail);
-  AnyEight<T> xs, rs;
-  if (whole) {
-    xs.load(x + col);
-    if (RESIDUAL) rs.load(r + col);
+  const uint32_t body = (p.width - head) / 8, tail = p.width - head - body * 8, behind = tail ? tail : 1;
+  uint32_t col[TURNS], row[TURNS], group[TURNS];
+  bool whole[TURNS], single[TURNS];
+  AnyEight<T, ALIKE> xs[TURNS], rs[TURNS];
+#pragma unroll
+  for (int q = 0; q < TURNS; q++) {
+    const uint32_t u = u0 + q * kDropAnyUnits, e = u - body;
+    const bool in_front = u >= body && e >= behind;
+    col[q] = in_front ? e - behind : head + body * 8 + (u < body ? (u - body) * 8 : e);
+    whole[q] = u < body && lane < kDropAnyUnits;
+    single[q] = u >= body && lane < kDropAnyUnits && (in_front ? col[q] < head : e < tail);
+    row[q] = static_cast<uint32_t>(t);
+    group[q] = col[q] / 8;
+    if (whole[q]) {
+      xs[q].load(x + col[q]);
+      if (RESIDUAL) rs[q].load(r + col[q]);
+    }
   }
-  const uint4 own = rng.group(static_cast<uint32_t>(t), col / 8);
-  uint4 above;
-  above.x = __shfl_down_sync(kFull, own.x, 1);
-  above.y = __shfl_down_sync(kFull, own.y, 1);
-  above.z = __shfl_down_sync(kFull, own.z, 1);
-  above.w = __shfl_down_sync(kFull, own.w, 1);
-  if (whole) {
-    const uint4 g = shift_pieces<__half>(own, above, (col & 7) * 2);
-    const uint32_t bits[4] = {g.x, g.y, g.z, g.w};
-    float f[8], o[8];
-    xs.get(f);
-    if (drops) rng.template apply<8>(f, bits);
-    if (RESIDUAL) {
-      rs.get(o);
+  uint4 g[TURNS];
 #pragma unroll
-      for (int j = 0; j < 8; j++) f[j] = fmaf(p.residual_scale, o[j], f[j]);
+  for (int q = 0; q < TURNS; q++) g[q] = make_uint4(0u, 0u, 0u, 0u);
+  if (drops) rng.template groups<TURNS>(row, group, g);
+  uint4(*runs)[33] = groups_of[threadIdx.x >> 5];
+#pragma unroll
+  for (int q = 0; q < TURNS; q++) runs[q][lane] = g[q];
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < TURNS; q++) {
+    uint32_t bits[4];  // of eight columns, which start head columns into the lane's group
+    load_bits<4>(reinterpret_cast<const uint32_t*>(runs[q]), lane * 8 + (head & 7), bits);
+    if (single[q]) {
+      float f = to_f32<T>(x[col[q]]);
+      if (drops) f = rng.keeps(g[q], col[q] & 7) ? f * rng.factor : 0.f;
+      if (RESIDUAL) f = fmaf(p.residual_scale, to_f32<T>(r[col[q]]), f);
+      out[col[q]] = from_f32<T>(f);
     }
+    if (whole[q]) {
+      float f[8], o[8];
+      xs[q].get(f);
+      if (drops) rng.template apply<8>(f, bits);
+      if (RESIDUAL) {
+        rs[q].get(o);
 #pragma unroll
-    for (int k = 0; k < NP; k++) {
-      float v[V];
+        for (int j = 0; j < 8; j++) f[j] = fmaf(p.residual_scale, o[j], f[j]);
+      }
 #pragma unroll
-      for (int j = 0; j < V; j++) v[j] = f[k * V + j];
-      Piece<T, V> piece;
-      piece.set(v);
-      piece.store(out + col + k * V);
+      for (int k = 0; k < NP; k++) {
+        float v[V];
+#pragma unroll
+        for (int j = 0; j < V; j++) v[j] = f[k * V + j];
+        Piece<T, V> piece;
+        piece.set(v);
+        piece.store(out + col[q] + k * V);
+      }
     }
-  } else if (single) {
-    float f = !drops ? to_f32<T>(x[col]) : rng.keeps(own, col & 7) ? to_f32<T>(x[col]) * rng.factor : 0.f;
-    if (RESIDUAL) f = fmaf(p.residual_scale, to_f32<T>(r[col]), f);
-    out[col] = from_f32<T>(f);
   }
 }
 
@@ -181,11 +203,22 @@ cudaError_t run(DropoutParams& p, bool vec, cudaStream_t stream) {
                        : reinterpret_cast<const void*>(dropout_kernel<T, kUnits, RESIDUAL, false>),
                   (p.tokens * groups.d + kDropThreads * kUnits - 1) / (kDropThreads * kUnits), stream, args);
   }
-  // at most 7 columns on either side of the pieces
-  uint32_t shares = (p.width / 8 + 14 + kDropAnyUnits - 1) / kDropAnyUnits;
+  const auto base = [](const void* q) { return reinterpret_cast<uintptr_t>(q) & 15; };
+  const auto apart = [](uint64_t stride) { return stride * sizeof(T) & 15; };
+  const bool alike = base(p.x) == base(p.out) && apart(p.x_stride) == apart(p.width) &&
+                     (!RESIDUAL || (base(p.residual) == base(p.out) && apart(p.residual_stride) == apart(p.width)));
+  // at most 7 columns on either side of the pieces; two turns a warp where the rows have them
+  const uint32_t units = p.width / 8 + 14, turns = units > kDropAnyUnits ? 2 : 1;
+  Divisor shares((units + turns * kDropAnyUnits - 1) / (turns * kDropAnyUnits));
+  const void* fn;
+  if (turns == 2)
+    fn = alike ? reinterpret_cast<const void*>(dropout_any_kernel<T, RESIDUAL, true, 2>)
+               : reinterpret_cast<const void*>(dropout_any_kernel<T, RESIDUAL, false, 2>);
+  else
+    fn = alike ? reinterpret_cast<const void*>(dropout_any_kernel<T, RESIDUAL, true, 1>)
+               : reinterpret_cast<const void*>(dropout_any_kernel<T, RESIDUAL, false, 1>);
   void* args[] = {&p, &shares};
-  return launch(reinterpret_cast<const void*>(dropout_any_kernel<T, RESIDUAL>),
-                (p.tokens * shares + kDropThreads / 32 - 1) / (kDropThreads / 32), stream, args);
+  return launch(fn, (p.tokens * shares.d + kDropThreads / 32 - 1) / (kDropThreads / 32), stream, args);
 }
 
 template <typename T>

@@ -9,6 +9,8 @@
 // probability, so that the mean stays the same.
 #pragma once
 
+#include <type_traits>
+
 #include "zc_internal.h"
 #include "zc_layer.cuh"
 
@@ -77,97 +79,125 @@ struct KeepRng {
   // Drops out the V values of a row from column `col` on, a multiple of V.
   template <int V>
   __device__ __forceinline__ void apply(float (&v)[V], uint32_t row, uint32_t col) const {
-    static_assert(V == 1 || V == 4 || V == 8, "a part of a group");
+    static_assert(V == 4 || V == 8, "a part of a group");
     const uint4 g = group(row, col / 8);
     if constexpr (V == 8) {
       const uint32_t w[4] = {g.x, g.y, g.z, g.w};
       apply<8>(v, w);
-    } else if constexpr (V == 4) {
+    } else {
       const uint32_t w[2] = {col & 4 ? g.z : g.x, col & 4 ? g.w : g.y};
       apply<4>(v, w);
-    } else {
-      v[0] = keeps(g, col & 7) ? v[0] * factor : 0.f;
     }
   }
+  // Values taken one by one: the bits of a row of `width` columns into shared memory (16-byte aligned,
+  // `width` rounded up to whole groups), by the threads `me` of `step`; and one value by them.
+  __device__ __forceinline__ void bits_of_row(uint16_t* bits, uint32_t row, uint32_t width, uint32_t me,
+                                              uint32_t step) const {
+    for (uint32_t c = me; c * 8 < width; c += step) *reinterpret_cast<uint4*>(bits + c * 8) = group(row, c);
+  }
+  __device__ __forceinline__ float apply(float v, uint16_t bits) const {
+    return keeps_low(bits) ? v * factor : 0.f;
+  }
 };
+
+// 2 W 16-bit values from value `first` on of a run of them in shared memory (4-byte aligned, and the word
+// behind them may be read).
+template <int W>
+__device__ __forceinline__ void load_bits(const uint32_t* run, uint32_t first, uint32_t (&bits)[W]) {
+  uint32_t w[W + 1];
+#pragma unroll
+  for (int j = 0; j <= W; j++) w[j] = run[first / 2 + j];
+#pragma unroll
+  for (int j = 0; j < W; j++) bits[j] = __funnelshift_r(w[j], w[j + 1], (first & 1) * 16);
+}
 
 // The same for a thread's columns of a ring of rows (RowRing, zc_norm.cuh): NV pieces of V, piece me +
 // i threads, each starting `lead` columns early, V / 2 words of bits a piece; `threads` is a multiple
 // of 32.  No group is drawn twice where that can be helped: a piece of four columns is half a group,
 // so of two neighbouring lanes each draws for one of two pieces and they trade halves; and a piece
-// that starts early takes the bits of the piece before it from the lane below.  What lane 0 needs
-// from the warp below it draws itself, the 32 lanes for the next 32 rows at once.
+// that starts early takes the bits of the piece before it from the lane below, through shared memory.
+// What lane 0 needs from the warp below it draws itself, the 32 lanes for the next 32 rows at once.
+// `smem`: keep_bytes(threads) with SHIFT, 16-byte aligned; a barrier of the warp or the CTA has to lie
+// between two rows.
 template <int V, int NV, bool SHIFT>
 struct KeepColumns {
   static constexpr int W = V / 2;
+  using Words = typename std::conditional<V == 8, uint4, uint2>::type;
   KeepRng rng;
-  uint32_t me, threads, first_group, lead;
-  uint32_t edge[SHIFT ? NV : 1][W];  // of the piece before lane 0's, of the lane's row of 32
+  uint32_t me, threads, lead;
   uint32_t turn = 0;
-  __device__ __forceinline__ KeepColumns(const Dropout& d, uint32_t me_, uint32_t threads_, uint32_t first,
-                                         uint32_t lead_)
-      : rng(d), me(me_), threads(threads_), first_group(first / 8), lead(lead_) {}
+  // Of this warp, for every piece: what lies before lane 0's, those of the lanes, one for reading past
+  // them, and those before lane 0's of 32 rows.
+  static constexpr int kSlots = 66;
+  Words* slots;
+  __host__ __device__ static constexpr int keep_bytes(int threads) {
+    return SHIFT ? threads / 32 * kSlots * NV * static_cast<int>(sizeof(Words)) : 0;
+  }
+  __device__ __forceinline__ KeepColumns(const Dropout& d, uint32_t me_, uint32_t threads_, uint32_t lead_, void* smem)
+      : rng(d), me(me_), threads(threads_), lead(lead_), slots(static_cast<Words*>(smem) + (me_ / 32) * (kSlots * NV)) {}
+
+  // What lies before lane 0's pieces, for 32 rows.  Inlined it would take the registers that the rounds'
+  // keys stay in.
+  __device__ __noinline__ static void draw_before(KeepRng rng, uint32_t row, uint32_t step, uint32_t me,
+                                                  uint32_t threads, Words* slots) {
+    const uint32_t lane = lane_id();
+    for (int i = 0; i < NV; i++) {
+      const uint32_t piece = me - lane + i * threads - 1;  // of 8 or 4 columns; it may lie before the row
+      const uint4 g = rng.group(row + lane * step, V == 8 ? piece : piece / 2);
+      if constexpr (V == 8)
+        slots[i * kSlots + 34 + lane] = g;
+      else
+        slots[i * kSlots + 34 + lane] = make_uint2(g.z, g.w);  // a half before an even piece is a second one
+    }
+  }
 
   // Draws the bits of row `row`, to be followed by row + step.
   __device__ __forceinline__ void draw(uint32_t row, uint32_t step, uint32_t (&bits)[NV][W]) {
     const uint32_t lane = lane_id();
-    uint32_t own[NV][W];
     if constexpr (V == 8) {
       uint4 g[NV];
       uint32_t rows[NV], at[NV];
 #pragma unroll
-      for (int i = 0; i < NV; i++) rows[i] = row, at[i] = first_group + me + i * threads;
+      for (int i = 0; i < NV; i++) rows[i] = row, at[i] = me + i * threads;
       rng.template groups<NV>(rows, at, g);
 #pragma unroll
-      for (int i = 0; i < NV; i++) own[i][0] = g[i].x, own[i][1] = g[i].y, own[i][2] = g[i].z, own[i][3] = g[i].w;
+      for (int i = 0; i < NV; i++) bits[i][0] = g[i].x, bits[i][1] = g[i].y, bits[i][2] = g[i].z, bits[i][3] = g[i].w;
     } else {
       static_assert(V == 4 && NV % 2 == 0, "pairs of pieces");
       const bool odd = lane & 1;
+      uint4 g[NV / 2];
+      uint32_t rows[NV / 2], at[NV / 2];
+#pragma unroll
+      for (int i = 0; i < NV; i += 2) rows[i / 2] = row, at[i / 2] = (me + (odd ? i + 1 : i) * threads) / 2;
+      rng.template groups<NV / 2>(rows, at, g);
 #pragma unroll
       for (int i = 0; i < NV; i += 2) {
-        const uint4 g = rng.group(row, first_group + (me + (odd ? i + 1 : i) * threads) / 2);
-        const uint32_t a = __shfl_xor_sync(kFull, odd ? g.x : g.z, 1), b = __shfl_xor_sync(kFull, odd ? g.y : g.w, 1);
-        own[i][0] = odd ? a : g.x, own[i][1] = odd ? b : g.y;
-        own[i + 1][0] = odd ? g.z : a, own[i + 1][1] = odd ? g.w : b;
+        const uint4 w = g[i / 2];
+        const uint32_t a = __shfl_xor_sync(kFull, odd ? w.x : w.z, 1), b = __shfl_xor_sync(kFull, odd ? w.y : w.w, 1);
+        bits[i][0] = odd ? a : w.x, bits[i][1] = odd ? b : w.y;
+        bits[i + 1][0] = odd ? w.z : a, bits[i + 1][1] = odd ? w.w : b;
       }
     }
-    if constexpr (!SHIFT) {
-#pragma unroll
-      for (int i = 0; i < NV; i++)
-#pragma unroll
-        for (int j = 0; j < W; j++) bits[i][j] = own[i][j];
-    } else {
+    if constexpr (SHIFT) {
+      if (lead == 0) return;
       if (turn == 0) {
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-          const uint32_t piece = me - lane + i * threads - 1;  // of 8 or 4 columns; it may lie before the row
-          const uint4 g = rng.group(row + lane * step, V == 8 ? piece : piece / 2);
-          edge[i][0] = V == 8 ? g.x : g.z;  // a half before an even piece is a second one
-          edge[i][1] = V == 8 ? g.y : g.w;
-          if constexpr (V == 8) edge[i][2] = g.z, edge[i][3] = g.w;
-        }
+        draw_before(rng, row, step, me, threads, slots);
+        __syncwarp();
       }
 #pragma unroll
       for (int i = 0; i < NV; i++) {
-        uint32_t before[W];
-#pragma unroll
-        for (int j = 0; j < W; j++) {
-          before[j] = __shfl_up_sync(kFull, own[i][j], 1);
-          const uint32_t e = __shfl_sync(kFull, edge[i][j], turn);
-          before[j] = lane ? before[j] : e;
-        }
-        uint4 w;
-        if constexpr (V == 8)  // 0 .. 7 columns early
-          w = lead ? shift_pieces<__half>(make_uint4(before[0], before[1], before[2], before[3]),
-                                          make_uint4(own[i][0], own[i][1], own[i][2], own[i][3]), 16 - 2 * lead)
-                   : make_uint4(own[i][0], own[i][1], own[i][2], own[i][3]);
+        Words* run = slots + i * kSlots;
+        if (lane == 0) run[0] = run[34 + turn];
+        if constexpr (V == 8)
+          run[1 + lane] = make_uint4(bits[i][0], bits[i][1], bits[i][2], bits[i][3]);
         else
-          w = shift_pieces<__half>(make_uint4(before[0], before[1], own[i][0], own[i][1]), make_uint4(0u, 0u, 0u, 0u),
-                                   8 - 2 * lead);
-        bits[i][0] = w.x, bits[i][1] = w.y;
-        if constexpr (V == 8) bits[i][2] = w.z, bits[i][3] = w.w;
+          run[1 + lane] = make_uint2(bits[i][0], bits[i][1]);
       }
+      __syncwarp();
       turn = (turn + 1) & 31;
+#pragma unroll
+      for (int i = 0; i < NV; i++)
+        load_bits<W>(reinterpret_cast<const uint32_t*>(slots + i * kSlots), (1 + lane) * V - lead, bits[i]);
     }
   }
   // Drops out the thread's columns of a row.

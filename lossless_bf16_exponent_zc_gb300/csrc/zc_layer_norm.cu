@@ -15,10 +15,13 @@ namespace {
 // Rows held in registers, NV pieces a thread: by a warp (WARP), or by a CTA.
 template <typename T, int V, int NV, bool WARP, bool BRANCH, bool DROP, int THREADS>
 __global__ void __launch_bounds__(THREADS) layer_norm_kernel(LayerNormParams p) {
+  constexpr bool kBits = DROP && V == 1;  // values one by one: a row's bits lie in shared memory
   __shared__ float red[2][32];
+  __shared__ __align__(16) uint16_t bits_of[kBits ? NV * THREADS : 8];
   pdl_begin();
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
   const uint32_t me = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
+  uint16_t* bits = bits_of + (kBits && WARP ? warp * (NV * 32) : 0);
   const uint32_t pieces = p.hidden / V;
   const float inv_d = 1.f / static_cast<float>(p.hidden);
   const uint64_t rows_a_turn = WARP ? static_cast<uint64_t>(gridDim.x) * kNormWarps : gridDim.x;
@@ -31,6 +34,14 @@ __global__ void __launch_bounds__(THREADS) layer_norm_kernel(LayerNormParams p) 
   for (uint64_t t = WARP ? static_cast<uint64_t>(blockIdx.x) * kNormWarps + warp : blockIdx.x; t < p.tokens;
        t += rows_a_turn) {
     float n[NV][V], sum = 0.f;
+    if constexpr (kBits) {
+      if (WARP) __syncwarp();  // the row before has been read (a CTA's sums lie in between)
+      KeepRng(p.drop).bits_of_row(bits, static_cast<uint32_t>(t), p.hidden, me, step);
+      if (WARP)
+        __syncwarp();
+      else
+        __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       const uint32_t c = me + i * step;
@@ -42,7 +53,10 @@ __global__ void __launch_bounds__(THREADS) layer_norm_kernel(LayerNormParams p) 
       if (BRANCH) {
         float y[V];
         Piece<T, V>::load(static_cast<const T*>(p.y) + t * p.y_stride + at).get(y);
-        if (DROP) KeepRng(p.drop).template apply<V>(y, static_cast<uint32_t>(t), c * V);
+        if constexpr (kBits)
+          y[0] = KeepRng(p.drop).apply(y[0], bits[c]);
+        else if constexpr (DROP)
+          KeepRng(p.drop).template apply<V>(y, static_cast<uint32_t>(t), c * V);
 #pragma unroll
         for (int j = 0; j < V; j++) n[i][j] = fmaf(p.residual_scale, n[i][j], y[j]);
         Piece<T, V> out;
@@ -131,7 +145,7 @@ __global__ void __launch_bounds__(kNormRingThreads, C == 8 ? 2 : 1) layer_norm_r
   __syncthreads();
   if (threadIdx.x < 16) red[0][threadIdx.x] = make_float2(0.f, 0.f);
   __syncthreads();
-  ColumnsOf<V, C / V, SHIFT, DROP> keep(p.drop, threadIdx.x, blockDim.x, 0, lead);
+  ColumnsOf<V, C / V, SHIFT, DROP> keep(p.drop, threadIdx.x, blockDim.x, lead, ring_smem + Ring::bytes(blockDim.x));
   int stage = 0, turn = 0;
   for (uint64_t t = walker; t < p.tokens; t += walkers) {
     float2 x[P];
@@ -200,9 +214,13 @@ template <typename T, int C, bool SHIFT, bool BRANCH, bool DROP>
 cudaError_t run_ring(LayerNormParams& p, int threads, uint64_t period, cudaStream_t stream, const DeviceInfo& dev) {
   static RingPrep prep;
   constexpr int V = kPieceOf<T>;
-  const int smem = static_cast<int>(RowRing<T, V, C, BRANCH ? 2 : 1, kLayerStages<C, BRANCH>>::bytes(threads));
+  const int smem = static_cast<int>(RowRing<T, V, C, BRANCH ? 2 : 1, kLayerStages<C, BRANCH>>::bytes(threads)) +
+                   ColumnsOf<V, C / V, SHIFT, DROP>::keep_bytes(threads);
   const void* fn = reinterpret_cast<const void*>(layer_norm_ring_kernel<T, V, C, SHIFT, BRANCH, DROP>);
-  static_assert(kLayerStages<C, BRANCH> * (BRANCH ? 2 : 1) * kNormRingThreads * C * sizeof(T) <= kNormRingSmem, "shared memory");
+  static_assert(kLayerStages<C, BRANCH> * (BRANCH ? 2 : 1) * kNormRingThreads * C * sizeof(T) +
+                        ColumnsOf<V, C / V, SHIFT, DROP>::keep_bytes(kNormRingThreads) <=
+                    kNormRingSmem,
+                "a CTA's shared memory");
   int fit = 0;
   cudaError_t e = prepare_ring(prep, fn, threads, smem, dev, 1, &fit);
   if (e != cudaSuccess) return e;
@@ -231,12 +249,11 @@ template <typename T, int V>
 cudaError_t run_width(LayerNormParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   const uint32_t d = p.hidden;
   constexpr int kWarp = kNormWarps * 32;
+  // A warp holds up to 256 values (65536 x 256 bf16 with dropout 29 us, by the ring 37; from 512 on the
+  // ring's 49 us beat a warp's 51, and 16384 x 1024 24 beat 36).
   if (d <= 256) return run_shape<T, V, 8 / V, true, kWarp>(p, kWarp, stream, dev);
-  if (d <= 512) return run_shape<T, V, 16 / V, true, kWarp>(p, kWarp, stream, dev);
   cudaError_t e;
   if constexpr (V > 1) {
-    if (d <= 1024 && p.tokens >= 16ull * static_cast<uint64_t>(dev.sm_count))
-      return run_shape<T, V, 32 / V, true, kWarp>(p, kWarp, stream, dev);
     if (run_ring<T, kLayerCols<T>, false>(p, stream, dev, &e)) return e;
     if constexpr (kLayerCols<T> != kLayerWideCols) {
       if (run_ring<T, kLayerWideCols, false>(p, stream, dev, &e)) return e;

@@ -1,8 +1,6 @@
 // zc_layer_norm.cuh -- what the layer norms' forward and backward kernels share.
 #pragma once
 
-#include <type_traits>
-
 #include "zc_dropout.cuh"
 #include "zc_norm.cuh"
 
@@ -71,7 +69,8 @@ __device__ __forceinline__ void cta_sum_pair(float& a, float& b, float* red) {
 
 // In place of a dropout's columns where there is none.
 struct NoColumns {
-  __device__ __forceinline__ NoColumns(const Dropout&, uint32_t, uint32_t, uint32_t, uint32_t) {}
+  __host__ __device__ static constexpr int keep_bytes(int) { return 0; }
+  __device__ __forceinline__ NoColumns(const Dropout&, uint32_t, uint32_t, uint32_t, void*) {}
 };
 template <int V, int NV, bool SHIFT, bool DROP>
 using ColumnsOf = typename std::conditional<DROP, KeepColumns<V, NV, SHIFT>, NoColumns>::type;

@@ -15,7 +15,9 @@ namespace {
 // registers until the end.
 template <typename T, int V, int NV, bool DROP, int THREADS>
 __global__ void __launch_bounds__(THREADS) layer_norm_bwd_kernel(LayerNormBwdParams p) {
+  constexpr bool kBits = DROP && V == 1;  // values one by one: a row's bits lie in shared memory
   __shared__ float red[2][2 * 32];
+  __shared__ __align__(16) uint16_t bits[kBits ? NV * THREADS : 8];
   pdl_begin();
   const uint32_t me = threadIdx.x, step = blockDim.x, pieces = p.hidden / V;
   const float inv_d = 1.f / static_cast<float>(p.hidden);
@@ -49,6 +51,10 @@ __global__ void __launch_bounds__(THREADS) layer_norm_bwd_kernel(LayerNormBwdPar
     }
     block_sum_f32<2>(sums, red[turn]);
     turn ^= 1;
+    if constexpr (kBits) {  // read before the next row's sums
+      KeepRng(p.drop).bits_of_row(bits, static_cast<uint32_t>(t), p.hidden, me, step);
+      __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       const uint32_t c = me + i * step;
@@ -67,7 +73,10 @@ __global__ void __launch_bounds__(THREADS) layer_norm_bwd_kernel(LayerNormBwdPar
       out.set(o);
       out.store(static_cast<T*>(p.dx) + t * p.hidden + at);
       if (p.dy) {
-        if (DROP) KeepRng(p.drop).template apply<V>(g, static_cast<uint32_t>(t), c * V);
+        if constexpr (kBits)
+          g[0] = KeepRng(p.drop).apply(g[0], bits[c]);
+        else if constexpr (DROP)
+          KeepRng(p.drop).template apply<V>(g, static_cast<uint32_t>(t), c * V);
         out.set(g);
         out.store(static_cast<T*>(p.dy) + t * p.hidden + at);
       }
@@ -123,7 +132,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) layer_norm_bwd_ring_kerne
 #pragma unroll
   for (int i = 0; i < P; i++) dw[i] = db[i] = splat(0.f);
   const InRow<V, C, SHIFT, Ring> in_row(ring);
-  ColumnsOf<V, C / V, SHIFT, DROP> keep(p.drop, threadIdx.x, blockDim.x, 0, lead);
+  ColumnsOf<V, C / V, SHIFT, DROP> keep(p.drop, threadIdx.x, blockDim.x, lead, ring_smem + Ring::bytes(blockDim.x));
   const float2* stats = reinterpret_cast<const float2*>(p.stats);
   float2 of_row = stats[walker];
   int stage = 0, turn = 0;
@@ -199,9 +208,12 @@ constexpr uint32_t kLayerWarpWidth = 256;
 template <typename T, int V, bool DROP>
 __global__ void __launch_bounds__(kNormWarps * 32) layer_norm_bwd_warp_kernel(LayerNormBwdParams p) {
   constexpr int NV = 8 / V;
+  constexpr bool kBits = DROP && V == 1;  // values one by one: a row's bits lie in shared memory
   __shared__ float tile[kNormWarps][kLayerWarpWidth];
+  __shared__ __align__(16) uint16_t bits_of[kNormWarps][kBits ? kLayerWarpWidth : 8];
   pdl_begin();
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, pieces = p.hidden / V;
+  uint16_t* bits = bits_of[warp];
   const float inv_d = 1.f / static_cast<float>(p.hidden);
   const uint64_t walkers = static_cast<uint64_t>(gridDim.x) * kNormWarps;
   float w[NV][V], dw[NV][V], db[NV][V];
@@ -247,6 +259,11 @@ __global__ void __launch_bounds__(kNormWarps * 32) layer_norm_bwd_warp_kernel(La
         b = fmaf(u[i][j], n[i][j], b);
       }
     }
+    if constexpr (kBits) {
+      __syncwarp();  // the row before has been read
+      KeepRng(p.drop).bits_of_row(bits, static_cast<uint32_t>(t), p.hidden, lane, 32);
+      __syncwarp();
+    }
     a = warp_sum_f32(a) * inv_d;
     b = warp_sum_f32(b) * inv_d;
 #pragma unroll
@@ -265,7 +282,10 @@ __global__ void __launch_bounds__(kNormWarps * 32) layer_norm_bwd_warp_kernel(La
       out.set(o);
       out.store(static_cast<T*>(p.dx) + at);
       if (!p.dy) continue;
-      if (DROP) KeepRng(p.drop).template apply<V>(g, static_cast<uint32_t>(t), c * V);
+      if constexpr (kBits)
+        g[0] = KeepRng(p.drop).apply(g[0], bits[c]);
+      else if constexpr (DROP)
+        KeepRng(p.drop).template apply<V>(g, static_cast<uint32_t>(t), c * V);
       out.set(g);
       out.store(static_cast<T*>(p.dy) + at);
     }
@@ -348,12 +368,16 @@ bool run_ring(LayerNormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev,
   constexpr int V = kPieceOf<T>;
   const int threads = static_cast<int>((p.hidden + (SHIFT ? V - 1 : 0) + C * 32 - 1) / (C * 32) * 32);
   if (threads > kNormRingThreads) return false;
-  const int smem = static_cast<int>(RowRing<T, V, C, 3, kLayerBwdStages<T, C>>::bytes(threads));
   static RingPrep prep[2];
   const bool drop = p.drop.rng != nullptr;
+  const int smem = static_cast<int>(RowRing<T, V, C, 3, kLayerBwdStages<T, C>>::bytes(threads)) +
+                   (drop ? KeepColumns<V, C / V, SHIFT>::keep_bytes(threads) : 0);
   const void* fn = drop ? reinterpret_cast<const void*>(layer_norm_bwd_ring_kernel<T, V, C, SHIFT, true>)
                         : reinterpret_cast<const void*>(layer_norm_bwd_ring_kernel<T, V, C, SHIFT, false>);
-  static_assert(kLayerBwdStages<T, C> * 3 * kNormRingThreads * C * sizeof(T) <= kNormRingSmem, "a CTA's shared memory");
+  static_assert(kLayerBwdStages<T, C> * 3 * kNormRingThreads * C * sizeof(T) +
+                        KeepColumns<V, C / V, SHIFT>::keep_bytes(kNormRingThreads) <=
+                    kNormRingSmem,
+                "a CTA's shared memory");
   int fit = 0;
   *e = prepare_ring(prep[drop], fn, threads, smem, dev, 1, &fit);
   if (*e != cudaSuccess) return true;
@@ -386,10 +410,9 @@ cudaError_t run_width(LayerNormBwdParams& p, cudaStream_t stream, const DeviceIn
     rows.add(p.dx, static_cast<uint64_t>(d) * sizeof(T));
     rows.add(p.dy, static_cast<uint64_t>(d) * sizeof(T));
     if (rows.alike) {
-      if (run_ring<T, kLayerCols<T>, true>(p, stream, dev, &e, rows.period())) return e;
-      if constexpr (kLayerCols<T> != kLayerWideCols) {
-        if (run_ring<T, kLayerWideCols, true>(p, stream, dev, &e, rows.period())) return e;
-      }
+      // 8 columns a thread leave more CTAs an SM (16384 x 1531 bf16 53 us, with 16 67; with dropout 87, 96).
+      if (run_ring<T, 8, true>(p, stream, dev, &e, rows.period())) return e;
+      if (run_ring<T, kLayerWideCols, true>(p, stream, dev, &e, rows.period())) return e;
     }
   }
   if (d <= 4096) return run_shape<T, V, 8 / V, 512>(p, static_cast<int>((d + 255) / 256 * 32), stream, dev);
