@@ -19,7 +19,7 @@ namespace {
 // Warps of a CTA: 16, whose sums are half as much to add up as twice 8 warps', while shared memory
 // has room for them.  A warp takes 4 tokens where there are not too many.
 template <int N>
-constexpr int kBalanceWarps = N <= 8 ? 16 : 8;
+constexpr int kBalanceWarps = N <= 16 ? 16 : 8;
 constexpr int kBackWarps = 8;
 
 // A row's p, from its logits in l; false, and p all zero, where no logit is above minus infinity.
@@ -369,7 +369,7 @@ struct BalanceCut {
   uint64_t chunk_tokens;
 };
 BalanceCut balance_cut(uint64_t tokens, uint32_t experts, uint64_t sequences) {
-  const uint64_t kTokens = 4 * (experts <= 256 ? kBalanceWarps<8> : kBalanceWarps<16>), kMost = 1216;
+  const uint64_t kTokens = 4 * (experts <= 512 ? kBalanceWarps<16> : kBalanceWarps<32>), kMost = 1216;
   const uint64_t n = tokens / sequences, most = sequences < kMost ? kMost / sequences : 1;
   uint64_t each = (n + most - 1) / most;
   each = each < kTokens ? kTokens : each;
