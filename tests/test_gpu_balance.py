@@ -116,6 +116,16 @@ def test_padding_may_hold_anything(moe, score):
         assert not d[~mask].any() and bool(torch.isfinite(d).all())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_logits_of_the_lowest_value_are_open(moe, dtype):
+    """Masks of the type's lowest value are logits like others: a row of them alone is uniform, one beside others nothing."""
+    logits, ids = make(40, 24, 3, dtype)
+    logits[::3] = torch.finfo(dtype).min
+    logits[1::3, 5:] = torch.finfo(dtype).min
+    got = check(moe, logits, ids)
+    assert int(got.counts.sum()) == int(((ids >= 0) & (ids < 24)).sum())
+
+
 def test_a_nan_that_counts_shows(moe):
     logits, ids = make(50, 24, 4, torch.float32)
     logits[7, 3] = math.nan

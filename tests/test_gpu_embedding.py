@@ -89,6 +89,32 @@ def test_runs_of_tokens(zc, emb, tokens, vocab):
         check_gradient(zc, emb, rows_of(tokens, 24, torch.float32), make(tokens, vocab, 3, skew=skew), vocab, torch.float32)
 
 
+@pytest.mark.parametrize("tokens", [1023, 1024, 1025, 4096, 8193, 32767, 32768, 32769])
+@pytest.mark.parametrize("vocab", [511, 512, 140000])
+def test_sizes_of_the_sort(zc, emb, tokens, vocab):
+    """One CTA, a cluster with every number of keys a thread, and the launches beyond; tables of one to two digits."""
+    check_gradient(zc, emb, rows_of(tokens, 8, torch.float32), make(tokens, vocab, tokens, torch.int32), vocab, torch.float32)
+
+
+@pytest.mark.parametrize("vocab", [1, 100, 2000, 70000])
+@pytest.mark.parametrize("width", [8, 4096, 20000])
+def test_tables_of_any_size_are_zeroed_once(zc, emb, vocab, width):
+    """The rows without a token are cut over the CTAs beside the sort and those after it: none is left out."""
+    if vocab * width > 1 << 29:
+        pytest.skip("covered by the smaller ones")
+    ids = torch.tensor([0, vocab - 1, vocab // 2], device="cuda")
+    for tokens in (3, 1500):
+        many = ids.repeat(tokens // 3)
+        dout = rows_of(len(many), width, torch.bfloat16)
+        room = torch.full((vocab * width + 64,), 7.0, device="cuda").bfloat16()
+        got = emb.lookup_backward(dout, many, vocab, emb.workspace(len(many), vocab, width), zc.new_status(),
+                                  dtable=room[32:-32].view(vocab, width))
+        used = torch.zeros(vocab, dtype=torch.bool, device="cuda")
+        used[ids] = True
+        assert not got[~used].any() and bool(got[used].any(1).all())
+        assert bool((room[:32] == 7).all()) and bool((room[-32:] == 7).all())
+
+
 @pytest.mark.parametrize("tokens", [31, 32, 33, 64, 95, 97])
 def test_runs_that_end_where_a_warp_does(zc, emb, tokens):
     for counts in ([tokens], [1, tokens - 1], [tokens - 1, 1], [16, 16, tokens - 32] if tokens > 32 else [tokens],

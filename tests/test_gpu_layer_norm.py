@@ -184,6 +184,40 @@ def test_in_place_and_again(norm, width):
             assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [40, 129, 1000, 1021, 4096, 9001])
+def test_all_and_none_dropped(norm, dtype, width):
+    """p = 1 leaves the residual, infinities and NaN in what is dropped too; a p that rounds to no step keeps all."""
+    from lossless_bf16_exponent_zc_gb300 import dropout
+    x, dh = (torch.randn((9, width), device="cuda").to(dtype) for _ in range(2))
+    y = torch.full_like(x, float("nan"))
+    y[::2] = float("inf")
+    w, rng, ws = torch.rand(width, device="cuda"), dropout.new_rng(5), norm.workspace(9, width)
+    x_new, h, stats = norm.add_layer_norm(y, x, w, p=1.0, rng=rng, save=True)
+    assert torch.equal(x_new, x) and torch.equal(h, norm.layer_norm(x, w)[0])
+    g = norm.add_layer_norm_backward(None, dh, x_new, stats, w, ws, p=1.0, rng=rng)
+    assert not g.dy.any() and torch.equal(g.dx, norm.layer_norm_backward(dh, x, stats, w, ws)[0])
+    for a, b in zip(norm.add_layer_norm(dh, x, w, p=1e-7, rng=rng), norm.add_layer_norm(dh, x, w)):
+        assert a is b or torch.equal(a, b)
+    g = norm.add_layer_norm_backward(None, dh, x_new, stats, w, ws, p=1e-7, rng=rng)
+    assert torch.equal(g.dy, g.dx)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [65, 520, 1021, 1531, 4081])
+def test_many_rows_a_walker(norm, dtype, width):
+    """Odd widths over more rows than a walker draws ahead for (32), every row against dropout.dropout's mask."""
+    from lossless_bf16_exponent_zc_gb300 import dropout
+    rows = 40 * 1300 if width < 1000 else 40 * 650
+    y = torch.ones((1, width), device="cuda").to(dtype).expand(rows, width).contiguous()
+    x, w, rng = torch.zeros_like(y), torch.ones(width, device="cuda"), dropout.new_rng(77, 5)
+    mask = dropout.dropout(y, 0.5, rng, 4)
+    x_new, _, stats = norm.add_layer_norm(y, x, w, p=0.5, rng=rng, call=4, save=True)
+    assert torch.equal(x_new, mask)
+    g = norm.add_layer_norm_backward(y, x, x_new, stats, w, norm.workspace(rows, width), p=0.5, rng=rng, call=4)
+    assert torch.equal(g.dy, mask) and torch.equal(g.dx, y)
+
+
 def test_no_tokens(norm):
     x, w = torch.zeros((0, 40), device="cuda"), torch.ones(40, device="cuda")
     h, stats = norm.layer_norm(x, w, save=True)

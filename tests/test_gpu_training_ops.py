@@ -153,7 +153,7 @@ def test_a_step_of_a_model(zc, score):
     co = torch.randn_like(c)
     ((c * co).sum() + 50 * loss).backward()
     ((ec * co.double()).sum() + 50 * want_loss).backward()
-    assert abs(float(loss) - float(want_loss)) < 2**-18 * float(want_loss)
+    assert abs(loss.item() - want_loss.item()) < 2**-18 * want_loss.item()
     for g, w in ((a, ea), (b, eb), (c, ec)):
         assert float((g.detach().double() - w.detach()).abs().max()) < 2**-14 * float(w.abs().max())
     for name in v:
@@ -263,3 +263,83 @@ def test_back_to_back_in_one_workspace(zc):
         assert torch.equal(c.counts[0], torch.bincount(experts[:, 0], minlength=64).int())
         assert math.isclose(float(c.loss), 1.0, rel_tol=1e-3)
     assert zc.status_value(st) == 0
+
+
+def test_two_graphs_with_a_workspace_each(zc):
+    """Graphs replayed side by side on two streams give what each gives by itself."""
+    from lossless_bf16_exponent_zc_gb300 import embedding, moe, norm
+    made = []
+    for seed in range(2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        ids = torch.randint(0, 700, (9000,), device="cuda", generator=g)
+        dout = torch.randn((9000, 136), device="cuda", generator=g)
+        logits = torch.randn((9000, 40), device="cuda", generator=g)
+        experts = torch.randint(0, 40, (9000, 3), device="cuda", generator=g, dtype=torch.int32)
+        w = torch.rand(136, device="cuda", generator=g)
+        st, ews = zc.new_status(), embedding.workspace(9000, 700, 136)
+        bws, nws = moe.balance_workspace(9000, 40), norm.workspace(9000, 136)
+        stats = norm.layer_norm(dout, w, save=True)[1]
+
+        def call(ids=ids, dout=dout, logits=logits, experts=experts, w=w, st=st, ews=ews, bws=bws, nws=nws, stats=stats):
+            return [embedding.lookup_backward(dout, ids, 700, ews, st), *moe.balance_loss(logits, experts, bws),
+                    *norm.layer_norm_backward(dout, dout, stats, w, nws)]
+
+        want = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call()
+        made.append((graph, out, want, torch.cuda.Stream(), call))  # the call keeps what the graph reads
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, _, _, stream, _ in made:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _, _ in made:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_from_several_threads(zc):
+    import threading
+
+    from lossless_bf16_exponent_zc_gb300 import dropout, embedding, moe, norm
+
+    def step(seed, rounds, out):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        ids = torch.randint(0, 90, (500,), device="cuda", generator=g)
+        table = torch.randn((90, 72), device="cuda", generator=g)
+        logits, experts = torch.randn((500, 8), device="cuda", generator=g), (ids % 8).to(torch.int32)[:, None]
+        w, rng, st = torch.ones(72, device="cuda"), dropout.new_rng(seed), zc.new_status()
+        ews, bws, nws = embedding.workspace(500, 90, 72), moe.balance_workspace(500, 8), norm.workspace(500, 72)
+        for i in range(rounds):
+            x = embedding.lookup(ids, table, st)
+            y = dropout.dropout(x, 0.2, rng, 1, residual=x)
+            x_new, h, stats = norm.add_layer_norm(y, x, w, p=0.2, rng=rng, save=True)
+            back = norm.add_layer_norm_backward(y, x, x_new, stats, w, nws, p=0.2, rng=rng)
+            out.append([y, x_new, h, back.dy, back.dx, back.dweight, *moe.balance_loss(logits, experts, bws),
+                        embedding.lookup_backward(back.dx, ids, 90, ews, st)])
+        torch.cuda.current_stream().synchronize()
+
+    want, got, errors = [[], []], [[], []], []
+    for seed in (0, 1):
+        step(seed, 1, want[seed])
+
+    def work(seed):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                step(seed, 30, got[seed])
+        except Exception as e:  # raised again by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(seed,)) for seed in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    torch.cuda.synchronize()
+    for seed in (0, 1):
+        assert len(got[seed]) == 30
+        for run in got[seed]:
+            assert all(torch.equal(a, b) for a, b in zip(run, want[seed][0]))
