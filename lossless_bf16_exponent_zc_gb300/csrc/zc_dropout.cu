@@ -197,11 +197,20 @@ cudaError_t run(DropoutParams& p, bool vec, cudaStream_t stream) {
   if (vec) {
     Divisor groups((p.width + 7) / 8);
     void* args[] = {&p, &groups};
-    constexpr int kUnits = sizeof(T) == 2 ? 4 : 2;
     const bool flat = p.width % 8 == 0 && p.x_stride == p.width && (!RESIDUAL || p.residual_stride == p.width);
-    return launch(flat ? reinterpret_cast<const void*>(dropout_kernel<T, kUnits, RESIDUAL, true>)
-                       : reinterpret_cast<const void*>(dropout_kernel<T, kUnits, RESIDUAL, false>),
-                  (p.tokens * groups.d + kDropThreads * kUnits - 1) / (kDropThreads * kUnits), stream, args);
+    const uint64_t all = p.tokens * groups.d;
+    // Two groups a thread, and four of 16-bit values with a residual where they are many (16384 x 4096 bf16
+    // 59 us, with two 62, with eight 72; without a residual 43, with four 47; 256 x 1024 1.7, with four 2.2).
+    if constexpr (sizeof(T) == 2 && RESIDUAL) {
+      if (all >= 4096ull * kDropThreads) {
+        return launch(flat ? reinterpret_cast<const void*>(dropout_kernel<T, 4, RESIDUAL, true>)
+                           : reinterpret_cast<const void*>(dropout_kernel<T, 4, RESIDUAL, false>),
+                      (all + kDropThreads * 4 - 1) / (kDropThreads * 4), stream, args);
+      }
+    }
+    return launch(flat ? reinterpret_cast<const void*>(dropout_kernel<T, 2, RESIDUAL, true>)
+                       : reinterpret_cast<const void*>(dropout_kernel<T, 2, RESIDUAL, false>),
+                  (all + kDropThreads * 2 - 1) / (kDropThreads * 2), stream, args);
   }
   const auto base = [](const void* q) { return reinterpret_cast<uintptr_t>(q) & 15; };
   const auto apart = [](uint64_t stride) { return stride * sizeof(T) & 15; };
