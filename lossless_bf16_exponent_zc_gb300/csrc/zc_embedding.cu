@@ -95,6 +95,38 @@ __global__ void __launch_bounds__(kEmbedThreads, 8) embed_kernel(EmbedParams p, 
   }
 }
 
+// Rows of many pieces: a warp takes 32 UNITS of a token's, so that it looks up one id.
+template <typename T, typename TT, int UNITS>
+__global__ void __launch_bounds__(kEmbedThreads) embed_wide_kernel(EmbedParams p, Divisor shares) {
+  constexpr int V = kPieceOf<T>;
+  pdl_begin();
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads / 32) + (threadIdx.x >> 5);
+  const uint64_t t = i >> 31 ? i / shares.d : shares(static_cast<uint32_t>(i));
+  if (t >= p.tokens) return;
+  const uint32_t c0 = static_cast<uint32_t>(i - t * shares.d) * (32 * UNITS) + lane_id(), pieces = p.hidden / V;
+  const int64_t id = id_at(p.ids, p.ids64, t);
+  const bool there = has_row(id, p.vocab, p.status);
+  const TT* row = static_cast<const TT*>(p.table) + (there ? static_cast<uint64_t>(id) * p.table_stride : 0);
+  T* out = static_cast<T*>(p.out) + t * p.hidden;
+  AnyValues<TT, V, true> v[UNITS];
+#pragma unroll
+  for (int q = 0; q < UNITS; q++) {
+    v[q].clear();
+    if (there && c0 + q * 32 < pieces) v[q].load(row + static_cast<uint64_t>(c0 + q * 32) * V);
+  }
+#pragma unroll
+  for (int q = 0; q < UNITS; q++) {
+    if (c0 + q * 32 >= pieces) continue;
+    float f[V];
+    v[q].get(f);
+#pragma unroll
+    for (int j = 0; j < V; j++) f[j] *= p.scale;
+    Piece<T, V> o;
+    o.set(f);
+    o.store(out + static_cast<uint64_t>(c0 + q * 32) * V);
+  }
+}
+
 // The same off 16 bytes: a lane takes a unit of a token's output (RowCut).
 template <typename T, typename TT>
 __global__ void __launch_bounds__(kEmbedThreads) embed_any_kernel(EmbedParams p, uint32_t shares) {
@@ -713,6 +745,13 @@ cudaError_t lookup(EmbedParams& p, bool vec, cudaStream_t stream, const DeviceIn
   if (all <= 2ull * kEmbedThreads * static_cast<uint64_t>(dev.sm_count))
     return run(reinterpret_cast<const void*>(embed_kernel<T, TT, 1>), ceil_div(all, kEmbedThreads), kEmbedThreads, 0,
                stream, args);
+  constexpr uint32_t kUnits = sizeof(TT) > sizeof(T) ? 2 : 4;
+  if (pieces.d >= 64) {
+    Divisor shares(static_cast<uint32_t>(ceil_div(pieces.d, 32 * kUnits)));
+    void* wide[] = {&p, &shares};
+    return run(reinterpret_cast<const void*>(embed_wide_kernel<T, TT, kUnits>),
+               ceil_div(p.tokens * shares.d, kEmbedThreads / 32), kEmbedThreads, 0, stream, wide);
+  }
   return run(reinterpret_cast<const void*>(embed_kernel<T, TT, 2>), ceil_div(all, 2 * kEmbedThreads), kEmbedThreads, 0,
              stream, args);
 }
