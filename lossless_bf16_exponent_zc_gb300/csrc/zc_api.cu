@@ -1064,7 +1064,7 @@ zc_status zc_embedding(const void* d_ids, int ids_are_int64, uint64_t tokens, co
 zc_status zc_embedding_workspace_size(uint64_t tokens, uint64_t vocab, uint32_t hidden, uint64_t* bytes) {
   if (!bytes) return ZC_ERR_INVALID_ARG;
   if (zc_status s = check_table(tokens, vocab, hidden)) return s;
-  *bytes = embed_workspace_bytes(tokens, vocab, hidden);
+  *bytes = embed_workspace_bytes(tokens, hidden);
   return ZC_OK;
 }
 
@@ -1081,7 +1081,7 @@ zc_status zc_embedding_backward(const void* d_dout, int dtype, uint64_t dout_str
   if (!aligned(d_ids, ids_are_int64 ? 8 : 4) || !aligned(d_dtable, tsize) || !aligned(d_ws, 16) ||
       !aligned(d_status, 4))
     return ZC_ERR_ALIGNMENT;
-  if (ws_bytes < embed_workspace_bytes(tokens, vocab, hidden)) return ZC_ERR_WORKSPACE;
+  if (ws_bytes < embed_workspace_bytes(tokens, hidden)) return ZC_ERR_WORKSPACE;
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return ZC_ERR_CUDA;
   EmbedBwdParams p = {};

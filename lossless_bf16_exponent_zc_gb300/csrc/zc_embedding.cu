@@ -181,7 +181,6 @@ __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(EmbedBwdParam
   for (uint32_t i = threadIdx.x; i < n; i += kSortThreads) {
     const uint32_t key = sort_key(p, first + i);
     atomicAdd(&hist[(key >> p.shift) & (bins - 1)], 1u);
-    if (!p.keys_in && key < p.vocab && p.present) atomicOr(&p.present[key >> 5], 1u << (key & 31));
   }
   __syncthreads();
   for (uint32_t e = threadIdx.x; e < bins; e += kSortThreads)
@@ -306,7 +305,7 @@ constexpr uint32_t kClusterBins = 512;
 constexpr uint32_t kFillRows = 32768;  // rows whose presence a CTA keeps at once
 
 struct ClusterSort {
-  uint32_t items, ctas, bits, passes, size;
+  uint32_t items, ctas, bits, passes;
   uint32_t fill, late;           // CTAs that zero rows: those beside the sort, and those that follow it on its SMs
   uint64_t fill_rows, late_rows;  // rows of each of them
 };
@@ -324,9 +323,9 @@ __device__ __forceinline__ void zero_row(uint8_t* row, uint64_t bytes) {
 }
 
 // Zeroes the rows of `first` .. `last` that no token asks for; `present` holds a bit for kFillRows.
-__device__ __forceinline__ void fill_rows(const EmbedBwdParams& p, uint64_t first, uint64_t last, uint32_t size,
+__device__ __forceinline__ void fill_rows(const EmbedBwdParams& p, uint64_t first, uint64_t last,
                                           uint32_t* present) {
-  const uint64_t bytes = static_cast<uint64_t>(p.hidden) * size;
+  const uint64_t bytes = static_cast<uint64_t>(p.hidden) * p.size;
   for (uint64_t v0 = first; v0 < last; v0 += kFillRows) {
     const uint32_t n = static_cast<uint32_t>(min(static_cast<uint64_t>(kFillRows), last - v0));
     for (uint32_t i = threadIdx.x; i < (n + 31) / 32; i += kClusterThreads) present[i] = 0;
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kClusterThreads, 2) embed_cluster_kernel(Embed
     const uint64_t rows = i < c.fill ? c.fill_rows : c.late_rows;
     const uint64_t first = i < c.fill ? i * rows : c.fill * c.fill_rows + (i - c.fill) * rows;
     if (first < p.vocab)
-      fill_rows(p, first, min(p.vocab, first + rows), c.size, reinterpret_cast<uint32_t*>(cluster_smem));
+      fill_rows(p, first, min(p.vocab, first + rows), reinterpret_cast<uint32_t*>(cluster_smem));
     return;
   }
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, rank = blockIdx.x;
@@ -628,6 +627,39 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedBwdPar
   }
 }
 
+// How many sorted keys are below `row`; the warp looks at 32 places at a time.
+__device__ __forceinline__ uint64_t keys_below(const EmbedBwdParams& p, uint64_t row) {
+  uint64_t from = 0, size = p.tokens;  // the answer is from .. from + size
+  while (size) {
+    const uint64_t step = (size + 31) / 32, at = from + step * (lane_id() + 1) - 1;
+    const bool below = at < from + size && p.keys_in[at] < row;
+    const uint32_t n = __popc(__ballot_sync(kFull, below));
+    const uint64_t end = from + size;
+    from += n * step;
+    size = min(step - 1, end - min(end, from));
+  }
+  return from;
+}
+
+// Zeroes the rows that no token asks for: a warp gap_rows of them, up to 32; a lane looks for one of them
+// among the keys from the first one's to the last one's.
+__device__ __forceinline__ void fill_gaps(const EmbedBwdParams& p, uint64_t warp) {
+  const uint64_t first = warp * p.gap_rows, last = min(p.vocab, first + p.gap_rows);
+  if (first >= last) return;
+  const uint64_t row = first + lane_id(), stop = keys_below(p, last);
+  uint64_t from = keys_below(p, first), size = stop - from;
+  while (size) {
+    const uint64_t half = size / 2;
+    const bool below = p.keys_in[from + half] < row;
+    from += below ? half + 1 : 0;
+    size = below ? size - half - 1 : half;
+  }
+  const bool there = from < stop && p.keys_in[from] == row;
+  const uint64_t bytes = static_cast<uint64_t>(p.hidden) * p.size;
+  for (uint32_t gaps = __ballot_sync(kFull, row < last && !there); gaps; gaps &= gaps - 1)
+    zero_row(static_cast<uint8_t*>(p.dtable) + (first + __ffs(gaps) - 1) * bytes, bytes);
+}
+
 // Rows whose tokens lie in several runs, of one slab.  Each warp looks at one run, and adds the parts of
 // the row that begins there and goes on; where those are many the warps of the CTA share them.
 constexpr uint32_t kJoinAlone = 16;  // parts that a warp adds by itself
@@ -638,6 +670,10 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedBwdParam
   __shared__ uint32_t many[kWarps];  // parts of a warp's row that are for all, or 0
   __shared__ uint32_t rows[kWarps];
   pdl_begin();
+  if (blockIdx.x >= p.join_ctas) {
+    fill_gaps(p, static_cast<uint64_t>(blockIdx.x - p.join_ctas) * kWarps + (threadIdx.x >> 5));
+    return;
+  }
   const uint64_t group = blockIdx.x / p.slabs;
   const uint32_t slab = static_cast<uint32_t>(blockIdx.x - group * p.slabs), lane = lane_id(), warp = threadIdx.x >> 5;
   const uint64_t run = group * kWarps + warp, first = run * p.run, next = first + p.run;
@@ -712,16 +748,6 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedBwdParam
   }
 }
 
-// Zeroes the rows that no token asks for, a warp a row.
-__global__ void __launch_bounds__(kEmbedThreads) embed_fill_kernel(EmbedBwdParams p, uint32_t size) {
-  pdl_begin();
-  const uint64_t warps = static_cast<uint64_t>(gridDim.x) * (kEmbedThreads / 32), bytes = static_cast<uint64_t>(p.hidden) * size;
-  for (uint64_t v = static_cast<uint64_t>(blockIdx.x) * (kEmbedThreads / 32) + (threadIdx.x >> 5); v < p.vocab; v += warps) {
-    if (p.present[v >> 5] >> (v & 31) & 1) continue;
-    zero_row(static_cast<uint8_t*>(p.dtable) + v * bytes, bytes);
-  }
-}
-
 // ------------------------------------------------------------------ launches
 uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
@@ -756,19 +782,26 @@ cudaError_t lookup(EmbedParams& p, bool vec, cudaStream_t stream, const DeviceIn
              stream, args);
 }
 
+constexpr uint64_t kGapWarps = 16;  // an SM's warps that zero rows beside the joins, or as many as 32 rows each make
 template <typename T, typename TT, bool VEC>
-cudaError_t sums(EmbedBwdParams& p, cudaStream_t stream) {
+cudaError_t sums(EmbedBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   void* args[] = {&p};
   const void* fn = VEC && p.accumulate ? reinterpret_cast<const void*>(embed_sum_kernel<T, TT, VEC, VEC>)
                                        : reinterpret_cast<const void*>(embed_sum_kernel<T, TT, VEC, false>);
   cudaError_t e = run(fn, ceil_div(p.runs * p.slabs, kEmbedThreads / 32), kEmbedThreads, 0, stream, args);
   if (e != cudaSuccess || p.runs < 2) return e;
-  return run(reinterpret_cast<const void*>(embed_join_kernel<T, TT, VEC>), ceil_div(p.runs, kEmbedThreads / 32) * p.slabs,
-             kEmbedThreads, 0, stream, args);
+  const uint64_t join = ceil_div(p.runs, kEmbedThreads / 32) * p.slabs,
+                 fill = p.tokens > kEmbedClusterTokens && !p.accumulate ? p.vocab : 0;
+  if (join > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+  p.join_ctas = static_cast<uint32_t>(join);
+  p.gap_rows = static_cast<uint32_t>(ceil_div(fill, kGapWarps * static_cast<uint64_t>(dev.sm_count)));
+  if (p.gap_rows > 32) p.gap_rows = 32;
+  const uint64_t gaps = fill ? ceil_div(fill, p.gap_rows * (kEmbedThreads / 32)) : 0;
+  return run(reinterpret_cast<const void*>(embed_join_kernel<T, TT, VEC>), join + gaps, kEmbedThreads, 0, stream, args);
 }
 template <typename T, typename TT>
-cudaError_t sums(EmbedBwdParams& p, bool vec, cudaStream_t stream) {
-  return vec ? sums<T, TT, true>(p, stream) : sums<T, TT, false>(p, stream);
+cudaError_t sums(EmbedBwdParams& p, bool vec, cudaStream_t stream, const DeviceInfo& dev) {
+  return vec ? sums<T, TT, true>(p, stream, dev) : sums<T, TT, false>(p, stream, dev);
 }
 
 // Tokens of a run: those that make the waves of warps, three CTAs an SM, take the least time, a warp
@@ -797,8 +830,8 @@ uint64_t embed_runs(uint64_t tokens, uint32_t hidden) {
 
 // Where a gradient's workspace holds what.
 struct EmbedWork {
-  uint64_t keys, tokens, counts, totals, present, parts, bytes;  // byte offsets; keys and tokens have two halves
-  EmbedWork(uint64_t n, uint64_t vocab, uint32_t hidden) {
+  uint64_t keys, tokens, counts, totals, parts, bytes;  // byte offsets; keys and tokens have two halves
+  EmbedWork(uint64_t n, uint32_t hidden) {
     const uint64_t chunks = ceil_div(n, kEmbedSortChunk), runs = embed_runs(n, hidden);
     uint64_t at = 0;
     auto take = [&](uint64_t words) {
@@ -811,18 +844,15 @@ struct EmbedWork {
     tokens = take(2 * n);
     counts = take(kSortBins * chunks);
     totals = take(kSortBins);
-    present = take(ceil_div(vocab, 32));
     bytes = at;
   }
 };
 
-cudaError_t sort_in_cluster(EmbedBwdParams& p, uint32_t bits, uint32_t size, cudaStream_t stream,
-                            const DeviceInfo& dev) {
+cudaError_t sort_in_cluster(EmbedBwdParams& p, uint32_t bits, cudaStream_t stream, const DeviceInfo& dev) {
   static KernelPrep prep;
   ClusterSort c = {};
   c.bits = bits;
   c.passes = static_cast<uint32_t>(ceil_div(bits, 9));
-  c.size = size;
   // one CTA holds a few tokens, and more of them a cluster, with as few a thread as that allows
   c.ctas = p.tokens <= 2 * kClusterThreads ? 1 : kEmbedClusterCtas;
   c.items = static_cast<uint32_t>(ceil_div(p.tokens, static_cast<uint64_t>(c.ctas) * kClusterThreads));
@@ -846,7 +876,7 @@ cudaError_t sort_in_cluster(EmbedBwdParams& p, uint32_t bits, uint32_t size, cud
     e = prepare_ring(fits[c.ctas > 1], fn, kClusterThreads, kMostSmem, dev, static_cast<int>(c.ctas), &fit);
     if (e != cudaSuccess) return e;
     const uint64_t beside = fit > 1 ? (static_cast<uint64_t>(fit) - 1) * c.ctas : 1;
-    const uint64_t row = static_cast<uint64_t>(p.hidden) * size;
+    const uint64_t row = static_cast<uint64_t>(p.hidden) * p.size;
     const uint64_t lost = (10 + p.tokens / 4096) * 20480 / row;
     c.fill = static_cast<uint32_t>(beside);
     c.late = c.ctas;
@@ -860,11 +890,9 @@ cudaError_t sort_in_cluster(EmbedBwdParams& p, uint32_t bits, uint32_t size, cud
   return launch_kernel(fn, dim3(grid), dim3(kClusterThreads), smem, stream, args, false, c.ctas);
 }
 
-cudaError_t sort_in_launches(EmbedBwdParams& p, uint32_t bits, uint32_t size, uint32_t* const (&keys)[2],
-                             uint32_t* const (&tokens)[2], cudaStream_t stream, const DeviceInfo& dev) {
+cudaError_t sort_in_launches(EmbedBwdParams& p, uint32_t bits, uint32_t* const (&keys)[2], uint32_t* const (&tokens)[2],
+                             cudaStream_t stream, const DeviceInfo& dev) {
   cudaError_t e = cudaSuccess;
-  if (p.present) e = cudaMemsetAsync(p.present, 0, ceil_div(p.vocab, 32) * 4, stream);
-  if (e != cudaSuccess) return e;
   const uint32_t passes = static_cast<uint32_t>(ceil_div(bits, kEmbedDigitBits));
   static KernelPrep prep;
   int per_sm = 0;
@@ -889,10 +917,7 @@ cudaError_t sort_in_launches(EmbedBwdParams& p, uint32_t bits, uint32_t size, ui
   if (e != cudaSuccess) return e;
   p.keys_in = keys[(passes + 1) & 1];
   p.tokens_in = tokens[(passes + 1) & 1];
-  if (!p.present) return e;
-  void* fill[] = {&p, &size};
-  const uint64_t most = 8ull * static_cast<uint64_t>(dev.sm_count), all = ceil_div(p.vocab, kEmbedThreads / 32);
-  return run(reinterpret_cast<const void*>(embed_fill_kernel), all < most ? all : most, kEmbedThreads, 0, stream, fill);
+  return e;
 }
 
 }  // namespace
@@ -911,46 +936,45 @@ cudaError_t launch_embed(const EmbedParams& params, int dtype, int table_f32, bo
   }
 }
 
-uint64_t embed_workspace_bytes(uint64_t tokens, uint64_t vocab, uint32_t hidden) {
-  return EmbedWork(tokens, vocab, hidden).bytes;
+uint64_t embed_workspace_bytes(uint64_t tokens, uint32_t hidden) {
+  return EmbedWork(tokens, hidden).bytes;
 }
 
 cudaError_t launch_embed_bwd(const EmbedBwdParams& params, int dtype, int table_f32, bool vec, void* ws,
                              cudaStream_t stream, const DeviceInfo& dev) {
   EmbedBwdParams p = params;
-  const EmbedWork at(p.tokens, p.vocab, p.hidden);
+  const EmbedWork at(p.tokens, p.hidden);
   uint8_t* base = static_cast<uint8_t*>(ws);
   uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(base + at.keys), reinterpret_cast<uint32_t*>(base + at.keys) + p.tokens};
   uint32_t* tokens[2] = {reinterpret_cast<uint32_t*>(base + at.tokens),
                          reinterpret_cast<uint32_t*>(base + at.tokens) + p.tokens};
   p.counts = reinterpret_cast<uint32_t*>(base + at.counts);
   p.totals = reinterpret_cast<uint32_t*>(base + at.totals);
-  p.present = p.accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + at.present);
   p.parts = reinterpret_cast<float*>(base + at.parts);
   p.sort_chunks = static_cast<uint32_t>(ceil_div(p.tokens, kEmbedSortChunk));
   p.run = embed_run(p.tokens, p.hidden, dev);
   p.runs = ceil_div(p.tokens, p.run);
   p.slabs = static_cast<uint32_t>(ceil_div(p.hidden, kSlab));
-  const uint32_t size = dtype == ZC_F32 || table_f32 ? 4 : 2;
+  p.size = dtype == ZC_F32 || table_f32 ? 4 : 2;
   uint32_t bits = 1;  // of the keys 0 .. vocab
   while (p.vocab >> bits) bits++;
   cudaError_t e;
   if (p.tokens <= kEmbedClusterTokens) {
     p.keys_out = keys[0];
     p.tokens_out = tokens[0];
-    e = sort_in_cluster(p, bits, size, stream, dev);
+    e = sort_in_cluster(p, bits, stream, dev);
     p.keys_in = keys[0];
     p.tokens_in = tokens[0];
   } else {
-    e = sort_in_launches(p, bits, size, keys, tokens, stream, dev);
+    e = sort_in_launches(p, bits, keys, tokens, stream, dev);
   }
   if (e != cudaSuccess) return e;
   if (p.tokens == 0) return e;
   switch (dtype) {
     case ZC_BF16:
-      return table_f32 ? sums<__nv_bfloat16, float>(p, vec, stream) : sums<__nv_bfloat16, __nv_bfloat16>(p, vec, stream);
-    case ZC_F16: return table_f32 ? sums<__half, float>(p, vec, stream) : sums<__half, __half>(p, vec, stream);
-    default: return sums<float, float>(p, vec, stream);
+      return table_f32 ? sums<__nv_bfloat16, float>(p, vec, stream, dev) : sums<__nv_bfloat16, __nv_bfloat16>(p, vec, stream, dev);
+    case ZC_F16: return table_f32 ? sums<__half, float>(p, vec, stream, dev) : sums<__half, __half>(p, vec, stream, dev);
+    default: return sums<float, float>(p, vec, stream, dev);
   }
 }
 

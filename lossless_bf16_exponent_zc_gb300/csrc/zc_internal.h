@@ -311,13 +311,14 @@ struct EmbedBwdParams {
   // set by the launch: the workspace, the pass of the sort, and the sums' cut
   const uint32_t *keys_in, *tokens_in;  // of the pass; NULL in the first, which reads the ids
   uint32_t *keys_out, *tokens_out, *counts, *totals;
-  uint32_t* present;  // a bit for every row that a token asks for; NULL with accumulate
   uint32_t sort_chunks, shift, digit_bits;
   float* parts;
   uint64_t runs;
   uint32_t run, slabs;  // sorted tokens that a warp adds up, and pieces of a row's columns
+  // the CTAs behind the first join_ctas zero unused rows, a warp gap_rows of them; size: bytes of a value
+  uint32_t join_ctas, gap_rows, size;
 };
-uint64_t embed_workspace_bytes(uint64_t tokens, uint64_t vocab, uint32_t hidden);
+uint64_t embed_workspace_bytes(uint64_t tokens, uint32_t hidden);
 cudaError_t launch_embed(const EmbedParams& p, int dtype, int table_f32, bool vec, cudaStream_t stream,
                          const DeviceInfo& dev);
 cudaError_t launch_embed_bwd(const EmbedBwdParams& p, int dtype, int table_f32, bool vec, void* ws, cudaStream_t stream,
