@@ -332,8 +332,8 @@ __device__ __forceinline__ void fill_rows(const EmbedBwdParams& p, uint64_t firs
     __syncthreads();
 #pragma unroll 8
     for (uint64_t i = threadIdx.x; i < p.tokens; i += kClusterThreads) {
-      const int64_t at = id_at(p.ids, p.ids64, i) - static_cast<int64_t>(v0);
-      if (at >= 0 && at < n) atomicOr(&present[at >> 5], 1u << (at & 31));
+      const uint64_t at = static_cast<uint64_t>(id_at(p.ids, p.ids64, i)) - v0;  // wraps below the first row
+      if (at < n) atomicOr(&present[at >> 5], 1u << (at & 31));
     }
     __syncthreads();
     for (uint32_t r = threadIdx.x >> 5; r < n; r += kClusterWarps)

@@ -108,6 +108,16 @@ def test_in_place(drop, width):
     assert torch.equal(drop.dropout(x, 0.4, rng, residual=b, out=b), want)
 
 
+@pytest.mark.parametrize("width", [64, 1000, 1021])
+def test_a_row_for_all_tokens(drop, width):
+    x = torch.randn((1, width), device="cuda").bfloat16().expand(300, width)
+    r = torch.randn((300, width), device="cuda").bfloat16()
+    keep, factor = kept(300, width, 0.3, 17, 0, 2)
+    check(drop.dropout(x, 0.3, drop.new_rng(17), 2, residual=r), x, keep, factor, r)
+    check(drop.dropout(r, 0.3, drop.new_rng(17), 2, residual=x), r, keep, factor, x)
+    check(drop.dropout(x, 0.3, drop.new_rng(17), 2), x, keep, factor)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_none_and_all(drop, dtype):
     x = torch.randn((6, 40), device="cuda").to(dtype)

@@ -155,6 +155,25 @@ def test_bad_ids(zc, emb):
     check_gradient(zc, emb, rows_of(50, 24, torch.float32), all_out, 10, torch.float32)
 
 
+@pytest.mark.parametrize("tokens", [600, 5000, 40000])
+@pytest.mark.parametrize("itype", [torch.int32, torch.int64])
+def test_ids_at_the_ends_of_their_type(zc, emb, tokens, itype):
+    ids, ends = make(tokens, 700, tokens, itype), torch.iinfo(itype)
+    ids[::7], ids[3::7] = ends.min, ends.min + 1
+    check_gradient(zc, emb, rows_of(tokens, 24, torch.bfloat16), ids, 700, torch.float32)
+    ids[5::7] = ends.max
+    check_rows(zc, emb, ids, rows_of(700, 24, torch.bfloat16), torch.bfloat16)
+    check_gradient(zc, emb, rows_of(tokens, 24, torch.bfloat16), ids, 700, torch.bfloat16)
+
+
+@pytest.mark.parametrize("width", [24, 1000, 1021])
+def test_a_row_for_all_tokens(zc, emb, width):
+    one = rows_of(1, width, torch.bfloat16).expand(900, width)
+    check_gradient(zc, emb, one, make(900, 50), 50, torch.float32)
+    ids = make(900, 50)
+    check_rows(zc, emb, ids, rows_of(1, width, torch.float32).expand(50, width), torch.bfloat16)
+
+
 def test_nothing(zc, emb):
     none = torch.zeros(0, dtype=torch.int64, device="cuda")
     assert emb.lookup(none, rows_of(5, 8, torch.float32), zc.new_status()).shape == (0, 8)

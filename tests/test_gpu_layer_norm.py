@@ -184,6 +184,25 @@ def test_in_place_and_again(norm, width):
             assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("width", [64, 129, 1000, 1021, 4096])
+def test_a_row_for_all_tokens(norm, width):
+    """Rows without a stride between them give what a copy gives, whatever kernel either takes, to the tolerances."""
+    from lossless_bf16_exponent_zc_gb300 import dropout
+    one = torch.randn((1, width), device="cuda").bfloat16().expand(300, width)
+    x = torch.randn((300, width), device="cuda").bfloat16()
+    w, rng, ws = torch.rand(width, device="cuda"), dropout.new_rng(4), norm.workspace(300, width)
+    h, stats = norm.layer_norm(one, w, save=True)
+    check_forward(h, stats, one.double(), torch.zeros_like(one, dtype=torch.float64), w, None)
+    keep, factor = kept(300, width, 0.2, 4, 0, 0)
+    z = torch.where(keep, one.double() * factor, 0.0) + x.double()
+    x_new, h, stats = norm.add_layer_norm(one, x, w, p=0.2, rng=rng, save=True)
+    off = 3 * U * (one.double().abs() * factor + x.double().abs())
+    within(x_new, z, off)
+    check_forward(h, stats, z, off, w, None)
+    got = norm.add_layer_norm_backward(one, one, x_new, stats, w, ws, p=0.2, rng=rng)
+    check_backward(got, one, one, x_new, stats, w, 1.0, keep, factor)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("width", [40, 129, 1000, 1021, 4096, 9001])
 def test_all_and_none_dropped(norm, dtype, width):
