@@ -311,25 +311,31 @@ __global__ void __launch_bounds__(kNormWarps * 32) layer_norm_bwd_warp_kernel(La
   flush(db, mine + p.hidden);
 }
 
-// Adds the CTAs' sums, in order: the warps take a share of the parts each, a lane a column.
-// blockIdx.y: 0 the weight's gradient, 1 the bias's.
-template <typename T>
+// Adds the CTAs' sums, in order: COLS columns a CTA, whose warps take a share of the parts each, 32 / COLS
+// of them at a time.  blockIdx.y: 0 the weight's gradient, 1 the bias's.
+template <typename T, int COLS>
 __global__ void __launch_bounds__(1024) layer_norm_parts_kernel(LayerNormBwdParams p) {
-  __shared__ float sums[32][33];
+  constexpr uint32_t kShares = 1024 / COLS;
+  __shared__ float sums[kShares][COLS + 1];
   pdl_begin();
-  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, share = threadIdx.x / COLS, in = threadIdx.x % COLS;
+  const uint32_t col = blockIdx.x * COLS + in;
   void* dst = blockIdx.y ? p.dbias : p.dweight;
   if (!dst) return;
   float s = 0.f;
-  const uint32_t first = p.ctas * warp / 32, last = p.ctas * (warp + 1) / 32;
+  const uint32_t first = p.ctas * share / kShares, last = p.ctas * (share + 1) / kShares;
   if (col < p.hidden) {
 #pragma unroll 8
     for (uint32_t i = first; i < last; i++) s += p.parts[(2ull * i + blockIdx.y) * p.hidden + col];
   }
-  sums[warp][lane] = s;
+  sums[share][in] = s;
   __syncthreads();
-  s = warp_sum_f32(sums[lane][warp]);
-  const uint32_t mine = blockIdx.x * 32 + warp;
+  const uint32_t mine = blockIdx.x * COLS + warp;
+  if (warp >= COLS) return;
+  s = 0.f;
+#pragma unroll
+  for (uint32_t q = 0; q < kShares; q += 32) s += sums[q + lane][warp];
+  s = warp_sum_f32(s);
   if (lane || mine >= p.hidden) return;
   if (p.params_f32)
     static_cast<float*>(dst)[mine] = s;
@@ -338,21 +344,27 @@ __global__ void __launch_bounds__(1024) layer_norm_parts_kernel(LayerNormBwdPara
 }
 
 template <typename T>
-cudaError_t add_parts(LayerNormBwdParams& p, cudaStream_t stream) {
+cudaError_t add_parts(LayerNormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   void* args[] = {&p};
-  return launch_kernel(reinterpret_cast<const void*>(layer_norm_parts_kernel<T>),
-                       dim3((p.hidden + 31) / 32, p.dbias ? 2 : 1), dim3(1024), 0, stream, args, false);
+  // 8 columns a CTA where that makes no more than two of them an SM: with 32 the narrow rows, which have
+  // the most parts, leave most SMs idle (both launches, 4096 x 512 bf16 14.3 us, with 8 columns 12.2;
+  // 1024 x 1024 11.2 and 8.4).  Wider rows are as fast with 16 and 32.
+  const uint32_t sums = p.dbias ? 2 : 1, eights = (p.hidden + 7) / 8;
+  const bool narrow = eights * sums <= 2 * static_cast<uint32_t>(dev.sm_count);
+  return launch_kernel(narrow ? reinterpret_cast<const void*>(layer_norm_parts_kernel<T, 8>)
+                              : reinterpret_cast<const void*>(layer_norm_parts_kernel<T, 32>),
+                       dim3(narrow ? eights : (p.hidden + 31) / 32, sums), dim3(1024), 0, stream, args, false);
 }
 
 template <typename T>
 cudaError_t run_walkers(LayerNormBwdParams& p, const void* fn, uint64_t most, uint64_t rows_a_cta, int threads, int smem,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, const DeviceInfo& dev) {
   if (most > norm_max_walkers(p.hidden)) most = norm_max_walkers(p.hidden);
   const uint64_t ctas = (p.tokens + rows_a_cta - 1) / rows_a_cta;
   p.ctas = static_cast<uint32_t>(ctas < most ? ctas : most);
   void* args[] = {&p};
   cudaError_t e = launch_kernel(fn, dim3(p.ctas), dim3(threads), smem, stream, args, false);
-  return e == cudaSuccess ? add_parts<T>(p, stream) : e;
+  return e == cudaSuccess ? add_parts<T>(p, stream, dev) : e;
 }
 
 template <typename T, int V, int NV, int THREADS>
@@ -360,7 +372,7 @@ cudaError_t run_shape(LayerNormBwdParams& p, int threads, cudaStream_t stream, c
   const void* fn = p.drop.rng ? reinterpret_cast<const void*>(layer_norm_bwd_kernel<T, V, NV, true, THREADS>)
                               : reinterpret_cast<const void*>(layer_norm_bwd_kernel<T, V, NV, false, THREADS>);
   const uint64_t most = static_cast<uint64_t>(dev.sm_count) * (threads > 256 ? 1024u / static_cast<unsigned>(threads) : 4u);
-  return run_walkers<T>(p, fn, most, 1, threads, 0, stream);
+  return run_walkers<T>(p, fn, most, 1, threads, 0, stream, dev);
 }
 
 template <typename T, int C, bool SHIFT>
@@ -384,7 +396,7 @@ bool run_ring(LayerNormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev,
   uint64_t most = static_cast<uint64_t>(fit);
   if (most > norm_max_walkers(p.hidden)) most = norm_max_walkers(p.hidden);
   if (most > period) most -= most % period;
-  *e = run_walkers<T>(p, fn, most, 1, threads, smem, stream);
+  *e = run_walkers<T>(p, fn, most, 1, threads, smem, stream, dev);
   return true;
 }
 
@@ -395,7 +407,7 @@ cudaError_t run_width(LayerNormBwdParams& p, cudaStream_t stream, const DeviceIn
   if (d <= kLayerWarpWidth) {
     const void* fn = p.drop.rng ? reinterpret_cast<const void*>(layer_norm_bwd_warp_kernel<T, V, true>)
                                 : reinterpret_cast<const void*>(layer_norm_bwd_warp_kernel<T, V, false>);
-    return run_walkers<T>(p, fn, 4ull * static_cast<uint64_t>(dev.sm_count), kNormWarps, kNormWarps * 32, 0, stream);
+    return run_walkers<T>(p, fn, 4ull * static_cast<uint64_t>(dev.sm_count), kNormWarps, kNormWarps * 32, 0, stream, dev);
   }
   if constexpr (V > 1) {
     if (run_ring<T, kLayerCols<T>, false>(p, stream, dev, &e)) return e;
@@ -410,8 +422,12 @@ cudaError_t run_width(LayerNormBwdParams& p, cudaStream_t stream, const DeviceIn
     rows.add(p.dx, static_cast<uint64_t>(d) * sizeof(T));
     rows.add(p.dy, static_cast<uint64_t>(d) * sizeof(T));
     if (rows.alike) {
-      // 8 columns a thread leave more CTAs an SM (16384 x 1531 bf16 53 us, with 16 67; with dropout 87, 96).
-      if (run_ring<T, 8, true>(p, stream, dev, &e, rows.period())) return e;
+      // 8 columns a thread (21916 x 1531 bf16 67 us, with 16 89; with dropout 113, 127), but not where that
+      // makes a little over 256 threads, one CTA an SM (16376 x 2049 90 us, with 16 columns 74; with dropout
+      // 147, 112; 13102 x 2561, 352 threads, 73, 80; fp32 with dropout 79, 92).
+      const uint32_t threads = (d + kPieceOf<T> - 1 + 255) / 256 * 32;
+      const bool one_cta = sizeof(T) == 2 && threads > 256 && threads <= 320;
+      if (!one_cta && run_ring<T, 8, true>(p, stream, dev, &e, rows.period())) return e;
       if (run_ring<T, kLayerWideCols, true>(p, stream, dev, &e, rows.period())) return e;
     }
   }
