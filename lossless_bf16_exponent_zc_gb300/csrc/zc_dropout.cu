@@ -1,8 +1,10 @@
 // zc_dropout.cu -- dropout with a mask that is never stored (zc_dropout.cuh), and the residual
 // addition behind it in the same pass:  out = a residual + D(x),  D(x) = x / (1 - p) where kept.
 //
-// The gradient of x is the dropout of out's gradient with the same seed, offset and call.  Bound by
-// memory, and next by the generator's instructions.
+// The gradient of x is the dropout of out's gradient with the same seed, offset and call.  Drawing twice
+// costs instructions where a stored mask would cost memory: 16384 x 4096 with a residual bf16 59.4 us and
+// fp32 116 (the copy's rate, 6.8 and 6.9 TB/s; 58% of the issue slots), bf16 without one 43 (92%; 67% of the
+// issue slots).
 #include "zc_dropout.cuh"
 #include "zc_internal.h"
 
@@ -108,8 +110,8 @@ struct AnyEight {
 // aligned piece on, or a column outside those (the ones behind the last piece, then the ones before
 // the first).  Eight such columns lie in two of the generator's groups: every lane draws one and
 // takes the second from the lane above, through shared memory, the last lane drawing for its
-// neighbour alone.  ALIKE: the
-// rows of all matrices start equally far into a piece.
+// neighbour alone.  ALIKE: the rows of all matrices start equally far into a piece.  16384 x 4095 bf16
+// with a residual 76 us (78% of the copy's rate, 62% of the issue slots at 42% of the warps), fp32 116.
 constexpr uint32_t kDropAnyUnits = 31;
 template <typename T, bool RESIDUAL, bool ALIKE, int TURNS>
 __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(DropoutParams p, Divisor shares) {

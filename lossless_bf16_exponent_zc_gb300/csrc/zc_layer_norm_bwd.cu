@@ -5,6 +5,11 @@
 // and over the rows  dw = sum dh n,  db = sum dh.  The forward pass has left m and r, so a row takes
 // two sums and one barrier.  D keeps what it kept before, drawn again from the counters
 // (zc_dropout.cuh).
+//
+// Bound by memory where rows are whole 16-byte pieces: 16384 x 4096 bf16 with dropout 111 us (90% of the
+// copy's rate), without 85 (93%), fp32 with dropout 230 (86%).  Off 16 bytes by the instructions that shift
+// pieces: 16384 x 1531 bf16 with dropout 87 us, fp32 88.  With few rows the second launch, which adds the
+// CTAs' sums, weighs as much as the first: 2331 x 1531 fp32 16 us, 64 x 4096 bf16 7.4.
 #include "zc_layer_norm.cuh"
 
 namespace zc {
@@ -12,7 +17,8 @@ namespace zc {
 namespace {
 
 // Columns of a thread in NV pieces, over all rows of its CTA; the sums of its columns stay in
-// registers until the end.
+// registers until the end.  For what the ring does not hold (4096 x 16384 bf16 with dropout 211 us, 47% of
+// the copy's rate; off 16 bytes, value by value, 4096 x 8191 410).
 template <typename T, int V, int NV, bool DROP, int THREADS>
 __global__ void __launch_bounds__(THREADS) layer_norm_bwd_kernel(LayerNormBwdParams p) {
   constexpr bool kBits = DROP && V == 1;  // values one by one: a row's bits lie in shared memory
@@ -94,7 +100,8 @@ __global__ void __launch_bounds__(THREADS) layer_norm_bwd_kernel(LayerNormBwdPar
     }
 }
 
-// The gradient's ring: three matrices, or two where nothing reaches x' but through h.
+// The gradient's ring: three matrices, or two where nothing reaches x' but through h.  4096 columns of 16
+// bits take two CTAs an SM of 256 threads, whose 122 registers hold 16 columns' sums, weights and a row.
 template <typename T, int V, int C, bool SHIFT, bool DROP>
 __global__ void __launch_bounds__(kNormRingThreads, 1) layer_norm_bwd_ring_kernel(LayerNormBwdParams p) {
   constexpr int P = C / 2, kStages = kLayerBwdStages<T, C>;
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) layer_norm_bwd_ring_kerne
 }
 
 // Narrow rows: every warp walks rows of its own, the next one's loads under way while it computes; a
-// CTA adds its warps' sums at the end.
+// CTA adds its warps' sums at the end (65536 x 256 bf16 with dropout 38.6 us, 64% of the copy's rate).
 constexpr uint32_t kLayerWarpWidth = 256;
 template <typename T, int V, bool DROP>
 __global__ void __launch_bounds__(kNormWarps * 32) layer_norm_bwd_warp_kernel(LayerNormBwdParams p) {

@@ -32,8 +32,8 @@ def new_rng(seed: int, offset: int = 0, device="cuda") -> torch.Tensor:
 
 def dropout(x: torch.Tensor, p: float, rng: torch.Tensor, call: int = 0, *, residual: torch.Tensor | None = None,
             residual_scale: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """residual_scale * residual + x where kept, times 1 / (1 - p), p rounded to 2^-16.  x: [rows, width].  out may be x
-    or residual itself where that is contiguous."""
+    """residual_scale * residual + dropout(x): a value of x, [rows, width], is kept and multiplied by 1 / (1 - p), p
+    rounded to 2^-16, or becomes zero.  out may be x or residual itself where that is contiguous."""
     return zc.native().dropout(x, p, rng, call, residual, residual_scale, out, stream)[0]
 
 
