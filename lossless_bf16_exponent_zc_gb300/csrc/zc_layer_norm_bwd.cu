@@ -102,8 +102,11 @@ __global__ void __launch_bounds__(THREADS) layer_norm_bwd_kernel(LayerNormBwdPar
 
 // The gradient's ring: three matrices, or two where nothing reaches x' but through h.  4096 columns of 16
 // bits take two CTAs an SM of 256 threads, whose 122 registers hold 16 columns' sums, weights and a row.
-template <typename T, int V, int C, bool SHIFT, bool DROP>
-__global__ void __launch_bounds__(kNormRingThreads, 1) layer_norm_bwd_ring_kernel(LayerNormBwdParams p) {
+// PAIR: 80 registers a thread, so that an SM holds two CTAs of up to kLayerPairThreads.
+constexpr int kLayerPairThreads = 384;
+template <typename T, int V, int C, bool SHIFT, bool DROP, bool PAIR>
+__global__ void __launch_bounds__(PAIR ? kLayerPairThreads : kNormRingThreads, PAIR ? 2 : 1)
+    layer_norm_bwd_ring_kernel(LayerNormBwdParams p) {
   constexpr int P = C / 2, kStages = kLayerBwdStages<T, C>;
   constexpr int kH = 0, kX = 1, kPast = 2;
   using Ring = RowRing<T, V, C, 3, kStages, SHIFT>;
@@ -396,8 +399,17 @@ bool run_ring(LayerNormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev,
   const bool drop = p.drop.rng != nullptr;
   const int smem = static_cast<int>(RowRing<T, V, C, 3, kLayerBwdStages<T, C>>::bytes(threads)) +
                    (drop ? KeepColumns<V, C / V, SHIFT>::keep_bytes(threads) : 0);
-  const void* fn = drop ? reinterpret_cast<const void*>(layer_norm_bwd_ring_kernel<T, V, C, SHIFT, true>)
-                        : reinterpret_cast<const void*>(layer_norm_bwd_ring_kernel<T, V, C, SHIFT, false>);
+  const void* fn = drop ? reinterpret_cast<const void*>(layer_norm_bwd_ring_kernel<T, V, C, SHIFT, true, false>)
+                        : reinterpret_cast<const void*>(layer_norm_bwd_ring_kernel<T, V, C, SHIFT, false, false>);
+  // 8 16-bit columns of more than 256 threads: with more registers an SM holds one such CTA (13102 x 2561 bf16
+  // 63 us, one CTA 73, 16 columns a thread 80; with dropout 98, 119, 110).  Smaller CTAs lose by it (87154 x 385
+  // 98 us instead of 73, 43633 x 769 72 and 69, with dropout 162 and 125, 115 and 115), and of fp32 shared
+  // memory holds no more.
+  if constexpr (C == 8 && sizeof(T) == 2) {
+    if (threads > 256 && threads <= kLayerPairThreads)
+      fn = drop ? reinterpret_cast<const void*>(layer_norm_bwd_ring_kernel<T, V, C, SHIFT, true, true>)
+                : reinterpret_cast<const void*>(layer_norm_bwd_ring_kernel<T, V, C, SHIFT, false, true>);
+  }
   static_assert(kLayerBwdStages<T, C> * 3 * kNormRingThreads * C * sizeof(T) +
                         KeepColumns<V, C / V, SHIFT>::keep_bytes(kNormRingThreads) <=
                     kNormRingSmem,
@@ -434,12 +446,8 @@ cudaError_t run_width(LayerNormBwdParams& p, cudaStream_t stream, const DeviceIn
     rows.add(p.dx, static_cast<uint64_t>(d) * sizeof(T));
     rows.add(p.dy, static_cast<uint64_t>(d) * sizeof(T));
     if (rows.alike) {
-      // 8 columns a thread (21916 x 1531 bf16 67 us, with 16 89; with dropout 113, 127), but not where that
-      // makes a little over 256 threads, one CTA an SM (16376 x 2049 90 us, with 16 columns 74; with dropout
-      // 147, 112; 13102 x 2561, 352 threads, 73, 80; fp32 with dropout 79, 92).
-      const uint32_t threads = (d + kPieceOf<T> - 1 + 255) / 256 * 32;
-      const bool one_cta = sizeof(T) == 2 && threads > 256 && threads <= 320;
-      if (!one_cta && run_ring<T, 8, true>(p, stream, dev, &e, rows.period())) return e;
+      // 8 columns a thread (21916 x 1531 bf16 67 us, with 16 89; with dropout 113, 127)
+      if (run_ring<T, 8, true>(p, stream, dev, &e, rows.period())) return e;
       if (run_ring<T, kLayerWideCols, true>(p, stream, dev, &e, rows.period())) return e;
     }
   }
