@@ -106,11 +106,22 @@ struct AnyEight {
   }
 };
 
+// 2 W 16-bit values from value `first` on of a run of them in shared memory (4-byte aligned, and the word
+// behind them may be read).
+template <int W>
+__device__ __forceinline__ void load_bits(const uint32_t* run, uint32_t first, uint32_t (&bits)[W]) {
+  uint32_t w[W + 1];
+#pragma unroll
+  for (int j = 0; j <= W; j++) w[j] = run[first / 2 + j];
+#pragma unroll
+  for (int j = 0; j < W; j++) bits[j] = __funnelshift_r(w[j], w[j + 1], (first & 1) * 16);
+}
+
 // Rows off 16 bytes.  A warp takes TURNS times 31 units of a row of the output: eight columns from an
 // aligned piece on, or a column outside those (the ones behind the last piece, then the ones before
 // the first).  Eight such columns lie in two of the generator's groups: every lane draws one and
 // takes the second from the lane above, through shared memory, the last lane drawing for its
-// neighbour alone.  ALIKE: the rows of all matrices start equally far into a piece.  16384 x 4095 bf16
+// neighbour alone.  (Selecting among the words of both groups took 79 us where this takes 76.)  ALIKE: the rows of all matrices start equally far into a piece.  16384 x 4095 bf16
 // with a residual 76 us (78% of the copy's rate, 62% of the issue slots at 42% of the warps), fp32 116.
 constexpr uint32_t kDropAnyUnits = 31;
 template <typename T, bool RESIDUAL, bool ALIKE, int TURNS>
