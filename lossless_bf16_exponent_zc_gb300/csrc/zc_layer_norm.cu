@@ -252,6 +252,18 @@ bool run_ring(LayerNormParams& p, cudaStream_t stream, const DeviceInfo& dev, cu
   return true;
 }
 
+template <typename T, bool SHIFT>
+bool run_ring(LayerNormParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e, uint64_t period = 1) {
+  if constexpr (sizeof(T) == 4) {
+    // 8 columns a thread of wide fp32 rows, where a CTA of them is large enough to draw beside its copies (4096 x
+    // 4096 with dropout 45 us, with 16 columns 48; 2331 x 1531 alone 8.2, 8.8), but 16 otherwise (16384 x 1024 with
+    // dropout 47 us, with 8 51; off 16 bytes 43577 x 385 50, 76; 8188 x 2049 48, 64; 4111 x 4081 50, 61).
+    if (p.y ? !SHIFT && p.hidden > 2048 : p.hidden > 1024)
+      if (run_ring<T, 8, SHIFT>(p, stream, dev, e, period)) return true;
+  }
+  return run_ring<T, kLayerWideCols, SHIFT>(p, stream, dev, e, period);
+}
+
 template <typename T, int V>
 cudaError_t run_width(LayerNormParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   const uint32_t d = p.hidden;
@@ -261,25 +273,14 @@ cudaError_t run_width(LayerNormParams& p, cudaStream_t stream, const DeviceInfo&
   if (d <= 256) return run_shape<T, V, 8 / V, true, kWarp>(p, kWarp, stream, dev);
   cudaError_t e;
   if constexpr (V > 1) {
-    if (run_ring<T, kLayerCols<T>, false>(p, stream, dev, &e)) return e;
-    if constexpr (kLayerCols<T> != kLayerWideCols) {
-      if (run_ring<T, kLayerWideCols, false>(p, stream, dev, &e)) return e;
-    }
+    if (run_ring<T, false>(p, stream, dev, &e)) return e;
   } else {
     RowPlaces rows;
     rows.add(p.x, p.x_stride * sizeof(T));
     rows.add(p.y, p.y_stride * sizeof(T));
     rows.add(p.x_new, static_cast<uint64_t>(d) * sizeof(T));
     rows.add(p.h, static_cast<uint64_t>(d) * sizeof(T));
-    if (rows.alike) {
-      // fp32 rows of 8 columns a thread that take more than 384 threads leave one CTA an SM, too few to draw in:
-      // with dropout 4111 x 4081 61 us, with 16 columns 50 (without 48 and 50; 5590 x 3001, two CTAs, 54).
-      const bool few = kLayerCols<T> == 8 && p.drop.rng && d + kPieceOf<T> - 1 > 384 * 8;
-      if (!few && run_ring<T, kLayerCols<T>, true>(p, stream, dev, &e, rows.period())) return e;
-      if constexpr (kLayerCols<T> != kLayerWideCols) {
-        if (run_ring<T, kLayerWideCols, true>(p, stream, dev, &e, rows.period())) return e;
-      }
-    }
+    if (rows.alike && run_ring<T, true>(p, stream, dev, &e, rows.period())) return e;
   }
   // Wider still, or rows that start elsewhere in one matrix than in another: a CTA holds a row in
   // registers.

@@ -7,8 +7,8 @@
 namespace zc {
 
 // The ring's shapes.  A thread has 16 columns of a row of 16-bit values (8 in twice the threads:
-// 16384 x 4096 bf16 with dropout 100 us forward and 118 back, with 16 94 and 110), of fp32 values 8,
-// and 16 where 8 of each of 512 threads do not hold the row.
+// 16384 x 4096 bf16 with dropout 100 us forward and 118 back, with 16 94 and 110); in the gradient of
+// fp32 ones 8, and 16 where 8 of each of 512 threads do not hold the row.
 template <typename T>
 constexpr int kLayerCols = sizeof(T) == 2 ? 16 : 8;
 constexpr int kLayerWideCols = 16;
