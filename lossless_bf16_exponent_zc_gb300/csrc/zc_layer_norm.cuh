@@ -6,11 +6,9 @@
 
 namespace zc {
 
-// The ring's shapes.  A thread has 16 columns of a row of 16-bit values (8 in twice the threads:
-// 16384 x 4096 bf16 with dropout 100 us forward and 118 back, with 16 94 and 110); in the gradient of
-// fp32 ones 8, and 16 where 8 of each of 512 threads do not hold the row.
-template <typename T>
-constexpr int kLayerCols = sizeof(T) == 2 ? 16 : 8;
+// The ring's shapes.  A thread has 16 columns of a row of 16-bit values (8 in twice the threads: 16384 x
+// 4096 bf16 with dropout 100 us forward and 118 back, with 16 94 and 110), or 8 where the launches' rules
+// find them faster.
 constexpr int kLayerWideCols = 16;
 // Stages, forward and back: more of them move no more bytes a second, for reads and writes share the
 // memory's bus (forward, 16 columns: 4 stages 96 us, 3 95, 2 91 to 94; without a branch 48, 48, 49.5;

@@ -434,10 +434,13 @@ cudaError_t run_width(LayerNormBwdParams& p, cudaStream_t stream, const DeviceIn
     return run_walkers<T>(p, fn, 4ull * static_cast<uint64_t>(dev.sm_count), kNormWarps, kNormWarps * 32, 0, stream, dev);
   }
   if constexpr (V > 1) {
-    if (run_ring<T, kLayerCols<T>, false>(p, stream, dev, &e)) return e;
-    if constexpr (kLayerCols<T> != kLayerWideCols) {
-      if (run_ring<T, kLayerWideCols, false>(p, stream, dev, &e)) return e;
-    }
+    // 8 columns a thread of fp32 rows (10922 x 1536 with dropout 58 us, with 16 67), of narrow 16-bit ones and of
+    // few: with dropout 65536 x 512 bf16 59 us, with 16 columns 83, 32768 x 1024 61 and 61, 2331 x 1536 12.6 and
+    // 14.8, 64 x 4096 6.0 and 7.4.  16 of the others, which have room for more on their way: 21845 x 1536 61 us,
+    // with 8 columns 66, 8192 x 4096 58 and 63.
+    if (sizeof(T) == 4 || d <= 1024 || p.tokens <= 16ull * static_cast<uint64_t>(dev.sm_count))
+      if (run_ring<T, 8, false>(p, stream, dev, &e)) return e;
+    if (run_ring<T, kLayerWideCols, false>(p, stream, dev, &e)) return e;
   } else {
     RowPlaces rows;
     rows.add(p.dh, p.dh_stride * sizeof(T));

@@ -1,6 +1,7 @@
 // zc_torch.cpp -- Python entry points of the operators around an expert-parallel exchange and of the
-// training step around it (moe.py, norm.py, dropout.py, embedding.py): torch tensors in, checked, outputs allocated by torch, and one call of the C ABI
-// (include/zc.h) on the current torch stream or the one given.  Argument marshalling only, as zc.py
+// training step around it (moe.py, norm.py, dropout.py, embedding.py): torch tensors in, checked, outputs
+// allocated by torch, and one call of the C ABI (include/zc.h) on the current torch stream or the one
+// given.  Argument marshalling only, as zc.py
 // does with ctypes; native because these operators run for a few microseconds in a decoding step,
 // where five allocations, a dozen attributes and a ctypes call in Python cost more than the kernels
 // (route of 8 tokens: 9.5 us of host time in Python).

@@ -13,8 +13,10 @@ operators are defined); arguments are checked, and outputs that are not given al
     x, h, _ = norm.add_layer_norm(block(h), x, next_weight, next_bias, p=0.1, rng=rng, call=layer)
 
 add_layer_norm drops out a block's output (dropout.py), adds it to the scaled residual stream and takes the next block's
-norm, in one pass: zc_layer_norm and zc_layer_norm_backward.  Activations are bfloat16, float16 or float32 matrices whose rows may be strided; weights and gate
-share a type, the activations' or float32.
+norm, in one pass: zc_layer_norm and zc_layer_norm_backward.
+
+Activations are bfloat16, float16 or float32 matrices whose rows may be strided; weights, biases and gates share a type,
+the activations' or float32.
 
 Calls run on the current torch stream, or on the one given as ``stream``.  On a given stream, what it reads and the
 outputs it is handed must be ready there (``stream.wait_stream(...)``) and stay alive until it has run; outputs it makes

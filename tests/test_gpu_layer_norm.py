@@ -237,6 +237,30 @@ def test_many_rows_a_walker(norm, dtype, width):
     assert torch.equal(g.dy, mask) and torch.equal(g.dx, y)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", [(40, 2049), (5000, 2049), (40, 3001), (4001, 3001), (3000, 3066), (2431, 1536), (2600, 1536),
+                                        (2600, 2560), (2433, 4096), (6000, 520), (9001, 1000), (5000, 385), (3000, 3200)])
+@pytest.mark.parametrize("p", [0.0, 0.35])
+def test_shapes_for_few_and_many_rows(norm, dtype, rows, width, p):
+    """A walker has one row, several or many of them, in CTAs of all sizes."""
+    from lossless_bf16_exponent_zc_gb300 import dropout
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    y, x, dh, past = (torch.randn((rows, width), device="cuda", generator=g).to(dtype) for _ in range(4))
+    w, b = (torch.randn(width, device="cuda", generator=g) for _ in range(2))
+    keep, factor = kept(rows, width, p, width, rows, 3) if p else (None, 1.0)
+    kw = dict(p=p, rng=dropout.new_rng(width, rows) if p else None, call=3)
+    x_new, h, stats = norm.add_layer_norm(y, x, w, b, save=True, **kw)
+    branch = y.double() * (keep * factor if p else 1.0)
+    want = x.double() + branch
+    off = 3 * U * (x.double().abs() + branch.abs())
+    within(x_new, want, off)
+    check_forward(h, stats, want, off, w, b)
+    got = norm.add_layer_norm_backward(past, dh, x_new, stats, w, norm.workspace(rows, width), **kw)
+    check_backward(got, past, dh, x_new, stats, w, 1.0, keep, factor)
+    alone, stats = norm.layer_norm(x, w, b, save=True)
+    check_forward(alone, stats, x.double(), torch.zeros_like(x, dtype=torch.float64), w, b)
+
+
 def test_no_tokens(norm):
     x, w = torch.zeros((0, 40), device="cuda"), torch.ones(40, device="cuda")
     h, stats = norm.layer_norm(x, w, save=True)
