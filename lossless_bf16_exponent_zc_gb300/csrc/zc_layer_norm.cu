@@ -9,7 +9,8 @@
 //
 // Bound by memory where rows are whole 16-byte pieces: 16384 x 4096 bf16 behind a dropped-out branch 92.5 us
 // (86% of the copy's rate), fp32 162 (98%), 8192 x 8192 bf16 85 (94%), the norm alone 48 (83%).  Off 16 bytes
-// by instructions: 16384 x 1531 bf16 with dropout 55 us, fp32 76.  8 rows of 4096: 2.1 us.
+// by instructions: 21916 x 1531 bf16 with dropout 70 us (56%), without 52; fp32 10958 x 1531 50 (80%).  8 rows
+// of 4096: 2.1 us.
 #include "zc_layer_norm.cuh"
 
 namespace zc {

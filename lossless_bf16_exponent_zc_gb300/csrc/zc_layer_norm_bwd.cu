@@ -8,8 +8,9 @@
 //
 // Bound by memory where rows are whole 16-byte pieces: 16384 x 4096 bf16 with dropout 111 us (90% of the
 // copy's rate), without 85 (93%), fp32 with dropout 230 (86%).  Off 16 bytes by the instructions that shift
-// pieces: 16384 x 1531 bf16 with dropout 87 us, fp32 88.  With few rows the second launch, which adds the
-// CTAs' sums, weighs as much as the first: 2331 x 1531 fp32 16 us, 64 x 4096 bf16 7.4.
+// pieces and trade the dropout's bits: 21916 x 1531 bf16 with dropout 110 us (45%), without 67 (59%), fp32 10958
+// x 1531 61 and 50 (82, 80%).  With few rows the second launch, which adds the CTAs' sums, weighs as much as
+// the first: 2331 x 1531 fp32 16 us, 64 x 4096 bf16 6.0.
 #include "zc_layer_norm.cuh"
 
 namespace zc {
@@ -357,8 +358,8 @@ template <typename T>
 cudaError_t add_parts(LayerNormBwdParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   void* args[] = {&p};
   // 8 columns a CTA where that makes no more than two of them an SM: with 32 the narrow rows, which have
-  // the most parts, leave most SMs idle (both launches, 4096 x 512 bf16 14.3 us, with 8 columns 12.2;
-  // 1024 x 1024 11.2 and 8.4).  Wider rows are as fast with 16 and 32.
+  // the most parts, leave most SMs idle (4096 x 512 bf16 takes 2.1 us longer, 1024 x 1024 2.8).  Wider rows are
+  // as fast with 16 and 32.
   const uint32_t sums = p.dbias ? 2 : 1, eights = (p.hidden + 7) / 8;
   const bool narrow = eights * sums <= 2 * static_cast<uint32_t>(dev.sm_count);
   return launch_kernel(narrow ? reinterpret_cast<const void*>(layer_norm_parts_kernel<T, 8>)
@@ -372,8 +373,8 @@ cudaError_t run_walkers(LayerNormBwdParams& p, const void* fn, uint64_t most, ui
   if (most > norm_max_walkers(p.hidden)) most = norm_max_walkers(p.hidden);
   const uint64_t ctas = (p.tokens + rows_a_cta - 1) / rows_a_cta;
   // Of few turns none is for a part of the CTAs alone: fewer sums to add up (1024 x 4096 bf16 with dropout,
-  // 256 CTAs instead of 304, 15.3 us, not 16.2).  Of many that costs more warps than it saves (65536 x 256,
-  // 14 turns, 40.4 us, not 38.6).
+  // 256 CTAs instead of 304, 0.9 us less).  Of many that costs more warps than it saves (65536 x 256, 14 turns,
+  // 40.4 us, not 38.6).
   const uint64_t turns = (ctas + most - 1) / most;
   if (turns <= 8) most = ((ctas + turns - 1) / turns + period - 1) / period * period;
   p.ctas = static_cast<uint32_t>(ctas < most ? ctas : most);
