@@ -244,13 +244,17 @@ template <typename T, int C, bool SHIFT>
 bool run_ring(LayerNormParams& p, cudaStream_t stream, const DeviceInfo& dev, cudaError_t* e, uint64_t period = 1) {
   const int threads = static_cast<int>((p.hidden + (SHIFT ? kPieceOf<T> - 1 : 0) + C * 32 - 1) / (C * 32) * 32);
   if (threads > kNormRingThreads) return false;
-  if (p.drop.rng)
-    *e = run_ring<T, C, SHIFT, true, true>(p, threads, period, stream, dev);
-  else if (p.y)
-    *e = run_ring<T, C, SHIFT, true, false>(p, threads, period, stream, dev);
-  else
+  if (!p.y) {
     *e = run_ring<T, C, SHIFT, false, false>(p, threads, period, stream, dev);
-  return true;
+    return true;
+  }
+  if constexpr (C == 8 && SHIFT) {
+    return false;  // never asked for (below)
+  } else {
+    *e = p.drop.rng ? run_ring<T, C, SHIFT, true, true>(p, threads, period, stream, dev)
+                    : run_ring<T, C, SHIFT, true, false>(p, threads, period, stream, dev);
+    return true;
+  }
 }
 
 template <typename T, bool SHIFT>
@@ -285,7 +289,9 @@ cudaError_t run_width(LayerNormParams& p, cudaStream_t stream, const DeviceInfo&
   }
   // Wider still, or rows that start elsewhere in one matrix than in another: a CTA holds a row in
   // registers.
-  if (d <= 4096) return run_shape<T, V, 8 / V, false, 512>(p, static_cast<int>((d + 255) / 256 * 32), stream, dev);
+  if constexpr (V == 1) {
+    if (d <= 4096) return run_shape<T, V, 8, false, 512>(p, static_cast<int>((d + 255) / 256 * 32), stream, dev);
+  }
   return run_shape<T, V, 16 / V, false, 1024>(p, static_cast<int>((d + 511) / 512 * 32), stream, dev);
 }
 

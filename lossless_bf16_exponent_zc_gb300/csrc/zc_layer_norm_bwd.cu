@@ -455,7 +455,9 @@ cudaError_t run_width(LayerNormBwdParams& p, cudaStream_t stream, const DeviceIn
       if (run_ring<T, kLayerWideCols, true>(p, stream, dev, &e, rows.period())) return e;
     }
   }
-  if (d <= 4096) return run_shape<T, V, 8 / V, 512>(p, static_cast<int>((d + 255) / 256 * 32), stream, dev);
+  if constexpr (V == 1) {
+    if (d <= 4096) return run_shape<T, V, 8, 512>(p, static_cast<int>((d + 255) / 256 * 32), stream, dev);
+  }
   return run_shape<T, V, 16 / V, 1024>(p, static_cast<int>((d + 511) / 512 * 32), stream, dev);
 }
 
