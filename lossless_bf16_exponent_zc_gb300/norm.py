@@ -133,6 +133,6 @@ def add_layer_norm_backward(dx_new: torch.Tensor | None, dh: torch.Tensor, x_new
                             stream=None) -> AddLayerNormGrads:
     """Gradients of add_layer_norm from those of its outputs (dx_new: what reaches x_new other than through h; None:
     nothing), the saved x_new and stats, and the p, rng and call of the forward call, rng's values unchanged.  Without
-    dropout and with a residual_scale of 1 dy and dx are one tensor."""
+    dropout and with a residual_scale of 1 (as float32, which the kernels take) dy and dx are one tensor."""
     return AddLayerNormGrads(*zc.native().layer_norm_backward(dx_new, dh, x_new, stats, weight, bias, p, rng, call,
                                                               residual_scale, True, ws, stream))

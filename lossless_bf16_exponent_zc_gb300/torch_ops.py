@@ -43,6 +43,8 @@ state must not change between a call and its gradient (autograd notices):
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import dropout, embedding, moe, norm, zc
@@ -450,7 +452,7 @@ def layer_norm_backward(dx_new: torch.Tensor | None, dh: torch.Tensor, x_new: to
 
 
 def _own_dy(p, residual_scale):
-    return p > 0 or residual_scale != 1.0
+    return p > 0 or ctypes.c_float(residual_scale).value != 1.0  # the extension's rule: of the scale that the kernel gets
 
 
 @layer_norm_backward.register_fake

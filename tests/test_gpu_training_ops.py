@@ -343,3 +343,21 @@ def test_from_several_threads(zc):
         assert len(got[seed]) == 30
         for run in got[seed]:
             assert all(torch.equal(a, b) for a, b in zip(run, want[seed][0]))
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("scale", [1 + 2**-40, 2**0.5 * 0.5**0.5, 0.99999999])
+def test_a_residual_scale_that_is_one_in_fp32(zc, bias, scale):
+    """The kernels take the scale as fp32: gradients like those of a scale of 1, which has one tensor for dy and dx."""
+    args = (leaf(10, 24), leaf(10, 24), leaf(24), leaf(24) if bias else None, None, 0.0, 0)
+    torch.library.opcheck(ops.add_layer_norm, (*args, scale, 1e-5))
+    gx, gh = torch.randn((10, 24), device="cuda"), torch.randn((10, 24), device="cuda")
+    made = []
+    for s in (scale, 1.0):
+        for a in args[:4]:
+            if a is not None:
+                a.grad = None
+        x_new, h, _ = ops.add_layer_norm(*args, s, 1e-5)
+        torch.autograd.backward([x_new, h], [gx, gh])
+        made.append([x_new, h, *(a.grad for a in args[:4] if a is not None)])
+    assert all(torch.equal(a, b) for a, b in zip(*made))

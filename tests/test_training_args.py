@@ -288,3 +288,16 @@ def test_wrong_values(fake):
         norm.layer_norm(t["x"], None)
     with pytest.raises(zc.ZcError):
         embedding.lookup_backward(t["dout"], t["ids"], 1 << 31, t["ws"], t["status"])
+
+
+SCALES_OF_ONE = [1 + 2**-40, 2**0.5 * 0.5**0.5, 0.99999999]  # 1 as float32, which is what the kernels take
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("scale,own", [*((s, False) for s in SCALES_OF_ONE), (1.0, False), (1 + 2**-22, True), (0.5, True)])
+def test_a_scale_of_one_after_rounding_has_one_gradient(fake, bias, scale, own):
+    """The operator's list as the native call makes it: dy is dx where the scale that the kernel gets is 1."""
+    from lossless_bf16_exponent_zc_gb300 import torch_ops  # noqa: F401
+    t = tensors("cuda:0")
+    got = torch.ops.zc.layer_norm_backward(None, t["dout"], t["x"], t["stats"], t["w"], bias, None, 0.0, 0, scale)
+    assert [g.shape for g in got] == [t["x"].shape, t["w"].shape] + [t["x"].shape] * own + [t["w"].shape] * bias
