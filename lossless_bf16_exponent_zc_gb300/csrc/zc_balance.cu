@@ -29,8 +29,10 @@ constexpr int kBalanceWarps = N <= 16 ? 16 : 8;
 constexpr int kBackWarps = 8;
 
 // A row's p, from its logits in l; false, and p all zero, where no logit is above minus infinity.
-// `raw` gets the exponentials or the sigmoids, `inv` the reciprocal of their sum.
-template <int N>
+// `raw` gets the exponentials or the sigmoids, `inv` the reciprocal of their sum.  SLOPE: in place of the
+// sigmoids s their derivatives s (1 - s), in which 1 - s = e s with e = exp(-logit) where the logit is above
+// zero: a difference from 1 would keep no bits of it from a logit of 17 on (at 10 it is off by 2^-11).
+template <int N, bool SLOPE>
 __device__ __forceinline__ bool probabilities(float (&l)[N], bool sigmoid_score, float (&raw)[N], float* inv) {
   float best = l[0];
 #pragma unroll
@@ -39,7 +41,11 @@ __device__ __forceinline__ bool probabilities(float (&l)[N], bool sigmoid_score,
   float sum = 0.f;
   if (sigmoid_score) {
 #pragma unroll
-    for (int j = 0; j < N; j++) raw[j] = __fdividef(1.f, 1.f + expf(-l[j]));  // 1 / infinity: zero
+    for (int j = 0; j < N; j++) {
+      const float e = expf(-l[j]), s = __fdividef(1.f, 1.f + e);  // 1 / infinity: zero
+      raw[j] = s;
+      if (SLOPE) l[j] = s * (l[j] > 0.f ? e * s : 1.f - s);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < N; j++) raw[j] = l[j] == -INFINITY ? 0.f : expf(l[j] - top);
@@ -50,7 +56,11 @@ __device__ __forceinline__ bool probabilities(float (&l)[N], bool sigmoid_score,
   const bool any = top > -INFINITY || sum != sum;
   *inv = any ? 1.f / sum : 0.f;
 #pragma unroll
-  for (int j = 0; j < N; j++) l[j] = any ? raw[j] * *inv : 0.f;
+  for (int j = 0; j < N; j++) {
+    const float q = any ? raw[j] * *inv : 0.f;
+    if (SLOPE && sigmoid_score) raw[j] = l[j];
+    l[j] = q;
+  }
   return any;
 }
 
@@ -82,7 +92,7 @@ __device__ __forceinline__ uint32_t add_tokens(const BalanceParams& p, uint64_t 
     const int32_t id = next_id;
     const bool in = next_in;
     if (kAhead) load(t + step);
-    if (!in || !probabilities<N>(l, p.sigmoid, raw, &inv)) continue;
+    if (!in || !probabilities<N, false>(l, p.sigmoid, raw, &inv)) continue;
     counted++;
 #pragma unroll
     for (int j = 0; j < N; j++) acc[j] += l[j];
@@ -292,7 +302,7 @@ __global__ void __launch_bounds__(kBackWarps * 32) balance_bwd_kernel(BalanceBwd
   load_row<T, N, VEC>(static_cast<const T*>(p.logits) + t * p.stride, p.experts, l);
   load_row<float, N, VEC>(p.slope + t / p.seq_tokens * p.experts, p.experts, c);
   const float g = *p.dloss;
-  const bool any = probabilities<N>(l, p.sigmoid, raw, &inv);
+  const bool any = probabilities<N, true>(l, p.sigmoid, raw, &inv);
   float mean = 0.f;
 #pragma unroll
   for (int j = 0; j < N; j++) {
@@ -302,7 +312,7 @@ __global__ void __launch_bounds__(kBackWarps * 32) balance_bwd_kernel(BalanceBwd
   mean = warp_sum_f32(mean);
 #pragma unroll
   for (int j = 0; j < N; j++) {
-    const float d = p.sigmoid ? raw[j] * (1.f - raw[j]) * inv : l[j];
+    const float d = p.sigmoid ? raw[j] * inv : l[j];
     l[j] = any ? d * (g * (c[j] - mean)) : 0.f;
   }
   store_row<T, N, VEC>(out, p.experts, l);

@@ -165,3 +165,32 @@ def test_gradient_against_differences(moe):
         along = d / d.norm()
         up, down = (float(moe.balance_loss(logits + s * along, ids, ws, score=score).loss) for s in (2**-6, -2**-6))
         assert abs((up - down) / 2**-5 - float((d * along).sum())) < 2**-12 * float(d.norm()) + 200 * U * 2**5
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [8, 61, 300, 1024])
+def test_the_gradient_of_saturated_sigmoids(moe, dtype, n):
+    """Logits up to 60 either way, where s is 1 to fp32 from 17 on: s (1 - s) keeps its relative error.  With u = 2^-24: of
+    s (1 - s) 12 u (an exponential, a reciprocal and four operations), of the sigmoids' sum 45 u (32 + 5 terms of 4 u), of
+    the mean slope 90 u more; below 250 u of s (1 - s) / Z (c + mean) in all, and half a step of the output.  So a value
+    larger than its room cannot be zero; one in whose row c and the mean agree to 250 u may be."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    logits = (torch.rand((120, n), device="cuda", generator=g) * 50 + 10).to(dtype)
+    logits = torch.where(torch.rand((120, n), device="cuda", generator=g) < 0.3, -logits, logits)
+    logits[0] = torch.linspace(10, 30, n, device="cuda").to(dtype)
+    ids = torch.randint(0, n, (120, 3), device="cuda", generator=g, dtype=torch.int32)
+    ws, dloss = moe.balance_workspace(120, n), torch.tensor(2.0**40, device="cuda")  # normal numbers up to logits of 60
+    slope = moe.balance_loss(logits, ids, ws, score="sigmoid").slope
+    d = moe.balance_loss_backward(dloss, logits, slope, score="sigmoid").double()
+    l, c = logits.double(), slope.double()
+    s, rest = torch.sigmoid(l), torch.sigmoid(-l)
+    z = s.sum(1, keepdim=True) + 1e-20
+    mean = (s / z * c).sum(1, keepdim=True)
+    want, f = 2.0**40 * s * rest / z * (c - mean), torch.finfo(dtype)
+    room = 2.0**40 * s * rest / z * (c + mean) * 250 * U + f.eps / 2 * want.abs() + f.smallest_normal * f.eps
+    past = want.abs() > f.max                                          # fp16: infinite
+    assert bool((((d - want).abs() <= room) | past).all())
+    assert bool(((logits > 17) & (want.abs() > room)).any())           # what a difference from 1 makes zero
+    logits[1::2] = math.inf
+    ends = moe.balance_loss_backward(dloss, logits, slope, score="sigmoid")
+    assert not ends[1::2].any() and torch.equal(ends[::2].double(), d[::2])
