@@ -671,7 +671,8 @@ zc_status zc_norm_backward(const zc_norm_backward_args* h_args, void* stream);
  *   d_loss    fp32: sum over s and e of slope[s][e] * (sum of p[t][e] over the run's tokens that count)
  * that is the mean over the runs of experts * sum_e (fraction of the slots) *
  * (mean probability): 1 for an even load.  Logits of tokens that the mask
- * leaves out are not read.
+ * leaves out are not read.  A workspace serves every batch of up to so many
+ * tokens in up to so many sequences.
  */
 zc_status zc_moe_balance_workspace_size(uint64_t tokens, uint32_t experts, uint64_t sequences, uint64_t* bytes);
 zc_status zc_moe_balance(const void* d_logits, int dtype, uint64_t logits_stride, uint64_t tokens, uint32_t experts,

@@ -390,19 +390,27 @@ struct BalanceCut {
   uint32_t chunks;
   uint64_t chunk_tokens;
 };
+constexpr uint64_t kBalanceMost = 1216;  // chunks of all sequences, if these are not more themselves
+uint64_t least_chunk(uint32_t experts) {
+  return 4 * static_cast<uint64_t>(experts <= 512 ? kBalanceWarps<16> : kBalanceWarps<32>);
+}
 BalanceCut balance_cut(uint64_t tokens, uint32_t experts, uint64_t sequences) {
-  const uint64_t kTokens = 4 * (experts <= 512 ? kBalanceWarps<16> : kBalanceWarps<32>), kMost = 1216;
-  const uint64_t n = tokens / sequences, most = sequences < kMost ? kMost / sequences : 1;
+  const uint64_t n = tokens / sequences, most = sequences < kBalanceMost ? kBalanceMost / sequences : 1;
   uint64_t each = (n + most - 1) / most;
-  each = each < kTokens ? kTokens : each;
+  each = each < least_chunk(experts) ? least_chunk(experts) : each;
   const uint64_t chunks = n ? (n + each - 1) / each : 1;
   return {static_cast<uint32_t>(chunks), each};
 }
 
 }  // namespace
 
+// Room for any batch of up to so many tokens in up to so many sequences.  The chunks themselves become fewer
+// where more tokens lengthen each of them: s sequences of n tokens have at most s n / least + s of them, least
+// being the shortest, and at most kBalanceMost or s.
 uint64_t balance_workspace_bytes(uint64_t tokens, uint32_t experts, uint64_t sequences) {
-  const uint64_t units = sequences * balance_cut(tokens, experts, sequences).chunks;
+  const uint64_t shortest = tokens / least_chunk(experts) + sequences;
+  const uint64_t most = sequences > kBalanceMost ? sequences : kBalanceMost;
+  const uint64_t units = shortest < most ? shortest : most;
   return 16 + 4 * (2 * units * experts + units + sequences * ((experts + 31) / 32));
 }
 

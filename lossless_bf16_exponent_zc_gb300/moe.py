@@ -117,7 +117,8 @@ def balance_workspace_size(tokens: int, num_experts: int, sequences: int = 1) ->
 
 
 def balance_workspace(tokens: int, num_experts: int, sequences: int = 1, device="cuda") -> torch.Tensor:
-    """A workspace for the balance loss of so many tokens; calls that share it must be ordered on one stream."""
+    """A workspace for the balance loss of up to so many tokens in up to so many sequences; calls that share it must be
+    ordered on one stream."""
     return torch.empty(balance_workspace_size(tokens, num_experts, sequences), dtype=torch.uint8, device=device)
 
 

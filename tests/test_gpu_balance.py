@@ -194,3 +194,22 @@ def test_the_gradient_of_saturated_sigmoids(moe, dtype, n):
     logits[1::2] = math.inf
     ends = moe.balance_loss_backward(dloss, logits, slope, score="sigmoid")
     assert not ends[1::2].any() and torch.equal(ends[::2].double(), d[::2])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("tokens,n,k,sequences,dtype", [(81920, 20, 2, 1, torch.bfloat16), (77825, 130, 3, 1, torch.float16),
+                                                        (84000, 33, 2, 7, torch.float32), (40001, 1024, 2, 1, torch.bfloat16),
+                                                        (39000, 600, 4, 2, torch.float32), (250000, 8, 1, 1250, torch.float32)])
+def test_many_tokens(moe, score, tokens, n, k, sequences, dtype):
+    """Chunks of more tokens than the shortest, in one sequence and in several, and more sequences than chunks."""
+    check(moe, *make(tokens, n, k, dtype, 0.2, seed=n), score=score, sequences=sequences, dloss=float(tokens))
+
+
+def test_a_workspace_for_the_largest_batch_serves_smaller_ones(moe):
+    """Fewer tokens may have more chunks: 77824 have the most."""
+    logits, ids = make(90112, 40, 2, torch.float32)
+    ws = moe.balance_workspace(90112, 40, 8)
+    for tokens, sequences in ((90112, 1), (77824, 1), (81920, 8), (77824, 4), (1024, 8), (512, 1), (90112, 8)):
+        want = check(moe, logits[:tokens], ids[:tokens], sequences=sequences)
+        got = moe.balance_loss(logits[:tokens], ids[:tokens], ws, sequences=sequences)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

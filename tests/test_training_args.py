@@ -301,3 +301,17 @@ def test_a_scale_of_one_after_rounding_has_one_gradient(fake, bias, scale, own):
     t = tensors("cuda:0")
     got = torch.ops.zc.layer_norm_backward(None, t["dout"], t["x"], t["stats"], t["w"], bias, None, 0.0, 0, scale)
     assert [g.shape for g in got] == [t["x"].shape, t["w"].shape] + [t["x"].shape] * own + [t["w"].shape] * bias
+
+
+@pytest.mark.parametrize("experts", [8, 256, 512, 513, 1024])
+def test_a_balance_workspace_holds_every_smaller_batch(experts):
+    """Up to so many tokens in up to so many sequences: also where the chunks of a sequence have reached their most."""
+    sizes = [1, 63, 64, 65, 1024, 38911, 38912, 38913, 40000, 60000, 77823, 77824, 77825, 81920, 90112, 155648, 155649,
+             1 << 20, (1 << 20) + 1, 2**31 - 1]
+    need = [moe.balance_workspace_size(t, experts) for t in sizes]
+    assert need == sorted(need)
+    length = 4096                                                       # sequences of one length
+    need = [moe.balance_workspace_size(n * length, experts, n) for n in (1, 2, 7, 19, 20, 304, 608, 609, 1000, 1216, 1217, 5000)]
+    assert need == sorted(need)
+    need = [moe.balance_workspace_size(1 << 20, experts, 1 << n) for n in range(21)]
+    assert need == sorted(need)
