@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 8) embed_kernel(EmbedParams p, 
   const uint64_t t0 = i0 >> 31 ? i0 / pieces.d : pieces(static_cast<uint32_t>(i0));
   const uint32_t c0 = static_cast<uint32_t>(i0 - t0 * pieces.d) + threadIdx.x;
   AnyValues<TT, V, true> v[UNITS];
+  float scale[UNITS];  // zero for no token, whose row stays positive zeros whatever the call's scale
   T* to[UNITS];
 #pragma unroll
   for (int q = 0; q < UNITS; q++) {
@@ -79,10 +80,12 @@ __global__ void __launch_bounds__(kEmbedThreads, 8) embed_kernel(EmbedParams p, 
     const uint64_t t = t0 + dt;
     to[q] = t < p.tokens ? static_cast<T*>(p.out) + t * p.hidden + first : nullptr;
     v[q].clear();
+    scale[q] = 0.f;
     if (!to[q]) continue;
     const int64_t id = id_at(p.ids, p.ids64, t);
-    if (has_row(id, p.vocab, p.status))
-      v[q].load(static_cast<const TT*>(p.table) + static_cast<uint64_t>(id) * p.table_stride + first);
+    if (!has_row(id, p.vocab, p.status)) continue;
+    scale[q] = p.scale;
+    v[q].load(static_cast<const TT*>(p.table) + static_cast<uint64_t>(id) * p.table_stride + first);
   }
 #pragma unroll
   for (int q = 0; q < UNITS; q++) {
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 8) embed_kernel(EmbedParams p, 
     float f[V];
     v[q].get(f);
 #pragma unroll
-    for (int j = 0; j < V; j++) f[j] *= p.scale;
+    for (int j = 0; j < V; j++) f[j] *= scale[q];
     Piece<T, V> o;
     o.set(f);
     o.store(to[q]);
@@ -109,6 +112,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_wide_kernel(EmbedParams p
   const uint32_t c0 = static_cast<uint32_t>(i - t * shares.d) * (32 * UNITS) + lane_id(), pieces = p.hidden / V;
   const int64_t id = id_at(p.ids, p.ids64, t);
   const bool there = has_row(id, p.vocab, p.status);
+  const float scale = there ? p.scale : 0.f;
   const TT* row = static_cast<const TT*>(p.table) + (there ? static_cast<uint64_t>(id) * p.table_stride : 0);
   T* out = static_cast<T*>(p.out) + t * p.hidden;
   AnyValues<TT, V, true> v[UNITS];
@@ -123,7 +127,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_wide_kernel(EmbedParams p
     float f[V];
     v[q].get(f);
 #pragma unroll
-    for (int j = 0; j < V; j++) f[j] *= p.scale;
+    for (int j = 0; j < V; j++) f[j] *= scale;
     Piece<T, V> o;
     o.set(f);
     o.store(out + static_cast<uint64_t>(c0 + q * 32) * V);
@@ -143,6 +147,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_any_kernel(EmbedParams p,
   const uint32_t values = cut.unit(static_cast<uint32_t>(i - t * shares) * 32 + lane_id(), p.hidden, &first);
   const int64_t id = id_at(p.ids, p.ids64, t);
   const bool there = has_row(id, p.vocab, p.status);
+  const float scale = there ? p.scale : 0.f;
   const TT* row = static_cast<const TT*>(p.table) + (there ? static_cast<uint64_t>(id) * p.table_stride : 0);
   if (values == V) {
     AnyValues<TT, V, false> v;
@@ -151,12 +156,12 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_any_kernel(EmbedParams p,
     float f[V];
     v.get(f);
 #pragma unroll
-    for (int j = 0; j < V; j++) f[j] *= p.scale;
+    for (int j = 0; j < V; j++) f[j] *= scale;
     Piece<T, V> o;
     o.set(f);
     o.store(out + first);
   } else if (values) {
-    out[first] = from_f32<T>(there ? p.scale * to_f32<TT>(row[first]) : 0.f);
+    out[first] = from_f32<T>(there ? scale * to_f32<TT>(row[first]) : 0.f);
   }
 }
 

@@ -219,3 +219,15 @@ def test_captured_and_replayed(zc, emb):
         graph.replay()
         assert torch.equal(d, emb.lookup_backward(dout, ids, 500, emb.workspace(3000, 500, 72), st))
         assert torch.equal(rows, emb.lookup(ids, table, st))
+
+
+@pytest.mark.parametrize("dtype,ttype", KINDS)
+@pytest.mark.parametrize("tokens,width", [(40, 24), (4000, 504), (2000, 1000), (40, 1021)])
+@pytest.mark.parametrize("scale", [-2.0, float("inf"), float("nan")])
+def test_no_token_is_a_row_of_zeros_whatever_the_scale(zc, emb, dtype, ttype, tokens, width, scale):
+    ids = make(tokens, 30)
+    ids[::5], ids[1::5] = -1, 30                                        # beyond the table: reported, and none too
+    rows = emb.lookup(ids, rows_of(30, width, ttype), zc.new_status(), scale=scale, dtype=dtype)
+    none = (ids < 0) | (ids >= 30)
+    assert torch.equal(rows[none].float().view(torch.int32), torch.zeros((int(none.sum()), width), dtype=torch.int32, device="cuda"))
+    assert bool((rows[~none] != 0).any(1).all())
