@@ -231,3 +231,19 @@ def test_no_token_is_a_row_of_zeros_whatever_the_scale(zc, emb, dtype, ttype, to
     none = (ids < 0) | (ids >= 30)
     assert torch.equal(rows[none].float().view(torch.int32), torch.zeros((int(none.sum()), width), dtype=torch.int32, device="cuda"))
     assert bool((rows[~none] != 0).any(1).all())
+
+
+@pytest.mark.parametrize("dtype,ttype", KINDS)
+@pytest.mark.parametrize("tokens,width", [(2001, 1024), (2001, 1000), (2001, 4104), (1203, 2048), (20001, 264), (20001, 136)])
+def test_many_wide_rows(zc, emb, dtype, ttype, tokens, width):
+    """Every token a row of its own: rows of one warp's share, of a part of one and of several, the last partly filled, and
+    narrow ones by pieces; negative ids and ids beyond the table, rows apart from one another."""
+    vocab = 3000
+    ids = make(tokens, vocab, width, torch.int32 if width % 3 else torch.int64, skew=False)
+    table = rows_of(vocab, width, ttype)
+    check_rows(zc, emb, ids, table, dtype, 1.7)
+    ids[7::50] = vocab + torch.arange(len(ids[7::50]), device="cuda").to(ids.dtype)
+    check_rows(zc, emb, ids, rows_of(vocab, width + 16, ttype, 2)[:, 8:8 + width], dtype, -0.6)
+    room = torch.full((tokens * width + 16,), 7.0, device="cuda").to(dtype)
+    check_rows(zc, emb, ids, table, dtype, 1.0, out=room[8:8 + tokens * width].view(tokens, width))
+    assert bool((room[:8] == 7).all()) and bool((room[8 + tokens * width:] == 7).all())
