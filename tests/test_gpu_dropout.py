@@ -177,3 +177,27 @@ def test_a_graph_draws_anew(drop):
         assert torch.equal(out, drop.dropout(x, 0.5, drop.new_rng(4, step), 3))
         seen.append(out.clone())
     assert not torch.equal(seen[0], seen[1])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", [(8200, 1032), (1030, 8208), (33000, 256)])
+def test_many_values_with_a_residual(drop, dtype, rows, width):
+    """More than 2^20 groups of eight columns, which 16-bit rows take four a thread: contiguous ones that end within a CTA's,
+    rows of wider matrices, in place, and a last row written up to its end."""
+    g = torch.Generator(device="cuda").manual_seed(width)
+    wide, other = (torch.randn((rows, width + w), device="cuda", generator=g).to(dtype) for w in (8, 16))
+    rng, p = drop.new_rng(21, 3), 0.3
+    keep, factor = kept(rows, width, p, 21, 3, 6)
+    x, r = wide[:, :width].contiguous(), other[:, :width].contiguous()
+    room = torch.full((rows * width + 16,), 7.0, device="cuda").to(dtype)
+    out = room[8:-8].view(rows, width)
+    check(drop.dropout(x, p, rng, 6, residual=r, residual_scale=-0.75, out=out), x, keep, factor, r, -0.75)
+    assert bool((room[:8] == 7).all()) and bool((room[-8:] == 7).all())
+    want = drop.dropout(x, p, rng, 6, residual=r)
+    check(want, x, keep, factor, r)
+    for a, b in ((wide[:, :width], r), (x, other[:, :width]), (wide[:, :width], other[:, :width])):
+        assert torch.equal(drop.dropout(a, p, rng, 6, residual=b), want)
+    x, r = wide[:, 8:], other[:, 8:8 + width]                           # rows that start within the matrices'
+    check(drop.dropout(x, p, rng, 6, residual=r), x, keep, factor, r)
+    a = r.contiguous()
+    assert torch.equal(drop.dropout(x, p, rng, 6, residual=a, out=a), drop.dropout(x, p, rng, 6, residual=r))
