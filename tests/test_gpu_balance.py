@@ -213,3 +213,12 @@ def test_a_workspace_for_the_largest_batch_serves_smaller_ones(moe):
         want = check(moe, logits[:tokens], ids[:tokens], sequences=sequences)
         got = moe.balance_loss(logits[:tokens], ids[:tokens], ws, sequences=sequences)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [1, 31, 32, 61, 64, 100, 128, 250, 256, 400, 512])
+@pytest.mark.parametrize("tokens,sequences", [(1025, 1), (1400, 7), (600, 3)])
+def test_widths_of_the_two_launches(moe, score, dtype, n, tokens, sequences):
+    """Every number of experts a lane, in pieces and one at a time, past what one cluster takes."""
+    check(moe, *make(tokens, n, min(n, 5), dtype, 0.3, seed=n), score=score, sequences=sequences, dloss=float(tokens))

@@ -247,3 +247,12 @@ def test_many_wide_rows(zc, emb, dtype, ttype, tokens, width):
     room = torch.full((tokens * width + 16,), 7.0, device="cuda").to(dtype)
     check_rows(zc, emb, ids, table, dtype, 1.0, out=room[8:8 + tokens * width].view(tokens, width))
     assert bool((room[:8] == 7).all()) and bool((room[8 + tokens * width:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype,ttype", KINDS)
+@pytest.mark.parametrize("tokens,vocab,width", [(5000, 2, 264), (5000, 2, 301), (9000, 40, 77), (40000, 3, 24), (40000, 900, 33)])
+def test_long_runs_written_and_added(zc, emb, dtype, ttype, tokens, vocab, width):
+    """Ids whose tokens lie in many runs, of several slabs, on 16 bytes and off them, in a table of their own and added to one."""
+    ids, dout = make(tokens, vocab, tokens), rows_of(tokens, width, dtype)
+    check_gradient(zc, emb, dout, ids, vocab + 5, ttype, 0.7)
+    check_gradient(zc, emb, dout, ids, vocab + 5, ttype, 0.7, rows_of(vocab + 5, width, ttype, 9), True)
