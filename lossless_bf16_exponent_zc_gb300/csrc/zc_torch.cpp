@@ -135,6 +135,12 @@ long integer(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised();  // an array of several values, say
+  return v != 0;
+}
+
 // A count that the C ABI takes as 32 bits; what it refuses as too large stays so.
 uint32_t count(PyObject* o, const char* what) {
   const long v = integer(o);
@@ -248,7 +254,7 @@ PyObject* moe_route(Args a) {
   const Matrix l = matrix(a[0], "logits");
   const int64_t tokens = l.t.size(0);
   const uint32_t k = count(a[1], "k");
-  const int dtype = dtype_of(l.t), score = score_of(a[2]), renormalize = PyObject_IsTrue(a[4]);
+  const int dtype = dtype_of(l.t), score = score_of(a[2]), renormalize = truth(a[4]);
   const float* bias = nullptr;
   if (a[3] != Py_None) bias = static_cast<const float*>(table(a[3], {l.t.size(1)}, at::kFloat, "bias").const_data_ptr());
   const float scale = real(a[5]);
@@ -274,7 +280,7 @@ PyObject* moe_route_backward(Args a) {
   const int64_t tokens = l.t.size(0), k = experts.size(1);
   table(a[2], {tokens, k}, at::kInt, "experts");
   const Tensor& dweights = table(a[0], {tokens, k}, at::kFloat, "dweights");
-  const int dtype = dtype_of(l.t), score = score_of(a[3]), renormalize = PyObject_IsTrue(a[4]);
+  const int dtype = dtype_of(l.t), score = score_of(a[3]), renormalize = truth(a[4]);
   const float scale = real(a[5]);
   const uint32_t width = narrow(l.width, "zc_moe_route_backward");
   const uint32_t slots = narrow(static_cast<uint64_t>(k), "zc_moe_route_backward");
@@ -639,7 +645,7 @@ PyObject* layer_norm(Args a) {
   n.params_f32 = kind == at::kFloat && x.t.scalar_type() != at::kFloat;
   n.residual_scale = real(a[7]);
   n.eps = real(a[8]);
-  const int save = PyObject_IsTrue(a[11]);
+  const bool save = truth(a[11]);
   const Launch on(a[12], x.t);
   Tensor x_new, stats;
   if (branch) x_new = on.output(a[9], x.t.sizes(), x.t.scalar_type(), "x_new");
@@ -657,6 +663,7 @@ PyObject* layer_norm(Args a) {
 PyObject* layer_norm_backward(Args a) {
   zc_layer_norm_backward_args n = {};
   const Matrix x = matrix(a[2], "x_new"), dh = same_as(a[1], x.t, "dh");
+  const bool bias = truth(a[5]), branch = truth(a[10]);
   n.dh = dh.p();
   n.dh_stride = dh.stride;
   n.x_new = x.p();
@@ -678,7 +685,6 @@ PyObject* layer_norm_backward(Args a) {
   if (!n.weight && x.t.size(1)) refuse("the norm takes a weight");
   n.params_f32 = kind == at::kFloat && x.t.scalar_type() != at::kFloat;
   n.residual_scale = real(a[9]);
-  const bool branch = PyObject_IsTrue(a[10]) == 1;
   if (!branch) n.residual_scale = 1.f;
   const Tensor& ws = tensor(a[11], "ws");
   if (!ws.is_contiguous()) refuse("libzc takes contiguous tensors");
@@ -686,7 +692,7 @@ PyObject* layer_norm_backward(Args a) {
   Tensor dx = on.fresh(x.t.sizes(), x.t.scalar_type()), dy, dbias;
   if (branch) dy = n.rng || n.residual_scale != 1.f ? on.fresh(x.t.sizes(), x.t.scalar_type()) : dx;
   Tensor dweight = on.fresh({x.t.size(1)}, kind);
-  if (PyObject_IsTrue(a[5]) == 1) dbias = on.fresh({x.t.size(1)}, kind);
+  if (bias) dbias = on.fresh({x.t.size(1)}, kind);
   n.dx = dx.mutable_data_ptr();
   if (branch && !dy.is_same(dx)) n.dy = dy.mutable_data_ptr();
   n.dweight = dweight.mutable_data_ptr();
@@ -755,7 +761,7 @@ PyObject* embedding_backward(Args a) {
   if (!ws.is_contiguous()) refuse("libzc takes contiguous tensors");
   const Tensor& status = table(a[4], {1}, at::kInt, "status");
   const float scale = real(a[5]);
-  const bool given = a[7] != Py_None, accumulate = PyObject_IsTrue(a[8]) == 1;
+  const bool given = a[7] != Py_None, accumulate = truth(a[8]);
   if (accumulate && !given) refuse("accumulate adds to a given dtable");
   at::ScalarType kind = kind_of(a[6], given ? tensor(a[7], "dtable").scalar_type() : g.t.scalar_type());
   const int dtype = check_kinds(g.t.scalar_type(), kind);

@@ -315,3 +315,23 @@ def test_a_balance_workspace_holds_every_smaller_batch(experts):
     assert need == sorted(need)
     need = [moe.balance_workspace_size(1 << 20, experts, 1 << n) for n in range(21)]
     assert need == sorted(need)
+
+
+class Unclear:
+    """What has no truth value, like an array of several numbers."""
+
+    def __bool__(self):
+        raise ArithmeticError("ambiguous")
+
+
+def test_flags_without_a_truth_value(fake):
+    t = tensors("cuda:0")
+    for call in (lambda: moe.route(t["logits"], 2, renormalize=Unclear()),
+                 lambda: moe.route_backward(t["logits"][:, :2].contiguous(), t["logits"], t["experts"], renormalize=Unclear()),
+                 lambda: norm.layer_norm(t["x"], t["w"], save=Unclear()),
+                 lambda: norm.add_layer_norm(t["y"], t["x"], t["w"], save=Unclear()),
+                 lambda: norm.layer_norm_backward(t["dout"], t["x"], t["stats"], t["w"], t["ws"], bias=Unclear()),
+                 lambda: embedding.lookup_backward(t["dout"], t["ids"], VOCAB, t["ws"], t["status"], dtable=t["dtable"],
+                                                   accumulate=Unclear())):
+        with pytest.raises(ArithmeticError, match="ambiguous"):
+            call()
