@@ -29,9 +29,10 @@ constexpr int kBalanceWarps = N <= 16 ? 16 : 8;
 constexpr int kBackWarps = 8;
 
 // A row's p, from its logits in l; false, and p all zero, where no logit is above minus infinity.
-// `raw` gets the exponentials or the sigmoids, `inv` the reciprocal of their sum.  SLOPE: in place of the
-// sigmoids s their derivatives s (1 - s), in which 1 - s = e s with e = exp(-logit) where the logit is above
-// zero: a difference from 1 would keep no bits of it from a logit of 17 on (at 10 it is off by 2^-11).
+// `raw` gets the exponentials or the sigmoids s, `inv` the reciprocal of their sum.  SLOPE: in place of s
+// the smaller of s and 1 - s, negative where that is s: s (1 - s) = m (1 - m) by it, and 1 - s = e s with
+// e = exp(-logit) where the logit is above zero.  A difference from 1 would keep no bits of it from a logit
+// of 17 on (at 10 it is off by 2^-11).
 template <int N, bool SLOPE>
 __device__ __forceinline__ bool probabilities(float (&l)[N], bool sigmoid_score, float (&raw)[N], float* inv) {
   float best = l[0];
@@ -43,23 +44,24 @@ __device__ __forceinline__ bool probabilities(float (&l)[N], bool sigmoid_score,
 #pragma unroll
     for (int j = 0; j < N; j++) {
       const float e = expf(-l[j]), s = __fdividef(1.f, 1.f + e);  // 1 / infinity: zero
-      raw[j] = s;
-      if (SLOPE) l[j] = s * (l[j] > 0.f ? e * s : 1.f - s);
+      raw[j] = !SLOPE ? s : l[j] > 0.f ? e * s : -s;
+      sum += s;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < N; j++) raw[j] = l[j] == -INFINITY ? 0.f : expf(l[j] - top);
+    for (int j = 0; j < N; j++) {
+      raw[j] = l[j] == -INFINITY ? 0.f : expf(l[j] - top);
+      sum += raw[j];
+    }
   }
-#pragma unroll
-  for (int j = 0; j < N; j++) sum += raw[j];
   sum = warp_sum_f32(sum) + (sigmoid_score ? 1e-20f : 0.f);
   const bool any = top > -INFINITY || sum != sum;
   *inv = any ? 1.f / sum : 0.f;
 #pragma unroll
   for (int j = 0; j < N; j++) {
-    const float q = any ? raw[j] * *inv : 0.f;
-    if (SLOPE && sigmoid_score) raw[j] = l[j];
-    l[j] = q;
+    float v = raw[j];
+    if (SLOPE && sigmoid_score) v = signbit(v) ? -v : 1.f - v;
+    l[j] = any ? v * *inv : 0.f;
   }
   return any;
 }
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(kBackWarps * 32) balance_bwd_kernel(BalanceBwd
   mean = warp_sum_f32(mean);
 #pragma unroll
   for (int j = 0; j < N; j++) {
-    const float d = p.sigmoid ? raw[j] * inv : l[j];
+    const float m = fabsf(raw[j]), d = p.sigmoid ? m * (1.f - m) * inv : l[j];
     l[j] = any ? d * (g * (c[j] - mean)) : 0.f;
   }
   store_row<T, N, VEC>(out, p.experts, l);
