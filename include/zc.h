@@ -656,7 +656,14 @@ zc_status zc_norm_backward(const zc_norm_backward_args* h_args, void* stream);
  * above, dropout, and the embedding that starts the residual stream.
  * Conventions as for the operators around an expert-parallel exchange: rows of
  * any alignment, fp32 inside, one rounding, sums in a fixed order, workspaces
- * that need no initialisation.
+ * that need no initialisation.  Two of these in more detail:
+ *   - fp32 inside: exponentials, the balance loss's sigmoids and the norms'
+ *     reciprocal square roots are good to a few units in the last place, not
+ *     rounded to nearest (zc_moe_route's sigmoids are), and quotients may be
+ *     products with a rounded reciprocal.
+ *   - The order of the sums over tokens of an embedding's gradient, dweight and
+ *     dbias follows from the sizes and the GPU's SMs: the same inputs give the
+ *     same bits on one kind of GPU, not on any.
  */
 
 /*

@@ -11,9 +11,14 @@
 // second launch the CTAs' sums in order: no result depends on timing.
 //
 // Nothing here is near the memory's rate.  16384 x 256 fp32 (17 MB, 2.5 us at the copy's rate), sigmoid, 8
-// sequences: forward 11.7 us in two launches, the first bound by its exponentials and divisions (65% of the
-// issue slots), the second by a chain of dependent loads, shuffles and barriers; gradient 8.3 us (74% of the
+// sequences: forward 11.6 us in two launches, the first bound by its exponentials and divisions (66% of the
+// issue slots), the second by a chain of dependent loads, shuffles and barriers; gradient 8.7 us (78% of the
 // issue slots).  5003 x 61 bf16 8.8 and 2.6 us.
+//
+// Sigmoids are taken by the fast quotient, within two units of the last place (zero from logits of -87.3 down,
+// where they are below 2^-126), not rounded as the router's, and p is the exponential or the sigmoid times
+// the rounded reciprocal of their sum.  The errors against 64 bits stay those of plain fp32; the router's
+// sigmoid took 13.3 us forward instead of 12.1 and 10.5 back instead of 9.6 (16384 x 256 fp32, other tensors).
 #include "zc_internal.h"
 #include "zc_layer.cuh"
 
@@ -285,8 +290,8 @@ __device__ __forceinline__ void store_row(T* row, uint32_t width, const float (&
   }
 }
 
-// A warp a token, read and written once: 16384 x 256 fp32 8.3 us (60% of the copy's rate; its exponentials
-// keep 74% of the issue slots busy).  Persistent warps with the next row on its way took 8.0 to 8.6 us, but
+// A warp a token, read and written once: 16384 x 256 fp32 8.7 us with sigmoids (57% of the copy's rate; its
+// exponentials keep 78% of the issue slots busy), 8.2 by softmax.  Persistent warps with the next row on its way took 8.0 to 8.6 us, but
 // 5.6 instead of 4.5 for 16384 x 64 bf16; two tokens a warp 8.5.
 template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kBackWarps * 32) balance_bwd_kernel(BalanceBwdParams p) {

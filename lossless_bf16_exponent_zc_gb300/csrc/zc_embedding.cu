@@ -3,9 +3,10 @@
 //
 //   out[t] = scale table[id_t],    dtable[v] = scale (sum over t with id_t = v, in order, of dout[t])
 //
-// The gradient sorts the tokens by id (a stable radix sort), so that every row of the table is
-// summed in fp32 in the order of its tokens and written once: no sum depends on timing.  Both directions
-// are bound by memory where there is much of it: 16384 tokens of 131072 x 4096 bf16, ids by 1 / rank, 33 us
+// The gradient sorts the tokens by id (a stable radix sort), cuts them into runs of up to 32, sums a row's
+// tokens in fp32 in their order within a run, then its runs in theirs, and writes every row of the table
+// once: no sum depends on timing.  (The runs' length follows from the sizes and the number of SMs: the same
+// bits on one kind of GPU, not on any.)  Both directions are bound by memory where there is much of it: 16384 tokens of 131072 x 4096 bf16, ids by 1 / rank, 33 us
 // forward (85% of the copy's rate) and 206 back (87%, most of it zeros for rows without a token), 68 added
 // to what the table holds.
 #include "zc_internal.h"

@@ -6,9 +6,9 @@
 
 namespace zc {
 
-// The ring's shapes.  A thread has 16 columns of a row of 16-bit values (8 in twice the threads: 16384 x
-// 4096 bf16 with dropout 100 us forward and 118 back, with 16 94 and 110), or 8 where the launches' rules
-// find them faster.
+// The ring's shapes.  A thread has 16 columns of a row of 16-bit values (16384 x 4096 bf16 with dropout
+// 92.5 us forward and 111 back, 8 in twice the threads 6 to 7% more), or 8 where the launches' rules find
+// them faster.
 constexpr int kLayerWideCols = 16;
 // Stages, forward and back: more of them move no more bytes a second, for reads and writes share the
 // memory's bus (forward, 16 columns: 4 stages 96 us, 3 95, 2 91 to 94; without a branch 48, 48, 49.5;

@@ -3,8 +3,9 @@
     x = embedding.lookup(ids, table, status, scale=hidden ** 0.5)                     # [tokens, hidden]
     dtable = embedding.lookup_backward(dx, ids, len(table), ws, status, scale=hidden ** 0.5)
 
-The gradient sorts the tokens by id, adds up every id's rows in float32 in the order of its tokens and writes each row of
-the table once, so the same inputs give the same bits.  Kernels: zc_embedding and zc_embedding_backward (include/zc.h);
+The gradient sorts the tokens by id, adds up every id's rows in float32, in the order of its tokens within runs of up to 32
+sorted tokens and then run by run, and writes each row of the table once.  So the same inputs give the same bits on one kind
+of GPU (the runs' length follows from its SMs).  Kernels: zc_embedding and zc_embedding_backward (include/zc.h);
 arguments are checked, and outputs that are not given allocated, in the native extension (csrc/zc_torch.cpp).  The rows
 are bfloat16, float16 or float32; the table has their type or float32.  ids: int32 or int64 [tokens]; a negative id is
 no token, an id beyond the table sets ERR_BAD_INDEX in status and is taken for none.
